@@ -10,8 +10,10 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -25,6 +27,7 @@ TOPK_BLOCKS = 512
 OUT_WIDTH = 2051
 DERR_REQUEST, DERR_CMP_PAGE, DERR_KV_PAGE, DERR_TIMEOUT = 1, 2, 4, 8
 DERR_IDX_BLOCK = 16
+DERR_CONTEXT = 32
 IDX_HEAD_DIM, IDX_MAX_TOPK = 128, 2048
 
 DT_F16, DT_BF16, DT_F32, DT_I32, DT_I64, DT_F8E4M3 = 1, 2, 3, 4, 5, 6
@@ -43,7 +46,9 @@ EXPORTED = ("qsa_status_string", "qsa_version", "qsa_select_workspace_bytes",
             "qsa_select_attend_fused_cluster",
             "qsa_static_scratch_bytes",
             "qsa_select_paged_tokens_static_scratch", "qsa_build_metadata",
-            "qsa_paged_mqa_logits", "qsa_top_k_per_row_decode")
+            "qsa_paged_mqa_logits", "qsa_top_k_per_row_decode",
+            "qsa_paged_append", "qsa_paged_attention_workspace_bytes", "qsa_paged_attention",
+            "qsa_evict_workspace_bytes", "qsa_evict_entries")
 
 
 class QSAError(RuntimeError):
@@ -178,6 +183,20 @@ def declare_signatures(lib):
         vp, ctypes.c_int, i64, i64, i64, i64, i64,
         vp, ctypes.c_int, i64,
         i64, vp, ctypes.c_int, i64, vp]
+    lib.qsa_paged_append.restype = ctypes.c_int
+    lib.qsa_paged_append.argtypes = [
+        vp, vp, vp, ctypes.c_int, i64, vp, vp, vp, vp, vp, vp, i64, vp, i64, i64, vp, vp]
+    lib.qsa_paged_attention_workspace_bytes.restype = sz
+    lib.qsa_paged_attention_workspace_bytes.argtypes = [i64] * 6
+    lib.qsa_paged_attention.restype = ctypes.c_int
+    lib.qsa_paged_attention.argtypes = [
+        vp, vp, ctypes.c_int, i64, i64, vp, vp, ctypes.c_float, i64,
+        vp, vp, vp, vp, i64, vp, i64, i64, vp, sz, vp, vp]
+    lib.qsa_evict_workspace_bytes.restype = sz
+    lib.qsa_evict_workspace_bytes.argtypes = [i64, i64]
+    lib.qsa_evict_entries.restype = ctypes.c_int
+    lib.qsa_evict_entries.argtypes = [
+        vp, vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, sz, vp, vp]
     return full
 
 
@@ -525,3 +544,243 @@ def qsa_top_k_per_row_decode(logits, next_n: int, seq_lens, topk_tokens: int, ou
         int(topk_tokens), _ptr(out), _tag(out), out.stride(0), _stream(stream))
     _check(st)
     return out
+
+
+# --- the paged K/V cache operators (include/qsa_cache.h) ------------------------
+
+_CACHE = struct.Struct("21q")       # qsa_paged_cache: 8-byte fields throughout
+_STRIDES3 = struct.Struct("3q")
+
+
+def _cache_struct(k_cache, v_cache, block_tables, k_scale, v_scale) -> bytes:
+    """A qsa_paged_cache of K and V views [pages, page_size, heads, dim].  Types
+    that the C struct does not carry are checked here."""
+    if k_cache.dim() != 4 or v_cache.dim() != 4 or block_tables.dim() != 2:
+        raise QSAError(3, "k/v caches [pages, page_size, heads, dim] and a 2-D block table expected")
+    shape = k_cache.shape
+    if shape != v_cache.shape:
+        raise QSAError(3, "k_cache and v_cache shapes differ")
+    if k_cache.dtype != v_cache.dtype:
+        raise QSAError(2, "k_cache and v_cache dtypes differ")
+    if block_tables.dtype != torch.int32:
+        raise QSAError(2, "block_tables must be int32")
+    reqs, cols = block_tables.shape
+    s0, s1 = block_tables.stride()
+    if s1 != 1 and cols > 1:
+        raise QSAError(4, "block-table columns must be contiguous")
+    ks = vs = 0
+    if k_scale is not None:
+        ks = _scale_ptr(k_scale, shape[2])
+    if v_scale is not None:
+        vs = _scale_ptr(v_scale, shape[2])
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), *shape, *k_cache.stride(),
+                       *v_cache.stride(), ks, vs, block_tables.data_ptr(), reqs, cols,
+                       s0 if reqs > 1 else max(s0, cols), _DTYPE_TAG.get(k_cache.dtype, 0))
+
+
+def _scale_ptr(scale, heads) -> int:
+    if scale.dtype != torch.float32:
+        raise QSAError(2, "K/V scales must be float32")
+    if scale.dim() != 1 or scale.shape[0] != heads or not scale.is_contiguous():
+        raise QSAError(3, "K/V scales must be contiguous [heads]")
+    return scale.data_ptr()
+
+
+def _typed(t, dtype, dims, what) -> int:
+    """The address of an argument whose C type is fixed (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise QSAError(2, f"{what} must be {dtype}")
+    if t.dim() != dims:
+        raise QSAError(3, f"{what} must be {dims}-D")
+    return t.data_ptr()
+
+
+def _flat(t, dtype, n, what) -> int:
+    """As _typed, for a contiguous tensor of exactly n elements."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise QSAError(2, f"{what} must be {dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise QSAError(3, f"{what} must be contiguous, {n} elements")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, reqs, what):
+    """(address, row stride) of a [reqs, cols] per-entry array."""
+    if t is None:
+        return 0, 0
+    p = _typed(t, dtype, 2, what)
+    if t.shape[0] != reqs:
+        raise QSAError(3, f"{what} needs one row per request")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise QSAError(4, f"{what} columns must be contiguous")
+    return p, t.stride(0) if reqs > 1 else max(t.stride(0), t.shape[1])
+
+
+def _word(t) -> int:
+    return _flat(t, torch.int32, 1, "error_word")
+
+
+def _launch_stream(stream, device_index) -> int:
+    # the current stream's handle without building a Stream object around it
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return _stream(stream) or 0
+
+
+def _on_stream(stream, raw, device_index):
+    """A context in which torch allocates for the launch stream, so that a
+    buffer made here is not handed out again while the launch uses it."""
+    if stream is None or raw == torch._C._cuda_getCurrentRawStream(device_index):
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(raw))
+
+
+def _need_tensor(t, what):
+    if not isinstance(t, torch.Tensor):
+        raise QSAError(1, f"{what} must be a tensor")
+
+
+def qsa_paged_append(k, v, k_cache, v_cache, block_tables, token_to_request, entries, *,
+                     k_scale=None, v_scale=None, positions=None, entry_positions=None,
+                     weight_sums=None, error_word=None, stream=None):
+    """Write new tokens' keys and values [T, heads, dim] into a paged cache
+    (include/qsa_cache.h): token t becomes entry entries[t] (int64, -1 =
+    padding) of request token_to_request[t] (int32).  entry_positions (int32)
+    and weight_sums (fp32), [requests, entries], get the token's position and
+    0.  Returns (k_cache, v_cache)."""
+    lib = load_library()
+    _on_current_device(k, v, k_cache, v_cache, block_tables, token_to_request, entries, k_scale,
+                       v_scale, positions, entry_positions, weight_sums, error_word)
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != k_cache.shape[2:]:
+        raise QSAError(3, "k and v must be [tokens, heads, dim] of the cache's heads and dim")
+    if k.dtype != v.dtype:
+        raise QSAError(2, "k and v dtypes differ")
+    T = k.shape[0]
+    cache = _cache_struct(k_cache, v_cache, block_tables, k_scale, v_scale)
+    reqs = block_tables.shape[0]
+    pos, pos_s0 = _rows(entry_positions, torch.int32, reqs, "entry_positions")
+    sums, sums_s0 = _rows(weight_sums, torch.float32, reqs, "weight_sums")
+    cols = [t.shape[1] for t in (entry_positions, weight_sums) if t is not None]
+    _check(lib.qsa_paged_append(
+        cache, k.data_ptr(), v.data_ptr(), _tag(k), T, _STRIDES3.pack(*k.stride()),
+        _STRIDES3.pack(*v.stride()), _flat(token_to_request, torch.int32, T, "token_to_request"),
+        _flat(entries, torch.int64, T, "entries"), _flat(positions, torch.int64, T, "positions"),
+        pos, pos_s0, sums, sums_s0, min(cols) if cols else 0, _word(error_word),
+        _launch_stream(stream, k.get_device())))
+    return k_cache, v_cache
+
+
+def qsa_paged_attention_workspace_bytes(num_reqs: int, next_n: int, num_heads: int,
+                                        kv_heads: int, head_dim: int,
+                                        weight_cols: int = 0) -> int:
+    return int(load_library().qsa_paged_attention_workspace_bytes(
+        num_reqs, next_n, num_heads, kv_heads, head_dim, weight_cols))
+
+
+def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next_n: int = 1,
+                        scale: float | None = None, window: int = 0, k_scale=None, v_scale=None,
+                        out=None, lse=None, weight_sums=None, weight_sums_out=None,
+                        workspace=None, error_word=None, stream=None):
+    """Dense attention of each request's next_n new tokens, q [requests*next_n,
+    heads, dim], over its cached entries (include/qsa_cache.h).  scale: 1/sqrt
+    (dim) unless given.  lse: fp32 [rows, heads], filled when given.
+    weight_sums / weight_sums_out: fp32 [requests, entries]; the second gets
+    the first plus the weight that each entry received in this call.  Returns
+    out [rows, heads, dim]."""
+    lib = load_library()
+    _on_current_device(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, out,
+                       lse, weight_sums, weight_sums_out, workspace, error_word)
+    if q.dim() != 3:
+        raise QSAError(3, "q must be [requests * next_n, heads, dim]")
+    cache = _cache_struct(k_cache, v_cache, block_tables, k_scale, v_scale)
+    rows, heads, dim = q.shape
+    reqs, cols = block_tables.shape
+    page_size, kv_heads = k_cache.shape[1], k_cache.shape[2]
+    if rows != reqs * next_n or dim != k_cache.shape[3]:
+        raise QSAError(3, "q must be [requests * next_n, heads, dim] of the cache's dim")
+    device = q.get_device()
+    raw = _launch_stream(stream, device)
+    weights = weight_sums is not None or weight_sums_out is not None
+    if out is None or workspace is None:
+        with _on_stream(stream, raw, device):
+            if out is None:
+                out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
+            if workspace is None:
+                workspace = _workspace(lib.qsa_paged_attention_workspace_bytes(
+                    reqs, next_n, heads, kv_heads, dim, cols * page_size if weights else 0),
+                    q.device)
+    if out.dtype != q.dtype:
+        raise QSAError(2, "out must have q's dtype")
+    if out.shape != q.shape:
+        raise QSAError(3, "out must have q's shape")
+    sums, sums_s0 = _rows(weight_sums, torch.float32, reqs, "weight_sums")
+    souts, souts_s0 = _rows(weight_sums_out, torch.float32, reqs, "weight_sums_out")
+    entry_cols = min([t.shape[1] for t in (weight_sums, weight_sums_out) if t is not None]) \
+        if weights else 0
+    _check(lib.qsa_paged_attention(
+        cache, q.data_ptr(), _tag(q), next_n, heads, _STRIDES3.pack(*q.stride()),
+        _flat(context_lens, torch.int32, reqs, "context_lens"),
+        dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+        _STRIDES3.pack(*out.stride()), _flat(lse, torch.float32, rows * heads, "lse"),
+        sums, sums_s0, souts, souts_s0, entry_cols, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _word(error_word), raw))
+    return out
+
+
+def qsa_evict_workspace_bytes(num_reqs: int, budget: int) -> int:
+    return int(load_library().qsa_evict_workspace_bytes(num_reqs, budget))
+
+
+def qsa_evict_entries(weight_sums, entry_positions, context_lens, k_cache, v_cache, block_tables,
+                      budget: int, *, num_sink: int = 0, num_recent: int = 0, kept=None,
+                      new_lens=None, weight_sums_out=None, entry_positions_out=None,
+                      workspace=None, error_word=None, stream=None):
+    """Cut every request down to at most `budget` cached entries, keeping the
+    first num_sink positions, the num_recent newest and then those of the
+    largest weight_sums; K and V are moved within the cache
+    (include/qsa_cache.h).  Returns (kept int32 [requests, budget], new_lens
+    int32 [requests], weight_sums_out fp32, entry_positions_out int32
+    [requests, budget])."""
+    lib = load_library()
+    _on_current_device(weight_sums, entry_positions, context_lens, k_cache, v_cache, block_tables,
+                       kept, new_lens, weight_sums_out, entry_positions_out, workspace, error_word)
+    cache = _cache_struct(k_cache, v_cache, block_tables, None, None)
+    reqs = block_tables.shape[0]
+    sums, sums_s0 = _rows(weight_sums, torch.float32, reqs, "weight_sums")
+    pos, pos_s0 = _rows(entry_positions, torch.int32, reqs, "entry_positions")
+    if not sums or not pos:
+        for t, what in ((weight_sums, "weight_sums"), (entry_positions, "entry_positions")):
+            _need_tensor(t, what)
+    device, dev = block_tables.get_device(), block_tables.device
+    raw = _launch_stream(stream, device)
+    if budget < 1:
+        raise QSAError(6, "budget must be at least 1")
+    if kept is None or new_lens is None or weight_sums_out is None or \
+            entry_positions_out is None or workspace is None:
+        with _on_stream(stream, raw, device):
+            if kept is None:
+                kept = torch.empty((reqs, budget), dtype=torch.int32, device=dev)
+            if new_lens is None:
+                new_lens = torch.empty(reqs, dtype=torch.int32, device=dev)
+            if weight_sums_out is None:
+                weight_sums_out = torch.empty((reqs, budget), dtype=torch.float32, device=dev)
+            if entry_positions_out is None:
+                entry_positions_out = torch.empty((reqs, budget), dtype=torch.int32, device=dev)
+            if workspace is None:
+                workspace = _workspace(lib.qsa_evict_workspace_bytes(reqs, budget), dev)
+    n = reqs * budget
+    _check(lib.qsa_evict_entries(
+        cache, sums, sums_s0, pos, pos_s0,
+        min(weight_sums.shape[1], entry_positions.shape[1]),
+        _flat(context_lens, torch.int32, reqs, "context_lens"), budget, num_sink, num_recent,
+        _flat(kept, torch.int32, n, "kept"), _flat(new_lens, torch.int32, reqs, "new_lens"),
+        _flat(weight_sums_out, torch.float32, n, "weight_sums_out"),
+        _flat(entry_positions_out, torch.int32, n, "entry_positions_out"),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _word(error_word), raw))
+    return kept, new_lens, weight_sums_out, entry_positions_out

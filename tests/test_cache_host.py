@@ -1,0 +1,213 @@
+"""Host-side checks of the paged-cache operators' C ABI and binding (no GPU):
+every bad argument is refused before any CUDA call, so fake, never dereferenced
+device addresses are enough."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import sparse_paged_attention_qsa_gb300 as qsa
+from sparse_paged_attention_qsa_gb300 import binding
+from sparse_paged_attention_qsa_gb300 import build as qbuild
+
+HDR = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                   "qsa_cache.h")
+NULL, DTYPE, SHAPE, STRIDE, ALIGN, CONTRACT, WORKSPACE, ALIAS = 1, 2, 3, 4, 5, 6, 7, 8
+
+
+@pytest.fixture(scope="module")
+def lib():
+    qbuild.build()
+    return qsa.load_library()
+
+
+def _addr(k):
+    return (1 << 36) * (k + 1)
+
+
+FIELDS = ("k v pages size heads dim ks0 ks1 ks2 ks3 vs0 vs1 vs2 vs3 kscale vscale bt reqs cols bts0 "
+          "dtype").split()
+
+
+def _cache(over):
+    a = dict(k=_addr(1), v=_addr(2), pages=64, size=16, heads=2, dim=64, ks0=2048, ks1=128, ks2=64,
+             ks3=1, vs0=2048, vs1=128, vs2=64, vs3=1, kscale=0, vscale=0, bt=_addr(3), reqs=4,
+             cols=8, bts0=8, dtype=1)
+    for f in list(over):
+        if f in a and f not in ("k_", "v_"):
+            a[f] = over.pop(f)
+    return binding._CACHE.pack(*[a[f] for f in FIELDS])
+
+
+def _arr(*v):
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+def test_header_constants_and_struct_match_the_binding():
+    src = open(HDR).read()
+    consts = dict(re.findall(r"#define\s+(QSA_\w+)\s+(\d+)u?\b", src))
+    assert int(consts["QSA_DERR_CONTEXT"]) == qsa.DERR_CONTEXT == 32
+    body = re.search(r"typedef struct qsa_paged_cache \{(.*?)\} qsa_paged_cache;", src, re.S)[1]
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    words = 0
+    for decl in body.split(";"):
+        for name in decl.split(","):
+            n = re.search(r"\[(\d+)\]", name)
+            words += int(n[1]) if n else bool(name.strip())
+    assert words == len(FIELDS) == binding._CACHE.size // 8
+
+
+def _append(lib, **over):
+    cache = _cache(over)
+    a = dict(cache=cache, nk=_addr(10), nv=_addr(11), dt=1, T=5, nks=_arr(128, 64, 1),
+             nvs=_arr(128, 64, 1), t2r=_addr(12), ent=_addr(13), pos=_addr(14), ep=_addr(15),
+             eps0=128, ws=_addr(16), wss0=128, ecols=128, err=_addr(17), stream=None)
+    a.update(over)
+    return lib.qsa_paged_append(*a.values())
+
+
+def _attend(lib, **over):
+    dims = {f: over[f] for f in ("reqs", "cols", "size", "heads", "dim") if f in over}
+    cache = _cache(over)
+    n = over.get("n", 1)
+    a = dict(cache=cache, q=_addr(10), dt=1, n=n, hq=4, qs=_arr(256, 64, 1), ctx=_addr(11),
+             scale=0.125, window=0, out=_addr(12), os=_arr(256, 64, 1), lse=_addr(13),
+             win=_addr(14), ws0=128, wout=_addr(15), wos0=128, ecols=128, work=_addr(16), bytes=None,
+             err=_addr(17), stream=None)
+    a.update(over)
+    if a["bytes"] is None:
+        a["bytes"] = lib.qsa_paged_attention_workspace_bytes(
+            dims.get("reqs", 4), n, a["hq"], dims.get("heads", 2), dims.get("dim", 64),
+            dims.get("cols", 8) * dims.get("size", 16) if a["win"] else 0)
+    return lib.qsa_paged_attention(*a.values())
+
+
+def _evict(lib, **over):
+    cache = _cache(over)
+    a = dict(cache=cache, sums=_addr(10), ss0=128, pos=_addr(11), ps0=128, ecols=128, ctx=_addr(12),
+             budget=32, sink=4, recent=8, kept=_addr(13), lens=_addr(14), so=_addr(15),
+             po=_addr(16), work=_addr(17), bytes=None, err=_addr(18), stream=None)
+    a.update(over)
+    if a["bytes"] is None:
+        a["bytes"] = lib.qsa_evict_workspace_bytes(4, max(a["budget"], 1))
+    return lib.qsa_evict_entries(*a.values())
+
+
+CACHE_REFUSALS = [
+    (dict(dtype=3), DTYPE), (dict(dtype=0), DTYPE), (dict(kscale=_addr(30)), CONTRACT),
+    (dict(vscale=_addr(30)), CONTRACT),
+    (dict(dim=32), SHAPE), (dict(dim=96), SHAPE), (dict(dim=512), SHAPE), (dict(heads=0), SHAPE),
+    (dict(heads=1025), SHAPE), (dict(size=4), SHAPE), (dict(size=24), SHAPE),
+    (dict(size=131072), SHAPE), (dict(pages=-1), SHAPE), (dict(pages=1 << 31), SHAPE),
+    (dict(reqs=-1), SHAPE), (dict(reqs=65536), SHAPE), (dict(cols=-1), SHAPE),
+    (dict(ks3=2), STRIDE), (dict(vs3=0), STRIDE), (dict(ks0=0), STRIDE), (dict(ks1=-128), STRIDE),
+    (dict(ks2=65), STRIDE), (dict(vs1=132), STRIDE), (dict(vs0=1 << 39), STRIDE),
+    (dict(bts0=7), STRIDE), (dict(bts0=1 << 39), STRIDE),
+    (dict(k=0), NULL), (dict(v=0), NULL), (dict(bt=0), NULL),
+    (dict(k=_addr(1) + 8), ALIGN), (dict(v=_addr(2) + 2), ALIGN), (dict(bt=_addr(3) + 2), ALIGN),
+]
+
+
+@pytest.mark.parametrize("call", [_append, _attend, _evict], ids=["append", "attend", "evict"])
+@pytest.mark.parametrize("over,status", CACHE_REFUSALS)
+def test_cache_descriptor_is_refused(lib, call, over, status):
+    assert call(lib, **dict(over), bytes=1 << 40) == status if call is not _append \
+        else call(lib, **dict(over)) == status
+
+
+@pytest.mark.parametrize("call", [_append, _attend, _evict], ids=["append", "attend", "evict"])
+def test_no_descriptor(lib, call):
+    assert call(lib, cache=None) == NULL
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dt=3), DTYPE), (dict(dt=2), DTYPE), (dict(dt=6), DTYPE), (dict(T=-1), SHAPE),
+    (dict(T=(1 << 24) + 1), SHAPE), (dict(ecols=-1), SHAPE), (dict(ecols=1 << 31), SHAPE),
+    (dict(nks=None), NULL), (dict(nvs=None), NULL), (dict(nk=None), NULL), (dict(nv=None), NULL),
+    (dict(t2r=None), NULL), (dict(ent=None), NULL),
+    (dict(nks=_arr(128, 64, 2)), STRIDE), (dict(nks=_arr(60, 64, 1)), STRIDE),
+    (dict(nvs=_arr(128, 68, 1)), STRIDE), (dict(nvs=_arr(-128, 64, 1)), STRIDE),
+    (dict(eps0=127), STRIDE), (dict(wss0=100), STRIDE),
+    (dict(nk=_addr(10) + 2), ALIGN), (dict(ent=_addr(13) + 4), ALIGN), (dict(t2r=_addr(12) + 2), ALIGN),
+    (dict(pos=_addr(14) + 4), ALIGN), (dict(ep=_addr(15) + 1), ALIGN), (dict(err=_addr(17) + 2), ALIGN),
+    (dict(nk=_addr(1) + 64), ALIAS), (dict(t2r=_addr(2)), ALIAS), (dict(ep=_addr(1)), ALIAS),
+    (dict(ws=_addr(13)), ALIAS), (dict(ep=_addr(16)), ALIAS), (dict(err=_addr(3)), ALIAS),
+    (dict(bt=_addr(1) + 256), ALIAS),
+])
+def test_append_refusals(lib, over, status):
+    assert _append(lib, **over) == status
+
+
+def test_append_without_tokens_is_a_noop(lib):
+    assert _append(lib, T=0, nk=None, nv=None, t2r=None, ent=None) == 0
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dt=2), DTYPE), (dict(dt=6), DTYPE), (dict(scale=0.0), CONTRACT),
+    (dict(scale=float("inf")), CONTRACT), (dict(scale=float("nan")), CONTRACT),
+    (dict(scale=-1.0), CONTRACT), (dict(window=-1), CONTRACT),
+    (dict(n=0), SHAPE), (dict(n=9), SHAPE), (dict(hq=3), SHAPE), (dict(hq=0), SHAPE),
+    (dict(hq=65538), SHAPE), (dict(ecols=127), SHAPE), (dict(ecols=1 << 31), SHAPE),
+    (dict(qs=None), NULL), (dict(os=None), NULL), (dict(q=None), NULL), (dict(out=None), NULL),
+    (dict(ctx=None), NULL), (dict(win=None, bytes=1 << 40), NULL), (dict(wout=None), NULL),
+    (dict(qs=_arr(256, 64, 2)), STRIDE), (dict(qs=_arr(0, 64, 1)), STRIDE),
+    (dict(os=_arr(256, 4, 1)), STRIDE), (dict(ws0=127), STRIDE), (dict(wos0=1 << 39), STRIDE),
+    (dict(q=_addr(10) + 8), ALIGN), (dict(out=_addr(12) + 8), ALIGN), (dict(ctx=_addr(11) + 2), ALIGN),
+    (dict(lse=_addr(13) + 1), ALIGN), (dict(work=_addr(16) + 16), ALIGN), (dict(err=_addr(17) + 1), ALIGN),
+    (dict(work=None), WORKSPACE), (dict(bytes=100), WORKSPACE),
+    (dict(out=_addr(10)), ALIAS), (dict(out=_addr(1) + 4096), ALIAS), (dict(lse=_addr(12)), ALIAS),
+    (dict(work=_addr(2)), ALIAS), (dict(wout=_addr(11)), ALIAS), (dict(err=_addr(12) + 4), ALIAS),
+    (dict(wout=_addr(14) + 16), ALIAS), (dict(wout=_addr(14), wos0=129), ALIAS),
+    (dict(out=_addr(14)), ALIAS),
+])
+def test_attention_refusals(lib, over, status):
+    assert _attend(lib, **over) == status
+
+
+def test_attention_without_requests_is_a_noop(lib):
+    assert _attend(lib, reqs=0, q=None, out=None, ctx=None, bytes=0, work=None) == 0
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(budget=0), CONTRACT), (dict(budget=1 << 31), CONTRACT), (dict(sink=-1), CONTRACT),
+    (dict(recent=-1), CONTRACT), (dict(sink=25), CONTRACT), (dict(sink=1 << 62), CONTRACT),
+    (dict(ecols=-1), SHAPE), (dict(ecols=1 << 31, ss0=1 << 31, ps0=1 << 31), SHAPE),
+    (dict(ss0=127), STRIDE), (dict(ps0=1), STRIDE),
+    (dict(sums=None), NULL), (dict(pos=None), NULL), (dict(ctx=None), NULL), (dict(kept=None), NULL),
+    (dict(lens=None), NULL), (dict(so=None), NULL), (dict(po=None), NULL),
+    (dict(sums=_addr(10) + 2), ALIGN), (dict(kept=_addr(13) + 2), ALIGN), (dict(work=_addr(17) + 4), ALIGN),
+    (dict(work=None), WORKSPACE), (dict(bytes=64), WORKSPACE),
+    (dict(so=_addr(10)), ALIAS), (dict(po=_addr(11)), ALIAS), (dict(lens=_addr(12)), ALIAS),
+    (dict(kept=_addr(15)), ALIAS), (dict(kept=_addr(1)), ALIAS), (dict(sums=_addr(2) + 64), ALIAS),
+    (dict(work=_addr(1)), ALIAS), (dict(err=_addr(14)), ALIAS),
+])
+def test_evict_refusals(lib, over, status):
+    assert _evict(lib, **over) == status
+
+
+def test_evict_without_requests_is_a_noop(lib):
+    assert _evict(lib, reqs=0, bytes=0, work=None) == 0
+
+
+def test_workspace_queries(lib):
+    w = qsa.qsa_paged_attention_workspace_bytes
+    assert w(4, 1, 8, 2, 128) > 0
+    assert w(4, 1, 8, 2, 128, 4096) >= w(4, 1, 8, 2, 128) + 4 * 8 * 4096 * 4
+    for bad in ((0, 1, 8, 2, 128), (4, 0, 8, 2, 128), (4, 9, 8, 2, 128), (4, 1, 9, 2, 128),
+                (4, 1, 8, 0, 128), (4, 1, 8, 2, 100), (65536, 1, 8, 2, 128), (4, 1, 8, 2, 128, -1)):
+        assert w(*bad) == 0
+    e = qsa.qsa_evict_workspace_bytes
+    assert e(4, 100) >= 4 * 100 * 8 and e(0, 5) == 0 and e(5, 0) == 0 and e(65535, 1 << 30) > 0
+
+
+def test_binding_refuses_host_tensors():
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.float16)
+    bt, i32 = torch.zeros((1, 4), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    f = torch.zeros((1, 64))
+    for call in (lambda: qsa.qsa_paged_append(k[0, :1], k[0, :1], k, k, bt, i32, i32.long()),
+                 lambda: qsa.qsa_paged_attention(k[0, :1], k, k, bt, i32),
+                 lambda: qsa.qsa_evict_entries(f, bt, i32, k, k, bt, 8)):
+        with pytest.raises(qsa.QSAError):
+            call()
