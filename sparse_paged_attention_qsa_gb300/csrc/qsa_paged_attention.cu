@@ -1,132 +1,118 @@
 // qsa_paged_attention.cu -- dense attention of a request's new tokens over
-// its paged K/V cache, declared in include/qsa_cache.h.
+// its paged K/V cache, declared in include/qsa_cache.h: the entry point and
+// the kernel that adds up the weights entries received.  The attention's own
+// kernels are in qsa_paged_attn_impl.cuh.
 //
-// One CTA per (row, query head) walks the row's entries, a warp an entry at a
-// time, with the running maximum and sum of a softmax in binary32; the warps
-// merge through shared memory.  A second kernel adds up the weights from the
-// logits that the first one leaves in the workspace.
+// Weights: an entry's weight is known only once its row's sum is, so the walk
+// leaves the logits (binary32, base 2) in the workspace and weights_kernel
+// reads them back, 8 bytes a head beside the 2 * dim * esize * kv_heads that
+// K and V take: 6 % for four heads of 128 on a 16-bit K/V head.  (Reading K
+// again instead would be half of the whole.)  Each entry's sum is one thread's,
+// in row and head order, so it does not change from run to run.
 #include "qsa_cache.h"
 #include "qsa_cache_host.h"
 #include "qsa_device.cuh"
 #include "qsa_host.h"
+#include "qsa_internal.h"
+#include "qsa_paged_attn.h"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-#include <cuda_runtime.h>
+#include <cstring>
+#include <mutex>
 
 namespace qsa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMaxDim = 256;
+constexpr int kWeightThreads = 128;
 
-struct DenseParams {
-  CacheView c;
-  const unsigned char* q;
-  int64_t q_row, q_head;      // bytes
-  unsigned char* out;
-  int64_t out_row, out_head;  // bytes
+struct WeightParams {
   const int32_t* ctx;
-  int next_n, heads, group;
-  float scale;
+  const float* z;             // [rows][heads][pitch] logits (base 2)
+  const float* lse2;          // [rows][heads]
+  int64_t pitch;
   int64_t window;
-  float* lse;                 // nullable
-  float* ml;                  // workspace: [rows*heads][2] maximum and sum
-  float* z;                   // workspace: [rows*heads][cap] logits, or null
+  int32_t cap, next_n, heads;
   const float* sums;
   int64_t sums_s0;
   float* sums_out;
   int64_t sums_out_s0;
-  uint32_t* err;
 };
 
-template <typename T> __device__ __forceinline__ float to_f(T x) { return (float)x; }
-
-template <typename T, typename KV>
-__global__ void __launch_bounds__(kWarps * 32)
-row_kernel(const DenseParams p) {
-  __shared__ float s_m[kWarps], s_l[kWarps], s_acc[kWarps][kMaxDim];
-  const int rh = blockIdx.x, h = rh % p.heads, row = rh / p.heads;
-  const int b = row / p.next_n, j = row % p.next_n, kvh = h / p.group;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.c.dim, per = D / 32;
-  const int64_t ctx = p.ctx[b];
-  const int64_t hi0 = ctx - p.next_n + j + 1;
-  const int64_t lo = p.window > 0 ? max((int64_t)0, hi0 - p.window) : 0;
-  const int64_t hi = min(hi0, (int64_t)p.c.cap);
-  if (ctx > p.c.cap && threadIdx.x == 0) report(p.err, QSA_DERR_CONTEXT);
-  const T* q = reinterpret_cast<const T*>(p.q + row * p.q_row + h * p.q_head);
-  const float ks = p.c.k_scale ? p.c.k_scale[kvh] : 1.f, vs = p.c.v_scale ? p.c.v_scale[kvh] : 1.f;
-  float qf[kMaxDim / 32], acc[kMaxDim / 32];
-  for (int i = 0; i < per; ++i) {
-    qf[i] = to_f(q[lane * per + i]);
-    acc[i] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int64_t e = lo + warp; e < hi; e += kWarps) {
-    const int32_t page = p.c.bt[(int64_t)b * p.c.bt_s0 + (e >> p.c.page_log2)];
-    float z = -INFINITY;
-    if (page < 0 || page >= p.c.num_pages) {
-      if (lane == 0) report(p.err, QSA_DERR_KV_PAGE);
-    } else {
-      const int64_t slot = e & (((int64_t)1 << p.c.page_log2) - 1);
-      const KV* k = reinterpret_cast<const KV*>(p.c.k + page * p.c.k_page + slot * p.c.k_token + kvh * p.c.k_head);
-      const KV* v = reinterpret_cast<const KV*>(p.c.v + page * p.c.v_page + slot * p.c.v_token + kvh * p.c.v_head);
-      float s = 0.f;
-      for (int i = 0; i < per; ++i) s = fmaf(qf[i], to_f(k[lane * per + i]), s);
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      z = s * ks * p.scale;
-      const float mn = fmaxf(m, z);
-      const float c = m == -INFINITY ? 0.f : expf(m - mn), w = expf(z - mn);
-      l = l * c + w;
-      for (int i = 0; i < per; ++i) acc[i] = acc[i] * c + w * to_f(v[lane * per + i]);
-      m = mn;
-    }
-    if (p.z && lane == 0) p.z[(int64_t)rh * p.c.cap + e] = z;
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  for (int i = 0; i < per; ++i) s_acc[warp][lane * per + i] = acc[i];
-  __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-  for (int w = 0; w < kWarps; ++w) L += s_m[w] == -INFINITY ? 0.f : s_l[w] * expf(s_m[w] - M);
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float o = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      if (s_m[w] != -INFINITY) o += s_acc[w][d] * expf(s_m[w] - M);
-    T* out = reinterpret_cast<T*>(p.out + row * p.out_row + h * p.out_head);
-    out[d] = (T)(M == -INFINITY ? 0.f : o / L * vs);
-  }
-  if (threadIdx.x == 0) {
-    if (p.lse) p.lse[rh] = M == -INFINITY ? -INFINITY : M + logf(L);
-    p.ml[2 * rh] = M;
-    p.ml[2 * rh + 1] = L;
-  }
-}
-
-__global__ void __launch_bounds__(256) weights_kernel(const DenseParams p) {
+// Thread: four entries of one request; the table's entries are a multiple of 8.
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightParams p) {
   const int b = blockIdx.y;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int e = ((int)blockIdx.x * kWeightThreads + threadIdx.x) * 4;
   const int64_t ctx = p.ctx[b];
-  if (e >= min(ctx, (int64_t)p.c.cap)) return;
-  float s = 0.f;
+  const int n = (int)min(ctx, (int64_t)p.cap);
+  if (e >= n) return;
+  pdl_wait();
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < p.next_n; ++j) {
     const int64_t hi = ctx - p.next_n + j + 1;
     const int64_t lo = p.window > 0 ? max((int64_t)0, hi - p.window) : 0;
-    if (e < lo || e >= hi) continue;
+    if (e + 3 < lo || e >= hi) continue;
+    const int64_t r0 = ((int64_t)b * p.next_n + j) * p.heads;
+    const bool in[4] = {e >= lo, e + 1 >= lo && e + 1 < hi, e + 2 >= lo && e + 2 < hi,
+                        e + 3 < hi};
+#pragma unroll 8
     for (int h = 0; h < p.heads; ++h) {
-      const int64_t rh = ((int64_t)b * p.next_n + j) * p.heads + h;
-      const float z = p.z[rh * p.c.cap + e];
-      if (z != -INFINITY) s += expf(z - p.ml[2 * rh]) / p.ml[2 * rh + 1];
+      const float4 z = *reinterpret_cast<const float4*>(p.z + (r0 + h) * p.pitch + e);
+      const float l = p.lse2[r0 + h];
+      // -inf (an absent entry): 0, also where the row saw nothing and l is -inf
+      s.x += in[0] && z.x != -INFINITY ? exp2f(z.x - l) : 0.f;
+      s.y += in[1] && z.y != -INFINITY ? exp2f(z.y - l) : 0.f;
+      s.z += in[2] && z.z != -INFINITY ? exp2f(z.z - l) : 0.f;
+      s.w += in[3] && z.w != -INFINITY ? exp2f(z.w - l) : 0.f;
     }
   }
-  p.sums_out[b * p.sums_out_s0 + e] = p.sums[b * p.sums_s0 + e] + s;
+  const float* src = p.sums + b * p.sums_s0 + e;
+  float* dst = p.sums_out + b * p.sums_out_s0 + e;
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (e + i < n) dst[i] = src[i] + v[i];
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// One of the cache's views as (dim, head, slot, page); a box is one head's
+// `rows` slots of up to 128 bytes, so that a row is one line of the swizzle.
+bool encode_view(CUtensorMap* map, const unsigned char* p, const CacheView& c, int esize,
+                 int64_t page, int64_t token, int64_t head, int rows) {
+  memset(map, 0, sizeof(*map));
+  if (c.num_pages == 0) return true;                       // no copy is ever issued
+  const auto fn = encode_fn();
+  if (!fn) return false;
+  const int row_bytes = c.dim * esize, inner = std::min(row_bytes, 128);
+  const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.heads,
+                              (cuuint64_t)1 << c.page_log2, (cuuint64_t)c.num_pages};
+  // a dimension of size 1 has any stride; the encoder wants a legal one
+  const cuuint64_t strides[3] = {(cuuint64_t)(head ? head : row_bytes), (cuuint64_t)token,
+                                 (cuuint64_t)(page ? page : token)};
+  const cuuint32_t box[4] = {(cuuint32_t)(inner / esize), 1, (cuuint32_t)rows, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(map, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
+            const_cast<unsigned char*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -135,6 +121,26 @@ bool sizes_ok(int64_t reqs, int64_t next_n, int64_t heads, int64_t kv_heads, int
   return reqs >= 0 && reqs <= QSA_CACHE_MAX_REQS && next_n >= 1 && next_n <= QSA_CACHE_MAX_NEXT &&
          kv_heads >= 1 && kv_heads <= QSA_CACHE_MAX_HEADS && heads >= 1 && heads % kv_heads == 0 &&
          heads * next_n <= 65536 && (dim == 64 || dim == 128 || dim == 256);
+}
+
+// The workspace: tiles before each request of a launch, the pieces of K/V
+// heads that the runs cut (at most two a run), then, when weights are asked
+// for, the rows' sums and logits.
+struct Layout {
+  size_t ml, o, lse2, z, total;
+};
+
+Layout layout_of(int64_t reqs, int64_t next_n, int64_t heads, int64_t kv_heads, int64_t dim,
+                 int64_t weight_cols) {
+  const size_t rows = (size_t)std::min<int64_t>(next_n * (heads / kv_heads), kPagedMaxRows);
+  const size_t all = (size_t)(reqs * next_n * heads);
+  Layout l;
+  l.ml = round256((kPagedBatch + 1) * sizeof(int32_t));
+  l.o = l.ml + round256(2 * kPagedMaxCtas * rows * 2 * sizeof(float));
+  l.lse2 = l.o + round256(2 * kPagedMaxCtas * rows * (size_t)dim * sizeof(float));
+  l.z = l.lse2 + (weight_cols > 0 ? round256(all * sizeof(float)) : 0);
+  l.total = l.z + all * (size_t)weight_cols * sizeof(float);
+  return l;
 }
 
 }  // namespace
@@ -146,9 +152,7 @@ extern "C" size_t qsa_paged_attention_workspace_bytes(
   if (!qsa::sizes_ok(num_reqs, next_n, num_heads, kv_heads, head_dim) || num_reqs == 0 ||
       weight_cols < 0 || weight_cols > INT32_MAX)
     return 0;
-  const __int128 rows = (__int128)num_reqs * next_n * num_heads;
-  const __int128 n = rows * 8 + 256 + rows * weight_cols * 4 + 256;
-  return n > ((__int128)1 << 60) ? 0 : (size_t)n;
+  return qsa::layout_of(num_reqs, next_n, num_heads, kv_heads, head_dim, weight_cols).total;
 }
 
 extern "C" qsa_status qsa_paged_attention(
@@ -160,7 +164,7 @@ extern "C" qsa_status qsa_paged_attention(
     qsa_stream_t stream) {
   using namespace qsa;
   using namespace qsa::cache_host;
-  DenseParams p{};
+  PagedParams p{};
   CacheSpans cs{};
   const qsa_status st = check_cache(cache, &p.c, &cs);
   if (st != QSA_OK) return st;
@@ -208,34 +212,73 @@ extern "C" qsa_status qsa_paged_attention(
   if (!workspace || workspace_bytes < need) return QSA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QSA_ERR_ALIGN;
   p.q = static_cast<const unsigned char*>(q);
-  p.q_row = q_strides[0] * 2;
-  p.q_head = q_strides[1] * 2;
+  p.q_row = R * next_n > 1 ? q_strides[0] * 2 : 0;
+  p.q_head = num_heads > 1 ? q_strides[1] * 2 : 0;
   p.out = static_cast<unsigned char*>(out);
-  p.out_row = out_strides[0] * 2;
-  p.out_head = out_strides[1] * 2;
+  p.out_row = R * next_n > 1 ? out_strides[0] * 2 : 0;
+  p.out_head = num_heads > 1 ? out_strides[1] * 2 : 0;
   p.ctx = context_lens;
   p.next_n = (int)next_n;
   p.heads = (int)num_heads;
   p.group = (int)(num_heads / cache->num_heads);
-  p.scale = scale;
+  p.rows = p.next_n * p.group;
+  p.chunks = (p.rows + kPagedMaxRows - 1) / kPagedMaxRows;
+  p.chunk_rows = std::min(p.rows, kPagedMaxRows);
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.window = window;
   p.lse = lse;
-  p.ml = static_cast<float*>(workspace);
-  const int64_t rows = R * next_n * num_heads;
-  if (weights) p.z = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + round256(rows * 8));
-  p.sums = weight_sums;
-  p.sums_s0 = weight_sums_stride0;
-  p.sums_out = weight_sums_out;
-  p.sums_out_s0 = weight_sums_out_stride0;
+  const Layout l = layout_of(R, next_n, num_heads, cache->num_heads, cache->head_dim,
+                             weights ? entries : 0);
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  p.pre = reinterpret_cast<int32_t*>(w);
+  p.part_ml = reinterpret_cast<float*>(w + l.ml);
+  p.part_o = reinterpret_cast<float*>(w + l.o);
+  if (weights && entries > 0) {
+    p.lse2 = reinterpret_cast<float*>(w + l.lse2);
+    p.z = reinterpret_cast<float*>(w + l.z);
+    p.z_pitch = entries;
+  }
   p.err = error_word;
   bind_calling_thread();
+  const bool bf16 = dtype == QSA_DT_BF16, fp8 = cache->dtype == QSA_DT_F8E4M3;
+  const int esize = fp8 ? 1 : 2;
+  const int wm = p.chunk_rows <= 16 ? 1 : p.chunk_rows <= 32 ? 2 : 4;
+  const int tile = paged_tile(p.c.dim * esize, wm);
+  const int rows = (int)std::min<int64_t>(cache->page_size, tile);
+  CUtensorMap kmap, vmap;
+  if (!encode_view(&kmap, p.c.k, p.c, esize, p.c.k_page, p.c.k_token, p.c.k_head, rows) ||
+      !encode_view(&vmap, p.c.v, p.c, esize, p.c.v_page, p.c.v_token, p.c.v_head, rows))
+    return QSA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool half = dtype == QSA_DT_F16, fp8 = cache->dtype == QSA_DT_F8E4M3;
-  auto kernel = half ? (fp8 ? row_kernel<__half, __nv_fp8_e4m3> : row_kernel<__half, __half>)
-                     : (fp8 ? row_kernel<__nv_bfloat16, __nv_fp8_e4m3>
-                            : row_kernel<__nv_bfloat16, __nv_bfloat16>);
-  kernel<<<(unsigned)rows, kWarps * 32, 0, s>>>(p);
-  if (weights && entries > 0)
-    weights_kernel<<<dim3((unsigned)((entries + 255) / 256), (unsigned)R), 256, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+  // a launch's tiles are counted in 31 bits
+  const int64_t per_row = std::max<int64_t>(1, ((int64_t)p.c.cap + tile - 1) / tile);
+  const int64_t step = std::max<int64_t>(1, std::min<int64_t>(kPagedBatch, INT32_MAX / per_row));
+  for (int64_t b0 = 0; b0 < R; b0 += step) {
+    p.b0 = (int32_t)b0;
+    p.batch = (int32_t)std::min<int64_t>(step, R - b0);
+    const cudaError_t e = p.c.dim == 64    ? launch_paged_64(p, bf16, fp8, kmap, vmap, s)
+                          : p.c.dim == 128 ? launch_paged_128(p, bf16, fp8, kmap, vmap, s)
+                                           : launch_paged_256(p, bf16, fp8, kmap, vmap, s);
+    if (e != cudaSuccess) return QSA_ERR_CUDA;
+  }
+  if (p.z) {
+    WeightParams wp{};
+    wp.ctx = context_lens;
+    wp.z = p.z;
+    wp.lse2 = p.lse2;
+    wp.pitch = p.z_pitch;
+    wp.window = window;
+    wp.cap = p.c.cap;
+    wp.next_n = p.next_n;
+    wp.heads = p.heads;
+    wp.sums = weight_sums;
+    wp.sums_s0 = weight_sums_stride0;
+    wp.sums_out = weight_sums_out;
+    wp.sums_out_s0 = weight_sums_out_stride0;
+    const int64_t per_cta = kWeightThreads * 4;
+    const dim3 grid((unsigned)((entries + per_cta - 1) / per_cta), (unsigned)R);
+    if (launch_after(weights_kernel, grid, dim3(kWeightThreads), 0, s, wp) != cudaSuccess)
+      return QSA_ERR_CUDA;
+  }
+  return QSA_OK;
 }

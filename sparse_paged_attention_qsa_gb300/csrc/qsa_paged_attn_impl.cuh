@@ -1,0 +1,918 @@
+// qsa_paged_attn_impl.cuh -- the kernels of the dense paged attention
+// (include/qsa_cache.h, qsa_paged_attention).
+//
+// For one K/V head of one request, its M = next_n * group query rows and its
+// entries e:  z_ie = c_i (q_i . k_e),  o_i = sum_e 2^(z_ie - m_i) v_e,
+// l_i = sum_e 2^(z_ie - m_i), m_i the running maximum; out = o / l.  4 M flops
+// for every K/V element of 1 or 2 bytes: for M <= 64 the bytes set the time, so
+// everything here serves one thing, that K and V stream through once at the
+// rate of the memory.
+//
+// paged_walk_kernel  The tiles (TT entries of one request and K/V head) of the
+//   whole batch, laid end to end, are cut into equal runs, one for each CTA
+//   of a single wave: every SM streams the same bytes whatever the lengths.
+//   One producer warp looks pages up and loads K and V tiles into a ring by
+//   TMA (swizzled, completion on mbarriers); four consumer warps share a
+//   tile: WM groups of 16 query rows by WK = 4 / WM slices of its tokens.
+//   Each warp keeps its rows' maximum, sum and output in registers: S = Q K^T
+//   and P V by mma.sync.m16n8k16 (binary32 accumulation) on fragments that
+//   ldmatrix reads from the ring.  (tcgen05 needs 64 or 128 rows and a round
+//   trip through tensor memory for the softmax; with at most 16 rows as a
+//   rule mma.sync is a third busy at the memory's rate.)  At a request's end,
+//   or the run's, the slices merge through shared memory into the output, or
+//   into a piece in the workspace when the K/V head's entries are cut.
+// paged_join_kernel  joins a cut K/V head's pieces.
+//
+// Rounding: q, K and V enter the products as they are (E4M3 as FP16, exactly;
+// BF16 queries of an E4M3 cache as FP16 after a power-of-two scaling of the
+// row, where only bits 2^-25 below the row's largest element can be lost).
+// The weights multiply V as a pair of 16-bit values (a value and what its
+// rounding left), 2^-16 (BF16) or 2^-22 (FP16) relative, for up to 32 rows
+// over a 16-bit cache, where the second product is free; above that, and for
+// E4M3 caches (whose elements carry 4 bits), as one value.  They are scaled by
+// 2^15 so that small ones stay normal in FP16.
+#pragma once
+
+#include "qsa_paged_attn.h"
+#include "qsa_device.cuh"
+#include "qsa_internal.h"
+
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <mutex>
+
+namespace qsa {
+namespace {
+
+constexpr int kConsumers = 128;                // threads of the four consumer warps
+constexpr int kWalkThreads = kConsumers + 32;  // + the producer warp
+constexpr float kShift = 15.f;                 // weights are 2^(z - m + kShift)
+constexpr int kJoinThreads = 256;
+constexpr size_t kSmemPerSm = 233472, kSmemPerCta = 232448, kSmemReserved = 1024;
+
+template <bool kFp8, int D, int WM>
+struct WalkShape {
+  static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);        // a token's K (or V) of one head
+  static constexpr int TT = paged_tile(kRowBytes, WM);
+  static constexpr int WK = 4 / WM;
+  static constexpr int kSlice = TT / WK;                      // tokens of a warp
+  static constexpr int NS = kSlice / 16;                      // in steps of 16
+  static constexpr int kChunkBytes = kRowBytes < 128 ? kRowBytes : 128;   // TMA inner extent
+  static constexpr int kChunks = kRowBytes / kChunkBytes;
+  static constexpr int kSlot = TT * kRowBytes;
+  static constexpr int kQPitch = D + 8;                       // halves; + 16 B against conflicts
+  static constexpr int kQBytes = 16 * WM * kQPitch * 2;
+  static constexpr int kMergeCols = D == 256 ? 32 : 64;
+  static constexpr int kMergeBytes = 64 * (kMergeCols + 4) * 4;
+  static constexpr int kStage = ((kQBytes > kMergeBytes ? kQBytes : kMergeBytes) + 1023) & ~1023;
+  static constexpr int kMisc = 2688;                          // barriers and small tables
+  static constexpr int kFixed = 1024 + kStage + kMisc + (kPagedBatch + 1) * 4;
+  static constexpr int fit(size_t smem) {
+    const int n = (int)((smem - kFixed) / kSlot);
+    return n > 16 ? 16 : n;
+  }
+  // two CTAs an SM where three slots of each fit, else one
+  static constexpr int kCtas = fit(kSmemPerSm / 2 - kSmemReserved) >= 3 ? 2 : 1;
+  static constexpr int S = kCtas == 2 ? fit(kSmemPerSm / 2 - kSmemReserved) : fit(kSmemPerCta);
+  static constexpr size_t kSmem = (size_t)kFixed + (size_t)S * kSlot;
+  static_assert(S >= 3, "the ring needs K, V and one slot ahead");
+  static constexpr bool kPair = !kFp8 && WM <= 2;             // weights as value + remainder
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+template <bool kBf16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (kBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (lo, hi) rounded to 16 bits each, lo in the low half
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool kBf16>
+__device__ __forceinline__ float2 unpack2(uint32_t r) {
+  if constexpr (kBf16)
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+  else
+    return h2f2(r);
+}
+// the two E4M3 values in the low (high) half of x, as FP16
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+      : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
+      : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+}
+
+// Visible entries [lo, hi) of token j of a request with ctx cached tokens,
+// cut to what the table holds.
+__device__ __forceinline__ void visible(const PagedParams& p, int32_t ctx, int j, int32_t* lo,
+                                        int32_t* hi) {
+  const int64_t h = (int64_t)ctx - p.next_n + j + 1;
+  const int64_t l = p.window > 0 ? h - p.window : 0;
+  const int64_t cap = p.c.cap;
+  *hi = (int32_t)(h < 0 ? 0 : h < cap ? h : cap);
+  *lo = (int32_t)(l < 0 ? 0 : l < cap ? l : cap);
+}
+
+// The tiles a request's entries span, [*first, *first + count).
+template <int TT>
+__device__ __forceinline__ int32_t tiles_of(const PagedParams& p, int32_t ctx, int32_t* first) {
+  int32_t lo, hi, x;
+  visible(p, ctx, 0, &lo, &x);
+  visible(p, ctx, p.next_n - 1, &x, &hi);
+  *first = lo / TT;
+  return hi > lo ? (hi + TT - 1) / TT - lo / TT : 0;
+}
+
+// Where a run's tile w lies: request, unit within it (K/V head, row chunk)
+// and tile; pre[] holds the tiles before each request.
+struct TileAt {
+  int b, unit, tile, count;
+};
+__device__ __forceinline__ TileAt tile_at(const int32_t* pre, int batch, int units, int64_t w) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((int64_t)pre[mid] * units <= w) lo = mid; else hi = mid - 1;
+  }
+  TileAt t;
+  t.b = lo;
+  t.count = pre[lo + 1] - pre[lo];
+  const int64_t in = w - (int64_t)pre[lo] * units;
+  t.unit = t.count > 0 ? (int)(in / t.count) : 0;
+  t.tile = t.count > 0 ? (int)(in - (int64_t)t.unit * t.count) : 0;
+  return t;
+}
+
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+template <typename T, bool kFp8, int D, int WM>
+__global__ void __launch_bounds__(kWalkThreads, (WalkShape<kFp8, D, WM>::kCtas))
+paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+  using W = WalkShape<kFp8, D, WM>;
+  constexpr bool kBf16 = sizeof(T) == 2 && !kFp8 && __is_same(T, __nv_bfloat16);   // product type
+  constexpr int TT = W::TT, WK = W::WK, NS = W::NS, S = W::S;
+  extern __shared__ unsigned char smem_raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  unsigned char* base = smem_raw + pad;
+  const uint32_t ring = raw + pad;
+  unsigned char* stage = base + S * W::kSlot;              // queries, or merge buffer
+  const uint32_t stage_a = ring + S * W::kSlot;
+  unsigned char* misc = stage + W::kStage;                 // kMisc bytes
+  const uint32_t bar_full = stage_a + W::kStage, bar_empty = bar_full + 8 * 16;
+  uint32_t* boxes = reinterpret_cast<uint32_t*>(misc + 256);       // [16] valid boxes of a slot
+  float* s_ml = reinterpret_cast<float*>(misc + 384);              // [4][16][2]
+  float* s_qs = reinterpret_cast<float*>(misc + 896);              // [64] row multipliers
+  float* s_f = reinterpret_cast<float*>(misc + 1152);              // [4][16] merge factors
+  float* s_row = reinterpret_cast<float*>(misc + 1408);            // [64] merged sums
+  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 1920);
+  int32_t* s_scan = reinterpret_cast<int32_t*>(misc + 1984);       // [160]
+  int32_t* pre = reinterpret_cast<int32_t*>(misc + W::kMisc);      // [batch + 1]
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 4);
+    }
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // tiles before each request
+  {
+    const int per = (p.batch + kWalkThreads - 1) / kWalkThreads;
+    const int lo = min(p.batch, tid * per), hi = min(p.batch, lo + per);
+    int32_t sum = 0, x;
+    for (int b = lo; b < hi; ++b) {
+      const int32_t n = tiles_of<TT>(p, p.ctx[p.b0 + b], &x);
+      pre[b + 1] = n;
+      sum += n;
+    }
+    s_scan[tid] = sum;
+    __syncthreads();
+    int32_t before = 0;
+    for (int i = 0; i < (lo < hi ? tid : 0); ++i) before += s_scan[i];
+    for (int b = lo; b < hi; ++b) {
+      before += pre[b + 1];
+      pre[b + 1] = before;
+    }
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+  }
+  const int units = p.c.heads * p.chunks;
+  const int64_t total = (int64_t)pre[p.batch] * units;
+  const int64_t w_begin = total * blockIdx.x / gridDim.x;
+  const int64_t w_end = total * (blockIdx.x + 1) / gridDim.x;
+  if (blockIdx.x == 0)
+    for (int i = tid; i <= p.batch; i += kWalkThreads) p.pre[i] = pre[i];
+
+  int issued = 0;                                          // producer: slots filled
+  if (warp == 4) {
+    // ---------------- producer ----------------
+    const int lg = p.c.page_log2;
+    const int box_rows = min(TT, 1 << lg);
+    const int n_boxes = TT / box_rows;
+    const int tile_cols = max(1, TT >> lg);
+    int chunk_b = -1, chunk_col = 0;                       // 32 page ids, one a lane
+    int32_t chunk_id = -1;
+    int64_t w = w_begin;
+    bool stop = false;
+    while (w < w_end && !stop) {
+      TileAt at = tile_at(pre, p.batch, units, w);
+      const int32_t ctx = p.ctx[p.b0 + at.b];
+      int32_t first, lo, hi, x;
+      tiles_of<TT>(p, ctx, &first);
+      visible(p, ctx, 0, &lo, &x);
+      visible(p, ctx, p.next_n - 1, &x, &hi);
+      if (ctx > p.c.cap && lane == 0) report(p.err, QSA_DERR_CONTEXT);
+      const int32_t* row = p.c.bt + (int64_t)(p.b0 + at.b) * p.c.bt_s0;
+      const int head = at.unit / p.chunks;
+      const int64_t seg_end = min(w_end, w + (at.count - at.tile));
+      for (int t = at.tile; w < seg_end; ++w, ++t) {
+        const int32_t e0 = (first + t) * TT;
+        const int col = e0 >> lg;
+        if (at.b != chunk_b || col < chunk_col || col + tile_cols > chunk_col + 32) {
+          chunk_b = at.b;
+          chunk_col = col;
+          chunk_id = col + lane < p.c.cols ? __ldg(row + col + lane) : -1;
+        }
+        const int32_t id = __shfl_sync(0xffffffffu, chunk_id,
+                                       col - chunk_col + (lane < n_boxes ? (lane * box_rows) >> lg : 0));
+        const int32_t be = e0 + lane * box_rows;
+        const bool want = lane < n_boxes && be < hi && be + box_rows > lo;
+        const bool good = want && id >= 0 && id < p.c.num_pages;
+        const uint32_t mask = __ballot_sync(0xffffffffu, good);
+        if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int s = issued % S, round = issued / S;
+          if (round > 0 && !stop) {
+            bool ok = *s_abort == 0 && mbar_wait(bar_empty + 8 * s, (uint32_t)((round - 1) & 1));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+              if (lane == 0) {
+                *s_abort = 1;
+                report(p.err, QSA_DERR_TIMEOUT);
+              }
+              stop = true;
+            }
+          }
+          if (stop) break;
+          const uint32_t full = bar_full + 8 * s, dst = ring + s * W::kSlot;
+          if (lane == 0) {
+            boxes[s] = mask;
+            mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * W::kRowBytes));
+          }
+          __syncwarp();
+          if (good) {
+#pragma unroll
+            for (int i = 0; i < W::kChunks; ++i)
+              tma_load_4d(dst + i * (TT * W::kChunkBytes) + lane * box_rows * W::kChunkBytes,
+                          kv ? &vmap : &kmap, i * (W::kChunkBytes / (kFp8 ? 1 : 2)), head,
+                          be & ((1 << lg) - 1), id, full);
+          }
+          ++issued;
+        }
+        if (stop) break;
+      }
+    }
+  } else {
+    // ---------------- consumers ----------------
+    const int wm = warp % WM, wk = warp / WM;
+    const int g = lane >> 2, q4 = lane & 3;
+    const int lg = p.c.page_log2;
+    const int box_log2 = min(lg, TT == 128 ? 7 : 6);
+    const uint32_t all_boxes = TT >> box_log2 >= 32 ? 0xffffffffu : (1u << (TT >> box_log2)) - 1u;
+    // ldmatrix source rows and the swizzle's exclusive-or, constant a lane
+    const int k_row = wk * W::kSlice + ((lane >> 4) << 3) + (lane & 7);       // K: tokens by 8
+    const int v_row = wk * W::kSlice + (((lane >> 3) & 1) << 3) + (lane & 7); // V: transposed
+    const int k_c = (lane >> 3) & 1, v_c = lane >> 4;
+    const int sw = W::kChunkBytes == 128 ? lane & 7 : (lane >> 1) & 3;
+    constexpr int kPer = W::kChunkBytes / 16;              // 16-byte pieces of a TMA row
+    const auto piece = [&](int row, int c) -> uint32_t {
+      return (uint32_t)((c / kPer) * (TT * W::kChunkBytes) + row * W::kChunkBytes +
+                        (((c % kPer) ^ sw) << 4));
+    };
+    const uint32_t q_addr = stage_a + (uint32_t)(((wm * 16 + (lane & 15)) * W::kQPitch +
+                                                  (lane >> 4) * 8) * 2);
+    // a slot's wait: after a time-out every warp runs its loops to their end
+    // without waiting, so that the barriers between them stay matched
+    const auto wait_full = [&](int n) {
+      if (*s_abort == 0 && !mbar_wait(bar_full + 8 * (n % S), (uint32_t)((n / S) & 1))) {
+        *s_abort = 1;
+        if (lane == 0) report(p.err, QSA_DERR_TIMEOUT);
+      }
+    };
+    const auto release = [&](int n) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_empty + 8 * (n % S));
+    };
+
+    // requests without a visible entry: zeros, here because no tile is theirs
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+      if (pre[b + 1] != pre[b]) continue;
+      const int64_t r0 = (int64_t)(p.b0 + b) * p.next_n;
+      if (p.ctx[p.b0 + b] > p.c.cap && tid == 0) report(p.err, QSA_DERR_CONTEXT);
+      const int n = p.next_n * p.heads;
+      for (int i = tid; i < n * (D / 8); i += kConsumers) {
+        const int rh = i / (D / 8), o = i % (D / 8);
+        *reinterpret_cast<uint4*>(p.out + (r0 + rh / p.heads) * p.out_row +
+                                  (rh % p.heads) * p.out_head + o * 16) = make_uint4(0, 0, 0, 0);
+      }
+      for (int i = tid; i < n; i += kConsumers) {
+        if (p.lse) p.lse[r0 * p.heads + i] = -INFINITY;
+        if (p.lse2) p.lse2[r0 * p.heads + i] = -INFINITY;
+      }
+    }
+
+    int slot = 0;                                          // slots consumed
+    int64_t w = w_begin;
+    while (w < w_end) {
+      const TileAt at = tile_at(pre, p.batch, units, w);
+      const int64_t seg_begin = w, seg_end = min(w_end, w + (at.count - at.tile));
+      const bool whole = at.tile == 0 && seg_end - seg_begin == at.count;
+      const int32_t ctx = p.ctx[p.b0 + at.b];
+      const int head = at.unit / p.chunks, chunk = at.unit - head * p.chunks;
+      const int row0 = chunk * kPagedMaxRows;
+      const int n_rows = min(kPagedMaxRows, p.rows - row0);          // of this unit
+      int32_t first, lo_all, hi_all, x;
+      tiles_of<TT>(p, ctx, &first);
+      visible(p, ctx, 0, &lo_all, &x);
+      visible(p, ctx, p.next_n - 1, &x, &hi_all);
+      // the entries that every row sees: a tile inside them needs no mask
+      int32_t lo_in, hi_in;
+      visible(p, ctx, p.next_n - 1, &lo_in, &x);
+      visible(p, ctx, 0, &x, &hi_in);
+      const int64_t q_row = (int64_t)(p.b0 + at.b) * p.next_n;
+      const auto row_ptr = [&](const unsigned char* t, int64_t rs, int64_t hs, int i) {
+        const int r = row0 + i, j = r / p.group;
+        return t + (q_row + j) * rs + (int64_t)(head * p.group + r - j * p.group) * hs;
+      };
+
+      // queries into shared memory (the merge buffer before is done with)
+      consumers_sync();
+      T* qs = reinterpret_cast<T*>(stage);
+      for (int i = tid; i < 16 * WM * (D / 8); i += kConsumers) {
+        const int r = i / (D / 8), o = i % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < n_rows)
+          v = *reinterpret_cast<const uint4*>(row_ptr(p.q, p.q_row, p.q_head, r) + o * 16);
+        if constexpr (!kFp8) {
+          *reinterpret_cast<uint4*>(qs + r * W::kQPitch + o * 8) = v;
+        } else {
+          // D/8 lanes (8, 16 or 32, aligned) hold one row: its largest
+          // magnitude, then FP16 with each 16 dims in the order in which the
+          // E4M3 fragments hold them (dims 4q, 4q+1 at 2q and 4q+2, 4q+3 at 8 + 2q)
+          float f[8];
+          const T* h = reinterpret_cast<const T*>(&v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = (float)h[k];
+          float mul = 1.f;
+          if constexpr (__is_same(T, __nv_bfloat16)) {
+            float a = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(f[k]));
+#pragma unroll
+            for (int k = 1; k < D / 8; k <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, k));
+            // largest magnitude to [2^14, 2^15); as it is where that has no exponent
+            const int e = (int)(__float_as_uint(a) >> 23);
+            if (e > 0 && e < 255) {
+              const int up = min(14 + 127 - e, 120);
+              mul = __uint_as_float((uint32_t)(127 - up) << 23);      // 2^-up
+              const float by = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) f[k] *= by;
+            }
+          }
+          uint32_t* dst = reinterpret_cast<uint32_t*>(qs + r * W::kQPitch + (o >> 1) * 16);
+          const int q2 = (o & 1) * 2;
+          dst[q2] = pack2<false>(f[0], f[1]);
+          dst[q2 + 4] = pack2<false>(f[2], f[3]);
+          dst[q2 + 1] = pack2<false>(f[4], f[5]);
+          dst[q2 + 5] = pack2<false>(f[6], f[7]);
+          if (o == 0) s_qs[r] = mul;
+        }
+      }
+      consumers_sync();
+
+      // this thread's rows: wm*16 + g and + 8
+      float mult[2];
+      int32_t row_lo[2], row_hi[2];
+      int row_j[2];
+      float* zp[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = wm * 16 + g + 8 * k, r = min(row0 + i, p.rows - 1);
+        row_j[k] = r / p.group;
+        visible(p, ctx, row_j[k], &row_lo[k], &row_hi[k]);
+        mult[k] = p.scale_log2;
+        if constexpr (kFp8) {
+          if (p.c.k_scale) mult[k] *= p.c.k_scale[head];
+          mult[k] *= s_qs[wm * 16 + g + 8 * k];
+        }
+        zp[k] = p.z && i < n_rows
+                    ? p.z + ((q_row + row_j[k]) * p.heads + head * p.group + r - row_j[k] * p.group) *
+                                p.z_pitch
+                    : nullptr;
+      }
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float o[D / 8][4];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+      for (int t = at.tile; w < seg_end; ++w, ++t) {
+        const int32_t e0 = (first + t) * TT;
+        const int32_t we = e0 + wk * W::kSlice;            // the warp's first entry
+        const int ks = slot, vs = slot + 1;
+        slot += 2;
+        wait_full(ks);
+        const uint32_t mask = boxes[ks % S];
+        const bool edge = e0 < lo_in || e0 + TT > hi_in || mask != all_boxes;
+        const uint32_t kb = ring + (ks % S) * W::kSlot, vb = ring + (vs % S) * W::kSlot;
+        float sc[NS][2][4];
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            sc[s][n][0] = sc[s][n][1] = sc[s][n][2] = sc[s][n][3] = 0.f;
+        if constexpr (!kFp8) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t a[4];
+            ldsm4(q_addr + kk * 32, a);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+              uint32_t b[4];
+              ldsm4(kb + piece(k_row + s * 16, 2 * kk + k_c), b);
+              mma16816<kBf16>(sc[s][0], a, b[0], b[1]);
+              mma16816<kBf16>(sc[s][1], a, b[2], b[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) {
+            uint32_t a0[4], a1[4];
+            ldsm4(q_addr + kk * 64, a0);
+            ldsm4(q_addr + kk * 64 + 32, a1);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+              uint32_t b[4];
+              ldsm4(kb + piece(k_row + s * 16, 2 * kk + k_c), b);
+              mma16816<false>(sc[s][0], a0, e4m3_lo(b[0]), e4m3_hi(b[0]));
+              mma16816<false>(sc[s][1], a0, e4m3_lo(b[2]), e4m3_hi(b[2]));
+              mma16816<false>(sc[s][0], a1, e4m3_lo(b[1]), e4m3_hi(b[1]));
+              mma16816<false>(sc[s][1], a1, e4m3_lo(b[3]), e4m3_hi(b[3]));
+            }
+          }
+        }
+        release(ks);
+        // logits; masked ones -inf
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float z0 = sc[s][n][2 * k] * mult[k], z1 = sc[s][n][2 * k + 1] * mult[k];
+              const int32_t e = we + s * 16 + n * 8 + 2 * q4;
+              if (edge) {
+                const bool in = (mask >> ((e - e0) >> box_log2)) & 1u;
+                if (!in || e < row_lo[k] || e >= row_hi[k]) z0 = -INFINITY;
+                if (!in || e + 1 < row_lo[k] || e + 1 >= row_hi[k]) z1 = -INFINITY;
+              }
+              if (zp[k] && e < hi_all) *reinterpret_cast<float2*>(zp[k] + e) = make_float2(z0, z1);
+              sc[s][n][2 * k] = z0;
+              sc[s][n][2 * k + 1] = z1;
+              mx[k] = fmaxf(mx[k], fmaxf(z0, z1));
+            }
+        float ref[2], al[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+          const float mn = fmaxf(m[k], mx[k]);
+          ref[k] = mn == -INFINITY ? 0.f : mn - kShift;    // nothing seen yet: all weights 0
+          al[k] = mn == m[k] ? 1.f : ex2(m[k] - mn);
+          m[k] = mn;
+        }
+        if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+          l[0] *= al[0];
+          l[1] *= al[1];
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= al[0];
+            o[i][1] *= al[0];
+            o[i][2] *= al[1];
+            o[i][3] *= al[1];
+          }
+        }
+        uint32_t ph[NS][4], pl[NS][4];
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float p0 = ex2(sc[s][n][2 * k] - ref[k]), p1 = ex2(sc[s][n][2 * k + 1] - ref[k]);
+              l[k] += p0 + p1;
+              const uint32_t h = pack2<kBf16>(p0, p1);
+              ph[s][2 * n + k] = h;
+              if constexpr (W::kPair) {
+                const float2 f = unpack2<kBf16>(h);
+                pl[s][2 * n + k] = pack2<kBf16>(p0 - f.x, p1 - f.y);
+              }
+            }
+        wait_full(vs);
+        if (!edge) {
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            if constexpr (!kFp8) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                uint32_t b[4];
+                ldsm4t(vb + piece(v_row + s * 16, 2 * i + v_c), b);
+                mma16816<kBf16>(o[2 * i], ph[s], b[0], b[1]);
+                mma16816<kBf16>(o[2 * i + 1], ph[s], b[2], b[3]);
+                if constexpr (W::kPair) {
+                  mma16816<kBf16>(o[2 * i], pl[s], b[0], b[1]);
+                  mma16816<kBf16>(o[2 * i + 1], pl[s], b[2], b[3]);
+                }
+              }
+            } else {
+              // a pair of tokens' E4M3 bytes (t0: d0 d1, t1: d0 d1) regrouped
+              // by dim, so that even and odd dims are two products
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) {
+                uint32_t b[4];
+                ldsm4t(vb + piece(v_row + s * 16, 2 * i + v_c), b);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) b[k] = __byte_perm(b[k], 0, 0x3120);
+                mma16816<false>(o[4 * i], ph[s], e4m3_lo(b[0]), e4m3_lo(b[1]));
+                mma16816<false>(o[4 * i + 1], ph[s], e4m3_hi(b[0]), e4m3_hi(b[1]));
+                mma16816<false>(o[4 * i + 2], ph[s], e4m3_lo(b[2]), e4m3_lo(b[3]));
+                mma16816<false>(o[4 * i + 3], ph[s], e4m3_hi(b[2]), e4m3_hi(b[3]));
+              }
+            }
+          }
+        } else {
+          // Some entry is hidden from some row.  0 times what it holds may be
+          // NaN, so V enters with the hidden entries zeroed, once for each
+          // token j that has rows here, and only those rows take the result.
+          const int ja = min(row0 + wm * 16, p.rows - 1) / p.group;
+          const int jb = min(row0 + wm * 16 + 15, p.rows - 1) / p.group;
+          for (int j = ja; j <= jb; ++j) {
+            int32_t lo, hi;
+            visible(p, ctx, j, &lo, &hi);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+              uint32_t keep[2];
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                const int32_t e = we + s * 16 + n * 8 + 2 * q4;
+                const bool in = (mask >> ((e - e0) >> box_log2)) & 1u;
+                keep[n] = (in && e >= lo && e < hi ? 0xffffu : 0u) |
+                          (in && e + 1 >= lo && e + 1 < hi ? 0xffff0000u : 0u);
+              }
+              const auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816<kBf16>(d, ph[s], b0 & keep[0], b1 & keep[1]);
+                if constexpr (W::kPair) mma16816<kBf16>(d, pl[s], b0 & keep[0], b1 & keep[1]);
+                if (row_j[0] == j) {
+                  acc[0] += d[0];
+                  acc[1] += d[1];
+                }
+                if (row_j[1] == j) {
+                  acc[2] += d[2];
+                  acc[3] += d[3];
+                }
+              };
+              if constexpr (!kFp8) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  uint32_t b[4];
+                  ldsm4t(vb + piece(v_row + s * 16, 2 * i + v_c), b);
+                  add(o[2 * i], b[0], b[1]);
+                  add(o[2 * i + 1], b[2], b[3]);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                  uint32_t b[4];
+                  ldsm4t(vb + piece(v_row + s * 16, 2 * i + v_c), b);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) b[k] = __byte_perm(b[k], 0, 0x3120);
+                  add(o[4 * i], e4m3_lo(b[0]), e4m3_lo(b[1]));
+                  add(o[4 * i + 1], e4m3_hi(b[0]), e4m3_hi(b[1]));
+                  add(o[4 * i + 2], e4m3_lo(b[2]), e4m3_lo(b[3]));
+                  add(o[4 * i + 3], e4m3_hi(b[2]), e4m3_hi(b[3]));
+                }
+              }
+            }
+          }
+        }
+        release(vs);
+      }
+
+      // ---- the segment's end: merge the WK slices, write the result or a piece
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+        if (q4 == 0) {
+          s_ml[(warp * 16 + g + 8 * k) * 2] = m[k];
+          s_ml[(warp * 16 + g + 8 * k) * 2 + 1] = l[k];
+        }
+      }
+      consumers_sync();
+      const int id = 2 * blockIdx.x + (seg_begin == w_begin ? 0 : 1);
+      if (tid < 16 * WM) {
+        const int i = tid, rm = i >> 4, rr = i & 15;       // row i: warps rm, rm + WM, ...
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int k = 0; k < WK; ++k) M = fmaxf(M, s_ml[((rm + k * WM) * 16 + rr) * 2]);
+#pragma unroll
+        for (int k = 0; k < WK; ++k) {
+          const int at_w = (rm + k * WM) * 16 + rr;
+          const float f = M == -INFINITY ? 0.f : ex2(s_ml[at_w * 2] - M);
+          s_f[at_w] = f;
+          L += s_ml[at_w * 2 + 1] * f;
+        }
+        s_row[i] = L;
+        if (i < n_rows) {
+          if (whole) {
+            const int r = row0 + i, j = r / p.group;
+            const int64_t rh = (q_row + j) * p.heads + head * p.group + r - j * p.group;
+            const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
+            if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
+            if (p.lse2) p.lse2[rh] = t;
+          } else {
+            float* ml = p.part_ml + ((int64_t)id * p.chunk_rows + i) * 2;
+            ml[0] = M;
+            ml[1] = L;
+          }
+        }
+      }
+      consumers_sync();
+      {
+        float f[2];
+        f[0] = s_f[warp * 16 + g];
+        f[1] = s_f[warp * 16 + g + 8];
+        float* buf = reinterpret_cast<float*>(stage);
+        constexpr int C = W::kMergeCols, P = C + 4;        // columns at a time, and their pitch
+        const float vscale = kFp8 && p.c.v_scale ? p.c.v_scale[head] : 1.f;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += C) {
+#pragma unroll
+          for (int i = 0; i < C / 8; ++i) {
+            const int n = c0 / 8 + i;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float* b = buf + (warp * 16 + g + 8 * k) * P;
+              // 0 * f where no entry was seen: the accumulators are 0 there
+              const float x = o[n][2 * k] * f[k], y = o[n][2 * k + 1] * f[k];
+              if constexpr (!kFp8) {
+                *reinterpret_cast<float2*>(b + i * 8 + 2 * q4) = make_float2(x, y);
+              } else {
+                // tile n holds the even (odd) dims of the 16 from 16 (n / 2)
+                b[(i >> 1) * 16 + 4 * q4 + (i & 1)] = x;
+                b[(i >> 1) * 16 + 4 * q4 + 2 + (i & 1)] = y;
+              }
+            }
+          }
+          consumers_sync();
+          for (int i = tid; i < n_rows * (C / 8); i += kConsumers) {
+            const int r = i / (C / 8), c = (i % (C / 8)) * 8;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < WK; ++k) {
+              const float4* b = reinterpret_cast<const float4*>(
+                  buf + (((r >> 4) + k * WM) * 16 + (r & 15)) * P + c);
+              const float4 a0 = b[0], a1 = b[1];
+              v[0] += a0.x; v[1] += a0.y; v[2] += a0.z; v[3] += a0.w;
+              v[4] += a1.x; v[5] += a1.y; v[6] += a1.z; v[7] += a1.w;
+            }
+            if (whole) {
+              const float L = s_row[r];
+              const float inv = L == 0.f ? 0.f : vscale / L;   // 0: a row that saw nothing
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                h[k] = pack2<__is_same(T, __nv_bfloat16)>(v[2 * k] * inv, v[2 * k + 1] * inv);
+              *reinterpret_cast<uint4*>(
+                  const_cast<unsigned char*>(row_ptr(p.out, p.out_row, p.out_head, r)) +
+                  (c0 + c) * 2) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+              float4* d = reinterpret_cast<float4*>(
+                  p.part_o + ((int64_t)id * p.chunk_rows + r) * D + c0 + c);
+              d[0] = make_float4(v[0], v[1], v[2], v[3]);
+              d[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+          }
+          if (c0 + C < D) consumers_sync();
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // after a time-out, let the copies this CTA issued land before it exits
+  if (*s_abort != 0 && warp == 4 && lane == 0) {
+    for (int n = issued > S ? issued - S : 0; n < issued; ++n)
+      mbar_wait(bar_full + 8 * (n % S), (uint32_t)((n / S) & 1), kDrainLimitNs);
+  }
+  pdl_trigger();
+}
+
+// CTA (c, i): row i of the unit that the start of CTA c's run cuts, if it is
+// the first such cut.
+template <typename T, int D, int TT>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int ctas) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+  __shared__ float s_w[kPagedMaxCtas], s_red[kJoinThreads / 32];
+  __shared__ __align__(16) float s_o[kGroups][D];
+  const int tid = threadIdx.x, c = blockIdx.x + 1, i = blockIdx.y;
+  pdl_wait();
+  const int units = p.c.heads * p.chunks;
+  const int64_t total = (int64_t)p.pre[p.batch] * units;
+  const int64_t cut = total * c / ctas;
+  if (cut >= total || cut == 0) return;
+  const TileAt at = tile_at(p.pre, p.batch, units, cut);
+  if (at.tile == 0) return;                                // between units
+  const int64_t x0 = cut - at.tile, x1 = x0 + at.count - 1;
+  const auto cta_of = [&](int64_t x) { return (int)(((x + 1) * ctas + total - 1) / total) - 1; };
+  const int c0 = cta_of(x0), c1 = cta_of(x1);
+  if (total * (c - 1) / ctas > x0) return;                 // an earlier run cuts it too
+  const int head = at.unit / p.chunks, chunk = at.unit - head * p.chunks;
+  const int row0 = chunk * kPagedMaxRows, r = row0 + i;
+  if (i >= min(kPagedMaxRows, p.rows - row0)) return;
+  const int n = c1 - c0 + 1;
+  const auto id_of = [&](int k) {                          // piece k's place in the workspace
+    return 2 * (c0 + k) + (k == 0 && total * c0 / ctas != x0 ? 1 : 0);
+  };
+  // runs without a tile lie between two others' and hold no piece
+  const auto has = [&](int k) {
+    return total * (c0 + k) / ctas < total * (c0 + k + 1) / ctas;
+  };
+  float mx = -INFINITY;
+  for (int k = tid; k < n; k += kJoinThreads) {
+    const float mk = has(k) ? p.part_ml[((int64_t)id_of(k) * p.chunk_rows + i) * 2] : -INFINITY;
+    s_w[k] = mk;
+    mx = fmaxf(mx, mk);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if ((tid & 31) == 0) s_red[tid >> 5] = mx;
+  __syncthreads();
+  float M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, s_red[k]);
+  __syncthreads();
+  float sum = 0.f;
+  for (int k = tid; k < n; k += kJoinThreads) {
+    const float f = s_w[k] == -INFINITY ? 0.f : ex2(s_w[k] - M);
+    s_w[k] = f;
+    if (has(k)) sum += f * p.part_ml[((int64_t)id_of(k) * p.chunk_rows + i) * 2 + 1];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((tid & 31) == 0) s_red[tid >> 5] = sum;
+  __syncthreads();
+  float L = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinThreads / 32; ++k) L += s_red[k];
+  const int grp = tid / kLanes, ln = tid % kLanes;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = grp; k < n; k += kGroups) {
+    const float f = s_w[k];
+    if (!has(k)) continue;
+    const float4 v = *reinterpret_cast<const float4*>(
+        p.part_o + ((int64_t)id_of(k) * p.chunk_rows + i) * D + ln * 4);
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  }
+  *reinterpret_cast<float4*>(&s_o[grp][ln * 4]) = acc;
+  __syncthreads();
+  const int64_t q_row = (int64_t)(p.b0 + at.b) * p.next_n;
+  const int j = r / p.group, h = head * p.group + r - j * p.group;
+  if (tid < D) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) v += s_o[k][tid];
+    const float vscale = p.c.v_scale ? p.c.v_scale[head] : 1.f;
+    T* out = reinterpret_cast<T*>(p.out + (q_row + j) * p.out_row + h * p.out_head);
+    out[tid] = from_f<T>(L == 0.f ? 0.f : v * (vscale / L));
+  }
+  if (tid == 0) {
+    const int64_t rh = (q_row + j) * p.heads + h;
+    const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
+    if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
+    if (p.lse2) p.lse2[rh] = t;
+  }
+}
+
+template <typename T, bool kFp8, int D, int WM>
+cudaError_t launch_walk(const PagedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                        cudaStream_t st) {
+  using W = WalkShape<kFp8, D, WM>;
+  static std::mutex mu;
+  static int sms[64];                                      // 0: not set up on that device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int n_sms;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (sms[dev] == 0) {
+      int n = 0;
+      e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+      if (e != cudaSuccess) return e;
+      e = cudaFuncSetAttribute(paged_walk_kernel<T, kFp8, D, WM>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W::kSmem);
+      if (e != cudaSuccess) return e;
+      sms[dev] = n;
+    }
+    n_sms = sms[dev];
+  }
+  const int64_t most = (int64_t)p.batch * p.c.heads * p.chunks *
+                       (((int64_t)p.c.cap + W::TT - 1) / W::TT);
+  int64_t ctas = (int64_t)n_sms * W::kCtas;
+  if (ctas > kPagedMaxCtas) ctas = kPagedMaxCtas;
+  if (ctas > most) ctas = most > 0 ? most : 1;
+  paged_walk_kernel<T, kFp8, D, WM><<<(unsigned)ctas, kWalkThreads, W::kSmem, st>>>(p, kmap, vmap);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ctas == 1) return e;             // one run cuts nothing
+  return launch_after(paged_join_kernel<T, D, W::TT>, dim3((unsigned)ctas - 1, (unsigned)p.chunk_rows),
+                      dim3(kJoinThreads), 0, st, p, (int)ctas);
+}
+
+template <typename T, bool kFp8, int D>
+cudaError_t launch_rows(const PagedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                        cudaStream_t st) {
+  if (p.chunk_rows <= 16) return launch_walk<T, kFp8, D, 1>(p, kmap, vmap, st);
+  if (p.chunk_rows <= 32) return launch_walk<T, kFp8, D, 2>(p, kmap, vmap, st);
+  return launch_walk<T, kFp8, D, 4>(p, kmap, vmap, st);
+}
+
+template <int D>
+cudaError_t launch_paged(const PagedParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, cudaStream_t st) {
+  if (bf16) return fp8 ? launch_rows<__nv_bfloat16, true, D>(p, kmap, vmap, st)
+                       : launch_rows<__nv_bfloat16, false, D>(p, kmap, vmap, st);
+  return fp8 ? launch_rows<__half, true, D>(p, kmap, vmap, st)
+             : launch_rows<__half, false, D>(p, kmap, vmap, st);
+}
+
+}  // namespace
+}  // namespace qsa
