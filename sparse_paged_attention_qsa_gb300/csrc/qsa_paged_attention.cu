@@ -50,8 +50,8 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightPar
   const int e = ((int)blockIdx.x * kWeightThreads + threadIdx.x) * 4;
   const int64_t ctx = p.ctx[b];
   const int n = (int)min(ctx, (int64_t)p.cap);
+  pdl_wait();          // on every path: the grid's end must mean the walk's and the join's
   if (e >= n) return;
-  pdl_wait();
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < p.next_n; ++j) {
     const int64_t hi = ctx - p.next_n + j + 1;
@@ -112,7 +112,9 @@ bool encode_view(CUtensorMap* map, const unsigned char* p, const CacheView& c, i
   return fn(map, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
             const_cast<unsigned char*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            // no wider than a row: what follows it is another head's
+            row_bytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                             : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }

@@ -8,9 +8,10 @@
 // everything here serves one thing, that K and V stream through once at the
 // rate of the memory.
 //
-// paged_walk_kernel  The tiles (TT entries of one request and K/V head) of the
-//   whole batch, laid end to end, are cut into equal runs, one for each CTA
-//   of a single wave: every SM streams the same bytes whatever the lengths.
+// paged_walk_kernel  The requests' tiles (TT entries), laid end to end, are cut
+//   into equal runs; a CTA walks one run for one K/V head (and up to 64 of its
+//   query rows), all CTAs in a single wave: every SM streams the same bytes
+//   whatever the lengths.
 //   One producer warp looks pages up and loads K and V tiles into a ring by
 //   TMA (swizzled, completion on mbarriers); four consumer warps share a
 //   tile: WM groups of 16 query rows by WK = 4 / WM slices of its tokens.
@@ -37,6 +38,7 @@
 #include "qsa_device.cuh"
 #include "qsa_internal.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -50,7 +52,8 @@ constexpr int kConsumers = 128;                // threads of the four consumer w
 constexpr int kWalkThreads = kConsumers + 32;  // + the producer warp
 constexpr float kShift = 15.f;                 // weights are 2^(z - m + kShift)
 constexpr int kJoinThreads = 256;
-constexpr size_t kSmemPerSm = 233472, kSmemPerCta = 232448, kSmemReserved = 1024;
+constexpr int kMaxSlots = 16;
+constexpr size_t kSmemPerSm = 233472, kSmemReserved = 1024;   // 228 KB, 1 KB of it a CTA's own
 
 template <bool kFp8, int D, int WM>
 struct WalkShape {
@@ -60,22 +63,25 @@ struct WalkShape {
   static constexpr int kSlice = TT / WK;                      // tokens of a warp
   static constexpr int NS = kSlice / 16;                      // in steps of 16
   static constexpr int kChunkBytes = kRowBytes < 128 ? kRowBytes : 128;   // TMA inner extent
-  static constexpr int kChunks = kRowBytes / kChunkBytes;
-  static constexpr int kSlot = TT * kRowBytes;
+  static constexpr int kChunks = kRowBytes / kChunkBytes;     // copies that fill a slot
+  static constexpr int kSlot = TT * kRowBytes;                // K (or V) of a tile
   static constexpr int kQPitch = D + 8;                       // halves; + 16 B against conflicts
   static constexpr int kQBytes = 16 * WM * kQPitch * 2;
-  static constexpr int kMergeCols = D == 256 ? 32 : 64;
+  static constexpr int kMergeCols = 32;
   static constexpr int kMergeBytes = 64 * (kMergeCols + 4) * 4;
   static constexpr int kStage = ((kQBytes > kMergeBytes ? kQBytes : kMergeBytes) + 1023) & ~1023;
-  static constexpr int kMisc = 2688;                          // barriers and small tables
+  static constexpr int kMisc = 2816;                          // barriers and small tables
   static constexpr int kFixed = 1024 + kStage + kMisc + (kPagedBatch + 1) * 4;
-  static constexpr int fit(size_t smem) {
-    const int n = (int)((smem - kFixed) / kSlot);
-    return n > 16 ? 16 : n;
+  static constexpr int fit(int ctas) {
+    const int n = (int)((kSmemPerSm / ctas - kSmemReserved - kFixed) / kSlot);
+    return n > kMaxSlots ? kMaxSlots : n;
   }
-  // two CTAs an SM where three slots of each fit, else one
-  static constexpr int kCtas = fit(kSmemPerSm / 2 - kSmemReserved) >= 3 ? 2 : 1;
-  static constexpr int S = kCtas == 2 ? fit(kSmemPerSm / 2 - kSmemReserved) : fit(kSmemPerCta);
+#ifdef QSA_PAGED_CTAS
+  static constexpr int kCtas = QSA_PAGED_CTAS;
+#else
+  static constexpr int kCtas = D == 256 ? 1 : 2;
+#endif
+  static constexpr int S = fit(kCtas);
   static constexpr size_t kSmem = (size_t)kFixed + (size_t)S * kSlot;
   static_assert(S >= 3, "the ring needs K, V and one slot ahead");
   static constexpr bool kPair = !kFp8 && WM <= 2;             // weights as value + remainder
@@ -163,24 +169,38 @@ __device__ __forceinline__ int32_t tiles_of(const PagedParams& p, int32_t ctx, i
   return hi > lo ? (hi + TT - 1) / TT - lo / TT : 0;
 }
 
-// Where a run's tile w lies: request, unit within it (K/V head, row chunk)
-// and tile; pre[] holds the tiles before each request.
-struct TileAt {
-  int b, unit, tile, count;
+// The requests' tiles laid end to end and cut into n runs: the first `more`
+// runs take each + 1 tiles.
+struct Runs {
+  int32_t total, each, more;
 };
-__device__ __forceinline__ TileAt tile_at(const int32_t* pre, int batch, int units, int64_t w) {
+__device__ __forceinline__ Runs cut_runs(int32_t total, int n) {
+  Runs r;
+  r.total = total;
+  r.each = total / n;
+  r.more = total - r.each * n;
+  return r;
+}
+__device__ __forceinline__ int32_t run_start(const Runs& r, int c) {
+  return r.each * c + min(c, r.more);
+}
+__device__ __forceinline__ int run_of(const Runs& r, int32_t x) {
+  const int32_t big = (r.each + 1) * r.more;
+  return x < big ? x / (r.each + 1) : r.more + (x - big) / r.each;
+}
+
+// Where tile w lies: the request, the tile within it and how many it has;
+// pre[] holds the tiles before each request.
+struct TileAt {
+  int b, tile, count;
+};
+__device__ __forceinline__ TileAt tile_at(const int32_t* pre, int batch, int32_t w) {
   int lo = 0, hi = batch - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)pre[mid] * units <= w) lo = mid; else hi = mid - 1;
+    if (pre[mid] <= w) lo = mid; else hi = mid - 1;
   }
-  TileAt t;
-  t.b = lo;
-  t.count = pre[lo + 1] - pre[lo];
-  const int64_t in = w - (int64_t)pre[lo] * units;
-  t.unit = t.count > 0 ? (int)(in / t.count) : 0;
-  t.tile = t.count > 0 ? (int)(in - (int64_t)t.unit * t.count) : 0;
-  return t;
+  return TileAt{lo, w - pre[lo], pre[lo + 1] - pre[lo]};
 }
 
 template <typename T>
@@ -247,10 +267,13 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     if (tid == 0) pre[0] = 0;
     __syncthreads();
   }
-  const int units = p.c.heads * p.chunks;
-  const int64_t total = (int64_t)pre[p.batch] * units;
-  const int64_t w_begin = total * blockIdx.x / gridDim.x;
-  const int64_t w_end = total * (blockIdx.x + 1) / gridDim.x;
+  // CTA: run * units + unit, so that the K/V heads of the same tokens, whose
+  // elements lie side by side, are read at the same time
+  const int units = p.c.heads * p.chunks, run = blockIdx.x / units, unit = blockIdx.x % units;
+  const int head = unit / p.chunks, chunk = unit - head * p.chunks;
+  const Runs runs = cut_runs(pre[p.batch], gridDim.x / units);
+  const int32_t w_begin = run_start(runs, run), w_end = run_start(runs, run + 1);
+  pdl_trigger();     // every CTA is resident: the join may be put in place (it waits)
   if (blockIdx.x == 0)
     for (int i = tid; i <= p.batch; i += kWalkThreads) p.pre[i] = pre[i];
 
@@ -263,10 +286,11 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     const int tile_cols = max(1, TT >> lg);
     int chunk_b = -1, chunk_col = 0;                       // 32 page ids, one a lane
     int32_t chunk_id = -1;
-    int64_t w = w_begin;
+    int32_t w = w_begin;
+    int s = 0, round = 0;                                  // ring position of the next slot
     bool stop = false;
     while (w < w_end && !stop) {
-      TileAt at = tile_at(pre, p.batch, units, w);
+      const TileAt at = tile_at(pre, p.batch, w);
       const int32_t ctx = p.ctx[p.b0 + at.b];
       int32_t first, lo, hi, x;
       tiles_of<TT>(p, ctx, &first);
@@ -274,8 +298,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       visible(p, ctx, p.next_n - 1, &x, &hi);
       if (ctx > p.c.cap && lane == 0) report(p.err, QSA_DERR_CONTEXT);
       const int32_t* row = p.c.bt + (int64_t)(p.b0 + at.b) * p.c.bt_s0;
-      const int head = at.unit / p.chunks;
-      const int64_t seg_end = min(w_end, w + (at.count - at.tile));
+      const int32_t seg_end = min(w_end, w + (at.count - at.tile));
       for (int t = at.tile; w < seg_end; ++w, ++t) {
         const int32_t e0 = (first + t) * TT;
         const int col = e0 >> lg;
@@ -293,8 +316,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const int s = issued % S, round = issued / S;
-          if (round > 0 && !stop) {
+          if (round > 0) {
             bool ok = *s_abort == 0 && mbar_wait(bar_empty + 8 * s, (uint32_t)((round - 1) & 1));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
@@ -303,9 +325,9 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                 report(p.err, QSA_DERR_TIMEOUT);
               }
               stop = true;
+              break;
             }
           }
-          if (stop) break;
           const uint32_t full = bar_full + 8 * s, dst = ring + s * W::kSlot;
           if (lane == 0) {
             boxes[s] = mask;
@@ -320,6 +342,10 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                           be & ((1 << lg) - 1), id, full);
           }
           ++issued;
+          if (++s == S) {
+            s = 0;
+            ++round;
+          }
         }
         if (stop) break;
       }
@@ -337,23 +363,29 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     const int k_c = (lane >> 3) & 1, v_c = lane >> 4;
     const int sw = W::kChunkBytes == 128 ? lane & 7 : (lane >> 1) & 3;
     constexpr int kPer = W::kChunkBytes / 16;              // 16-byte pieces of a TMA row
-    const auto piece = [&](int row, int c) -> uint32_t {
-      return (uint32_t)((c / kPer) * (TT * W::kChunkBytes) + row * W::kChunkBytes +
-                        (((c % kPer) ^ sw) << 4));
+    const auto piece = [&](int row, int c) -> uint32_t {   // 16-byte piece c of a row of a slot
+      return (uint32_t)(row * W::kChunkBytes + ((c ^ sw) << 4));
     };
     const uint32_t q_addr = stage_a + (uint32_t)(((wm * 16 + (lane & 15)) * W::kQPitch +
                                                   (lane >> 4) * 8) * 2);
     // a slot's wait: after a time-out every warp runs its loops to their end
     // without waiting, so that the barriers between them stay matched
-    const auto wait_full = [&](int n) {
-      if (*s_abort == 0 && !mbar_wait(bar_full + 8 * (n % S), (uint32_t)((n / S) & 1))) {
+    int slot = 0;                                          // ring position, and its phase
+    uint32_t phase = 0;
+    const auto wait_full = [&]() {
+      if (!mbar_try_wait(bar_full + 8 * slot, phase) && *s_abort == 0 &&
+          !mbar_wait(bar_full + 8 * slot, phase)) {
         *s_abort = 1;
         if (lane == 0) report(p.err, QSA_DERR_TIMEOUT);
       }
     };
-    const auto release = [&](int n) {
+    const auto release = [&]() {                           // and on to the next slot
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_empty + 8 * (n % S));
+      if (lane == 0) mbar_arrive(bar_empty + 8 * slot);
+      if (++slot == S) {
+        slot = 0;
+        phase ^= 1;
+      }
     };
 
     // requests without a visible entry: zeros, here because no tile is theirs
@@ -373,16 +405,14 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       }
     }
 
-    int slot = 0;                                          // slots consumed
-    int64_t w = w_begin;
+    const int row0 = chunk * kPagedMaxRows;
+    const int n_rows = min(kPagedMaxRows, p.rows - row0);            // of this unit
+    int32_t w = w_begin;
     while (w < w_end) {
-      const TileAt at = tile_at(pre, p.batch, units, w);
-      const int64_t seg_begin = w, seg_end = min(w_end, w + (at.count - at.tile));
+      const TileAt at = tile_at(pre, p.batch, w);
+      const int32_t seg_begin = w, seg_end = min(w_end, w + (at.count - at.tile));
       const bool whole = at.tile == 0 && seg_end - seg_begin == at.count;
       const int32_t ctx = p.ctx[p.b0 + at.b];
-      const int head = at.unit / p.chunks, chunk = at.unit - head * p.chunks;
-      const int row0 = chunk * kPagedMaxRows;
-      const int n_rows = min(kPagedMaxRows, p.rows - row0);          // of this unit
       int32_t first, lo_all, hi_all, x;
       tiles_of<TT>(p, ctx, &first);
       visible(p, ctx, 0, &lo_all, &x);
@@ -471,49 +501,48 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       for (int t = at.tile; w < seg_end; ++w, ++t) {
         const int32_t e0 = (first + t) * TT;
         const int32_t we = e0 + wk * W::kSlice;            // the warp's first entry
-        const int ks = slot, vs = slot + 1;
-        slot += 2;
-        wait_full(ks);
-        const uint32_t mask = boxes[ks % S];
+        wait_full();
+        const uint32_t mask = boxes[slot];
         const bool edge = e0 < lo_in || e0 + TT > hi_in || mask != all_boxes;
-        const uint32_t kb = ring + (ks % S) * W::kSlot, vb = ring + (vs % S) * W::kSlot;
         float sc[NS][2][4];
 #pragma unroll
         for (int s = 0; s < NS; ++s)
 #pragma unroll
           for (int n = 0; n < 2; ++n)
             sc[s][n][0] = sc[s][n][1] = sc[s][n][2] = sc[s][n][3] = 0.f;
-        if constexpr (!kFp8) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t a[4];
-            ldsm4(q_addr + kk * 32, a);
+        for (int ch = 0; ch < W::kChunks; ++ch) {
+          const uint32_t kb = ring + slot * W::kSlot + ch * (TT * W::kChunkBytes);
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-              uint32_t b[4];
-              ldsm4(kb + piece(k_row + s * 16, 2 * kk + k_c), b);
-              mma16816<kBf16>(sc[s][0], a, b[0], b[1]);
-              mma16816<kBf16>(sc[s][1], a, b[2], b[3]);
-            }
-          }
-        } else {
+          for (int kk = 0; kk < kPer / 2; ++kk) {          // two 16-byte pieces at a time
+            const int k = ch * (kPer / 2) + kk;
+            if constexpr (!kFp8) {
+              uint32_t a[4];
+              ldsm4(q_addr + k * 32, a);
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            uint32_t a0[4], a1[4];
-            ldsm4(q_addr + kk * 64, a0);
-            ldsm4(q_addr + kk * 64 + 32, a1);
+              for (int st = 0; st < NS; ++st) {
+                uint32_t b[4];
+                ldsm4(kb + piece(k_row + st * 16, 2 * kk + k_c), b);
+                mma16816<kBf16>(sc[st][0], a, b[0], b[1]);
+                mma16816<kBf16>(sc[st][1], a, b[2], b[3]);
+              }
+            } else {
+              uint32_t a0[4], a1[4];
+              ldsm4(q_addr + k * 64, a0);
+              ldsm4(q_addr + k * 64 + 32, a1);
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-              uint32_t b[4];
-              ldsm4(kb + piece(k_row + s * 16, 2 * kk + k_c), b);
-              mma16816<false>(sc[s][0], a0, e4m3_lo(b[0]), e4m3_hi(b[0]));
-              mma16816<false>(sc[s][1], a0, e4m3_lo(b[2]), e4m3_hi(b[2]));
-              mma16816<false>(sc[s][0], a1, e4m3_lo(b[1]), e4m3_hi(b[1]));
-              mma16816<false>(sc[s][1], a1, e4m3_lo(b[3]), e4m3_hi(b[3]));
+              for (int st = 0; st < NS; ++st) {
+                uint32_t b[4];
+                ldsm4(kb + piece(k_row + st * 16, 2 * kk + k_c), b);
+                mma16816<false>(sc[st][0], a0, e4m3_lo(b[0]), e4m3_hi(b[0]));
+                mma16816<false>(sc[st][1], a0, e4m3_lo(b[2]), e4m3_hi(b[2]));
+                mma16816<false>(sc[st][0], a1, e4m3_lo(b[1]), e4m3_hi(b[1]));
+                mma16816<false>(sc[st][1], a1, e4m3_lo(b[3]), e4m3_hi(b[3]));
+              }
             }
           }
         }
-        release(ks);
+        release();
         // logits; masked ones -inf
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -571,95 +600,92 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                 pl[s][2 * n + k] = pack2<kBf16>(p0 - f.x, p1 - f.y);
               }
             }
-        wait_full(vs);
-        if (!edge) {
+        // P V.  Where some entry is hidden from some row, 0 times what it holds
+        // may be NaN: V enters with the hidden entries zeroed, once for each
+        // token j that has rows here, and only those rows take the result.
+        const int ja = min(row0 + wm * 16, p.rows - 1) / p.group;
+        const int jb = edge ? min(row0 + wm * 16 + 15, p.rows - 1) / p.group : ja;
+        wait_full();
 #pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            if constexpr (!kFp8) {
+        for (int ch = 0; ch < W::kChunks; ++ch) {
+          const uint32_t vb = ring + slot * W::kSlot + ch * (TT * W::kChunkBytes);
+          constexpr int kTiles = kFp8 ? kPer * 2 : kPer;   // of 8 dims
+          if (!edge) {
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
+            for (int st = 0; st < NS; ++st)
+#pragma unroll
+              for (int i = 0; i < kPer / 2; ++i) {
                 uint32_t b[4];
-                ldsm4t(vb + piece(v_row + s * 16, 2 * i + v_c), b);
-                mma16816<kBf16>(o[2 * i], ph[s], b[0], b[1]);
-                mma16816<kBf16>(o[2 * i + 1], ph[s], b[2], b[3]);
-                if constexpr (W::kPair) {
-                  mma16816<kBf16>(o[2 * i], pl[s], b[0], b[1]);
-                  mma16816<kBf16>(o[2 * i + 1], pl[s], b[2], b[3]);
-                }
-              }
-            } else {
-              // a pair of tokens' E4M3 bytes (t0: d0 d1, t1: d0 d1) regrouped
-              // by dim, so that even and odd dims are two products
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i) {
-                uint32_t b[4];
-                ldsm4t(vb + piece(v_row + s * 16, 2 * i + v_c), b);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) b[k] = __byte_perm(b[k], 0, 0x3120);
-                mma16816<false>(o[4 * i], ph[s], e4m3_lo(b[0]), e4m3_lo(b[1]));
-                mma16816<false>(o[4 * i + 1], ph[s], e4m3_hi(b[0]), e4m3_hi(b[1]));
-                mma16816<false>(o[4 * i + 2], ph[s], e4m3_lo(b[2]), e4m3_lo(b[3]));
-                mma16816<false>(o[4 * i + 3], ph[s], e4m3_hi(b[2]), e4m3_hi(b[3]));
-              }
-            }
-          }
-        } else {
-          // Some entry is hidden from some row.  0 times what it holds may be
-          // NaN, so V enters with the hidden entries zeroed, once for each
-          // token j that has rows here, and only those rows take the result.
-          const int ja = min(row0 + wm * 16, p.rows - 1) / p.group;
-          const int jb = min(row0 + wm * 16 + 15, p.rows - 1) / p.group;
-          for (int j = ja; j <= jb; ++j) {
-            int32_t lo, hi;
-            visible(p, ctx, j, &lo, &hi);
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-              uint32_t keep[2];
-#pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                const int32_t e = we + s * 16 + n * 8 + 2 * q4;
-                const bool in = (mask >> ((e - e0) >> box_log2)) & 1u;
-                keep[n] = (in && e >= lo && e < hi ? 0xffffu : 0u) |
-                          (in && e + 1 >= lo && e + 1 < hi ? 0xffff0000u : 0u);
-              }
-              const auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816<kBf16>(d, ph[s], b0 & keep[0], b1 & keep[1]);
-                if constexpr (W::kPair) mma16816<kBf16>(d, pl[s], b0 & keep[0], b1 & keep[1]);
-                if (row_j[0] == j) {
-                  acc[0] += d[0];
-                  acc[1] += d[1];
-                }
-                if (row_j[1] == j) {
-                  acc[2] += d[2];
-                  acc[3] += d[3];
-                }
-              };
-              if constexpr (!kFp8) {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                  uint32_t b[4];
-                  ldsm4t(vb + piece(v_row + s * 16, 2 * i + v_c), b);
-                  add(o[2 * i], b[0], b[1]);
-                  add(o[2 * i + 1], b[2], b[3]);
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                  uint32_t b[4];
-                  ldsm4t(vb + piece(v_row + s * 16, 2 * i + v_c), b);
+                ldsm4t(vb + piece(v_row + st * 16, 2 * i + v_c), b);
+                if constexpr (!kFp8) {
+                  float(&o0)[4] = o[ch * kTiles + 2 * i], (&o1)[4] = o[ch * kTiles + 2 * i + 1];
+                  mma16816<kBf16>(o0, ph[st], b[0], b[1]);
+                  mma16816<kBf16>(o1, ph[st], b[2], b[3]);
+                  if constexpr (W::kPair) {
+                    mma16816<kBf16>(o0, pl[st], b[0], b[1]);
+                    mma16816<kBf16>(o1, pl[st], b[2], b[3]);
+                  }
+                } else {
+                  // a pair of tokens' E4M3 bytes (t0: d0 d1, t1: d0 d1) regrouped
+                  // by dim, so that even and odd dims are two products
 #pragma unroll
                   for (int k = 0; k < 4; ++k) b[k] = __byte_perm(b[k], 0, 0x3120);
-                  add(o[4 * i], e4m3_lo(b[0]), e4m3_lo(b[1]));
-                  add(o[4 * i + 1], e4m3_hi(b[0]), e4m3_hi(b[1]));
-                  add(o[4 * i + 2], e4m3_lo(b[2]), e4m3_lo(b[3]));
-                  add(o[4 * i + 3], e4m3_hi(b[2]), e4m3_hi(b[3]));
+                  const int n = ch * kTiles + 4 * i;
+                  mma16816<false>(o[n], ph[st], e4m3_lo(b[0]), e4m3_lo(b[1]));
+                  mma16816<false>(o[n + 1], ph[st], e4m3_hi(b[0]), e4m3_hi(b[1]));
+                  mma16816<false>(o[n + 2], ph[st], e4m3_lo(b[2]), e4m3_lo(b[3]));
+                  mma16816<false>(o[n + 3], ph[st], e4m3_hi(b[2]), e4m3_hi(b[3]));
+                }
+              }
+          } else {
+            for (int j = ja; j <= jb; ++j) {
+              int32_t lo, hi;
+              visible(p, ctx, j, &lo, &hi);
+#pragma unroll
+              for (int st = 0; st < NS; ++st) {
+                uint32_t keep[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  const int32_t e = we + st * 16 + n * 8 + 2 * q4;
+                  const bool in = (mask >> ((e - e0) >> box_log2)) & 1u;
+                  keep[n] = (in && e >= lo && e < hi ? 0xffffu : 0u) |
+                            (in && e + 1 >= lo && e + 1 < hi ? 0xffff0000u : 0u);
+                }
+                const auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+                  float d[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816<kBf16>(d, ph[st], b0 & keep[0], b1 & keep[1]);
+                  if constexpr (W::kPair) mma16816<kBf16>(d, pl[st], b0 & keep[0], b1 & keep[1]);
+                  if (row_j[0] == j) {
+                    acc[0] += d[0];
+                    acc[1] += d[1];
+                  }
+                  if (row_j[1] == j) {
+                    acc[2] += d[2];
+                    acc[3] += d[3];
+                  }
+                };
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) {
+                  uint32_t b[4];
+                  ldsm4t(vb + piece(v_row + st * 16, 2 * i + v_c), b);
+                  if constexpr (!kFp8) {
+                    add(o[ch * kTiles + 2 * i], b[0], b[1]);
+                    add(o[ch * kTiles + 2 * i + 1], b[2], b[3]);
+                  } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) b[k] = __byte_perm(b[k], 0, 0x3120);
+                    const int n = ch * kTiles + 4 * i;
+                    add(o[n], e4m3_lo(b[0]), e4m3_lo(b[1]));
+                    add(o[n + 1], e4m3_hi(b[0]), e4m3_hi(b[1]));
+                    add(o[n + 2], e4m3_lo(b[2]), e4m3_lo(b[3]));
+                    add(o[n + 3], e4m3_hi(b[2]), e4m3_hi(b[3]));
+                  }
                 }
               }
             }
           }
         }
-        release(vs);
+        release();
       }
 
       // ---- the segment's end: merge the WK slices, write the result or a piece
@@ -768,42 +794,36 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     for (int n = issued > S ? issued - S : 0; n < issued; ++n)
       mbar_wait(bar_full + 8 * (n % S), (uint32_t)((n / S) & 1), kDrainLimitNs);
   }
-  pdl_trigger();
 }
 
-// CTA (c, i): row i of the unit that the start of CTA c's run cuts, if it is
-// the first such cut.
-template <typename T, int D, int TT>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int ctas) {
+// CTA (c - 1, i, unit): row i of the unit in the request that the start of run
+// c cuts, if it is the first such cut.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int n_runs) {
   constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
   __shared__ float s_w[kPagedMaxCtas], s_red[kJoinThreads / 32];
   __shared__ __align__(16) float s_o[kGroups][D];
-  const int tid = threadIdx.x, c = blockIdx.x + 1, i = blockIdx.y;
+  const int tid = threadIdx.x, c = blockIdx.x + 1, i = blockIdx.y, unit = blockIdx.z;
   pdl_wait();
   const int units = p.c.heads * p.chunks;
-  const int64_t total = (int64_t)p.pre[p.batch] * units;
-  const int64_t cut = total * c / ctas;
-  if (cut >= total || cut == 0) return;
-  const TileAt at = tile_at(p.pre, p.batch, units, cut);
-  if (at.tile == 0) return;                                // between units
-  const int64_t x0 = cut - at.tile, x1 = x0 + at.count - 1;
-  const auto cta_of = [&](int64_t x) { return (int)(((x + 1) * ctas + total - 1) / total) - 1; };
-  const int c0 = cta_of(x0), c1 = cta_of(x1);
-  if (total * (c - 1) / ctas > x0) return;                 // an earlier run cuts it too
-  const int head = at.unit / p.chunks, chunk = at.unit - head * p.chunks;
+  const Runs runs = cut_runs(p.pre[p.batch], n_runs);
+  const int32_t cut = run_start(runs, c);
+  if (cut >= runs.total) return;
+  const TileAt at = tile_at(p.pre, p.batch, cut);
+  const int32_t x0 = cut - at.tile;
+  // between requests, or an earlier run's start cuts this one too
+  if (at.tile == 0 || run_start(runs, c - 1) > x0) return;
+  const int c0 = c - 1, c1 = run_of(runs, x0 + at.count - 1);
+  const int head = unit / p.chunks, chunk = unit - head * p.chunks;
   const int row0 = chunk * kPagedMaxRows, r = row0 + i;
   if (i >= min(kPagedMaxRows, p.rows - row0)) return;
   const int n = c1 - c0 + 1;
-  const auto id_of = [&](int k) {                          // piece k's place in the workspace
-    return 2 * (c0 + k) + (k == 0 && total * c0 / ctas != x0 ? 1 : 0);
-  };
-  // runs without a tile lie between two others' and hold no piece
-  const auto has = [&](int k) {
-    return total * (c0 + k) / ctas < total * (c0 + k + 1) / ctas;
-  };
+  // piece k's place in the workspace: a run's first segment, or its other one
+  const int second = run_start(runs, c0) != x0;
+  const auto id_of = [&](int k) { return 2 * ((c0 + k) * units + unit) + (k == 0 ? second : 0); };
   float mx = -INFINITY;
   for (int k = tid; k < n; k += kJoinThreads) {
-    const float mk = has(k) ? p.part_ml[((int64_t)id_of(k) * p.chunk_rows + i) * 2] : -INFINITY;
+    const float mk = p.part_ml[((int64_t)id_of(k) * p.chunk_rows + i) * 2];
     s_w[k] = mk;
     mx = fmaxf(mx, mk);
   }
@@ -819,7 +839,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   for (int k = tid; k < n; k += kJoinThreads) {
     const float f = s_w[k] == -INFINITY ? 0.f : ex2(s_w[k] - M);
     s_w[k] = f;
-    if (has(k)) sum += f * p.part_ml[((int64_t)id_of(k) * p.chunk_rows + i) * 2 + 1];
+    sum += f * p.part_ml[((int64_t)id_of(k) * p.chunk_rows + i) * 2 + 1];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -833,7 +853,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
 #pragma unroll 4
   for (int k = grp; k < n; k += kGroups) {
     const float f = s_w[k];
-    if (!has(k)) continue;
     const float4 v = *reinterpret_cast<const float4*>(
         p.part_o + ((int64_t)id_of(k) * p.chunk_rows + i) * D + ln * 4);
     acc.x += f * v.x;
@@ -885,16 +904,18 @@ cudaError_t launch_walk(const PagedParams& p, const CUtensorMap& kmap, const CUt
     }
     n_sms = sms[dev];
   }
-  const int64_t most = (int64_t)p.batch * p.c.heads * p.chunks *
-                       (((int64_t)p.c.cap + W::TT - 1) / W::TT);
-  int64_t ctas = (int64_t)n_sms * W::kCtas;
-  if (ctas > kPagedMaxCtas) ctas = kPagedMaxCtas;
-  if (ctas > most) ctas = most > 0 ? most : 1;
-  paged_walk_kernel<T, kFp8, D, WM><<<(unsigned)ctas, kWalkThreads, W::kSmem, st>>>(p, kmap, vmap);
+  // runs: as many as fill one wave, no more than there can be tiles
+  const int units = p.c.heads * p.chunks;
+  const int64_t tiles = (int64_t)p.batch * (((int64_t)p.c.cap + W::TT - 1) / W::TT);
+  int64_t n_runs = std::min(n_sms * W::kCtas, kPagedMaxCtas) / units;
+  n_runs = std::max<int64_t>(1, std::min(n_runs, tiles));
+  paged_walk_kernel<T, kFp8, D, WM>
+      <<<(unsigned)(n_runs * units), kWalkThreads, W::kSmem, st>>>(p, kmap, vmap);
   e = cudaGetLastError();
-  if (e != cudaSuccess || ctas == 1) return e;             // one run cuts nothing
-  return launch_after(paged_join_kernel<T, D, W::TT>, dim3((unsigned)ctas - 1, (unsigned)p.chunk_rows),
-                      dim3(kJoinThreads), 0, st, p, (int)ctas);
+  if (e != cudaSuccess || n_runs == 1) return e;           // one run cuts nothing
+  return launch_after(paged_join_kernel<T, D>,
+                      dim3((unsigned)n_runs - 1, (unsigned)p.chunk_rows, (unsigned)units),
+                      dim3(kJoinThreads), 0, st, p, (int)n_runs);
 }
 
 template <typename T, bool kFp8, int D>
