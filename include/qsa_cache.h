@@ -8,9 +8,9 @@
  *
  * Conventions (device pointers, fail-closed validation, no allocation,
  * asynchronous launch on the caller's stream, device-side data errors
- * reported in *error_word, any host thread) are those of qsa.h.  Operators
- * with a workspace clobber it; calls that share one must not overlap on the
- * GPU.  No call keeps anything from another.
+ * reported in *error_word, any host thread) are those of qsa.h.  The
+ * attention clobbers its workspace (the others need none); calls that share
+ * one must not overlap on the GPU.  No call keeps anything from another.
  *
  * A request's cached tokens are its ENTRIES 0, 1, 2, ...: entry e of request
  * b is slot e % page_size of page block_tables[b, e / page_size].  Without
@@ -36,6 +36,8 @@ extern "C" {
 #define QSA_CACHE_MAX_PAGE 65536   /* to 65536 */
 #define QSA_CACHE_MAX_HEADS 1024   /* K/V heads; query heads x next_n <= 65536 */
 #define QSA_CACHE_MAX_REQS 65535   /* requests in one call */
+#define QSA_CACHE_MAX_ENTRIES 1073741824 /* entries of a request that count; a
+                                            table that holds more is past it */
 #define QSA_CACHE_MAX_NEXT 8       /* new tokens per request in one call */
 
 /*
@@ -77,8 +79,8 @@ typedef struct qsa_paged_cache {
  *
  *   e < 0: nothing.  Otherwise, for every K/V head h,
  *   K[page, slot, h, :] = k[t, h, :], V likewise; into an E4M3 cache
- *   k[t, h, :] / k_scale[h], rounded to nearest even, magnitudes above 448
- *   to 448, NaN to NaN;
+ *   k[t, h, :] * (1 / k_scale[h]) (both in binary32), rounded to nearest
+ *   even, magnitudes above 448 to 448, NaN to NaN;
  *   entry_positions[r, e] = positions[t] (e itself when positions is NULL);
  *   weight_sums[r, e] = 0.
  *
@@ -171,9 +173,6 @@ QSA_API qsa_status qsa_paged_attention(
     void* workspace, size_t workspace_bytes,
     uint32_t* error_word, qsa_stream_t stream);
 
-/* Workspace for qsa_evict_entries.  Alignment 256 bytes. */
-QSA_API size_t qsa_evict_workspace_bytes(int64_t num_reqs, int64_t budget);
-
 /*
  * qsa_evict_entries -- cut every request down to at most `budget` entries.
  * Request b has n = min(context_lens[b], table_cols*page_size, entry_cols)
@@ -203,14 +202,12 @@ QSA_API size_t qsa_evict_workspace_bytes(int64_t num_reqs, int64_t budget);
  *   weight_sums       fp32 [num_reqs, entry_cols], row stride weight_sums_stride0
  *   entry_positions   int32 [num_reqs, entry_cols], row stride
  *                     entry_positions_stride0
- *   budget            >= 1; num_sink, num_recent >= 0, num_sink + num_recent
+ *   budget            1 .. QSA_CACHE_MAX_ENTRIES; num_sink, num_recent >= 0, num_sink + num_recent
  *                     <= budget (positions are distinct, so that many entries
  *                     are protected at most; of more, the first stay)
  *   kept, weight_sums_out, entry_positions_out
  *                     int32, fp32, int32 [num_reqs, budget], contiguous
  *   new_lens          int32 [num_reqs]
- *   workspace         >= qsa_evict_workspace_bytes(num_reqs, budget) bytes,
- *                     256-byte aligned
  */
 QSA_API qsa_status qsa_evict_entries(
     const qsa_paged_cache* cache,
@@ -218,7 +215,6 @@ QSA_API qsa_status qsa_evict_entries(
     const int32_t* entry_positions, int64_t entry_positions_stride0, int64_t entry_cols,
     const int32_t* context_lens, int64_t budget, int64_t num_sink, int64_t num_recent,
     int32_t* kept, int32_t* new_lens, float* weight_sums_out, int32_t* entry_positions_out,
-    void* workspace, size_t workspace_bytes,
     uint32_t* error_word, qsa_stream_t stream);
 
 #ifdef __cplusplus

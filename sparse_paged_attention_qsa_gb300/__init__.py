@@ -10,7 +10,7 @@ from .binding import (  # noqa: F401
     COMPRESS_RATIO, DERR_CMP_PAGE, DERR_CONTEXT, DERR_KV_PAGE, DERR_REQUEST, DERR_TIMEOUT, EXPORTED,
     LIB_PATH, OUT_WIDTH, TOKEN_TOPK, TOPK_BLOCKS, QSAError, declare_signatures, load_library,
     qsa_attention_workspace_bytes,
-    qsa_build_metadata, qsa_decode, qsa_evict_entries, qsa_evict_workspace_bytes,
+    qsa_build_metadata, qsa_decode, qsa_evict_entries,
     qsa_paged_append, qsa_paged_attention, qsa_paged_attention_workspace_bytes,
     qsa_paged_mqa_logits, qsa_select_attend,
     qsa_select_attend_fused_rows, qsa_select_attend_fused_cluster,

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -48,7 +49,7 @@ EXPORTED = ("qsa_status_string", "qsa_version", "qsa_select_workspace_bytes",
             "qsa_select_paged_tokens_static_scratch", "qsa_build_metadata",
             "qsa_paged_mqa_logits", "qsa_top_k_per_row_decode",
             "qsa_paged_append", "qsa_paged_attention_workspace_bytes", "qsa_paged_attention",
-            "qsa_evict_workspace_bytes", "qsa_evict_entries")
+            "qsa_evict_entries")
 
 
 class QSAError(RuntimeError):
@@ -192,11 +193,9 @@ def declare_signatures(lib):
     lib.qsa_paged_attention.argtypes = [
         vp, vp, ctypes.c_int, i64, i64, vp, vp, ctypes.c_float, i64,
         vp, vp, vp, vp, i64, vp, i64, i64, vp, sz, vp, vp]
-    lib.qsa_evict_workspace_bytes.restype = sz
-    lib.qsa_evict_workspace_bytes.argtypes = [i64, i64]
     lib.qsa_evict_entries.restype = ctypes.c_int
     lib.qsa_evict_entries.argtypes = [
-        vp, vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, sz, vp, vp]
+        vp, vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp]
     return full
 
 
@@ -631,13 +630,19 @@ def _launch_stream(stream, device_index) -> int:
     return _stream(stream) or 0
 
 
-def _on_stream(stream, raw, device_index):
+def _on_stream(stream, device_index):
     """A context in which torch allocates for the launch stream, so that a
     buffer made here is not handed out again while the launch uses it."""
-    if stream is None or raw == torch._C._cuda_getCurrentRawStream(device_index):
-        return contextlib.nullcontext()
+    if stream is None:
+        return _HERE
+    raw = _stream(stream) or 0
+    if raw == torch._C._cuda_getCurrentRawStream(device_index):
+        return _HERE
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                              else torch.cuda.ExternalStream(raw))
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _need_tensor(t, what):
@@ -653,7 +658,7 @@ def qsa_paged_append(k, v, k_cache, v_cache, block_tables, token_to_request, ent
     padding) of request token_to_request[t] (int32).  entry_positions (int32)
     and weight_sums (fp32), [requests, entries], get the token's position and
     0.  Returns (k_cache, v_cache)."""
-    lib = load_library()
+    lib = _lib or load_library()
     _on_current_device(k, v, k_cache, v_cache, block_tables, token_to_request, entries, k_scale,
                        v_scale, positions, entry_positions, weight_sums, error_word)
     if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != k_cache.shape[2:]:
@@ -675,6 +680,7 @@ def qsa_paged_append(k, v, k_cache, v_cache, block_tables, token_to_request, ent
     return k_cache, v_cache
 
 
+@functools.lru_cache(maxsize=256)      # a function of its arguments alone
 def qsa_paged_attention_workspace_bytes(num_reqs: int, next_n: int, num_heads: int,
                                         kv_heads: int, head_dim: int,
                                         weight_cols: int = 0) -> int:
@@ -692,7 +698,7 @@ def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next
     weight_sums / weight_sums_out: fp32 [requests, entries]; the second gets
     the first plus the weight that each entry received in this call.  Returns
     out [rows, heads, dim]."""
-    lib = load_library()
+    lib = _lib or load_library()
     _on_current_device(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, out,
                        lse, weight_sums, weight_sums_out, workspace, error_word)
     if q.dim() != 3:
@@ -707,11 +713,11 @@ def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next
     raw = _launch_stream(stream, device)
     weights = weight_sums is not None or weight_sums_out is not None
     if out is None or workspace is None:
-        with _on_stream(stream, raw, device):
+        with _on_stream(stream, device):
             if out is None:
                 out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
             if workspace is None:
-                workspace = _workspace(lib.qsa_paged_attention_workspace_bytes(
+                workspace = _workspace(qsa_paged_attention_workspace_bytes(
                     reqs, next_n, heads, kv_heads, dim, cols * page_size if weights else 0),
                     q.device)
     if out.dtype != q.dtype:
@@ -732,23 +738,19 @@ def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next
     return out
 
 
-def qsa_evict_workspace_bytes(num_reqs: int, budget: int) -> int:
-    return int(load_library().qsa_evict_workspace_bytes(num_reqs, budget))
-
-
 def qsa_evict_entries(weight_sums, entry_positions, context_lens, k_cache, v_cache, block_tables,
                       budget: int, *, num_sink: int = 0, num_recent: int = 0, kept=None,
                       new_lens=None, weight_sums_out=None, entry_positions_out=None,
-                      workspace=None, error_word=None, stream=None):
+                      error_word=None, stream=None):
     """Cut every request down to at most `budget` cached entries, keeping the
     first num_sink positions, the num_recent newest and then those of the
     largest weight_sums; K and V are moved within the cache
     (include/qsa_cache.h).  Returns (kept int32 [requests, budget], new_lens
     int32 [requests], weight_sums_out fp32, entry_positions_out int32
     [requests, budget])."""
-    lib = load_library()
+    lib = _lib or load_library()
     _on_current_device(weight_sums, entry_positions, context_lens, k_cache, v_cache, block_tables,
-                       kept, new_lens, weight_sums_out, entry_positions_out, workspace, error_word)
+                       kept, new_lens, weight_sums_out, entry_positions_out, error_word)
     cache = _cache_struct(k_cache, v_cache, block_tables, None, None)
     reqs = block_tables.shape[0]
     sums, sums_s0 = _rows(weight_sums, torch.float32, reqs, "weight_sums")
@@ -760,9 +762,8 @@ def qsa_evict_entries(weight_sums, entry_positions, context_lens, k_cache, v_cac
     raw = _launch_stream(stream, device)
     if budget < 1:
         raise QSAError(6, "budget must be at least 1")
-    if kept is None or new_lens is None or weight_sums_out is None or \
-            entry_positions_out is None or workspace is None:
-        with _on_stream(stream, raw, device):
+    if kept is None or new_lens is None or weight_sums_out is None or entry_positions_out is None:
+        with _on_stream(stream, device):
             if kept is None:
                 kept = torch.empty((reqs, budget), dtype=torch.int32, device=dev)
             if new_lens is None:
@@ -771,8 +772,6 @@ def qsa_evict_entries(weight_sums, entry_positions, context_lens, k_cache, v_cac
                 weight_sums_out = torch.empty((reqs, budget), dtype=torch.float32, device=dev)
             if entry_positions_out is None:
                 entry_positions_out = torch.empty((reqs, budget), dtype=torch.int32, device=dev)
-            if workspace is None:
-                workspace = _workspace(lib.qsa_evict_workspace_bytes(reqs, budget), dev)
     n = reqs * budget
     _check(lib.qsa_evict_entries(
         cache, sums, sums_s0, pos, pos_s0,
@@ -780,7 +779,5 @@ def qsa_evict_entries(weight_sums, entry_positions, context_lens, k_cache, v_cac
         _flat(context_lens, torch.int32, reqs, "context_lens"), budget, num_sink, num_recent,
         _flat(kept, torch.int32, n, "kept"), _flat(new_lens, torch.int32, reqs, "new_lens"),
         _flat(weight_sums_out, torch.float32, n, "weight_sums_out"),
-        _flat(entry_positions_out, torch.int32, n, "entry_positions_out"),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _word(error_word), raw))
+        _flat(entry_positions_out, torch.int32, n, "entry_positions_out"), _word(error_word), raw))
     return kept, new_lens, weight_sums_out, entry_positions_out

@@ -4,9 +4,9 @@
 // A pure move of num_tokens * 2 * heads * dim elements, so it is bound by
 // memory (and, for the few tokens of a decode step, by one chain of
 // dependent loads: request and entry, then the page id, then the store).  A
-// token's K and V rows are cut into 16-byte pieces of the cache; a thread
-// takes kPieces of one token, so the chain is walked once for them, and its
-// source loads do not wait for it.
+// token's K and V rows are cut into 16-byte pieces of the cache, dealt out to
+// a power of two of threads, kPieces each: the chain is walked once for them,
+// and their source loads do not wait for it.
 #include "qsa_cache.h"
 #include "qsa_cache_host.h"
 #include "qsa_device.cuh"
@@ -40,100 +40,107 @@ struct AppendParams {
   uint32_t* err;
 };
 
-// Eight 16-bit values of type T to eight E4M3 bytes: value / scale in
-// binary32 (an exact operand, one rounding), then to nearest even, saturating.
+// Eight 16-bit values of type T to eight E4M3 bytes: value * inverse in
+// binary32, then to nearest even, saturating.  (The product and the inverse
+// are off by 2^-23 together, E4M3's own rounding by 2^-4: the quotient itself
+// took twice the instructions and made the kernel bound by them.)
 template <typename T>
-__device__ __forceinline__ uint2 to_e4m3(uint4 x, float scale) {
+__device__ __forceinline__ uint2 to_e4m3(uint4 x, float inverse) {
   const T* h = reinterpret_cast<const T*>(&x);
   uint16_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = make_float2((float)h[2 * i] / scale, (float)h[2 * i + 1] / scale);
+    const float2 f = make_float2((float)h[2 * i] * inverse, (float)h[2 * i + 1] * inverse);
     o[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
 }
 
-// kFp8: an E4M3 cache; T: the new tokens' type.  A piece is 16 bytes of the
-// cache; kPieces of a token's go to one thread, `per` threads to a token.
-template <typename T, bool kFp8, int kPieces>
-__global__ void __launch_bounds__(kAppendThreads)
-append_kernel(const AppendParams p, int per) {
-  constexpr int kElems = kFp8 ? 16 : 8;                 // elements of a piece
-  const int64_t id = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
-  const int64_t t = id / per;
-  if (t >= p.num_tokens) return;
-  const int part = (int)(id - t * per);
-  const int row = p.c.heads * p.c.dim / kElems;         // pieces of a token's K
-  const int dim_pieces = p.c.dim / kElems;
+constexpr int kPieces = 4;
 
-  uint4 x[kPieces][kFp8 ? 2 : 1];
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int piece = part + i * per;
-    if (piece < 2 * row) {
-      const bool is_v = piece >= row;
-      const int u = is_v ? piece - row : piece;
-      const int h = u / dim_pieces, o = u - h * dim_pieces;
-      const unsigned char* src = is_v ? p.v + t * p.v_token + h * p.v_head
-                                      : p.k + t * p.k_token + h * p.k_head;
-#pragma unroll
-      for (int j = 0; j < (kFp8 ? 2 : 1); ++j)
-        x[i][j] = ld_stream16(src + (int64_t)o * (kElems * 2) + j * 16);
-    }
-  }
+// kFp8: an E4M3 cache; T: the new tokens' type.  2^lt_log2 threads a token;
+// 2^dim_log2 pieces a head.
+template <typename T, bool kFp8>
+__global__ void __launch_bounds__(kAppendThreads)
+append_kernel(const AppendParams p, int lt_log2, int dim_log2) {
+  const int part = threadIdx.x & ((1 << lt_log2) - 1);
+  const int64_t t = ((int64_t)blockIdx.x << (8 - lt_log2)) + (threadIdx.x >> lt_log2);
+  static_assert(kAppendThreads == 256, "8 bits of thread index");
+  if (t >= p.num_tokens) return;
+  const int row = p.c.heads << dim_log2;                // pieces of a token's K
+  const unsigned char* k_src = p.k + t * p.k_token;
+  const unsigned char* v_src = p.v + t * p.v_token;
   const int64_t e = p.entries[t];
-  if (e < 0) return;                                    // padding
   const int32_t r = p.t2r[t];
-  uint32_t bad = 0;
   int32_t page = -1;
-  if (r < 0 || r >= p.c.num_reqs) {
-    bad = QSA_DERR_REQUEST;
-  } else if (e >= p.cap) {
-    bad = QSA_DERR_CONTEXT;
-  } else {
-    page = p.c.bt[(int64_t)r * p.c.bt_s0 + (e >> p.c.page_log2)];
-    if (page < 0 || page >= p.c.num_pages) bad = QSA_DERR_KV_PAGE;
-  }
-  if (bad) {
-    if (part == 0) report(p.err, bad);
-    return;
-  }
-  const int64_t slot = e & (((int64_t)1 << p.c.page_log2) - 1);
+  int64_t k_dst = 0, v_dst = 0;
+  for (int i0 = part; i0 < 2 * row; i0 += kPieces << lt_log2) {
+    uint4 x[kPieces][kFp8 ? 2 : 1];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int piece = part + i * per;
-    if (piece < 2 * row) {
-      const bool is_v = piece >= row;
-      const int u = is_v ? piece - row : piece;
-      const int h = u / dim_pieces, o = u - h * dim_pieces;
-      unsigned char* dst = is_v ? p.c.v + page * p.c.v_page + slot * p.c.v_token + h * p.c.v_head
-                                : p.c.k + page * p.c.k_page + slot * p.c.k_token + h * p.c.k_head;
-      uint4 y = x[i][0];
-      if constexpr (kFp8) {
-        const float* sc = is_v ? p.c.v_scale : p.c.k_scale;
-        const float s = sc ? sc[h] : 1.f;
-        const uint2 a = to_e4m3<T>(x[i][0], s), b = to_e4m3<T>(x[i][1], s);
-        y = make_uint4(a.x, a.y, b.x, b.y);
+    for (int j = 0; j < kPieces; ++j) {
+      const int i = i0 + (j << lt_log2);
+      if (i < 2 * row) {
+        const bool is_v = i >= row;
+        const int u = is_v ? i - row : i, h = u >> dim_log2, o = u & ((1 << dim_log2) - 1);
+        const unsigned char* src = is_v ? v_src + h * p.v_head : k_src + h * p.k_head;
+#pragma unroll
+        for (int q = 0; q < (kFp8 ? 2 : 1); ++q)
+          x[j][q] = ld_stream16(src + o * (kFp8 ? 32 : 16) + q * 16);
       }
-      *reinterpret_cast<uint4*>(dst + o * 16) = y;
+    }
+    if (i0 == part) {                                   // where the token goes
+      if (e < 0) return;                                // padding
+      uint32_t bad = 0;
+      if (r < 0 || r >= p.c.num_reqs) {
+        bad = QSA_DERR_REQUEST;
+      } else if (e >= p.cap) {
+        bad = QSA_DERR_CONTEXT;
+      } else {
+        page = p.c.bt[(int64_t)r * p.c.bt_s0 + (e >> p.c.page_log2)];
+        if (page < 0 || page >= p.c.num_pages) bad = QSA_DERR_KV_PAGE;
+      }
+      if (bad) {
+        if (part == 0) report(p.err, bad);
+        return;
+      }
+      const int64_t slot = e & (((int64_t)1 << p.c.page_log2) - 1);
+      k_dst = page * p.c.k_page + slot * p.c.k_token;
+      v_dst = page * p.c.v_page + slot * p.c.v_token;
+    }
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int i = i0 + (j << lt_log2);
+      if (i < 2 * row) {
+        const bool is_v = i >= row;
+        const int u = is_v ? i - row : i, h = u >> dim_log2, o = u & ((1 << dim_log2) - 1);
+        unsigned char* dst = is_v ? p.c.v + v_dst + h * p.c.v_head : p.c.k + k_dst + h * p.c.k_head;
+        uint4 y = x[j][0];
+        if constexpr (kFp8) {
+          const float* sc = is_v ? p.c.v_scale : p.c.k_scale;
+          const float inv = sc ? 1.f / sc[h] : 1.f;
+          const uint2 lo = to_e4m3<T>(x[j][0], inv), hi = to_e4m3<T>(x[j][1], inv);
+          y = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+        *reinterpret_cast<uint4*>(dst + o * 16) = y;
+      }
     }
   }
   if (part == 0) {
     if (p.entry_pos)
-      p.entry_pos[(int64_t)r * p.entry_pos_s0 + e] =
-          (int32_t)(p.positions ? p.positions[t] : e);
+      p.entry_pos[(int64_t)r * p.entry_pos_s0 + e] = (int32_t)(p.positions ? p.positions[t] : e);
     if (p.sums) p.sums[(int64_t)r * p.sums_s0 + e] = 0.f;
   }
 }
 
 template <typename T, bool kFp8>
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st) {
-  const int pieces = 2 * p.c.heads * p.c.dim / (kFp8 ? 16 : 8);
-  constexpr int kPieces = 4;
-  const int per = (pieces + kPieces - 1) / kPieces;
-  const int64_t grid = (p.num_tokens * per + kAppendThreads - 1) / kAppendThreads;
-  append_kernel<T, kFp8, kPieces><<<(unsigned)grid, kAppendThreads, 0, st>>>(p, per);
+  const int head_pieces = p.c.dim / (kFp8 ? 16 : 8);
+  int dim_log2 = 0, lt_log2 = 0;
+  while ((1 << dim_log2) < head_pieces) ++dim_log2;
+  while ((kPieces << lt_log2) < 2 * p.c.heads * head_pieces && lt_log2 < 8) ++lt_log2;
+  const int64_t per_cta = kAppendThreads >> lt_log2;
+  const int64_t grid = (p.num_tokens + per_cta - 1) / per_cta;
+  append_kernel<T, kFp8><<<(unsigned)grid, kAppendThreads, 0, st>>>(p, lt_log2, dim_log2);
   return cudaGetLastError();
 }
 
@@ -155,7 +162,6 @@ extern "C" qsa_status qsa_paged_append(
   if (dtype != QSA_DT_F16 && dtype != QSA_DT_BF16) return QSA_ERR_DTYPE;
   if (cache->dtype != QSA_DT_F8E4M3 && cache->dtype != dtype) return QSA_ERR_DTYPE;
   if (!k_strides || !v_strides) return QSA_ERR_NULL;
-  // a launch covers num_tokens x (pieces / 4) threads in 2^31 - 1 CTAs
   if (num_tokens < 0 || num_tokens > (int64_t)1 << 24) return QSA_ERR_SHAPE;
   const bool book = entry_positions || weight_sums;
   if (book && (entry_cols < 0 || entry_cols > INT32_MAX)) return QSA_ERR_SHAPE;

@@ -22,8 +22,11 @@ struct CacheView {
   const float* v_scale;
   int32_t num_reqs, cols;
   int32_t page_log2, heads, dim;
-  int32_t cap;                // entries a table row can hold (saturated)
+  int32_t cap;                // entries a table row can hold, at most kMaxEntries
 };
+
+// Entries of a request that the operators count (more bytes than a GPU has).
+constexpr int32_t kMaxEntries = QSA_CACHE_MAX_ENTRIES;
 
 namespace cache_host {
 
@@ -141,7 +144,7 @@ inline qsa_status check_cache(const qsa_paged_cache* c, CacheView* view, CacheSp
   view->page_log2 = lg;
   view->heads = (int32_t)c->num_heads;
   view->dim = (int32_t)c->head_dim;
-  view->cap = cap > INT32_MAX ? INT32_MAX : (int32_t)cap;
+  view->cap = cap > kMaxEntries ? kMaxEntries : (int32_t)cap;
   spans->k = span(c->k, kx);
   spans->v = span(c->v, vx);
   spans->tables = rows_span(c->block_tables, c->num_reqs, c->table_cols, c->table_stride0);

@@ -2,27 +2,41 @@
 // the least attention weight, declared in include/qsa_cache.h
 // (qsa_evict_entries).
 //
-// rank_kernel  per request: the budget-th largest key (protected entries, then
-//              the weight sums' order-preserving bits) by radix select; in
-//              entry order, which entries of equal key stay, which places
-//              below the budget fall free (holes) and which kept entries lie
-//              above it (movers).  As many of one as of the other, so the i-th
-//              mover goes to the i-th hole: no entry is written that is read,
-//              and only what has to move moves.
-// move_kernel  copies the movers' K and V.
+// rank_kernel  a cluster of 1 to 8 CTAs per request, each over a slice of its
+//              entries: the budget-th largest key (protected entries, then the
+//              weight sums' order-preserving bits) by radix select, histograms
+//              summed through distributed shared memory; then, in entry order,
+//              which entries of equal key stay, which places below the budget
+//              fall free (holes) and which kept entries lie above it (movers).
+//              As many of one as of the other, so the i-th mover goes to the
+//              i-th hole: no entry is written that is read, so the moves need
+//              no order, and only what has to move moves.  kept[] is the list
+//              of moves, so there is no workspace.
+// move_kernel  a warp looks 32 places of kept[] over and copies the K and V of
+//              those that move, every lane's pieces in flight at once.
 #include "qsa_cache.h"
 #include "qsa_cache_host.h"
 #include "qsa_device.cuh"
 #include "qsa_host.h"
+#include "qsa_internal.h"
 
 #include <algorithm>
+#include <climits>
+#include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <mutex>
 
 namespace qsa {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kRankThreads = 1024;
+constexpr int kRankWarps = kRankThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxSlice = 24576;          // entries of a CTA whose keys fit in shared memory
 constexpr int kMoveThreads = 256;
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
 
@@ -39,8 +53,6 @@ struct EvictParams {
   int32_t* new_lens;
   float* sums_out;
   int32_t* pos_out;
-  int32_t* moves;             // workspace: [reqs, budget, 2] (from, to)
-  int32_t* count;             // workspace: [reqs] moves of a request
   uint32_t* err;
 };
 
@@ -52,185 +64,424 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Sum of v over the threads before this one; *total over all of them.
-__device__ __forceinline__ int block_prefix(int v, int* s_warp, int* total) {
+struct RankShared {
+  int hist[3][kBins];         // one a pass: each is read by the other CTAs while the next fills
+  int warp[kRankWarps];
+  uint32_t lo, hi;            // of the slice's keys (unprotected or not)
+  int newest;                 // of the slice's positions
+  int movers;                 // of the slice
+  int holes;
+  int digit, need, ties;      // of the pass: its bin, what is still to take, what it holds
+};
+
+// Sum of v over the warps before this one (one value a warp, from lane 0);
+// *total over all of them.
+__device__ __forceinline__ int warps_before(int v, int* s_warp, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
   __syncthreads();                       // s_warp free again
-  if (lane == 31) s_warp[warp] = x;
+  if (lane == 0) s_warp[warp] = v;
   __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < kRankThreads / 32; ++i) {
-    const int c = s_warp[i];
-    if (i < warp) before += c;
-    all += c;
-  }
-  *total = all;
-  return before + x - v;
+  const int c = s_warp[lane];
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+  *total = __reduce_add_sync(0xffffffffu, c);
+  return before;
 }
 
-__global__ void __launch_bounds__(kRankThreads)
-rank_kernel(const EvictParams p) {
-  __shared__ int s_hist[2048];
-  __shared__ int s_warp[kRankThreads / 32];
-  __shared__ int s_newest, s_digit, s_need;
-  const int b = blockIdx.x, tid = threadIdx.x;
+// kCached: the slice's keys are kept in shared memory (and, later, the lists of
+// its holes and movers in place of the positions); else every sweep forms the
+// keys from the inputs again, and the movers pass through pos_out.
+template <bool kCached>
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p, int max_slice) {
+  extern __shared__ __align__(16) unsigned char rank_smem[];
+  RankShared& sh = *reinterpret_cast<RankShared*>(rank_smem);
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(rank_smem + sizeof(RankShared));   // [max_slice]
+  int32_t* s_pos = reinterpret_cast<int32_t*>(s_key + (kCached ? max_slice : 0));  // [max_slice]
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  // a lone CTA needs no cluster barrier
+  const auto sync_all = [&] {
+    if (ranks > 1) cluster.sync(); else __syncthreads();
+  };
+  // f(rank, its shared memory), the remote reads of all ranks in flight at once
+  const auto each_rank = [&](auto f) {
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < ranks) f(r, ranks > 1 ? *cluster.map_shared_rank(&sh, r) : sh);
+  };
+  const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* w = p.sums + b * p.sums_s0;
   const int32_t* pos = p.pos + b * p.pos_s0;
   const int32_t ctx = p.ctx[b];
   const int n = max(0, min(ctx, p.cap));
   const int len = min(n, p.budget);
   int32_t* kept = p.kept + (int64_t)b * p.budget;
-  int32_t* moves = p.moves + (int64_t)b * p.budget * 2;
-  if (tid == 0) {
+  float* sums_out = p.sums_out + (int64_t)b * p.budget;
+  int32_t* pos_out = p.pos_out + (int64_t)b * p.budget;
+  pdl_trigger();
+  if (rank == 0 && tid == 0) {
     if (ctx > p.cap) report(p.err, QSA_DERR_CONTEXT);
     p.new_lens[b] = len;
-    s_newest = INT32_MIN;
   }
-  int moved = 0;
-  if (n > p.budget) {
-    __syncthreads();
+  if (n <= p.budget) {                   // the same for the whole cluster
+    for (int i = rank * kRankThreads + tid; i < p.budget; i += ranks * kRankThreads) {
+      kept[i] = i < len ? i : -1;
+      sums_out[i] = i < len ? w[i] : 0.f;
+      pos_out[i] = i < len ? pos[i] : -1;
+    }
+    return;
+  }
+  const int slice = (n + ranks - 1) / ranks;
+  const int e0 = min(n, rank * slice), ne = min(n, e0 + slice) - e0;
+
+  // keys and the newest position; every place below the budget starts as if
+  // its entry stayed
+  for (int i = tid; i < 3 * kBins; i += kRankThreads) (&sh.hist[0][0])[i] = 0;
+  if (tid == 0) {
+    sh.lo = 0xFFFFFFFFu;
+    sh.hi = 0u;
+    sh.newest = INT32_MIN;
+  }
+  __syncthreads();
+  {
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
     int newest = INT32_MIN;
-    for (int e = tid; e < n; e += kRankThreads) newest = max(newest, pos[e]);
-    atomicMax(&s_newest, newest);
-    __syncthreads();
-    // position > newest - recent, in 64 bits: neither may wrap
-    const int64_t after = (int64_t)s_newest - p.recent;
-    const auto key_of = [&](int e) {
-      const int32_t q = pos[e];
-      return q < p.sink || q > after ? kProtected : weight_key(w[e]);
-    };
-    // the budget-th largest key, 11 + 11 + 10 bits at a time
-    uint32_t prefix = 0, mask = 0;
-    int need = p.budget;                   // entries still to take below the digits found
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int bins = pass == 2 ? 1024 : 2048;
-      for (int i = tid; i < bins; i += kRankThreads) s_hist[i] = 0;
-      __syncthreads();
-      for (int e = tid; e < n; e += kRankThreads) {
-        const uint32_t k = key_of(e);
-        if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
+#pragma unroll 4
+    for (int i = tid; i < ne; i += kRankThreads) {
+      const float f = w[e0 + i];
+      const uint32_t k = weight_key(f);
+      const int32_t q = pos[e0 + i];
+      if constexpr (kCached) {
+        s_key[i] = k;
+        s_pos[i] = q;
       }
-      __syncthreads();
-      // bins from the top: the one in which the count reaches `need`
-      int total = 0;
-      const int per = bins / kRankThreads;              // 2, 2, 1
-      int mine = 0;
-      const int top = bins - 1 - tid * per;
-      for (int i = 0; i < per; ++i) mine += s_hist[top - i];
-      int before = block_prefix(mine, s_warp, &total);
-      for (int i = 0; i < per; ++i) {
-        const int c = s_hist[top - i];
-        if (before < need && before + c >= need) {
-          s_digit = top - i;
-          s_need = need - before;
+      if (e0 + i < p.budget) {
+        kept[e0 + i] = e0 + i;
+        if constexpr (kCached) {
+          sums_out[e0 + i] = f;
+          pos_out[e0 + i] = q;
         }
-        before += c;
       }
-      __syncthreads();
-      prefix |= (uint32_t)s_digit << shift;
-      mask |= (uint32_t)(bins - 1) << shift;
-      need = s_need;
-      __syncthreads();
+      lo = min(lo, k);
+      hi = max(hi, k);
+      newest = max(newest, q);
     }
-    // in entry order: ties by entry, then holes and movers
-    int ties = 0, holes = 0;
-    for (int e0 = 0; e0 < n; e0 += kRankThreads) {
-      const int e = e0 + tid;
-      const bool there = e < n;
-      const uint32_t k = there ? key_of(e) : 0u;
-      const bool tie = there && k == prefix;
-      int total = 0;
-      const int rank = ties + block_prefix(tie, s_warp, &total);
-      ties += total;
-      const bool keep = there && (k > prefix || (tie && rank < need));
-      const bool hole = there && e < p.budget && !keep;
-      const bool mover = keep && e >= p.budget;
-      // both counts in one prefix sum: neither passes 2^10 in a step
-      const int both = block_prefix((int)hole | (int)mover << 16, s_warp, &total);
-      if (hole) moves[2 * (holes + (both & 0xffff)) + 1] = e;
-      if (mover) moves[2 * (moved + (both >> 16))] = e;
-      if (there && e < p.budget && keep) kept[e] = e;
-      holes += total & 0xffff;
-      moved += total >> 16;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    if (lane == 0) {
+      atomicMin(&sh.lo, lo);
+      atomicMax(&sh.hi, hi);
+      atomicMax(&sh.newest, newest);
     }
-    __syncthreads();
-    for (int i = tid; i < moved; i += kRankThreads) kept[moves[2 * i + 1]] = moves[2 * i];
-    __syncthreads();
-  } else {
-    for (int i = tid; i < p.budget; i += kRankThreads) kept[i] = i < len ? i : -1;
-    __syncthreads();
   }
-  if (tid == 0) p.count[b] = moved;
-  for (int i = tid; i < p.budget; i += kRankThreads) {
-    const int e = kept[i];
-    p.sums_out[(int64_t)b * p.budget + i] = i < len ? w[e] : 0.f;
-    p.pos_out[(int64_t)b * p.budget + i] = i < len ? pos[e] : -1;
+  sync_all();
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+  int newest = INT32_MIN;
+  each_rank([&](int, const RankShared& o) {
+    lo = min(lo, o.lo);
+    hi = max(hi, o.hi);
+    newest = max(newest, o.newest);
+  });
+  // position > newest - recent, in 64 bits: neither may wrap
+  const int64_t after = (int64_t)newest - p.recent;
+  // Keys relative to the smallest, so that the digits spread over the range
+  // that occurs: span + 1 stands for the protected entries (hi is at most that
+  // of +inf, so it does not wrap).
+  const uint32_t span = hi - lo;
+  const auto final_key = [&](uint32_t k, int32_t q) {
+    return q < p.sink || q > after ? span + 1 : k - lo;
+  };
+  const auto key_of = [&](int i) {
+    if constexpr (kCached) return s_key[i];
+    return final_key(weight_key(w[e0 + i]), pos[e0 + i]);
+  };
+  const int bits = 32 - __clz(span + 1);
+
+  // the budget-th largest key, up to 11 bits at a time from the top
+  uint32_t prefix = 0, mask = 0;
+  int need = p.budget, left = bits, pass = 0;
+  while (left > 0) {
+    const int width = min(left, 11), shift = left - width;
+    const int bins = 1 << width;
+    for (int i = tid; i < ne; i += kRankThreads) {
+      uint32_t k;
+      if (kCached && pass == 0) {
+        k = final_key(s_key[i], s_pos[i]);
+        s_key[i] = k;
+      } else {
+        k = key_of(i);
+      }
+      if ((k & mask) == prefix) atomicAdd(&sh.hist[pass][(k >> shift) & (bins - 1)], 1);
+    }
+    sync_all();
+    // bins from the top, two a thread: the one in which the count reaches `need`
+    int c[2] = {0, 0};
+    const int top = bins - 1 - 2 * tid;
+    each_rank([&](int, const RankShared& o) {
+      if (top >= 1) {                    // bins is even
+        const int2 h = *reinterpret_cast<const int2*>(&o.hist[pass][top - 1]);
+        c[0] += h.y;
+        c[1] += h.x;
+      }
+    });
+    int x = c[0] + c[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    int total;
+    const int mine = __shfl_sync(0xffffffffu, x, 31);
+    int before = warps_before(mine, sh.warp, &total) + x - c[0] - c[1];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (before < need && before + c[i] >= need) {
+        sh.digit = top - i;
+        sh.need = need - before;
+        sh.ties = c[i];
+      }
+      before += c[i];
+    }
+    __syncthreads();
+    prefix |= (uint32_t)sh.digit << shift;
+    mask |= (uint32_t)(bins - 1) << shift;
+    need = sh.need;
+    left = shift;
+    ++pass;
+    if (sh.ties == need) break;            // the whole bin stays: no need to look into it
+  }
+  // The first `need` of the bin's entries stay (of equal key, where the bin
+  // holds more).  The last pass's histogram counted them slice by slice.
+  int ties_before = 0;
+  each_rank([&](int r, const RankShared& o) {
+    if (r < rank) ties_before += o.hist[pass - 1][sh.digit];
+  });
+  const bool some = sh.ties != need;
+  // Each warp takes a contiguous part of the slice, 32 entries at a time.
+  const int part = ((ne + kRankThreads - 1) / kRankThreads) * 32;
+  const int i0 = min(ne, warp * part), i1 = min(ne, i0 + part);
+  const uint32_t below = (1u << lane) - 1u;
+  if (some) {
+    int mine = 0, total;
+    for (int i = i0; i < i1; i += 32)
+      mine += __popc(__ballot_sync(0xffffffffu,
+                                   i + lane < i1 && (key_of(i + lane) & mask) == prefix));
+    ties_before += warps_before(mine, sh.warp, &total);
+  }
+  // visit(entry, hole, mover, holes and movers of the warp before it)
+  const auto sweep = [&](auto visit) {
+    int t = ties_before, holes = 0, movers = 0;
+    for (int i = i0; i < i1; i += 32) {
+      const bool there = i + lane < i1;
+      const uint32_t k = (there ? key_of(i + lane) : 0u) & mask;
+      const bool tie = there && k == prefix;
+      const uint32_t tied = __ballot_sync(0xffffffffu, tie);
+      const bool keep = there && (k > prefix || (tie && (!some || t + __popc(tied & below) < need)));
+      t += __popc(tied);
+      const int e = e0 + i + lane;
+      const bool hole = there && e < p.budget && !keep, mover = keep && e >= p.budget;
+      const uint32_t h = __ballot_sync(0xffffffffu, hole), m = __ballot_sync(0xffffffffu, mover);
+      visit(e, hole, mover, holes + __popc(h & below), movers + __popc(m & below));
+      holes += __popc(h);
+      movers += __popc(m);
+    }
+    return make_int2(holes, movers);
+  };
+  const int2 counts = sweep([](int, bool, bool, int, int) {});
+  int holes, movers;
+  const int hole_at = warps_before(counts.x, sh.warp, &holes);
+  const int mover_at = warps_before(counts.y, sh.warp, &movers);
+  if (tid == 0) {
+    sh.holes = holes;
+    sh.movers = movers;
+  }
+  if constexpr (kCached) {
+    // holes from the front of the list, movers from its back (an entry is at
+    // most one of the two); then hole i of the request takes mover i, in
+    // whichever CTA's list that is
+    sweep([&](int e, bool hole, bool mover, int h, int m) {
+      if (hole) s_pos[hole_at + h] = e;
+      if (mover) s_pos[max_slice - 1 - (mover_at + m)] = e;
+    });
+    sync_all();
+    int first[kMaxCluster], base = 0, run = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) first[r] = INT_MAX;
+    each_rank([&](int r, const RankShared& o) {
+      first[r] = run;
+      run += o.movers;
+      if (r < rank) base += o.holes;
+    });
+    for (int i = tid; i < holes; i += kRankThreads) {
+      int r = 0, at = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q)
+        if (base + i >= first[q]) {
+          r = q;
+          at = first[q];
+        }
+      const int32_t* list = ranks > 1 ? cluster.map_shared_rank(s_pos, r) : s_pos;
+      const int from = list[max_slice - 1 - (base + i - at)], to = s_pos[i];
+      kept[to] = from;
+      sums_out[to] = w[from];
+      pos_out[to] = pos[from];
+    }
+    sync_all();                          // no CTA leaves while another reads its shared memory
+  } else {
+    sync_all();
+    int hole_base = hole_at, mover_base = mover_at;
+    each_rank([&](int r, const RankShared& o) {
+      if (r < rank) {
+        hole_base += o.holes;
+        mover_base += o.movers;
+      }
+    });
+    sweep([&](int e, bool, bool mover, int, int m) {
+      if (mover) pos_out[mover_base + m] = e;
+    });
+    sync_all();
+    sweep([&](int e, bool hole, bool, int h, int) {
+      if (hole) kept[e] = __ldcg(pos_out + hole_base + h);
+    });
+    sync_all();
+    for (int i = rank * kRankThreads + tid; i < p.budget; i += ranks * kRankThreads) {
+      const int e = __ldcg(kept + i);
+      sums_out[i] = w[e];
+      pos_out[i] = pos[e];
+    }
   }
 }
 
-// CTA (x, b) takes the moves x, x + gridDim.x, ... of request b; the threads
-// share a move's 16-byte pieces of K and V.
-__global__ void __launch_bounds__(kMoveThreads)
-move_kernel(const EvictParams p, int head_bytes) {
-  const int b = blockIdx.y;
-  const int count = p.count[b];
-  const int32_t* moves = p.moves + (int64_t)b * p.budget * 2;
+constexpr int kMovePieces = 8;            // 16-byte pieces of a lane in flight
+
+// A warp of request b looks over 32 places of kept[] at a time; its lanes share
+// the 16-byte pieces of a moving entry's K and V.
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p, int head_log2) {
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int row = p.c.heads << head_log2;                  // pieces of an entry's K
+  const int32_t* kept = p.kept + (int64_t)b * p.budget;
   const int32_t* bt = p.c.bt + (int64_t)b * p.c.bt_s0;
   const int slot_mask = (1 << p.c.page_log2) - 1;
-  const int head_pieces = head_bytes / 16, row = p.c.heads * head_pieces;
-  for (int m = blockIdx.x; m < count; m += gridDim.x) {
-    const int from = moves[2 * m], to = moves[2 * m + 1];
-    const int32_t pf = bt[from >> p.c.page_log2], pt = bt[to >> p.c.page_log2];
-    if (pf < 0 || pf >= p.c.num_pages || pt < 0 || pt >= p.c.num_pages) {
-      if (threadIdx.x == 0) report(p.err, QSA_DERR_KV_PAGE);
-      continue;
+  pdl_wait();
+  const int warp = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  const int stride = gridDim.x * (kMoveThreads / 32);
+  // one place a lane, the places of a warp `stride` apart so that a run of
+  // moves is spread over the warps
+  for (int i0 = warp; i0 < p.budget; i0 += 32 * stride) {
+    const int mine = i0 + lane * stride;
+    int src = mine < p.budget ? kept[mine] : -1;
+    int32_t page_f = -1, page_t = -1;
+    const bool moves = src >= 0 && src != mine;
+    if (moves) {
+      page_f = bt[src >> p.c.page_log2];
+      page_t = bt[mine >> p.c.page_log2];
     }
-    const int sf = from & slot_mask, st = to & slot_mask;
-    for (int i = threadIdx.x; i < 2 * row; i += kMoveThreads) {
-      const bool is_v = i >= row;
-      const int u = is_v ? i - row : i;
-      const int h = u / head_pieces, o = u - h * head_pieces;
-      unsigned char* base = is_v ? p.c.v : p.c.k;
-      const int64_t ps = is_v ? p.c.v_page : p.c.k_page, ts = is_v ? p.c.v_token : p.c.k_token;
-      unsigned char* at = base + h * (is_v ? p.c.v_head : p.c.k_head) + o * 16;
-      *reinterpret_cast<uint4*>(at + pt * ps + st * ts) =
-          *reinterpret_cast<const uint4*>(at + pf * ps + sf * ts);
+    const bool fine = moves && page_f >= 0 && page_f < p.c.num_pages && page_t >= 0 &&
+                      page_t < p.c.num_pages;
+    if (moves && !fine) report(p.err, QSA_DERR_KV_PAGE);
+    for (uint32_t todo = __ballot_sync(0xffffffffu, fine); todo; todo &= todo - 1) {
+      const int who = __ffs(todo) - 1;
+      const int from = __shfl_sync(0xffffffffu, src, who), to = __shfl_sync(0xffffffffu, mine, who);
+      const int64_t pf = __shfl_sync(0xffffffffu, page_f, who);
+      const int64_t pt = __shfl_sync(0xffffffffu, page_t, who);
+      const int64_t sf = from & slot_mask, st = to & slot_mask;
+      const unsigned char* kf = p.c.k + pf * p.c.k_page + sf * p.c.k_token;
+      const unsigned char* vf = p.c.v + pf * p.c.v_page + sf * p.c.v_token;
+      const int64_t k_to = pt * p.c.k_page + st * p.c.k_token - (pf * p.c.k_page + sf * p.c.k_token);
+      const int64_t v_to = pt * p.c.v_page + st * p.c.v_token - (pf * p.c.v_page + sf * p.c.v_token);
+      const auto source = [&](int i) {
+        const bool is_v = i >= row;
+        const int u = is_v ? i - row : i, h = u >> head_log2, o = u & ((1 << head_log2) - 1);
+        return (is_v ? vf + h * p.c.v_head : kf + h * p.c.k_head) + o * 16;
+      };
+      for (int i0 = 0; i0 < 2 * row; i0 += 32 * kMovePieces) {
+        uint4 x[kMovePieces];
+#pragma unroll
+        for (int j = 0; j < kMovePieces; ++j) {
+          const int i = i0 + j * 32 + lane;
+          if (i < 2 * row) x[j] = *reinterpret_cast<const uint4*>(source(i));
+        }
+#pragma unroll
+        for (int j = 0; j < kMovePieces; ++j) {
+          const int i = i0 + j * 32 + lane;
+          if (i < 2 * row)
+            *reinterpret_cast<uint4*>(const_cast<unsigned char*>(source(i)) +
+                                      (i >= row ? v_to : k_to)) = x[j];
+        }
+      }
     }
   }
 }
 
-size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+struct EvictDevice {
+  int sms = 0;
+};
+
+cudaError_t evict_device(EvictDevice** out) {
+  static std::mutex mu;
+  static EvictDevice info[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  EvictDevice& d = info[dev];
+  if (d.sms == 0) {
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(rank_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(sizeof(RankShared) + kMaxSlice * 8));
+    if (e != cudaSuccess) return e;
+    d.sms = n;
+  }
+  *out = &d;
+  return cudaSuccess;
+}
+
+// CTAs of a request's cluster: as many as leave every request a cluster of its
+// own, with at least kMinSlice entries each.
+constexpr int64_t kMinSlice = 4096;
+
+cudaError_t launch_rank(const EvictParams& p, int reqs, int sms, cudaStream_t st) {
+  int ranks = 1;
+  while (ranks < kMaxCluster && (int64_t)reqs * ranks * 2 <= sms &&
+         (int64_t)p.cap >= kMinSlice * ranks * 2)
+    ranks *= 2;
+  const int64_t slice = ((int64_t)p.cap + ranks - 1) / ranks;
+  const bool cached = slice <= kMaxSlice;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(reqs * ranks));
+  cfg.blockDim = dim3(kRankThreads);
+  cfg.dynamicSmemBytes = sizeof(RankShared) + (cached ? (size_t)slice * 8 : 0);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cached ? cudaLaunchKernelEx(&cfg, rank_kernel<true>, p, (int)slice)
+                : cudaLaunchKernelEx(&cfg, rank_kernel<false>, p, (int)slice);
+}
 
 }  // namespace
 }  // namespace qsa
-
-extern "C" size_t qsa_evict_workspace_bytes(int64_t num_reqs, int64_t budget) {
-  if (num_reqs <= 0 || num_reqs > QSA_CACHE_MAX_REQS || budget <= 0 || budget > INT32_MAX) return 0;
-  const __int128 n = (__int128)num_reqs * budget * 8;
-  if (n > ((__int128)1 << 60)) return 0;
-  return qsa::round256((size_t)n) + qsa::round256((size_t)num_reqs * 4);
-}
 
 extern "C" qsa_status qsa_evict_entries(
     const qsa_paged_cache* cache, const float* weight_sums, int64_t weight_sums_stride0,
     const int32_t* entry_positions, int64_t entry_positions_stride0, int64_t entry_cols,
     const int32_t* context_lens, int64_t budget, int64_t num_sink, int64_t num_recent,
     int32_t* kept, int32_t* new_lens, float* weight_sums_out, int32_t* entry_positions_out,
-    void* workspace, size_t workspace_bytes, uint32_t* error_word, qsa_stream_t stream) {
+    uint32_t* error_word, qsa_stream_t stream) {
   using namespace qsa;
   using namespace qsa::cache_host;
   EvictParams p{};
   CacheSpans cs{};
   const qsa_status st = check_cache(cache, &p.c, &cs);
   if (st != QSA_OK) return st;
-  if (budget < 1 || budget > INT32_MAX || num_sink < 0 || num_recent < 0 || num_sink > budget ||
+  if (budget < 1 || budget > kMaxEntries || num_sink < 0 || num_recent < 0 || num_sink > budget ||
       num_recent > budget - num_sink)
     return QSA_ERR_CONTRACT;
   if (entry_cols < 0 || entry_cols > INT32_MAX) return QSA_ERR_SHAPE;
@@ -239,8 +490,6 @@ extern "C" qsa_status qsa_evict_entries(
     return QSA_ERR_STRIDE;
   const int64_t R = cache->num_reqs;
   if (R == 0) return QSA_OK;
-  const size_t need = qsa_evict_workspace_bytes(R, budget);
-  if (need == 0) return QSA_ERR_SHAPE;
   if (!context_lens || !kept || !new_lens || !weight_sums_out || !entry_positions_out)
     return QSA_ERR_NULL;
   if (entry_cols > 0 && (!weight_sums || !entry_positions)) return QSA_ERR_NULL;
@@ -248,20 +497,17 @@ extern "C" qsa_status qsa_evict_entries(
       !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(weight_sums_out, 4) ||
       !aligned(entry_positions_out, 4) || !aligned(error_word, 4))
     return QSA_ERR_ALIGN;
-  const Span ws = span(workspace, (int64_t)need);
-  const Span outs[6] = {rows_span(kept, R, budget, budget), span(new_lens, R * 4),
+  const Span outs[5] = {rows_span(kept, R, budget, budget), span(new_lens, R * 4),
                         rows_span(weight_sums_out, R, budget, budget),
                         rows_span(entry_positions_out, R, budget, budget),
-                        span(error_word, 4), ws};
+                        span(error_word, 4)};
   const Span ins[6] = {rows_span(weight_sums, R, entry_cols, weight_sums_stride0),
                        rows_span(entry_positions, R, entry_cols, entry_positions_stride0),
                        span(context_lens, R * 4), cs.tables, cs.k_scale, cs.v_scale};
-  if (any_overlap(outs, 6, ins, 6)) return QSA_ERR_ALIAS;
+  if (any_overlap(outs, 5, ins, 6)) return QSA_ERR_ALIAS;
   for (const Span& o : {cs.k, cs.v}) {
-    if (any_overlap(&o, 1, ins, 6) || any_overlap(&o, 1, outs, 6)) return QSA_ERR_ALIAS;
+    if (any_overlap(&o, 1, ins, 6) || any_overlap(&o, 1, outs, 5)) return QSA_ERR_ALIAS;
   }
-  if (!workspace || workspace_bytes < need) return QSA_ERR_WORKSPACE;
-  if (!aligned(workspace, 256)) return QSA_ERR_ALIGN;
   p.sums = weight_sums;
   p.sums_s0 = weight_sums_stride0;
   p.pos = entry_positions;
@@ -275,17 +521,22 @@ extern "C" qsa_status qsa_evict_entries(
   p.new_lens = new_lens;
   p.sums_out = weight_sums_out;
   p.pos_out = entry_positions_out;
-  p.moves = static_cast<int32_t*>(workspace);
-  p.count = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) +
-                                       round256((size_t)R * budget * 8));
   p.err = error_word;
   bind_calling_thread();
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  rank_kernel<<<(unsigned)R, kRankThreads, 0, s>>>(p);
+  EvictDevice* dev = nullptr;
+  if (evict_device(&dev) != cudaSuccess) return QSA_ERR_CUDA;
+  if (launch_rank(p, (int)R, dev->sms, s) != cudaSuccess) return QSA_ERR_CUDA;
   const int64_t most = std::min<int64_t>(budget, std::max<int64_t>(0, p.cap - budget));
-  if (most > 0) {
-    const dim3 grid((unsigned)std::min<int64_t>(most, std::max<int64_t>(1, 8192 / R)), (unsigned)R);
-    move_kernel<<<grid, kMoveThreads, 0, s>>>(p, (int)(cache->head_dim * dtype_size(cache->dtype)));
-  }
-  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+  if (most == 0) return QSA_OK;          // no request can have an entry too many
+  const int64_t warps = kMoveThreads / 32;
+  const int64_t wave = std::max<int64_t>(1, (int64_t)dev->sms * (2048 / kMoveThreads) / R);
+  // every place is looked at; a warp's share is at least one, at most 32
+  const int64_t ctas = std::max((most + warps - 1) / warps, (budget + 32 * warps - 1) / (32 * warps));
+  const dim3 grid((unsigned)std::min(ctas, wave), (unsigned)R);
+  int head_log2 = 0;
+  while (((int64_t)16 << head_log2) < cache->head_dim * dtype_size(cache->dtype)) ++head_log2;
+  return launch_after(move_kernel, grid, dim3(kMoveThreads), 0, s, p, head_log2) == cudaSuccess
+             ? QSA_OK
+             : QSA_ERR_CUDA;
 }

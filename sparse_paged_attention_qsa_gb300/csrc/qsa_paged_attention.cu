@@ -183,7 +183,7 @@ extern "C" qsa_status qsa_paged_attention(
   const int64_t entries = cache->table_cols * cache->page_size;
   if (weights) {
     if (!weight_sums || !weight_sums_out) return QSA_ERR_NULL;
-    if (entries > INT32_MAX || entry_cols < entries || entry_cols > INT32_MAX) return QSA_ERR_SHAPE;
+    if (entries > kMaxEntries || entry_cols < entries || entry_cols > INT32_MAX) return QSA_ERR_SHAPE;
     if (!row_stride_ok(weight_sums_stride0, entry_cols) ||
         !row_stride_ok(weight_sums_out_stride0, entry_cols))
       return QSA_ERR_STRIDE;

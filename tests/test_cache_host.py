@@ -88,10 +88,8 @@ def _evict(lib, **over):
     cache = _cache(over)
     a = dict(cache=cache, sums=_addr(10), ss0=128, pos=_addr(11), ps0=128, ecols=128, ctx=_addr(12),
              budget=32, sink=4, recent=8, kept=_addr(13), lens=_addr(14), so=_addr(15),
-             po=_addr(16), work=_addr(17), bytes=None, err=_addr(18), stream=None)
+             po=_addr(16), err=_addr(18), stream=None)
     a.update(over)
-    if a["bytes"] is None:
-        a["bytes"] = lib.qsa_evict_workspace_bytes(4, max(a["budget"], 1))
     return lib.qsa_evict_entries(*a.values())
 
 
@@ -113,8 +111,9 @@ CACHE_REFUSALS = [
 @pytest.mark.parametrize("call", [_append, _attend, _evict], ids=["append", "attend", "evict"])
 @pytest.mark.parametrize("over,status", CACHE_REFUSALS)
 def test_cache_descriptor_is_refused(lib, call, over, status):
-    assert call(lib, **dict(over), bytes=1 << 40) == status if call is not _append \
-        else call(lib, **dict(over)) == status
+    if call is _attend:
+        over = dict(over, bytes=1 << 40)
+    assert call(lib, **over) == status
 
 
 @pytest.mark.parametrize("call", [_append, _attend, _evict], ids=["append", "attend", "evict"])
@@ -171,24 +170,23 @@ def test_attention_without_requests_is_a_noop(lib):
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(budget=0), CONTRACT), (dict(budget=1 << 31), CONTRACT), (dict(sink=-1), CONTRACT),
+    (dict(budget=0), CONTRACT), (dict(budget=(1 << 30) + 1), CONTRACT), (dict(sink=-1), CONTRACT),
     (dict(recent=-1), CONTRACT), (dict(sink=25), CONTRACT), (dict(sink=1 << 62), CONTRACT),
     (dict(ecols=-1), SHAPE), (dict(ecols=1 << 31, ss0=1 << 31, ps0=1 << 31), SHAPE),
     (dict(ss0=127), STRIDE), (dict(ps0=1), STRIDE),
     (dict(sums=None), NULL), (dict(pos=None), NULL), (dict(ctx=None), NULL), (dict(kept=None), NULL),
     (dict(lens=None), NULL), (dict(so=None), NULL), (dict(po=None), NULL),
-    (dict(sums=_addr(10) + 2), ALIGN), (dict(kept=_addr(13) + 2), ALIGN), (dict(work=_addr(17) + 4), ALIGN),
-    (dict(work=None), WORKSPACE), (dict(bytes=64), WORKSPACE),
+    (dict(sums=_addr(10) + 2), ALIGN), (dict(kept=_addr(13) + 2), ALIGN), (dict(po=_addr(16) + 1), ALIGN),
     (dict(so=_addr(10)), ALIAS), (dict(po=_addr(11)), ALIAS), (dict(lens=_addr(12)), ALIAS),
     (dict(kept=_addr(15)), ALIAS), (dict(kept=_addr(1)), ALIAS), (dict(sums=_addr(2) + 64), ALIAS),
-    (dict(work=_addr(1)), ALIAS), (dict(err=_addr(14)), ALIAS),
+    (dict(so=_addr(1)), ALIAS), (dict(err=_addr(14)), ALIAS),
 ])
 def test_evict_refusals(lib, over, status):
     assert _evict(lib, **over) == status
 
 
 def test_evict_without_requests_is_a_noop(lib):
-    assert _evict(lib, reqs=0, bytes=0, work=None) == 0
+    assert _evict(lib, reqs=0) == 0
 
 
 def test_workspace_queries(lib):
@@ -198,8 +196,6 @@ def test_workspace_queries(lib):
     for bad in ((0, 1, 8, 2, 128), (4, 0, 8, 2, 128), (4, 9, 8, 2, 128), (4, 1, 9, 2, 128),
                 (4, 1, 8, 0, 128), (4, 1, 8, 2, 100), (65536, 1, 8, 2, 128), (4, 1, 8, 2, 128, -1)):
         assert w(*bad) == 0
-    e = qsa.qsa_evict_workspace_bytes
-    assert e(4, 100) >= 4 * 100 * 8 and e(0, 5) == 0 and e(5, 0) == 0 and e(65535, 1 << 30) > 0
 
 
 def test_binding_refuses_host_tensors():

@@ -398,7 +398,8 @@ def test_append(T, hk, d, size, layout, dtype, cache):
         x = x.float().cpu().numpy()
         if cache != E4M3:
             return x.astype(np.float64)
-        return C.to_e4m3((x / s.cpu().numpy()[:, None]).astype(np.float64))   # a binary32 quotient
+        inverse = np.float32(1) / s.cpu().numpy()[:, None]        # both steps in binary32
+        return C.to_e4m3((x * inverse).astype(np.float64))
 
     want = C.append(stored(nk, ks), stored(nv, vs), _f64(k), _f64(v), tables.cpu().numpy(),
                     req.numpy(), ent.numpy(), None, pos.numpy(), ep.cpu().numpy(),
@@ -593,7 +594,8 @@ def test_bounded_cache_decode(dtype, cache):
             x = x.float().cpu().numpy()
             if s is None:
                 return x.astype(np.float64)
-            return C.to_e4m3((x / s.cpu().numpy()[:, None]).astype(np.float64))
+            inverse = np.float32(1) / s.cpu().numpy()[:, None]
+            return C.to_e4m3((x * inverse).astype(np.float64))
 
         want = C.append(stored(nk, ks), stored(nv, vs), _f64(k), _f64(v), tables.cpu().numpy(),
                         t2r.cpu().numpy(), entries.cpu().numpy(), limit, seen.cpu().numpy(),
