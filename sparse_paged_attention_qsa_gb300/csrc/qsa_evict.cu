@@ -65,13 +65,20 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 struct RankShared {
-  int hist[3][kBins];         // one a pass: each is read by the other CTAs while the next fills
+  // one a pass: each is read by the other CTAs while the next fills
+  int hist[3][kBins];
+  int coarse[3][kBins / 32];  // sums of 32 bins
   int warp[kRankWarps];
-  uint32_t lo, hi;            // of the slice's keys (unprotected or not)
-  int newest;                 // of the slice's positions
-  int movers;                 // of the slice
-  int holes;
+  // of the slice
+  uint32_t lo, hi;            // keys (of unprotected and protected entries alike)
+  int newest;                 // positions
+  int holes, movers;
+  // of the request, as warp 0 put it together
+  uint32_t all_lo, all_hi;
+  int all_newest;
   int digit, need, ties;      // of the pass: its bin, what is still to take, what it holds
+  int ties_before;            // of the slice
+  int first_hole[kMaxCluster], first_mover[kMaxCluster];
 };
 
 // Sum of v over the warps before this one (one value a warp, from lane 0);
@@ -87,26 +94,24 @@ __device__ __forceinline__ int warps_before(int v, int* s_warp, int* total) {
   return before;
 }
 
+// ranks: CTAs of a request's cluster.
 // kCached: the slice's keys are kept in shared memory (and, later, the lists of
 // its holes and movers in place of the positions); else every sweep forms the
 // keys from the inputs again, and the movers pass through pos_out.
-template <bool kCached>
+template <bool kCached, int ranks>
 __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p, int max_slice) {
   extern __shared__ __align__(16) unsigned char rank_smem[];
   RankShared& sh = *reinterpret_cast<RankShared*>(rank_smem);
   uint32_t* s_key = reinterpret_cast<uint32_t*>(rank_smem + sizeof(RankShared));   // [max_slice]
   int32_t* s_pos = reinterpret_cast<int32_t*>(s_key + (kCached ? max_slice : 0));  // [max_slice]
   cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int rank = ranks > 1 ? (int)cluster.block_rank() : 0;
   // a lone CTA needs no cluster barrier
   const auto sync_all = [&] {
     if (ranks > 1) cluster.sync(); else __syncthreads();
   };
-  // f(rank, its shared memory), the remote reads of all ranks in flight at once
-  const auto each_rank = [&](auto f) {
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-      if (r < ranks) f(r, ranks > 1 ? *cluster.map_shared_rank(&sh, r) : sh);
+  const auto of_rank = [&](int r) -> const RankShared& {
+    return ranks > 1 ? *cluster.map_shared_rank(&sh, r) : sh;
   };
   const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* w = p.sums + b * p.sums_s0;
@@ -175,13 +180,20 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
     }
   }
   sync_all();
-  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-  int newest = INT32_MIN;
-  each_rank([&](int, const RankShared& o) {
-    lo = min(lo, o.lo);
-    hi = max(hi, o.hi);
-    newest = max(newest, o.newest);
-  });
+  if (warp == 0) {                       // a lane a rank
+    const RankShared& o = of_rank(lane < ranks ? lane : 0);
+    const uint32_t l = __reduce_min_sync(0xffffffffu, o.lo);
+    const uint32_t h = __reduce_max_sync(0xffffffffu, o.hi);
+    const int q = __reduce_max_sync(0xffffffffu, o.newest);
+    if (lane == 0) {
+      sh.all_lo = l;
+      sh.all_hi = h;
+      sh.all_newest = q;
+    }
+  }
+  __syncthreads();
+  const uint32_t lo = sh.all_lo, hi = sh.all_hi;
+  const int newest = sh.all_newest;
   // position > newest - recent, in 64 bits: neither may wrap
   const int64_t after = (int64_t)newest - p.recent;
   // Keys relative to the smallest, so that the digits spread over the range
@@ -213,34 +225,54 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
       }
       if ((k & mask) == prefix) atomicAdd(&sh.hist[pass][(k >> shift) & (bins - 1)], 1);
     }
-    sync_all();
-    // bins from the top, two a thread: the one in which the count reaches `need`
-    int c[2] = {0, 0};
-    const int top = bins - 1 - 2 * tid;
-    each_rank([&](int, const RankShared& o) {
-      if (top >= 1) {                    // bins is even
-        const int2 h = *reinterpret_cast<const int2*>(&o.hist[pass][top - 1]);
-        c[0] += h.y;
-        c[1] += h.x;
-      }
-    });
-    int x = c[0] + c[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+    __syncthreads();
+    for (int c = warp; c < kBins / 32; c += kRankWarps) {
+      const int x = __reduce_add_sync(0xffffffffu, sh.hist[pass][c * 32 + lane]);
+      if (lane == 0) sh.coarse[pass][c] = x;
     }
-    int total;
-    const int mine = __shfl_sync(0xffffffffu, x, 31);
-    int before = warps_before(mine, sh.warp, &total) + x - c[0] - c[1];
+    sync_all();
+    // From the top, the bin in which the count reaches `need`: first among the
+    // sums of 32 bins, two a lane, then among the 32 (a few loads from each
+    // rank, where the whole histograms would be 8 KB from each).
+    if (warp == 0) {
+      int c0 = 0, c1 = 0;                // sums 63 - 2 lane and 62 - 2 lane
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (before < need && before + c[i] >= need) {
-        sh.digit = top - i;
-        sh.need = need - before;
-        sh.ties = c[i];
+      for (int r = 0; r < ranks; ++r) {
+        const int2 h = *reinterpret_cast<const int2*>(&of_rank(r).coarse[pass][62 - 2 * lane]);
+        c0 += h.y;
+        c1 += h.x;
       }
-      before += c[i];
+      int x = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const int before = x - c0 - c1;
+      const uint32_t here = __ballot_sync(0xffffffffu, before < need && x >= need);
+      const int who = __ffs(here) - 1;
+      const bool second = before + c0 < need;
+      const int group = __shfl_sync(0xffffffffu, 63 - 2 * lane - (second ? 1 : 0), who);
+      const int above = __shfl_sync(0xffffffffu, before + (second ? c0 : 0), who);
+      int c = 0, earlier = 0;            // bin 31 - lane of the group; the lower ranks' part
+#pragma unroll
+      for (int r = 0; r < ranks; ++r) {
+        const int h = of_rank(r).hist[pass][group * 32 + 31 - lane];
+        c += h;
+        if (r < rank) earlier += h;
+      }
+      x = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (above + x - c < need && above + x >= need) {
+        sh.digit = group * 32 + 31 - lane;
+        sh.need = need - (above + x - c);
+        sh.ties = c;
+        sh.ties_before = earlier;
+      }
     }
     __syncthreads();
     prefix |= (uint32_t)sh.digit << shift;
@@ -250,12 +282,9 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
     ++pass;
     if (sh.ties == need) break;            // the whole bin stays: no need to look into it
   }
-  // The first `need` of the bin's entries stay (of equal key, where the bin
-  // holds more).  The last pass's histogram counted them slice by slice.
-  int ties_before = 0;
-  each_rank([&](int r, const RankShared& o) {
-    if (r < rank) ties_before += o.hist[pass - 1][sh.digit];
-  });
+  // the first `need` of the bin's entries stay (of equal key, where the bin
+  // holds more)
+  int ties_before = sh.ties_before;
   const bool some = sh.ties != need;
   // Each warp takes a contiguous part of the slice, 32 entries at a time.
   const int part = ((ne + kRankThreads - 1) / kRankThreads) * 32;
@@ -295,6 +324,27 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
     sh.holes = holes;
     sh.movers = movers;
   }
+  // holes and movers of the ranks before each one
+  const auto ranks_before = [&] {
+    if (warp == 0) {
+      const RankShared& o = of_rank(lane < ranks ? lane : 0);
+      const int h = o.holes, m = o.movers;
+      int x = lane < ranks ? h : 0, y = lane < ranks ? m : 0;
+#pragma unroll
+      for (int d = 1; d < kMaxCluster; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
+        if (lane >= d) {
+          x += u;
+          y += v;
+        }
+      }
+      if (lane < ranks) {
+        sh.first_hole[lane] = x - h;
+        sh.first_mover[lane] = y - m;
+      }
+    }
+    __syncthreads();
+  };
   if constexpr (kCached) {
     // holes from the front of the list, movers from its back (an entry is at
     // most one of the two); then hole i of the request takes mover i, in
@@ -304,22 +354,12 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
       if (mover) s_pos[max_slice - 1 - (mover_at + m)] = e;
     });
     sync_all();
-    int first[kMaxCluster], base = 0, run = 0;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) first[r] = INT_MAX;
-    each_rank([&](int r, const RankShared& o) {
-      first[r] = run;
-      run += o.movers;
-      if (r < rank) base += o.holes;
-    });
+    ranks_before();
+    const int base = sh.first_hole[rank];
     for (int i = tid; i < holes; i += kRankThreads) {
-      int r = 0, at = 0;
-#pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q)
-        if (base + i >= first[q]) {
-          r = q;
-          at = first[q];
-        }
+      int r = 0;
+      while (r + 1 < ranks && base + i >= sh.first_mover[r + 1]) ++r;
+      const int at = sh.first_mover[r];
       const int32_t* list = ranks > 1 ? cluster.map_shared_rank(s_pos, r) : s_pos;
       const int from = list[max_slice - 1 - (base + i - at)], to = s_pos[i];
       kept[to] = from;
@@ -329,13 +369,9 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
     sync_all();                          // no CTA leaves while another reads its shared memory
   } else {
     sync_all();
-    int hole_base = hole_at, mover_base = mover_at;
-    each_rank([&](int r, const RankShared& o) {
-      if (r < rank) {
-        hole_base += o.holes;
-        mover_base += o.movers;
-      }
-    });
+    ranks_before();
+    const int hole_base = sh.first_hole[rank] + hole_at;
+    const int mover_base = sh.first_mover[rank] + mover_at;
     sweep([&](int e, bool, bool mover, int, int m) {
       if (mover) pos_out[mover_base + m] = e;
     });
@@ -413,34 +449,35 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
   }
 }
 
-struct EvictDevice {
-  int sms = 0;
-};
-
-cudaError_t evict_device(EvictDevice** out) {
+// The SMs of the current device; the rank kernels' set-up once per device.
+cudaError_t evict_device(int* n_sms) {
   static std::mutex mu;
-  static EvictDevice info[64];
+  static int sms[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
-  EvictDevice& d = info[dev];
-  if (d.sms == 0) {
+  if (sms[dev] == 0) {
     int n = 0;
     e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(rank_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(sizeof(RankShared) + kMaxSlice * 8));
-    if (e != cudaSuccess) return e;
-    d.sms = n;
+    for (auto k : {rank_kernel<true, 1>, rank_kernel<true, 2>, rank_kernel<true, 4>,
+                   rank_kernel<true, 8>}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(sizeof(RankShared) + kMaxSlice * 8));
+      if (e != cudaSuccess) return e;
+    }
+    sms[dev] = n;
   }
-  *out = &d;
+  *n_sms = sms[dev];
   return cudaSuccess;
 }
 
 // CTAs of a request's cluster: as many as leave every request a cluster of its
-// own, with at least kMinSlice entries each.
+// own, with at least kMinSlice entries each (16 requests of up to 65536 entries:
+// 132, 76, 31 and 31 us with 1, 2, 4 and 8 CTAs, where slices of 65536 and
+// 32768 do not fit in shared memory; 64 of 2064: 8.8 us with 1, 10.5 with 2).
 constexpr int64_t kMinSlice = 4096;
 
 cudaError_t launch_rank(const EvictParams& p, int reqs, int sms, cudaStream_t st) {
@@ -462,8 +499,15 @@ cudaError_t launch_rank(const EvictParams& p, int reqs, int sms, cudaStream_t st
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cached ? cudaLaunchKernelEx(&cfg, rank_kernel<true>, p, (int)slice)
-                : cudaLaunchKernelEx(&cfg, rank_kernel<false>, p, (int)slice);
+  const auto kernel = cached ? (ranks == 1   ? rank_kernel<true, 1>
+                                : ranks == 2 ? rank_kernel<true, 2>
+                                : ranks == 4 ? rank_kernel<true, 4>
+                                             : rank_kernel<true, 8>)
+                             : (ranks == 1   ? rank_kernel<false, 1>
+                                : ranks == 2 ? rank_kernel<false, 2>
+                                : ranks == 4 ? rank_kernel<false, 4>
+                                             : rank_kernel<false, 8>);
+  return cudaLaunchKernelEx(&cfg, kernel, p, (int)slice);
 }
 
 }  // namespace
@@ -524,13 +568,13 @@ extern "C" qsa_status qsa_evict_entries(
   p.err = error_word;
   bind_calling_thread();
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  EvictDevice* dev = nullptr;
-  if (evict_device(&dev) != cudaSuccess) return QSA_ERR_CUDA;
-  if (launch_rank(p, (int)R, dev->sms, s) != cudaSuccess) return QSA_ERR_CUDA;
+  int sms = 0;
+  if (evict_device(&sms) != cudaSuccess) return QSA_ERR_CUDA;
+  if (launch_rank(p, (int)R, sms, s) != cudaSuccess) return QSA_ERR_CUDA;
   const int64_t most = std::min<int64_t>(budget, std::max<int64_t>(0, p.cap - budget));
   if (most == 0) return QSA_OK;          // no request can have an entry too many
   const int64_t warps = kMoveThreads / 32;
-  const int64_t wave = std::max<int64_t>(1, (int64_t)dev->sms * (2048 / kMoveThreads) / R);
+  const int64_t wave = std::max<int64_t>(1, (int64_t)sms * (2048 / kMoveThreads) / R);
   // every place is looked at; a warp's share is at least one, at most 32
   const int64_t ctas = std::max((most + warps - 1) / warps, (budget + 32 * warps - 1) / (32 * warps));
   const dim3 grid((unsigned)std::min(ctas, wave), (unsigned)R);
