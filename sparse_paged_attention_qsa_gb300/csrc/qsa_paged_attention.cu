@@ -44,24 +44,30 @@ struct WeightParams {
   int64_t sums_out_s0;
 };
 
-// Thread: four entries of one request; the table's entries are a multiple of 8.
+// A lane holds four entries of one request (the table's entries are a multiple
+// of 8), a warp a part of the heads, so that their logits are all in flight at
+// once; the parts are added in warp order.
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightParams p) {
-  const int b = blockIdx.y;
-  const int e = ((int)blockIdx.x * kWeightThreads + threadIdx.x) * 4;
+  constexpr int kParts = kWeightThreads / 32;
+  __shared__ float4 s_part[kParts][32];
+  const int b = blockIdx.y, lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int e = ((int)blockIdx.x * 32 + lane) * 4;
+  pdl_wait();          // on every path: the grid's end must mean the walk's and the join's
   const int64_t ctx = p.ctx[b];
   const int n = (int)min(ctx, (int64_t)p.cap);
-  pdl_wait();          // on every path: the grid's end must mean the walk's and the join's
-  if (e >= n) return;
+  if ((int)blockIdx.x * 128 >= n) return;
+  const int per = (p.heads + kParts - 1) / kParts;
+  const int h0 = part * per, h1 = min(p.heads, h0 + per);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < p.next_n; ++j) {
     const int64_t hi = ctx - p.next_n + j + 1;
     const int64_t lo = p.window > 0 ? max((int64_t)0, hi - p.window) : 0;
-    if (e + 3 < lo || e >= hi) continue;
+    if (e + 3 < lo || e >= hi || e >= n) continue;
     const int64_t r0 = ((int64_t)b * p.next_n + j) * p.heads;
     const bool in[4] = {e >= lo, e + 1 >= lo && e + 1 < hi, e + 2 >= lo && e + 2 < hi,
-                        e + 3 < hi};
+                        e + 3 >= lo && e + 3 < hi};
 #pragma unroll 8
-    for (int h = 0; h < p.heads; ++h) {
+    for (int h = h0; h < h1; ++h) {
       const float4 z = *reinterpret_cast<const float4*>(p.z + (r0 + h) * p.pitch + e);
       const float l = p.lse2[r0 + h];
       // -inf (an absent entry): 0, also where the row saw nothing and l is -inf
@@ -71,12 +77,15 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightPar
       s.w += in[3] && z.w != -INFINITY ? exp2f(z.w - l) : 0.f;
     }
   }
-  const float* src = p.sums + b * p.sums_s0 + e;
-  float* dst = p.sums_out + b * p.sums_out_s0 + e;
-  const float v[4] = {s.x, s.y, s.z, s.w};
+  s_part[part][lane] = s;
+  __syncthreads();
+  if (e + part < n) {                    // warp i: the i-th entry of each four
+    static_assert(kParts == 4, "a warp an entry of four");
+    float v = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (e + i < n) dst[i] = src[i] + v[i];
+    for (int k = 0; k < kParts; ++k) v += reinterpret_cast<const float*>(&s_part[k][lane])[part];
+    p.sums_out[b * p.sums_out_s0 + e + part] = p.sums[b * p.sums_s0 + e + part] + v;
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -125,8 +134,8 @@ bool sizes_ok(int64_t reqs, int64_t next_n, int64_t heads, int64_t kv_heads, int
          heads * next_n <= 65536 && (dim == 64 || dim == 128 || dim == 256);
 }
 
-// The workspace: tiles before each request of a launch, the pieces of K/V
-// heads that the runs cut (at most two a run), then, when weights are asked
+// The workspace: where each run starts, the pieces of K/V heads that the
+// runs cut (at most two a run), then, when weights are asked
 // for, the rows' sums and logits.
 struct Layout {
   size_t ml, o, lse2, z, total;
@@ -137,7 +146,7 @@ Layout layout_of(int64_t reqs, int64_t next_n, int64_t heads, int64_t kv_heads, 
   const size_t rows = (size_t)std::min<int64_t>(next_n * (heads / kv_heads), kPagedMaxRows);
   const size_t all = (size_t)(reqs * next_n * heads);
   Layout l;
-  l.ml = round256((kPagedBatch + 1) * sizeof(int32_t));
+  l.ml = round256(kPagedMaxCtas * sizeof(int4));
   l.o = l.ml + round256(2 * kPagedMaxCtas * rows * 2 * sizeof(float));
   l.lse2 = l.o + round256(2 * kPagedMaxCtas * rows * (size_t)dim * sizeof(float));
   l.z = l.lse2 + (weight_cols > 0 ? round256(all * sizeof(float)) : 0);
@@ -232,7 +241,7 @@ extern "C" qsa_status qsa_paged_attention(
   const Layout l = layout_of(R, next_n, num_heads, cache->num_heads, cache->head_dim,
                              weights ? entries : 0);
   unsigned char* w = static_cast<unsigned char*>(workspace);
-  p.pre = reinterpret_cast<int32_t*>(w);
+  p.starts = reinterpret_cast<int4*>(w);
   p.part_ml = reinterpret_cast<float*>(w + l.ml);
   p.part_o = reinterpret_cast<float*>(w + l.o);
   if (weights && entries > 0) {
@@ -277,7 +286,7 @@ extern "C" qsa_status qsa_paged_attention(
     wp.sums_s0 = weight_sums_stride0;
     wp.sums_out = weight_sums_out;
     wp.sums_out_s0 = weight_sums_out_stride0;
-    const int64_t per_cta = kWeightThreads * 4;
+    const int64_t per_cta = 128;
     const dim3 grid((unsigned)((entries + per_cta - 1) / per_cta), (unsigned)R);
     if (launch_after(weights_kernel, grid, dim3(kWeightThreads), 0, s, wp) != cudaSuccess)
       return QSA_ERR_CUDA;

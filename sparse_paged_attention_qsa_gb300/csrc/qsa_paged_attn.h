@@ -33,7 +33,7 @@ struct PagedParams {
   float* lse2;                // workspace: [rows][heads] log2 sums, or null
   float* z;                   // workspace: [rows][heads][z_pitch] logits (base 2), or null
   int64_t z_pitch;
-  int32_t* pre;               // workspace: [kPagedBatch + 1] tiles before each request
+  int4* starts;               // workspace: [kPagedMaxCtas] request, tile, its tiles, all tiles
   float* part_ml;             // workspace: [2 * kPagedMaxCtas][chunk_rows][2]
   float* part_o;              // workspace: [2 * kPagedMaxCtas][chunk_rows][dim]
   uint32_t* err;

@@ -203,15 +203,6 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* pre, int batch, int32_t
   return TileAt{lo, w - pre[lo], pre[lo + 1] - pre[lo]};
 }
 
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-
 template <typename T, bool kFp8, int D, int WM>
 __global__ void __launch_bounds__(kWalkThreads, (WalkShape<kFp8, D, WM>::kCtas))
 paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
@@ -274,8 +265,10 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   const Runs runs = cut_runs(pre[p.batch], gridDim.x / units);
   const int32_t w_begin = run_start(runs, run), w_end = run_start(runs, run + 1);
   pdl_trigger();     // every CTA is resident: the join may be put in place (it waits)
-  if (blockIdx.x == 0)
-    for (int i = tid; i <= p.batch; i += kWalkThreads) p.pre[i] = pre[i];
+  if (unit == 0 && tid == 0 && w_begin < w_end) {          // where the run starts, for the join
+    const TileAt at = tile_at(pre, p.batch, w_begin);
+    p.starts[run] = make_int4(at.b, at.tile, at.count, runs.total);
+  }
 
   int issued = 0;                                          // producer: slots filled
   if (warp == 4) {
@@ -288,6 +281,9 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     int32_t chunk_id = -1;
     int32_t w = w_begin;
     int s = 0, round = 0;                                  // ring position of the next slot
+    // K and V pass through once: they give way in L2 to what is read again
+    // (queries, pages, logits), unless other CTAs walk the same tiles
+    const uint64_t policy = p.chunks == 1 ? evict_first_policy() : evict_normal_policy();
     bool stop = false;
     while (w < w_end && !stop) {
       const TileAt at = tile_at(pre, p.batch, w);
@@ -339,7 +335,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
             for (int i = 0; i < W::kChunks; ++i)
               tma_load_4d(dst + i * (TT * W::kChunkBytes) + lane * box_rows * W::kChunkBytes,
                           kv ? &vmap : &kmap, i * (W::kChunkBytes / (kFp8 ? 1 : 2)), head,
-                          be & ((1 << lg) - 1), id, full);
+                          be & ((1 << lg) - 1), id, full, policy);
           }
           ++issued;
           if (++s == S) {
@@ -797,86 +793,91 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
 }
 
 // CTA (c - 1, i, unit): row i of the unit in the request that the start of run
-// c cuts, if it is the first such cut.
+// c cuts, if it is the first such cut.  D/4 threads hold a row; the others take
+// further pieces of it, or, where there are few, further rows (then the CTAs of
+// those rows have nothing to do).
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int n_runs) {
   constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
-  __shared__ float s_w[kPagedMaxCtas], s_red[kJoinThreads / 32];
+  constexpr int kFew = 8;                                  // pieces that one group walks
   __shared__ __align__(16) float s_o[kGroups][D];
-  const int tid = threadIdx.x, c = blockIdx.x + 1, i = blockIdx.y, unit = blockIdx.z;
+  __shared__ float s_m[kGroups], s_l[kGroups];
+  const int tid = threadIdx.x, c = blockIdx.x + 1, unit = blockIdx.z;
+  const int grp = tid / kLanes, ln = tid % kLanes;
   pdl_wait();
   const int units = p.c.heads * p.chunks;
-  const Runs runs = cut_runs(p.pre[p.batch], n_runs);
+  // a run without tiles has written no start: the one before the first of
+  // those ends with the last tile, which run 0 knows
+  const Runs runs = cut_runs(p.starts[0].w, n_runs);
   const int32_t cut = run_start(runs, c);
-  if (cut >= runs.total) return;
-  const TileAt at = tile_at(p.pre, p.batch, cut);
-  const int32_t x0 = cut - at.tile;
+  if (runs.total == 0 || cut >= runs.total) return;
+  const int4 at = p.starts[c];                             // request, tile, its tiles, all
+  const int32_t x0 = cut - at.y;
   // between requests, or an earlier run's start cuts this one too
-  if (at.tile == 0 || run_start(runs, c - 1) > x0) return;
-  const int c0 = c - 1, c1 = run_of(runs, x0 + at.count - 1);
+  if (at.y == 0 || run_start(runs, c - 1) > x0) return;
+  const int c0 = c - 1, n = run_of(runs, x0 + at.z - 1) - c0 + 1;
+  const bool few = n <= kFew;
+  if (few && blockIdx.y % kGroups != 0) return;
+  const int i = blockIdx.y + (few ? grp : 0);              // the row, and its pieces:
+  const int k0 = few ? 0 : grp, dk = few ? 1 : kGroups;
   const int head = unit / p.chunks, chunk = unit - head * p.chunks;
   const int row0 = chunk * kPagedMaxRows, r = row0 + i;
-  if (i >= min(kPagedMaxRows, p.rows - row0)) return;
-  const int n = c1 - c0 + 1;
+  const bool there = i < min(kPagedMaxRows, p.rows - row0);
   // piece k's place in the workspace: a run's first segment, or its other one
   const int second = run_start(runs, c0) != x0;
-  const auto id_of = [&](int k) { return 2 * ((c0 + k) * units + unit) + (k == 0 ? second : 0); };
-  float mx = -INFINITY;
-  for (int k = tid; k < n; k += kJoinThreads) {
-    const float mk = p.part_ml[((int64_t)id_of(k) * p.chunk_rows + i) * 2];
-    s_w[k] = mk;
-    mx = fmaxf(mx, mk);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if ((tid & 31) == 0) s_red[tid >> 5] = mx;
-  __syncthreads();
-  float M = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, s_red[k]);
-  __syncthreads();
-  float sum = 0.f;
-  for (int k = tid; k < n; k += kJoinThreads) {
-    const float f = s_w[k] == -INFINITY ? 0.f : ex2(s_w[k] - M);
-    s_w[k] = f;
-    sum += f * p.part_ml[((int64_t)id_of(k) * p.chunk_rows + i) * 2 + 1];
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((tid & 31) == 0) s_red[tid >> 5] = sum;
-  __syncthreads();
-  float L = 0.f;
-#pragma unroll
-  for (int k = 0; k < kJoinThreads / 32; ++k) L += s_red[k];
-  const int grp = tid / kLanes, ln = tid % kLanes;
+  const auto piece_row = [&](int k) {
+    return (int64_t)(2 * ((c0 + k) * units + unit) + (k == 0 ? second : 0)) * p.chunk_rows + i;
+  };
+  float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (there) {
 #pragma unroll 4
-  for (int k = grp; k < n; k += kGroups) {
-    const float f = s_w[k];
-    const float4 v = *reinterpret_cast<const float4*>(
-        p.part_o + ((int64_t)id_of(k) * p.chunk_rows + i) * D + ln * 4);
-    acc.x += f * v.x;
-    acc.y += f * v.y;
-    acc.z += f * v.z;
-    acc.w += f * v.w;
+    for (int k = k0; k < n; k += dk) {
+      const int64_t at_k = piece_row(k);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at_k * 2);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at_k * D + ln * 4);
+      const float mn = fmaxf(m, ml.x);
+      const float a = mn == m ? 1.f : ex2(m - mn), f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+      l = l * a + ml.y * f;
+      acc.x = acc.x * a + v.x * f;
+      acc.y = acc.y * a + v.y * f;
+      acc.z = acc.z * a + v.z * f;
+      acc.w = acc.w * a + v.w * f;
+      m = mn;
+    }
   }
-  *reinterpret_cast<float4*>(&s_o[grp][ln * 4]) = acc;
-  __syncthreads();
-  const int64_t q_row = (int64_t)(p.b0 + at.b) * p.next_n;
-  const int j = r / p.group, h = head * p.group + r - j * p.group;
-  if (tid < D) {
-    float v = 0.f;
+  if (!few) {                                              // the groups' parts of the row
+    if (ln == 0) {
+      s_m[grp] = m;
+      s_l[grp] = l;
+    }
+    *reinterpret_cast<float4*>(&s_o[grp][ln * 4]) = acc;
+    __syncthreads();
+    if (grp != 0) return;
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) v += s_o[k][tid];
-    const float vscale = p.c.v_scale ? p.c.v_scale[head] : 1.f;
-    T* out = reinterpret_cast<T*>(p.out + (q_row + j) * p.out_row + h * p.out_head);
-    out[tid] = from_f<T>(L == 0.f ? 0.f : v * (vscale / L));
+    for (int k = 1; k < kGroups; ++k) {
+      const float mk = s_m[k], mn = fmaxf(m, mk);
+      const float a = mn == m ? 1.f : ex2(m - mn), f = mk == -INFINITY ? 0.f : ex2(mk - mn);
+      const float4 v = *reinterpret_cast<const float4*>(&s_o[k][ln * 4]);
+      l = l * a + s_l[k] * f;
+      acc.x = acc.x * a + v.x * f;
+      acc.y = acc.y * a + v.y * f;
+      acc.z = acc.z * a + v.z * f;
+      acc.w = acc.w * a + v.w * f;
+      m = mn;
+    }
   }
-  if (tid == 0) {
-    const int64_t rh = (q_row + j) * p.heads + h;
-    const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
-    if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
-    if (p.lse2) p.lse2[rh] = t;
+  if (!there) return;
+  const int j = r / p.group, h = head * p.group + r - j * p.group;
+  const int64_t row = (int64_t)(p.b0 + at.x) * p.next_n + j;
+  const float inv = l == 0.f ? 0.f : (p.c.v_scale ? p.c.v_scale[head] : 1.f) / l;
+  constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
+  *reinterpret_cast<uint2*>(p.out + row * p.out_row + h * p.out_head + ln * 8) =
+      make_uint2(pack2<kBf16>(acc.x * inv, acc.y * inv), pack2<kBf16>(acc.z * inv, acc.w * inv));
+  if (ln == 0) {
+    const float t = l == 0.f ? -INFINITY : m - kShift + log2f(l);
+    if (p.lse) p.lse[row * p.heads + h] = t * 0.693147180559945309f;
+    if (p.lse2) p.lse2[row * p.heads + h] = t;
   }
 }
 
