@@ -11,7 +11,7 @@
 
 namespace qsa {
 
-constexpr int kPagedBatch = 1024;   // requests per launch (their tile counts in shared memory)
+constexpr int kPagedBatch = 512;    // requests per launch (their tables in shared memory)
 constexpr int kPagedMaxCtas = 512;  // CTAs of the tile walk (what the workspace is sized for)
 constexpr int kPagedMaxRows = 64;   // query rows of one K/V head that share a walk
 
@@ -48,9 +48,25 @@ cudaError_t launch_paged_128(const PagedParams& p, bool bf16, bool fp8, const CU
 cudaError_t launch_paged_256(const PagedParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, cudaStream_t st);
 
-// Tokens of a tile, for an element of `dim * esize` bytes and `wm` groups of
-// 16 query rows: 128 where they take at most 128 bytes each and no more than
-// two row groups share the walk, else 64.
-constexpr int paged_tile(int row_bytes, int wm) { return row_bytes <= 128 && wm <= 2 ? 128 : 64; }
+// The shape of a CTA, for heads of `dim`, row_bytes of K (or V) a token and wm
+// groups of 16 query rows; what was measured, in us:
+//   four consumer warps, for up to 16 rows of heads below 256 two CTAs an SM;
+//   for more rows eight warps in one CTA (16-bit heads of 128: 32 rows 92 with
+//   eight, 111 with four; 64 rows 260 and 305); heads of 256 hold twice the
+//   output a row, so four warps with all registers (32 rows 181 against 331);
+//   ring slots of 16 KB, but of 32 KB for heads of 256 (E4M3: 138 against 167)
+//   and for 32 rows of 16-bit heads of 128 (92 against 108, where 64 rows take
+//   373 with 32 KB and 260 with 16); at most 64 tokens a warp, whose logits are
+//   in its registers.  Narrower heads with up to 16 rows in one CTA an SM and
+//   32 KB slots instead: 84 against 83 (131072 tokens), but 65 against 48 where
+//   requests are short, and 344 against 285 for E4M3 heads of 128.
+constexpr int paged_warps(int dim, int wm) { return wm == 1 || dim == 256 ? 4 : 8; }
+constexpr int paged_ctas(int dim, int wm) { return wm == 1 && dim < 256 ? 2 : 1; }
+// tokens of a tile
+constexpr int paged_tile(int dim, int row_bytes, int wm) {
+  const int slot = dim == 256 || (wm == 2 && row_bytes == 256) ? 32768 : 16384;
+  const int most = 64 * (paged_warps(dim, wm) / wm), t = slot / row_bytes;
+  return t < most ? t : most;
+}
 
 }  // namespace qsa

@@ -48,42 +48,50 @@
 namespace qsa {
 namespace {
 
-constexpr int kConsumers = 128;                // threads of the four consumer warps
-constexpr int kWalkThreads = kConsumers + 32;  // + the producer warp
 constexpr float kShift = 15.f;                 // weights are 2^(z - m + kShift)
 constexpr int kJoinThreads = 256;
 constexpr int kMaxSlots = 16;
-constexpr size_t kSmemPerSm = 233472, kSmemReserved = 1024;   // 228 KB, 1 KB of it a CTA's own
+constexpr int kSmemPerSm = 233472, kSmemReserved = 1024;   // 228 KB, 1 KB of it a CTA's own
+
+// Small tables of a CTA, behind the ring, the queries and the merge buffer.
+struct WalkTables {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];   // mbarriers of the ring
+  uint64_t q_full[2], q_empty[2];               // and of the two query slots
+  uint32_t boxes[kMaxSlots];                    // the slot's copies that found a page
+  float ml[8][16][2];                           // maximum and sum of a warp's rows
+  float qs[kPagedMaxRows];                      // what the queries were divided by
+  int32_t scan[9 * 32];
+  int32_t ctx[kPagedBatch];                     // cached tokens of each request
+  int32_t pre[kPagedBatch + 1];                 // tiles before each
+  int32_t abort;
+  int32_t pad[2];
+};
+static_assert(sizeof(WalkTables) % 16 == 0, "a whole number of 16-byte pieces");
 
 template <bool kFp8, int D, int WM>
 struct WalkShape {
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);        // a token's K (or V) of one head
-  static constexpr int TT = paged_tile(kRowBytes, WM);
-  static constexpr int WK = 4 / WM;
+  static constexpr int NW = paged_warps(D, WM);               // consumer warps
+  static constexpr int kConsumers = NW * 32;
+  static constexpr int kThreads = kConsumers + 32;            // + the producer warp
+  static constexpr int TT = paged_tile(D, kRowBytes, WM);
+  static constexpr int WK = NW / WM;
   static constexpr int kSlice = TT / WK;                      // tokens of a warp
   static constexpr int NS = kSlice / 16;                      // in steps of 16
   static constexpr int kChunkBytes = kRowBytes < 128 ? kRowBytes : 128;   // TMA inner extent
   static constexpr int kChunks = kRowBytes / kChunkBytes;     // copies that fill a slot
   static constexpr int kSlot = TT * kRowBytes;                // K (or V) of a tile
   static constexpr int kQPitch = D + 8;                       // halves; + 16 B against conflicts
-  static constexpr int kQBytes = 16 * WM * kQPitch * 2;
-  static constexpr int kMergeCols = 32;
-  static constexpr int kMergeBytes = 64 * (kMergeCols + 4) * 4;
-  static constexpr int kStage = ((kQBytes > kMergeBytes ? kQBytes : kMergeBytes) + 1023) & ~1023;
-  static constexpr int kMisc = 2816;                          // barriers and small tables
-  static constexpr int kFixed = 1024 + kStage + kMisc + (kPagedBatch + 1) * 4;
-  static constexpr int fit(int ctas) {
-    const int n = (int)((kSmemPerSm / ctas - kSmemReserved - kFixed) / kSlot);
-    return n > kMaxSlots ? kMaxSlots : n;
-  }
-#ifdef QSA_PAGED_CTAS
-  static constexpr int kCtas = QSA_PAGED_CTAS;
-#else
-  static constexpr int kCtas = D == 256 ? 1 : 2;
-#endif
-  static constexpr int S = fit(kCtas);
+  static constexpr int kQBytes = 16 * WM * kQPitch * 2;       // a query slot
+  static constexpr int kQSlots = kFp8 ? 3 : 2;                // the third: as FP16, reordered
+  static constexpr int kMergeBytes = NW == 8 ? 128 * 40 * 4 : 17408;   // at least 32 columns
+  static constexpr int kFixed = 1024 + kQSlots * kQBytes + kMergeBytes + (int)sizeof(WalkTables);
+  static constexpr int kCtas = paged_ctas(D, WM);
+  static constexpr int kFit = (kSmemPerSm / kCtas - kSmemReserved - kFixed) / kSlot;
+  static constexpr int S = kFit < kMaxSlots ? kFit : kMaxSlots;
   static constexpr size_t kSmem = (size_t)kFixed + (size_t)S * kSlot;
   static_assert(S >= 3, "the ring needs K, V and one slot ahead");
+  static_assert(NS >= 1 && NS <= 4, "logits of a tile stay in registers");
   static constexpr bool kPair = !kFp8 && WM <= 2;             // weights as value + remainder
 };
 
@@ -144,8 +152,9 @@ __device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
       : "=r"(r) : "r"(x));
   return r;
 }
+template <int kThreads>
 __device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
 
 // Visible entries [lo, hi) of token j of a request with ctx cached tokens,
@@ -204,7 +213,7 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* pre, int batch, int32_t
 }
 
 template <typename T, bool kFp8, int D, int WM>
-__global__ void __launch_bounds__(kWalkThreads, (WalkShape<kFp8, D, WM>::kCtas))
+__global__ void __launch_bounds__((WalkShape<kFp8, D, WM>::kThreads), (WalkShape<kFp8, D, WM>::kCtas))
 paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
   using W = WalkShape<kFp8, D, WM>;
@@ -216,41 +225,49 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
   unsigned char* base = smem_raw + pad;
   const uint32_t ring = raw + pad;
-  unsigned char* stage = base + S * W::kSlot;              // queries, or merge buffer
-  const uint32_t stage_a = ring + S * W::kSlot;
-  unsigned char* misc = stage + W::kStage;                 // kMisc bytes
-  const uint32_t bar_full = stage_a + W::kStage, bar_empty = bar_full + 8 * 16;
-  uint32_t* boxes = reinterpret_cast<uint32_t*>(misc + 256);       // [16] valid boxes of a slot
-  float* s_ml = reinterpret_cast<float*>(misc + 384);              // [4][16][2]
-  float* s_qs = reinterpret_cast<float*>(misc + 896);              // [64] row multipliers
-  float* s_f = reinterpret_cast<float*>(misc + 1152);              // [4][16] merge factors
-  float* s_row = reinterpret_cast<float*>(misc + 1408);            // [64] merged sums
-  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 1920);
-  int32_t* s_scan = reinterpret_cast<int32_t*>(misc + 1984);       // [160]
-  int32_t* pre = reinterpret_cast<int32_t*>(misc + W::kMisc);      // [batch + 1]
+  const uint32_t queries = ring + S * W::kSlot;            // query slots, then the merge buffer
+  constexpr int kBehind = S * W::kSlot + W::kQSlots * W::kQBytes;
+  float* merge = reinterpret_cast<float*>(base + kBehind);
+  WalkTables& tb = *reinterpret_cast<WalkTables*>(base + kBehind + W::kMergeBytes);
+  const uint32_t bar_full = ring + kBehind + W::kMergeBytes, bar_empty = bar_full + 8 * kMaxSlots;
+  const uint32_t bar_qfull = bar_empty + 8 * kMaxSlots, bar_qempty = bar_qfull + 16;
+  volatile int32_t* s_abort = &tb.abort;
+  int32_t* pre = tb.pre;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, 4);
+      mbar_init(bar_empty + 8 * s, W::NW);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_qfull + 8 * s, 1);
+      mbar_init(bar_qempty + 8 * s, W::NW);
     }
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // rows past the last query stay zero in every slot
+  for (int i = tid; i < W::kQSlots * W::kQBytes / 16; i += W::kThreads)
+    reinterpret_cast<uint4*>(base + S * W::kSlot)[i] = make_uint4(0, 0, 0, 0);
   // tiles before each request
   {
-    const int per = (p.batch + kWalkThreads - 1) / kWalkThreads;
+    const int per = (p.batch + W::kThreads - 1) / W::kThreads;
     const int lo = min(p.batch, tid * per), hi = min(p.batch, lo + per);
     int32_t sum = 0, x;
     for (int b = lo; b < hi; ++b) {
-      const int32_t n = tiles_of<TT>(p, p.ctx[p.b0 + b], &x);
+      const int32_t ctx = p.ctx[p.b0 + b];
+      const int32_t n = tiles_of<TT>(p, ctx, &x);
+      tb.ctx[b] = ctx;
       pre[b + 1] = n;
       sum += n;
     }
-    s_scan[tid] = sum;
+    tb.scan[tid] = sum;
+    // the zeros above were written through the generic proxy, copies follow
+    // through the async one
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     int32_t before = 0;
-    for (int i = 0; i < (lo < hi ? tid : 0); ++i) before += s_scan[i];
+    for (int i = 0; i < (lo < hi ? tid : 0); ++i) before += tb.scan[i];
     for (int b = lo; b < hi; ++b) {
       before += pre[b + 1];
       pre[b + 1] = before;
@@ -265,43 +282,103 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   const Runs runs = cut_runs(pre[p.batch], gridDim.x / units);
   const int32_t w_begin = run_start(runs, run), w_end = run_start(runs, run + 1);
   pdl_trigger();     // every CTA is resident: the join may be put in place (it waits)
-  if (unit == 0 && tid == 0 && w_begin < w_end) {          // where the run starts, for the join
-    const TileAt at = tile_at(pre, p.batch, w_begin);
+  // where the run starts, for the join; run 0 always says how many tiles there are
+  if (unit == 0 && tid == 0 && (run == 0 || w_begin < w_end)) {
+    TileAt at = {0, 0, 0};
+    if (w_begin < w_end) at = tile_at(pre, p.batch, w_begin);
     p.starts[run] = make_int4(at.b, at.tile, at.count, runs.total);
   }
 
-  int issued = 0;                                          // producer: slots filled
-  if (warp == 4) {
+  const int row0 = chunk * kPagedMaxRows;
+  const int n_rows = min(kPagedMaxRows, p.rows - row0);    // query rows of this unit
+  const auto row_ptr = [&](const unsigned char* t, int64_t rs, int64_t hs, int b, int i) {
+    const int r = row0 + i, j = r / p.group;
+    return t + ((int64_t)(p.b0 + b) * p.next_n + j) * rs +
+           (int64_t)(head * p.group + r - j * p.group) * hs;
+  };
+
+  int issued = 0, segments = 0;                            // producer: slots, queries loaded
+  if (warp == W::NW) {
     // ---------------- producer ----------------
     const int lg = p.c.page_log2;
     const int box_rows = min(TT, 1 << lg);
     const int n_boxes = TT / box_rows;
     const int tile_cols = max(1, TT >> lg);
-    int chunk_b = -1, chunk_col = 0;                       // 32 page ids, one a lane
-    int32_t chunk_id = -1;
     int32_t w = w_begin;
     int s = 0, round = 0;                                  // ring position of the next slot
-    // K and V pass through once: they give way in L2 to what is read again
-    // (queries, pages, logits), unless other CTAs walk the same tiles
-    const uint64_t policy = p.chunks == 1 ? evict_first_policy() : evict_normal_policy();
+    // Narrow rows, and K and V beside logits that are read again, give way in L2
+    // first (E4M3 heads of 128: 292 us against 296, FP16 heads of 64: 45 against
+    // 48); wide rows go through as anything does (heads of 256: 635 against 656).
+    const uint64_t policy = p.chunks == 1 && (p.z != nullptr || W::kRowBytes <= 128)
+                                ? evict_first_policy() : evict_normal_policy();
     bool stop = false;
+    // a slot free again; false (and the walk stopped) after the limit
+    const auto wait_empty = [&](uint32_t bar, uint32_t phase) {
+      bool ok = *s_abort == 0 && mbar_wait(bar, phase);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) {
+          *s_abort = 1;
+          report(p.err, QSA_DERR_TIMEOUT);
+        }
+        stop = true;
+      }
+      return ok;
+    };
+    // 32 page ids of a request, one a lane; the next segment's are on their way
+    // while this one's tiles are issued
+    const auto first_col = [&](const TileAt& at) {
+      int32_t first;
+      tiles_of<TT>(p, tb.ctx[at.b], &first);
+      return ((first + at.tile) * TT) >> lg;
+    };
+    const auto page_ids = [&](int b, int col) {
+      return col + lane < p.c.cols ? __ldg(p.c.bt + (int64_t)(p.b0 + b) * p.c.bt_s0 + col + lane)
+                                   : -1;
+    };
+    TileAt at = {0, 0, 0};
+    int chunk_col = 0;
+    int32_t chunk_id = -1;
+    if (w < w_end) {
+      at = tile_at(pre, p.batch, w);
+      chunk_col = first_col(at);
+      chunk_id = page_ids(at.b, chunk_col);
+    }
     while (w < w_end && !stop) {
-      const TileAt at = tile_at(pre, p.batch, w);
-      const int32_t ctx = p.ctx[p.b0 + at.b];
+      const int32_t ctx = tb.ctx[at.b];
       int32_t first, lo, hi, x;
       tiles_of<TT>(p, ctx, &first);
       visible(p, ctx, 0, &lo, &x);
       visible(p, ctx, p.next_n - 1, &x, &hi);
       if (ctx > p.c.cap && lane == 0) report(p.err, QSA_DERR_CONTEXT);
-      const int32_t* row = p.c.bt + (int64_t)(p.b0 + at.b) * p.c.bt_s0;
       const int32_t seg_end = min(w_end, w + (at.count - at.tile));
+      TileAt next = at;
+      int next_col = 0;
+      int32_t next_id = -1;
+      if (seg_end < w_end) {
+        next = tile_at(pre, p.batch, seg_end);
+        next_col = first_col(next);
+        next_id = page_ids(next.b, next_col);
+      }
+      // the segment's queries
+      {
+        const int qs = segments & 1;
+        if (segments >= 2 && !wait_empty(bar_qempty + 8 * qs, (uint32_t)((segments / 2 - 1) & 1)))
+          break;
+        const uint32_t full = bar_qfull + 8 * qs;
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)(n_rows * D * 2));
+        __syncwarp();
+        for (int i = lane; i < n_rows; i += 32)
+          bulk_load(queries + qs * W::kQBytes + i * W::kQPitch * 2,
+                    row_ptr(p.q, p.q_row, p.q_head, at.b, i), D * 2, full);
+        ++segments;
+      }
       for (int t = at.tile; w < seg_end; ++w, ++t) {
         const int32_t e0 = (first + t) * TT;
         const int col = e0 >> lg;
-        if (at.b != chunk_b || col < chunk_col || col + tile_cols > chunk_col + 32) {
-          chunk_b = at.b;
+        if (col + tile_cols > chunk_col + 32) {
           chunk_col = col;
-          chunk_id = col + lane < p.c.cols ? __ldg(row + col + lane) : -1;
+          chunk_id = page_ids(at.b, col);
         }
         const int32_t id = __shfl_sync(0xffffffffu, chunk_id,
                                        col - chunk_col + (lane < n_boxes ? (lane * box_rows) >> lg : 0));
@@ -312,21 +389,10 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (round > 0) {
-            bool ok = *s_abort == 0 && mbar_wait(bar_empty + 8 * s, (uint32_t)((round - 1) & 1));
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
-              if (lane == 0) {
-                *s_abort = 1;
-                report(p.err, QSA_DERR_TIMEOUT);
-              }
-              stop = true;
-              break;
-            }
-          }
+          if (round > 0 && !wait_empty(bar_empty + 8 * s, (uint32_t)((round - 1) & 1))) break;
           const uint32_t full = bar_full + 8 * s, dst = ring + s * W::kSlot;
           if (lane == 0) {
-            boxes[s] = mask;
+            tb.boxes[s] = mask;
             mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * W::kRowBytes));
           }
           __syncwarp();
@@ -345,13 +411,16 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         }
         if (stop) break;
       }
+      at = next;
+      chunk_col = next_col;
+      chunk_id = next_id;
     }
   } else {
     // ---------------- consumers ----------------
     const int wm = warp % WM, wk = warp / WM;
     const int g = lane >> 2, q4 = lane & 3;
     const int lg = p.c.page_log2;
-    const int box_log2 = min(lg, TT == 128 ? 7 : 6);
+    const int box_log2 = min(lg, TT == 256 ? 8 : TT == 128 ? 7 : 6);
     const uint32_t all_boxes = TT >> box_log2 >= 32 ? 0xffffffffu : (1u << (TT >> box_log2)) - 1u;
     // ldmatrix source rows and the swizzle's exclusive-or, constant a lane
     const int k_row = wk * W::kSlice + ((lane >> 4) << 3) + (lane & 7);       // K: tokens by 8
@@ -362,19 +431,19 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     const auto piece = [&](int row, int c) -> uint32_t {   // 16-byte piece c of a row of a slot
       return (uint32_t)(row * W::kChunkBytes + ((c ^ sw) << 4));
     };
-    const uint32_t q_addr = stage_a + (uint32_t)(((wm * 16 + (lane & 15)) * W::kQPitch +
+    const uint32_t q_lane = queries + (uint32_t)(((wm * 16 + (lane & 15)) * W::kQPitch +
                                                   (lane >> 4) * 8) * 2);
     // a slot's wait: after a time-out every warp runs its loops to their end
     // without waiting, so that the barriers between them stay matched
     int slot = 0;                                          // ring position, and its phase
     uint32_t phase = 0;
-    const auto wait_full = [&]() {
-      if (!mbar_try_wait(bar_full + 8 * slot, phase) && *s_abort == 0 &&
-          !mbar_wait(bar_full + 8 * slot, phase)) {
+    const auto wait_for = [&](uint32_t bar, uint32_t ph) {
+      if (!mbar_try_wait(bar, ph) && *s_abort == 0 && !mbar_wait(bar, ph)) {
         *s_abort = 1;
         if (lane == 0) report(p.err, QSA_DERR_TIMEOUT);
       }
     };
+    const auto wait_full = [&]() { wait_for(bar_full + 8 * slot, phase); };
     const auto release = [&]() {                           // and on to the next slot
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_empty + 8 * slot);
@@ -388,27 +457,25 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
       if (pre[b + 1] != pre[b]) continue;
       const int64_t r0 = (int64_t)(p.b0 + b) * p.next_n;
-      if (p.ctx[p.b0 + b] > p.c.cap && tid == 0) report(p.err, QSA_DERR_CONTEXT);
+      if (tb.ctx[b] > p.c.cap && tid == 0) report(p.err, QSA_DERR_CONTEXT);
       const int n = p.next_n * p.heads;
-      for (int i = tid; i < n * (D / 8); i += kConsumers) {
+      for (int i = tid; i < n * (D / 8); i += W::kConsumers) {
         const int rh = i / (D / 8), o = i % (D / 8);
         *reinterpret_cast<uint4*>(p.out + (r0 + rh / p.heads) * p.out_row +
                                   (rh % p.heads) * p.out_head + o * 16) = make_uint4(0, 0, 0, 0);
       }
-      for (int i = tid; i < n; i += kConsumers) {
+      for (int i = tid; i < n; i += W::kConsumers) {
         if (p.lse) p.lse[r0 * p.heads + i] = -INFINITY;
         if (p.lse2) p.lse2[r0 * p.heads + i] = -INFINITY;
       }
     }
 
-    const int row0 = chunk * kPagedMaxRows;
-    const int n_rows = min(kPagedMaxRows, p.rows - row0);            // of this unit
     int32_t w = w_begin;
-    while (w < w_end) {
+    for (int seg = 0; w < w_end; ++seg) {
       const TileAt at = tile_at(pre, p.batch, w);
       const int32_t seg_begin = w, seg_end = min(w_end, w + (at.count - at.tile));
       const bool whole = at.tile == 0 && seg_end - seg_begin == at.count;
-      const int32_t ctx = p.ctx[p.b0 + at.b];
+      const int32_t ctx = tb.ctx[at.b];
       int32_t first, lo_all, hi_all, x;
       tiles_of<TT>(p, ctx, &first);
       visible(p, ctx, 0, &lo_all, &x);
@@ -418,25 +485,21 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       visible(p, ctx, p.next_n - 1, &lo_in, &x);
       visible(p, ctx, 0, &x, &hi_in);
       const int64_t q_row = (int64_t)(p.b0 + at.b) * p.next_n;
-      const auto row_ptr = [&](const unsigned char* t, int64_t rs, int64_t hs, int i) {
-        const int r = row0 + i, j = r / p.group;
-        return t + (q_row + j) * rs + (int64_t)(head * p.group + r - j * p.group) * hs;
-      };
 
-      // queries into shared memory (the merge buffer before is done with)
-      consumers_sync();
-      T* qs = reinterpret_cast<T*>(stage);
-      for (int i = tid; i < 16 * WM * (D / 8); i += kConsumers) {
-        const int r = i / (D / 8), o = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < n_rows)
-          v = *reinterpret_cast<const uint4*>(row_ptr(p.q, p.q_row, p.q_head, r) + o * 16);
-        if constexpr (!kFp8) {
-          *reinterpret_cast<uint4*>(qs + r * W::kQPitch + o * 8) = v;
-        } else {
+      // the queries: as they came, or for E4M3 as FP16 in the third slot
+      const int qs = seg & 1;
+      wait_for(bar_qfull + 8 * qs, (uint32_t)((seg >> 1) & 1));
+      const uint32_t q_addr = q_lane + (kFp8 ? 2 : qs) * W::kQBytes;
+      if constexpr (kFp8) {
+        const unsigned char* src = base + S * W::kSlot + qs * W::kQBytes;
+        uint32_t* fp16 = reinterpret_cast<uint32_t*>(base + S * W::kSlot + 2 * W::kQBytes);
+        consumers_sync<W::kConsumers>();                   // all are done with the last ones
+        for (int i = tid; i < 16 * WM * (D / 8); i += W::kConsumers) {
           // D/8 lanes (8, 16 or 32, aligned) hold one row: its largest
           // magnitude, then FP16 with each 16 dims in the order in which the
           // E4M3 fragments hold them (dims 4q, 4q+1 at 2q and 4q+2, 4q+3 at 8 + 2q)
+          const int r = i / (D / 8), o = i % (D / 8);
+          const uint4 v = *reinterpret_cast<const uint4*>(src + r * W::kQPitch * 2 + o * 16);
           float f[8];
           const T* h = reinterpret_cast<const T*>(&v);
 #pragma unroll
@@ -458,16 +521,16 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
               for (int k = 0; k < 8; ++k) f[k] *= by;
             }
           }
-          uint32_t* dst = reinterpret_cast<uint32_t*>(qs + r * W::kQPitch + (o >> 1) * 16);
+          uint32_t* dst = fp16 + (r * W::kQPitch + (o >> 1) * 16) / 2;
           const int q2 = (o & 1) * 2;
           dst[q2] = pack2<false>(f[0], f[1]);
           dst[q2 + 4] = pack2<false>(f[2], f[3]);
           dst[q2 + 1] = pack2<false>(f[4], f[5]);
           dst[q2 + 5] = pack2<false>(f[6], f[7]);
-          if (o == 0) s_qs[r] = mul;
+          if (o == 0) tb.qs[r] = mul;
         }
+        consumers_sync<W::kConsumers>();
       }
-      consumers_sync();
 
       // this thread's rows: wm*16 + g and + 8
       float mult[2];
@@ -482,8 +545,9 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         mult[k] = p.scale_log2;
         if constexpr (kFp8) {
           if (p.c.k_scale) mult[k] *= p.c.k_scale[head];
-          mult[k] *= s_qs[wm * 16 + g + 8 * k];
+          mult[k] *= tb.qs[wm * 16 + g + 8 * k];
         }
+        const int64_t q_row = (int64_t)(p.b0 + at.b) * p.next_n;
         zp[k] = p.z && i < n_rows
                     ? p.z + ((q_row + row_j[k]) * p.heads + head * p.group + r - row_j[k] * p.group) *
                                 p.z_pitch
@@ -498,7 +562,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         const int32_t e0 = (first + t) * TT;
         const int32_t we = e0 + wk * W::kSlice;            // the warp's first entry
         wait_full();
-        const uint32_t mask = boxes[slot];
+        const uint32_t mask = tb.boxes[slot];
         const bool edge = e0 < lo_in || e0 + TT > hi_in || mask != all_boxes;
         float sc[NS][2][4];
 #pragma unroll
@@ -685,110 +749,102 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       }
 
       // ---- the segment's end: merge the WK slices, write the result or a piece
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_qempty + 8 * qs);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
         l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-        if (q4 == 0) {
-          s_ml[(warp * 16 + g + 8 * k) * 2] = m[k];
-          s_ml[(warp * 16 + g + 8 * k) * 2 + 1] = l[k];
-        }
       }
-      consumers_sync();
-      const int id = 2 * blockIdx.x + (seg_begin == w_begin ? 0 : 1);
-      if (tid < 16 * WM) {
-        const int i = tid, rm = i >> 4, rr = i & 15;       // row i: warps rm, rm + WM, ...
-        float M = -INFINITY, L = 0.f;
+      const int64_t id = 2 * (int64_t)blockIdx.x + (seg_begin == w_begin ? 0 : 1);
+      const float vscale = kFp8 && p.c.v_scale ? p.c.v_scale[head] : 1.f;
+      // the real rows of every slice side by side, as many columns at a time
+      // as the buffer holds (all of them for up to 16 rows and slices)
+      const int cols = min(D, (W::kMergeBytes / 4 / (WK * n_rows) - 8) & ~31);
+      const int pitch = cols + 8;
+      for (int c0 = 0; c0 < D; c0 += cols) {
+        const int c1 = min(D, c0 + cols);
+        consumers_sync<W::kConsumers>();                   // the buffer is free
 #pragma unroll
-        for (int k = 0; k < WK; ++k) M = fmaxf(M, s_ml[((rm + k * WM) * 16 + rr) * 2]);
+        for (int k = 0; k < 2; ++k) {
+          const int i = wm * 16 + g + 8 * k;
+          if (i < n_rows) {
+            float* b = merge + (wk * n_rows + i) * pitch - c0;
 #pragma unroll
-        for (int k = 0; k < WK; ++k) {
-          const int at_w = (rm + k * WM) * 16 + rr;
-          const float f = M == -INFINITY ? 0.f : ex2(s_ml[at_w * 2] - M);
-          s_f[at_w] = f;
-          L += s_ml[at_w * 2 + 1] * f;
-        }
-        s_row[i] = L;
-        if (i < n_rows) {
-          if (whole) {
-            const int r = row0 + i, j = r / p.group;
-            const int64_t rh = (q_row + j) * p.heads + head * p.group + r - j * p.group;
-            const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
-            if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
-            if (p.lse2) p.lse2[rh] = t;
-          } else {
-            float* ml = p.part_ml + ((int64_t)id * p.chunk_rows + i) * 2;
-            ml[0] = M;
-            ml[1] = L;
-          }
-        }
-      }
-      consumers_sync();
-      {
-        float f[2];
-        f[0] = s_f[warp * 16 + g];
-        f[1] = s_f[warp * 16 + g + 8];
-        float* buf = reinterpret_cast<float*>(stage);
-        constexpr int C = W::kMergeCols, P = C + 4;        // columns at a time, and their pitch
-        const float vscale = kFp8 && p.c.v_scale ? p.c.v_scale[head] : 1.f;
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += C) {
-#pragma unroll
-          for (int i = 0; i < C / 8; ++i) {
-            const int n = c0 / 8 + i;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float* b = buf + (warp * 16 + g + 8 * k) * P;
-              // 0 * f where no entry was seen: the accumulators are 0 there
-              const float x = o[n][2 * k] * f[k], y = o[n][2 * k + 1] * f[k];
-              if constexpr (!kFp8) {
-                *reinterpret_cast<float2*>(b + i * 8 + 2 * q4) = make_float2(x, y);
-              } else {
-                // tile n holds the even (odd) dims of the 16 from 16 (n / 2)
-                b[(i >> 1) * 16 + 4 * q4 + (i & 1)] = x;
-                b[(i >> 1) * 16 + 4 * q4 + 2 + (i & 1)] = y;
+            for (int n = 0; n < D / 8; ++n) {
+              if (n * 8 >= c0 && n * 8 < c1) {
+                if constexpr (!kFp8) {
+                  *reinterpret_cast<float2*>(b + n * 8 + 2 * q4) =
+                      make_float2(o[n][2 * k], o[n][2 * k + 1]);
+                } else {
+                  // tile n holds the even (odd) dims of the 16 from 16 (n / 2)
+                  b[(n >> 1) * 16 + 4 * q4 + (n & 1)] = o[n][2 * k];
+                  b[(n >> 1) * 16 + 4 * q4 + 2 + (n & 1)] = o[n][2 * k + 1];
+                }
               }
             }
-          }
-          consumers_sync();
-          for (int i = tid; i < n_rows * (C / 8); i += kConsumers) {
-            const int r = i / (C / 8), c = (i % (C / 8)) * 8;
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < WK; ++k) {
-              const float4* b = reinterpret_cast<const float4*>(
-                  buf + (((r >> 4) + k * WM) * 16 + (r & 15)) * P + c);
-              const float4 a0 = b[0], a1 = b[1];
-              v[0] += a0.x; v[1] += a0.y; v[2] += a0.z; v[3] += a0.w;
-              v[4] += a1.x; v[5] += a1.y; v[6] += a1.z; v[7] += a1.w;
-            }
-            if (whole) {
-              const float L = s_row[r];
-              const float inv = L == 0.f ? 0.f : vscale / L;   // 0: a row that saw nothing
-              uint32_t h[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                h[k] = pack2<__is_same(T, __nv_bfloat16)>(v[2 * k] * inv, v[2 * k + 1] * inv);
-              *reinterpret_cast<uint4*>(
-                  const_cast<unsigned char*>(row_ptr(p.out, p.out_row, p.out_head, r)) +
-                  (c0 + c) * 2) = make_uint4(h[0], h[1], h[2], h[3]);
-            } else {
-              float4* d = reinterpret_cast<float4*>(
-                  p.part_o + ((int64_t)id * p.chunk_rows + r) * D + c0 + c);
-              d[0] = make_float4(v[0], v[1], v[2], v[3]);
-              d[1] = make_float4(v[4], v[5], v[6], v[7]);
+            if (q4 == 0) {
+              tb.ml[warp][g + 8 * k][0] = m[k];
+              tb.ml[warp][g + 8 * k][1] = l[k];
             }
           }
-          if (c0 + C < D) consumers_sync();
+        }
+        consumers_sync<W::kConsumers>();
+        const int groups = (c1 - c0) / 8;
+        for (int it = tid; it < n_rows * groups; it += W::kConsumers) {
+          const int i = it / groups, c = (it - i * groups) * 8;
+          const float* ml[WK];
+          float M = -INFINITY, L = 0.f, f[WK];
+#pragma unroll
+          for (int k = 0; k < WK; ++k) {
+            ml[k] = tb.ml[(i >> 4) + k * WM][i & 15];
+            M = fmaxf(M, ml[k][0]);
+          }
+          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < WK; ++k) {
+            f[k] = M == -INFINITY ? 0.f : ex2(ml[k][0] - M);
+            L += ml[k][1] * f[k];
+            const float4* b = reinterpret_cast<const float4*>(merge + (k * n_rows + i) * pitch + c);
+            const float4 a0 = b[0], a1 = b[1];
+            v[0] += a0.x * f[k]; v[1] += a0.y * f[k]; v[2] += a0.z * f[k]; v[3] += a0.w * f[k];
+            v[4] += a1.x * f[k]; v[5] += a1.y * f[k]; v[6] += a1.z * f[k]; v[7] += a1.w * f[k];
+          }
+          if (whole) {
+            const float inv = L == 0.f ? 0.f : vscale / L;   // 0: a row that saw nothing
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = pack2<__is_same(T, __nv_bfloat16)>(v[2 * k] * inv, v[2 * k + 1] * inv);
+            *reinterpret_cast<uint4*>(
+                const_cast<unsigned char*>(row_ptr(p.out, p.out_row, p.out_head, at.b, i)) +
+                (c0 + c) * 2) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (c0 + c == 0) {
+              const int r = row0 + i, j = r / p.group;
+              const int64_t rh = ((int64_t)(p.b0 + at.b) * p.next_n + j) * p.heads +
+                                 head * p.group + r - j * p.group;
+              const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
+              if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
+              if (p.lse2) p.lse2[rh] = t;
+            }
+          } else {
+            float4* d = reinterpret_cast<float4*>(p.part_o + (id * p.chunk_rows + i) * D + c0 + c);
+            d[0] = make_float4(v[0], v[1], v[2], v[3]);
+            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+            if (c0 + c == 0)
+              *reinterpret_cast<float2*>(p.part_ml + (id * p.chunk_rows + i) * 2) = make_float2(M, L);
+          }
         }
       }
     }
   }
   __syncthreads();
   // after a time-out, let the copies this CTA issued land before it exits
-  if (*s_abort != 0 && warp == 4 && lane == 0) {
+  if (*s_abort != 0 && warp == W::NW && lane == 0) {
     for (int n = issued > S ? issued - S : 0; n < issued; ++n)
       mbar_wait(bar_full + 8 * (n % S), (uint32_t)((n / S) & 1), kDrainLimitNs);
+    for (int n = segments > 2 ? segments - 2 : 0; n < segments; ++n)
+      mbar_wait(bar_qfull + 8 * (n & 1), (uint32_t)((n >> 1) & 1), kDrainLimitNs);
   }
 }
 
@@ -806,8 +862,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   const int grp = tid / kLanes, ln = tid % kLanes;
   pdl_wait();
   const int units = p.c.heads * p.chunks;
-  // a run without tiles has written no start: the one before the first of
-  // those ends with the last tile, which run 0 knows
+  // run 0 has said how many tiles there are; a run without tiles says nothing
   const Runs runs = cut_runs(p.starts[0].w, n_runs);
   const int32_t cut = run_start(runs, c);
   if (runs.total == 0 || cut >= runs.total) return;
@@ -911,7 +966,7 @@ cudaError_t launch_walk(const PagedParams& p, const CUtensorMap& kmap, const CUt
   int64_t n_runs = std::min(n_sms * W::kCtas, kPagedMaxCtas) / units;
   n_runs = std::max<int64_t>(1, std::min(n_runs, tiles));
   paged_walk_kernel<T, kFp8, D, WM>
-      <<<(unsigned)(n_runs * units), kWalkThreads, W::kSmem, st>>>(p, kmap, vmap);
+      <<<(unsigned)(n_runs * units), W::kThreads, W::kSmem, st>>>(p, kmap, vmap);
   e = cudaGetLastError();
   if (e != cudaSuccess || n_runs == 1) return e;           // one run cuts nothing
   return launch_after(paged_join_kernel<T, D>,
