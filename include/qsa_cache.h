@@ -113,14 +113,14 @@ QSA_API qsa_status qsa_paged_append(
     uint32_t* error_word, qsa_stream_t stream);
 
 /*
- * Workspace for qsa_paged_attention: bytes for a batch of num_reqs requests
- * with next_n new tokens each, num_heads query heads over kv_heads K/V heads
- * of head_dim; weight_cols: table_cols * page_size when weight sums are asked
- * for, else 0.  0 for sizes that the call refuses.  Alignment 256 bytes.
+ * Workspace for qsa_paged_attention: bytes for next_n new tokens a request
+ * with num_heads query heads over this cache, with_weights != 0 when weight
+ * sums are asked for.  What the cache's pointers hold does not matter.  0 for a
+ * call that needs none (short tables, no weight sums) and for one that is
+ * refused.  Alignment 256 bytes.
  */
-QSA_API size_t qsa_paged_attention_workspace_bytes(
-    int64_t num_reqs, int64_t next_n, int64_t num_heads, int64_t kv_heads, int64_t head_dim,
-    int64_t weight_cols);
+QSA_API size_t qsa_paged_attention_workspace_bytes(const qsa_paged_cache* cache, int64_t next_n,
+                                                   int64_t num_heads, int with_weights);
 
 /*
  * qsa_paged_attention -- dense attention of next_n new tokens per request.
@@ -160,7 +160,7 @@ QSA_API size_t qsa_paged_attention_workspace_bytes(
  *                 place), or must not overlap.  entry_cols >= table_cols *
  *                 page_size
  *   workspace     >= qsa_paged_attention_workspace_bytes(...) bytes, 256-byte
- *                 aligned
+ *                 aligned; may be NULL where that is 0
  */
 QSA_API qsa_status qsa_paged_attention(
     const qsa_paged_cache* cache,

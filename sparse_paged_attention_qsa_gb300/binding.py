@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
 import os
 import struct
 import threading
@@ -188,7 +187,7 @@ def declare_signatures(lib):
     lib.qsa_paged_append.argtypes = [
         vp, vp, vp, ctypes.c_int, i64, vp, vp, vp, vp, vp, vp, i64, vp, i64, i64, vp, vp]
     lib.qsa_paged_attention_workspace_bytes.restype = sz
-    lib.qsa_paged_attention_workspace_bytes.argtypes = [i64] * 6
+    lib.qsa_paged_attention_workspace_bytes.argtypes = [vp, i64, i64, ctypes.c_int]
     lib.qsa_paged_attention.restype = ctypes.c_int
     lib.qsa_paged_attention.argtypes = [
         vp, vp, ctypes.c_int, i64, i64, vp, vp, ctypes.c_float, i64,
@@ -680,12 +679,12 @@ def qsa_paged_append(k, v, k_cache, v_cache, block_tables, token_to_request, ent
     return k_cache, v_cache
 
 
-@functools.lru_cache(maxsize=256)      # a function of its arguments alone
-def qsa_paged_attention_workspace_bytes(num_reqs: int, next_n: int, num_heads: int,
-                                        kv_heads: int, head_dim: int,
-                                        weight_cols: int = 0) -> int:
+def qsa_paged_attention_workspace_bytes(k_cache, v_cache, block_tables, *, next_n: int = 1,
+                                        num_heads: int, with_weights: bool = False) -> int:
+    """Bytes of workspace that qsa_paged_attention needs for this cache."""
     return int(load_library().qsa_paged_attention_workspace_bytes(
-        num_reqs, next_n, num_heads, kv_heads, head_dim, weight_cols))
+        _cache_struct(k_cache, v_cache, block_tables, None, None), next_n, num_heads,
+        bool(with_weights)))
 
 
 def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next_n: int = 1,
@@ -705,21 +704,20 @@ def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next
         raise QSAError(3, "q must be [requests * next_n, heads, dim]")
     cache = _cache_struct(k_cache, v_cache, block_tables, k_scale, v_scale)
     rows, heads, dim = q.shape
-    reqs, cols = block_tables.shape
-    page_size, kv_heads = k_cache.shape[1], k_cache.shape[2]
+    reqs = block_tables.shape[0]
     if rows != reqs * next_n or dim != k_cache.shape[3]:
         raise QSAError(3, "q must be [requests * next_n, heads, dim] of the cache's dim")
     device = q.get_device()
     raw = _launch_stream(stream, device)
     weights = weight_sums is not None or weight_sums_out is not None
-    if out is None or workspace is None:
+    need = lib.qsa_paged_attention_workspace_bytes(cache, next_n, heads, weights) \
+        if workspace is None else 0
+    if out is None or need:
         with _on_stream(stream, device):
             if out is None:
                 out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
-            if workspace is None:
-                workspace = _workspace(qsa_paged_attention_workspace_bytes(
-                    reqs, next_n, heads, kv_heads, dim, cols * page_size if weights else 0),
-                    q.device)
+            if need:
+                workspace = _workspace(need, q.device)
     if out.dtype != q.dtype:
         raise QSAError(2, "out must have q's dtype")
     if out.shape != q.shape:
@@ -733,8 +731,10 @@ def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next
         _flat(context_lens, torch.int32, reqs, "context_lens"),
         dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
         _STRIDES3.pack(*out.stride()), _flat(lse, torch.float32, rows * heads, "lse"),
-        sums, sums_s0, souts, souts_s0, entry_cols, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _word(error_word), raw))
+        sums, sums_s0, souts, souts_s0, entry_cols,
+        0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _word(error_word), raw))
     return out
 
 

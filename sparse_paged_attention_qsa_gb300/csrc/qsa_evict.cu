@@ -13,7 +13,9 @@
 //              no order, and only what has to move moves.  kept[] is the list
 //              of moves, so there is no workspace.
 // move_kernel  a warp looks 32 places of kept[] over and copies the K and V of
-//              those that move, every lane's pieces in flight at once.
+//              those that move, every lane's pieces in flight at once.  Where a
+//              request can move but little (a decode step's eviction), the rank
+//              kernel's own warps do it, in one launch.
 #include "qsa_cache.h"
 #include "qsa_cache_host.h"
 #include "qsa_device.cuh"
@@ -49,6 +51,8 @@ struct EvictParams {
   const int32_t* ctx;
   int32_t cap;                // entries a request can have here
   int32_t budget, sink, recent;
+  int32_t head_log2;          // log2 of the 16-byte pieces of an entry's head
+  int32_t move_here;          // the rank kernel moves K and V itself
   int32_t* kept;              // [reqs, budget]
   int32_t* new_lens;
   float* sums_out;
@@ -62,6 +66,41 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
   const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+constexpr int kMovePieces = 8;            // 16-byte pieces of a lane in flight
+
+// A warp copies one entry's K and V, its lanes sharing the 16-byte pieces.
+__device__ __forceinline__ void move_entry(const CacheView& c, int head_log2, int64_t page_from,
+                                           int from, int64_t page_to, int to) {
+  const int lane = threadIdx.x & 31;
+  const int row = c.heads << head_log2;                    // pieces of an entry's K
+  const int slot_mask = (1 << c.page_log2) - 1;
+  const int64_t sf = from & slot_mask, st = to & slot_mask;
+  const unsigned char* kf = c.k + page_from * c.k_page + sf * c.k_token;
+  const unsigned char* vf = c.v + page_from * c.v_page + sf * c.v_token;
+  const int64_t k_to = (page_to - page_from) * c.k_page + (st - sf) * c.k_token;
+  const int64_t v_to = (page_to - page_from) * c.v_page + (st - sf) * c.v_token;
+  const auto source = [&](int i) {
+    const bool is_v = i >= row;
+    const int u = is_v ? i - row : i, h = u >> head_log2, o = u & ((1 << head_log2) - 1);
+    return (is_v ? vf + h * c.v_head : kf + h * c.k_head) + o * 16;
+  };
+  for (int i0 = 0; i0 < 2 * row; i0 += 32 * kMovePieces) {
+    uint4 x[kMovePieces];
+#pragma unroll
+    for (int j = 0; j < kMovePieces; ++j) {
+      const int i = i0 + j * 32 + lane;
+      if (i < 2 * row) x[j] = *reinterpret_cast<const uint4*>(source(i));
+    }
+#pragma unroll
+    for (int j = 0; j < kMovePieces; ++j) {
+      const int i = i0 + j * 32 + lane;
+      if (i < 2 * row)
+        *reinterpret_cast<uint4*>(const_cast<unsigned char*>(source(i)) + (i >= row ? v_to : k_to)) =
+            x[j];
+    }
+  }
 }
 
 struct RankShared {
@@ -365,6 +404,19 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
       kept[to] = from;
       sums_out[to] = w[from];
       pos_out[to] = pos[from];
+      s_key[i] = from;                   // for the moves below
+    }
+    if (p.move_here) {
+      __syncthreads();
+      const int32_t* bt = p.c.bt + (int64_t)b * p.c.bt_s0;
+      for (int i = warp; i < holes; i += kRankWarps) {
+        const int from = (int)s_key[i], to = s_pos[i];
+        const int32_t pf = bt[from >> p.c.page_log2], pt = bt[to >> p.c.page_log2];
+        if (pf >= 0 && pf < p.c.num_pages && pt >= 0 && pt < p.c.num_pages)
+          move_entry(p.c, p.head_log2, pf, from, pt, to);
+        else if (lane == 0)
+          report(p.err, QSA_DERR_KV_PAGE);
+      }
     }
     sync_all();                          // no CTA leaves while another reads its shared memory
   } else {
@@ -388,16 +440,12 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
   }
 }
 
-constexpr int kMovePieces = 8;            // 16-byte pieces of a lane in flight
-
 // A warp of request b looks over 32 places of kept[] at a time; its lanes share
 // the 16-byte pieces of a moving entry's K and V.
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p, int head_log2) {
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int row = p.c.heads << head_log2;                  // pieces of an entry's K
   const int32_t* kept = p.kept + (int64_t)b * p.budget;
   const int32_t* bt = p.c.bt + (int64_t)b * p.c.bt_s0;
-  const int slot_mask = (1 << p.c.page_log2) - 1;
   pdl_wait();
   const int warp = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
   const int stride = gridDim.x * (kMoveThreads / 32);
@@ -418,33 +466,9 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
     for (uint32_t todo = __ballot_sync(0xffffffffu, fine); todo; todo &= todo - 1) {
       const int who = __ffs(todo) - 1;
       const int from = __shfl_sync(0xffffffffu, src, who), to = __shfl_sync(0xffffffffu, mine, who);
-      const int64_t pf = __shfl_sync(0xffffffffu, page_f, who);
-      const int64_t pt = __shfl_sync(0xffffffffu, page_t, who);
-      const int64_t sf = from & slot_mask, st = to & slot_mask;
-      const unsigned char* kf = p.c.k + pf * p.c.k_page + sf * p.c.k_token;
-      const unsigned char* vf = p.c.v + pf * p.c.v_page + sf * p.c.v_token;
-      const int64_t k_to = pt * p.c.k_page + st * p.c.k_token - (pf * p.c.k_page + sf * p.c.k_token);
-      const int64_t v_to = pt * p.c.v_page + st * p.c.v_token - (pf * p.c.v_page + sf * p.c.v_token);
-      const auto source = [&](int i) {
-        const bool is_v = i >= row;
-        const int u = is_v ? i - row : i, h = u >> head_log2, o = u & ((1 << head_log2) - 1);
-        return (is_v ? vf + h * p.c.v_head : kf + h * p.c.k_head) + o * 16;
-      };
-      for (int i0 = 0; i0 < 2 * row; i0 += 32 * kMovePieces) {
-        uint4 x[kMovePieces];
-#pragma unroll
-        for (int j = 0; j < kMovePieces; ++j) {
-          const int i = i0 + j * 32 + lane;
-          if (i < 2 * row) x[j] = *reinterpret_cast<const uint4*>(source(i));
-        }
-#pragma unroll
-        for (int j = 0; j < kMovePieces; ++j) {
-          const int i = i0 + j * 32 + lane;
-          if (i < 2 * row)
-            *reinterpret_cast<uint4*>(const_cast<unsigned char*>(source(i)) +
-                                      (i >= row ? v_to : k_to)) = x[j];
-        }
-      }
+      const int pf = __shfl_sync(0xffffffffu, page_f, who);
+      const int pt = __shfl_sync(0xffffffffu, page_t, who);
+      move_entry(p.c, p.head_log2, pf, from, pt, to);
     }
   }
 }
@@ -480,13 +504,22 @@ cudaError_t evict_device(int* n_sms) {
 // 32768 do not fit in shared memory; 64 of 2064: 8.8 us with 1, 10.5 with 2).
 constexpr int64_t kMinSlice = 4096;
 
-cudaError_t launch_rank(const EvictParams& p, int reqs, int sms, cudaStream_t st) {
+// Bytes that the rank kernel's CTA moves itself: about what it does in the time
+// of a second launch.
+constexpr int64_t kMoveHereBytes = 512 << 10;
+
+// `most` entries can move in a request; *moved says whether they have been.
+cudaError_t launch_rank(EvictParams& p, int reqs, int64_t most, int sms, cudaStream_t st,
+                        bool* moved) {
   int ranks = 1;
   while (ranks < kMaxCluster && (int64_t)reqs * ranks * 2 <= sms &&
          (int64_t)p.cap >= kMinSlice * ranks * 2)
     ranks *= 2;
   const int64_t slice = ((int64_t)p.cap + ranks - 1) / ranks;
   const bool cached = slice <= kMaxSlice;
+  const int64_t entry_bytes = (int64_t)2 * p.c.heads * (16 << p.head_log2);
+  p.move_here = cached && most * entry_bytes <= kMoveHereBytes;
+  *moved = p.move_here;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(reqs * ranks));
   cfg.blockDim = dim3(kRankThreads);
@@ -570,17 +603,16 @@ extern "C" qsa_status qsa_evict_entries(
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int sms = 0;
   if (evict_device(&sms) != cudaSuccess) return QSA_ERR_CUDA;
-  if (launch_rank(p, (int)R, sms, s) != cudaSuccess) return QSA_ERR_CUDA;
+  while (((int64_t)16 << p.head_log2) < cache->head_dim * dtype_size(cache->dtype)) ++p.head_log2;
   const int64_t most = std::min<int64_t>(budget, std::max<int64_t>(0, p.cap - budget));
-  if (most == 0) return QSA_OK;          // no request can have an entry too many
+  bool moved = false;
+  if (launch_rank(p, (int)R, most, sms, s, &moved) != cudaSuccess) return QSA_ERR_CUDA;
+  if (moved || most == 0) return QSA_OK;   // 0: no request can have an entry too many
   const int64_t warps = kMoveThreads / 32;
   const int64_t wave = std::max<int64_t>(1, (int64_t)sms * (2048 / kMoveThreads) / R);
   // every place is looked at; a warp's share is at least one, at most 32
   const int64_t ctas = std::max((most + warps - 1) / warps, (budget + 32 * warps - 1) / (32 * warps));
   const dim3 grid((unsigned)std::min(ctas, wave), (unsigned)R);
-  int head_log2 = 0;
-  while (((int64_t)16 << head_log2) < cache->head_dim * dtype_size(cache->dtype)) ++head_log2;
-  return launch_after(move_kernel, grid, dim3(kMoveThreads), 0, s, p, head_log2) == cudaSuccess
-             ? QSA_OK
-             : QSA_ERR_CUDA;
+  return launch_after(move_kernel, grid, dim3(kMoveThreads), 0, s, p) == cudaSuccess ? QSA_OK
+                                                                                     : QSA_ERR_CUDA;
 }

@@ -128,42 +128,49 @@ bool encode_view(CUtensorMap* map, const unsigned char* p, const CacheView& c, i
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-bool sizes_ok(int64_t reqs, int64_t next_n, int64_t heads, int64_t kv_heads, int64_t dim) {
-  return reqs >= 0 && reqs <= QSA_CACHE_MAX_REQS && next_n >= 1 && next_n <= QSA_CACHE_MAX_NEXT &&
-         kv_heads >= 1 && kv_heads <= QSA_CACHE_MAX_HEADS && heads >= 1 && heads % kv_heads == 0 &&
-         heads * next_n <= 65536 && (dim == 64 || dim == 128 || dim == 256);
+bool sizes_ok(const qsa_paged_cache& c, int64_t next_n, int64_t heads) {
+  return next_n >= 1 && next_n <= QSA_CACHE_MAX_NEXT && heads >= 1 && heads % c.num_heads == 0 &&
+         heads * next_n <= 65536;
 }
 
 // The workspace: where each run starts, the pieces of K/V heads that the
-// runs cut (at most two a run), then, when weights are asked
-// for, the rows' sums and logits.
+// runs cut (at most two a run), neither where requests are walked whole;
+// then, when weights are asked for, the rows' sums and logits.
 struct Layout {
+  bool whole;
   size_t ml, o, lse2, z, total;
 };
 
-Layout layout_of(int64_t reqs, int64_t next_n, int64_t heads, int64_t kv_heads, int64_t dim,
-                 int64_t weight_cols) {
-  const size_t rows = (size_t)std::min<int64_t>(next_n * (heads / kv_heads), kPagedMaxRows);
-  const size_t all = (size_t)(reqs * next_n * heads);
+// 0 as the total where it cannot be addressed.
+Layout layout_of(const qsa_paged_cache& c, const CacheView& v, int64_t next_n, int64_t heads,
+                 bool weights) {
+  const size_t rows = (size_t)std::min<int64_t>(next_n * (heads / c.num_heads), kPagedMaxRows);
+  const int64_t all = c.num_reqs * next_n * heads, entries = weights ? v.cap : 0;
   Layout l;
-  l.ml = round256(kPagedMaxCtas * sizeof(int4));
-  l.o = l.ml + round256(2 * kPagedMaxCtas * rows * 2 * sizeof(float));
-  l.lse2 = l.o + round256(2 * kPagedMaxCtas * rows * (size_t)dim * sizeof(float));
-  l.z = l.lse2 + (weight_cols > 0 ? round256(all * sizeof(float)) : 0);
-  l.total = l.z + all * (size_t)weight_cols * sizeof(float);
+  l.whole = (int64_t)v.cap * 2 * c.head_dim * cache_host::dtype_size(c.dtype) <= kPagedWholeBytes;
+  l.ml = l.whole ? 0 : round256(kPagedMaxCtas * sizeof(int4));
+  l.o = l.ml + (l.whole ? 0 : round256(2 * kPagedMaxCtas * rows * 2 * sizeof(float)));
+  l.lse2 = l.o + (l.whole ? 0 : round256(2 * kPagedMaxCtas * rows * (size_t)c.head_dim * sizeof(float)));
+  l.z = l.lse2 + (entries > 0 ? round256((size_t)all * sizeof(float)) : 0);
+  const __int128 total = (__int128)l.z + (__int128)all * entries * 4;
+  l.total = total < ((__int128)1 << 60) ? (size_t)total : 0;
+  if (l.total == 0) l.total = total == 0 ? 0 : SIZE_MAX;
   return l;
 }
 
 }  // namespace
 }  // namespace qsa
 
-extern "C" size_t qsa_paged_attention_workspace_bytes(
-    int64_t num_reqs, int64_t next_n, int64_t num_heads, int64_t kv_heads, int64_t head_dim,
-    int64_t weight_cols) {
-  if (!qsa::sizes_ok(num_reqs, next_n, num_heads, kv_heads, head_dim) || num_reqs == 0 ||
-      weight_cols < 0 || weight_cols > INT32_MAX)
+extern "C" size_t qsa_paged_attention_workspace_bytes(const qsa_paged_cache* cache, int64_t next_n,
+                                                      int64_t num_heads, int with_weights) {
+  using namespace qsa;
+  CacheView view{};
+  cache_host::CacheSpans spans{};
+  if (cache_host::check_cache(cache, &view, &spans) != QSA_OK || cache->num_reqs == 0 ||
+      !sizes_ok(*cache, next_n, num_heads))
     return 0;
-  return qsa::layout_of(num_reqs, next_n, num_heads, kv_heads, head_dim, weight_cols).total;
+  const size_t n = layout_of(*cache, view, next_n, num_heads, with_weights != 0).total;
+  return n == SIZE_MAX ? 0 : n;
 }
 
 extern "C" qsa_status qsa_paged_attention(
@@ -183,7 +190,7 @@ extern "C" qsa_status qsa_paged_attention(
   if (cache->dtype != QSA_DT_F8E4M3 && cache->dtype != dtype) return QSA_ERR_DTYPE;
   if (!(std::isfinite(scale) && scale > 0.f) || window < 0) return QSA_ERR_CONTRACT;
   const int64_t R = cache->num_reqs;
-  if (!sizes_ok(R, next_n, num_heads, cache->num_heads, cache->head_dim)) return QSA_ERR_SHAPE;
+  if (!sizes_ok(*cache, next_n, num_heads)) return QSA_ERR_SHAPE;
   if (!q_strides || !out_strides) return QSA_ERR_NULL;
   const int64_t shape[3] = {R * next_n, num_heads, cache->head_dim};
   if (!strides_ok(shape, q_strides, 3, 2) || !strides_ok(shape, out_strides, 3, 2))
@@ -204,9 +211,9 @@ extern "C" qsa_status qsa_paged_attention(
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(context_lens, 4) || !aligned(lse, 4) ||
       !aligned(weight_sums, 4) || !aligned(weight_sums_out, 4) || !aligned(error_word, 4))
     return QSA_ERR_ALIGN;
-  const size_t need = qsa_paged_attention_workspace_bytes(R, next_n, num_heads, cache->num_heads,
-                                                          cache->head_dim, weights ? entries : 0);
-  if (need == 0) return QSA_ERR_SHAPE;
+  const Layout l = layout_of(*cache, p.c, next_n, num_heads, weights);
+  const size_t need = l.total;
+  if (need == SIZE_MAX) return QSA_ERR_SHAPE;
   const Span ws = span(workspace, (int64_t)need);
   const Span sums_in = weights ? rows_span(weight_sums, R, entry_cols, weight_sums_stride0) : Span{};
   const Span outs[5] = {span(out, ox), span(lse, R * next_n * num_heads * 4),
@@ -220,7 +227,7 @@ extern "C" qsa_status qsa_paged_attention(
                         weight_sums_stride0 == weight_sums_out_stride0;
   for (int i = 0; i < 5; ++i)
     if (!(i == 2 && in_place) && overlaps(outs[i], sums_in)) return QSA_ERR_ALIAS;
-  if (!workspace || workspace_bytes < need) return QSA_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QSA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QSA_ERR_ALIGN;
   p.q = static_cast<const unsigned char*>(q);
   p.q_row = R * next_n > 1 ? q_strides[0] * 2 : 0;
@@ -238,9 +245,8 @@ extern "C" qsa_status qsa_paged_attention(
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.window = window;
   p.lse = lse;
-  const Layout l = layout_of(R, next_n, num_heads, cache->num_heads, cache->head_dim,
-                             weights ? entries : 0);
   unsigned char* w = static_cast<unsigned char*>(workspace);
+  p.whole = l.whole;
   p.starts = reinterpret_cast<int4*>(w);
   p.part_ml = reinterpret_cast<float*>(w + l.ml);
   p.part_o = reinterpret_cast<float*>(w + l.o);

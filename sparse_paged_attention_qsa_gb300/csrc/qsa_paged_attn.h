@@ -27,6 +27,7 @@ struct PagedParams {
   int32_t rows;               // query rows of a K/V head: next_n * group
   int32_t chunks;             // of at most kPagedMaxRows of them
   int32_t chunk_rows;         // rows of a full chunk
+  int32_t whole;              // runs end where a request does: nothing is left to join
   float scale_log2;           // scale * log2(e)
   int64_t window;
   float* lse;                 // nullable
@@ -68,5 +69,9 @@ constexpr int paged_tile(int dim, int row_bytes, int wm) {
   const int most = 64 * (paged_warps(dim, wm) / wm), t = slot / row_bytes;
   return t < most ? t : most;
 }
+
+// A request whose K and V of one head take no more than this is not cut: a CTA
+// streams it in about the time that a join takes.
+constexpr int64_t kPagedWholeBytes = 256 << 10;
 
 }  // namespace qsa

@@ -280,10 +280,19 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   const int units = p.c.heads * p.chunks, run = blockIdx.x / units, unit = blockIdx.x % units;
   const int head = unit / p.chunks, chunk = unit - head * p.chunks;
   const Runs runs = cut_runs(pre[p.batch], gridDim.x / units);
-  const int32_t w_begin = run_start(runs, run), w_end = run_start(runs, run + 1);
+  int32_t w_begin = run_start(runs, run), w_end = run_start(runs, run + 1);
+  if (p.whole) {                         // on to the next request's first tile
+    const auto snap = [&](int32_t w) {
+      if (w >= runs.total) return runs.total;
+      const TileAt at = tile_at(pre, p.batch, w);
+      return at.tile > 0 ? w - at.tile + at.count : w;
+    };
+    w_begin = snap(w_begin);
+    w_end = snap(w_end);
+  }
   pdl_trigger();     // every CTA is resident: the join may be put in place (it waits)
   // where the run starts, for the join; run 0 always says how many tiles there are
-  if (unit == 0 && tid == 0 && (run == 0 || w_begin < w_end)) {
+  if (!p.whole && unit == 0 && tid == 0 && (run == 0 || w_begin < w_end)) {
     TileAt at = {0, 0, 0};
     if (w_begin < w_end) at = tile_at(pre, p.batch, w_begin);
     p.starts[run] = make_int4(at.b, at.tile, at.count, runs.total);
@@ -962,13 +971,14 @@ cudaError_t launch_walk(const PagedParams& p, const CUtensorMap& kmap, const CUt
   }
   // runs: as many as fill one wave, no more than there can be tiles
   const int units = p.c.heads * p.chunks;
-  const int64_t tiles = (int64_t)p.batch * (((int64_t)p.c.cap + W::TT - 1) / W::TT);
+  const int64_t tiles =
+      (int64_t)p.batch * (p.whole ? 1 : ((int64_t)p.c.cap + W::TT - 1) / W::TT);
   int64_t n_runs = std::min(n_sms * W::kCtas, kPagedMaxCtas) / units;
   n_runs = std::max<int64_t>(1, std::min(n_runs, tiles));
   paged_walk_kernel<T, kFp8, D, WM>
       <<<(unsigned)(n_runs * units), W::kThreads, W::kSmem, st>>>(p, kmap, vmap);
   e = cudaGetLastError();
-  if (e != cudaSuccess || n_runs == 1) return e;           // one run cuts nothing
+  if (e != cudaSuccess || n_runs == 1 || p.whole) return e;   // nothing has been cut
   return launch_after(paged_join_kernel<T, D>,
                       dim3((unsigned)n_runs - 1, (unsigned)p.chunk_rows, (unsigned)units),
                       dim3(kJoinThreads), 0, st, p, (int)n_runs);

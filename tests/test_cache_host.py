@@ -69,18 +69,15 @@ def _append(lib, **over):
 
 
 def _attend(lib, **over):
-    dims = {f: over[f] for f in ("reqs", "cols", "size", "heads", "dim") if f in over}
     cache = _cache(over)
-    n = over.get("n", 1)
-    a = dict(cache=cache, q=_addr(10), dt=1, n=n, hq=4, qs=_arr(256, 64, 1), ctx=_addr(11),
+    a = dict(cache=cache, q=_addr(10), dt=1, n=1, hq=4, qs=_arr(256, 64, 1), ctx=_addr(11),
              scale=0.125, window=0, out=_addr(12), os=_arr(256, 64, 1), lse=_addr(13),
              win=_addr(14), ws0=128, wout=_addr(15), wos0=128, ecols=128, work=_addr(16), bytes=None,
              err=_addr(17), stream=None)
     a.update(over)
     if a["bytes"] is None:
-        a["bytes"] = lib.qsa_paged_attention_workspace_bytes(
-            dims.get("reqs", 4), n, a["hq"], dims.get("heads", 2), dims.get("dim", 64),
-            dims.get("cols", 8) * dims.get("size", 16) if a["win"] else 0)
+        a["bytes"] = lib.qsa_paged_attention_workspace_bytes(cache, a["n"], a["hq"],
+                                                             a["win"] is not None)
     return lib.qsa_paged_attention(*a.values())
 
 
@@ -156,6 +153,7 @@ def test_append_without_tokens_is_a_noop(lib):
     (dict(q=_addr(10) + 8), ALIGN), (dict(out=_addr(12) + 8), ALIGN), (dict(ctx=_addr(11) + 2), ALIGN),
     (dict(lse=_addr(13) + 1), ALIGN), (dict(work=_addr(16) + 16), ALIGN), (dict(err=_addr(17) + 1), ALIGN),
     (dict(work=None), WORKSPACE), (dict(bytes=100), WORKSPACE),
+    (dict(cols=4096, bts0=4096, win=None, wout=None, work=None), WORKSPACE),
     (dict(out=_addr(10)), ALIAS), (dict(out=_addr(1) + 4096), ALIAS), (dict(lse=_addr(12)), ALIAS),
     (dict(work=_addr(2)), ALIAS), (dict(wout=_addr(11)), ALIAS), (dict(err=_addr(12) + 4), ALIAS),
     (dict(wout=_addr(14) + 16), ALIAS), (dict(wout=_addr(14), wos0=129), ALIAS),
@@ -190,12 +188,23 @@ def test_evict_without_requests_is_a_noop(lib):
 
 
 def test_workspace_queries(lib):
-    w = qsa.qsa_paged_attention_workspace_bytes
-    assert w(4, 1, 8, 2, 128) > 0
-    assert w(4, 1, 8, 2, 128, 4096) >= w(4, 1, 8, 2, 128) + 4 * 8 * 4096 * 4
-    for bad in ((0, 1, 8, 2, 128), (4, 0, 8, 2, 128), (4, 9, 8, 2, 128), (4, 1, 9, 2, 128),
-                (4, 1, 8, 0, 128), (4, 1, 8, 2, 100), (65536, 1, 8, 2, 128), (4, 1, 8, 2, 128, -1)):
-        assert w(*bad) == 0
+    w = lib.qsa_paged_attention_workspace_bytes
+    short, long = _cache({}), _cache(dict(cols=4096, bts0=4096))
+    assert w(short, 1, 8, 0) == 0                     # 128 entries: nothing is cut
+    assert w(short, 1, 8, 1) >= 4 * 8 * (128 + 1) * 4
+    assert w(long, 1, 8, 0) > 0
+    assert w(long, 1, 8, 1) >= w(long, 1, 8, 0) + 4 * 8 * 65536 * 4
+    for n, hq in ((0, 8), (9, 8), (1, 7), (1, 0), (2, 65536)):
+        assert w(long, n, hq, 0) == 0
+    assert w(None, 1, 8, 0) == 0 and w(_cache(dict(reqs=0, cols=4096, bts0=4096)), 1, 8, 1) == 0
+    # logits past any address space: refused
+    huge = dict(reqs=65535, cols=1 << 26, bts0=1 << 26)
+    assert w(_cache(dict(huge)), 8, 8192, 1) == 0
+
+
+def test_short_tables_need_no_workspace(lib):
+    # refused for another reason, or launched (which fails here): never for the workspace
+    assert _attend(lib, win=None, wout=None, work=None, bytes=0, q=None) == NULL
 
 
 def test_binding_refuses_host_tensors():

@@ -161,6 +161,16 @@ def test_attention_head_groups(hq, hk, next_n, d):
     check(Case([150, 1], hq, hk, d, 64, BF16, E4M3, next_n=next_n, seed=hq + 1))
 
 
+@pytest.mark.parametrize("hq,hk,next_n", [(3, 1, 1), (17, 1, 1), (12, 4, 3), (16, 1, 8), (64, 1, 1),
+                                          (20, 1, 4)])
+@pytest.mark.parametrize("d,dtype,cache", [(64, F16, F16), (128, BF16, E4M3), (256, BF16, BF16)])
+def test_attention_cut_requests(hq, hk, next_n, d, dtype, cache):
+    # long enough that every request is cut between CTAs, in few and in many pieces
+    check(Case([2600], hq, hk, d, 32, dtype, cache, next_n=next_n, seed=hq), sums=True)
+    check(Case([2049, 3, 1500, 0, 2600], hq, hk, d, 64, dtype, cache, next_n=next_n, seed=hq + 1),
+          sums=True)
+
+
 def test_attention_worked_size_of_the_packed_cache():
     check(Case([519], 3, 1, 256, 512, F16, layout="packed", seed=3))
 
@@ -334,7 +344,8 @@ def test_attention_other_streams_threads_and_graphs():
         t.join()
     assert found == [True] * 3
     # two graphs that share one workspace, replayed in turn on new inputs
-    need = qsa.qsa_paged_attention_workspace_bytes(4, 1, 8, 2, 128, sums.shape[1])
+    need = qsa.qsa_paged_attention_workspace_bytes(c.k, c.v, c.tables, num_heads=8,
+                                                   with_weights=True)
     ws = torch.empty(need, dtype=torch.uint8, device=DEV)
     outs, lses, sums_out = [], [], torch.zeros_like(sums)
     graphs = []
