@@ -134,10 +134,10 @@ bool sizes_ok(const qsa_paged_cache& c, int64_t next_n, int64_t heads) {
 }
 
 // The workspace: where each run starts, the pieces of K/V heads that the
-// runs cut (at most two a run), neither where requests are walked whole;
+// runs cut (at most two a run), neither in the modes without a second kernel;
 // then, when weights are asked for, the rows' sums and logits.
 struct Layout {
-  bool whole;
+  PagedMode mode;
   size_t ml, o, lse2, z, total;
 };
 
@@ -147,10 +147,14 @@ Layout layout_of(const qsa_paged_cache& c, const CacheView& v, int64_t next_n, i
   const size_t rows = (size_t)std::min<int64_t>(next_n * (heads / c.num_heads), kPagedMaxRows);
   const int64_t all = c.num_reqs * next_n * heads, entries = weights ? v.cap : 0;
   Layout l;
-  l.whole = (int64_t)v.cap * 2 * c.head_dim * cache_host::dtype_size(c.dtype) <= kPagedWholeBytes;
-  l.ml = l.whole ? 0 : round256(kPagedMaxCtas * sizeof(int4));
-  l.o = l.ml + (l.whole ? 0 : round256(2 * kPagedMaxCtas * rows * 2 * sizeof(float)));
-  l.lse2 = l.o + (l.whole ? 0 : round256(2 * kPagedMaxCtas * rows * (size_t)c.head_dim * sizeof(float)));
+  const int64_t request = (int64_t)v.cap * 2 * c.head_dim * cache_host::dtype_size(c.dtype);
+  l.mode = request <= kPagedWholeBytes ? kPagedWhole
+           : rows <= 16 && c.num_reqs * request <= kPagedCluster8 * kPagedWholeBytes ? kPagedCluster
+                                                                                     : kPagedCut;
+  const bool pieces = l.mode == kPagedCut;
+  l.ml = pieces ? round256(kPagedMaxCtas * sizeof(int4)) : 0;
+  l.o = l.ml + (pieces ? round256(2 * kPagedMaxCtas * rows * 2 * sizeof(float)) : 0);
+  l.lse2 = l.o + (pieces ? round256(2 * kPagedMaxCtas * rows * (size_t)c.head_dim * sizeof(float)) : 0);
   l.z = l.lse2 + (entries > 0 ? round256((size_t)all * sizeof(float)) : 0);
   const __int128 total = (__int128)l.z + (__int128)all * entries * 4;
   l.total = total < ((__int128)1 << 60) ? (size_t)total : 0;
@@ -246,7 +250,7 @@ extern "C" qsa_status qsa_paged_attention(
   p.window = window;
   p.lse = lse;
   unsigned char* w = static_cast<unsigned char*>(workspace);
-  p.whole = l.whole;
+  p.mode = l.mode;
   p.starts = reinterpret_cast<int4*>(w);
   p.part_ml = reinterpret_cast<float*>(w + l.ml);
   p.part_o = reinterpret_cast<float*>(w + l.o);

@@ -15,6 +15,19 @@ constexpr int kPagedBatch = 512;    // requests per launch (their tables in shar
 constexpr int kPagedMaxCtas = 512;  // CTAs of the tile walk (what the workspace is sized for)
 constexpr int kPagedMaxRows = 64;   // query rows of one K/V head that share a walk
 
+// How the requests' tiles are dealt out.
+enum PagedMode : int32_t {
+  kPagedCut,       // equal runs over the GPU; a second kernel joins the requests they cut
+  kPagedWhole,     // runs that end where a request does: nothing to join
+  kPagedCluster,   // up to 8 equal runs a K/V head, one cluster, joined through its shared memory
+};
+// A request whose K and V of one head take no more than this is not cut: a CTA
+// streams it in about the time that a second launch takes.  And where a K/V
+// head's requests take no more than that for each CTA of a cluster, up to 16
+// query rows are walked by one.
+constexpr int64_t kPagedWholeBytes = 256 << 10;
+constexpr int kPagedCluster8 = 8;
+
 struct PagedParams {
   CacheView c;
   const unsigned char* q;
@@ -27,7 +40,7 @@ struct PagedParams {
   int32_t rows;               // query rows of a K/V head: next_n * group
   int32_t chunks;             // of at most kPagedMaxRows of them
   int32_t chunk_rows;         // rows of a full chunk
-  int32_t whole;              // runs end where a request does: nothing is left to join
+  int32_t mode;               // a PagedMode
   float scale_log2;           // scale * log2(e)
   int64_t window;
   float* lse;                 // nullable
@@ -69,9 +82,5 @@ constexpr int paged_tile(int dim, int row_bytes, int wm) {
   const int most = 64 * (paged_warps(dim, wm) / wm), t = slot / row_bytes;
   return t < most ? t : most;
 }
-
-// A request whose K and V of one head take no more than this is not cut: a CTA
-// streams it in about the time that a join takes.
-constexpr int64_t kPagedWholeBytes = 256 << 10;
 
 }  // namespace qsa

@@ -23,6 +23,9 @@
 //   or the run's, the slices merge through shared memory into the output, or
 //   into a piece in the workspace when the K/V head's entries are cut.
 // paged_join_kernel  joins a cut K/V head's pieces.
+// Short work needs no second kernel: its runs end where requests do, or are one
+// cluster a K/V head, whose CTAs keep their pieces in shared memory and join
+// them there (PagedMode).
 //
 // Rounding: q, K and V enter the products as they are (E4M3 as FP16, exactly;
 // BF16 queries of an E4M3 cache as FP16 after a power-of-two scaling of the
@@ -40,6 +43,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -68,7 +72,7 @@ struct WalkTables {
 };
 static_assert(sizeof(WalkTables) % 16 == 0, "a whole number of 16-byte pieces");
 
-template <bool kFp8, int D, int WM>
+template <bool kFp8, int D, int WM, bool kCluster>
 struct WalkShape {
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);        // a token's K (or V) of one head
   static constexpr int NW = paged_warps(D, WM);               // consumer warps
@@ -85,8 +89,11 @@ struct WalkShape {
   static constexpr int kQBytes = 16 * WM * kQPitch * 2;       // a query slot
   static constexpr int kQSlots = kFp8 ? 3 : 2;                // the third: as FP16, reordered
   static constexpr int kMergeBytes = NW == 8 ? 128 * 40 * 4 : 17408;   // at least 32 columns
-  static constexpr int kFixed = 1024 + kQSlots * kQBytes + kMergeBytes + (int)sizeof(WalkTables);
-  static constexpr int kCtas = paged_ctas(D, WM);
+  // of the first and the last segment: 16 rows and their maximum and sum
+  static constexpr int kPieceBytes = kCluster ? 2 * 16 * (D + 4) * 4 : 0;
+  static constexpr int kFixed =
+      1024 + kQSlots * kQBytes + kMergeBytes + kPieceBytes + (int)sizeof(WalkTables);
+  static constexpr int kCtas = kCluster ? 1 : paged_ctas(D, WM);
   static constexpr int kFit = (kSmemPerSm / kCtas - kSmemReserved - kFixed) / kSlot;
   static constexpr int S = kFit < kMaxSlots ? kFit : kMaxSlots;
   static constexpr size_t kSmem = (size_t)kFixed + (size_t)S * kSlot;
@@ -212,11 +219,12 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* pre, int batch, int32_t
   return TileAt{lo, w - pre[lo], pre[lo + 1] - pre[lo]};
 }
 
-template <typename T, bool kFp8, int D, int WM>
-__global__ void __launch_bounds__((WalkShape<kFp8, D, WM>::kThreads), (WalkShape<kFp8, D, WM>::kCtas))
+template <typename T, bool kFp8, int D, int WM, bool kCluster>
+__global__ void __launch_bounds__((WalkShape<kFp8, D, WM, kCluster>::kThreads),
+                                  (WalkShape<kFp8, D, WM, kCluster>::kCtas))
 paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
-  using W = WalkShape<kFp8, D, WM>;
+  using W = WalkShape<kFp8, D, WM, kCluster>;
   constexpr bool kBf16 = sizeof(T) == 2 && !kFp8 && __is_same(T, __nv_bfloat16);   // product type
   constexpr int TT = W::TT, WK = W::WK, NS = W::NS, S = W::S;
   extern __shared__ unsigned char smem_raw[];
@@ -228,8 +236,10 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   const uint32_t queries = ring + S * W::kSlot;            // query slots, then the merge buffer
   constexpr int kBehind = S * W::kSlot + W::kQSlots * W::kQBytes;
   float* merge = reinterpret_cast<float*>(base + kBehind);
-  WalkTables& tb = *reinterpret_cast<WalkTables*>(base + kBehind + W::kMergeBytes);
-  const uint32_t bar_full = ring + kBehind + W::kMergeBytes, bar_empty = bar_full + 8 * kMaxSlots;
+  constexpr int kTables = kBehind + W::kMergeBytes + W::kPieceBytes;
+  float* pieces = reinterpret_cast<float*>(base + kBehind + W::kMergeBytes);   // [2][16][D + 4]
+  WalkTables& tb = *reinterpret_cast<WalkTables*>(base + kTables);
+  const uint32_t bar_full = ring + kTables, bar_empty = bar_full + 8 * kMaxSlots;
   const uint32_t bar_qfull = bar_empty + 8 * kMaxSlots, bar_qempty = bar_qfull + 16;
   volatile int32_t* s_abort = &tb.abort;
   int32_t* pre = tb.pre;
@@ -276,12 +286,15 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     __syncthreads();
   }
   // CTA: run * units + unit, so that the K/V heads of the same tokens, whose
-  // elements lie side by side, are read at the same time
-  const int units = p.c.heads * p.chunks, run = blockIdx.x / units, unit = blockIdx.x % units;
+  // elements lie side by side, are read at the same time; a cluster's are the
+  // runs of one unit
+  const int units = p.c.heads * p.chunks, n_runs = gridDim.x / units;
+  const int run = kCluster ? blockIdx.x % n_runs : blockIdx.x / units;
+  const int unit = kCluster ? blockIdx.x / n_runs : blockIdx.x % units;
   const int head = unit / p.chunks, chunk = unit - head * p.chunks;
-  const Runs runs = cut_runs(pre[p.batch], gridDim.x / units);
+  const Runs runs = cut_runs(pre[p.batch], n_runs);
   int32_t w_begin = run_start(runs, run), w_end = run_start(runs, run + 1);
-  if (p.whole) {                         // on to the next request's first tile
+  if (!kCluster && p.mode == kPagedWhole) {   // on to the next request's first tile
     const auto snap = [&](int32_t w) {
       if (w >= runs.total) return runs.total;
       const TileAt at = tile_at(pre, p.batch, w);
@@ -292,7 +305,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   }
   pdl_trigger();     // every CTA is resident: the join may be put in place (it waits)
   // where the run starts, for the join; run 0 always says how many tiles there are
-  if (!p.whole && unit == 0 && tid == 0 && (run == 0 || w_begin < w_end)) {
+  if (!kCluster && p.mode == kPagedCut && unit == 0 && tid == 0 && (run == 0 || w_begin < w_end)) {
     TileAt at = {0, 0, 0};
     if (w_begin < w_end) at = tile_at(pre, p.batch, w_begin);
     p.starts[run] = make_int4(at.b, at.tile, at.count, runs.total);
@@ -306,6 +319,8 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
            (int64_t)(head * p.group + r - j * p.group) * hs;
   };
 
+  // the request that starts in this run and is cut: its place, and its pieces
+  int own_b = -1, own_piece = 0, own_runs = 0;
   int issued = 0, segments = 0;                            // producer: slots, queries loaded
   if (warp == W::NW) {
     // ---------------- producer ----------------
@@ -765,7 +780,13 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
         l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
       }
-      const int64_t id = 2 * (int64_t)blockIdx.x + (seg_begin == w_begin ? 0 : 1);
+      const int which = seg_begin == w_begin ? 0 : 1;      // first segment, or the last
+      const int64_t id = 2 * (int64_t)blockIdx.x + which;
+      if (kCluster && !whole && at.tile == 0) {
+        own_b = at.b;
+        own_piece = which;
+        own_runs = run_of(runs, seg_begin + at.count - 1) - run + 1;
+      }
       const float vscale = kFp8 && p.c.v_scale ? p.c.v_scale[head] : 1.f;
       // the real rows of every slice side by side, as many columns at a time
       // as the buffer holds (all of them for up to 16 rows and slices)
@@ -836,6 +857,11 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
               if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
               if (p.lse2) p.lse2[rh] = t;
             }
+          } else if constexpr (kCluster) {
+            float* d = pieces + (which * 16 + i) * (D + 4);
+            reinterpret_cast<float4*>(d + c0 + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(d + c0 + c)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            if (c0 + c == 0) *reinterpret_cast<float2*>(d + D) = make_float2(M, L);
           } else {
             float4* d = reinterpret_cast<float4*>(p.part_o + (id * p.chunk_rows + i) * D + c0 + c);
             d[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -846,6 +872,48 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         }
       }
     }
+  }
+  if constexpr (kCluster) {
+    // every thread of the cluster comes here, also after a time-out
+    auto cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    if (own_b >= 0) {                                      // consumers of the owner
+      const float vscale = kFp8 && p.c.v_scale ? p.c.v_scale[head] : 1.f;
+      for (int it = tid; it < n_rows * (D / 4); it += W::kConsumers) {
+        const int i = it / (D / 4), ln = it % (D / 4);
+        float M = -INFINITY, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < own_runs; ++k) {
+          // the later runs hold theirs as a first segment
+          const float* d = cluster.map_shared_rank(pieces, run + k) +
+                           ((k == 0 ? own_piece : 0) * 16 + i) * (D + 4);
+          const float2 ml = *reinterpret_cast<const float2*>(d + D);
+          const float4 v = *reinterpret_cast<const float4*>(d + ln * 4);
+          const float mn = fmaxf(M, ml.x);
+          const float a = mn == M ? 1.f : ex2(M - mn), f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+          L = L * a + ml.y * f;
+          acc.x = acc.x * a + v.x * f;
+          acc.y = acc.y * a + v.y * f;
+          acc.z = acc.z * a + v.z * f;
+          acc.w = acc.w * a + v.w * f;
+          M = mn;
+        }
+        const float inv = L == 0.f ? 0.f : vscale / L;
+        constexpr bool kOut = __is_same(T, __nv_bfloat16);
+        *reinterpret_cast<uint2*>(
+            const_cast<unsigned char*>(row_ptr(p.out, p.out_row, p.out_head, own_b, i)) + ln * 8) =
+            make_uint2(pack2<kOut>(acc.x * inv, acc.y * inv), pack2<kOut>(acc.z * inv, acc.w * inv));
+        if (ln == 0) {
+          const int r = row0 + i, j = r / p.group;
+          const int64_t rh = ((int64_t)(p.b0 + own_b) * p.next_n + j) * p.heads + head * p.group +
+                             r - j * p.group;
+          const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
+          if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
+          if (p.lse2) p.lse2[rh] = t;
+        }
+      }
+    }
+    cluster.sync();                                        // its pieces have been read
   }
   __syncthreads();
   // after a time-out, let the copies this CTA issued land before it exits
@@ -945,48 +1013,81 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   }
 }
 
-template <typename T, bool kFp8, int D, int WM>
-cudaError_t launch_walk(const PagedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                        cudaStream_t st) {
-  using W = WalkShape<kFp8, D, WM>;
+// The SMs of the current device; the kernel's set-up once per device.
+template <typename T, bool kFp8, int D, int WM, bool kCluster>
+cudaError_t walk_device(int* n_sms) {
   static std::mutex mu;
   static int sms[64];                                      // 0: not set up on that device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  int n_sms;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (sms[dev] == 0) {
-      int n = 0;
-      e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-      if (e != cudaSuccess) return e;
-      e = cudaFuncSetAttribute(paged_walk_kernel<T, kFp8, D, WM>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W::kSmem);
-      if (e != cudaSuccess) return e;
-      sms[dev] = n;
-    }
-    n_sms = sms[dev];
+  std::lock_guard<std::mutex> lock(mu);
+  if (sms[dev] == 0) {
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(paged_walk_kernel<T, kFp8, D, WM, kCluster>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)WalkShape<kFp8, D, WM, kCluster>::kSmem);
+    if (e != cudaSuccess) return e;
+    sms[dev] = n;
   }
+  *n_sms = sms[dev];
+  return cudaSuccess;
+}
+
+template <typename T, bool kFp8, int D, int WM>
+cudaError_t launch_walk(const PagedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                        cudaStream_t st) {
+  using W = WalkShape<kFp8, D, WM, false>;
+  int n_sms = 0;
+  cudaError_t e = walk_device<T, kFp8, D, WM, false>(&n_sms);
+  if (e != cudaSuccess) return e;
   // runs: as many as fill one wave, no more than there can be tiles
   const int units = p.c.heads * p.chunks;
   const int64_t tiles =
-      (int64_t)p.batch * (p.whole ? 1 : ((int64_t)p.c.cap + W::TT - 1) / W::TT);
+      (int64_t)p.batch * (p.mode == kPagedWhole ? 1 : ((int64_t)p.c.cap + W::TT - 1) / W::TT);
   int64_t n_runs = std::min(n_sms * W::kCtas, kPagedMaxCtas) / units;
   n_runs = std::max<int64_t>(1, std::min(n_runs, tiles));
-  paged_walk_kernel<T, kFp8, D, WM>
+  paged_walk_kernel<T, kFp8, D, WM, false>
       <<<(unsigned)(n_runs * units), W::kThreads, W::kSmem, st>>>(p, kmap, vmap);
   e = cudaGetLastError();
-  if (e != cudaSuccess || n_runs == 1 || p.whole) return e;   // nothing has been cut
+  if (e != cudaSuccess || n_runs == 1 || p.mode == kPagedWhole) return e;   // nothing has been cut
   return launch_after(paged_join_kernel<T, D>,
                       dim3((unsigned)n_runs - 1, (unsigned)p.chunk_rows, (unsigned)units),
                       dim3(kJoinThreads), 0, st, p, (int)n_runs);
 }
 
+// As launch_walk for up to 16 rows, in one kernel: a cluster of up to 8 runs a unit.
+template <typename T, bool kFp8, int D>
+cudaError_t launch_cluster(const PagedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                           cudaStream_t st) {
+  using W = WalkShape<kFp8, D, 1, true>;
+  int n_sms = 0;
+  const cudaError_t e = walk_device<T, kFp8, D, 1, true>(&n_sms);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)p.batch * (((int64_t)p.c.cap + W::TT - 1) / W::TT);
+  const unsigned n_runs = (unsigned)std::min<int64_t>(kPagedCluster8, tiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_runs * (unsigned)(p.c.heads * p.chunks));
+  cfg.blockDim = dim3(W::kThreads);
+  cfg.dynamicSmemBytes = W::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = n_runs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_walk_kernel<T, kFp8, D, 1, true>, p, kmap, vmap);
+}
+
 template <typename T, bool kFp8, int D>
 cudaError_t launch_rows(const PagedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                         cudaStream_t st) {
+  if (p.mode == kPagedCluster) return launch_cluster<T, kFp8, D>(p, kmap, vmap, st);
   if (p.chunk_rows <= 16) return launch_walk<T, kFp8, D, 1>(p, kmap, vmap, st);
   if (p.chunk_rows <= 32) return launch_walk<T, kFp8, D, 2>(p, kmap, vmap, st);
   return launch_walk<T, kFp8, D, 4>(p, kmap, vmap, st);

@@ -171,6 +171,16 @@ def test_attention_cut_requests(hq, hk, next_n, d, dtype, cache):
           sums=True)
 
 
+@pytest.mark.parametrize("hq,hk,next_n", [(1, 1, 1), (3, 1, 1), (12, 4, 3), (16, 2, 2), (16, 1, 1)])
+@pytest.mark.parametrize("d,dtype,cache,lens", [
+    (64, F16, F16, [1100, 5, 0, 700]), (64, BF16, E4M3, [2300, 2, 2299]), (128, F16, F16, [1000]),
+    (128, BF16, E4M3, [1200, 1, 64, 1199]), (256, BF16, BF16, [600, 0, 31]), (256, F16, E4M3, [1030])])
+def test_attention_in_one_cluster(hq, hk, next_n, d, dtype, cache, lens):
+    # short work whose requests are still cut: joined within one cluster of CTAs
+    check(Case(lens, hq, hk, d, 16, dtype, cache, next_n=next_n, seed=hq + d), sums=True)
+    check(Case(lens, hq, hk, d, 64, dtype, cache, next_n=next_n, window=520, seed=hq))
+
+
 def test_attention_worked_size_of_the_packed_cache():
     check(Case([519], 3, 1, 256, 512, F16, layout="packed", seed=3))
 
