@@ -38,6 +38,7 @@ constexpr int kRankThreads = 1024;
 constexpr int kRankWarps = kRankThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
+constexpr int kSpare = 8;
 constexpr int kMaxSlice = 24576;          // entries of a CTA whose keys fit in shared memory
 constexpr int kMoveThreads = 256;
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
@@ -117,7 +118,7 @@ struct RankShared {
   int all_newest;
   int digit, need, ties;      // of the pass: its bin, what is still to take, what it holds
   int ties_before;            // of the slice
-  int first_hole[kMaxCluster], first_mover[kMaxCluster];
+  int first_hole[kMaxCluster + 1], first_mover[kMaxCluster + 1];   // then all of them
 };
 
 // Sum of v over the warps before this one (one value a warp, from lane 0);
@@ -141,8 +142,11 @@ template <bool kCached, int ranks>
 __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p, int max_slice) {
   extern __shared__ __align__(16) unsigned char rank_smem[];
   RankShared& sh = *reinterpret_cast<RankShared*>(rank_smem);
-  uint32_t* s_key = reinterpret_cast<uint32_t*>(rank_smem + sizeof(RankShared));   // [max_slice]
-  int32_t* s_pos = reinterpret_cast<int32_t*>(s_key + (kCached ? max_slice : 0));  // [max_slice]
+  // [max_slice + kSpare] and [max_slice]
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(rank_smem + sizeof(RankShared));
+  int32_t* s_pos = reinterpret_cast<int32_t*>(s_key + (kCached ? max_slice + kSpare : 0));
+  // which entries stay, 32 a word
+  uint32_t* s_keep = reinterpret_cast<uint32_t*>(s_pos + (kCached ? max_slice : 0));
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = ranks > 1 ? (int)cluster.block_rank() : 0;
   // a lone CTA needs no cluster barrier
@@ -189,7 +193,7 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
   {
     uint32_t lo = 0xFFFFFFFFu, hi = 0u;
     int newest = INT32_MIN;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = tid; i < ne; i += kRankThreads) {
       const float f = w[e0 + i];
       const uint32_t k = weight_key(f);
@@ -336,29 +340,50 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
                                    i + lane < i1 && (key_of(i + lane) & mask) == prefix));
     ties_before += warps_before(mine, sh.warp, &total);
   }
-  // visit(entry, hole, mover, holes and movers of the warp before it)
-  const auto sweep = [&](auto visit) {
-    int t = ties_before, holes = 0, movers = 0;
-    for (int i = i0; i < i1; i += 32) {
-      const bool there = i + lane < i1;
-      const uint32_t k = (there ? key_of(i + lane) : 0u) & mask;
-      const bool tie = there && k == prefix;
-      const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-      const bool keep = there && (k > prefix || (tie && (!some || t + __popc(tied & below) < need)));
-      t += __popc(tied);
-      const int e = e0 + i + lane;
-      const bool hole = there && e < p.budget && !keep, mover = keep && e >= p.budget;
-      const uint32_t h = __ballot_sync(0xffffffffu, hole), m = __ballot_sync(0xffffffffu, mover);
-      visit(e, hole, mover, holes + __popc(h & below), movers + __popc(m & below));
-      holes += __popc(h);
-      movers += __popc(m);
-    }
-    return make_int2(holes, movers);
+  // which of the 32 entries from i on stay; `ties` counts the bin's on the way
+  const auto kept_of = [&](int i, int* ties) {
+    const bool there = i + lane < i1;
+    const uint32_t k = (there ? key_of(i + lane) : 0u) & mask;
+    if (!some) return __ballot_sync(0xffffffffu, there && k >= prefix);
+    const uint32_t tied = __ballot_sync(0xffffffffu, there && k == prefix);
+    const uint32_t keep = __ballot_sync(
+        0xffffffffu, there && (k > prefix || (k == prefix && *ties + __popc(tied & below) < need)));
+    *ties += __popc(tied);
+    return keep;
   };
-  const int2 counts = sweep([](int, bool, bool, int, int) {});
-  int holes, movers;
-  const int hole_at = warps_before(counts.x, sh.warp, &holes);
-  const int mover_at = warps_before(counts.y, sh.warp, &movers);
+  // the first n of 32 places
+  const auto first = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+  // of the places from i on that `keep` says stay: holes and movers
+  const auto holes_of = [&](int i, uint32_t keep) {
+    return first(min(i1 - i, p.budget - e0 - i)) & ~keep;
+  };
+  const auto movers_of = [&](int i, uint32_t keep) { return keep & ~first(p.budget - e0 - i); };
+  int holes = 0, movers = 0;
+  if (!some) {                           // each lane counts its own
+#pragma unroll 4
+    for (int i = i0; i < i1; i += 32) {
+      const bool there = i + lane < i1, low = e0 + i + lane < p.budget;
+      const bool stays = there && (key_of(there ? i + lane : i) & mask) >= prefix;
+      holes += there && low && !stays;
+      movers += stays && !low;
+      if constexpr (kCached) {
+        const uint32_t keep = __ballot_sync(0xffffffffu, stays);
+        if (lane == 0) s_keep[i >> 5] = keep;
+      }
+    }
+    holes = __reduce_add_sync(0xffffffffu, holes);
+    movers = __reduce_add_sync(0xffffffffu, movers);
+  } else {
+    for (int i = i0, t = ties_before; i < i1; i += 32) {
+      const uint32_t keep = kept_of(i, &t);
+      if (kCached && lane == 0) s_keep[i >> 5] = keep;
+      holes += __popc(holes_of(i, keep));
+      movers += __popc(movers_of(i, keep));
+    }
+  }
+  int hole_at = holes, mover_at = movers;
+  hole_at = warps_before(hole_at, sh.warp, &holes);
+  mover_at = warps_before(mover_at, sh.warp, &movers);
   if (tid == 0) {
     sh.holes = holes;
     sh.movers = movers;
@@ -378,39 +403,64 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
         }
       }
       if (lane < ranks) {
-        sh.first_hole[lane] = x - h;
-        sh.first_mover[lane] = y - m;
+        sh.first_hole[lane + 1] = x;
+        sh.first_mover[lane + 1] = y;
       }
+      if (lane == 0) sh.first_hole[0] = sh.first_mover[0] = 0;
     }
     __syncthreads();
   };
   if constexpr (kCached) {
     // holes from the front of the list, movers from its back (an entry is at
-    // most one of the two); then hole i of the request takes mover i, in
-    // whichever CTA's list that is
-    sweep([&](int e, bool hole, bool mover, int h, int m) {
-      if (hole) s_pos[hole_at + h] = e;
-      if (mover) s_pos[max_slice - 1 - (mover_at + m)] = e;
-    });
+    // most one of the two)
+#pragma unroll 2
+    for (int i = i0; i < i1; i += 32) {
+      const uint32_t keep = s_keep[i >> 5];
+      if (e0 + i < p.budget) {
+        const uint32_t h = holes_of(i, keep);
+        if (h >> lane & 1u) s_pos[hole_at + __popc(h & below)] = e0 + i + lane;
+        hole_at += __popc(h);
+      }
+      if (e0 + i + 32 > p.budget) {
+        const uint32_t m = movers_of(i, keep);
+        if (m >> lane & 1u) s_pos[max_slice - 1 - (mover_at + __popc(m & below))] = e0 + i + lane;
+        mover_at += __popc(m);
+      }
+    }
     sync_all();
     ranks_before();
-    const int base = sh.first_hole[rank];
-    for (int i = tid; i < holes; i += kRankThreads) {
+    // hole i of the request takes mover i, whichever CTAs' lists they are in;
+    // the CTAs share the request's holes evenly
+    const int all = sh.first_hole[ranks], share = (all + ranks - 1) / ranks;
+    const int begin = min(all, rank * share), end = min(all, begin + share);
+    const auto list_of = [&](const int* firsts, int i, int* in) {
       int r = 0;
-      while (r + 1 < ranks && base + i >= sh.first_mover[r + 1]) ++r;
-      const int at = sh.first_mover[r];
-      const int32_t* list = ranks > 1 ? cluster.map_shared_rank(s_pos, r) : s_pos;
-      const int from = list[max_slice - 1 - (base + i - at)], to = s_pos[i];
+#pragma unroll
+      for (int q = 1; q < ranks; ++q)
+        if (i >= firsts[q]) r = q;
+      *in = i - firsts[r];
+      return ranks > 1 ? cluster.map_shared_rank(s_pos, r) : s_pos;
+    };
+    for (int i = begin + tid; i < end; i += kRankThreads) {
+      int ih, im;
+      const int32_t* lh = list_of(sh.first_hole, i, &ih);
+      const int32_t* lm = list_of(sh.first_mover, i, &im);
+      const int to = lh[ih], from = lm[max_slice - 1 - im];
       kept[to] = from;
       sums_out[to] = w[from];
       pos_out[to] = pos[from];
-      s_key[i] = from;                   // for the moves below
+      if (p.move_here) {
+        // in place of the keys: at most half of the request's entries are
+        // holes, so a CTA's share of pairs is a slice and a rounding
+        s_key[2 * (i - begin)] = from;
+        s_key[2 * (i - begin) + 1] = to;
+      }
     }
     if (p.move_here) {
       __syncthreads();
       const int32_t* bt = p.c.bt + (int64_t)b * p.c.bt_s0;
-      for (int i = warp; i < holes; i += kRankWarps) {
-        const int from = (int)s_key[i], to = s_pos[i];
+      for (int i = warp; i < end - begin; i += kRankWarps) {
+        const int from = (int)s_key[2 * i], to = (int)s_key[2 * i + 1];
         const int32_t pf = bt[from >> p.c.page_log2], pt = bt[to >> p.c.page_log2];
         if (pf >= 0 && pf < p.c.num_pages && pt >= 0 && pt < p.c.num_pages)
           move_entry(p.c, p.head_log2, pf, from, pt, to);
@@ -424,13 +474,18 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
     ranks_before();
     const int hole_base = sh.first_hole[rank] + hole_at;
     const int mover_base = sh.first_mover[rank] + mover_at;
-    sweep([&](int e, bool, bool mover, int, int m) {
-      if (mover) pos_out[mover_base + m] = e;
-    });
+    int m_at = mover_base, h_at = hole_base;
+    for (int i = i0, t = ties_before; i < i1; i += 32) {
+      const uint32_t m = movers_of(i, kept_of(i, &t));
+      if (m >> lane & 1u) pos_out[m_at + __popc(m & below)] = e0 + i + lane;
+      m_at += __popc(m);
+    }
     sync_all();
-    sweep([&](int e, bool hole, bool, int h, int) {
-      if (hole) kept[e] = __ldcg(pos_out + hole_base + h);
-    });
+    for (int i = i0, t = ties_before; i < i1; i += 32) {
+      const uint32_t h = holes_of(i, kept_of(i, &t));
+      if (h >> lane & 1u) kept[e0 + i + lane] = __ldcg(pos_out + h_at + __popc(h & below));
+      h_at += __popc(h);
+    }
     sync_all();
     for (int i = rank * kRankThreads + tid; i < p.budget; i += ranks * kRankThreads) {
       const int e = __ldcg(kept + i);
@@ -473,6 +528,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
   }
 }
 
+// Shared memory for a slice whose keys it holds: keys, positions, a bit each.
+size_t rank_smem_bytes(int64_t slice) {
+  return sizeof(RankShared) + (size_t)(2 * slice + kSpare + (slice + 31) / 32) * 4;
+}
+
 // The SMs of the current device; the rank kernels' set-up once per device.
 cudaError_t evict_device(int* n_sms) {
   static std::mutex mu;
@@ -489,7 +549,7 @@ cudaError_t evict_device(int* n_sms) {
     for (auto k : {rank_kernel<true, 1>, rank_kernel<true, 2>, rank_kernel<true, 4>,
                    rank_kernel<true, 8>}) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)(sizeof(RankShared) + kMaxSlice * 8));
+                               (int)rank_smem_bytes(kMaxSlice));
       if (e != cudaSuccess) return e;
     }
     sms[dev] = n;
@@ -523,7 +583,7 @@ cudaError_t launch_rank(EvictParams& p, int reqs, int64_t most, int sms, cudaStr
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(reqs * ranks));
   cfg.blockDim = dim3(kRankThreads);
-  cfg.dynamicSmemBytes = sizeof(RankShared) + (cached ? (size_t)slice * 8 : 0);
+  cfg.dynamicSmemBytes = cached ? rank_smem_bytes(slice) : sizeof(RankShared);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -533,6 +533,15 @@ def test_evict_long_requests(n, kind):
                  500)
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
+@pytest.mark.parametrize("budget", [1, 5, 16, 40])
+def test_evict_short_requests_of_a_long_table(budget, kind):
+    # a cluster's slices of a few entries, some of none
+    lens = [1, 2, 9, 10, 11, 17, 31, 33, 80]
+    _check_evict(_evict_case(lens, budget, budget // 4, budget // 4, seed=budget, kind=kind,
+                             cols=2100), budget, budget // 4, budget // 4)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16, E4M3])
 @pytest.mark.parametrize("layout,hk,d,size", [("packed", 1, 256, 512), ("heads", 3, 64, 8),
                                               ("wide", 5, 128, 32)])
