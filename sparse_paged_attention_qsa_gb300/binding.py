@@ -690,14 +690,14 @@ def qsa_paged_attention_workspace_bytes(k_cache, v_cache, block_tables, *, next_
 def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next_n: int = 1,
                         scale: float | None = None, window: int = 0, k_scale=None, v_scale=None,
                         out=None, lse=None, weight_sums=None, weight_sums_out=None,
-                        workspace=None, error_word=None, stream=None):
+                        workspace=None, error_word=None, stream=None, library=None):
     """Dense attention of each request's next_n new tokens, q [requests*next_n,
     heads, dim], over its cached entries (include/qsa_cache.h).  scale: 1/sqrt
     (dim) unless given.  lse: fp32 [rows, heads], filled when given.
     weight_sums / weight_sums_out: fp32 [requests, entries]; the second gets
     the first plus the weight that each entry received in this call.  Returns
-    out [rows, heads, dim]."""
-    lib = _lib or load_library()
+    out [rows, heads, dim].  `library` as in qsa_select_paged_tokens."""
+    lib = library or _lib or load_library()
     _on_current_device(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, out,
                        lse, weight_sums, weight_sums_out, workspace, error_word)
     if q.dim() != 3:

@@ -7,12 +7,12 @@ into ``sparse_paged_attention_qsa_gb300/libqsa.so`` (cudart linked
 statically).  Objects go to ``_build/`` next to this file.
 
 ``build_wait_test()`` builds ``libqsa_waittest.so``, a test-only variant of
-the selection and attention entry points compiled with QSA_WAIT_TEST: its
-stage waits give up after 2 ms and it exports one extra symbol that makes
-the first CTA of the score kernel (or of the fused small-batch kernel) leave
-one stage fill without a copy, so the failure-detection test can make a
-device wait run out.  The product library
-carries neither.
+the selection and attention entry points compiled with QSA_WAIT_TEST (the
+dense paged attention for heads of 64): its stage waits give up after 2 ms and
+it exports two extra symbols that make the first CTA of the score kernel (or
+of the fused small-batch kernel), or of the paged attention's walk, leave one
+stage fill without a copy, so the failure-detection tests can make a device
+wait run out.  The product library carries neither.
 """
 from __future__ import annotations
 
@@ -30,7 +30,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqsa.so")
 WAIT_TEST_LIB = os.path.join(PKG, "libqsa_waittest.so")
-WAIT_TEST_SOURCES = ("qsa_abi.cu", "qsa_select.cu", "qsa_attention.cu", "qsa_fused.cu")
+WAIT_TEST_SOURCES = ("qsa_abi.cu", "qsa_select.cu", "qsa_attention.cu", "qsa_fused.cu",
+                     "qsa_paged_attention.cu", "qsa_paged_attn_64.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]

@@ -31,6 +31,10 @@ namespace {
 
 constexpr int kWeightThreads = 128;
 
+#ifdef QSA_WAIT_TEST
+int32_t g_test_withhold = -1;
+#endif
+
 struct WeightParams {
   const int32_t* ctx;
   const float* z;             // [rows][heads][pitch] logits (base 2)
@@ -277,9 +281,15 @@ extern "C" qsa_status qsa_paged_attention(
   for (int64_t b0 = 0; b0 < R; b0 += step) {
     p.b0 = (int32_t)b0;
     p.batch = (int32_t)std::min<int64_t>(step, R - b0);
+#ifdef QSA_WAIT_TEST
+    p.test_withhold = b0 == 0 ? g_test_withhold : -1;      // heads of 64 alone are built
+    const cudaError_t e = p.c.dim == 64 ? launch_paged_64(p, bf16, fp8, kmap, vmap, s)
+                                        : cudaErrorNotSupported;
+#else
     const cudaError_t e = p.c.dim == 64    ? launch_paged_64(p, bf16, fp8, kmap, vmap, s)
                           : p.c.dim == 128 ? launch_paged_128(p, bf16, fp8, kmap, vmap, s)
                                            : launch_paged_256(p, bf16, fp8, kmap, vmap, s);
+#endif
     if (e != cudaSuccess) return QSA_ERR_CUDA;
   }
   if (p.z) {
@@ -303,3 +313,12 @@ extern "C" qsa_status qsa_paged_attention(
   }
   return QSA_OK;
 }
+
+#ifdef QSA_WAIT_TEST
+// Test build only, declared in no public header: the next attention launches
+// leave slot fill `issue` of the walk's CTA 0 without a copy (-1: none).
+extern "C" __attribute__((visibility("default"))) void qsa_test_withhold_paged_fill(
+    int32_t issue) {
+  qsa::g_test_withhold = issue;
+}
+#endif

@@ -51,6 +51,9 @@ struct PagedParams {
   float* part_ml;             // workspace: [2 * kPagedMaxCtas][chunk_rows][2]
   float* part_o;              // workspace: [2 * kPagedMaxCtas][chunk_rows][dim]
   uint32_t* err;
+#ifdef QSA_WAIT_TEST
+  int32_t test_withhold;      // test build: CTA 0 issues no copy for this slot fill (-1: none)
+#endif
 };
 
 // The kernels' part of a call: the walk over the tiles and the join of what

@@ -321,6 +321,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
 
   // the request that starts in this run and is cut: its place, and its pieces
   int own_b = -1, own_piece = 0, own_runs = 0;
+  int withheld = -1;                                       // test build: a slot fill left out
   int issued = 0, segments = 0;                            // producer: slots, queries loaded
   if (warp == W::NW) {
     // ---------------- producer ----------------
@@ -415,17 +416,26 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         for (int kv = 0; kv < 2; ++kv) {
           if (round > 0 && !wait_empty(bar_empty + 8 * s, (uint32_t)((round - 1) & 1))) break;
           const uint32_t full = bar_full + 8 * s, dst = ring + s * W::kSlot;
-          if (lane == 0) {
-            tb.boxes[s] = mask;
-            mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * W::kRowBytes));
-          }
-          __syncwarp();
-          if (good) {
+#ifdef QSA_WAIT_TEST
+          // test build: leave this fill without a copy, so the consumers'
+          // wait on it runs out (the failure-detection test)
+          const bool withhold = blockIdx.x == 0 && issued == p.test_withhold;
+          if (withhold) withheld = issued;
+          if (!withhold)
+#endif
+          {
+            if (lane == 0) {
+              tb.boxes[s] = mask;
+              mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * W::kRowBytes));
+            }
+            __syncwarp();
+            if (good) {
 #pragma unroll
-            for (int i = 0; i < W::kChunks; ++i)
-              tma_load_4d(dst + i * (TT * W::kChunkBytes) + lane * box_rows * W::kChunkBytes,
-                          kv ? &vmap : &kmap, i * (W::kChunkBytes / (kFp8 ? 1 : 2)), head,
-                          be & ((1 << lg) - 1), id, full, policy);
+              for (int i = 0; i < W::kChunks; ++i)
+                tma_load_4d(dst + i * (TT * W::kChunkBytes) + lane * box_rows * W::kChunkBytes,
+                            kv ? &vmap : &kmap, i * (W::kChunkBytes / (kFp8 ? 1 : 2)), head,
+                            be & ((1 << lg) - 1), id, full, policy);
+            }
           }
           ++issued;
           if (++s == S) {
@@ -919,7 +929,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   // after a time-out, let the copies this CTA issued land before it exits
   if (*s_abort != 0 && warp == W::NW && lane == 0) {
     for (int n = issued > S ? issued - S : 0; n < issued; ++n)
-      mbar_wait(bar_full + 8 * (n % S), (uint32_t)((n / S) & 1), kDrainLimitNs);
+      if (n != withheld) mbar_wait(bar_full + 8 * (n % S), (uint32_t)((n / S) & 1), kDrainLimitNs);
     for (int n = segments > 2 ? segments - 2 : 0; n < segments; ++n)
       mbar_wait(bar_qfull + 8 * (n & 1), (uint32_t)((n >> 1) & 1), kDrainLimitNs);
   }
