@@ -267,8 +267,7 @@ extern "C" qsa_status qsa_paged_attention(
   bind_calling_thread();
   const bool bf16 = dtype == QSA_DT_BF16, fp8 = cache->dtype == QSA_DT_F8E4M3;
   const int esize = fp8 ? 1 : 2;
-  const int wm = p.chunk_rows <= 16 ? 1 : p.chunk_rows <= 32 ? 2 : 4;
-  const int tile = paged_tile(p.c.dim, p.c.dim * esize, wm);
+  const int tile = paged_tile(p.c.dim, p.c.dim * esize, paged_sets(p.chunk_rows));
   const int rows = (int)std::min<int64_t>(cache->page_size, tile);
   CUtensorMap kmap, vmap;
   if (!encode_view(&kmap, p.c.k, p.c, esize, p.c.k_page, p.c.k_token, p.c.k_head, rows) ||

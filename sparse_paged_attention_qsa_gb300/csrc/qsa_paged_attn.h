@@ -65,18 +65,22 @@ cudaError_t launch_paged_128(const PagedParams& p, bool bf16, bool fp8, const CU
 cudaError_t launch_paged_256(const PagedParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, cudaStream_t st);
 
-// The shape of a CTA, for heads of `dim`, row_bytes of K (or V) a token and wm
-// groups of 16 query rows; what was measured, in us:
-//   four consumer warps, for up to 16 rows of heads below 256 two CTAs an SM;
-//   for more rows eight warps in one CTA (16-bit heads of 128: 32 rows 92 with
-//   eight, 111 with four; 64 rows 260 and 305); heads of 256 hold twice the
-//   output a row, so four warps with all registers (32 rows 181 against 331);
-//   ring slots of 16 KB, but of 32 KB for heads of 256 (E4M3: 138 against 167)
+// The shape of a CTA that walks up to `rows` query rows of heads of `dim`, with
+// row_bytes of K (or V) a token; what was measured, in us:
+//   wm sets of warps, each with 16 rows.  Up to 16 rows of heads below 256 two
+//   CTAs an SM with four consumer warps each; for more rows one CTA with eight
+//   (16-bit heads of 128, 32 rows: 92 with eight warps, 111 with four; 64 rows:
+//   260 and 305).  Two sets of rows in one warp, which share what it reads and
+//   converts of K and V, leave too few warps: 16-bit 32 rows 103 against 88,
+//   E4M3 117 against 108.  Heads of 256 hold twice the output a row, so four
+//   warps with all registers (32 rows: 181 against 331).
+//   Ring slots of 16 KB, but of 32 KB for heads of 256 (E4M3: 138 against 167)
 //   and for 32 rows of 16-bit heads of 128 (92 against 108, where 64 rows take
 //   373 with 32 KB and 260 with 16); at most 64 tokens a warp, whose logits are
 //   in its registers.  Narrower heads with up to 16 rows in one CTA an SM and
 //   32 KB slots instead: 84 against 83 (131072 tokens), but 65 against 48 where
 //   requests are short, and 344 against 285 for E4M3 heads of 128.
+constexpr int paged_sets(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 constexpr int paged_warps(int dim, int wm) { return wm == 1 || dim == 256 ? 4 : 8; }
 constexpr int paged_ctas(int dim, int wm) { return wm == 1 && dim < 256 ? 2 : 1; }
 // tokens of a tile

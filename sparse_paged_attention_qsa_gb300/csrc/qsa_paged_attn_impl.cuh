@@ -13,8 +13,8 @@
 //   query rows), all CTAs in a single wave: every SM streams the same bytes
 //   whatever the lengths.
 //   One producer warp looks pages up and loads K and V tiles into a ring by
-//   TMA (swizzled, completion on mbarriers); four consumer warps share a
-//   tile: WM groups of 16 query rows by WK = 4 / WM slices of its tokens.
+//   TMA (swizzled, completion on mbarriers); four or eight consumer warps share a
+//   tile: WM sets of 16 query rows by WK slices of its tokens.
 //   Each warp keeps its rows' maximum, sum and output in registers: S = Q K^T
 //   and P V by mma.sync.m16n8k16 (binary32 accumulation) on fragments that
 //   ldmatrix reads from the ring.  (tcgen05 needs 64 or 128 rows and a round
@@ -62,7 +62,7 @@ struct WalkTables {
   uint64_t full[kMaxSlots], empty[kMaxSlots];   // mbarriers of the ring
   uint64_t q_full[2], q_empty[2];               // and of the two query slots
   uint32_t boxes[kMaxSlots];                    // the slot's copies that found a page
-  float ml[8][16][2];                           // maximum and sum of a warp's rows
+  float ml[8][16][2];                            // maximum and sum of the warps' rows
   float qs[kPagedMaxRows];                      // what the queries were divided by
   int32_t scan[9 * 32];
   int32_t ctx[kPagedBatch];                     // cached tokens of each request
@@ -75,7 +75,8 @@ static_assert(sizeof(WalkTables) % 16 == 0, "a whole number of 16-byte pieces");
 template <bool kFp8, int D, int WM, bool kCluster>
 struct WalkShape {
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);        // a token's K (or V) of one head
-  static constexpr int NW = paged_warps(D, WM);               // consumer warps
+  static constexpr int NW = paged_warps(D, WM);           // consumer warps
+  static constexpr int kRows = 16 * WM;                       // query rows they hold
   static constexpr int kConsumers = NW * 32;
   static constexpr int kThreads = kConsumers + 32;            // + the producer warp
   static constexpr int TT = paged_tile(D, kRowBytes, WM);
@@ -86,7 +87,7 @@ struct WalkShape {
   static constexpr int kChunks = kRowBytes / kChunkBytes;     // copies that fill a slot
   static constexpr int kSlot = TT * kRowBytes;                // K (or V) of a tile
   static constexpr int kQPitch = D + 8;                       // halves; + 16 B against conflicts
-  static constexpr int kQBytes = 16 * WM * kQPitch * 2;       // a query slot
+  static constexpr int kQBytes = kRows * kQPitch * 2;         // a query slot
   static constexpr int kQSlots = kFp8 ? 3 : 2;                // the third: as FP16, reordered
   static constexpr int kMergeBytes = NW == 8 ? 128 * 40 * 4 : 17408;   // at least 32 columns
   // of the first and the last segment: 16 rows and their maximum and sum
@@ -99,7 +100,7 @@ struct WalkShape {
   static constexpr size_t kSmem = (size_t)kFixed + (size_t)S * kSlot;
   static_assert(S >= 3, "the ring needs K, V and one slot ahead");
   static_assert(NS >= 1 && NS <= 4, "logits of a tile stay in registers");
-  static constexpr bool kPair = !kFp8 && WM <= 2;             // weights as value + remainder
+  static constexpr bool kPair = !kFp8 && kRows <= 32;         // weights as value + remainder
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -528,7 +529,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         const unsigned char* src = base + S * W::kSlot + qs * W::kQBytes;
         uint32_t* fp16 = reinterpret_cast<uint32_t*>(base + S * W::kSlot + 2 * W::kQBytes);
         consumers_sync<W::kConsumers>();                   // all are done with the last ones
-        for (int i = tid; i < 16 * WM * (D / 8); i += W::kConsumers) {
+        for (int i = tid; i < W::kRows * (D / 8); i += W::kConsumers) {
           // D/8 lanes (8, 16 or 32, aligned) hold one row: its largest
           // magnitude, then FP16 with each 16 dims in the order in which the
           // E4M3 fragments hold them (dims 4q, 4q+1 at 2q and 4q+2, 4q+3 at 8 + 2q)
@@ -566,29 +567,24 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         consumers_sync<W::kConsumers>();
       }
 
-      // this thread's rows: wm*16 + g and + 8
+      // this thread's rows, k = 0 and 1
+      const auto row_of = [&](int k) { return wm * 16 + g + 8 * k; };
+      const auto token_of = [&](int i) { return min(row0 + i, p.rows - 1) / p.group; };
       float mult[2];
-      int32_t row_lo[2], row_hi[2];
-      int row_j[2];
-      float* zp[2];
+      float* z_at[2];                                     // its logits' row, or null
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int i = wm * 16 + g + 8 * k, r = min(row0 + i, p.rows - 1);
-        row_j[k] = r / p.group;
-        visible(p, ctx, row_j[k], &row_lo[k], &row_hi[k]);
         mult[k] = p.scale_log2;
         if constexpr (kFp8) {
           if (p.c.k_scale) mult[k] *= p.c.k_scale[head];
-          mult[k] *= tb.qs[wm * 16 + g + 8 * k];
+          mult[k] *= tb.qs[row_of(k)];
         }
-        const int64_t q_row = (int64_t)(p.b0 + at.b) * p.next_n;
-        zp[k] = p.z && i < n_rows
-                    ? p.z + ((q_row + row_j[k]) * p.heads + head * p.group + r - row_j[k] * p.group) *
-                                p.z_pitch
-                    : nullptr;
+        const int r = min(row0 + row_of(k), p.rows - 1), j = r / p.group;
+        const int64_t rh = ((int64_t)(p.b0 + at.b) * p.next_n + j) * p.heads + head * p.group + r -
+                           j * p.group;
+        z_at[k] = p.z && row_of(k) < n_rows ? p.z + rh * p.z_pitch : nullptr;
       }
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-      float o[D / 8][4];
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
@@ -638,31 +634,49 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         }
         release();
         // logits; masked ones -inf
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float z0 = sc[s][n][2 * k] * mult[k], z1 = sc[s][n][2 * k + 1] * mult[k];
-              const int32_t e = we + s * 16 + n * 8 + 2 * q4;
-              if (edge) {
-                const bool in = (mask >> ((e - e0) >> box_log2)) & 1u;
-                if (!in || e < row_lo[k] || e >= row_hi[k]) z0 = -INFINITY;
-                if (!in || e + 1 < row_lo[k] || e + 1 >= row_hi[k]) z1 = -INFINITY;
-              }
-              if (zp[k] && e < hi_all) *reinterpret_cast<float2*>(zp[k] + e) = make_float2(z0, z1);
-              sc[s][n][2 * k] = z0;
-              sc[s][n][2 * k + 1] = z1;
-              mx[k] = fmaxf(mx[k], fmaxf(z0, z1));
-            }
         float ref[2], al[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-          const float mn = fmaxf(m[k], mx[k]);
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              sc[s][n][2 * k] *= mult[k];
+              sc[s][n][2 * k + 1] *= mult[k];
+            }
+          if (edge) {
+            int32_t lo, hi;
+            visible(p, ctx, token_of(row_of(k)), &lo, &hi);
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const int32_t e = we + s * 16 + n * 8 + 2 * q4 + x;
+                  const bool in = (mask >> ((e - e0) >> box_log2)) & 1u;
+                  if (!in || e < lo || e >= hi) sc[s][n][2 * k + x] = -INFINITY;
+                }
+          }
+          if (z_at[k]) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                const int32_t e = we + s * 16 + n * 8 + 2 * q4;
+                if (e < hi_all)
+                  *reinterpret_cast<float2*>(z_at[k] + e) =
+                      make_float2(sc[s][n][2 * k], sc[s][n][2 * k + 1]);
+              }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) mx = fmaxf(mx, fmaxf(sc[s][n][2 * k], sc[s][n][2 * k + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[k], mx);
           ref[k] = mn == -INFINITY ? 0.f : mn - kShift;    // nothing seen yet: all weights 0
           al[k] = mn == m[k] ? 1.f : ex2(m[k] - mn);
           m[k] = mn;
@@ -697,8 +711,6 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         // P V.  Where some entry is hidden from some row, 0 times what it holds
         // may be NaN: V enters with the hidden entries zeroed, once for each
         // token j that has rows here, and only those rows take the result.
-        const int ja = min(row0 + wm * 16, p.rows - 1) / p.group;
-        const int jb = edge ? min(row0 + wm * 16 + 15, p.rows - 1) / p.group : ja;
         wait_full();
 #pragma unroll
         for (int ch = 0; ch < W::kChunks; ++ch) {
@@ -732,9 +744,13 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                 }
               }
           } else {
+            const int ja = token_of(wm * 16), jb = token_of(wm * 16 + 15);
             for (int j = ja; j <= jb; ++j) {
               int32_t lo, hi;
               visible(p, ctx, j, &lo, &hi);
+              bool mine[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) mine[k] = token_of(row_of(k)) == j;
 #pragma unroll
               for (int st = 0; st < NS; ++st) {
                 uint32_t keep[2];
@@ -745,34 +761,32 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                   keep[n] = (in && e >= lo && e < hi ? 0xffffu : 0u) |
                             (in && e + 1 >= lo && e + 1 < hi ? 0xffff0000u : 0u);
                 }
-                const auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+                const auto add = [&](int n, uint32_t b0, uint32_t b1) {
                   float d[4] = {0.f, 0.f, 0.f, 0.f};
                   mma16816<kBf16>(d, ph[st], b0 & keep[0], b1 & keep[1]);
                   if constexpr (W::kPair) mma16816<kBf16>(d, pl[st], b0 & keep[0], b1 & keep[1]);
-                  if (row_j[0] == j) {
-                    acc[0] += d[0];
-                    acc[1] += d[1];
-                  }
-                  if (row_j[1] == j) {
-                    acc[2] += d[2];
-                    acc[3] += d[3];
-                  }
+#pragma unroll
+                  for (int k = 0; k < 2; ++k)
+                    if (mine[k]) {
+                      o[n][2 * k] += d[2 * k];
+                      o[n][2 * k + 1] += d[2 * k + 1];
+                    }
                 };
 #pragma unroll
                 for (int i = 0; i < kPer / 2; ++i) {
                   uint32_t b[4];
                   ldsm4t(vb + piece(v_row + st * 16, 2 * i + v_c), b);
                   if constexpr (!kFp8) {
-                    add(o[ch * kTiles + 2 * i], b[0], b[1]);
-                    add(o[ch * kTiles + 2 * i + 1], b[2], b[3]);
+                    add(ch * kTiles + 2 * i, b[0], b[1]);
+                    add(ch * kTiles + 2 * i + 1, b[2], b[3]);
                   } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) b[k] = __byte_perm(b[k], 0, 0x3120);
                     const int n = ch * kTiles + 4 * i;
-                    add(o[n], e4m3_lo(b[0]), e4m3_lo(b[1]));
-                    add(o[n + 1], e4m3_hi(b[0]), e4m3_hi(b[1]));
-                    add(o[n + 2], e4m3_lo(b[2]), e4m3_lo(b[3]));
-                    add(o[n + 3], e4m3_hi(b[2]), e4m3_hi(b[3]));
+                    add(n, e4m3_lo(b[0]), e4m3_lo(b[1]));
+                    add(n + 1, e4m3_hi(b[0]), e4m3_hi(b[1]));
+                    add(n + 2, e4m3_lo(b[2]), e4m3_lo(b[3]));
+                    add(n + 3, e4m3_hi(b[2]), e4m3_hi(b[3]));
                   }
                 }
               }
@@ -807,7 +821,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         consumers_sync<W::kConsumers>();                   // the buffer is free
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int i = wm * 16 + g + 8 * k;
+          const int i = row_of(k);
           if (i < n_rows) {
             float* b = merge + (wk * n_rows + i) * pitch - c0;
 #pragma unroll
@@ -1098,9 +1112,11 @@ template <typename T, bool kFp8, int D>
 cudaError_t launch_rows(const PagedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                         cudaStream_t st) {
   if (p.mode == kPagedCluster) return launch_cluster<T, kFp8, D>(p, kmap, vmap, st);
-  if (p.chunk_rows <= 16) return launch_walk<T, kFp8, D, 1>(p, kmap, vmap, st);
-  if (p.chunk_rows <= 32) return launch_walk<T, kFp8, D, 2>(p, kmap, vmap, st);
-  return launch_walk<T, kFp8, D, 4>(p, kmap, vmap, st);
+  switch (paged_sets(p.chunk_rows)) {
+    case 1: return launch_walk<T, kFp8, D, 1>(p, kmap, vmap, st);
+    case 2: return launch_walk<T, kFp8, D, 2>(p, kmap, vmap, st);
+    default: return launch_walk<T, kFp8, D, 4>(p, kmap, vmap, st);
+  }
 }
 
 template <int D>
