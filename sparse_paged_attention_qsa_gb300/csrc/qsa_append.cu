@@ -11,6 +11,7 @@
 #include "qsa_cache_host.h"
 #include "qsa_device.cuh"
 #include "qsa_host.h"
+#include "qsa_internal.h"
 
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -71,6 +72,7 @@ append_kernel(const AppendParams p, int lt_log2, int dim_log2) {
   const int part = threadIdx.x & ((1 << lt_log2) - 1);
   const int64_t t = ((int64_t)blockIdx.x << (8 - lt_log2)) + (threadIdx.x >> lt_log2);
   static_assert(kAppendThreads == 256, "8 bits of thread index");
+  pdl_wait();          // on every path: the grid's end must mean its predecessor's
   if (t >= p.num_tokens) return;
   const int row = p.c.heads << dim_log2;                // pieces of a token's K
   const unsigned char* k_src = p.k + t * p.k_token;
@@ -145,8 +147,8 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t st) {
   while ((kPiecesOf<kFp8> << lt_log2) < 2 * p.c.heads * head_pieces && lt_log2 < 8) ++lt_log2;
   const int64_t per_cta = kAppendThreads >> lt_log2;
   const int64_t grid = (p.num_tokens + per_cta - 1) / per_cta;
-  append_kernel<T, kFp8><<<(unsigned)grid, kAppendThreads, 0, st>>>(p, lt_log2, dim_log2);
-  return cudaGetLastError();
+  return launch_after(append_kernel<T, kFp8>, dim3((unsigned)grid), dim3(kAppendThreads), 0, st, p,
+                      lt_log2, dim_log2);
 }
 
 }  // namespace

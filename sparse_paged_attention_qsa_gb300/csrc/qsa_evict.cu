@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
   const auto of_rank = [&](int r) -> const RankShared& {
     return ranks > 1 ? *cluster.map_shared_rank(&sh, r) : sh;
   };
+  pdl_wait();          // on every path: the grid's end must mean its predecessor's
   const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* w = p.sums + b * p.sums_s0;
   const int32_t* pos = p.pos + b * p.pos_s0;
@@ -585,13 +586,15 @@ cudaError_t launch_rank(EvictParams& p, int reqs, int64_t most, int sms, cudaStr
   cfg.blockDim = dim3(kRankThreads);
   cfg.dynamicSmemBytes = cached ? rank_smem_bytes(slice) : sizeof(RankShared);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const auto kernel = cached ? (ranks == 1   ? rank_kernel<true, 1>
                                 : ranks == 2 ? rank_kernel<true, 2>
                                 : ranks == 4 ? rank_kernel<true, 4>

@@ -260,6 +260,9 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   // rows past the last query stay zero in every slot
   for (int i = tid; i < W::kQSlots * W::kQBytes / 16; i += W::kThreads)
     reinterpret_cast<uint4*>(base + S * W::kSlot)[i] = make_uint4(0, 0, 0, 0);
+  // launched while the kernel before it on the stream may still run: what that
+  // one wrote, and what it read and this one writes, is touched from here on
+  pdl_wait();
   // tiles before each request
   {
     const int per = (p.batch + W::kThreads - 1) / W::kThreads;
@@ -1074,9 +1077,8 @@ cudaError_t launch_walk(const PagedParams& p, const CUtensorMap& kmap, const CUt
       (int64_t)p.batch * (p.mode == kPagedWhole ? 1 : ((int64_t)p.c.cap + W::TT - 1) / W::TT);
   int64_t n_runs = std::min(n_sms * W::kCtas, kPagedMaxCtas) / units;
   n_runs = std::max<int64_t>(1, std::min(n_runs, tiles));
-  paged_walk_kernel<T, kFp8, D, WM, false>
-      <<<(unsigned)(n_runs * units), W::kThreads, W::kSmem, st>>>(p, kmap, vmap);
-  e = cudaGetLastError();
+  e = launch_after(paged_walk_kernel<T, kFp8, D, WM, false>, dim3((unsigned)(n_runs * units)),
+                   dim3(W::kThreads), W::kSmem, st, p, kmap, vmap);
   if (e != cudaSuccess || n_runs == 1 || p.mode == kPagedWhole) return e;   // nothing has been cut
   return launch_after(paged_join_kernel<T, D>,
                       dim3((unsigned)n_runs - 1, (unsigned)p.chunk_rows, (unsigned)units),
@@ -1098,13 +1100,15 @@ cudaError_t launch_cluster(const PagedParams& p, const CUtensorMap& kmap, const 
   cfg.blockDim = dim3(W::kThreads);
   cfg.dynamicSmemBytes = W::kSmem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = n_runs;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, paged_walk_kernel<T, kFp8, D, 1, true>, p, kmap, vmap);
 }
 
