@@ -43,8 +43,8 @@ extern "C" {
 /*
  * A paged K/V cache.  K and V are views [num_pages, page_size, num_heads,
  * head_dim]; strides in elements, the last one 1, the others multiples of 16
- * bytes and at least head_dim (the stride of a dimension of size 1 is not
- * looked at).  So K and V may be two tensors, or lie side by side in one (the
+ * bytes and such that no two elements of a view share an address (the stride of
+ * a dimension of size 1 is not looked at).  So K and V may be two tensors, or lie side by side in one (the
  * exact-packed cache of qsa.h is strides {262144, 512, any, 1} with v = k +
  * 256), tokens or heads outermost within a page; the two views must not
  * share an element.
@@ -81,7 +81,8 @@ typedef struct qsa_paged_cache {
  *   K[page, slot, h, :] = k[t, h, :], V likewise; into an E4M3 cache
  *   k[t, h, :] * (1 / k_scale[h]) (both in binary32), rounded to nearest
  *   even, magnitudes above 448 to 448, NaN to NaN;
- *   entry_positions[r, e] = positions[t] (e itself when positions is NULL);
+ *   entry_positions[r, e] = positions[t] (e itself when positions is NULL), as
+ *   32 bits;
  *   weight_sums[r, e] = 0.
  *
  * A request outside [0, num_reqs) (QSA_DERR_REQUEST), an entry past the table
@@ -152,7 +153,8 @@ QSA_API size_t qsa_paged_attention_workspace_bytes(const qsa_paged_cache* cache,
  *   next_n        1 .. QSA_CACHE_MAX_NEXT
  *   scale         finite and > 0
  *   window        >= 0
- *   out           as q (strides out_strides); overlaps no input
+ *   out           as q (strides out_strides, no two elements at one address);
+ *                 overlaps no input
  *   lse           fp32 [num_reqs*next_n, num_heads] contiguous, or NULL
  *   weight_sums, weight_sums_out  fp32 [num_reqs, entry_cols], row strides
  *                 weight_sums_stride0 and weight_sums_out_stride0, both NULL or

@@ -78,6 +78,24 @@ inline bool strides_ok(const int64_t* shape, const int64_t* strides, int rank, i
   return true;
 }
 
+// Whether no two elements share an address: the strides in ascending order, each
+// passes what the smaller ones reach.  (All are at least the last dimension's
+// extent: strides_ok.)
+inline bool separate(const int64_t* shape, const int64_t* strides, int rank) {
+  __int128 reach = shape[rank - 1];      // elements that the dimensions taken so far span
+  bool taken[4] = {false, false, false, false};
+  for (int step = 0; step + 1 < rank; ++step) {
+    int next = -1;
+    for (int i = 0; i + 1 < rank; ++i)
+      if (!taken[i] && (next < 0 || strides[i] < strides[next])) next = i;
+    taken[next] = true;
+    if (shape[next] <= 1) continue;
+    if (strides[next] < reach) return false;
+    reach += (__int128)(shape[next] - 1) * strides[next];
+  }
+  return true;
+}
+
 // Bytes from the first to the last element, or -1 where that passes 2^62.
 inline int64_t extent(const int64_t* shape, const int64_t* strides, int rank, int64_t esize) {
   __int128 last = 0;
@@ -112,7 +130,8 @@ inline qsa_status check_cache(const qsa_paged_cache* c, CacheView* view, CacheSp
     return QSA_ERR_SHAPE;
   const int64_t es = dtype_size(c->dtype);
   const int64_t shape[4] = {c->num_pages, c->page_size, c->num_heads, c->head_dim};
-  if (!strides_ok(shape, c->k_strides, 4, es) || !strides_ok(shape, c->v_strides, 4, es))
+  if (!strides_ok(shape, c->k_strides, 4, es) || !strides_ok(shape, c->v_strides, 4, es) ||
+      !separate(shape, c->k_strides, 4) || !separate(shape, c->v_strides, 4))
     return QSA_ERR_STRIDE;
   if (!row_stride_ok(c->table_stride0, c->table_cols)) return QSA_ERR_STRIDE;
   const int64_t kx = extent(shape, c->k_strides, 4, es), vx = extent(shape, c->v_strides, 4, es);

@@ -201,7 +201,8 @@ extern "C" qsa_status qsa_paged_attention(
   if (!sizes_ok(*cache, next_n, num_heads)) return QSA_ERR_SHAPE;
   if (!q_strides || !out_strides) return QSA_ERR_NULL;
   const int64_t shape[3] = {R * next_n, num_heads, cache->head_dim};
-  if (!strides_ok(shape, q_strides, 3, 2) || !strides_ok(shape, out_strides, 3, 2))
+  if (!strides_ok(shape, q_strides, 3, 2) || !strides_ok(shape, out_strides, 3, 2) ||
+      !separate(shape, out_strides, 3))
     return QSA_ERR_STRIDE;
   const bool weights = weight_sums || weight_sums_out;
   const int64_t entries = cache->table_cols * cache->page_size;

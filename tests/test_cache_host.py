@@ -99,7 +99,8 @@ CACHE_REFUSALS = [
     (dict(reqs=-1), SHAPE), (dict(reqs=65536), SHAPE), (dict(cols=-1), SHAPE),
     (dict(ks3=2), STRIDE), (dict(vs3=0), STRIDE), (dict(ks0=0), STRIDE), (dict(ks1=-128), STRIDE),
     (dict(ks2=65), STRIDE), (dict(vs1=132), STRIDE), (dict(vs0=1 << 39), STRIDE),
-    (dict(bts0=7), STRIDE), (dict(bts0=1 << 39), STRIDE),
+    (dict(ks1=64), STRIDE), (dict(ks0=1024), STRIDE), (dict(vs2=128), STRIDE),
+    (dict(ks2=1024, ks1=64, ks0=1024), STRIDE), (dict(bts0=7), STRIDE), (dict(bts0=1 << 39), STRIDE),
     (dict(k=0), NULL), (dict(v=0), NULL), (dict(bt=0), NULL),
     (dict(k=_addr(1) + 8), ALIGN), (dict(v=_addr(2) + 2), ALIGN), (dict(bt=_addr(3) + 2), ALIGN),
 ]
@@ -149,7 +150,8 @@ def test_append_without_tokens_is_a_noop(lib):
     (dict(qs=None), NULL), (dict(os=None), NULL), (dict(q=None), NULL), (dict(out=None), NULL),
     (dict(ctx=None), NULL), (dict(win=None, bytes=1 << 40), NULL), (dict(wout=None), NULL),
     (dict(qs=_arr(256, 64, 2)), STRIDE), (dict(qs=_arr(0, 64, 1)), STRIDE),
-    (dict(os=_arr(256, 4, 1)), STRIDE), (dict(ws0=127), STRIDE), (dict(wos0=1 << 39), STRIDE),
+    (dict(os=_arr(256, 4, 1)), STRIDE), (dict(os=_arr(64, 64, 1)), STRIDE),
+    (dict(os=_arr(192, 64, 1)), STRIDE), (dict(ws0=127), STRIDE), (dict(wos0=1 << 39), STRIDE),
     (dict(q=_addr(10) + 8), ALIGN), (dict(out=_addr(12) + 8), ALIGN), (dict(ctx=_addr(11) + 2), ALIGN),
     (dict(lse=_addr(13) + 1), ALIGN), (dict(work=_addr(16) + 16), ALIGN), (dict(err=_addr(17) + 1), ALIGN),
     (dict(work=None), WORKSPACE), (dict(bytes=100), WORKSPACE),

@@ -385,6 +385,91 @@ def test_attention_other_streams_threads_and_graphs():
     assert torch.equal(outs[0], new)
 
 
+def test_calls_in_a_row_see_what_was_written_before_them():
+    # no host wait between steps that rewrite, in place, what the calls read (the kernels are
+    # launched while their predecessor drains): every step as if it had run alone
+    gen = torch.Generator(device=DEV).manual_seed(17)
+    for lens, cols in (([2000, 70, 900], 64), ([30, 5, 20], 1), ([900, 3], 30)):
+        c = Case(lens, 8, 2, 128, 32, F16, seed=18, cols=cols)
+        n = len(lens)
+        steps = 12
+        qs = _values((steps, *c.q.shape), F16, gen)
+        nks = _values((steps, n, 2, 128), F16, gen)
+        ctxs = torch.stack([c.ctx - 5 * i if i % 3 else c.ctx for i in range(steps)]).clamp(min=1)
+        t2r = torch.arange(n, dtype=torch.int32, device=DEV)
+        sums = torch.zeros((n, cols * 32), device=DEV)
+        pos = torch.arange(cols * 32, dtype=torch.int32, device=DEV).repeat(n, 1)
+        k0, v0 = c.k.clone(), c.v.clone()
+
+        def step(i, wait):
+            c.q.copy_(qs[i])
+            c.ctx.copy_(ctxs[i])
+            if wait:
+                torch.cuda.synchronize()
+            qsa.qsa_paged_append(nks[i], nks[i], c.k, c.v, c.tables, t2r, c.ctx.long() - 1,
+                                 weight_sums=sums, entry_positions=pos)
+            if wait:
+                torch.cuda.synchronize()
+            out = qsa.qsa_paged_attention(c.q, c.k, c.v, c.tables, c.ctx, weight_sums=sums,
+                                          weight_sums_out=sums)
+            if wait:
+                torch.cuda.synchronize()
+            return [out, *qsa.qsa_evict_entries(sums, pos, c.ctx, c.k, c.v, c.tables, 16)]
+
+        def run(wait):
+            c.k.copy_(k0)
+            c.v.copy_(v0)
+            sums.zero_()
+            return [[t.clone() for t in step(i, wait)] for i in range(steps)]
+
+        alone = run(True)
+        for got, want in zip(run(False), alone):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+_FIRST_IN_A_GRAPH = """
+import torch
+import sparse_paged_attention_qsa_gb300 as qsa
+torch.manual_seed(0)
+k, v = torch.randn((2, 80, 64, 2, 128), device="cuda").half()
+tables = torch.randperm(80, device="cuda").to(torch.int32).view(2, 40)
+ctx = torch.tensor([2500, 700], dtype=torch.int32, device="cuda")
+q = torch.randn((2, 8, 128), device="cuda").half()
+sums = torch.rand((2, 2560), device="cuda")
+added = torch.zeros_like(sums)
+pos = torch.arange(2560, dtype=torch.int32, device="cuda").repeat(2, 1)
+t2r = torch.arange(2, dtype=torch.int32, device="cuda")
+def step(k, v):
+    qsa.qsa_paged_append(q[:, :2], q[:, 2:4], k, v, tables, t2r, ctx.long() - 1)
+    out = qsa.qsa_paged_attention(q, k, v, tables, ctx, weight_sums=sums, weight_sums_out=added)
+    return [out, added, *qsa.qsa_evict_entries(sums, pos, ctx, k, v, tables, 600, num_sink=2)]
+kg, vg = k.clone(), v.clone()
+torch.cuda.synchronize()
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.stream(s):
+    with torch.cuda.graph(g, stream=s):
+        got = step(kg, vg)
+torch.cuda.synchronize()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+want = step(k, v)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert torch.equal(k, kg) and torch.equal(v, vg)
+"""
+
+
+def test_first_calls_inside_a_graph_capture():
+    # a fresh process whose first calls (the kernels' one-time set-up) are captured
+    import subprocess
+    import sys
+    root = __file__.rsplit("/tests/", 1)[0]
+    r = subprocess.run([sys.executable, "-c", _FIRST_IN_A_GRAPH], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
+
+
 # --- append ------------------------------------------------------------------------
 
 
