@@ -71,36 +71,57 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 constexpr int kMovePieces = 8;            // 16-byte pieces of a lane in flight
 
-// A warp copies one entry's K and V, its lanes sharing the 16-byte pieces.
-__device__ __forceinline__ void move_entry(const CacheView& c, int head_log2, int64_t page_from,
-                                           int from, int64_t page_to, int to) {
+// A warp copies the K and V of up to 32 entries, one a lane (`from` to `to`; the
+// same number twice: nothing to do), the lanes sharing the 16-byte pieces of
+// each; up to kMovePieces blocks of 32 pieces, of one entry or of several, are in
+// flight at once.
+__device__ __forceinline__ void move_entries(const CacheView& c, const int32_t* bt, int head_log2,
+                                             int from, int to, uint32_t* err) {
   const int lane = threadIdx.x & 31;
   const int row = c.heads << head_log2;                    // pieces of an entry's K
   const int slot_mask = (1 << c.page_log2) - 1;
-  const int64_t sf = from & slot_mask, st = to & slot_mask;
-  const unsigned char* kf = c.k + page_from * c.k_page + sf * c.k_token;
-  const unsigned char* vf = c.v + page_from * c.v_page + sf * c.v_token;
-  const int64_t k_to = (page_to - page_from) * c.k_page + (st - sf) * c.k_token;
-  const int64_t v_to = (page_to - page_from) * c.v_page + (st - sf) * c.v_token;
-  const auto source = [&](int i) {
-    const bool is_v = i >= row;
-    const int u = is_v ? i - row : i, h = u >> head_log2, o = u & ((1 << head_log2) - 1);
-    return (is_v ? vf + h * c.v_head : kf + h * c.k_head) + o * 16;
-  };
-  for (int i0 = 0; i0 < 2 * row; i0 += 32 * kMovePieces) {
+  const bool moves = from != to;
+  int32_t page_from = -1, page_to = -1;
+  if (moves) {
+    page_from = bt[from >> c.page_log2];
+    page_to = bt[to >> c.page_log2];
+  }
+  const bool fine = moves && page_from >= 0 && page_from < c.num_pages && page_to >= 0 &&
+                    page_to < c.num_pages;
+  if (moves && !fine) report(err, QSA_DERR_KV_PAGE);
+  uint32_t todo = __ballot_sync(0xffffffffu, fine);
+  int f = 0, t = 0;                                        // the entry at hand
+  int64_t pf = 0, pt = 0;
+  int i0 = 2 * row;                                        // its next block
+  while (todo != 0 || i0 < 2 * row) {
     uint4 x[kMovePieces];
+    unsigned char* dst[kMovePieces];
 #pragma unroll
     for (int j = 0; j < kMovePieces; ++j) {
-      const int i = i0 + j * 32 + lane;
-      if (i < 2 * row) x[j] = *reinterpret_cast<const uint4*>(source(i));
+      dst[j] = nullptr;
+      if (i0 >= 2 * row && todo != 0) {
+        const int who = __ffs(todo) - 1;
+        todo &= todo - 1;
+        f = __shfl_sync(0xffffffffu, from, who);
+        t = __shfl_sync(0xffffffffu, to, who);
+        pf = __shfl_sync(0xffffffffu, page_from, who);
+        pt = __shfl_sync(0xffffffffu, page_to, who);
+        i0 = 0;
+      }
+      const int i = i0 + lane;
+      if (i < 2 * row) {
+        const bool is_v = i >= row;
+        const int u = is_v ? i - row : i, h = u >> head_log2, o = u & ((1 << head_log2) - 1);
+        unsigned char* at = (is_v ? c.v + h * c.v_head : c.k + h * c.k_head) + o * 16;
+        const int64_t ps = is_v ? c.v_page : c.k_page, ts = is_v ? c.v_token : c.k_token;
+        x[j] = *reinterpret_cast<const uint4*>(at + pf * ps + (f & slot_mask) * ts);
+        dst[j] = at + pt * ps + (t & slot_mask) * ts;
+      }
+      if (i0 < 2 * row) i0 += 32;
     }
 #pragma unroll
-    for (int j = 0; j < kMovePieces; ++j) {
-      const int i = i0 + j * 32 + lane;
-      if (i < 2 * row)
-        *reinterpret_cast<uint4*>(const_cast<unsigned char*>(source(i)) + (i >= row ? v_to : k_to)) =
-            x[j];
-    }
+    for (int j = 0; j < kMovePieces; ++j)
+      if (dst[j]) *reinterpret_cast<uint4*>(dst[j]) = x[j];
   }
 }
 
@@ -460,13 +481,12 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
     if (p.move_here) {
       __syncthreads();
       const int32_t* bt = p.c.bt + (int64_t)b * p.c.bt_s0;
-      for (int i = warp; i < end - begin; i += kRankWarps) {
-        const int from = (int)s_key[2 * i], to = (int)s_key[2 * i + 1];
-        const int32_t pf = bt[from >> p.c.page_log2], pt = bt[to >> p.c.page_log2];
-        if (pf >= 0 && pf < p.c.num_pages && pt >= 0 && pt < p.c.num_pages)
-          move_entry(p.c, p.head_log2, pf, from, pt, to);
-        else if (lane == 0)
-          report(p.err, QSA_DERR_KV_PAGE);
+      // neighbouring pairs to different warps
+      for (int i0 = warp; i0 < end - begin; i0 += 32 * kRankWarps) {
+        const int i = i0 + lane * kRankWarps;
+        const bool there = i < end - begin;
+        move_entries(p.c, bt, p.head_log2, there ? (int)s_key[2 * i] : 0,
+                     there ? (int)s_key[2 * i + 1] : 0, p.err);
       }
     }
     sync_all();                          // no CTA leaves while another reads its shared memory
@@ -509,23 +529,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
   // moves is spread over the warps
   for (int i0 = warp; i0 < p.budget; i0 += 32 * stride) {
     const int mine = i0 + lane * stride;
-    int src = mine < p.budget ? kept[mine] : -1;
-    int32_t page_f = -1, page_t = -1;
-    const bool moves = src >= 0 && src != mine;
-    if (moves) {
-      page_f = bt[src >> p.c.page_log2];
-      page_t = bt[mine >> p.c.page_log2];
-    }
-    const bool fine = moves && page_f >= 0 && page_f < p.c.num_pages && page_t >= 0 &&
-                      page_t < p.c.num_pages;
-    if (moves && !fine) report(p.err, QSA_DERR_KV_PAGE);
-    for (uint32_t todo = __ballot_sync(0xffffffffu, fine); todo; todo &= todo - 1) {
-      const int who = __ffs(todo) - 1;
-      const int from = __shfl_sync(0xffffffffu, src, who), to = __shfl_sync(0xffffffffu, mine, who);
-      const int pf = __shfl_sync(0xffffffffu, page_f, who);
-      const int pt = __shfl_sync(0xffffffffu, page_t, who);
-      move_entry(p.c, p.head_log2, pf, from, pt, to);
-    }
+    const int src = mine < p.budget ? kept[mine] : -1;     // -1: behind the end
+    move_entries(p.c, bt, p.head_log2, src < 0 ? 0 : src, src < 0 ? 0 : mine, p.err);
   }
 }
 
@@ -560,14 +565,16 @@ cudaError_t evict_device(int* n_sms) {
 }
 
 // CTAs of a request's cluster: as many as leave every request a cluster of its
-// own, with at least kMinSlice entries each (16 requests of up to 65536 entries:
-// 132, 76, 31 and 31 us with 1, 2, 4 and 8 CTAs, where slices of 65536 and
-// 32768 do not fit in shared memory; 64 of 2064: 8.8 us with 1, 10.5 with 2).
-constexpr int64_t kMinSlice = 4096;
+// own, with at least kMinSlice entries each (16 requests of up to 65536 entries
+// took 132, 76, 31 and 31 us with 1, 2, 4 and 8 CTAs, where slices of 65536 and
+// 32768 do not fit in shared memory; with a slice of 4096 at least 8 requests of
+// 16384 take 62.7 us, with 2048 or less 59.8, but 64 of 2064 9.6 and 10.9).
+constexpr int64_t kMinSlice = 2048;
 
-// Bytes that the rank kernel's CTA moves itself: about what it does in the time
-// of a second launch.
-constexpr int64_t kMoveHereBytes = 512 << 10;
+// Bytes that the rank kernel's CTAs move themselves for a request: more are
+// sooner moved by a kernel over the whole GPU (16 entries of 4 KB in each of 64
+// requests: 9.6 us against 13.0; 515 of 512 bytes in 3: 16.9 against 8.7).
+constexpr int64_t kMoveHereBytes = 64 << 10;
 
 // `most` entries can move in a request; *moved says whether they have been.
 cudaError_t launch_rank(EvictParams& p, int reqs, int64_t most, int sms, cudaStream_t st,

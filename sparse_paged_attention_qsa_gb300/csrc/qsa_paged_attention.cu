@@ -29,7 +29,7 @@
 namespace qsa {
 namespace {
 
-constexpr int kWeightThreads = 128;
+constexpr int kWeightParts = 16;          // warps of a CTA, at most
 
 #ifdef QSA_WAIT_TEST
 int32_t g_test_withhold = -1;
@@ -49,45 +49,49 @@ struct WeightParams {
 };
 
 // A lane holds four entries of one request (the table's entries are a multiple
-// of 8), a warp a part of the heads, so that their logits are all in flight at
-// once; the parts are added in warp order.
-__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightParams p) {
-  constexpr int kParts = kWeightThreads / 32;
-  __shared__ float4 s_part[kParts][32];
+// of 8), a warp a part of the (row, head) pairs, so that their logits are all in
+// flight at once; the parts are added in warp order.
+__global__ void __launch_bounds__(kWeightParts * 32) weights_kernel(const WeightParams p) {
+  __shared__ float4 s_part[kWeightParts][32];
   const int b = blockIdx.y, lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int parts = blockDim.x >> 5;
   const int e = ((int)blockIdx.x * 32 + lane) * 4;
   pdl_wait();          // on every path: the grid's end must mean the walk's and the join's
   const int64_t ctx = p.ctx[b];
   const int n = (int)min(ctx, (int64_t)p.cap);
   if ((int)blockIdx.x * 128 >= n) return;
-  const int per = (p.heads + kParts - 1) / kParts;
-  const int h0 = part * per, h1 = min(p.heads, h0 + per);
+  const int pairs = p.next_n * p.heads, per = (pairs + parts - 1) / parts;
+  const int x0 = part * per, x1 = min(pairs, x0 + per);
+  const int64_t first = (int64_t)b * pairs;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < p.next_n; ++j) {
+  int j = x0 / p.heads, left = (j + 1) * p.heads - x0;     // pairs of token j still to come
+  for (int x = x0; x < x1;) {
     const int64_t hi = ctx - p.next_n + j + 1;
     const int64_t lo = p.window > 0 ? max((int64_t)0, hi - p.window) : 0;
-    if (e + 3 < lo || e >= hi || e >= n) continue;
-    const int64_t r0 = ((int64_t)b * p.next_n + j) * p.heads;
-    const bool in[4] = {e >= lo, e + 1 >= lo && e + 1 < hi, e + 2 >= lo && e + 2 < hi,
-                        e + 3 >= lo && e + 3 < hi};
+    const int end = min(x1, x + left);
+    if (e + 3 >= lo && e < min(hi, (int64_t)n)) {
+      const bool in[4] = {e >= lo, e + 1 >= lo && e + 1 < hi, e + 2 >= lo && e + 2 < hi,
+                          e + 3 >= lo && e + 3 < hi};
 #pragma unroll 8
-    for (int h = h0; h < h1; ++h) {
-      const float4 z = *reinterpret_cast<const float4*>(p.z + (r0 + h) * p.pitch + e);
-      const float l = p.lse2[r0 + h];
-      // -inf (an absent entry): 0, also where the row saw nothing and l is -inf
-      s.x += in[0] && z.x != -INFINITY ? exp2f(z.x - l) : 0.f;
-      s.y += in[1] && z.y != -INFINITY ? exp2f(z.y - l) : 0.f;
-      s.z += in[2] && z.z != -INFINITY ? exp2f(z.z - l) : 0.f;
-      s.w += in[3] && z.w != -INFINITY ? exp2f(z.w - l) : 0.f;
+      for (int y = x; y < end; ++y) {
+        const float4 z = *reinterpret_cast<const float4*>(p.z + (first + y) * p.pitch + e);
+        const float l = p.lse2[first + y];
+        // -inf (an absent entry): 0, also where the row saw nothing and l is -inf
+        s.x += in[0] && z.x != -INFINITY ? exp2f(z.x - l) : 0.f;
+        s.y += in[1] && z.y != -INFINITY ? exp2f(z.y - l) : 0.f;
+        s.z += in[2] && z.z != -INFINITY ? exp2f(z.z - l) : 0.f;
+        s.w += in[3] && z.w != -INFINITY ? exp2f(z.w - l) : 0.f;
+      }
     }
+    x = end;
+    ++j;
+    left = p.heads;
   }
   s_part[part][lane] = s;
   __syncthreads();
-  if (e + part < n) {                    // warp i: the i-th entry of each four
-    static_assert(kParts == 4, "a warp an entry of four");
+  if (part < 4 && e + part < n) {        // warp i: the i-th entry of each four
     float v = 0.f;
-#pragma unroll
-    for (int k = 0; k < kParts; ++k) v += reinterpret_cast<const float*>(&s_part[k][lane])[part];
+    for (int k = 0; k < parts; ++k) v += reinterpret_cast<const float*>(&s_part[k][lane])[part];
     p.sums_out[b * p.sums_out_s0 + e + part] = p.sums[b * p.sums_s0 + e + part] + v;
   }
 }
@@ -308,7 +312,10 @@ extern "C" qsa_status qsa_paged_attention(
     wp.sums_out_s0 = weight_sums_out_stride0;
     const int64_t per_cta = 128;
     const dim3 grid((unsigned)((entries + per_cta - 1) / per_cta), (unsigned)R);
-    if (launch_after(weights_kernel, grid, dim3(kWeightThreads), 0, s, wp) != cudaSuccess)
+    // eight pairs a warp; four warps at least, one for each entry of a lane's
+    const int pairs = p.next_n * p.heads;
+    const int parts = std::max(4, std::min(kWeightParts, (pairs + 7) / 8));
+    if (launch_after(weights_kernel, grid, dim3(parts * 32), 0, s, wp) != cudaSuccess)
       return QSA_ERR_CUDA;
   }
   return QSA_OK;

@@ -711,9 +711,15 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                 pl[s][2 * n + k] = pack2<kBf16>(p0 - f.x, p1 - f.y);
               }
             }
-        // P V.  Where some entry is hidden from some row, 0 times what it holds
-        // may be NaN: V enters with the hidden entries zeroed, once for each
-        // token j that has rows here, and only those rows take the result.
+        // P V.  Where an entry is hidden, 0 times what it holds may be NaN: in an
+        // edge tile V enters with the entries zeroed that not all of the warp's
+        // rows see; those that some see, a few at each end, are added one by one
+        // to the rows that see them.
+        int32_t lo_a = 0, hi_a = 0, lo_b = 0, hi_b = 0;    // of the first and the last row's token
+        if (edge) {
+          visible(p, ctx, token_of(wm * 16), &lo_a, &hi_a);
+          visible(p, ctx, token_of(wm * 16 + 15), &lo_b, &hi_b);
+        }
         wait_full();
 #pragma unroll
         for (int ch = 0; ch < W::kChunks; ++ch) {
@@ -747,50 +753,89 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                 }
               }
           } else {
-            const int ja = token_of(wm * 16), jb = token_of(wm * 16 + 15);
-            for (int j = ja; j <= jb; ++j) {
-              int32_t lo, hi;
-              visible(p, ctx, j, &lo, &hi);
-              bool mine[2];
 #pragma unroll
-              for (int k = 0; k < 2; ++k) mine[k] = token_of(row_of(k)) == j;
+            for (int st = 0; st < NS; ++st) {
+              uint32_t keep[2];
 #pragma unroll
-              for (int st = 0; st < NS; ++st) {
-                uint32_t keep[2];
+              for (int n = 0; n < 2; ++n) {
+                const int32_t e = we + st * 16 + n * 8 + 2 * q4;
+                const bool in = (mask >> ((e - e0) >> box_log2)) & 1u;
+                keep[n] = (in && e >= lo_b && e < hi_a ? 0xffffu : 0u) |
+                          (in && e + 1 >= lo_b && e + 1 < hi_a ? 0xffff0000u : 0u);
+              }
+              const auto add = [&](int n, uint32_t b0, uint32_t b1) {
+                mma16816<kBf16>(o[n], ph[st], b0 & keep[0], b1 & keep[1]);
+                if constexpr (W::kPair) mma16816<kBf16>(o[n], pl[st], b0 & keep[0], b1 & keep[1]);
+              };
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                  const int32_t e = we + st * 16 + n * 8 + 2 * q4;
-                  const bool in = (mask >> ((e - e0) >> box_log2)) & 1u;
-                  keep[n] = (in && e >= lo && e < hi ? 0xffffu : 0u) |
-                            (in && e + 1 >= lo && e + 1 < hi ? 0xffff0000u : 0u);
+              for (int i = 0; i < kPer / 2; ++i) {
+                uint32_t b[4];
+                ldsm4t(vb + piece(v_row + st * 16, 2 * i + v_c), b);
+                if constexpr (!kFp8) {
+                  add(ch * kTiles + 2 * i, b[0], b[1]);
+                  add(ch * kTiles + 2 * i + 1, b[2], b[3]);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) b[k] = __byte_perm(b[k], 0, 0x3120);
+                  const int n = ch * kTiles + 4 * i;
+                  add(n, e4m3_lo(b[0]), e4m3_lo(b[1]));
+                  add(n + 1, e4m3_hi(b[0]), e4m3_hi(b[1]));
+                  add(n + 2, e4m3_lo(b[2]), e4m3_lo(b[3]));
+                  add(n + 3, e4m3_hi(b[2]), e4m3_hi(b[3]));
                 }
-                const auto add = [&](int n, uint32_t b0, uint32_t b1) {
-                  float d[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma16816<kBf16>(d, ph[st], b0 & keep[0], b1 & keep[1]);
-                  if constexpr (W::kPair) mma16816<kBf16>(d, pl[st], b0 & keep[0], b1 & keep[1]);
+              }
+            }
+          }
+        }
+        if (edge && (lo_a != lo_b || hi_a != hi_b)) {
+          int32_t lo[2], hi[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) visible(p, ctx, token_of(row_of(k)), &lo[k], &hi[k]);
+          // [lo_a, mid) and [from, hi_b): what some rows see and not all
+          const int32_t mid = min(lo_b, hi_b), from = max(hi_a, mid);
+#pragma unroll
+          for (int st = 0; st < NS; ++st) {
+            const int32_t t0 = we + st * 16, t1 = t0 + 16;
+            for (int32_t e = max(lo_a, t0); e < min(hi_b, t1); ++e) {
+              if (e >= mid && e < from) {                  // all rows see it
+                e = from - 1;
+                continue;
+              }
+              if (!((mask >> ((e - e0) >> box_log2)) & 1u)) continue;
+              const int at = e - t0, owner = (lane & 28) | (at & 7) >> 1, upper = at >> 3;
+              float w[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t h = __shfl_sync(0xffffffffu, upper ? ph[st][2 + k] : ph[st][k], owner);
+                const float2 f = unpack2<kBf16>(h);
+                w[k] = at & 1 ? f.y : f.x;
+                if constexpr (W::kPair) {
+                  const uint32_t r = __shfl_sync(0xffffffffu, upper ? pl[st][2 + k] : pl[st][k], owner);
+                  const float2 d = unpack2<kBf16>(r);
+                  w[k] += at & 1 ? d.y : d.x;
+                }
+              }
+              const int row = e - e0, rsw = W::kChunkBytes == 128 ? row & 7 : (row >> 1) & 3;
+              const bool sees[2] = {e >= lo[0] && e < hi[0], e >= lo[1] && e < hi[1]};
+              const unsigned char* v = base + slot * W::kSlot + row * W::kChunkBytes + q4 * 4;
+#pragma unroll
+              for (int c = 0; c < W::kRowBytes / 16; ++c) {  // four bytes of each 16-byte piece
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(
+                    v + (c / kPer) * (TT * W::kChunkBytes) + (((c % kPer) ^ rsw) << 4));
+                const auto add = [&](float (&acc)[4], float2 f) {
 #pragma unroll
                   for (int k = 0; k < 2; ++k)
-                    if (mine[k]) {
-                      o[n][2 * k] += d[2 * k];
-                      o[n][2 * k + 1] += d[2 * k + 1];
+                    if (sees[k]) {
+                      acc[2 * k] = fmaf(w[k], f.x, acc[2 * k]);
+                      acc[2 * k + 1] = fmaf(w[k], f.y, acc[2 * k + 1]);
                     }
                 };
-#pragma unroll
-                for (int i = 0; i < kPer / 2; ++i) {
-                  uint32_t b[4];
-                  ldsm4t(vb + piece(v_row + st * 16, 2 * i + v_c), b);
-                  if constexpr (!kFp8) {
-                    add(ch * kTiles + 2 * i, b[0], b[1]);
-                    add(ch * kTiles + 2 * i + 1, b[2], b[3]);
-                  } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) b[k] = __byte_perm(b[k], 0, 0x3120);
-                    const int n = ch * kTiles + 4 * i;
-                    add(n, e4m3_lo(b[0]), e4m3_lo(b[1]));
-                    add(n + 1, e4m3_hi(b[0]), e4m3_hi(b[1]));
-                    add(n + 2, e4m3_lo(b[2]), e4m3_lo(b[3]));
-                    add(n + 3, e4m3_hi(b[2]), e4m3_hi(b[3]));
-                  }
+                if constexpr (!kFp8) {
+                  add(o[c], unpack2<kBf16>(x));
+                } else {                                   // even and odd dims
+                  const uint32_t y = __byte_perm(x, 0, 0x3120);
+                  add(o[2 * c], h2f2(e4m3_lo(y)));
+                  add(o[2 * c + 1], h2f2(e4m3_hi(y)));
                 }
               }
             }
