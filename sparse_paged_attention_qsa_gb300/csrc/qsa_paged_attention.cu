@@ -256,7 +256,8 @@ extern "C" qsa_status qsa_paged_attention(
   p.chunks = (p.rows + kPagedMaxRows - 1) / kPagedMaxRows;
   p.chunk_rows = std::min(p.rows, kPagedMaxRows);
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  p.window = window;
+  // a window past every capacity (2^30 at most) hides nothing, whatever it is
+  p.window = (int32_t)std::min<int64_t>(window, INT32_MAX - 16);
   p.lse = lse;
   unsigned char* w = static_cast<unsigned char*>(workspace);
   p.mode = l.mode;

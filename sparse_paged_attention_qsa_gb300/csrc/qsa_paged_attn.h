@@ -42,7 +42,7 @@ struct PagedParams {
   int32_t chunk_rows;         // rows of a full chunk
   int32_t mode;               // a PagedMode
   float scale_log2;           // scale * log2(e)
-  int64_t window;
+  int32_t window;             // 0: none; at most INT32_MAX - 16
   float* lse;                 // nullable
   float* lse2;                // workspace: [rows][heads] log2 sums, or null
   float* z;                   // workspace: [rows][heads][z_pitch] logits (base 2), or null

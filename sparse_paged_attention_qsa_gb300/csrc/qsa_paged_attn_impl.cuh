@@ -61,10 +61,11 @@ constexpr int kSmemPerSm = 233472, kSmemReserved = 1024;   // 228 KB, 1 KB of it
 struct WalkTables {
   uint64_t full[kMaxSlots], empty[kMaxSlots];   // mbarriers of the ring
   uint64_t q_full[2], q_empty[2];               // and of the two query slots
-  uint32_t boxes[kMaxSlots];                    // the slot's copies that found a page
+  uint32_t boxes[kMaxSlots];                    // a bit per copy, 0: it had no page
   float ml[8][16][2];                            // maximum and sum of the warps' rows
   float qs[kPagedMaxRows];                      // what the queries were divided by
-  int32_t scan[9 * 32];
+  int32_t scan[12];                             // tiles of the requests of each warp
+  uint8_t token[kPagedMaxRows];                 // the row's token of the draft
   int32_t ctx[kPagedBatch];                     // cached tokens of each request
   int32_t pre[kPagedBatch + 1];                 // tiles before each
   int32_t abort;
@@ -96,7 +97,12 @@ struct WalkShape {
       1024 + kQSlots * kQBytes + kMergeBytes + kPieceBytes + (int)sizeof(WalkTables);
   static constexpr int kCtas = kCluster ? 1 : paged_ctas(D, WM);
   static constexpr int kFit = (kSmemPerSm / kCtas - kSmemReserved - kFixed) / kSlot;
-  static constexpr int S = kFit < kMaxSlots ? kFit : kMaxSlots;
+  // two CTAs keep four tiles each on their way; a fifth was slower (FP16 heads of
+  // 64 236 us against 229, E4M3 128 against 121, heads of 128 with weights 241
+  // against 228) and three no better (234, 126, 227); one CTA takes what fits
+  // (heads of 256 602 us with four, 597 with five)
+  static constexpr int kMost = kCtas == 2 ? 4 : kMaxSlots;
+  static constexpr int S = kFit < kMost ? kFit : kMost;
   static constexpr size_t kSmem = (size_t)kFixed + (size_t)S * kSlot;
   static_assert(S >= 3, "the ring needs K, V and one slot ahead");
   static_assert(NS >= 1 && NS <= 4, "logits of a tile stay in registers");
@@ -169,11 +175,11 @@ __device__ __forceinline__ void consumers_sync() {
 // cut to what the table holds.
 __device__ __forceinline__ void visible(const PagedParams& p, int32_t ctx, int j, int32_t* lo,
                                         int32_t* hi) {
-  const int64_t h = (int64_t)ctx - p.next_n + j + 1;
-  const int64_t l = p.window > 0 ? h - p.window : 0;
-  const int64_t cap = p.c.cap;
-  *hi = (int32_t)(h < 0 ? 0 : h < cap ? h : cap);
-  *lo = (int32_t)(l < 0 ? 0 : l < cap ? l : cap);
+  // 32 bits hold it all: h >= -7, and the window is at most INT32_MAX - 16
+  const int32_t cap = (int32_t)p.c.cap;
+  const int32_t h = max(ctx, 0) - p.next_n + j + 1;
+  *hi = min(max(h, 0), cap);
+  *lo = p.window > 0 ? min(max(h - p.window, 0), cap) : 0;
 }
 
 // The tiles a request's entries span, [*first, *first + count).
@@ -245,6 +251,16 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   volatile int32_t* s_abort = &tb.abort;
   int32_t* pre = tb.pre;
 
+  // CTA: run * units + unit, so that the K/V heads of the same tokens, whose
+  // elements lie side by side, are read at the same time; a cluster's are the
+  // runs of one unit
+  const int units = p.c.heads * p.chunks, n_runs = gridDim.x / units;
+  const int run = kCluster ? blockIdx.x % n_runs : blockIdx.x / units;
+  const int unit = kCluster ? blockIdx.x / n_runs : blockIdx.x % units;
+  const int head = unit / p.chunks, chunk = unit - head * p.chunks;
+  const int row0 = chunk * kPagedMaxRows;
+  const int n_rows = min(kPagedMaxRows, p.rows - row0);    // query rows of this unit
+
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(bar_full + 8 * s, 1);
@@ -275,13 +291,21 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       pre[b + 1] = n;
       sum += n;
     }
-    tb.scan[tid] = sum;
+    int32_t upto = sum;                                    // of this warp's threads to here
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, upto, k);
+      if (lane >= k) upto += v;
+    }
+    if (lane == 31) tb.scan[warp] = upto;
+    for (int i = tid; i < kPagedMaxRows; i += W::kThreads)
+      tb.token[i] = (uint8_t)(min(row0 + i, p.rows - 1) / p.group);
     // the zeros above were written through the generic proxy, copies follow
     // through the async one
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    int32_t before = 0;
-    for (int i = 0; i < (lo < hi ? tid : 0); ++i) before += tb.scan[i];
+    int32_t before = upto - sum;
+    for (int i = 0; i < warp; ++i) before += tb.scan[i];
     for (int b = lo; b < hi; ++b) {
       before += pre[b + 1];
       pre[b + 1] = before;
@@ -289,13 +313,6 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     if (tid == 0) pre[0] = 0;
     __syncthreads();
   }
-  // CTA: run * units + unit, so that the K/V heads of the same tokens, whose
-  // elements lie side by side, are read at the same time; a cluster's are the
-  // runs of one unit
-  const int units = p.c.heads * p.chunks, n_runs = gridDim.x / units;
-  const int run = kCluster ? blockIdx.x % n_runs : blockIdx.x / units;
-  const int unit = kCluster ? blockIdx.x / n_runs : blockIdx.x % units;
-  const int head = unit / p.chunks, chunk = unit - head * p.chunks;
   const Runs runs = cut_runs(pre[p.batch], n_runs);
   int32_t w_begin = run_start(runs, run), w_end = run_start(runs, run + 1);
   if (!kCluster && p.mode == kPagedWhole) {   // on to the next request's first tile
@@ -315,10 +332,8 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     p.starts[run] = make_int4(at.b, at.tile, at.count, runs.total);
   }
 
-  const int row0 = chunk * kPagedMaxRows;
-  const int n_rows = min(kPagedMaxRows, p.rows - row0);    // query rows of this unit
   const auto row_ptr = [&](const unsigned char* t, int64_t rs, int64_t hs, int b, int i) {
-    const int r = row0 + i, j = r / p.group;
+    const int r = row0 + i, j = tb.token[i];
     return t + ((int64_t)(p.b0 + b) * p.next_n + j) * rs +
            (int64_t)(head * p.group + r - j * p.group) * hs;
   };
@@ -415,6 +430,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         const bool want = lane < n_boxes && be < hi && be + box_rows > lo;
         const bool good = want && id >= 0 && id < p.c.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, good);
+        const uint32_t unseen = ~__ballot_sync(0xffffffffu, want);   // and not asked about
         if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -429,7 +445,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
 #endif
           {
             if (lane == 0) {
-              tb.boxes[s] = mask;
+              tb.boxes[s] = mask | unseen;
               mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * W::kRowBytes));
             }
             __syncwarp();
@@ -459,7 +475,6 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
     const int g = lane >> 2, q4 = lane & 3;
     const int lg = p.c.page_log2;
     const int box_log2 = min(lg, TT == 256 ? 8 : TT == 128 ? 7 : 6);
-    const uint32_t all_boxes = TT >> box_log2 >= 32 ? 0xffffffffu : (1u << (TT >> box_log2)) - 1u;
     // ldmatrix source rows and the swizzle's exclusive-or, constant a lane
     const int k_row = wk * W::kSlice + ((lane >> 4) << 3) + (lane & 7);       // K: tokens by 8
     const int v_row = wk * W::kSlice + (((lane >> 3) & 1) << 3) + (lane & 7); // V: transposed
@@ -572,7 +587,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
 
       // this thread's rows, k = 0 and 1
       const auto row_of = [&](int k) { return wm * 16 + g + 8 * k; };
-      const auto token_of = [&](int i) { return min(row0 + i, p.rows - 1) / p.group; };
+      const auto token_of = [&](int i) { return (int)tb.token[i]; };
       float mult[2];
       float* z_at[2];                                     // its logits' row, or null
 #pragma unroll
@@ -582,7 +597,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
           if (p.c.k_scale) mult[k] *= p.c.k_scale[head];
           mult[k] *= tb.qs[row_of(k)];
         }
-        const int r = min(row0 + row_of(k), p.rows - 1), j = r / p.group;
+        const int r = min(row0 + row_of(k), p.rows - 1), j = token_of(row_of(k));
         const int64_t rh = ((int64_t)(p.b0 + at.b) * p.next_n + j) * p.heads + head * p.group + r -
                            j * p.group;
         z_at[k] = p.z && row_of(k) < n_rows ? p.z + rh * p.z_pitch : nullptr;
@@ -596,7 +611,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         const int32_t we = e0 + wk * W::kSlice;            // the warp's first entry
         wait_full();
         const uint32_t mask = tb.boxes[slot];
-        const bool edge = e0 < lo_in || e0 + TT > hi_in || mask != all_boxes;
+        const bool edge = e0 < lo_in || e0 + TT > hi_in || mask != 0xffffffffu;
         float sc[NS][2][4];
 #pragma unroll
         for (int s = 0; s < NS; ++s)
@@ -922,7 +937,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
                 const_cast<unsigned char*>(row_ptr(p.out, p.out_row, p.out_head, at.b, i)) +
                 (c0 + c) * 2) = make_uint4(h[0], h[1], h[2], h[3]);
             if (c0 + c == 0) {
-              const int r = row0 + i, j = r / p.group;
+              const int r = row0 + i, j = token_of(i);
               const int64_t rh = ((int64_t)(p.b0 + at.b) * p.next_n + j) * p.heads +
                                  head * p.group + r - j * p.group;
               const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
@@ -976,7 +991,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
             const_cast<unsigned char*>(row_ptr(p.out, p.out_row, p.out_head, own_b, i)) + ln * 8) =
             make_uint2(pack2<kOut>(acc.x * inv, acc.y * inv), pack2<kOut>(acc.z * inv, acc.w * inv));
         if (ln == 0) {
-          const int r = row0 + i, j = r / p.group;
+          const int r = row0 + i, j = tb.token[i];
           const int64_t rh = ((int64_t)(p.b0 + own_b) * p.next_n + j) * p.heads + head * p.group +
                              r - j * p.group;
           const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
