@@ -151,7 +151,7 @@ QSA_API size_t qsa_paged_attention_workspace_bytes(const qsa_paged_cache* cache,
  *                 16-byte aligned.  num_heads: a multiple of the cache's
  *   context_lens  int32 [num_reqs]: cached tokens, the new ones included
  *   next_n        1 .. QSA_CACHE_MAX_NEXT
- *   scale         finite and > 0
+ *   scale         > 0, scale * log2(e) finite in binary32
  *   window        >= 0
  *   out           as q (strides out_strides, no two elements at one address);
  *                 overlaps no input

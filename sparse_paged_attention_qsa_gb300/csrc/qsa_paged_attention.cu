@@ -40,7 +40,7 @@ struct WeightParams {
   const float* z;             // [rows][heads][pitch] logits (base 2)
   const float* lse2;          // [rows][heads]
   int64_t pitch;
-  int64_t window;
+  int32_t window;
   int32_t cap, next_n, heads;
   const float* sums;
   int64_t sums_s0;
@@ -137,8 +137,8 @@ bool encode_view(CUtensorMap* map, const unsigned char* p, const CacheView& c, i
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 bool sizes_ok(const qsa_paged_cache& c, int64_t next_n, int64_t heads) {
-  return next_n >= 1 && next_n <= QSA_CACHE_MAX_NEXT && heads >= 1 && heads % c.num_heads == 0 &&
-         heads * next_n <= 65536;
+  return next_n >= 1 && next_n <= QSA_CACHE_MAX_NEXT && heads >= 1 && heads <= 65536 &&
+         heads % c.num_heads == 0 && heads * next_n <= 65536;
 }
 
 // The workspace: where each run starts, the pieces of K/V heads that the
@@ -200,7 +200,8 @@ extern "C" qsa_status qsa_paged_attention(
   if (st != QSA_OK) return st;
   if (dtype != QSA_DT_F16 && dtype != QSA_DT_BF16) return QSA_ERR_DTYPE;
   if (cache->dtype != QSA_DT_F8E4M3 && cache->dtype != dtype) return QSA_ERR_DTYPE;
-  if (!(std::isfinite(scale) && scale > 0.f) || window < 0) return QSA_ERR_CONTRACT;
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!(std::isfinite(scale_log2) && scale > 0.f) || window < 0) return QSA_ERR_CONTRACT;
   const int64_t R = cache->num_reqs;
   if (!sizes_ok(*cache, next_n, num_heads)) return QSA_ERR_SHAPE;
   if (!q_strides || !out_strides) return QSA_ERR_NULL;
@@ -255,7 +256,7 @@ extern "C" qsa_status qsa_paged_attention(
   p.rows = p.next_n * p.group;
   p.chunks = (p.rows + kPagedMaxRows - 1) / kPagedMaxRows;
   p.chunk_rows = std::min(p.rows, kPagedMaxRows);
-  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   // a window past every capacity (2^30 at most) hides nothing, whatever it is
   p.window = (int32_t)std::min<int64_t>(window, INT32_MAX - 16);
   p.lse = lse;
@@ -303,7 +304,7 @@ extern "C" qsa_status qsa_paged_attention(
     wp.z = p.z;
     wp.lse2 = p.lse2;
     wp.pitch = p.z_pitch;
-    wp.window = window;
+    wp.window = p.window;
     wp.cap = p.c.cap;
     wp.next_n = p.next_n;
     wp.heads = p.heads;

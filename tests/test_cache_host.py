@@ -165,6 +165,19 @@ def test_attention_refusals(lib, over, status):
     assert _attend(lib, **over) == status
 
 
+@pytest.mark.parametrize("hq", [1 << 61, 1 << 62, (1 << 63) - 2])
+def test_attention_head_counts_past_64_bits(lib, hq):
+    # heads * next_n wraps to a small number for some of these
+    assert _attend(lib, hq=hq, n=8, work=None, bytes=0) == SHAPE
+    assert lib.qsa_paged_attention_workspace_bytes(_cache({}), 8, hq, 1) == 0
+
+
+def test_attention_scales_past_binary32_are_refused(lib):
+    most = 3.4028234e38
+    assert _attend(lib, scale=most) == CONTRACT
+    assert _attend(lib, scale=most / 1.5, q=None) == NULL      # that one is not
+
+
 def test_attention_without_requests_is_a_noop(lib):
     assert _attend(lib, reqs=0, q=None, out=None, ctx=None, bytes=0, work=None) == 0
 

@@ -192,6 +192,12 @@ def test_attention_windows(window, next_n):
                seed=window), sums=True)
 
 
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 31 - 1, 2 ** 31, 2 ** 62, 2 ** 63 - 1])
+def test_attention_windows_past_every_capacity(window):
+    # contexts shorter than the draft too: rows of it see nothing
+    check(Case([1, 2, 7, 700, 0], 4, 2, 64, 16, F16, next_n=8, window=window, seed=19), sums=True)
+
+
 @pytest.mark.parametrize("lens", [[1], [0], [0, 0, 0], [64] * 40, list(range(0, 130, 7)),
                                   [4000, 1, 1, 1, 0, 3999], [20000]])
 def test_attention_ragged_batches(lens):
