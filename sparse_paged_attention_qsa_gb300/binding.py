@@ -611,11 +611,13 @@ def _rows(t, dtype, reqs, what):
     if t is None:
         return 0, 0
     p = _typed(t, dtype, 2, what)
-    if t.shape[0] != reqs:
+    n, cols = t.shape
+    s0, s1 = t.stride()
+    if n != reqs:
         raise QSAError(3, f"{what} needs one row per request")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    if s1 != 1 and cols > 1:
         raise QSAError(4, f"{what} columns must be contiguous")
-    return p, t.stride(0) if reqs > 1 else max(t.stride(0), t.shape[1])
+    return p, s0 if reqs > 1 else max(s0, cols)
 
 
 def _word(t) -> int:
@@ -642,6 +644,8 @@ def _on_stream(stream, device_index):
 
 
 _HERE = contextlib.nullcontext()
+_raw_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc if torch.version.cuda else None
+_raw_free = torch._C._cuda_cudaCachingAllocator_raw_delete if torch.version.cuda else None
 
 
 def _need_tensor(t, what):
@@ -712,12 +716,12 @@ def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next
     weights = weight_sums is not None or weight_sums_out is not None
     need = lib.qsa_paged_attention_workspace_bytes(cache, next_n, heads, weights) \
         if workspace is None else 0
-    if out is None or need:
-        with _on_stream(stream, device):
-            if out is None:
+    if out is None:
+        if stream is None:
+            out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
+        else:
+            with _on_stream(stream, device):
                 out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
-            if need:
-                workspace = _workspace(need, q.device)
     if out.dtype != q.dtype:
         raise QSAError(2, "out must have q's dtype")
     if out.shape != q.shape:
@@ -726,15 +730,24 @@ def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next
     souts, souts_s0 = _rows(weight_sums_out, torch.float32, reqs, "weight_sums_out")
     entry_cols = min([t.shape[1] for t in (weight_sums, weight_sums_out) if t is not None]) \
         if weights else 0
-    _check(lib.qsa_paged_attention(
-        cache, q.data_ptr(), _tag(q), next_n, heads, _STRIDES3.pack(*q.stride()),
-        _flat(context_lens, torch.int32, reqs, "context_lens"),
-        dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
-        _STRIDES3.pack(*out.stride()), _flat(lse, torch.float32, rows * heads, "lse"),
-        sums, sums_s0, souts, souts_s0, entry_cols,
-        0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _word(error_word), raw))
+    ctx = _flat(context_lens, torch.int32, reqs, "context_lens")
+    lse_ptr, word = _flat(lse, torch.float32, rows * heads, "lse"), _word(error_word)
+    if workspace is None:
+        # from torch's allocator, for the launch stream, without a tensor around it
+        # (which costs the host 2 to 3 us more, as much as a launch)
+        ws = _raw_alloc(need, raw) if need else 0
+    else:
+        ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    try:
+        status = lib.qsa_paged_attention(
+            cache, q.data_ptr(), _tag(q), next_n, heads, _STRIDES3.pack(*q.stride()), ctx,
+            dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+            _STRIDES3.pack(*out.stride()), lse_ptr, sums, sums_s0, souts, souts_s0, entry_cols,
+            ws, need, word, raw)
+    finally:
+        if workspace is None and ws:
+            _raw_free(ws)        # back to the stream's pool: what comes next on it follows the launch
+    _check(status)
     return out
 
 
