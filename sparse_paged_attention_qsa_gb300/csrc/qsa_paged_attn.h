@@ -75,9 +75,14 @@ cudaError_t launch_paged_256(const PagedParams& p, bool bf16, bool fp8, const CU
 //   E4M3 117 against 108.  Heads of 256 hold twice the output a row, so four
 //   warps with all registers (32 rows: 181 against 331).
 //   Ring slots of 16 KB, but of 32 KB for heads of 256 (E4M3: 138 against 167)
-//   and for 32 rows of 16-bit heads of 128 (92 against 108, where 64 rows take
-//   373 with 32 KB and 260 with 16); at most 64 tokens a warp, whose logits are
-//   in its registers.  Narrower heads with up to 16 rows in one CTA an SM and
+//   and, where a warp's part of 16 KB is 32 tokens or fewer, for 17 rows and more
+//   of 256-byte rows of K (32 rows: 92 against 108; 64: 198 against 230, 256 short
+//   requests 137 against 129) and for 17 to 32 of 128-byte rows (FP16 heads of 64:
+//   128 against 166; E4M3 heads of 128: 102 against 112, 32 requests of about 1000
+//   tokens 37.2 against 35.5).  At most 64 tokens a warp, whose logits are in its
+//   registers (64 rows with 128 tokens: E4M3 heads of 64 206 against 242, but short
+//   requests of heads of 128 211 against 179).  Narrower heads with up to 16 rows
+//   in one CTA an SM and
 //   32 KB slots instead: 84 against 83 (131072 tokens), but 65 against 48 where
 //   requests are short, and 344 against 285 for E4M3 heads of 128.
 constexpr int paged_sets(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
@@ -85,7 +90,7 @@ constexpr int paged_warps(int dim, int wm) { return wm == 1 || dim == 256 ? 4 : 
 constexpr int paged_ctas(int dim, int wm) { return wm == 1 && dim < 256 ? 2 : 1; }
 // tokens of a tile
 constexpr int paged_tile(int dim, int row_bytes, int wm) {
-  const int slot = dim == 256 || (wm == 2 && row_bytes == 256) ? 32768 : 16384;
+  const int slot = dim == 256 || (wm >= 2 && row_bytes == 256) || (wm == 2 && row_bytes == 128) ? 32768 : 16384;
   const int most = 64 * (paged_warps(dim, wm) / wm), t = slot / row_bytes;
   return t < most ? t : most;
 }
