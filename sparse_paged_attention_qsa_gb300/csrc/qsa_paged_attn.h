@@ -82,16 +82,15 @@ cudaError_t launch_paged_256(const PagedParams& p, bool bf16, bool fp8, const CU
 //   tokens 37.2 against 35.5).  At most 64 tokens a warp, whose logits are in its
 //   registers (64 rows with 128 tokens: E4M3 heads of 64 206 against 242, but short
 //   requests of heads of 128 211 against 179).  Narrower heads with up to 16 rows
-//   in one CTA an SM and
-//   32 KB slots instead: 84 against 83 (131072 tokens), but 65 against 48 where
-//   requests are short, and 344 against 285 for E4M3 heads of 128.
+//   in one CTA an SM and 32 KB slots instead: 84 against 83 (131072 tokens), but 65
+//   against 48 where requests are short, and 344 against 285 for E4M3 heads of 128.
 constexpr int paged_sets(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 constexpr int paged_warps(int dim, int wm) { return wm == 1 || dim == 256 ? 4 : 8; }
 constexpr int paged_ctas(int dim, int wm) { return wm == 1 && dim < 256 ? 2 : 1; }
 // tokens of a tile
 constexpr int paged_tile(int dim, int row_bytes, int wm) {
-  const int slot = dim == 256 || (wm >= 2 && row_bytes == 256) || (wm == 2 && row_bytes == 128) ? 32768 : 16384;
-  const int most = 64 * (paged_warps(dim, wm) / wm), t = slot / row_bytes;
+  const bool large = dim == 256 || (wm >= 2 && row_bytes == 256) || (wm == 2 && row_bytes == 128);
+  const int most = 64 * (paged_warps(dim, wm) / wm), t = (large ? 32768 : 16384) / row_bytes;
   return t < most ? t : most;
 }
 

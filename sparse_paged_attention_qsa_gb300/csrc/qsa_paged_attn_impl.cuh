@@ -226,6 +226,13 @@ __device__ __forceinline__ TileAt tile_at(const int32_t* pre, int batch, int32_t
   return TileAt{lo, w - pre[lo], pre[lo + 1] - pre[lo]};
 }
 
+// Where the tile behind the last one of at's request lies (there is one): in the
+// next request as a rule.
+__device__ __forceinline__ TileAt tile_behind(const int32_t* pre, int batch, const TileAt& at) {
+  const int32_t w = pre[at.b + 1], n = pre[min(at.b + 2, batch)] - w;
+  return n > 0 ? TileAt{at.b + 1, 0, n} : tile_at(pre, batch, w);
+}
+
 template <typename T, bool kFp8, int D, int WM, bool kCluster>
 __global__ void __launch_bounds__((WalkShape<kFp8, D, WM, kCluster>::kThreads),
                                   (WalkShape<kFp8, D, WM, kCluster>::kCtas))
@@ -399,11 +406,6 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       TileAt next = at;
       int next_col = 0;
       int32_t next_id = -1;
-      if (seg_end < w_end) {
-        next = tile_at(pre, p.batch, seg_end);
-        next_col = first_col(next);
-        next_id = page_ids(next.b, next_col);
-      }
       // the segment's queries
       {
         const int qs = segments & 1;
@@ -464,6 +466,11 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
           }
         }
         if (stop) break;
+        if (t == at.tile && seg_end < w_end) {             // on their way during the others
+          next = tile_behind(pre, p.batch, at);
+          next_col = first_col(next);
+          next_id = page_ids(next.b, next_col);
+        }
       }
       at = next;
       chunk_col = next_col;
@@ -523,9 +530,14 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       }
     }
 
+    // merging: the real rows of every slice side by side, as many columns at a time
+    // as the buffer holds (all of them for up to 16 rows and slices)
+    const int cols = min(D, (W::kMergeBytes / 4 / (WK * n_rows) - 8) & ~31);
+    const int pitch = cols + 8;
     int32_t w = w_begin;
+    TileAt at = {0, 0, 0};
     for (int seg = 0; w < w_end; ++seg) {
-      const TileAt at = tile_at(pre, p.batch, w);
+      at = seg == 0 ? tile_at(pre, p.batch, w) : tile_behind(pre, p.batch, at);
       const int32_t seg_begin = w, seg_end = min(w_end, w + (at.count - at.tile));
       const bool whole = at.tile == 0 && seg_end - seg_begin == at.count;
       const int32_t ctx = tb.ctx[at.b];
@@ -875,10 +887,6 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         own_runs = run_of(runs, seg_begin + at.count - 1) - run + 1;
       }
       const float vscale = kFp8 && p.c.v_scale ? p.c.v_scale[head] : 1.f;
-      // the real rows of every slice side by side, as many columns at a time
-      // as the buffer holds (all of them for up to 16 rows and slices)
-      const int cols = min(D, (W::kMergeBytes / 4 / (WK * n_rows) - 8) & ~31);
-      const int pitch = cols + 8;
       for (int c0 = 0; c0 < D; c0 += cols) {
         const int c1 = min(D, c0 + cols);
         consumers_sync<W::kConsumers>();                   // the buffer is free
