@@ -12,7 +12,7 @@
 //   into equal runs; a CTA walks one run for one K/V head (and up to 64 of its
 //   query rows), all CTAs in a single wave: every SM streams the same bytes
 //   whatever the lengths.
-//   One producer warp looks pages up and loads K and V tiles into a ring by
+//   Two producer warps look pages up and load K and V tiles into a ring by
 //   TMA (swizzled, completion on mbarriers); four or eight consumer warps share a
 //   tile: WM sets of 16 query rows by WK slices of its tokens.
 //   Each warp keeps its rows' maximum, sum and output in registers: S = Q K^T
@@ -79,7 +79,7 @@ struct WalkShape {
   static constexpr int NW = paged_warps(D, WM);           // consumer warps
   static constexpr int kRows = 16 * WM;                       // query rows they hold
   static constexpr int kConsumers = NW * 32;
-  static constexpr int kThreads = kConsumers + 32;            // + the producer warp
+  static constexpr int kThreads = kConsumers + 64;            // + K's and V's producer
   static constexpr int TT = paged_tile(D, kRowBytes, WM);
   static constexpr int WK = NW / WM;
   static constexpr int kSlice = TT / WK;                      // tokens of a warp
@@ -348,15 +348,20 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   // the request that starts in this run and is cut: its place, and its pieces
   int own_b = -1, own_piece = 0, own_runs = 0;
   int withheld = -1;                                       // test build: a slot fill left out
-  int issued = 0, segments = 0;                            // producer: slots, queries loaded
-  if (warp == W::NW) {
-    // ---------------- producer ----------------
+  int issued = 0, segments = 0;                            // producers: slots, queries loaded
+  if (warp >= W::NW) {
+    // ---------------- producers ----------------
+    // Tile t's K is slot fill 2t, its V 2t + 1; a warp each, since a copy takes its
+    // warp 80 to 100 cycles to issue and small pages need many (one warp for both:
+    // pages of 8, FP16 heads of 256 244 us against 155, E4M3 heads of 64 137 against
+    // 96; pages of 16 157 against 142 and 92 against 75; of 64 no difference).
+    const int kv = warp - W::NW;
     const int lg = p.c.page_log2;
     const int box_rows = min(TT, 1 << lg);
     const int n_boxes = TT / box_rows;
     const int tile_cols = max(1, TT >> lg);
     int32_t w = w_begin;
-    int s = 0, round = 0;                                  // ring position of the next slot
+    int s = kv, round = 0;                                 // ring position of the next fill
     // Narrow rows, and K and V beside logits that are read again, give way in L2
     // first (E4M3 heads of 128: 292 us against 296, FP16 heads of 64: 45 against
     // 48); wide rows go through as anything does (heads of 256: 635 against 656).
@@ -401,13 +406,12 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       tiles_of<TT>(p, ctx, &first);
       visible(p, ctx, 0, &lo, &x);
       visible(p, ctx, p.next_n - 1, &x, &hi);
-      if (ctx > p.c.cap && lane == 0) report(p.err, QSA_DERR_CONTEXT);
+      if (ctx > p.c.cap && tid == W::kConsumers) report(p.err, QSA_DERR_CONTEXT);
       const int32_t seg_end = min(w_end, w + (at.count - at.tile));
       TileAt next = at;
       int next_col = 0;
       int32_t next_id = -1;
-      // the segment's queries
-      {
+      if (kv == 0) {                                       // the segment's queries
         const int qs = segments & 1;
         if (segments >= 2 && !wait_empty(bar_qempty + 8 * qs, (uint32_t)((segments / 2 - 1) & 1)))
           break;
@@ -433,39 +437,37 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
         const bool good = want && id >= 0 && id < p.c.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, good);
         const uint32_t unseen = ~__ballot_sync(0xffffffffu, want);   // and not asked about
-        if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (round > 0 && !wait_empty(bar_empty + 8 * s, (uint32_t)((round - 1) & 1))) break;
-          const uint32_t full = bar_full + 8 * s, dst = ring + s * W::kSlot;
+        if (__any_sync(0xffffffffu, want && !good) && tid == W::kConsumers)
+          report(p.err, QSA_DERR_KV_PAGE);
+        if (round > 0 && !wait_empty(bar_empty + 8 * s, (uint32_t)((round - 1) & 1))) break;
+        const uint32_t full = bar_full + 8 * s, dst = ring + s * W::kSlot;
 #ifdef QSA_WAIT_TEST
-          // test build: leave this fill without a copy, so the consumers'
-          // wait on it runs out (the failure-detection test)
-          const bool withhold = blockIdx.x == 0 && issued == p.test_withhold;
-          if (withhold) withheld = issued;
-          if (!withhold)
+        // test build: leave this fill without a copy, so the consumers'
+        // wait on it runs out (the failure-detection test)
+        const bool withhold = blockIdx.x == 0 && 2 * issued + kv == p.test_withhold;
+        if (withhold) withheld = issued;
+        if (!withhold)
 #endif
-          {
-            if (lane == 0) {
-              tb.boxes[s] = mask | unseen;
-              mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * W::kRowBytes));
-            }
-            __syncwarp();
-            if (good) {
-#pragma unroll
-              for (int i = 0; i < W::kChunks; ++i)
-                tma_load_4d(dst + i * (TT * W::kChunkBytes) + lane * box_rows * W::kChunkBytes,
-                            kv ? &vmap : &kmap, i * (W::kChunkBytes / (kFp8 ? 1 : 2)), head,
-                            be & ((1 << lg) - 1), id, full, policy);
-            }
+        {
+          if (lane == 0) {
+            tb.boxes[s] = mask | unseen;
+            mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * W::kRowBytes));
           }
-          ++issued;
-          if (++s == S) {
-            s = 0;
-            ++round;
+          __syncwarp();
+          if (good) {
+#pragma unroll
+            for (int i = 0; i < W::kChunks; ++i)
+              tma_load_4d(dst + i * (TT * W::kChunkBytes) + lane * box_rows * W::kChunkBytes,
+                          kv ? &vmap : &kmap, i * (W::kChunkBytes / (kFp8 ? 1 : 2)), head,
+                          be & ((1 << lg) - 1), id, full, policy);
           }
         }
-        if (stop) break;
+        ++issued;
+        s += 2;
+        if (s >= S) {
+          s -= S;
+          ++round;
+        }
         if (t == at.tile && seg_end < w_end) {             // on their way during the others
           next = tile_behind(pre, p.batch, at);
           next_col = first_col(next);
@@ -1012,9 +1014,11 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
   }
   __syncthreads();
   // after a time-out, let the copies this CTA issued land before it exits
-  if (*s_abort != 0 && warp == W::NW && lane == 0) {
-    for (int n = issued > S ? issued - S : 0; n < issued; ++n)
-      if (n != withheld) mbar_wait(bar_full + 8 * (n % S), (uint32_t)((n / S) & 1), kDrainLimitNs);
+  if (*s_abort != 0 && warp >= W::NW && lane == 0) {
+    for (int i = max(0, issued - (S + 1) / 2); i < issued; ++i) {
+      const int n = 2 * i + warp - W::NW;
+      if (i != withheld) mbar_wait(bar_full + 8 * (n % S), (uint32_t)((n / S) & 1), kDrainLimitNs);
+    }
     for (int n = segments > 2 ? segments - 2 : 0; n < segments; ++n)
       mbar_wait(bar_qfull + 8 * (n & 1), (uint32_t)((n >> 1) & 1), kDrainLimitNs);
   }
