@@ -29,7 +29,7 @@
 namespace qsa {
 namespace {
 
-constexpr int kWeightParts = 16;          // warps of a CTA, at most
+constexpr int kWeightParts = 8;          // warps of a CTA, at most
 
 #ifdef QSA_WAIT_TEST
 int32_t g_test_withhold = -1;
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kWeightParts * 32) weights_kernel(const Weight
     if (e + 3 >= lo && e < min(hi, (int64_t)n)) {
       const bool in[4] = {e >= lo, e + 1 >= lo && e + 1 < hi, e + 2 >= lo && e + 2 < hi,
                           e + 3 >= lo && e + 3 < hi};
-#pragma unroll 8
+#pragma unroll 4
       for (int y = x; y < end; ++y) {
         const float4 z = *reinterpret_cast<const float4*>(p.z + (first + y) * p.pitch + e);
         const float l = p.lse2[first + y];
