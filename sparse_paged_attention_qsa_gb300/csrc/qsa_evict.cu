@@ -40,6 +40,7 @@ constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kSpare = 8;
 constexpr int kMaxSlice = 24576;          // entries of a CTA whose keys fit in shared memory
+constexpr int kLoads = 4;
 constexpr int kMoveThreads = 256;
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
 
@@ -215,25 +216,38 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
   {
     uint32_t lo = 0xFFFFFFFFu, hi = 0u;
     int newest = INT32_MIN;
-#pragma unroll 8
-    for (int i = tid; i < ne; i += kRankThreads) {
-      const float f = w[e0 + i];
-      const uint32_t k = weight_key(f);
-      const int32_t q = pos[e0 + i];
-      if constexpr (kCached) {
-        s_key[i] = k;
-        s_pos[i] = q;
+    // a thread's loads in flight before the stores that could alias them: with
+    // four of each, 26 requests of 47685 entries take 61.9 us, 40 of 5261 15.1
+    // (one after another 65.5 and 15.9, eight 62.0 and 16.2)
+    for (int i0 = tid; i0 < ne; i0 += kLoads * kRankThreads) {
+      float f[kLoads];
+      int32_t q[kLoads];
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int i = min(i0 + j * kRankThreads, ne - 1);
+        f[j] = w[e0 + i];
+        q[j] = pos[e0 + i];
       }
-      if (e0 + i < p.budget) {
-        kept[e0 + i] = e0 + i;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int i = i0 + j * kRankThreads;
+        if (i >= ne) break;
+        const uint32_t k = weight_key(f[j]);
         if constexpr (kCached) {
-          sums_out[e0 + i] = f;
-          pos_out[e0 + i] = q;
+          s_key[i] = k;
+          s_pos[i] = q[j];
         }
+        if (e0 + i < p.budget) {
+          kept[e0 + i] = e0 + i;
+          if constexpr (kCached) {
+            sums_out[e0 + i] = f[j];
+            pos_out[e0 + i] = q[j];
+          }
+        }
+        lo = min(lo, k);
+        hi = max(hi, k);
+        newest = max(newest, q[j]);
       }
-      lo = min(lo, k);
-      hi = max(hi, k);
-      newest = max(newest, q);
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
