@@ -47,7 +47,7 @@ extern "C" {
  * a dimension of size 1 is not looked at).  So K and V may be two tensors, or lie side by side in one (the
  * exact-packed cache of qsa.h is strides {262144, 512, any, 1} with v = k +
  * 256), tokens or heads outermost within a page; the two views must not
- * share an element.
+ * share an element (qsa_paged_append refuses one view given as both).
  *
  *   dtype         QSA_DT_F16, QSA_DT_BF16 or QSA_DT_F8E4M3
  *   head_dim      64, 128 or 256

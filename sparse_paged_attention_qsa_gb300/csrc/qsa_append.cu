@@ -186,6 +186,7 @@ extern "C" qsa_status qsa_paged_append(
       !aligned(entries, 8) || !aligned(positions, 8) || !aligned(entry_positions, 4) ||
       !aligned(weight_sums, 4) || !aligned(error_word, 4))
     return QSA_ERR_ALIGN;
+  if (p.c.k == p.c.v && p.c.num_pages > 0) return QSA_ERR_ALIAS;   // one tensor given twice
   // the cache's K and V may interleave in one buffer, so their spans are
   // outputs that may overlap each other
   const Span book_outs[3] = {

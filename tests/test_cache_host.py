@@ -137,6 +137,10 @@ def test_append_refusals(lib, over, status):
     assert _append(lib, **over) == status
 
 
+def test_append_refuses_one_view_as_both(lib):
+    assert _append(lib, v=_addr(1)) == ALIAS
+
+
 def test_append_without_tokens_is_a_noop(lib):
     assert _append(lib, T=0, nk=None, nv=None, t2r=None, ent=None) == 0
 
