@@ -3,7 +3,11 @@
 //
 // For one K/V head of one request, its M = next_n * group query rows and its
 // entries e:  z_ie = c_i (q_i . k_e),  o_i = sum_e 2^(z_ie - m_i) v_e,
-// l_i = sum_e 2^(z_ie - m_i), m_i the running maximum; out = o / l.  4 M flops
+// l_i = sum_e 2^(z_ie - m_i); out = o / l.  The reference m_i is the running
+// maximum less kShift, rounded up: its own binary32 value is what every sum,
+// merge and lse uses, so logits of any size subtract from it without a weight
+// passing 2^kShift (the maximum less the shift, rounded to nearest, is off by up to
+// half a unit of a logit past 2^24, and weights of 2^16 are infinite in FP16).  4 M flops
 // for every K/V element of 1 or 2 bytes: for M <= 64 the bytes set the time, so
 // everything here serves one thing, that K and V stream through once at the
 // rate of the memory.
@@ -15,7 +19,7 @@
 //   Two producer warps look pages up and load K and V tiles into a ring by
 //   TMA (swizzled, completion on mbarriers); four or eight consumer warps share a
 //   tile: WM sets of 16 query rows by WK slices of its tokens.
-//   Each warp keeps its rows' maximum, sum and output in registers: S = Q K^T
+//   Each warp keeps its rows' reference, sum and output in registers: S = Q K^T
 //   and P V by mma.sync.m16n8k16 (binary32 accumulation) on fragments that
 //   ldmatrix reads from the ring.  (tcgen05 needs 64 or 128 rows and a round
 //   trip through tensor memory for the softmax; with at most 16 rows as a
@@ -34,7 +38,7 @@
 // rounding left), 2^-16 (BF16) or 2^-22 (FP16) relative, for up to 32 rows
 // over a 16-bit cache, where the second product is free; above that, and for
 // E4M3 caches (whose elements carry 4 bits), as one value.  They are scaled by
-// 2^15 so that small ones stay normal in FP16.
+// 2^15 (the reference's shift) so that small ones stay normal in FP16.
 #pragma once
 
 #include "qsa_paged_attn.h"
@@ -52,7 +56,7 @@
 namespace qsa {
 namespace {
 
-constexpr float kShift = 15.f;                 // weights are 2^(z - m + kShift)
+constexpr float kShift = 15.f;                 // the largest weight is about 2^kShift
 constexpr int kJoinThreads = 256;
 constexpr int kMaxSlots = 16;
 constexpr int kSmemPerSm = 233472, kSmemReserved = 1024;   // 228 KB, 1 KB of it a CTA's own
@@ -62,7 +66,7 @@ struct WalkTables {
   uint64_t full[kMaxSlots], empty[kMaxSlots];   // mbarriers of the ring
   uint64_t q_full[2], q_empty[2];               // and of the two query slots
   uint32_t boxes[kMaxSlots];                    // a bit per copy, 0: it had no page
-  float ml[8][16][2];                            // maximum and sum of the warps' rows
+  float ml[8][16][2];                            // reference and sum of the warps' rows
   float qs[kPagedMaxRows];                      // what the queries were divided by
   int32_t scan[12];                             // tiles of the requests of each warp
   uint8_t token[kPagedMaxRows];                 // the row's token of the draft
@@ -91,7 +95,7 @@ struct WalkShape {
   static constexpr int kQBytes = kRows * kQPitch * 2;         // a query slot
   static constexpr int kQSlots = kFp8 ? 3 : 2;                // the third: as FP16, reordered
   static constexpr int kMergeBytes = NW == 8 ? 128 * 40 * 4 : 17408;   // at least 32 columns
-  // of the first and the last segment: 16 rows and their maximum and sum
+  // of the first and the last segment: 16 rows and their reference and sum
   static constexpr int kPieceBytes = kCluster ? 2 * 16 * (D + 4) * 4 : 0;
   static constexpr int kFixed =
       1024 + kQSlots * kQBytes + kMergeBytes + kPieceBytes + (int)sizeof(WalkTables);
@@ -708,8 +712,8 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
             for (int n = 0; n < 2; ++n) mx = fmaxf(mx, fmaxf(sc[s][n][2 * k], sc[s][n][2 * k + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[k], mx);
-          ref[k] = mn == -INFINITY ? 0.f : mn - kShift;    // nothing seen yet: all weights 0
+          const float mn = fmaxf(m[k], __fadd_ru(mx, -kShift));
+          ref[k] = mn == -INFINITY ? 0.f : mn;             // nothing seen yet: all weights 0
           al[k] = mn == m[k] ? 1.f : ex2(m[k] - mn);
           m[k] = mn;
         }
@@ -950,7 +954,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
               const int r = row0 + i, j = token_of(i);
               const int64_t rh = ((int64_t)(p.b0 + at.b) * p.next_n + j) * p.heads +
                                  head * p.group + r - j * p.group;
-              const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
+              const float t = L == 0.f ? -INFINITY : M + log2f(L);
               if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
               if (p.lse2) p.lse2[rh] = t;
             }
@@ -1004,7 +1008,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
           const int r = row0 + i, j = tb.token[i];
           const int64_t rh = ((int64_t)(p.b0 + own_b) * p.next_n + j) * p.heads + head * p.group +
                              r - j * p.group;
-          const float t = L == 0.f ? -INFINITY : M - kShift + log2f(L);
+          const float t = L == 0.f ? -INFINITY : M + log2f(L);
           if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
           if (p.lse2) p.lse2[rh] = t;
         }
@@ -1106,7 +1110,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   *reinterpret_cast<uint2*>(p.out + row * p.out_row + h * p.out_head + ln * 8) =
       make_uint2(pack2<kBf16>(acc.x * inv, acc.y * inv), pack2<kBf16>(acc.z * inv, acc.w * inv));
   if (ln == 0) {
-    const float t = l == 0.f ? -INFINITY : m - kShift + log2f(l);
+    const float t = l == 0.f ? -INFINITY : m + log2f(l);
     if (p.lse) p.lse[row * p.heads + h] = t * 0.693147180559945309f;
     if (p.lse2) p.lse2[row * p.heads + h] = t;
   }

@@ -249,6 +249,52 @@ def test_attention_extreme_logits():
     check(c, sums=True)
 
 
+def _fill(t, x):
+    raw = torch.tensor(x).to(t.dtype)
+    if t.dtype == E4M3:
+        t.view(torch.uint8).fill_(int(raw.view(torch.uint8)))
+    else:
+        t.fill_(raw.item())
+
+
+@pytest.mark.parametrize("hq,lens", [(4, [300, 0, 17]), (4, [1100, 5]), (4, [9000, 5]),
+                                     (16, [2300, 5]), (17, [700, 33]), (64, [1500])])
+@pytest.mark.parametrize("dtype,cache", [(F16, F16), (F16, E4M3), (BF16, E4M3)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("peak", [False, True])
+def test_attention_logits_past_binary32s_integers(peak, sign, dtype, cache, hq, lens):
+    """Finite logits of 2^24 to 2^28 in base 2, where binary32 no longer holds a logit
+    less 15.  Every entry's key is the same, but for one with peak: the others' weights are then
+    0.  q and K have at most 8 bits and equal elements, so that the products' sums are exact and
+    the logits' error does not enter the weights; scale, its product and the lse's conversion
+    round at most 7 times, below 2^-21 of the lse."""
+    top = 448.0 if cache == E4M3 else None
+    for a in (1216, 1792, 2944, 4032) if cache == F16 else (6656, 14336, 40960, 57344):
+        c = Case(lens, hq, 1, 64, 16, dtype, cache, seed=hq)
+        b = top or float(a)
+        if c.k_scale is not None:
+            c.k_scale.fill_(0.5)
+        c.q.fill_(a)
+        _fill(c.k, sign * b * (0.5 if peak and sign > 0 else 1))
+        if peak:
+            for i, n in enumerate(lens):
+                _fill(c.k[int(c.tables[i, n // 3 // 16]), n // 3 % 16],
+                      sign * b * (1 if sign > 0 else 0.5))
+        r = c.oracle()
+        out, lse, err = c.run()
+        n = max(lens)
+        weight = 2.0 ** -20 + (n / 16 + 32) * 2.0 ** -23
+        pair = 2.0 ** -11 if cache == E4M3 else HALF[dtype] if hq > 32 else 2.0 ** -22
+        tol = (weight + pair) * r["spread"] + HALF[dtype] * np.abs(r["out"]) + 2.0 ** -25
+        assert torch.isfinite(out).all()
+        assert (np.abs(_f64(out) - r["out"]) <= tol).all(), np.abs(_f64(out) - r["out"]).max()
+        got, fin = lse.double().cpu().numpy(), np.isfinite(r["lse"])
+        assert np.abs(r["lse"][fin]).max() > 0.69 * 2 ** 23
+        assert np.array_equal(np.isneginf(got), np.isneginf(r["lse"]))
+        assert (np.abs(got - r["lse"])[fin] <= weight + 2.0 ** -21 * np.abs(r["lse"][fin])).all()
+        assert int(err.item()) == 0
+
+
 def test_attention_bad_pages_and_contexts():
     c = Case([200, 90, 64, 33], 4, 2, 128, 32, BF16, seed=6)
     c.tables[0, 2] = -1
