@@ -141,8 +141,9 @@ QSA_API size_t qsa_paged_attention_workspace_bytes(const qsa_paged_cache* cache,
  * A row that sees no entry gets zeros and an lse of -inf; rows of requests
  * with a context length of 0 or less are such rows.  What a masked or absent
  * entry holds (infinities and NaN too) does not matter.  The softmax's
- * statistics and sums are binary32; the results are the same bit for bit each
- * time a call is repeated on one kind of GPU.
+ * statistics and sums are binary32, so q . K_e, z_e and the sum of |V_e| over the
+ * entries that a row sees have to be finite there; the results are the same bit
+ * for bit each time a call is repeated on one kind of GPU.
  *
  * Arguments
  *   q             [num_reqs*next_n, num_heads, head_dim], dtype QSA_DT_F16 or

@@ -4,9 +4,9 @@
 // For one K/V head of one request, its M = next_n * group query rows and its
 // entries e:  z_ie = c_i (q_i . k_e),  o_i = sum_e 2^(z_ie - m_i) v_e,
 // l_i = sum_e 2^(z_ie - m_i); out = o / l.  The reference m_i is the running
-// maximum less kShift, rounded up: its own binary32 value is what every sum,
+// maximum less a shift, rounded up: its own binary32 value is what every sum,
 // merge and lse uses, so logits of any size subtract from it without a weight
-// passing 2^kShift (the maximum less the shift, rounded to nearest, is off by up to
+// passing 2^shift (the maximum less the shift, rounded to nearest, is off by up to
 // half a unit of a logit past 2^24, and weights of 2^16 are infinite in FP16).  4 M flops
 // for every K/V element of 1 or 2 bytes: for M <= 64 the bytes set the time, so
 // everything here serves one thing, that K and V stream through once at the
@@ -37,8 +37,7 @@
 // The weights multiply V as a pair of 16-bit values (a value and what its
 // rounding left), 2^-16 (BF16) or 2^-22 (FP16) relative, for up to 32 rows
 // over a 16-bit cache, where the second product is free; above that, and for
-// E4M3 caches (whose elements carry 4 bits), as one value.  They are scaled by
-// 2^15 (the reference's shift) so that small ones stay normal in FP16.
+// E4M3 caches (whose elements carry 4 bits), as one value.
 #pragma once
 
 #include "qsa_paged_attn.h"
@@ -56,7 +55,10 @@
 namespace qsa {
 namespace {
 
-constexpr float kShift = 15.f;                 // the largest weight is about 2^kShift
+// The largest weight is about 2^shift: 15 where weights are FP16, so that small ones
+// stay normal; BF16 has binary32's exponents and needs none, and 2^15 times a value
+// past 2^113 would leave them.
+constexpr float paged_shift(bool bf16) { return bf16 ? 0.f : 15.f; }
 constexpr int kJoinThreads = 256;
 constexpr int kMaxSlots = 16;
 constexpr int kSmemPerSm = 233472, kSmemReserved = 1024;   // 228 KB, 1 KB of it a CTA's own
@@ -712,7 +714,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
             for (int n = 0; n < 2; ++n) mx = fmaxf(mx, fmaxf(sc[s][n][2 * k], sc[s][n][2 * k + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[k], __fadd_ru(mx, -kShift));
+          const float mn = fmaxf(m[k], __fadd_ru(mx, -paged_shift(kBf16)));
           ref[k] = mn == -INFINITY ? 0.f : mn;             // nothing seen yet: all weights 0
           al[k] = mn == m[k] ? 1.f : ex2(m[k] - mn);
           m[k] = mn;

@@ -295,6 +295,24 @@ def test_attention_logits_past_binary32s_integers(peak, sign, dtype, cache, hq, 
         assert int(err.item()) == 0
 
 
+# rows of a K/V head, cached tokens and page: walked whole, in one cluster, cut and joined
+_MODES = [(4, [300, 0, 17]), (16, [1100, 5]), (4, [9000, 5]), (17, [1500, 33]), (64, [1500])]
+
+
+@pytest.mark.parametrize("hq,lens", _MODES)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_values_up_to_bf16s_range(d, hq, lens):
+    """BF16 values of 1e35 in one entry and 1e30 in all the others, equal ones included:
+    their sum is finite in binary32, so every result is."""
+    c = Case(lens, hq, 1, d, 16, BF16, seed=hq + d)
+    c.v.mul_(1e30)
+    for i, n in enumerate(lens):
+        _fill(c.v[int(c.tables[i, n // 2 // 16]), n // 2 % 16, :, : d // 2], 1e35)
+    out, _ = check(c)
+    _fill(c.v, 1e34)
+    check(c)
+
+
 def test_attention_bad_pages_and_contexts():
     c = Case([200, 90, 64, 33], 4, 2, 128, 32, BF16, seed=6)
     c.tables[0, 2] = -1
