@@ -41,7 +41,7 @@ int32_t g_test_withhold = -1;
 struct WeightParams {
   const int32_t* ctx;
   const float* z;             // [rows][heads][pitch] logits (base 2)
-  const float* lse2;          // [rows][heads]
+  const float2* stats;        // [rows][heads] reference and log2 of the sum
   int64_t pitch;
   int32_t window;
   int32_t cap, next_n, heads;
@@ -78,12 +78,12 @@ __global__ void __launch_bounds__(kWeightParts * 32) weights_kernel(const Weight
 #pragma unroll 4
       for (int y = x; y < end; ++y) {
         const float4 z = *reinterpret_cast<const float4*>(p.z + (first + y) * p.pitch + e);
-        const float l = p.lse2[first + y];
-        // -inf (an absent entry): 0, also where the row saw nothing and l is -inf
-        s.x += in[0] && z.x != -INFINITY ? exp2f(z.x - l) : 0.f;
-        s.y += in[1] && z.y != -INFINITY ? exp2f(z.y - l) : 0.f;
-        s.z += in[2] && z.z != -INFINITY ? exp2f(z.z - l) : 0.f;
-        s.w += in[3] && z.w != -INFINITY ? exp2f(z.w - l) : 0.f;
+        const float2 r = p.stats[first + y];
+        // -inf (an absent entry): 0, also where the row saw nothing and r.x is -inf
+        s.x += in[0] && z.x != -INFINITY ? exp2f(z.x - r.x - r.y) : 0.f;
+        s.y += in[1] && z.y != -INFINITY ? exp2f(z.y - r.x - r.y) : 0.f;
+        s.z += in[2] && z.z != -INFINITY ? exp2f(z.z - r.x - r.y) : 0.f;
+        s.w += in[3] && z.w != -INFINITY ? exp2f(z.w - r.x - r.y) : 0.f;
       }
     }
     x = end;
@@ -149,7 +149,7 @@ bool sizes_ok(const qsa_paged_cache& c, int64_t next_n, int64_t heads) {
 // then, when weights are asked for, the rows' sums and logits.
 struct Layout {
   PagedMode mode;
-  size_t ml, o, lse2, z, total;
+  size_t ml, o, stats, z, total;
 };
 
 // 0 as the total where it cannot be addressed.
@@ -165,8 +165,8 @@ Layout layout_of(const qsa_paged_cache& c, const CacheView& v, int64_t next_n, i
   const bool pieces = l.mode == kPagedCut;
   l.ml = pieces ? round256(kPagedMaxCtas * sizeof(int4)) : 0;
   l.o = l.ml + (pieces ? round256(2 * kPagedMaxCtas * rows * 2 * sizeof(float)) : 0);
-  l.lse2 = l.o + (pieces ? round256(2 * kPagedMaxCtas * rows * (size_t)c.head_dim * sizeof(float)) : 0);
-  l.z = l.lse2 + (entries > 0 ? round256((size_t)all * sizeof(float)) : 0);
+  l.stats = l.o + (pieces ? round256(2 * kPagedMaxCtas * rows * (size_t)c.head_dim * sizeof(float)) : 0);
+  l.z = l.stats + (entries > 0 ? round256((size_t)all * sizeof(float2)) : 0);
   const __int128 total = (__int128)l.z + (__int128)all * entries * 4;
   l.total = total < ((__int128)1 << 60) ? (size_t)total : 0;
   if (l.total == 0) l.total = total == 0 ? 0 : SIZE_MAX;
@@ -269,7 +269,7 @@ extern "C" qsa_status qsa_paged_attention(
   p.part_ml = reinterpret_cast<float*>(w + l.ml);
   p.part_o = reinterpret_cast<float*>(w + l.o);
   if (weights && entries > 0) {
-    p.lse2 = reinterpret_cast<float*>(w + l.lse2);
+    p.stats = reinterpret_cast<float2*>(w + l.stats);
     p.z = reinterpret_cast<float*>(w + l.z);
     p.z_pitch = entries;
   }
@@ -305,7 +305,7 @@ extern "C" qsa_status qsa_paged_attention(
     WeightParams wp{};
     wp.ctx = context_lens;
     wp.z = p.z;
-    wp.lse2 = p.lse2;
+    wp.stats = p.stats;
     wp.pitch = p.z_pitch;
     wp.window = p.window;
     wp.cap = p.c.cap;

@@ -44,7 +44,7 @@ struct PagedParams {
   float scale_log2;           // scale * log2(e)
   int32_t window;             // 0: none; at most INT32_MAX - 16
   float* lse;                 // nullable
-  float* lse2;                // workspace: [rows][heads] log2 sums, or null
+  float2* stats;              // workspace: [rows][heads] reference and log2 of the sum, or null
   float* z;                   // workspace: [rows][heads][z_pitch] logits (base 2), or null
   int64_t z_pitch;
   int4* starts;               // workspace: [kPagedMaxCtas] request, tile, its tiles, all tiles

@@ -188,6 +188,14 @@ __device__ __forceinline__ void visible(const PagedParams& p, int32_t ctx, int j
   *lo = p.window > 0 ? min(max(h - p.window, 0), cap) : 0;
 }
 
+// What a row's reference m and sum l (0: it saw nothing) leave: its lse, and for the
+// weights the two apart, since their sum is off by half a unit of a large logit.
+__device__ __forceinline__ void store_stats(const PagedParams& p, int64_t rh, float m, float l) {
+  const float log_l = log2f(l);
+  if (p.lse) p.lse[rh] = l == 0.f ? -INFINITY : (m + log_l) * 0.693147180559945309f;
+  if (p.stats) p.stats[rh] = make_float2(m, log_l);
+}
+
 // The tiles a request's entries span, [*first, *first + count).
 template <int TT>
 __device__ __forceinline__ int32_t tiles_of(const PagedParams& p, int32_t ctx, int32_t* first) {
@@ -534,7 +542,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
       }
       for (int i = tid; i < n; i += W::kConsumers) {
         if (p.lse) p.lse[r0 * p.heads + i] = -INFINITY;
-        if (p.lse2) p.lse2[r0 * p.heads + i] = -INFINITY;
+        if (p.stats) p.stats[r0 * p.heads + i] = make_float2(-INFINITY, 0.f);
       }
     }
 
@@ -956,9 +964,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
               const int r = row0 + i, j = token_of(i);
               const int64_t rh = ((int64_t)(p.b0 + at.b) * p.next_n + j) * p.heads +
                                  head * p.group + r - j * p.group;
-              const float t = L == 0.f ? -INFINITY : M + log2f(L);
-              if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
-              if (p.lse2) p.lse2[rh] = t;
+              store_stats(p, rh, M, L);
             }
           } else if constexpr (kCluster) {
             float* d = pieces + (which * 16 + i) * (D + 4);
@@ -1010,9 +1016,7 @@ paged_walk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap kmap,
           const int r = row0 + i, j = tb.token[i];
           const int64_t rh = ((int64_t)(p.b0 + own_b) * p.next_n + j) * p.heads + head * p.group +
                              r - j * p.group;
-          const float t = L == 0.f ? -INFINITY : M + log2f(L);
-          if (p.lse) p.lse[rh] = t * 0.693147180559945309f;
-          if (p.lse2) p.lse2[rh] = t;
+          store_stats(p, rh, M, L);
         }
       }
     }
@@ -1111,11 +1115,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
   *reinterpret_cast<uint2*>(p.out + row * p.out_row + h * p.out_head + ln * 8) =
       make_uint2(pack2<kBf16>(acc.x * inv, acc.y * inv), pack2<kBf16>(acc.z * inv, acc.w * inv));
-  if (ln == 0) {
-    const float t = l == 0.f ? -INFINITY : m + log2f(l);
-    if (p.lse) p.lse[row * p.heads + h] = t * 0.693147180559945309f;
-    if (p.lse2) p.lse2[row * p.heads + h] = t;
-  }
+  if (ln == 0) store_stats(p, row * p.heads + h, m, l);
 }
 
 // The SMs of the current device; the kernel's set-up once per device.

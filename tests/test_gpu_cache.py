@@ -313,6 +313,33 @@ def test_attention_values_up_to_bf16s_range(d, hq, lens):
     check(c)
 
 
+@pytest.mark.parametrize("hq,lens", _MODES)
+@pytest.mark.parametrize("dtype,cache", [(F16, F16), (BF16, E4M3), (BF16, BF16)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_weight_sums_of_large_logits(sign, dtype, cache, hq, lens):
+    """Equal keys give equal weights however large the logits are (up to 2^28 in base 2): the
+    weights' error is that of the exponential and of the sum, not of the lse's own rounding.
+    The weight is 2^((z - m) - log2 l): z - m exact, log2 l below 32 off by 2^-18 (one unit of
+    its own, half of one of the difference's), which makes ln 2 * 2^-18 of the weight; the sum
+    l and the exponential as in `bounds`; the sum over heads at most 64 more additions."""
+    for a in (64.0, 1216.0, 4032.0):
+        c = Case(lens, hq, 1, 64, 16, dtype, cache, seed=hq)
+        if c.k_scale is not None:
+            c.k_scale.fill_(1.0)
+        _fill(c.q, a)
+        _fill(c.k, sign * (448.0 if cache == E4M3 else a))
+        cols = c.tables.shape[1] * 16
+        base, added = torch.zeros((len(lens), cols), device=DEV), torch.zeros(
+            (len(lens), cols), device=DEV)
+        c.run(weight_sums=base, weight_sums_out=added)
+        got = added.double().cpu().numpy()
+        for i, n in enumerate(lens):
+            rel = 2.0 ** -18 + 2.0 ** -20 + (n / 16 + 32) * 2.0 ** -23 + 64 * 2.0 ** -24
+            if n:
+                assert (np.abs(got[i, :n] * n / hq - 1) <= rel).all(), np.abs(got[i, :n] * n / hq - 1).max()
+            assert not got[i, n:].any()
+
+
 def test_attention_bad_pages_and_contexts():
     c = Case([200, 90, 64, 33], 4, 2, 128, 32, BF16, seed=6)
     c.tables[0, 2] = -1
