@@ -260,6 +260,13 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+def _workspace_bytes(workspace) -> int:
+    """What the library may write behind a caller's workspace."""
+    if not workspace.is_contiguous():      # a broadcast or strided one holds less than numel says
+        raise QSAError(7, "workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def qsa_select_paged_tokens(q_sel, cmp_cache, cmp_page_table, token_to_request, seq_lens,
                             query_positions, token_topk: int = TOKEN_TOPK,
                             compress_ratio: int = COMPRESS_RATIO, out=None, workspace=None,
@@ -293,7 +300,7 @@ def qsa_select_paged_tokens(q_sel, cmp_cache, cmp_page_table, token_to_request, 
         _ptr(query_positions), _tag(query_positions),
         int(token_topk), int(compress_ratio),
         _ptr(out), _tag(out), out.shape[1], out.stride(0),
-        _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(workspace), _workspace_bytes(workspace),
         _ptr(error_word), _stream(stream))
     _check(st)
     return out
@@ -333,7 +340,7 @@ def qsa_sparse_attention(q, k_cache, v_cache, kv_page_table, token_to_request, i
         _ptr(indices), _tag(indices), width, indices.stride(0),
         float(scale),
         _ptr(out), _tag(out), _arr(out.stride()),
-        _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(workspace), _workspace_bytes(workspace),
         _ptr(error_word), _stream(stream))
     _check(st)
     return out
@@ -424,7 +431,7 @@ def qsa_select_attend(q_sel, cmp_cache, cmp_page_table, token_to_request, seq_le
         kv_page_table.stride(0),
         float(scale),
         _ptr(out), _tag(out), _arr(out.stride()),
-        _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(workspace), _workspace_bytes(workspace),
         _ptr(error_word), _stream(stream))
     _check(st)
     return indices, out
@@ -737,7 +744,7 @@ def qsa_paged_attention(q, k_cache, v_cache, block_tables, context_lens, *, next
         # (which costs the host 2 to 3 us more, as much as a launch)
         ws = _raw_alloc(need, raw) if need else 0
     else:
-        ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, need = workspace.data_ptr(), _workspace_bytes(workspace)
     try:
         status = lib.qsa_paged_attention(
             cache, q.data_ptr(), _tag(q), next_n, heads, _STRIDES3.pack(*q.stride()), ctx,

@@ -235,3 +235,60 @@ def test_binding_refuses_host_tensors():
                  lambda: qsa.qsa_evict_entries(f, bt, i32, k, k, bt, 8)):
         with pytest.raises(qsa.QSAError):
             call()
+
+
+class _Recorder:
+    """Stands in for the library: says what it would have been given."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_bytes"):
+            return lambda *a: 4096
+
+        def call(*a):
+            self.calls.append((name, a))
+            return 0
+        return call
+
+
+@pytest.fixture
+def recorder(monkeypatch):
+    """The binding on host tensors in front of a recorder: nothing can be launched."""
+    rec = _Recorder()
+    monkeypatch.setattr(binding, "_lib", rec)
+    monkeypatch.setattr(binding, "load_library", lambda: rec)
+    monkeypatch.setattr(binding, "_on_current_device", lambda *t: None)
+    monkeypatch.setattr(binding, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(binding, "_stream", lambda s: 0)
+    monkeypatch.setattr(binding, "_launch_stream", lambda s, d: 0)
+    return rec
+
+
+def _workspace_calls(ws):
+    h = dict(dtype=torch.float16)
+    i32, i64 = torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64)
+    bt = torch.zeros((1, 1), dtype=torch.int32)
+    kv = torch.zeros((1, 512, 2, 256), **h)
+    sel = (torch.zeros((1, 4, 128), **h), torch.zeros((1, 128, 1, 128), **h), bt, i32, i32, i64)
+    att = (torch.zeros((1, 3, 256), **h), kv[:, :, :1], kv[:, :, 1:], bt)
+    return [lambda: qsa.qsa_select_paged_tokens(*sel, workspace=ws),
+            lambda: qsa.qsa_sparse_attention(*att, i32, torch.zeros((1, 2051), dtype=torch.int32),
+                                             workspace=ws),
+            lambda: qsa.qsa_select_attend(*sel, *att, workspace=ws),
+            lambda: qsa.qsa_paged_attention(*att, i32, workspace=ws)]
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_a_workspace_that_holds_less_than_its_elements_is_refused(recorder, which):
+    one = torch.zeros(1, dtype=torch.uint8)
+    wide = torch.zeros(200, dtype=torch.uint8)
+    for ws in (one.expand(1 << 20), wide.as_strided((100, 100), (1, 1)), wide[::2]):
+        with pytest.raises(qsa.QSAError) as e:
+            _workspace_calls(ws)[which]()
+        assert e.value.status == WORKSPACE
+    assert not recorder.calls
+    _workspace_calls(wide)[which]()                  # one that is what it says goes on
+    (name, args), = recorder.calls
+    assert args[args.index(wide.data_ptr()) + 1] == 200, name
