@@ -196,8 +196,8 @@ QSA_API qsa_status qsa_paged_attention(
  *   weight_sums_out[b, i], entry_positions_out[b, i]
  *                  of that entry; 0 and -1 for i >= new_lens[b]
  *
- * The inputs are not written, so the next step takes the outputs in their
- * place.  A page that holds entries below `budget` must belong to one request
+ * The inputs are not written.  (A next step that appends and attends needs room
+ * behind the budget in its per-entry arrays: qsa_evict_entries_strided.)  A page that holds entries below `budget` must belong to one request
  * alone.  An entry whose page is absent still counts; its K and V are not
  * moved (QSA_DERR_KV_PAGE).
  *
@@ -218,6 +218,25 @@ QSA_API qsa_status qsa_evict_entries(
     const int32_t* entry_positions, int64_t entry_positions_stride0, int64_t entry_cols,
     const int32_t* context_lens, int64_t budget, int64_t num_sink, int64_t num_recent,
     int32_t* kept, int32_t* new_lens, float* weight_sums_out, int32_t* entry_positions_out,
+    uint32_t* error_word, qsa_stream_t stream);
+
+/*
+ * qsa_evict_entries_strided -- qsa_evict_entries with weight_sums_out and
+ * entry_positions_out as rows of wider arrays: row b starts at b * the array's
+ * stride0 (>= budget); columns from budget on are left as they were.  With two
+ * arrays [num_reqs, entry_cols] of each kind, entry_cols >= the table's entries,
+ * used as input and output in turn, the outputs and new_lens are what the next
+ * step's append (whose tokens become the entries from new_lens[b] on), attention
+ * and eviction take.
+ */
+QSA_API qsa_status qsa_evict_entries_strided(
+    const qsa_paged_cache* cache,
+    const float* weight_sums, int64_t weight_sums_stride0,
+    const int32_t* entry_positions, int64_t entry_positions_stride0, int64_t entry_cols,
+    const int32_t* context_lens, int64_t budget, int64_t num_sink, int64_t num_recent,
+    int32_t* kept, int32_t* new_lens,
+    float* weight_sums_out, int64_t weight_sums_out_stride0,
+    int32_t* entry_positions_out, int64_t entry_positions_out_stride0,
     uint32_t* error_word, qsa_stream_t stream);
 
 #ifdef __cplusplus

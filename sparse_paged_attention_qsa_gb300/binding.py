@@ -48,7 +48,7 @@ EXPORTED = ("qsa_status_string", "qsa_version", "qsa_select_workspace_bytes",
             "qsa_select_paged_tokens_static_scratch", "qsa_build_metadata",
             "qsa_paged_mqa_logits", "qsa_top_k_per_row_decode",
             "qsa_paged_append", "qsa_paged_attention_workspace_bytes", "qsa_paged_attention",
-            "qsa_evict_entries")
+            "qsa_evict_entries", "qsa_evict_entries_strided")
 
 
 class QSAError(RuntimeError):
@@ -195,6 +195,9 @@ def declare_signatures(lib):
     lib.qsa_evict_entries.restype = ctypes.c_int
     lib.qsa_evict_entries.argtypes = [
         vp, vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+    lib.qsa_evict_entries_strided.restype = ctypes.c_int
+    lib.qsa_evict_entries_strided.argtypes = [
+        vp, vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, i64, vp, i64, vp, vp]
     return full
 
 
@@ -627,6 +630,17 @@ def _rows(t, dtype, reqs, what):
     return p, s0 if reqs > 1 else max(s0, cols)
 
 
+def _budget_rows(t, dtype, reqs, budget, what):
+    """(address, row stride) of an output of `budget` columns a request: contiguous
+    with that many elements, or the first columns of a wider [reqs, cols] array."""
+    if t.dtype == dtype and t.numel() == reqs * budget and t.is_contiguous():
+        return t.data_ptr(), budget
+    p, s0 = _rows(t, dtype, reqs, what)
+    if t.shape[1] < budget:
+        raise QSAError(3, f"{what} must hold {budget} columns")
+    return p, s0
+
+
 def _word(t) -> int:
     return _flat(t, torch.int32, 1, "error_word")
 
@@ -767,7 +781,9 @@ def qsa_evict_entries(weight_sums, entry_positions, context_lens, k_cache, v_cac
     largest weight_sums; K and V are moved within the cache
     (include/qsa_cache.h).  Returns (kept int32 [requests, budget], new_lens
     int32 [requests], weight_sums_out fp32, entry_positions_out int32
-    [requests, budget])."""
+    [requests, budget]).  weight_sums_out and entry_positions_out may be given
+    wider, as the next step's append and attention need them: their columns
+    from budget on stay as they are."""
     lib = _lib or load_library()
     _on_current_device(weight_sums, entry_positions, context_lens, k_cache, v_cache, block_tables,
                        kept, new_lens, weight_sums_out, entry_positions_out, error_word)
@@ -792,12 +808,14 @@ def qsa_evict_entries(weight_sums, entry_positions, context_lens, k_cache, v_cac
                 weight_sums_out = torch.empty((reqs, budget), dtype=torch.float32, device=dev)
             if entry_positions_out is None:
                 entry_positions_out = torch.empty((reqs, budget), dtype=torch.int32, device=dev)
-    n = reqs * budget
-    _check(lib.qsa_evict_entries(
+    souts, souts_s0 = _budget_rows(weight_sums_out, torch.float32, reqs, budget, "weight_sums_out")
+    pouts, pouts_s0 = _budget_rows(entry_positions_out, torch.int32, reqs, budget,
+                                   "entry_positions_out")
+    _check(lib.qsa_evict_entries_strided(
         cache, sums, sums_s0, pos, pos_s0,
         min(weight_sums.shape[1], entry_positions.shape[1]),
         _flat(context_lens, torch.int32, reqs, "context_lens"), budget, num_sink, num_recent,
-        _flat(kept, torch.int32, n, "kept"), _flat(new_lens, torch.int32, reqs, "new_lens"),
-        _flat(weight_sums_out, torch.float32, n, "weight_sums_out"),
-        _flat(entry_positions_out, torch.int32, n, "entry_positions_out"), _word(error_word), raw))
+        _flat(kept, torch.int32, reqs * budget, "kept"),
+        _flat(new_lens, torch.int32, reqs, "new_lens"), souts, souts_s0, pouts, pouts_s0,
+        _word(error_word), raw))
     return kept, new_lens, weight_sums_out, entry_positions_out

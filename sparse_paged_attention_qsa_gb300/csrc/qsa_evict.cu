@@ -1,6 +1,6 @@
 // qsa_evict.cu -- evicting the entries of a paged K/V cache that received
 // the least attention weight, declared in include/qsa_cache.h
-// (qsa_evict_entries).
+// (qsa_evict_entries, qsa_evict_entries_strided).
 //
 // rank_kernel  a cluster of 1 to 8 CTAs per request, each over a slice of its
 //              entries: the budget-th largest key (protected entries, then the
@@ -57,8 +57,10 @@ struct EvictParams {
   int32_t move_here;          // the rank kernel moves K and V itself
   int32_t* kept;              // [reqs, budget]
   int32_t* new_lens;
-  float* sums_out;
+  float* sums_out;            // rows of budget
+  int64_t sums_out_s0;
   int32_t* pos_out;
+  int64_t pos_out_s0;
   uint32_t* err;
 };
 
@@ -186,8 +188,8 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictParams p,
   const int n = max(0, min(ctx, p.cap));
   const int len = min(n, p.budget);
   int32_t* kept = p.kept + (int64_t)b * p.budget;
-  float* sums_out = p.sums_out + (int64_t)b * p.budget;
-  int32_t* pos_out = p.pos_out + (int64_t)b * p.budget;
+  float* sums_out = p.sums_out + b * p.sums_out_s0;
+  int32_t* pos_out = p.pos_out + b * p.pos_out_s0;
   pdl_trigger();
   if (rank == 0 && tid == 0) {
     if (ctx > p.cap) report(p.err, QSA_DERR_CONTEXT);
@@ -630,12 +632,13 @@ cudaError_t launch_rank(EvictParams& p, int reqs, int64_t most, int sms, cudaStr
 }  // namespace
 }  // namespace qsa
 
-extern "C" qsa_status qsa_evict_entries(
+extern "C" qsa_status qsa_evict_entries_strided(
     const qsa_paged_cache* cache, const float* weight_sums, int64_t weight_sums_stride0,
     const int32_t* entry_positions, int64_t entry_positions_stride0, int64_t entry_cols,
     const int32_t* context_lens, int64_t budget, int64_t num_sink, int64_t num_recent,
-    int32_t* kept, int32_t* new_lens, float* weight_sums_out, int32_t* entry_positions_out,
-    uint32_t* error_word, qsa_stream_t stream) {
+    int32_t* kept, int32_t* new_lens, float* weight_sums_out, int64_t weight_sums_out_stride0,
+    int32_t* entry_positions_out, int64_t entry_positions_out_stride0, uint32_t* error_word,
+    qsa_stream_t stream) {
   using namespace qsa;
   using namespace qsa::cache_host;
   EvictParams p{};
@@ -647,7 +650,9 @@ extern "C" qsa_status qsa_evict_entries(
     return QSA_ERR_CONTRACT;
   if (entry_cols < 0 || entry_cols > INT32_MAX) return QSA_ERR_SHAPE;
   if (!row_stride_ok(weight_sums_stride0, entry_cols) ||
-      !row_stride_ok(entry_positions_stride0, entry_cols))
+      !row_stride_ok(entry_positions_stride0, entry_cols) ||
+      !row_stride_ok(weight_sums_out_stride0, budget) ||
+      !row_stride_ok(entry_positions_out_stride0, budget))
     return QSA_ERR_STRIDE;
   const int64_t R = cache->num_reqs;
   if (R == 0) return QSA_OK;
@@ -659,8 +664,8 @@ extern "C" qsa_status qsa_evict_entries(
       !aligned(entry_positions_out, 4) || !aligned(error_word, 4))
     return QSA_ERR_ALIGN;
   const Span outs[5] = {rows_span(kept, R, budget, budget), span(new_lens, R * 4),
-                        rows_span(weight_sums_out, R, budget, budget),
-                        rows_span(entry_positions_out, R, budget, budget),
+                        rows_span(weight_sums_out, R, budget, weight_sums_out_stride0),
+                        rows_span(entry_positions_out, R, budget, entry_positions_out_stride0),
                         span(error_word, 4)};
   const Span ins[6] = {rows_span(weight_sums, R, entry_cols, weight_sums_stride0),
                        rows_span(entry_positions, R, entry_cols, entry_positions_stride0),
@@ -681,7 +686,9 @@ extern "C" qsa_status qsa_evict_entries(
   p.kept = kept;
   p.new_lens = new_lens;
   p.sums_out = weight_sums_out;
+  p.sums_out_s0 = weight_sums_out_stride0;
   p.pos_out = entry_positions_out;
+  p.pos_out_s0 = entry_positions_out_stride0;
   p.err = error_word;
   bind_calling_thread();
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -699,4 +706,16 @@ extern "C" qsa_status qsa_evict_entries(
   const dim3 grid((unsigned)std::min(ctas, wave), (unsigned)R);
   return launch_after(move_kernel, grid, dim3(kMoveThreads), 0, s, p) == cudaSuccess ? QSA_OK
                                                                                      : QSA_ERR_CUDA;
+}
+
+extern "C" qsa_status qsa_evict_entries(
+    const qsa_paged_cache* cache, const float* weight_sums, int64_t weight_sums_stride0,
+    const int32_t* entry_positions, int64_t entry_positions_stride0, int64_t entry_cols,
+    const int32_t* context_lens, int64_t budget, int64_t num_sink, int64_t num_recent,
+    int32_t* kept, int32_t* new_lens, float* weight_sums_out, int32_t* entry_positions_out,
+    uint32_t* error_word, qsa_stream_t stream) {
+  return qsa_evict_entries_strided(cache, weight_sums, weight_sums_stride0, entry_positions,
+                                   entry_positions_stride0, entry_cols, context_lens, budget,
+                                   num_sink, num_recent, kept, new_lens, weight_sums_out, budget,
+                                   entry_positions_out, budget, error_word, stream);
 }

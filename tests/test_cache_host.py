@@ -202,6 +202,27 @@ def test_evict_refusals(lib, over, status):
     assert _evict(lib, **over) == status
 
 
+def _evict_strided(lib, **over):
+    cache = _cache(over)
+    a = dict(cache=cache, sums=_addr(10), ss0=128, pos=_addr(11), ps0=128, ecols=128, ctx=_addr(12),
+             budget=32, sink=4, recent=8, kept=_addr(13), lens=_addr(14), so=_addr(15), so0=128,
+             po=_addr(16), po0=128, err=_addr(18), stream=None)
+    a.update(over)
+    return lib.qsa_evict_entries_strided(*a.values())
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(so0=31), STRIDE), (dict(po0=0), STRIDE), (dict(so0=-128), STRIDE), (dict(po0=1 << 39), STRIDE),
+    (dict(so=None), NULL), (dict(po=_addr(16) + 2), ALIGN), (dict(budget=0), CONTRACT),
+    (dict(so=_addr(10)), ALIAS), (dict(po=_addr(11)), ALIAS),
+    # between the other's rows: their extents overlap
+    (dict(so=_addr(10) + 128), ALIAS), (dict(po=_addr(15) + 256), ALIAS),
+    (dict(kept=_addr(15) + 3 * 512), ALIAS),
+])
+def test_evict_strided_refusals(lib, over, status):
+    assert _evict_strided(lib, **over) == status
+
+
 def test_evict_without_requests_is_a_noop(lib):
     assert _evict(lib, reqs=0) == 0
 
@@ -292,3 +313,30 @@ def test_a_workspace_that_holds_less_than_its_elements_is_refused(recorder, whic
     _workspace_calls(wide)[which]()                  # one that is what it says goes on
     (name, args), = recorder.calls
     assert args[args.index(wide.data_ptr()) + 1] == 200, name
+
+
+def test_evict_outputs_wider_than_the_budget(recorder):
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.float16)
+    bt, lens = torch.zeros((2, 2), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    sums, pos = torch.zeros((2, 32)), torch.zeros((2, 32), dtype=torch.int32)
+
+    def call(so, po):
+        return qsa.qsa_evict_entries(sums, pos, lens, k, k, bt, 24, weight_sums_out=so,
+                                     entry_positions_out=po)
+
+    so, po = torch.zeros((2, 40)), torch.zeros((2, 32), dtype=torch.int32)
+    assert call(so, po)[2:] == (so, po)
+    call(so[:, :24], po[:, 8:])
+    call(torch.zeros((2, 24)), torch.zeros(48, dtype=torch.int32))
+    got = [(a[12], a[13], a[14], a[15]) for _, a in recorder.calls]
+    assert got[0] == (so.data_ptr(), 40, po.data_ptr(), 32)
+    assert got[1] == (so.data_ptr(), 40, po.data_ptr() + 32, 32)
+    assert (got[2][1], got[2][3]) == (24, 24)
+    recorder.calls.clear()
+    for bad, status in ((torch.zeros((2, 23)), SHAPE), (torch.zeros((3, 24)), SHAPE),
+                        (torch.zeros(96), SHAPE), (torch.zeros((2, 32), dtype=torch.float64), DTYPE),
+                        (torch.zeros((32, 2)).t(), STRIDE)):
+        with pytest.raises(qsa.QSAError) as e:
+            call(bad, po)
+        assert e.value.status == status
+    assert not recorder.calls

@@ -747,6 +747,23 @@ def test_evict_bad_pages_contexts_and_positions():
     _check_evict(case, 20, 2, 2)
 
 
+@pytest.mark.parametrize("lens,budget", [([900, 1300, 20], 256), ([40000, 100], 3000)])
+def test_evict_into_wider_arrays(lens, budget):
+    case = _evict_case(lens, budget, 4, 32, seed=25)
+    k, v, tables, sums, pos, ctx = case
+    kk, vv = k.clone(), v.clone()
+    plain = _check_evict(case, budget, 4, 32)
+    so = torch.full((len(lens), sums.shape[1] + 3), 7.0, device=DEV)
+    po = torch.full((len(lens), sums.shape[1]), -9, dtype=torch.int32, device=DEV)
+    got = qsa.qsa_evict_entries(sums, pos, ctx, kk, vv, tables, budget, num_sink=4, num_recent=32,
+                                weight_sums_out=so[:, 1:], entry_positions_out=po)
+    assert got[2].data_ptr() == so[:, 1:].data_ptr() and got[3] is po
+    assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+    assert torch.equal(so[:, 1:budget + 1], plain[2]) and torch.equal(po[:, :budget], plain[3])
+    assert (so[:, 0] == 7).all() and (so[:, budget + 1:] == 7).all() and (po[:, budget:] == -9).all()
+    assert torch.equal(k, kk) and torch.equal(v, vv)
+
+
 def test_evict_strided_inputs_repeats_and_graph():
     lens, budget = [900, 1300], 256
     case = _evict_case(lens, budget, 4, 32, seed=24)
@@ -849,3 +866,73 @@ def test_bounded_cache_decode(dtype, cache):
                 top = int(newest[b])
                 assert {0, 1} <= held and set(range(max(0, top - 7), top + 1)) <= held
     assert evictions >= 3
+
+
+@pytest.mark.parametrize("each", [True, False])
+@pytest.mark.parametrize("dtype,cache,n", [(F16, F16, 1), (BF16, E4M3, 3), (BF16, BF16, 8)])
+def test_bounded_cache_decode_with_arrays_in_turn(dtype, cache, n, each):
+    """The loop that the README shows: the eviction writes the per-entry arrays that the next
+    step reads, nothing is copied between steps.  n new tokens a request and step; an eviction
+    each step, or when a request has no room for the next one."""
+    hq, hk, d, size, budget, cols, steps = 8, 2, 64, 16, 40, 4, 37 if n == 1 else 14
+    gen = torch.Generator(device=DEV).manual_seed(33)
+    lens0 = [45, 0, 52]
+    reqs, limit = len(lens0), cols * size
+    k_cache, v_cache = make_cache(reqs * cols, size, hk, d, cache, "split", gen)
+    tables = torch.randperm(reqs * cols, generator=torch.Generator().manual_seed(2)).view(
+        reqs, cols).to(torch.int32).to(DEV)
+    ks = vs = None
+    if cache == E4M3:
+        ks, vs = torch.full((2, hk), 0.02, device=DEV)
+    entry_positions = torch.arange(limit, dtype=torch.int32, device=DEV).repeat(reqs, 1)
+    sums = torch.rand((reqs, limit), generator=gen, device=DEV)
+    sums2, entry_positions2 = torch.empty_like(sums), torch.empty_like(entry_positions)
+    seen = torch.tensor(lens0, device=DEV)
+    lens = seen.to(torch.int32)
+    t2r = torch.arange(reqs, dtype=torch.int32, device=DEV).repeat_interleave(n)
+    j = torch.arange(n, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    evictions = 0
+    for step in range(steps):
+        k_new, v_new = _values((2, reqs * n, hk, d), dtype, gen)
+        entries = (lens.long()[:, None] + j).flatten()
+        positions = (seen[:, None] + j).flatten()
+        lens, seen = lens + n, seen + n
+        qsa.qsa_paged_append(k_new, v_new, k_cache, v_cache, tables, t2r, entries, k_scale=ks,
+                             v_scale=vs, positions=positions, entry_positions=entry_positions,
+                             weight_sums=sums, error_word=err)
+        for b in range(reqs):                  # the new tokens are there, and weigh nothing yet
+            at = slice(int(lens[b]) - n, int(lens[b]))
+            assert entry_positions[b, at].tolist() == positions.view(reqs, n)[b].tolist()
+            assert not sums[b, at].any()
+        q = _values((reqs * n, hq, d), dtype, gen)
+        old = sums.double().cpu().numpy()
+        r = C.attention(_f64(q), _f64(k_cache), _f64(v_cache), tables.cpu().numpy(), lens.tolist(),
+                        n, d ** -0.5, 0, _f64(ks), _f64(vs))
+        out = qsa.qsa_paged_attention(q, k_cache, v_cache, tables, lens, next_n=n, k_scale=ks,
+                                      v_scale=vs, weight_sums=sums, weight_sums_out=sums,
+                                      error_word=err)
+        c = Case.__new__(Case)
+        c.q, c.k, c.next_n = q, k_cache, n
+        tol, _, rel = bounds(c, r, limit)
+        assert (np.abs(_f64(out) - r["out"]) <= tol).all()
+        got = sums.double().cpu().numpy()
+        for b, m in enumerate(lens.tolist()):
+            want = old[b, :m] + r["weights"][b, :m]
+            assert (np.abs(got[b, :m] - want)
+                    <= rel * r["weights"][b, :m] + 2.0 ** -22 * want).all()
+        if not each and int(lens.max()) + n <= limit:
+            continue
+        evictions += int(lens.max()) > budget
+        w = C.evict(sums.cpu().numpy(), entry_positions.cpu().numpy(), lens.tolist(),
+                    tables.cpu().numpy(), size, k_cache.shape[0], budget, 2, 8)
+        wk, wv = (C.apply_moves(_f64(t), w[4], tables.cpu().numpy()) for t in (k_cache, v_cache))
+        kept, lens, _, _ = qsa.qsa_evict_entries(
+            sums, entry_positions, lens, k_cache, v_cache, tables, budget, num_sink=2, num_recent=8,
+            weight_sums_out=sums2, entry_positions_out=entry_positions2, error_word=err)
+        sums, sums2 = sums2, sums
+        entry_positions, entry_positions2 = entry_positions2, entry_positions
+        for g, e in zip((kept, lens, sums[:, :budget], entry_positions[:, :budget]), w):
+            assert np.array_equal(g.cpu().numpy(), e)
+        assert np.array_equal(_f64(k_cache), wk) and np.array_equal(_f64(v_cache), wv)
+    assert evictions >= 2 and int(err.item()) == 0
