@@ -567,6 +567,57 @@ def test_first_calls_inside_a_graph_capture():
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
 
 
+class Thin(Case):
+    """A case under a wide table: pages only where a request has tokens, the other
+    columns hold ids that may not be looked at."""
+
+    def __init__(self, lens, hq, hk, d, size, cols, dtype=F16, cache=None, **kw):
+        used = [-(-n // size) for n in lens]
+        total = sum(used)
+        super().__init__([total * size], hq, hk, d, size, dtype, cache, cols=total, spare=1, **kw)
+        tables = torch.full((len(lens), cols), 2 ** 31 - 1, dtype=torch.int32)
+        ids, at = self.tables[0].cpu(), 0
+        for b, n in enumerate(used):
+            tables[b, :n] = ids[at:at + n]
+            at += n
+        self.tables, self.lens = tables.to(DEV), lens
+        self.ctx = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        gen = torch.Generator(device=DEV).manual_seed(len(lens))
+        self.q = _values((len(lens) * self.next_n, hq, d), dtype, gen)
+
+
+@pytest.mark.parametrize("hq,hk,next_n", [(17, 1, 1), (32, 1, 1), (33, 1, 1), (64, 1, 1), (16, 2, 4),
+                                          (40, 1, 2)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_many_rows_of_heads_of_128(hq, hk, next_n, dtype):
+    check(Case([300, 17, 2], hq, hk, 128, 16, dtype, next_n=next_n, seed=hq), sums=True)
+    check(Case([2049, 3, 700, 0], hq, hk, 128, 64, dtype, next_n=next_n, window=1500, seed=hq + 1),
+          sums=True)
+
+
+@pytest.mark.parametrize("hk,rows,lens", [(76, 17, [1100, 40]), (100, 17, [1100]), (160, 17, [1100, 3]),
+                                          (40, 2, [1100, 9]), (320, 1, [90, 0, 33]), (1024, 2, [20])])
+def test_attention_more_heads_than_a_wave_holds(hk, rows, lens):
+    # two runs a head, one, more heads than CTAs; clusters past one wave; whole requests
+    check(Case(lens, hk * rows, hk, 64, 16, F16, seed=hk), sums=True)
+
+
+@pytest.mark.parametrize("size", [1024, 4096, 65536])
+@pytest.mark.parametrize("d,dtype,cache", [(64, BF16, BF16), (128, F16, E4M3), (256, F16, F16)])
+def test_attention_large_pages(d, dtype, cache, size):
+    check(Thin([5, size, size + 77], 3, 1, d, size, 4, dtype, cache, seed=size), sums=True)
+
+
+@pytest.mark.parametrize("rows", [2, 20])
+def test_attention_many_requests_of_a_long_table(rows):
+    # several launches of walk and join over one workspace; long requests at both sides of
+    # each launch's end
+    lens = [(7 * i) % 60 for i in range(1100)]
+    for b in (3, 500, 511, 512, 513, 1023, 1024, 1099):
+        lens[b] = 4000 + b
+    check(Thin(lens, rows, 1, 64, 64, 90, F16, seed=9), sums=True)
+
+
 # --- append ------------------------------------------------------------------------
 
 
@@ -722,6 +773,51 @@ def test_evict_short_requests_of_a_long_table(budget, kind):
     lens = [1, 2, 9, 10, 11, 17, 31, 33, 80]
     _check_evict(_evict_case(lens, budget, budget // 4, budget // 4, seed=budget, kind=kind,
                              cols=2100), budget, budget // 4, budget // 4)
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
+@pytest.mark.parametrize("reqs,cap,budget", [(2, 200704, 9000), (19, 200704, 700), (21, 100352, 20000),
+                                             (40, 50176, 5000), (78, 25088, 24000), (200, 25088, 64)])
+def test_evict_keys_outside_shared_memory(reqs, cap, budget, kind):
+    """Tables whose slices pass what a CTA's shared memory holds: clusters of 8, 4, 2 and 1.
+    A few long requests, one of them the whole table."""
+    gen = torch.Generator(device=DEV).manual_seed(reqs)
+    cpu = torch.Generator().manual_seed(reqs)
+    size = 512
+    lens = [(37 * b) % 100 for b in range(reqs)]
+    lens[0], lens[reqs // 2], lens[-1] = cap, budget + 1, cap - 12345
+    used = [-(-n // size) for n in lens]
+    k, v = make_cache(sum(used) + 1, size, 1, 64, F16, "split", gen)
+    ids, at = torch.randperm(sum(used) + 1, generator=cpu), 0
+    tables = torch.full((reqs, cap // size), -1, dtype=torch.int32)
+    for b, n in enumerate(used):
+        tables[b, :n] = ids[at:at + n]
+        at += n
+    if kind == "spread":
+        sums = torch.rand((reqs, cap), generator=cpu).pow(6)
+    elif kind == "ties":
+        sums = torch.randint(0, 3, (reqs, cap), generator=cpu).float()
+    else:
+        pick = torch.tensor([0.0, -0.0, 1.0, -1.0, float("inf"), -float("inf"), float("nan"), 1e-45,
+                             3e38, 1.0000001])
+        sums = pick[torch.randint(0, 10, (reqs, cap), generator=cpu)]
+    pos = torch.randperm(cap, generator=cpu).to(torch.int32).repeat(reqs, 1)
+    case = (k, v, tables.to(DEV), sums.to(DEV), pos.to(DEV),
+            torch.tensor(lens, dtype=torch.int32, device=DEV))
+    _check_evict(case, budget, 4, min(500, budget // 2))
+
+
+@pytest.mark.parametrize("size", [1024, 65536])
+def test_append_and_evict_large_pages(size):
+    lens, budget = [size + 40, 70, size], size - 5
+    k, v, tables, sums, pos, ctx = case = _evict_case(lens, budget, 2, 9, size, 1, 64, BF16, seed=size)
+    _check_evict(case, budget, 2, 9)
+    nk = _values((3, 1, 64), BF16, torch.Generator(device=DEV).manual_seed(1))
+    t2r = torch.arange(3, dtype=torch.int32, device=DEV)
+    ent = torch.tensor([size - 1, size, 2 * size - 1], device=DEV)
+    qsa.qsa_paged_append(nk, nk, k, v, tables, t2r, ent)
+    for i, e in enumerate(ent.tolist()):
+        assert torch.equal(k[int(tables[i, e // size]), e % size], nk[i])
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16, E4M3])
