@@ -558,6 +558,7 @@ def qsa_top_k_per_row_decode(logits, next_n: int, seq_lens, topk_tokens: int, ou
 
 _CACHE = struct.Struct("21q")       # qsa_paged_cache: 8-byte fields throughout
 _STRIDES3 = struct.Struct("3q")
+_MAX_ENTRIES = 1 << 30              # QSA_CACHE_MAX_ENTRIES
 
 
 def _cache_struct(k_cache, v_cache, block_tables, k_scale, v_scale) -> bytes:
@@ -796,8 +797,8 @@ def qsa_evict_entries(weight_sums, entry_positions, context_lens, k_cache, v_cac
             _need_tensor(t, what)
     device, dev = block_tables.get_device(), block_tables.device
     raw = _launch_stream(stream, device)
-    if budget < 1:
-        raise QSAError(6, "budget must be at least 1")
+    if not 1 <= budget <= _MAX_ENTRIES:    # before anything of that size is allocated
+        raise QSAError(6, f"budget must be 1 to {_MAX_ENTRIES}")
     if kept is None or new_lens is None or weight_sums_out is None or entry_positions_out is None:
         with _on_stream(stream, device):
             if kept is None:

@@ -340,3 +340,13 @@ def test_evict_outputs_wider_than_the_budget(recorder):
             call(bad, po)
         assert e.value.status == status
     assert not recorder.calls
+
+
+@pytest.mark.parametrize("budget", [0, -1, (1 << 30) + 1, 1 << 60, 1 << 70])
+def test_evict_budgets_are_refused_before_results_are_allocated(recorder, budget):
+    assert binding._MAX_ENTRIES == int(re.search(r"QSA_CACHE_MAX_ENTRIES (\d+)", open(HDR).read())[1])
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.float16)
+    bt, lens = torch.zeros((2, 2), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(qsa.QSAError) as e:
+        qsa.qsa_evict_entries(torch.zeros((2, 32)), bt.repeat(1, 16), lens, k, k, bt, budget)
+    assert e.value.status == CONTRACT and not recorder.calls
