@@ -51,8 +51,9 @@ extern "C" {
  *
  *   dtype         QSA_DT_F16, QSA_DT_BF16 or QSA_DT_F8E4M3
  *   head_dim      64, 128 or 256
- *   k_scale, v_scale  fp32 [num_heads] or NULL (all 1): an element stands for
- *                 its value times its head's scale; QSA_DT_F8E4M3 only
+ *   k_scale, v_scale  fp32 [num_heads] or NULL (all 1), each from 2^-64 to
+ *                 2^64: an element stands for its value times its head's
+ *                 scale; QSA_DT_F8E4M3 only
  *   block_tables  int32 [num_reqs, table_cols] (num_reqs <=
  *                 QSA_CACHE_MAX_REQS), row stride table_stride0,
  *                 column stride 1; a page id outside [0, num_pages) makes its
@@ -145,6 +146,16 @@ QSA_API size_t qsa_paged_attention_workspace_bytes(const qsa_paged_cache* cache,
  * entries that a row sees have to be finite there; the results are the same bit
  * for bit each time a call is repeated on one kind of GPU.
  *
+ * The weights enter the product with V rounded, relative to themselves, by 2^-22
+ * (FP16) or 2^-16 (BF16) where next_n * num_heads / cache->num_heads is 32 or less
+ * and the cache is not E4M3; by 2^-12 (FP16, and any E4M3 cache) or 2^-9 (BF16)
+ * elsewhere.  lse and weight sums do not carry that rounding.
+ *
+ * Weight sums need every logit until its row is complete: num_reqs * next_n *
+ * num_heads * table_cols * page_size * 4 bytes of workspace, whatever the
+ * contexts and the window (64 requests, 32 heads, a table of 131072 entries: 1.1
+ * GB).  A table cut to the columns that the longest context needs keeps it small.
+ *
  * Arguments
  *   q             [num_reqs*next_n, num_heads, head_dim], dtype QSA_DT_F16 or
  *                 QSA_DT_BF16, the cache's own unless it is E4M3; strides in
@@ -200,6 +211,10 @@ QSA_API qsa_status qsa_paged_attention(
  * behind the budget in its per-entry arrays: qsa_evict_entries_strided.)  A page that holds entries below `budget` must belong to one request
  * alone.  An entry whose page is absent still counts; its K and V are not
  * moved (QSA_DERR_KV_PAGE).
+ *
+ * An eviction renumbers entries.  What holds token numbers of its own stays as it
+ * was: a cache that qsa_sparse_attention reads through selected token numbers, or
+ * whose compressed keys the selection scores, must not be evicted from.
  *
  * Arguments
  *   weight_sums       fp32 [num_reqs, entry_cols], row stride weight_sums_stride0

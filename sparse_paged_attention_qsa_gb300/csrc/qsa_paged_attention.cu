@@ -7,8 +7,9 @@
 // leaves the logits (binary32, base 2) in the workspace and weights_kernel
 // reads them back, 8 bytes a head beside the 2 * dim * esize * kv_heads that
 // K and V take: 6 % for four heads of 128 on a 16-bit K/V head.  (Reading K
-// again instead would be half of the whole.)  Each entry's sum is one thread's,
-// in row and head order, so it does not change from run to run.
+// again instead would be half of the whole.)  Up to eight warps each add a part of
+// an entry's (row, head) pairs in order, and the parts are added in warp order, so
+// the sum does not change from run to run.
 #include "qsa_cache.h"
 #include "qsa_cache_host.h"
 #include "qsa_device.cuh"

@@ -22,7 +22,8 @@ enum PagedMode : int32_t {
   kPagedCluster,   // up to 8 equal runs a K/V head, one cluster, joined through its shared memory
 };
 // A request whose K and V of one head take no more than this is not cut: a CTA
-// streams it in about the time that a second launch takes.  And where a K/V
+// streams it in about the time that a second launch takes (a cluster, which needs
+// none, was not tried below this size).  And where a K/V
 // head's requests take no more than that for each CTA of a cluster, up to 16
 // query rows are walked by one.
 constexpr int64_t kPagedWholeBytes = 256 << 10;

@@ -21,9 +21,13 @@
 //   tile: WM sets of 16 query rows by WK slices of its tokens.
 //   Each warp keeps its rows' reference, sum and output in registers: S = Q K^T
 //   and P V by mma.sync.m16n8k16 (binary32 accumulation) on fragments that
-//   ldmatrix reads from the ring.  (tcgen05 needs 64 or 128 rows and a round
-//   trip through tensor memory for the softmax; with at most 16 rows as a
-//   rule mma.sync is a third busy at the memory's rate.)  At a request's end,
+//   ldmatrix reads from the ring.  (With at most 16 rows as a rule mma.sync is
+//   a third busy at the memory's rate.  From 17 rows on it is not: every set of 16
+//   reads, and for E4M3 converts, the tile again, 64 rows at 0.56 to 0.68 of the
+//   copy rate, 0.25 to 0.30 for E4M3.  tcgen05 with the tokens, then the head's
+//   dims, as M and the query rows as N could share the tile; it has not been
+//   built, so what its softmax by columns and the staging of the weights cost is not
+//   known.)  At a request's end,
 //   or the run's, the slices merge through shared memory into the output, or
 //   into a piece in the workspace when the K/V head's entries are cut.
 // paged_join_kernel  joins a cut K/V head's pieces.
