@@ -1032,3 +1032,74 @@ def test_bounded_cache_decode_with_arrays_in_turn(dtype, cache, n, each):
             assert np.array_equal(g.cpu().numpy(), e)
         assert np.array_equal(_f64(k_cache), wk) and np.array_equal(_f64(v_cache), wv)
     assert evictions >= 2 and int(err.item()) == 0
+
+
+def test_bounded_cache_decode_in_two_graphs():
+    """The README's loop captured: one graph for each direction of the per-entry arrays and of the
+    lengths, replayed in turn, against the same steps run one by one."""
+    hq, hk, d, size, budget, cols, steps = 8, 2, 128, 16, 300, 24, 7
+    lens0 = [300, 12, 331]
+    reqs, limit = len(lens0), cols * size
+    gen = torch.Generator(device=DEV).manual_seed(41)
+    k0, v0 = make_cache(reqs * cols, size, hk, d, F16, "split", gen)
+    tables = torch.randperm(reqs * cols, generator=torch.Generator().manual_seed(3)).view(
+        reqs, cols).to(torch.int32).to(DEV)
+    t2r = torch.arange(reqs, dtype=torch.int32, device=DEV)
+    new = _values((steps, 2, reqs, hk, d), F16, gen)
+    qs = _values((steps, reqs, hq, d), F16, gen)
+    sums0 = torch.rand((reqs, limit), generator=gen, device=DEV)
+
+    class State:
+        def __init__(self):
+            self.k, self.v = k0.clone(), v0.clone()
+            self.seen = torch.tensor(lens0, device=DEV)
+            self.lens = [self.seen.to(torch.int32), torch.zeros(reqs, dtype=torch.int32, device=DEV)]
+            self.sums = [sums0.clone(), torch.full_like(sums0, 9.0)]
+            self.pos = [torch.arange(limit, dtype=torch.int32, device=DEV).repeat(reqs, 1),
+                        torch.full((reqs, limit), -5, dtype=torch.int32, device=DEV)]
+            self.new, self.q = new[0].clone(), qs[0].clone()
+
+        def step(self, way):
+            lens, sums, pos = self.lens[way], self.sums[way], self.pos[way]
+            entries = lens.long()
+            lens += 1
+            qsa.qsa_paged_append(self.new[0], self.new[1], self.k, self.v, tables, t2r, entries,
+                                 positions=self.seen, entry_positions=pos, weight_sums=sums)
+            self.seen += 1
+            out = qsa.qsa_paged_attention(self.q, self.k, self.v, tables, lens, weight_sums=sums,
+                                          weight_sums_out=sums)
+            kept = qsa.qsa_evict_entries(
+                sums, pos, lens, self.k, self.v, tables, budget, num_sink=2, num_recent=8,
+                new_lens=self.lens[1 - way], weight_sums_out=self.sums[1 - way],
+                entry_positions_out=self.pos[1 - way])[0]
+            return out, kept
+
+        def feed(self, i):
+            self.new.copy_(new[i])
+            self.q.copy_(qs[i])
+
+        def all(self):
+            return [self.k, self.v, self.seen, *self.lens, *self.sums, *self.pos]
+
+    eager, want = State(), []
+    for i in range(steps):
+        eager.feed(i)
+        want.append([t.clone() for t in eager.step(i % 2)])
+    torch.cuda.synchronize()
+    s, graphs, results = State(), [], []
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for way in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                results.append(s.step(way))
+            graphs.append(g)
+    torch.cuda.synchronize()
+    for i in range(steps):                      # nothing waits between the replays
+        s.feed(i)
+        graphs[i % 2].replay()
+        want_out, want_kept = want[i]
+        out, kept = results[i % 2]
+        assert torch.equal(out, want_out) and torch.equal(kept, want_kept)
+    assert all(torch.equal(a, b) for a, b in zip(s.all(), eager.all()))
+    assert eager.lens[steps % 2].tolist() == [budget, 12 + steps, budget]
