@@ -208,9 +208,10 @@ QSA_API qsa_status qsa_paged_attention(
  *                  of that entry; 0 and -1 for i >= new_lens[b]
  *
  * The inputs are not written.  (A next step that appends and attends needs room
- * behind the budget in its per-entry arrays: qsa_evict_entries_strided.)  A page that holds entries below `budget` must belong to one request
- * alone.  An entry whose page is absent still counts; its K and V are not
- * moved (QSA_DERR_KV_PAGE).
+ * behind the budget in its per-entry arrays: qsa_evict_entries_strided.)  A page
+ * that holds entries below `budget` must belong to one request alone.  An entry
+ * whose page is absent still counts; its K and V are not moved
+ * (QSA_DERR_KV_PAGE).
  *
  * An eviction renumbers entries.  What holds token numbers of its own stays as it
  * was: a cache that qsa_sparse_attention reads through selected token numbers, or
