@@ -48,7 +48,9 @@ EXPORTED = ("qsa_status_string", "qsa_version", "qsa_select_workspace_bytes",
             "qsa_select_paged_tokens_static_scratch", "qsa_build_metadata",
             "qsa_paged_mqa_logits", "qsa_top_k_per_row_decode",
             "qsa_paged_append", "qsa_paged_attention_workspace_bytes", "qsa_paged_attention",
-            "qsa_evict_entries", "qsa_evict_entries_strided")
+            "qsa_evict_entries", "qsa_evict_entries_strided",
+            "qsa_qk_norm_rope", "qsa_chunk_attention_workspace_bytes", "qsa_chunk_attention",
+            "qsa_prefix_attention")
 
 
 class QSAError(RuntimeError):
@@ -198,6 +200,20 @@ def declare_signatures(lib):
     lib.qsa_evict_entries_strided.restype = ctypes.c_int
     lib.qsa_evict_entries_strided.argtypes = [
         vp, vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, i64, vp, i64, vp, vp]
+    lib.qsa_qk_norm_rope.restype = ctypes.c_int
+    lib.qsa_qk_norm_rope.argtypes = [
+        vp, vp, ctypes.c_int, i64, i64, i64, i64, vp, vp, vp, vp, ctypes.c_int, ctypes.c_float,
+        vp, vp, i64, ctypes.c_int, vp, vp, vp, vp, vp]
+    lib.qsa_chunk_attention_workspace_bytes.restype = sz
+    lib.qsa_chunk_attention_workspace_bytes.argtypes = [vp, i64, i64, i64]
+    lib.qsa_chunk_attention.restype = ctypes.c_int
+    lib.qsa_chunk_attention.argtypes = [
+        vp, vp, ctypes.c_int, i64, i64, vp, vp, vp, ctypes.c_float, i64, i64,
+        vp, vp, vp, vp, sz, vp, vp]
+    lib.qsa_prefix_attention.restype = ctypes.c_int
+    lib.qsa_prefix_attention.argtypes = [
+        vp, vp, i64, vp, vp, ctypes.c_int, i64, i64, vp, vp, vp, ctypes.c_float,
+        vp, vp, vp, vp, sz, vp, vp]
     return full
 
 
@@ -820,3 +836,149 @@ def qsa_evict_entries(weight_sums, entry_positions, context_lens, k_cache, v_cac
         _flat(new_lens, torch.int32, reqs, "new_lens"), souts, souts_s0, pouts, pouts_s0,
         _word(error_word), raw))
     return kept, new_lens, weight_sums_out, entry_positions_out
+
+
+# --- norms with rotation (include/qsa_rope.h), attention of ragged chunks
+# --- (include/qsa_chunk.h) --------------------------------------------------------
+
+
+def qsa_qk_norm_rope(q, k, positions, q_weight=None, k_weight=None, *, inv_freq=None,
+                     eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None,
+                     stream=None):
+    """Root-mean-square norm of every head of q [T, q_heads, dim] and k [T,
+    k_heads, dim] (None: queries alone) with weights [dim], then the rotation of
+    its first 2 * len(inv_freq) elements by the token's position (int64 [T]; a
+    negative one leaves the token's outputs as they were), in one pass
+    (include/qsa_rope.h).  Pairs lie half the rotated elements apart, or side by
+    side with interleaved.  Returns (q_out, k_out); q_out=q, k_out=k work in
+    place."""
+    lib = _lib or load_library()
+    _on_current_device(q, k, positions, q_weight, k_weight, inv_freq, q_out, k_out)
+    if q.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[::2] != q.shape[::2])):
+        raise QSAError(3, "q [tokens, heads, dim] and k [tokens, heads, dim] expected")
+    T, hq, dim = q.shape
+    dtype, wdtype = q.dtype, DT_F32
+    if k is not None and k.dtype != dtype:
+        raise QSAError(2, "q and k dtypes differ")
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    for w in weights:
+        if w.dtype != weights[0].dtype or w.dtype not in (dtype, torch.float32):
+            raise QSAError(2, "weights must be of q's dtype or float32, both the same")
+        if w.numel() != dim or not w.is_contiguous():
+            raise QSAError(3, "weights must be contiguous [dim]")
+        wdtype = _tag(w)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _flat(inv_freq, torch.float32, rot // 2, "inv_freq")
+    for t, like, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t is not None and (like is None or t.shape != like.shape):
+            raise QSAError(3, f"{what} must have its input's shape")
+        if t is not None and t.dtype != dtype:
+            raise QSAError(2, f"{what} must have q's dtype")
+    device = q.get_device()
+    if q_out is None or (k is not None and k_out is None):
+        with _on_stream(stream, device):
+            if q_out is None:
+                q_out = torch.empty((T, hq, dim), dtype=dtype, device=q.device)
+            if k is not None and k_out is None:
+                k_out = torch.empty(k.shape, dtype=dtype, device=q.device)
+    none = _STRIDES3.pack(0, 0, 1)
+    _check(lib.qsa_qk_norm_rope(
+        q.data_ptr(), 0 if k is None else k.data_ptr(), _tag(q), T, hq,
+        0 if k is None else k.shape[1], dim, _STRIDES3.pack(*q.stride()),
+        none if k is None else _STRIDES3.pack(*k.stride()),
+        0 if q_weight is None else q_weight.data_ptr(),
+        0 if k_weight is None else k_weight.data_ptr(), wdtype, eps,
+        _flat(positions, torch.int64, T, "positions"),
+        0 if inv_freq is None else inv_freq.data_ptr(), rot, bool(interleaved),
+        q_out.data_ptr(), 0 if k is None else k_out.data_ptr(), _STRIDES3.pack(*q_out.stride()),
+        none if k is None else _STRIDES3.pack(*k_out.stride()), _launch_stream(stream, device)))
+    return q_out, k_out
+
+
+def qsa_chunk_attention_workspace_bytes(k_cache, v_cache, block_tables, *, num_tokens: int,
+                                        num_heads: int, prefix_cols: int = -1) -> int:
+    """Bytes of workspace that qsa_chunk_attention (prefix_cols -1) or
+    qsa_prefix_attention needs for up to num_tokens new tokens over this cache."""
+    return int(load_library().qsa_chunk_attention_workspace_bytes(
+        _cache_struct(k_cache, v_cache, block_tables, None, None), num_tokens, num_heads,
+        prefix_cols))
+
+
+def _chunk_call(fn, lib, prefix, q, k_cache, v_cache, block_tables, query_start_loc, context_lens,
+                scale, rule, k_scale, v_scale, out, lse, workspace, error_word, stream):
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[-1]:
+        raise QSAError(3, "q must be [tokens, heads, dim] of the cache's dim")
+    cache = _cache_struct(k_cache, v_cache, block_tables, k_scale, v_scale)
+    rows, heads, dim = q.shape
+    reqs = block_tables.shape[0]
+    starts = _flat(query_start_loc, torch.int32, reqs + 1, "query_start_loc")
+    ctx = _flat(context_lens, torch.int32, reqs, "context_lens")
+    lse_ptr, word = _flat(lse, torch.float32, rows * heads, "lse"), _word(error_word)
+    device = q.get_device()
+    raw = _launch_stream(stream, device)
+    if out is None:
+        with _on_stream(stream, device):
+            out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
+    if out.dtype != q.dtype:
+        raise QSAError(2, "out must have q's dtype")
+    if out.shape != q.shape:
+        raise QSAError(3, "out must have q's shape")
+    if workspace is None:
+        need = lib.qsa_chunk_attention_workspace_bytes(cache, rows, heads,
+                                                       prefix[1] if prefix else -1)
+        ws = _raw_alloc(need, raw) if need else 0      # as in qsa_paged_attention
+    else:
+        ws, need = workspace.data_ptr(), _workspace_bytes(workspace)
+    try:
+        status = fn(cache, *prefix, q.data_ptr(), _tag(q), rows, heads,
+                    _STRIDES3.pack(*q.stride()), starts, ctx,
+                    dim ** -0.5 if scale is None else scale, *rule, out.data_ptr(),
+                    _STRIDES3.pack(*out.stride()), lse_ptr, ws, need, word, raw)
+    finally:
+        if workspace is None and ws:
+            _raw_free(ws)
+    _check(status)
+    return out
+
+
+def qsa_chunk_attention(q, k_cache, v_cache, block_tables, query_start_loc, context_lens, *,
+                        scale: float | None = None, window: int = 0, num_sink: int = 0,
+                        k_scale=None, v_scale=None, out=None, lse=None, workspace=None,
+                        error_word=None, stream=None):
+    """Attention of ragged chunks of new tokens, q [tokens, heads, dim], over
+    their requests' cached entries (include/qsa_chunk.h): request b's are the
+    rows [query_start_loc[b], query_start_loc[b+1]) (int32 [requests + 1]), the
+    last of its context_lens[b] (int32) entries.  A token sees the entries up to
+    its own, with a window the last `window` of them and the first num_sink.
+    scale: 1/sqrt(dim) unless given.  lse: fp32 [tokens, heads], filled when
+    given.  Rows of no request are left as they were.  Returns out."""
+    lib = _lib or load_library()
+    _on_current_device(q, k_cache, v_cache, block_tables, query_start_loc, context_lens, k_scale,
+                       v_scale, out, lse, workspace, error_word)
+    return _chunk_call(lib.qsa_chunk_attention, lib, (), q, k_cache, v_cache, block_tables,
+                       query_start_loc, context_lens, scale, (window, num_sink), k_scale, v_scale,
+                       out, lse, workspace, error_word, stream)
+
+
+def qsa_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_len, block_tables,
+                         query_start_loc, context_lens, *, scale: float | None = None,
+                         k_scale=None, v_scale=None, out=None, lse=None, workspace=None,
+                         error_word=None, stream=None):
+    """qsa_chunk_attention where every row sees besides the entries [0,
+    prefix_len) (int32 [1]) of prefix_table (int32 [columns]), which the batch
+    shares and which are read once for all of it (include/qsa_chunk.h);
+    block_tables and context_lens count what lies behind the prefix."""
+    lib = _lib or load_library()
+    _on_current_device(q, k_cache, v_cache, prefix_table, prefix_len, block_tables,
+                       query_start_loc, context_lens, k_scale, v_scale, out, lse, workspace,
+                       error_word)
+    if prefix_table.dim() != 1:
+        raise QSAError(3, "prefix_table must be 1-D")
+    cols = prefix_table.shape[0]
+    prefix = (_flat(prefix_table, torch.int32, cols, "prefix_table"), cols,
+              _flat(prefix_len, torch.int32, 1, "prefix_len"))
+    return _chunk_call(lib.qsa_prefix_attention, lib, prefix, q, k_cache, v_cache, block_tables,
+                       query_start_loc, context_lens, scale, (), k_scale, v_scale, out, lse,
+                       workspace, error_word, stream)

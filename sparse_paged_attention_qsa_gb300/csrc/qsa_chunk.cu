@@ -1,0 +1,228 @@
+// qsa_chunk.cu -- attention of ragged chunks of new tokens over the paged K/V
+// cache, declared in include/qsa_chunk.h.
+#include "qsa_chunk_attn.h"
+#include "qsa_cache_host.h"
+#include "qsa_device.cuh"
+#include "qsa_host.h"
+#include "qsa_internal.h"
+#include "qsa_chunk.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+namespace qsa {
+namespace {
+
+constexpr int kRowWarps = 4;
+
+// A CTA for each row and head: its warps take every fourth entry each, a lane
+// D/32 dims, and join their sums.
+template <typename T, typename CT, int D>
+__global__ void __launch_bounds__(kRowWarps * 32) chunk_row_kernel(const ChunkParams p) {
+  constexpr int N = D / 32;
+  __shared__ float s_m[kRowWarps], s_l[kRowWarps], s_o[kRowWarps][D];
+  const int t = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = h / p.group;
+  if (t < p.starts[0] || t >= p.starts[p.c.num_reqs]) return;
+  int b = 0, up = p.c.num_reqs - 1;
+  while (b < up) {
+    const int mid = (b + up + 1) >> 1;
+    if (p.starts[mid] <= t) b = mid; else up = mid - 1;
+  }
+  const int start = max(p.starts[b], 0), n = min(p.starts[b + 1], p.tokens) - start;
+  const int ctx = max(p.ctx[b], 0), h0 = ctx - n + (t - start) + 1;
+  const int hi = min(max(h0, 0), p.c.cap);
+  const int lo = p.window > 0 ? min(max(h0 - p.window, 0), p.c.cap) : 0;
+  if (ctx > p.c.cap && threadIdx.x == 0) report(p.err, QSA_DERR_CONTEXT);
+  int prefix = p.prefix_table ? max(*p.prefix_len, 0) : 0;
+  if (prefix > p.prefix_cap) {
+    prefix = p.prefix_cap;
+    if (threadIdx.x == 0) report(p.err, QSA_DERR_CONTEXT);
+  }
+  const T* q = reinterpret_cast<const T*>(p.q + t * p.q_row + h * p.q_head);
+  float x[N], o[N], m = -INFINITY, l = 0.f;
+  const float ks = p.c.k_scale ? p.c.k_scale[kvh] : 1.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = (float)q[lane * N + i];
+    o[i] = 0.f;
+  }
+  for (int part = 0; part < 2; ++part) {
+    const int32_t* table = part ? p.c.bt + b * p.c.bt_s0 : p.prefix_table;
+    const int end = part ? hi : prefix;
+    for (int e = warp; e < end; e += kRowWarps) {
+      if (part && e >= p.sink && e < lo) {
+        e += (lo - e) / kRowWarps * kRowWarps;
+        if (e < lo) continue;
+      }
+      const int id = table[e >> p.c.page_log2];
+      if (id < 0 || id >= p.c.num_pages) {
+        if (lane == 0) report(p.err, QSA_DERR_KV_PAGE);
+        continue;
+      }
+      const int slot = e & ((1 << p.c.page_log2) - 1);
+      const CT* k = reinterpret_cast<const CT*>(p.c.k + id * p.c.k_page + slot * p.c.k_token +
+                                                kvh * p.c.k_head);
+      const CT* v = reinterpret_cast<const CT*>(p.c.v + id * p.c.v_page + slot * p.c.v_token +
+                                                kvh * p.c.v_head);
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) z = fmaf(x[i], (float)k[lane * N + i], z);
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
+      z *= p.scale_log2 * ks;
+      const float mn = fmaxf(m, z), a = exp2f(m - mn), w = exp2f(z - mn);
+      m = mn;
+      l = l * a + w;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = o[i] * a + w * (float)v[lane * N + i];
+    }
+  }
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) s_o[warp][lane * N + i] = o[i];
+  __syncthreads();
+  if (warp != 0) return;
+  float M = -INFINITY, L = 0.f;
+  for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, s_m[w]);
+  float f[kRowWarps];
+  for (int w = 0; w < kRowWarps; ++w) {
+    f[w] = M == -INFINITY ? 0.f : exp2f(s_m[w] - M);
+    L += s_l[w] * f[w];
+  }
+  const float inv = L == 0.f ? 0.f : (p.c.v_scale ? p.c.v_scale[kvh] : 1.f) / L;
+  T* out = reinterpret_cast<T*>(p.out + t * p.out_row + h * p.out_head);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float v = 0.f;
+    for (int w = 0; w < kRowWarps; ++w) v += s_o[w][lane * N + i] * f[w];
+    out[lane * N + i] = (T)(v * inv);
+  }
+  if (lane == 0 && p.lse)
+    p.lse[(int64_t)t * p.heads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+}
+
+template <typename T, typename CT>
+void launch_rows(const ChunkParams& p, cudaStream_t st) {
+  const dim3 grid((unsigned)p.tokens, (unsigned)p.heads);
+  switch (p.c.dim) {
+    case 64: chunk_row_kernel<T, CT, 64><<<grid, kRowWarps * 32, 0, st>>>(p); break;
+    case 128: chunk_row_kernel<T, CT, 128><<<grid, kRowWarps * 32, 0, st>>>(p); break;
+    default: chunk_row_kernel<T, CT, 256><<<grid, kRowWarps * 32, 0, st>>>(p);
+  }
+}
+
+bool sizes_ok(const qsa_paged_cache& c, int64_t tokens, int64_t heads) {
+  return tokens >= 0 && tokens <= QSA_CHUNK_MAX_TOKENS && heads >= 1 && heads <= 65535 &&
+         heads % c.num_heads == 0 && tokens * heads <= INT32_MAX;
+}
+
+qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* prefix_table,
+                  int64_t prefix_cols, const int32_t* prefix_len, const void* q, qsa_dtype dtype,
+                  int64_t tokens, int64_t heads, const int64_t* q_strides, const int32_t* starts,
+                  const int32_t* ctx, float scale, int64_t window, int64_t sink, void* out,
+                  const int64_t* out_strides, float* lse, void* workspace, size_t workspace_bytes,
+                  uint32_t* error_word, qsa_stream_t stream) {
+  using namespace cache_host;
+  ChunkParams p{};
+  CacheSpans cs{};
+  const qsa_status st = check_cache(cache, &p.c, &cs);
+  if (st != QSA_OK) return st;
+  if (dtype != QSA_DT_F16 && dtype != QSA_DT_BF16) return QSA_ERR_DTYPE;
+  if (cache->dtype != QSA_DT_F8E4M3 && cache->dtype != dtype) return QSA_ERR_DTYPE;
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!(std::isfinite(scale_log2) && scale > 0.f) || window < 0 || sink < 0) return QSA_ERR_CONTRACT;
+  const int64_t R = cache->num_reqs;
+  if (!sizes_ok(*cache, tokens, heads)) return QSA_ERR_SHAPE;
+  if (prefix && (prefix_cols < 0 || prefix_cols > INT32_MAX)) return QSA_ERR_SHAPE;
+  if (!q_strides || !out_strides) return QSA_ERR_NULL;
+  const int64_t shape[3] = {tokens, heads, cache->head_dim};
+  if (!strides_ok(shape, q_strides, 3, 2) || !strides_ok(shape, out_strides, 3, 2) ||
+      !separate(shape, out_strides, 3))
+    return QSA_ERR_STRIDE;
+  if (R == 0 || tokens == 0) return QSA_OK;
+  const int64_t qx = extent(shape, q_strides, 3, 2), ox = extent(shape, out_strides, 3, 2);
+  if (qx < 0 || ox < 0) return QSA_ERR_STRIDE;
+  if (!q || !out || !starts || !ctx) return QSA_ERR_NULL;
+  if (prefix && (!prefix_len || (prefix_cols > 0 && !prefix_table))) return QSA_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(starts, 4) || !aligned(ctx, 4) ||
+      !aligned(lse, 4) || !aligned(error_word, 4) ||
+      (prefix && (!aligned(prefix_table, 4) || !aligned(prefix_len, 4))))
+    return QSA_ERR_ALIGN;
+  const Span outs[4] = {span(out, ox), span(lse, tokens * heads * 4), span(error_word, 4),
+                        span(workspace, 0)};
+  const Span ins[10] = {span(q, qx), cs.k, cs.v, cs.tables, cs.k_scale, cs.v_scale,
+                        span(starts, (R + 1) * 4), span(ctx, R * 4),
+                        prefix ? span(prefix_table, prefix_cols * 4) : Span{},
+                        prefix ? span(prefix_len, 4) : Span{}};
+  if (any_overlap(outs, 4, ins, 10)) return QSA_ERR_ALIAS;
+  if (!aligned(workspace, 256)) return QSA_ERR_ALIGN;
+  const int64_t pcap = prefix ? prefix_cols << p.c.page_log2 : 0;
+  p.prefix_table = prefix && prefix_cols > 0 ? prefix_table : nullptr;
+  p.prefix_cap = (int32_t)std::min<int64_t>(pcap, kMaxEntries);
+  p.prefix_len = prefix_len;
+  p.q = static_cast<const unsigned char*>(q);
+  p.q_row = tokens > 1 ? q_strides[0] * 2 : 0;
+  p.q_head = heads > 1 ? q_strides[1] * 2 : 0;
+  p.out = static_cast<unsigned char*>(out);
+  p.out_row = tokens > 1 ? out_strides[0] * 2 : 0;
+  p.out_head = heads > 1 ? out_strides[1] * 2 : 0;
+  p.starts = starts;
+  p.ctx = ctx;
+  p.tokens = (int32_t)tokens;
+  p.heads = (int32_t)heads;
+  p.group = (int32_t)(heads / cache->num_heads);
+  p.scale_log2 = scale_log2;
+  p.window = (int32_t)std::min<int64_t>(window, INT32_MAX - 16);
+  p.sink = (int32_t)std::min<int64_t>(sink, kMaxEntries);
+  p.lse = lse;
+  p.err = error_word;
+  bind_calling_thread();
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == QSA_DT_BF16;
+  if (cache->dtype == QSA_DT_F8E4M3)
+    bf16 ? launch_rows<__nv_bfloat16, __nv_fp8_e4m3>(p, s) : launch_rows<__half, __nv_fp8_e4m3>(p, s);
+  else
+    bf16 ? launch_rows<__nv_bfloat16, __nv_bfloat16>(p, s) : launch_rows<__half, __half>(p, s);
+  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace qsa
+
+extern "C" size_t qsa_chunk_attention_workspace_bytes(const qsa_paged_cache* cache,
+                                                      int64_t num_tokens, int64_t num_heads,
+                                                      int64_t prefix_cols) {
+  (void)cache, (void)num_tokens, (void)num_heads, (void)prefix_cols;
+  return 0;
+}
+
+extern "C" qsa_status qsa_chunk_attention(
+    const qsa_paged_cache* cache, const void* q, qsa_dtype dtype, int64_t num_tokens,
+    int64_t num_heads, const int64_t q_strides[3], const int32_t* query_start_loc,
+    const int32_t* context_lens, float scale, int64_t window, int64_t num_sink, void* out,
+    const int64_t out_strides[3], float* lse, void* workspace, size_t workspace_bytes,
+    uint32_t* error_word, qsa_stream_t stream) {
+  return qsa::attend(cache, false, nullptr, 0, nullptr, q, dtype, num_tokens, num_heads, q_strides,
+                     query_start_loc, context_lens, scale, window, num_sink, out, out_strides, lse,
+                     workspace, workspace_bytes, error_word, stream);
+}
+
+extern "C" qsa_status qsa_prefix_attention(
+    const qsa_paged_cache* cache, const int32_t* prefix_table, int64_t prefix_cols,
+    const int32_t* prefix_len, const void* q, qsa_dtype dtype, int64_t num_tokens,
+    int64_t num_heads, const int64_t q_strides[3], const int32_t* query_start_loc,
+    const int32_t* context_lens, float scale, void* out, const int64_t out_strides[3], float* lse,
+    void* workspace, size_t workspace_bytes, uint32_t* error_word, qsa_stream_t stream) {
+  return qsa::attend(cache, true, prefix_table, prefix_cols, prefix_len, q, dtype, num_tokens,
+                     num_heads, q_strides, query_start_loc, context_lens, scale, 0, 0, out,
+                     out_strides, lse, workspace, workspace_bytes, error_word, stream);
+}
