@@ -2,6 +2,7 @@
 // cache, declared in include/qsa_chunk.h.
 #include "qsa_chunk_attn.h"
 #include "qsa_cache_host.h"
+#include "qsa_cache_map.h"
 #include "qsa_device.cuh"
 #include "qsa_host.h"
 #include "qsa_internal.h"
@@ -120,6 +121,40 @@ void launch_rows(const ChunkParams& p, cudaStream_t st) {
   }
 }
 
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// The workspace: the plan of a call's row tiles, the pieces of those that runs
+// cut (at most two a run), and with a prefix the results of both lists.
+struct Layout {
+  int64_t max_tiles, part_rows;
+  size_t tiles, pos, first, cuts, part_ml, part_o, res_ml[2], res_o[2], total;
+};
+Layout layout_of(const qsa_paged_cache& c, int64_t tokens, int64_t heads, bool prefix) {
+  const int64_t rows = tokens * (heads / c.num_heads), rt = chunk_rows((int)c.head_dim);
+  const int64_t tiles = (rows + rt - 1) / rt;
+  Layout l;
+  l.max_tiles = tiles + std::min(c.num_reqs, tokens) + (prefix ? tiles : 0);
+  l.part_rows = std::min(rows, rt);
+  size_t at = round256(sizeof(ChunkPlan));
+  const auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at += round256(bytes);
+    return x;
+  };
+  l.tiles = take((size_t)l.max_tiles * sizeof(ChunkTile));
+  l.pos = take((size_t)(l.max_tiles + 1) * 8);
+  l.first = take((size_t)c.num_reqs * 4);
+  l.cuts = take(kChunkMaxCtas * sizeof(int2));
+  l.part_ml = take((size_t)(2 * kChunkMaxCtas * l.part_rows) * 8);
+  l.part_o = take((size_t)(2 * kChunkMaxCtas * l.part_rows * c.head_dim) * 4);
+  for (int i = 0; i < 2; ++i) {
+    l.res_ml[i] = prefix ? take((size_t)(tokens * heads) * 8) : 0;
+    l.res_o[i] = prefix ? take((size_t)(tokens * heads * c.head_dim) * 4) : 0;
+  }
+  l.total = at;
+  return l;
+}
+
 bool sizes_ok(const qsa_paged_cache& c, int64_t tokens, int64_t heads) {
   return tokens >= 0 && tokens <= QSA_CHUNK_MAX_TOKENS && heads >= 1 && heads <= 65535 &&
          heads % c.num_heads == 0 && tokens * heads <= INT32_MAX;
@@ -157,13 +192,17 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
       !aligned(lse, 4) || !aligned(error_word, 4) ||
       (prefix && (!aligned(prefix_table, 4) || !aligned(prefix_len, 4))))
     return QSA_ERR_ALIGN;
+  const bool fp8 = cache->dtype == QSA_DT_F8E4M3;
+  const Layout l = layout_of(*cache, tokens, heads, prefix);
+  const size_t need = fp8 ? 0 : l.total;
   const Span outs[4] = {span(out, ox), span(lse, tokens * heads * 4), span(error_word, 4),
-                        span(workspace, 0)};
+                        span(workspace, (int64_t)need)};
   const Span ins[10] = {span(q, qx), cs.k, cs.v, cs.tables, cs.k_scale, cs.v_scale,
                         span(starts, (R + 1) * 4), span(ctx, R * 4),
                         prefix ? span(prefix_table, prefix_cols * 4) : Span{},
                         prefix ? span(prefix_len, 4) : Span{}};
   if (any_overlap(outs, 4, ins, 10)) return QSA_ERR_ALIAS;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QSA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QSA_ERR_ALIGN;
   const int64_t pcap = prefix ? prefix_cols << p.c.page_log2 : 0;
   p.prefix_table = prefix && prefix_cols > 0 ? prefix_table : nullptr;
@@ -182,17 +221,39 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   p.group = (int32_t)(heads / cache->num_heads);
   p.scale_log2 = scale_log2;
   p.window = (int32_t)std::min<int64_t>(window, INT32_MAX - 16);
-  p.sink = (int32_t)std::min<int64_t>(sink, kMaxEntries);
+  p.sink = window > 0 ? (int32_t)std::min<int64_t>(sink, kMaxEntries) : 0;
   p.lse = lse;
   p.err = error_word;
   bind_calling_thread();
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == QSA_DT_BF16;
-  if (cache->dtype == QSA_DT_F8E4M3)
+  if (fp8) {
     bf16 ? launch_rows<__nv_bfloat16, __nv_fp8_e4m3>(p, s) : launch_rows<__half, __nv_fp8_e4m3>(p, s);
-  else
-    bf16 ? launch_rows<__nv_bfloat16, __nv_bfloat16>(p, s) : launch_rows<__half, __half>(p, s);
-  return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+  }
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  p.max_tiles = (int32_t)l.max_tiles;
+  p.plan = reinterpret_cast<ChunkPlan*>(w);
+  p.tiles = reinterpret_cast<ChunkTile*>(w + l.tiles);
+  p.pos = reinterpret_cast<int64_t*>(w + l.pos);
+  p.first = reinterpret_cast<int32_t*>(w + l.first);
+  p.cuts = reinterpret_cast<int2*>(w + l.cuts);
+  p.part_rows = (int32_t)l.part_rows;
+  p.part_ml = reinterpret_cast<float*>(w + l.part_ml);
+  p.part_o = reinterpret_cast<float*>(w + l.part_o);
+  for (int i = 0; i < 2 && prefix; ++i) {
+    p.res_ml[i] = reinterpret_cast<float*>(w + l.res_ml[i]);
+    p.res_o[i] = reinterpret_cast<float*>(w + l.res_o[i]);
+  }
+  const int box = (int)std::min<int64_t>(cache->page_size, chunk_tile(p.c.dim));
+  CUtensorMap kmap, vmap;
+  if (!encode_view(&kmap, p.c.k, p.c, 2, p.c.k_page, p.c.k_token, p.c.k_head, box) ||
+      !encode_view(&vmap, p.c.v, p.c, 2, p.c.v_page, p.c.v_token, p.c.v_head, box))
+    return QSA_ERR_CUDA;
+  const cudaError_t e = p.c.dim == 64    ? launch_chunk_64(p, bf16, fp8, kmap, vmap, s)
+                        : p.c.dim == 128 ? launch_chunk_128(p, bf16, fp8, kmap, vmap, s)
+                                         : launch_chunk_256(p, bf16, fp8, kmap, vmap, s);
+  return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 
 }  // namespace
@@ -201,8 +262,14 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
 extern "C" size_t qsa_chunk_attention_workspace_bytes(const qsa_paged_cache* cache,
                                                       int64_t num_tokens, int64_t num_heads,
                                                       int64_t prefix_cols) {
-  (void)cache, (void)num_tokens, (void)num_heads, (void)prefix_cols;
-  return 0;
+  using namespace qsa;
+  CacheView view{};
+  cache_host::CacheSpans spans{};
+  if (cache_host::check_cache(cache, &view, &spans) != QSA_OK || cache->num_reqs == 0 ||
+      num_tokens == 0 || !sizes_ok(*cache, num_tokens, num_heads) ||
+      cache->dtype == QSA_DT_F8E4M3)
+    return 0;
+  return layout_of(*cache, num_tokens, num_heads, prefix_cols >= 0).total;
 }
 
 extern "C" qsa_status qsa_chunk_attention(

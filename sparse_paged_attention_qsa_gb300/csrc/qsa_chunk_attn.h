@@ -1,12 +1,37 @@
-// qsa_chunk_attn.h -- what the entry points of the chunk attention
-// (include/qsa_chunk.h) hand to its kernels.
+// qsa_chunk_attn.h -- launch interface between the entry points of the chunk
+// attention (include/qsa_chunk.h, qsa_chunk.cu) and its kernels, compiled per
+// head width (qsa_chunk_attn_{64,128,256}.cu).
 #pragma once
 
 #include "qsa_cache_host.h"
 
 #include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
 
 namespace qsa {
+
+constexpr int kChunkMaxCtas = 152;     // CTAs of the tile walk, one an SM (what the workspace is sized for)
+
+// Tokens of a K/V tile, and the query rows of a K/V head that share a walk over
+// the tiles: two tensor memory accumulators of 128 rows, one for heads of 256.
+constexpr int chunk_tile(int dim) { return dim == 256 ? 64 : 128; }
+constexpr int chunk_rows(int dim) { return dim == 256 ? 128 : 256; }
+// What a row tile costs beside its K/V tiles, in K/V tiles: its queries come in
+// and its output goes out while the products wait.
+constexpr int kChunkExtra = 2;
+
+// Query rows of one K/V head that walk K/V tiles together.  Row i of a request
+// is head i % group of its token i / group.
+struct ChunkTile {
+  int32_t req;                  // its request; -1: the prefix, whose rows are all requests'
+  int32_t row0, rows, tiles;    // rows [row0, row0 + rows), K/V tiles they see
+};
+struct ChunkPlan {
+  int64_t total;                // cost of all row tiles of one K/V head
+  int32_t n, n_prefix;          // row tiles, the first ones the prefix's
+  int32_t token0, tokens;       // rows of q that belong to requests
+};
 
 struct ChunkParams {
   CacheView c;
@@ -22,9 +47,28 @@ struct ChunkParams {
   int32_t tokens, heads, group;
   float scale_log2;             // scale * log2(e)
   int32_t window;               // 0: none; at most INT32_MAX - 16
-  int32_t sink;
+  int32_t sink;                 // 0 without a window
   float* lse;                   // nullable
   uint32_t* err;
+  // workspace
+  int32_t max_tiles;
+  ChunkPlan* plan;
+  ChunkTile* tiles;             // [max_tiles]
+  int64_t* pos;                 // [max_tiles + 1] cost of the row tiles before each
+  int32_t* first;               // [num_reqs] each request's first row tile
+  int2* cuts;                   // [kChunkMaxCtas] row tile (-1: none) and head that a run cuts
+  int32_t part_rows;            // rows of a row tile, at most
+  float* part_ml;               // [2 * kChunkMaxCtas][part_rows][2]
+  float* part_o;                // [2 * kChunkMaxCtas][part_rows][dim]
+  float* res_ml[2];             // with a prefix: whole results [tokens][heads][2], of the
+  float* res_o[2];              //   prefix and of the requests' own entries [..][dim]
 };
+
+cudaError_t launch_chunk_64(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, cudaStream_t st);
+cudaError_t launch_chunk_128(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
+                             const CUtensorMap& vmap, cudaStream_t st);
+cudaError_t launch_chunk_256(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
+                             const CUtensorMap& vmap, cudaStream_t st);
 
 }  // namespace qsa

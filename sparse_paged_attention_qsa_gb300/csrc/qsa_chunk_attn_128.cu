@@ -1,0 +1,13 @@
+// qsa_chunk_attn_128.cu -- the chunk attention's kernels for heads of 128
+// (qsa_chunk_attn_impl.cuh).
+#include "qsa_chunk_attn_impl.cuh"
+
+namespace qsa {
+
+cudaError_t launch_chunk_128(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, cudaStream_t st) {
+  if (fp8) return cudaErrorNotSupported;
+  return launch_chunk<128>(p, bf16, kmap, vmap, st);
+}
+
+}  // namespace qsa

@@ -1,0 +1,1057 @@
+// qsa_chunk_attn_impl.cuh -- the kernels of the chunk attention
+// (include/qsa_chunk.h).
+//
+// For one K/V head, rows i (a request's tokens by the group's heads) and entries
+// e:  s_ie = q_i . k_e,  o_i = sum_e w_ie v_e,  l_i = sum_e w_ie,
+// w_ie = 2^(c (s_ie - m_i) + shift); out = o / l.
+//
+// chunk_plan_kernel  cuts each request's rows into row tiles (and, where there is
+//   a prefix, all requests' rows once more) and lays their K/V tiles end to end.
+// chunk_walk_kernel  one CTA an SM walks an equal run of them.
+//   Two producer warps look pages up and load K and V tiles into a ring by TMA;
+//   one thread issues the products, S = Q K^T with Q and K in shared memory into
+//   tensor memory, then O += P V with P in tensor memory: 128 rows a product, two
+//   products' S and O beside each other, so that one is in the softmax while the
+//   other is in the tensor pipe.  Two warpgroups form the softmax, a thread a
+//   row: no reduction crosses threads.  The two are two halves of 256 rows over
+//   the same K/V tiles, or, for 128 rows and fewer, every other K/V tile of the
+//   same rows, merged at the row tile's end.  (Heads of 256 hold one O of 256
+//   columns: one warpgroup, two S.)
+// chunk_join_kernel, chunk_join_all_kernel  join the pieces of row tiles that runs
+//   cut; with a prefix, the prefix's and the requests' own.
+//
+// The reference m_i is a product that occurred, the row's maximum when it was
+// taken, subtracted before the scaling: logits of any size keep the differences
+// that binary32 products have.  It moves only when weights would pass 2^15 (FP16)
+// or 2^8 (BF16), and O in tensor memory is rescaled at such moves alone.
+//
+// Rounding: q, K and V enter the products as they are, weights rounded to the
+// type of V.
+#pragma once
+
+#include "qsa_chunk_attn.h"
+#include "qsa_device.cuh"
+#include "qsa_internal.h"
+#include "qsa_tcgen05.cuh"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <mutex>
+
+namespace qsa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kChunkJoinThreads = 256;
+constexpr int kTileFlags = 16;      // tiles whose page masks are kept
+
+// A weight is at most 2^(shift + slack).  FP16 weights stay normal down to 2^-22 of
+// the largest; BF16 has binary32's exponents.
+constexpr float chunk_shift(bool bf16) { return bf16 ? 0.f : 8.f; }
+constexpr float chunk_slack(bool bf16) { return bf16 ? 8.f : 7.f; }
+
+__device__ __forceinline__ float cex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t cpack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// A row's lse: the weights are 2^(mult (s - m) + shift), l their sum.
+template <bool kBf16>
+__device__ __forceinline__ float row_lse(float m, float l, float mult) {
+  return l == 0.f ? -INFINITY : fmaf(m, mult, log2f(l) - chunk_shift(kBf16)) * 0.693147180559945309f;
+}
+template <int kId, int kThreads>
+__device__ __forceinline__ void named_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kThreads) : "memory");
+}
+
+// --- geometry ---------------------------------------------------------------------
+
+// The rows of request b, cut to what q holds.
+__device__ __forceinline__ void request_rows(const ChunkParams& p, int b, int32_t* t0, int32_t* n) {
+  const int32_t s = min(max(p.starts[b], 0), p.tokens);
+  *t0 = s;
+  *n = min(max(p.starts[b + 1], s), p.tokens) - s;
+}
+
+// What the rows of a row tile see: token j of a request sees the entries e below
+// hi(j) with e >= lo(j) or e < sink.
+struct Sight {
+  int32_t base;            // hi(j) = base + j before it is cut to [0, cap]
+  int32_t cap, window, sink;
+  bool prefix;             // all rows see [0, cap)
+  int32_t ns, w0, tiles;   // K/V tiles: ns from 0 on, then from w0 on
+  __device__ __forceinline__ int32_t hi(int j) const {
+    return prefix ? cap : min(max(base + j, 0), cap);
+  }
+  __device__ __forceinline__ int32_t lo(int j) const {
+    return window > 0 ? min(max(base + j - window, 0), cap) : 0;
+  }
+  __device__ __forceinline__ int32_t at(int t) const { return t < ns ? t : t - ns + w0; }
+};
+__device__ __forceinline__ int32_t prefix_entries(const ChunkParams& p) {
+  return p.prefix_table ? min(max(*p.prefix_len, 0), p.prefix_cap) : 0;
+}
+template <int TT>
+__device__ __forceinline__ Sight prefix_sight(const ChunkParams& p) {
+  Sight s;
+  s.cap = prefix_entries(p);
+  s.prefix = true;
+  s.base = s.window = s.sink = s.ns = s.w0 = 0;
+  s.tiles = (s.cap + TT - 1) / TT;
+  return s;
+}
+template <int TT>
+__device__ __forceinline__ Sight request_sight(const ChunkParams& p, int32_t ctx, int32_t n, int j0,
+                                               int j1) {
+  Sight s;
+  s.prefix = false;
+  s.base = max(ctx, 0) - n + 1;
+  s.cap = p.c.cap;
+  s.window = p.window;
+  s.sink = p.sink;
+  const int32_t hi = s.hi(j1), lo = s.lo(j0);
+  const int32_t sink = p.window > 0 ? min(p.sink, hi) : 0;
+  s.w0 = lo / TT;
+  s.ns = (sink + TT - 1) / TT;
+  if (s.ns >= s.w0 && s.ns > 0) s.ns = s.w0 = 0;
+  s.tiles = hi > 0 ? s.ns + (hi + TT - 1) / TT - s.w0 : 0;
+  return s;
+}
+__device__ __forceinline__ int32_t tile_cost(int32_t tiles) {
+  return tiles > 0 ? tiles + kChunkExtra : 1;
+}
+
+// Equal runs of all heads' row tiles.  Where the heads divide the CTAs evenly
+// enough every head has the same runs, so that the K/V heads of the same
+// entries, whose elements lie side by side, are read at the same time.
+struct ChunkRuns {
+  int64_t total, each, more;    // of one head, or of all
+  int n;                        // runs of it
+  bool by_head;
+};
+__device__ __forceinline__ ChunkRuns chunk_runs(int64_t total, int heads, int ctas) {
+  ChunkRuns r;
+  const int per = ctas / heads;
+  r.by_head = per > 0 && per * heads * 16 >= ctas * 15;
+  r.n = r.by_head ? per : ctas;
+  r.total = r.by_head ? total : total * heads;
+  r.each = r.total / r.n;
+  r.more = r.total - r.each * r.n;
+  return r;
+}
+__device__ __forceinline__ int64_t chunk_run_start(const ChunkRuns& r, int c) {
+  return r.each * c + min((int64_t)c, r.more);
+}
+__device__ __forceinline__ int chunk_run_of(const ChunkRuns& r, int64_t x) {
+  const int64_t big = (r.each + 1) * r.more;
+  return (int)(x < big ? x / (r.each + 1) : r.more + (x - big) / r.each);
+}
+// the CTA that walks run c of a head
+__device__ __forceinline__ int chunk_cta(const ChunkRuns& r, int heads, int head, int c) {
+  return r.by_head ? c * heads + head : c;
+}
+// the runs [*c0, *c1] that hold K/V tiles of row tile k of a head, and where it begins
+__device__ __forceinline__ int64_t chunk_owners(const ChunkParams& p, const ChunkRuns& r, int64_t total,
+                                                int head, int k, int* c0, int* c1) {
+  const int64_t a = p.pos[k], b = p.pos[k + 1], base = r.by_head ? 0 : total * head;
+  *c0 = chunk_run_of(r, base + a + (b - a > kChunkExtra ? kChunkExtra : 0));
+  *c1 = chunk_run_of(r, base + b - 1);
+  return base + a;
+}
+
+// The segments of a CTA: K/V tiles [t0, t1) of a row tile of one K/V head.
+struct Segment {
+  int k, head, t0, t1, which;
+  bool whole;
+  ChunkTile tile;
+};
+struct Walk {
+  int64_t x, x1, total, base;    // position, end; cost of a head; where the head begins
+  int k, n, head;
+  bool first;
+};
+__device__ __forceinline__ Walk walk_begin(const ChunkParams& p, int heads) {
+  Walk w;
+  const ChunkPlan plan = *p.plan;
+  w.total = plan.total;
+  w.n = plan.n;
+  w.first = true;
+  const ChunkRuns r = chunk_runs(plan.total, heads, gridDim.x);
+  if (r.by_head) {
+    const int run = blockIdx.x / heads;
+    w.head = blockIdx.x % heads;
+    w.base = 0;
+    w.x = run < r.n ? chunk_run_start(r, run) : 0;
+    w.x1 = run < r.n ? chunk_run_start(r, run + 1) : 0;
+  } else {
+    w.x = chunk_run_start(r, blockIdx.x);
+    w.x1 = chunk_run_start(r, blockIdx.x + 1);
+    w.head = plan.total > 0 ? (int)(w.x / plan.total) : 0;
+    w.base = w.total * w.head;
+  }
+  int lo = 0, hi = w.n - 1;
+  const int64_t at = w.x - w.base;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.pos[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  w.k = lo;
+  return w;
+}
+// The next segment with something to do; false at the run's end.
+__device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment* s) {
+  while (w.x < w.x1) {
+    if (w.k == w.n) {
+      w.k = 0;
+      ++w.head;
+      w.base += w.total;
+    }
+    const int64_t a = w.base + p.pos[w.k], b = w.base + p.pos[w.k + 1];
+    const int64_t end = b < w.x1 ? b : w.x1;
+    s->k = w.k;
+    s->head = w.head;
+    s->tile = p.tiles[w.k];
+    const int extra = s->tile.tiles > 0 ? kChunkExtra : 0;
+    s->t0 = (int)max((int64_t)0, w.x - a - extra);
+    s->t1 = s->tile.tiles > 0 ? (int)max((int64_t)0, end - a - extra) : 0;
+    s->whole = s->t0 == 0 && s->t1 == s->tile.tiles;
+    s->which = w.first ? 0 : 1;
+    w.first = false;
+    w.x = end;
+    ++w.k;
+    if (s->t1 > s->t0 || s->tile.tiles == 0) return true;
+  }
+  return false;
+}
+
+// --- plan -------------------------------------------------------------------------
+
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, k);
+    if (lane >= k) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t y = warp_sums[lane];
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int64_t z = __shfl_up_sync(0xffffffffu, y, k);
+      if (lane >= k) y += z;
+    }
+    warp_sums[lane] = y;
+  }
+  __syncthreads();
+  *all = warp_sums[31];
+  return x - v + (warp ? warp_sums[warp - 1] : 0);
+}
+
+// One CTA: row tiles of each request, then the cost of each row tile, both summed
+// up.  Row tiles past what the workspace holds (starts that are not in order) are
+// left out.
+template <int TT, int RT>
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+  __shared__ int64_t s_sums[32];
+  const int tid = threadIdx.x, R = p.c.num_reqs;
+  pdl_wait();
+  const int32_t token0 = min(max(p.starts[0], 0), p.tokens);
+  const int32_t tokens = min(max(p.starts[R], token0), p.tokens) - token0;
+  const Sight pre = prefix_sight<TT>(p);
+  if (tid == 0 && p.prefix_table && *p.prefix_len > p.prefix_cap) report(p.err, QSA_DERR_CONTEXT);
+  const int64_t all_rows = (int64_t)tokens * p.group;
+  const int n_prefix = pre.tiles > 0 ? (int)((all_rows + RT - 1) / RT) : 0;
+  int64_t before = n_prefix, all;
+  for (int b0 = 0; b0 < R; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int64_t k = 0;
+    if (b < R) {
+      int32_t t0, n;
+      request_rows(p, b, &t0, &n);
+      k = ((int64_t)n * p.group + RT - 1) / RT;
+      if (n > 0 && p.ctx[b] > p.c.cap) report(p.err, QSA_DERR_CONTEXT);
+    }
+    const int64_t at = before + block_scan(k, s_sums, &all);
+    if (b < R) p.first[b] = (int)min(at, (int64_t)p.max_tiles);
+    before += all;
+  }
+  const int n = (int)min(before, (int64_t)p.max_tiles);
+  __syncthreads();
+  int64_t cost = 0;
+  for (int k0 = 0; k0 < n; k0 += kPlanThreads) {
+    const int k = k0 + tid;
+    int64_t c = 0;
+    if (k < n) {
+      ChunkTile t;
+      if (k < n_prefix) {
+        t.req = -1;
+        t.row0 = k * RT;
+        t.rows = (int)min((int64_t)RT, all_rows - t.row0);
+        t.tiles = pre.tiles;
+      } else {
+        int lo = 0, hi = R - 1;              // the last request that begins at or before k
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (p.first[mid] <= k) lo = mid; else hi = mid - 1;
+        }
+        int32_t t0, m;
+        request_rows(p, lo, &t0, &m);
+        t.req = lo;
+        t.row0 = (k - p.first[lo]) * RT;
+        t.rows = (int)min((int64_t)RT, (int64_t)m * p.group - t.row0);
+        t.tiles = request_sight<TT>(p, p.ctx[lo], m, t.row0 / p.group,
+                                    (t.row0 + t.rows - 1) / p.group).tiles;
+      }
+      p.tiles[k] = t;
+      c = tile_cost(t.tiles);
+    }
+    const int64_t at = cost + block_scan(c, s_sums, &all);
+    if (k < n) p.pos[k] = at;
+    cost += all;
+  }
+  if (tid == 0) {
+    p.pos[n] = cost;
+    *p.plan = ChunkPlan{cost, n, n_prefix, token0, tokens};
+  }
+  if (tid < kChunkMaxCtas) p.cuts[tid] = make_int2(-1, 0);
+}
+
+// --- walk -------------------------------------------------------------------------
+
+struct ChunkTables {
+  uint64_t full[16], empty[16];            // ring: K's slots, then V's
+  uint64_t s_full[2], p_ready[2], q_ready, unit_done, pv_done, drain;
+  uint32_t boxes[kTileFlags];              // a bit per copy of a tile, 0: it had no page
+  uint32_t bad[8][4];                      // entries of a V slot that hold what is not finite
+  float ml[256][2];
+  uint32_t tmem;
+  int32_t abort;
+  int32_t pad[2];
+};
+
+template <int D>
+struct ChunkShape {
+  static constexpr int TT = chunk_tile(D), RT = chunk_rows(D);
+  static constexpr int kGroups = RT / 128;
+  static constexpr int kSoft = kGroups * 128;              // softmax threads
+  static constexpr int kThreads = kSoft + 128;             // + K's, V's producer, the issuer
+  static constexpr int kBlocks = D / 64;                   // of 64 dims: a line of 128 bytes
+  static constexpr int kSlot = TT * D * 2;
+  static constexpr int kQTile = 128 * D * 2;
+  static constexpr int NS = D == 64 ? 4 : 2;               // slots of K, and of V
+  static constexpr int kQ = 2 * NS * kSlot;                // offsets: ring, queries, tables
+  static constexpr int kTables = kQ + kGroups * kQTile;
+  static constexpr size_t kSmem = 1024 + kTables + sizeof(ChunkTables);
+  // tensor memory columns
+  static constexpr int kS = TT, kP = D == 128 ? 0 : 2 * TT;
+  static constexpr int kO = D == 128 ? 256 : D == 64 ? 384 : 256;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1)
+chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+  using C = ChunkShape<D>;
+  constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
+  constexpr int TT = C::TT, NS = C::NS;
+  extern __shared__ unsigned char smem_raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  unsigned char* base = smem_raw + pad;
+  const uint32_t ring = raw + pad;
+  ChunkTables& tb = *reinterpret_cast<ChunkTables*>(base + C::kTables);
+  const auto bar = [&](uint64_t& b) { return (uint32_t)__cvta_generic_to_shared(&b); };
+  volatile int32_t* s_abort = &tb.abort;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2 * NS; ++i) {
+      mbar_init(bar(tb.full[i]), 1);
+      mbar_init(bar(tb.empty[i]), 1);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(bar(tb.s_full[u]), 1);
+      mbar_init(bar(tb.p_ready[u]), 4);
+    }
+    mbar_init(bar(tb.q_ready), C::kSoft / 32);
+    mbar_init(bar(tb.unit_done), 1);
+    mbar_init(bar(tb.pv_done), 1);
+    mbar_init(bar(tb.drain), 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  constexpr int kIssuer = C::kSoft / 32 + 2;
+  if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(&tb.tmem)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  const uint32_t tmem = tb.tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  // After a time-out nothing waits any more: roles run their loops to the end, so
+  // that the barriers between the softmax's warps stay matched.
+  const auto wait_for = [&](uint32_t b, uint32_t phase) {
+    if (!mbar_try_wait(b, phase) && *s_abort == 0 && !mbar_wait(b, phase)) {
+      *s_abort = 1;
+      report(p.err, QSA_DERR_TIMEOUT);
+    }
+  };
+  const auto sight_of = [&](const Segment& s) {
+    if (s.tile.req < 0) return prefix_sight<TT>(p);
+    int32_t t0, n;
+    request_rows(p, s.tile.req, &t0, &n);
+    return request_sight<TT>(p, p.ctx[s.tile.req], n, s.tile.row0 / p.group,
+                             (s.tile.row0 + s.tile.rows - 1) / p.group);
+  };
+
+  const int heads = p.c.heads;
+  Walk walk = walk_begin(p, heads);
+  Segment seg;
+  int issued = 0;                                          // a producer's fills
+  bool used = false;                                       // the issuer's products
+  if (warp == kIssuer - 2 || warp == kIssuer - 1) {
+    // ---------------- producers ----------------
+    const int kv = warp - (kIssuer - 2);
+    const int lg = p.c.page_log2;
+    const int box_rows = min(TT, 1 << lg), n_boxes = TT / box_rows;
+    const uint64_t policy = evict_normal_policy();
+    bool stop = false;
+    while (!stop && walk_next(p, walk, &seg)) {
+      const Sight s = sight_of(seg);
+      const int32_t* table = s.prefix ? p.prefix_table : p.c.bt + (int64_t)seg.tile.req * p.c.bt_s0;
+      // the entries that some row sees: [0, sink) and [lo, end)
+      const int32_t end = s.hi((seg.tile.row0 + seg.tile.rows - 1) / p.group);
+      const int32_t lo = s.lo(seg.tile.row0 / p.group), sink = s.window > 0 ? min(s.sink, end) : 0;
+      int col0 = -64;                                      // 32 page ids from this column on
+      int32_t ids = -1;
+      for (int t = seg.t0; t < seg.t1; ++t) {
+        const int32_t e0 = s.at(t) * TT;
+        const int col = e0 >> lg, cols = max(1, TT >> lg);
+        if (col < col0 || col + cols > col0 + 32) {
+          col0 = col;
+          // the columns of entries below `end` are inside the table
+          ids = ((int64_t)(col + lane) << lg) < end ? __ldg(table + col + lane) : -1;
+        }
+        const int32_t id =
+            __shfl_sync(0xffffffffu, ids, col - col0 + (lane < n_boxes ? (lane * box_rows) >> lg : 0));
+        const int32_t be = e0 + lane * box_rows;
+        const bool want = lane < n_boxes && be < end && (be + box_rows > lo || be < sink);
+        const bool good = want && id >= 0 && id < p.c.num_pages;
+        const uint32_t mask = __ballot_sync(0xffffffffu, good);
+        if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
+        const int i = issued % NS, slot = kv * NS + i;
+        if (issued >= NS) {
+          bool ok = *s_abort == 0 && mbar_wait(bar(tb.empty[slot]), (uint32_t)((issued / NS - 1) & 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            if (lane == 0 && *s_abort == 0) {
+              *s_abort = 1;
+              report(p.err, QSA_DERR_TIMEOUT);
+            }
+            stop = true;
+            break;
+          }
+        }
+        const uint32_t full = bar(tb.full[slot]), dst = ring + slot * C::kSlot;
+        if (kv == 0) {
+          if (lane == 0) tb.boxes[issued % kTileFlags] = mask;
+        } else if (lane < 4) {
+          tb.bad[i][lane] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * D * 2));
+        __syncwarp();
+        if (good) {
+#pragma unroll
+          for (int c = 0; c < C::kBlocks; ++c)
+            tma_load_4d(dst + c * (TT * 128) + lane * box_rows * 128, kv ? &vmap : &kmap, c * 64,
+                        seg.head, be & ((1 << lg) - 1), id, full, policy);
+        }
+        ++issued;
+      }
+    }
+  } else if (warp >= kIssuer) {
+    // ---------------- issuer ----------------
+    if (warp == kIssuer && lane == 0) {
+      constexpr uint32_t kQk = tc5_idesc(kBf16, 128, TT, false), kPv = tc5_idesc(kBf16, 128, D, true);
+      int fill = 0, units = 0;                             // tiles, row tiles before this segment
+      int ready[2] = {0, 0};
+      while (*s_abort == 0 && walk_next(p, walk, &seg)) {
+        const int tiles = seg.t1 - seg.t0;
+        if (tiles <= 0) continue;
+        const bool dual = seg.tile.rows > 128;
+        const int steps = dual ? 2 * tiles : tiles;
+        wait_for(bar(tb.q_ready), (uint32_t)(units & 1));
+        ++units;
+        if (*s_abort) break;
+        tc5_fence_after();
+        const auto qk = [&](int s) {
+          const int u = s & 1, f = fill + (dual ? s >> 1 : s), i = f % NS;
+          if (!dual || u == 0) {
+            wait_for(bar(tb.full[i]), (uint32_t)((f / NS) & 1));
+            tc5_fence_after();
+          }
+          if (*s_abort) return;
+          // 16 dims a product: 32 bytes on in a line of 64, then the next block of lines
+          const uint64_t q = tc5_desc(ring + C::kQ + (dual ? u * C::kQTile : 0), 16);
+          const uint64_t k = tc5_desc(ring + i * C::kSlot, 16);
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            tc5_mma_ss(tmem + u * C::kS, q + (x >> 2) * (128 * 128 / 16) + (x & 3) * 2,
+                       k + (x >> 2) * (TT * 128 / 16) + (x & 3) * 2, kQk, x > 0);
+          used = true;
+          tc5_commit(bar(tb.s_full[u]));
+          if (!dual || u == 1) tc5_commit(bar(tb.empty[i]));
+        };
+        const auto pv = [&](int s) {
+          const int u = s & 1, f = fill + (dual ? s >> 1 : s), i = f % NS, slot = NS + i;
+          wait_for(bar(tb.p_ready[u]), (uint32_t)(ready[u] & 1));
+          ++ready[u];
+          wait_for(bar(tb.full[slot]), (uint32_t)((f / NS) & 1));
+          if (*s_abort) return;
+          tc5_fence_after();
+          const uint64_t v = tc5_desc(ring + slot * C::kSlot, TT * 128);
+          const uint32_t o = tmem + C::kO + (C::kGroups == 2 ? u * D : 0);
+          const uint32_t pa = tmem + C::kP + u * (D == 128 ? C::kS : TT / 2);
+          const bool more = C::kGroups == 2 ? s > 1 : s > 0;
+#pragma unroll
+          for (int x = 0; x < TT / 16; ++x)
+            tc5_mma_ts(o, pa + x * 8, v + x * (16 * 128 / 16), kPv, more || x > 0);
+          if (!dual || u == 1) tc5_commit(bar(tb.empty[slot]));
+          if (C::kGroups == 1) tc5_commit(bar(tb.pv_done));
+          if (s + 1 == steps) tc5_commit(bar(tb.unit_done));
+        };
+        qk(0);
+        for (int s = 0; s < steps && *s_abort == 0; ++s) {
+          if (s + 1 < steps) qk(s + 1);
+          pv(s);
+        }
+        fill += tiles;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax ----------------
+    const int g = warp >> 2, wl = warp & 3, r = wl * 32 + lane;   // warpgroup; row of 128
+    const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
+    const int box_log2 = min(p.c.page_log2, TT == 128 ? 7 : 6);
+    int fill = 0, units = 0, steps_done = 0;
+    int got[2] = {0, 0};
+    while (walk_next(p, walk, &seg)) {
+      const int tiles = seg.t1 - seg.t0;
+      const bool dual = seg.tile.rows > 128;
+      const Sight s = sight_of(seg);
+      const int32_t first_token =
+          seg.tile.req < 0 ? p.plan->token0 : min(max(p.starts[seg.tile.req], 0), p.tokens);
+      // queries: 16-byte pieces of the rows' lines
+      if (tiles > 0) {
+        constexpr int kPieces = D / 8;
+        const int all = seg.tile.rows * kPieces;
+        for (int i0 = tid; i0 < all; i0 += C::kSoft * 8) {
+          uint4 v[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int i = i0 + x * C::kSoft;
+            if (i < all) {
+              const int row = seg.tile.row0 + i / kPieces, j = row / p.group;
+              v[x] = *reinterpret_cast<const uint4*>(
+                  p.q + (int64_t)(first_token + j) * p.q_row +
+                  (int64_t)(seg.head * p.group + row - j * p.group) * p.q_head + i % kPieces * 16);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int i = i0 + x * C::kSoft;
+            if (i < all) {
+              const int row = i / kPieces, piece = i % kPieces;
+              *reinterpret_cast<uint4*>(base + C::kQ + (row >> 7) * C::kQTile + (piece >> 3) * (128 * 128) +
+                                        (row & 127) * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v[x];
+            }
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(tb.q_ready));
+      }
+      // this thread's row, and what all rows see
+      const int row = (dual ? g * 128 : 0) + r;
+      const bool mine = row < seg.tile.rows;
+      const int j = (seg.tile.row0 + min(row, seg.tile.rows - 1)) / p.group;
+      const int32_t hi = s.hi(j), lo = s.lo(j), sink = s.window > 0 ? min(s.sink, hi) : 0;
+      const int ja = seg.tile.row0 / p.group, jb = (seg.tile.row0 + seg.tile.rows - 1) / p.group;
+      const int32_t in_hi = s.hi(ja), in_lo = s.lo(jb);
+      const int32_t in_sink = s.window > 0 ? min(s.sink, in_hi) : 0;
+      const float mult = p.scale_log2;
+      float m = -INFINITY, l = 0.f;
+      const int steps = dual ? 2 * tiles : tiles;
+      for (int st = C::kGroups == 2 ? g : 0; st < steps; st += C::kGroups) {
+        const int u = st & 1, t = dual ? st >> 1 : st, f = fill + t;
+        const int32_t e0 = s.at(seg.t0 + t) * TT;
+        wait_for(bar(tb.s_full[u]), (uint32_t)(got[u] & 1));
+        ++got[u];
+        tc5_fence_after();
+        const uint32_t boxes = tb.boxes[f % kTileFlags];
+        const bool edge = e0 + TT > in_hi || (e0 < in_lo && e0 + TT > in_sink) ||
+                          boxes != (1u << (TT >> box_log2)) - 1;
+        uint32_t vis[TT / 32];
+        if (edge) {
+#pragma unroll
+          for (int w = 0; w < TT / 32; ++w) {
+            const int32_t b = e0 + w * 32;
+            const auto upto = [&](int32_t x) -> uint32_t {   // entries below x
+              const int32_t n = min(max(x - b, 0), 32);
+              return n == 32 ? 0xffffffffu : (1u << n) - 1;
+            };
+            uint32_t v = (upto(hi) & ~upto(lo)) | upto(sink);
+            uint32_t there = 0;
+            if (box_log2 >= 5) {
+              there = (boxes >> ((w * 32) >> box_log2)) & 1u ? 0xffffffffu : 0u;
+            } else {
+              const uint32_t one = (1u << (1 << box_log2)) - 1;
+              for (int x = 0; x < 32 >> box_log2; ++x)
+                if ((boxes >> (((w * 32) >> box_log2) + x)) & 1u) there |= one << (x << box_log2);
+            }
+            vis[w] = v & there;
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < TT / 32; ++w) vis[w] = 0xffffffffu;
+        }
+        // S comes from tensor memory twice, 32 columns at a time, for the maximum and
+        // for the weights: all of it at once does not fit in registers
+        const uint32_t zs = lanes + u * C::kS;
+        const auto columns = [&](auto&& use) {
+          uint32_t z[2][32];
+          tc5_ld32(zs, z[0]);
+#pragma unroll
+          for (int w = 0; w < TT / 32; ++w) {
+            uint32_t(&x)[32] = z[w & 1];
+            tc5_wait_ld();
+            tc5_hold(x);
+            if (w + 1 < TT / 32) tc5_ld32(zs + (w + 1) * 32, z[(w + 1) & 1]);
+            if (edge) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((vis[w] >> i) & 1u)) x[i] = 0xff800000u;
+            }
+            use(w, x);
+          }
+        };
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        columns([&](int, uint32_t(&x)[32]) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
+        });
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), old = m;
+        const bool move = (top - m) * mult > chunk_slack(kBf16);
+        if (move) m = top;
+        if (__any_sync(0xffffffffu, move)) {
+          const float a = !move ? 1.f : old == -INFINITY ? 0.f : cex2((old - m) * mult);
+          l *= a;
+          if (C::kGroups == 2 ? st > 1 : st > 0) {
+            // the product before this one into the same O: done with two buffers of
+            // S and O (S of this step came behind it), else to be waited for
+            if (C::kGroups == 1) wait_for(bar(tb.pv_done), (uint32_t)((steps_done + st - 1) & 1));
+            tc5_fence_after();
+            const uint32_t o = lanes + C::kO + (C::kGroups == 2 ? u * D : 0);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t x[32];
+              tc5_ld32(o + c, x);
+              tc5_wait_ld();
+              tc5_hold(x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * a);
+              tc5_st(o + c, x);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float2 mult2 = make_float2(mult, mult), ref2 = make_float2(-ref, -ref);
+        const float2 shift2 = make_float2(chunk_shift(kBf16), chunk_shift(kBf16));
+        const uint32_t pa = lanes + C::kP + u * (D == 128 ? C::kS : TT / 2);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        columns([&](int w, uint32_t(&x)[32]) {
+          uint32_t h[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 z = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            const float2 y = ffma2(fadd2(z, ref2), mult2, shift2);
+            const float2 e = make_float2(cex2(y.x), cex2(y.y));
+            sum[i & 1] = fadd2(sum[i & 1], e);
+            h[i] = cpack2<kBf16>(e.x, e.y);
+          }
+          tc5_st(pa + w * 16, h);
+        });
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        if (edge) {
+          // 0 times what a hidden entry holds may be NaN: whatever is not finite in
+          // V leaves the tile, and rows that see it get NaN
+          const int i = f % NS, slot = NS + i;
+          wait_for(bar(tb.full[slot]), (uint32_t)((f / NS) & 1));
+          constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kUp = kBf16 ? 0x00800080u : 0x04000400u;
+          uint4* v = reinterpret_cast<uint4*>(base + slot * C::kSlot);
+          for (int x = r; x < C::kSlot / 16; x += 128) {
+            const uint4 y = v[x];
+            const uint32_t e = ((y.x & kExp) + kUp) | ((y.y & kExp) + kUp) | ((y.z & kExp) + kUp) |
+                               ((y.w & kExp) + kUp);
+            if (e & 0x80008000u) {
+              const int token = x >> 3 & (TT - 1);         // lines of 8 pieces, blocks of TT lines
+              atomicOr(&tb.bad[i][token >> 5], 1u << (token & 31));
+              __threadfence_block();
+              v[x] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (g == 0) named_sync<3, 128>();
+          else named_sync<4, 128>();
+#pragma unroll
+          for (int w = 0; w < TT / 32; ++w)
+            if (vis[w] & *reinterpret_cast<volatile uint32_t*>(&tb.bad[i][w])) l = NAN;
+        }
+        tc5_wait_st();
+        tc5_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(tb.p_ready[u]));
+      }
+      steps_done += steps;
+      fill += tiles;
+      // ---- the row tile's end
+      if (tiles > 0) {
+        wait_for(bar(tb.unit_done), (uint32_t)(units & 1));
+        ++units;
+        tc5_fence_after();
+      }
+      const bool split = C::kGroups == 2 && !dual;         // both warpgroups hold the same rows
+      float f0 = 1.f, f1 = 0.f;
+      if (split && steps > 1) {
+        float4* stage = reinterpret_cast<float4*>(base + C::kQ);
+        if (g == 1) {
+          tb.ml[r][0] = m;
+          tb.ml[r][1] = l;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t x[32];
+            tc5_ld32(lanes + C::kO + D + c, x);
+            tc5_wait_ld();
+            tc5_hold(x);
+            if (mine) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                stage[r * (D / 4) + ((c / 4 + i) ^ (r & 7))] =
+                    make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
+                                __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
+            }
+          }
+        }
+        named_sync<2, 256>();
+        if (g == 0) {
+          const float m1 = tb.ml[r][0], l1 = tb.ml[r][1], M = fmaxf(m, m1);
+          f0 = m == -INFINITY ? 0.f : cex2((m - M) * mult);
+          f1 = m1 == -INFINITY ? 0.f : cex2((m1 - M) * mult);
+          l = l * f0 + l1 * f1;
+          m = M;
+        }
+      }
+      if (!split || g == 0) {
+        const int qrow = seg.tile.row0 + row, qj = qrow / p.group;
+        const int64_t token = first_token + qj;
+        const int head = seg.head * p.group + qrow - qj * p.group;
+        const bool direct = seg.whole && !p.res_o[0];
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t rh = token * p.heads + head;
+        const int64_t piece = (2 * (int64_t)blockIdx.x + seg.which) * p.part_rows + row;
+        const int list = seg.tile.req < 0 ? 0 : 1;
+        float* dst = seg.whole ? p.res_o[list] + rh * D : p.part_o + piece * D;
+        if (mine) {
+          if (!direct)
+            *reinterpret_cast<float2*>(seg.whole ? p.res_ml[list] + rh * 2 : p.part_ml + piece * 2) =
+                make_float2(m, l);
+          else if (p.lse)
+            p.lse[rh] = row_lse<kBf16>(m, l, mult);
+        }
+        unsigned char* out = p.out + token * p.out_row + head * p.out_head;
+        const float4* stage = reinterpret_cast<const float4*>(base + C::kQ);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t x[32];
+          if (tiles > 0) {
+            tc5_ld32(lanes + C::kO + (C::kGroups == 2 && dual ? g * D : 0) + c, x);
+            tc5_wait_ld();
+            tc5_hold(x);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 0;
+          }
+          if (!mine) continue;
+          float o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]);
+          if (split && steps > 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 y = stage[r * (D / 4) + ((c / 4 + i) ^ (r & 7))];
+              o[4 * i] = o[4 * i] * f0 + y.x * f1;
+              o[4 * i + 1] = o[4 * i + 1] * f0 + y.y * f1;
+              o[4 * i + 2] = o[4 * i + 2] * f0 + y.z * f1;
+              o[4 * i + 3] = o[4 * i + 3] * f0 + y.w * f1;
+            }
+          }
+          if (direct) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(out + (c + 8 * i) * 2) = make_uint4(
+                  cpack2<kBf16>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                  cpack2<kBf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                  cpack2<kBf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                  cpack2<kBf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(dst + c + 4 * i) =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        // a run's first row tile, where it is not its beginning: for the join
+        if (seg.which == 0 && seg.t0 > 0 && row == 0) p.cuts[blockIdx.x] = make_int2(seg.k, seg.head);
+      }
+      if (split && steps > 1) named_sync<2, 256>();          // the stage is free for queries
+      tc5_fence_before();
+    }
+  }
+  __syncthreads();
+  // after a time-out, what this CTA issued lands before it exits
+  if (*s_abort != 0) {
+    if (warp < kIssuer && warp >= kIssuer - 2 && lane == 0)
+      for (int i = max(0, issued - NS); i < issued; ++i)
+        mbar_wait(bar(tb.full[(warp - (kIssuer - 2)) * NS + i % NS]), (uint32_t)((i / NS) & 1), kDrainLimitNs);
+    if (warp == kIssuer && lane == 0 && used) {
+      tc5_commit(bar(tb.drain));
+      mbar_wait(bar(tb.drain), 0, kDrainLimitNs);
+    }
+    __syncthreads();
+  }
+  if (warp == kIssuer) {
+    tc5_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+  }
+}
+
+// --- join -------------------------------------------------------------------------
+
+// A row's sums so far, four elements a thread.
+struct Acc {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float2 ml, float4 v, float mult) {
+    const float mn = fmaxf(m, ml.x);
+    const float a = mn == m ? 1.f : cex2((m - mn) * mult);
+    const float f = ml.x == -INFINITY ? 0.f : cex2((ml.x - mn) * mult);
+    l = l * a + ml.y * f;
+    o.x = o.x * a + v.x * f;
+    o.y = o.y * a + v.y * f;
+    o.z = o.z * a + v.z * f;
+    o.w = o.w * a + v.w * f;
+    m = mn;
+  }
+};
+
+// Adds what the runs [c0, c1] left of local row i of a row tile that begins at x0;
+// of them this thread's: k0, k0 + dk, ...
+template <int D>
+__device__ __forceinline__ void add_pieces(const ChunkParams& p, const ChunkRuns& r, int head, int64_t x0,
+                                           int c0, int c1, int i, int ln, int k0, int dk, Acc& acc) {
+#pragma unroll 4
+  for (int c = c0 + k0; c <= c1; c += dk) {
+    const int second = c == c0 && chunk_run_start(r, c) < x0;
+    const int64_t at = (int64_t)(2 * chunk_cta(r, p.c.heads, head, c) + second) * p.part_rows + i;
+    acc.add(*reinterpret_cast<const float2*>(p.part_ml + at * 2),
+            *reinterpret_cast<const float4*>(p.part_o + at * D + ln * 4), p.scale_log2);
+  }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void store_row(const ChunkParams& p, int64_t token, int head, int ln, const Acc& a) {
+  constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
+  const float inv = a.l == 0.f ? 0.f : 1.f / a.l;
+  *reinterpret_cast<uint2*>(p.out + token * p.out_row + head * p.out_head + ln * 8) =
+      make_uint2(cpack2<kBf16>(a.o.x * inv, a.o.y * inv), cpack2<kBf16>(a.o.z * inv, a.o.w * inv));
+  if (ln == 0 && p.lse)
+    p.lse[token * p.heads + head] = row_lse<kBf16>(a.m, a.l, p.scale_log2);
+}
+
+// CTA (c, y): rows of the row tile that the start of CTA c's run cuts, if that is
+// its first cut.  D/4 threads a row; where it has many pieces, all threads one row.
+template <typename T, int D>
+__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const ChunkParams p, int ctas) {
+  constexpr int L = D / 4, kG = kChunkJoinThreads / L, kFew = 12;
+  __shared__ __align__(16) float4 s_o[kChunkJoinThreads];
+  __shared__ float2 s_ml[kG];
+  const int tid = threadIdx.x, grp = tid / L, ln = tid % L;
+  pdl_wait();
+  const int2 cut = p.cuts[blockIdx.x];
+  if (cut.x < 0) return;
+  const int heads = p.c.heads;
+  const ChunkPlan plan = *p.plan;
+  const ChunkRuns r = chunk_runs(plan.total, heads, ctas);
+  int c0, c1;
+  const int64_t x0 = chunk_owners(p, r, plan.total, cut.y, cut.x, &c0, &c1);
+  const int c = r.by_head ? blockIdx.x / heads : blockIdx.x;
+  if (c != c0 + 1) return;
+  const ChunkTile t = p.tiles[cut.x];
+  int32_t t0, n;
+  request_rows(p, t.req, &t0, &n);
+  const bool few = c1 - c0 < kFew;
+  for (int i0 = blockIdx.y * (few ? kG : 1); i0 < t.rows; i0 += gridDim.y * (few ? kG : 1)) {
+    const int i = few ? i0 + grp : i0;
+    Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (i < t.rows)
+      add_pieces<D>(p, r, cut.y, x0, c0, c1, i, ln, few ? 0 : grp, few ? 1 : kG, a);
+    if (!few) {
+      __syncthreads();
+      s_o[tid] = a.o;
+      if (ln == 0) s_ml[grp] = make_float2(a.m, a.l);
+      __syncthreads();
+      if (grp > 0) continue;
+      for (int k = 1; k < kG; ++k) a.add(s_ml[k], s_o[k * L + ln], p.scale_log2);
+    }
+    if (i < t.rows) {
+      const int row = t.row0 + i, j = row / p.group;
+      store_row<T, D>(p, t0 + j, cut.y * p.group + row - j * p.group, ln, a);
+    }
+  }
+}
+
+// With a prefix: CTA (token, K/V head), D/4 threads a row; every row's two results.
+template <typename T, int D>
+__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const ChunkParams p, int ctas) {
+  constexpr int L = D / 4, kG = kChunkJoinThreads / L, RT = chunk_rows(D);
+  const int tid = threadIdx.x, lane = tid & 31, grp = tid / L, ln = tid % L;
+  const int heads = p.c.heads, R = p.c.num_reqs;
+  pdl_wait();
+  const ChunkPlan plan = *p.plan;
+  const ChunkRuns r = chunk_runs(plan.total, heads, ctas);
+  const int head = blockIdx.y;
+  for (int32_t token = plan.token0 + blockIdx.x; token < plan.token0 + plan.tokens; token += gridDim.x) {
+    // the last request that starts at or before the token, 32 at a time
+    int b = 0;
+    for (int step = 1 << 15; step >= 1; step >>= 5) {
+      const int64_t x = (int64_t)b + (int64_t)lane * step;
+      const uint32_t le = __ballot_sync(0xffffffffu, x < R && p.starts[min(x, (int64_t)R - 1)] <= token);
+      b += le ? (31 - __clz(le)) * step : 0;
+    }
+    int32_t t0, n;
+    request_rows(p, b, &t0, &n);
+    const bool own = token >= t0 && token < t0 + n;
+    for (int g = grp; g < p.group; g += kG) {
+      const int64_t rh = (int64_t)token * p.heads + head * p.group + g;
+      Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      for (int list = 0; list < 2; ++list) {
+        const int64_t row = (int64_t)(token - (list ? t0 : plan.token0)) * p.group + g;
+        const int64_t k = (list ? p.first[b] : 0) + row / RT;
+        if (list ? !own || k >= plan.n : k >= plan.n_prefix) continue;
+        int c0, c1;
+        const int64_t x0 = chunk_owners(p, r, plan.total, head, (int)k, &c0, &c1);
+        if (c0 == c1)
+          a.add(*reinterpret_cast<const float2*>(p.res_ml[list] + rh * 2),
+                *reinterpret_cast<const float4*>(p.res_o[list] + rh * D + ln * 4), p.scale_log2);
+        else
+          add_pieces<D>(p, r, head, x0, c0, c1, (int)(row % RT), ln, 0, 1, a);
+      }
+      store_row<T, D>(p, token, head * p.group + g, ln, a);
+    }
+  }
+}
+
+// --- launch -----------------------------------------------------------------------
+
+// The SMs of the current device; the kernel's set-up once per device.
+template <typename T, int D>
+cudaError_t chunk_device(int* n_sms) {
+  static std::mutex mu;
+  static int sms[64];                                      // 0: not set up on that device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (sms[dev] == 0) {
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(chunk_walk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)ChunkShape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    sms[dev] = std::min(n, kChunkMaxCtas);
+  }
+  *n_sms = sms[dev];
+  return cudaSuccess;
+}
+
+template <typename T, int D>
+cudaError_t launch_chunk_typed(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               cudaStream_t st) {
+  using C = ChunkShape<D>;
+  int ctas = 0;
+  cudaError_t e = chunk_device<T, D>(&ctas);
+  if (e != cudaSuccess) return e;
+  e = launch_after(chunk_plan_kernel<C::TT, C::RT>, dim3(1), dim3(kPlanThreads), 0, st, p);
+  if (e != cudaSuccess) return e;
+  e = launch_after(chunk_walk_kernel<T, D>, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, st, p,
+                   kmap, vmap);
+  if (e != cudaSuccess) return e;
+  if (p.res_o[0])
+    return launch_after(chunk_join_all_kernel<T, D>,
+                        dim3((unsigned)std::min(p.tokens, 16384), (unsigned)p.c.heads),
+                        dim3(kChunkJoinThreads), 0, st, p, ctas);
+  const int64_t rows = std::min<int64_t>((int64_t)p.tokens * p.group, C::RT);
+  return launch_after(chunk_join_kernel<T, D>, dim3((unsigned)ctas, (unsigned)std::min<int64_t>(rows, 16)),
+                      dim3(kChunkJoinThreads), 0, st, p, ctas);
+}
+
+template <int D>
+cudaError_t launch_chunk(const ChunkParams& p, bool bf16, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, cudaStream_t st) {
+  return bf16 ? launch_chunk_typed<__nv_bfloat16, D>(p, kmap, vmap, st)
+              : launch_chunk_typed<__half, D>(p, kmap, vmap, st);
+}
+
+}  // namespace
+}  // namespace qsa
