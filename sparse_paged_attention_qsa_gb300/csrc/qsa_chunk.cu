@@ -3,123 +3,16 @@
 #include "qsa_chunk_attn.h"
 #include "qsa_cache_host.h"
 #include "qsa_cache_map.h"
-#include "qsa_device.cuh"
 #include "qsa_host.h"
-#include "qsa_internal.h"
 #include "qsa_chunk.h"
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 namespace qsa {
 namespace {
-
-constexpr int kRowWarps = 4;
-
-// A CTA for each row and head: its warps take every fourth entry each, a lane
-// D/32 dims, and join their sums.
-template <typename T, typename CT, int D>
-__global__ void __launch_bounds__(kRowWarps * 32) chunk_row_kernel(const ChunkParams p) {
-  constexpr int N = D / 32;
-  __shared__ float s_m[kRowWarps], s_l[kRowWarps], s_o[kRowWarps][D];
-  const int t = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = h / p.group;
-  if (t < p.starts[0] || t >= p.starts[p.c.num_reqs]) return;
-  int b = 0, up = p.c.num_reqs - 1;
-  while (b < up) {
-    const int mid = (b + up + 1) >> 1;
-    if (p.starts[mid] <= t) b = mid; else up = mid - 1;
-  }
-  const int start = max(p.starts[b], 0), n = min(p.starts[b + 1], p.tokens) - start;
-  const int ctx = max(p.ctx[b], 0), h0 = ctx - n + (t - start) + 1;
-  const int hi = min(max(h0, 0), p.c.cap);
-  const int lo = p.window > 0 ? min(max(h0 - p.window, 0), p.c.cap) : 0;
-  if (ctx > p.c.cap && threadIdx.x == 0) report(p.err, QSA_DERR_CONTEXT);
-  int prefix = p.prefix_table ? max(*p.prefix_len, 0) : 0;
-  if (prefix > p.prefix_cap) {
-    prefix = p.prefix_cap;
-    if (threadIdx.x == 0) report(p.err, QSA_DERR_CONTEXT);
-  }
-  const T* q = reinterpret_cast<const T*>(p.q + t * p.q_row + h * p.q_head);
-  float x[N], o[N], m = -INFINITY, l = 0.f;
-  const float ks = p.c.k_scale ? p.c.k_scale[kvh] : 1.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] = (float)q[lane * N + i];
-    o[i] = 0.f;
-  }
-  for (int part = 0; part < 2; ++part) {
-    const int32_t* table = part ? p.c.bt + b * p.c.bt_s0 : p.prefix_table;
-    const int end = part ? hi : prefix;
-    for (int e = warp; e < end; e += kRowWarps) {
-      if (part && e >= p.sink && e < lo) {
-        e += (lo - e) / kRowWarps * kRowWarps;
-        if (e < lo) continue;
-      }
-      const int id = table[e >> p.c.page_log2];
-      if (id < 0 || id >= p.c.num_pages) {
-        if (lane == 0) report(p.err, QSA_DERR_KV_PAGE);
-        continue;
-      }
-      const int slot = e & ((1 << p.c.page_log2) - 1);
-      const CT* k = reinterpret_cast<const CT*>(p.c.k + id * p.c.k_page + slot * p.c.k_token +
-                                                kvh * p.c.k_head);
-      const CT* v = reinterpret_cast<const CT*>(p.c.v + id * p.c.v_page + slot * p.c.v_token +
-                                                kvh * p.c.v_head);
-      float z = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) z = fmaf(x[i], (float)k[lane * N + i], z);
-#pragma unroll
-      for (int i = 1; i < 32; i <<= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
-      z *= p.scale_log2 * ks;
-      const float mn = fmaxf(m, z), a = exp2f(m - mn), w = exp2f(z - mn);
-      m = mn;
-      l = l * a + w;
-#pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = o[i] * a + w * (float)v[lane * N + i];
-    }
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) s_o[warp][lane * N + i] = o[i];
-  __syncthreads();
-  if (warp != 0) return;
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, s_m[w]);
-  float f[kRowWarps];
-  for (int w = 0; w < kRowWarps; ++w) {
-    f[w] = M == -INFINITY ? 0.f : exp2f(s_m[w] - M);
-    L += s_l[w] * f[w];
-  }
-  const float inv = L == 0.f ? 0.f : (p.c.v_scale ? p.c.v_scale[kvh] : 1.f) / L;
-  T* out = reinterpret_cast<T*>(p.out + t * p.out_row + h * p.out_head);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float v = 0.f;
-    for (int w = 0; w < kRowWarps; ++w) v += s_o[w][lane * N + i] * f[w];
-    out[lane * N + i] = (T)(v * inv);
-  }
-  if (lane == 0 && p.lse)
-    p.lse[(int64_t)t * p.heads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
-}
-
-template <typename T, typename CT>
-void launch_rows(const ChunkParams& p, cudaStream_t st) {
-  const dim3 grid((unsigned)p.tokens, (unsigned)p.heads);
-  switch (p.c.dim) {
-    case 64: chunk_row_kernel<T, CT, 64><<<grid, kRowWarps * 32, 0, st>>>(p); break;
-    case 128: chunk_row_kernel<T, CT, 128><<<grid, kRowWarps * 32, 0, st>>>(p); break;
-    default: chunk_row_kernel<T, CT, 256><<<grid, kRowWarps * 32, 0, st>>>(p);
-  }
-}
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -194,7 +87,7 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
     return QSA_ERR_ALIGN;
   const bool fp8 = cache->dtype == QSA_DT_F8E4M3;
   const Layout l = layout_of(*cache, tokens, heads, prefix);
-  const size_t need = fp8 ? 0 : l.total;
+  const size_t need = l.total;
   const Span outs[4] = {span(out, ox), span(lse, tokens * heads * 4), span(error_word, 4),
                         span(workspace, (int64_t)need)};
   const Span ins[10] = {span(q, qx), cs.k, cs.v, cs.tables, cs.k_scale, cs.v_scale,
@@ -227,10 +120,6 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   bind_calling_thread();
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == QSA_DT_BF16;
-  if (fp8) {
-    bf16 ? launch_rows<__nv_bfloat16, __nv_fp8_e4m3>(p, s) : launch_rows<__half, __nv_fp8_e4m3>(p, s);
-    return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
-  }
   unsigned char* w = static_cast<unsigned char*>(workspace);
   p.max_tiles = (int32_t)l.max_tiles;
   p.plan = reinterpret_cast<ChunkPlan*>(w);
@@ -247,8 +136,8 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   }
   const int box = (int)std::min<int64_t>(cache->page_size, chunk_tile(p.c.dim));
   CUtensorMap kmap, vmap;
-  if (!encode_view(&kmap, p.c.k, p.c, 2, p.c.k_page, p.c.k_token, p.c.k_head, box) ||
-      !encode_view(&vmap, p.c.v, p.c, 2, p.c.v_page, p.c.v_token, p.c.v_head, box))
+  if (!encode_view(&kmap, p.c.k, p.c, fp8 ? 1 : 2, p.c.k_page, p.c.k_token, p.c.k_head, box) ||
+      !encode_view(&vmap, p.c.v, p.c, fp8 ? 1 : 2, p.c.v_page, p.c.v_token, p.c.v_head, box))
     return QSA_ERR_CUDA;
   const cudaError_t e = p.c.dim == 64    ? launch_chunk_64(p, bf16, fp8, kmap, vmap, s)
                         : p.c.dim == 128 ? launch_chunk_128(p, bf16, fp8, kmap, vmap, s)
@@ -266,8 +155,7 @@ extern "C" size_t qsa_chunk_attention_workspace_bytes(const qsa_paged_cache* cac
   CacheView view{};
   cache_host::CacheSpans spans{};
   if (cache_host::check_cache(cache, &view, &spans) != QSA_OK || cache->num_reqs == 0 ||
-      num_tokens == 0 || !sizes_ok(*cache, num_tokens, num_heads) ||
-      cache->dtype == QSA_DT_F8E4M3)
+      num_tokens == 0 || !sizes_ok(*cache, num_tokens, num_heads))
     return 0;
   return layout_of(*cache, num_tokens, num_heads, prefix_cols >= 0).total;
 }

@@ -6,8 +6,7 @@ namespace qsa {
 
 cudaError_t launch_chunk_64(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
                             const CUtensorMap& vmap, cudaStream_t st) {
-  if (fp8) return cudaErrorNotSupported;
-  return launch_chunk<64>(p, bf16, kmap, vmap, st);
+  return launch_chunk<64>(p, bf16, fp8, kmap, vmap, st);
 }
 
 }  // namespace qsa

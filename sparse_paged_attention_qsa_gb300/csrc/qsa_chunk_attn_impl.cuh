@@ -16,7 +16,8 @@
 //   row: no reduction crosses threads.  The two are two halves of 256 rows over
 //   the same K/V tiles, or, for 128 rows and fewer, every other K/V tile of the
 //   same rows, merged at the row tile's end.  (Heads of 256 hold one O of 256
-//   columns: one warpgroup, two S.)
+//   columns: one warpgroup, two S.)  E4M3 tiles are widened to FP16 by a warpgroup
+//   of their own on the way to the ring.
 // chunk_join_kernel, chunk_join_all_kernel  join the pieces of row tiles that runs
 //   cut; with a prefix, the prefix's and the requests' own.
 //
@@ -25,8 +26,10 @@
 // that binary32 products have.  It moves only when weights would pass 2^15 (FP16)
 // or 2^8 (BF16), and O in tensor memory is rescaled at such moves alone.
 //
-// Rounding: q, K and V enter the products as they are, weights rounded to the
-// type of V.
+// Rounding: q, K and V enter the products as they are (E4M3 as FP16, exactly; BF16
+// queries of an E4M3 cache as FP16 after a power-of-two scaling of the row, where
+// only bits 2^-25 below the row's largest element can be lost), weights rounded to
+// the products' type.
 #pragma once
 
 #include "qsa_chunk_attn.h"
@@ -347,41 +350,92 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
 // --- walk -------------------------------------------------------------------------
 
 struct ChunkTables {
-  uint64_t full[16], empty[16];            // ring: K's slots, then V's
+  uint64_t full[16], empty[16];            // ring: K's slots, then V's; E4M3: both in turn
   uint64_t s_full[2], p_ready[2], q_ready, unit_done, pv_done, drain;
+  uint64_t in_full[8], in_empty[8];        // E4M3: tiles as they came, K's and V's in turn
   uint32_t boxes[kTileFlags];              // a bit per copy of a tile, 0: it had no page
   uint32_t bad[8][4];                      // entries of a V slot that hold what is not finite
-  float ml[256][2];
+  float ml[128][2];
+  float q_mul[256];                        // E4M3: what a row's queries were divided by
   uint32_t tmem;
   int32_t abort;
   int32_t pad[2];
 };
 
-template <int D>
+template <int D, bool kFp8>
 struct ChunkShape {
   static constexpr int TT = chunk_tile(D), RT = chunk_rows(D);
   static constexpr int kGroups = RT / 128;
   static constexpr int kSoft = kGroups * 128;              // softmax threads
-  static constexpr int kThreads = kSoft + 128;             // + K's, V's producer, the issuer
+  static constexpr int kConvert = kFp8 ? 128 : 0;          // and those that widen E4M3 tiles
+  static constexpr int kThreads = kSoft + kConvert + 128;  // + K's, V's producer, the issuer
   static constexpr int kBlocks = D / 64;                   // of 64 dims: a line of 128 bytes
   static constexpr int kSlot = TT * D * 2;
   static constexpr int kQTile = 128 * D * 2;
-  static constexpr int NS = D == 64 ? 4 : 2;               // slots of K, and of V
-  static constexpr int kQ = 2 * NS * kSlot;                // offsets: ring, queries, tables
-  static constexpr int kTables = kQ + kGroups * kQTile;
+  // Slots: K's and V's of their own, two each (heads of 64 four).  E4M3 tiles come in
+  // as they are and are widened into a ring that K and V share: its third slot is
+  // filled while the products read two.
+  static constexpr int NS = kFp8 ? (D == 64 ? 6 : 3) : (D == 64 ? 4 : 2);
+  static constexpr int kIn = TT * D, NI = kFp8 ? (D == 64 ? 8 : 3) : 0;
+  static constexpr int kQ = (kFp8 ? NS : 2 * NS) * kSlot;  // offsets: ring, queries, E4M3, tables
+  static constexpr int kStaged = kQ + kGroups * kQTile;
+  static constexpr int kTables = kStaged + NI * kIn;
   static constexpr size_t kSmem = 1024 + kTables + sizeof(ChunkTables);
   // tensor memory columns
   static constexpr int kS = TT, kP = D == 128 ? 0 : 2 * TT;
   static constexpr int kO = D == 128 ? 256 : D == 64 ? 384 : 256;
   static_assert(kSmem <= 232448, "shared memory");
+  // the ring's slot of tile f's K (V), and the phase in which it is full
+  static __device__ __forceinline__ int slot(int f, int kv) { return kFp8 ? (2 * f + kv) % NS : kv * NS + f % NS; }
+  static __device__ __forceinline__ uint32_t phase(int f, int kv) { return (uint32_t)((kFp8 ? (2 * f + kv) / NS : f / NS) & 1); }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1)
+// Two E4M3 values (the low, the high half of x) as FP16, exactly.
+__device__ __forceinline__ uint32_t widen_lo(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// 8 BF16 values of a row, whose others are in the kLanes aligned lanes, as FP16:
+// divided by the power of two *mul that brings the row's largest magnitude to
+// [2^14, 2^15) (1 where that has no exponent).
+template <int kLanes>
+__device__ __forceinline__ uint4 to_fp16(uint4 v, float* mul) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  float f[8], a = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[2 * k] = __uint_as_float(u[k] << 16);
+    f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    a = fmaxf(a, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+  }
+#pragma unroll
+  for (int k = 1; k < kLanes; k <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, k));
+  const int e = (int)(__float_as_uint(a) >> 23);
+  float by = 1.f;
+  *mul = 1.f;
+  if (e > 0 && e < 255) {
+    const int up = min(14 + 127 - e, 120);
+    *mul = __uint_as_float((uint32_t)(127 - up) << 23);
+    by = __uint_as_float((uint32_t)(127 + up) << 23);
+  }
+  return make_uint4(cpack2<false>(f[0] * by, f[1] * by), cpack2<false>(f[2] * by, f[3] * by),
+                    cpack2<false>(f[4] * by, f[5] * by), cpack2<false>(f[6] * by, f[7] * by));
+}
+
+// T: the type of q and out; the products' is T, or FP16 over an E4M3 cache.
+template <typename T, int D, bool kFp8>
+__global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
 chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
-  using C = ChunkShape<D>;
-  constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
+  using C = ChunkShape<D, kFp8>;
+  constexpr bool kOutBf16 = __is_same(T, __nv_bfloat16), kBf16 = kOutBf16 && !kFp8;
   constexpr int TT = C::TT, NS = C::NS;
   extern __shared__ unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -394,9 +448,13 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
   volatile int32_t* s_abort = &tb.abort;
 
   if (tid == 0) {
-    for (int i = 0; i < 2 * NS; ++i) {
-      mbar_init(bar(tb.full[i]), 1);
+    for (int i = 0; i < (kFp8 ? NS : 2 * NS); ++i) {
+      mbar_init(bar(tb.full[i]), kFp8 ? 4 : 1);
       mbar_init(bar(tb.empty[i]), 1);
+    }
+    for (int i = 0; i < C::NI; ++i) {
+      mbar_init(bar(tb.in_full[i]), 1);
+      mbar_init(bar(tb.in_empty[i]), 4);
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(bar(tb.s_full[u]), 1);
@@ -409,7 +467,7 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  constexpr int kIssuer = C::kSoft / 32 + 2;
+  constexpr int kIssuer = (C::kSoft + C::kConvert) / 32 + 2;
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(&tb.tmem)),
@@ -475,9 +533,13 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
         const bool good = want && id >= 0 && id < p.c.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, good);
         if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
-        const int i = issued % NS, slot = kv * NS + i;
-        if (issued >= NS) {
-          bool ok = *s_abort == 0 && mbar_wait(bar(tb.empty[slot]), (uint32_t)((issued / NS - 1) & 1));
+        // the slot that this fill takes: of the ring, or of the tiles as they come
+        const int n = kFp8 ? 2 * issued + kv : issued;
+        const int slot = kFp8 ? n % C::NI : C::slot(issued, kv), fills = kFp8 ? n / C::NI : issued / NS;
+        const uint32_t full = kFp8 ? bar(tb.in_full[slot]) : bar(tb.full[slot]);
+        const uint32_t empty = kFp8 ? bar(tb.in_empty[slot]) : bar(tb.empty[slot]);
+        if (fills > 0) {
+          bool ok = *s_abort == 0 && mbar_wait(empty, (uint32_t)((fills - 1) & 1));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
             if (lane == 0 && *s_abort == 0) {
@@ -488,20 +550,21 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
             break;
           }
         }
-        const uint32_t full = bar(tb.full[slot]), dst = ring + slot * C::kSlot;
         if (kv == 0) {
           if (lane == 0) tb.boxes[issued % kTileFlags] = mask;
-        } else if (lane < 4) {
-          tb.bad[i][lane] = 0;
+        } else if (!kFp8 && lane < 4) {
+          tb.bad[slot - NS][lane] = 0;
         }
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * D * 2));
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * D * (kFp8 ? 1 : 2)));
         __syncwarp();
         if (good) {
+          constexpr int kLine = kFp8 && D == 64 ? 64 : 128, kLines = D * (kFp8 ? 1 : 2) / kLine;
+          const uint32_t dst = ring + (kFp8 ? C::kStaged + slot * C::kIn : slot * C::kSlot);
 #pragma unroll
-          for (int c = 0; c < C::kBlocks; ++c)
-            tma_load_4d(dst + c * (TT * 128) + lane * box_rows * 128, kv ? &vmap : &kmap, c * 64,
-                        seg.head, be & ((1 << lg) - 1), id, full, policy);
+          for (int c = 0; c < kLines; ++c)
+            tma_load_4d(dst + c * (TT * kLine) + lane * box_rows * kLine, kv ? &vmap : &kmap,
+                        c * (kFp8 ? kLine : 64), seg.head, be & ((1 << lg) - 1), id, full, policy);
         }
         ++issued;
       }
@@ -522,9 +585,9 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
         if (*s_abort) break;
         tc5_fence_after();
         const auto qk = [&](int s) {
-          const int u = s & 1, f = fill + (dual ? s >> 1 : s), i = f % NS;
+          const int u = s & 1, f = fill + (dual ? s >> 1 : s), i = C::slot(f, 0);
           if (!dual || u == 0) {
-            wait_for(bar(tb.full[i]), (uint32_t)((f / NS) & 1));
+            wait_for(bar(tb.full[i]), C::phase(f, 0));
             tc5_fence_after();
           }
           if (*s_abort) return;
@@ -540,10 +603,10 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
           if (!dual || u == 1) tc5_commit(bar(tb.empty[i]));
         };
         const auto pv = [&](int s) {
-          const int u = s & 1, f = fill + (dual ? s >> 1 : s), i = f % NS, slot = NS + i;
+          const int u = s & 1, f = fill + (dual ? s >> 1 : s), slot = C::slot(f, 1);
           wait_for(bar(tb.p_ready[u]), (uint32_t)(ready[u] & 1));
           ++ready[u];
-          wait_for(bar(tb.full[slot]), (uint32_t)((f / NS) & 1));
+          wait_for(bar(tb.full[slot]), C::phase(f, 1));
           if (*s_abort) return;
           tc5_fence_after();
           const uint64_t v = tc5_desc(ring + slot * C::kSlot, TT * 128);
@@ -566,6 +629,46 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
       }
     }
     __syncwarp();
+  } else if (kFp8 && warp >= C::kSoft / 32) {
+    // ---------------- E4M3 tiles to FP16 ----------------
+    if constexpr (kFp8) {
+      const int ct = tid - C::kSoft;
+      int n = 0;                                           // K's and V's tiles in turn
+      while (*s_abort == 0 && walk_next(p, walk, &seg)) {
+        for (int end = n + 2 * (seg.t1 - seg.t0); n < end; ++n) {
+          const int in = n % C::NI, out = n % NS;
+          wait_for(bar(tb.in_full[in]), (uint32_t)((n / C::NI) & 1));
+          if (n >= NS) wait_for(bar(tb.empty[out]), (uint32_t)((n / NS - 1) & 1));
+          if ((n & 1) && ct < 4) tb.bad[out][ct] = 0;
+          // 16 values a thread: a piece of a line, two pieces of a line of FP16.
+          // Eight threads read one line (heads of 64: two); those of the second half
+          // store their second piece first, so that the eight write to all banks.
+          constexpr int kLine = D == 64 ? 64 : 128, kPieces = D / 16;
+          const unsigned char* src = base + C::kStaged + in * C::kIn;
+          unsigned char* dst = base + out * C::kSlot;
+#pragma unroll 4
+          for (int i = ct; i < TT * kPieces; i += 128) {
+            const int row = i / kPieces, x = i % kPieces;  // dims [16 x, 16 x + 16)
+            const int sw = D == 64 ? (row >> 1) & 3 : row & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                src + (x * 16 / kLine) * (TT * kLine) + row * kLine + (((x % (kLine / 16)) ^ sw) << 4));
+            uint4 h[2];
+            h[0] = make_uint4(widen_lo(v.x), widen_hi(v.x), widen_lo(v.y), widen_hi(v.y));
+            h[1] = make_uint4(widen_lo(v.z), widen_hi(v.z), widen_lo(v.w), widen_hi(v.w));
+            unsigned char* line = dst + (x >> 2) * (TT * 128) + row * 128;
+            const int second = (x >> 2) & 1, y = 2 * (x & 3);
+            *reinterpret_cast<uint4*>(line + (((y + second) ^ (row & 7)) << 4)) = second ? h[1] : h[0];
+            *reinterpret_cast<uint4*>(line + (((y + 1 - second) ^ (row & 7)) << 4)) = second ? h[0] : h[1];
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(tb.full[out]));
+            mbar_arrive(bar(tb.in_empty[in]));
+          }
+        }
+      }
+    }
   } else {
     // ---------------- softmax ----------------
     const int g = warp >> 2, wl = warp & 3, r = wl * 32 + lane;   // warpgroup; row of 128
@@ -583,11 +686,13 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
       if (tiles > 0) {
         constexpr int kPieces = D / 8;
         const int all = seg.tile.rows * kPieces;
-        for (int i0 = tid; i0 < all; i0 += C::kSoft * 8) {
-          uint4 v[8];
+        constexpr int kAhead = 4;
+        for (int i0 = tid; i0 - lane < all; i0 += C::kSoft * kAhead) {
+          uint4 v[kAhead];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
+          for (int x = 0; x < kAhead; ++x) {
             const int i = i0 + x * C::kSoft;
+            v[x] = make_uint4(0, 0, 0, 0);
             if (i < all) {
               const int row = seg.tile.row0 + i / kPieces, j = row / p.group;
               v[x] = *reinterpret_cast<const uint4*>(
@@ -596,13 +701,16 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
             }
           }
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int i = i0 + x * C::kSoft;
-            if (i < all) {
-              const int row = i / kPieces, piece = i % kPieces;
+          for (int x = 0; x < kAhead; ++x) {
+            const int i = i0 + x * C::kSoft, row = i / kPieces, piece = i % kPieces;
+            if constexpr (kFp8) {
+              float mul = 1.f;
+              if constexpr (kOutBf16) v[x] = to_fp16<kPieces>(v[x], &mul);
+              if (i < all && piece == 0) tb.q_mul[row] = mul;
+            }
+            if (i < all)
               *reinterpret_cast<uint4*>(base + C::kQ + (row >> 7) * C::kQTile + (piece >> 3) * (128 * 128) +
                                         (row & 127) * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v[x];
-            }
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -617,7 +725,16 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
       const int ja = seg.tile.row0 / p.group, jb = (seg.tile.row0 + seg.tile.rows - 1) / p.group;
       const int32_t in_hi = s.hi(ja), in_lo = s.lo(jb);
       const int32_t in_sink = s.window > 0 ? min(s.sink, in_hi) : 0;
-      const float mult = p.scale_log2;
+      float mult = p.scale_log2, q_mul = 1.f;
+      if constexpr (kFp8) {
+        if (tiles > 0 && kOutBf16) {                       // the row's is another thread's
+          if (C::kGroups == 2) named_sync<2, 256>();
+          else named_sync<3, 128>();
+          q_mul = tb.q_mul[mine ? row : 0];
+        }
+        if (p.c.k_scale) mult *= p.c.k_scale[seg.head];
+        mult *= q_mul;
+      }
       float m = -INFINITY, l = 0.f;
       const int steps = dual ? 2 * tiles : tiles;
       for (int st = C::kGroups == 2 ? g : 0; st < steps; st += C::kGroups) {
@@ -723,8 +840,8 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
         if (edge) {
           // 0 times what a hidden entry holds may be NaN: whatever is not finite in
           // V leaves the tile, and rows that see it get NaN
-          const int i = f % NS, slot = NS + i;
-          wait_for(bar(tb.full[slot]), (uint32_t)((f / NS) & 1));
+          const int slot = C::slot(f, 1), i = kFp8 ? slot : slot - NS;
+          wait_for(bar(tb.full[slot]), C::phase(f, 1));
           constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kUp = kBf16 ? 0x00800080u : 0x04000400u;
           uint4* v = reinterpret_cast<uint4*>(base + slot * C::kSlot);
           for (int x = r; x < C::kSlot / 16; x += 128) {
@@ -794,7 +911,7 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
         const int64_t token = first_token + qj;
         const int head = seg.head * p.group + qrow - qj * p.group;
         const bool direct = seg.whole && !p.res_o[0];
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l == 0.f ? 0.f : (kFp8 && p.c.v_scale ? p.c.v_scale[seg.head] : 1.f) / l;
         const int64_t rh = token * p.heads + head;
         const int64_t piece = (2 * (int64_t)blockIdx.x + seg.which) * p.part_rows + row;
         const int list = seg.tile.req < 0 ? 0 : 1;
@@ -802,7 +919,7 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
         if (mine) {
           if (!direct)
             *reinterpret_cast<float2*>(seg.whole ? p.res_ml[list] + rh * 2 : p.part_ml + piece * 2) =
-                make_float2(m, l);
+                make_float2(m * q_mul, l);               // as the products of q itself
           else if (p.lse)
             p.lse[rh] = row_lse<kBf16>(m, l, mult);
         }
@@ -837,10 +954,10 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4*>(out + (c + 8 * i) * 2) = make_uint4(
-                  cpack2<kBf16>(o[8 * i] * inv, o[8 * i + 1] * inv),
-                  cpack2<kBf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                  cpack2<kBf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                  cpack2<kBf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                  cpack2<kOutBf16>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                  cpack2<kOutBf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                  cpack2<kOutBf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                  cpack2<kOutBf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -858,9 +975,16 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
   __syncthreads();
   // after a time-out, what this CTA issued lands before it exits
   if (*s_abort != 0) {
-    if (warp < kIssuer && warp >= kIssuer - 2 && lane == 0)
-      for (int i = max(0, issued - NS); i < issued; ++i)
-        mbar_wait(bar(tb.full[(warp - (kIssuer - 2)) * NS + i % NS]), (uint32_t)((i / NS) & 1), kDrainLimitNs);
+    if (warp < kIssuer && warp >= kIssuer - 2 && lane == 0) {
+      const int kv = warp - (kIssuer - 2);
+      for (int i = max(0, issued - 8); i < issued; ++i) {
+        const int n = kFp8 ? 2 * i + kv : i, slots = kFp8 ? C::NI : NS;
+        const int last = kFp8 ? 2 * issued - 2 + kv : issued - 1;
+        if (n + slots <= last) continue;                   // refilled since
+        mbar_wait(kFp8 ? bar(tb.in_full[n % slots]) : bar(tb.full[C::slot(i, kv)]),
+                  (uint32_t)((n / slots) & 1), kDrainLimitNs);
+      }
+    }
     if (warp == kIssuer && lane == 0 && used) {
       tc5_commit(bar(tb.drain));
       mbar_wait(bar(tb.drain), 0, kDrainLimitNs);
@@ -893,33 +1017,41 @@ struct Acc {
   }
 };
 
+// What the logits of a K/V head are multiplied by, base 2.
+__device__ __forceinline__ float head_mult(const ChunkParams& p, int head) {
+  return p.scale_log2 * (p.c.k_scale ? p.c.k_scale[head] : 1.f);
+}
+
 // Adds what the runs [c0, c1] left of local row i of a row tile that begins at x0;
 // of them this thread's: k0, k0 + dk, ...
 template <int D>
 __device__ __forceinline__ void add_pieces(const ChunkParams& p, const ChunkRuns& r, int head, int64_t x0,
-                                           int c0, int c1, int i, int ln, int k0, int dk, Acc& acc) {
+                                           int c0, int c1, int i, int ln, int k0, int dk, float mult,
+                                           Acc& acc) {
 #pragma unroll 4
   for (int c = c0 + k0; c <= c1; c += dk) {
     const int second = c == c0 && chunk_run_start(r, c) < x0;
     const int64_t at = (int64_t)(2 * chunk_cta(r, p.c.heads, head, c) + second) * p.part_rows + i;
     acc.add(*reinterpret_cast<const float2*>(p.part_ml + at * 2),
-            *reinterpret_cast<const float4*>(p.part_o + at * D + ln * 4), p.scale_log2);
+            *reinterpret_cast<const float4*>(p.part_o + at * D + ln * 4), mult);
   }
 }
 
-template <typename T, int D>
-__device__ __forceinline__ void store_row(const ChunkParams& p, int64_t token, int head, int ln, const Acc& a) {
-  constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
-  const float inv = a.l == 0.f ? 0.f : 1.f / a.l;
+// kBf16: of out; kBf16W: of the weights, whose shift l holds.
+template <bool kBf16, bool kBf16W, int D>
+__device__ __forceinline__ void store_row(const ChunkParams& p, int64_t token, int kv_head, int g, int ln,
+                                          float mult, const Acc& a) {
+  const float inv = a.l == 0.f ? 0.f : (p.c.v_scale ? p.c.v_scale[kv_head] : 1.f) / a.l;
+  const int head = kv_head * p.group + g;
   *reinterpret_cast<uint2*>(p.out + token * p.out_row + head * p.out_head + ln * 8) =
       make_uint2(cpack2<kBf16>(a.o.x * inv, a.o.y * inv), cpack2<kBf16>(a.o.z * inv, a.o.w * inv));
   if (ln == 0 && p.lse)
-    p.lse[token * p.heads + head] = row_lse<kBf16>(a.m, a.l, p.scale_log2);
+    p.lse[token * p.heads + head] = row_lse<kBf16W>(a.m, a.l, mult);
 }
 
 // CTA (c, y): rows of the row tile that the start of CTA c's run cuts, if that is
 // its first cut.  D/4 threads a row; where it has many pieces, all threads one row.
-template <typename T, int D>
+template <bool kBf16, bool kBf16W, int D>
 __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const ChunkParams p, int ctas) {
   constexpr int L = D / 4, kG = kChunkJoinThreads / L, kFew = 12;
   __shared__ __align__(16) float4 s_o[kChunkJoinThreads];
@@ -939,28 +1071,29 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const Chu
   int32_t t0, n;
   request_rows(p, t.req, &t0, &n);
   const bool few = c1 - c0 < kFew;
+  const float mult = head_mult(p, cut.y);
   for (int i0 = blockIdx.y * (few ? kG : 1); i0 < t.rows; i0 += gridDim.y * (few ? kG : 1)) {
     const int i = few ? i0 + grp : i0;
     Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (i < t.rows)
-      add_pieces<D>(p, r, cut.y, x0, c0, c1, i, ln, few ? 0 : grp, few ? 1 : kG, a);
+      add_pieces<D>(p, r, cut.y, x0, c0, c1, i, ln, few ? 0 : grp, few ? 1 : kG, mult, a);
     if (!few) {
       __syncthreads();
       s_o[tid] = a.o;
       if (ln == 0) s_ml[grp] = make_float2(a.m, a.l);
       __syncthreads();
       if (grp > 0) continue;
-      for (int k = 1; k < kG; ++k) a.add(s_ml[k], s_o[k * L + ln], p.scale_log2);
+      for (int k = 1; k < kG; ++k) a.add(s_ml[k], s_o[k * L + ln], mult);
     }
     if (i < t.rows) {
       const int row = t.row0 + i, j = row / p.group;
-      store_row<T, D>(p, t0 + j, cut.y * p.group + row - j * p.group, ln, a);
+      store_row<kBf16, kBf16W, D>(p, t0 + j, cut.y, row - j * p.group, ln, mult, a);
     }
   }
 }
 
 // With a prefix: CTA (token, K/V head), D/4 threads a row; every row's two results.
-template <typename T, int D>
+template <bool kBf16, bool kBf16W, int D>
 __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const ChunkParams p, int ctas) {
   constexpr int L = D / 4, kG = kChunkJoinThreads / L, RT = chunk_rows(D);
   const int tid = threadIdx.x, lane = tid & 31, grp = tid / L, ln = tid % L;
@@ -969,6 +1102,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const
   const ChunkPlan plan = *p.plan;
   const ChunkRuns r = chunk_runs(plan.total, heads, ctas);
   const int head = blockIdx.y;
+  const float mult = head_mult(p, head);
   for (int32_t token = plan.token0 + blockIdx.x; token < plan.token0 + plan.tokens; token += gridDim.x) {
     // the last request that starts at or before the token, 32 at a time
     int b = 0;
@@ -991,11 +1125,11 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const
         const int64_t x0 = chunk_owners(p, r, plan.total, head, (int)k, &c0, &c1);
         if (c0 == c1)
           a.add(*reinterpret_cast<const float2*>(p.res_ml[list] + rh * 2),
-                *reinterpret_cast<const float4*>(p.res_o[list] + rh * D + ln * 4), p.scale_log2);
+                *reinterpret_cast<const float4*>(p.res_o[list] + rh * D + ln * 4), mult);
         else
-          add_pieces<D>(p, r, head, x0, c0, c1, (int)(row % RT), ln, 0, 1, a);
+          add_pieces<D>(p, r, head, x0, c0, c1, (int)(row % RT), ln, 0, 1, mult, a);
       }
-      store_row<T, D>(p, token, head * p.group + g, ln, a);
+      store_row<kBf16, kBf16W, D>(p, token, head, g, ln, mult, a);
     }
   }
 }
@@ -1003,7 +1137,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const
 // --- launch -----------------------------------------------------------------------
 
 // The SMs of the current device; the kernel's set-up once per device.
-template <typename T, int D>
+template <typename T, int D, bool kFp8>
 cudaError_t chunk_device(int* n_sms) {
   static std::mutex mu;
   static int sms[64];                                      // 0: not set up on that device
@@ -1016,8 +1150,8 @@ cudaError_t chunk_device(int* n_sms) {
     int n = 0;
     e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(chunk_walk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)ChunkShape<D>::kSmem);
+    e = cudaFuncSetAttribute(chunk_walk_kernel<T, D, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)ChunkShape<D, kFp8>::kSmem);
     if (e != cudaSuccess) return e;
     sms[dev] = std::min(n, kChunkMaxCtas);
   }
@@ -1025,32 +1159,36 @@ cudaError_t chunk_device(int* n_sms) {
   return cudaSuccess;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kFp8>
 cudaError_t launch_chunk_typed(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                cudaStream_t st) {
-  using C = ChunkShape<D>;
+  using C = ChunkShape<D, kFp8>;
+  constexpr bool kBf16 = __is_same(T, __nv_bfloat16), kBf16W = kBf16 && !kFp8;
   int ctas = 0;
-  cudaError_t e = chunk_device<T, D>(&ctas);
+  cudaError_t e = chunk_device<T, D, kFp8>(&ctas);
   if (e != cudaSuccess) return e;
   e = launch_after(chunk_plan_kernel<C::TT, C::RT>, dim3(1), dim3(kPlanThreads), 0, st, p);
   if (e != cudaSuccess) return e;
-  e = launch_after(chunk_walk_kernel<T, D>, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, st, p,
+  e = launch_after(chunk_walk_kernel<T, D, kFp8>, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, st, p,
                    kmap, vmap);
   if (e != cudaSuccess) return e;
   if (p.res_o[0])
-    return launch_after(chunk_join_all_kernel<T, D>,
+    return launch_after(chunk_join_all_kernel<kBf16, kBf16W, D>,
                         dim3((unsigned)std::min(p.tokens, 16384), (unsigned)p.c.heads),
                         dim3(kChunkJoinThreads), 0, st, p, ctas);
   const int64_t rows = std::min<int64_t>((int64_t)p.tokens * p.group, C::RT);
-  return launch_after(chunk_join_kernel<T, D>, dim3((unsigned)ctas, (unsigned)std::min<int64_t>(rows, 16)),
+  return launch_after(chunk_join_kernel<kBf16, kBf16W, D>,
+                      dim3((unsigned)ctas, (unsigned)std::min<int64_t>(rows, 16)),
                       dim3(kChunkJoinThreads), 0, st, p, ctas);
 }
 
 template <int D>
-cudaError_t launch_chunk(const ChunkParams& p, bool bf16, const CUtensorMap& kmap,
+cudaError_t launch_chunk(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, cudaStream_t st) {
-  return bf16 ? launch_chunk_typed<__nv_bfloat16, D>(p, kmap, vmap, st)
-              : launch_chunk_typed<__half, D>(p, kmap, vmap, st);
+  if (fp8) return bf16 ? launch_chunk_typed<__nv_bfloat16, D, true>(p, kmap, vmap, st)
+                       : launch_chunk_typed<__half, D, true>(p, kmap, vmap, st);
+  return bf16 ? launch_chunk_typed<__nv_bfloat16, D, false>(p, kmap, vmap, st)
+              : launch_chunk_typed<__half, D, false>(p, kmap, vmap, st);
 }
 
 }  // namespace
