@@ -61,6 +61,11 @@ __device__ __forceinline__ float cex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 template <bool kBf16>
 __device__ __forceinline__ uint32_t cpack2(float lo, float hi) {
   uint32_t r;
@@ -382,9 +387,19 @@ struct ChunkShape {
   static constexpr int kTables = kStaged + NI * kIn;
   static constexpr size_t kSmem = 1024 + kTables + sizeof(ChunkTables);
   // tensor memory columns
-  static constexpr int kS = TT, kP = D == 128 ? 0 : 2 * TT;
+  static constexpr int kS = TT, kP = D == 128 ? 64 : 2 * TT;
   static constexpr int kO = D == 128 ? 256 : D == 64 ? 384 : 256;
   static_assert(kSmem <= 232448, "shared memory");
+  // Registers: 384 threads of 168 at launch, dealt out as 208, 208 and 88 a thread
+  // of a warpgroup; over an E4M3 cache 512 of 128 as 160, 160, 96, 96.
+  static __device__ __forceinline__ void more_registers() {
+    if constexpr (kGroups == 2 && kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    else if constexpr (kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  }
+  static __device__ __forceinline__ void fewer_registers() {
+    if constexpr (kGroups == 2 && kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    else if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  }
   // the ring's slot of tile f's K (V), and the phase in which it is full
   static __device__ __forceinline__ int slot(int f, int kv) { return kFp8 ? (2 * f + kv) % NS : kv * NS + f % NS; }
   static __device__ __forceinline__ uint32_t phase(int f, int kv) { return (uint32_t)((kFp8 ? (2 * f + kv) / NS : f / NS) & 1); }
@@ -503,173 +518,8 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
   Segment seg;
   int issued = 0;                                          // a producer's fills
   bool used = false;                                       // the issuer's products
-  if (warp == kIssuer - 2 || warp == kIssuer - 1) {
-    // ---------------- producers ----------------
-    const int kv = warp - (kIssuer - 2);
-    const int lg = p.c.page_log2;
-    const int box_rows = min(TT, 1 << lg), n_boxes = TT / box_rows;
-    const uint64_t policy = evict_normal_policy();
-    bool stop = false;
-    while (!stop && walk_next(p, walk, &seg)) {
-      const Sight s = sight_of(seg);
-      const int32_t* table = s.prefix ? p.prefix_table : p.c.bt + (int64_t)seg.tile.req * p.c.bt_s0;
-      // the entries that some row sees: [0, sink) and [lo, end)
-      const int32_t end = s.hi((seg.tile.row0 + seg.tile.rows - 1) / p.group);
-      const int32_t lo = s.lo(seg.tile.row0 / p.group), sink = s.window > 0 ? min(s.sink, end) : 0;
-      int col0 = -64;                                      // 32 page ids from this column on
-      int32_t ids = -1;
-      for (int t = seg.t0; t < seg.t1; ++t) {
-        const int32_t e0 = s.at(t) * TT;
-        const int col = e0 >> lg, cols = max(1, TT >> lg);
-        if (col < col0 || col + cols > col0 + 32) {
-          col0 = col;
-          // the columns of entries below `end` are inside the table
-          ids = ((int64_t)(col + lane) << lg) < end ? __ldg(table + col + lane) : -1;
-        }
-        const int32_t id =
-            __shfl_sync(0xffffffffu, ids, col - col0 + (lane < n_boxes ? (lane * box_rows) >> lg : 0));
-        const int32_t be = e0 + lane * box_rows;
-        const bool want = lane < n_boxes && be < end && (be + box_rows > lo || be < sink);
-        const bool good = want && id >= 0 && id < p.c.num_pages;
-        const uint32_t mask = __ballot_sync(0xffffffffu, good);
-        if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
-        // the slot that this fill takes: of the ring, or of the tiles as they come
-        const int n = kFp8 ? 2 * issued + kv : issued;
-        const int slot = kFp8 ? n % C::NI : C::slot(issued, kv), fills = kFp8 ? n / C::NI : issued / NS;
-        const uint32_t full = kFp8 ? bar(tb.in_full[slot]) : bar(tb.full[slot]);
-        const uint32_t empty = kFp8 ? bar(tb.in_empty[slot]) : bar(tb.empty[slot]);
-        if (fills > 0) {
-          bool ok = *s_abort == 0 && mbar_wait(empty, (uint32_t)((fills - 1) & 1));
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) {
-            if (lane == 0 && *s_abort == 0) {
-              *s_abort = 1;
-              report(p.err, QSA_DERR_TIMEOUT);
-            }
-            stop = true;
-            break;
-          }
-        }
-        if (kv == 0) {
-          if (lane == 0) tb.boxes[issued % kTileFlags] = mask;
-        } else if (!kFp8 && lane < 4) {
-          tb.bad[slot - NS][lane] = 0;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * D * (kFp8 ? 1 : 2)));
-        __syncwarp();
-        if (good) {
-          constexpr int kLine = kFp8 && D == 64 ? 64 : 128, kLines = D * (kFp8 ? 1 : 2) / kLine;
-          const uint32_t dst = ring + (kFp8 ? C::kStaged + slot * C::kIn : slot * C::kSlot);
-#pragma unroll
-          for (int c = 0; c < kLines; ++c)
-            tma_load_4d(dst + c * (TT * kLine) + lane * box_rows * kLine, kv ? &vmap : &kmap,
-                        c * (kFp8 ? kLine : 64), seg.head, be & ((1 << lg) - 1), id, full, policy);
-        }
-        ++issued;
-      }
-    }
-  } else if (warp >= kIssuer) {
-    // ---------------- issuer ----------------
-    if (warp == kIssuer && lane == 0) {
-      constexpr uint32_t kQk = tc5_idesc(kBf16, 128, TT, false), kPv = tc5_idesc(kBf16, 128, D, true);
-      int fill = 0, units = 0;                             // tiles, row tiles before this segment
-      int ready[2] = {0, 0};
-      while (*s_abort == 0 && walk_next(p, walk, &seg)) {
-        const int tiles = seg.t1 - seg.t0;
-        if (tiles <= 0) continue;
-        const bool dual = seg.tile.rows > 128;
-        const int steps = dual ? 2 * tiles : tiles;
-        wait_for(bar(tb.q_ready), (uint32_t)(units & 1));
-        ++units;
-        if (*s_abort) break;
-        tc5_fence_after();
-        const auto qk = [&](int s) {
-          const int u = s & 1, f = fill + (dual ? s >> 1 : s), i = C::slot(f, 0);
-          if (!dual || u == 0) {
-            wait_for(bar(tb.full[i]), C::phase(f, 0));
-            tc5_fence_after();
-          }
-          if (*s_abort) return;
-          // 16 dims a product: 32 bytes on in a line of 64, then the next block of lines
-          const uint64_t q = tc5_desc(ring + C::kQ + (dual ? u * C::kQTile : 0), 16);
-          const uint64_t k = tc5_desc(ring + i * C::kSlot, 16);
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x)
-            tc5_mma_ss(tmem + u * C::kS, q + (x >> 2) * (128 * 128 / 16) + (x & 3) * 2,
-                       k + (x >> 2) * (TT * 128 / 16) + (x & 3) * 2, kQk, x > 0);
-          used = true;
-          tc5_commit(bar(tb.s_full[u]));
-          if (!dual || u == 1) tc5_commit(bar(tb.empty[i]));
-        };
-        const auto pv = [&](int s) {
-          const int u = s & 1, f = fill + (dual ? s >> 1 : s), slot = C::slot(f, 1);
-          wait_for(bar(tb.p_ready[u]), (uint32_t)(ready[u] & 1));
-          ++ready[u];
-          wait_for(bar(tb.full[slot]), C::phase(f, 1));
-          if (*s_abort) return;
-          tc5_fence_after();
-          const uint64_t v = tc5_desc(ring + slot * C::kSlot, TT * 128);
-          const uint32_t o = tmem + C::kO + (C::kGroups == 2 ? u * D : 0);
-          const uint32_t pa = tmem + C::kP + u * (D == 128 ? C::kS : TT / 2);
-          const bool more = C::kGroups == 2 ? s > 1 : s > 0;
-#pragma unroll
-          for (int x = 0; x < TT / 16; ++x)
-            tc5_mma_ts(o, pa + x * 8, v + x * (16 * 128 / 16), kPv, more || x > 0);
-          if (!dual || u == 1) tc5_commit(bar(tb.empty[slot]));
-          if (C::kGroups == 1) tc5_commit(bar(tb.pv_done));
-          if (s + 1 == steps) tc5_commit(bar(tb.unit_done));
-        };
-        qk(0);
-        for (int s = 0; s < steps && *s_abort == 0; ++s) {
-          if (s + 1 < steps) qk(s + 1);
-          pv(s);
-        }
-        fill += tiles;
-      }
-    }
-    __syncwarp();
-  } else if (kFp8 && warp >= C::kSoft / 32) {
-    // ---------------- E4M3 tiles to FP16 ----------------
-    if constexpr (kFp8) {
-      const int ct = tid - C::kSoft;
-      int n = 0;                                           // K's and V's tiles in turn
-      while (*s_abort == 0 && walk_next(p, walk, &seg)) {
-        for (int end = n + 2 * (seg.t1 - seg.t0); n < end; ++n) {
-          const int in = n % C::NI, out = n % NS;
-          wait_for(bar(tb.in_full[in]), (uint32_t)((n / C::NI) & 1));
-          if (n >= NS) wait_for(bar(tb.empty[out]), (uint32_t)((n / NS - 1) & 1));
-          if ((n & 1) && ct < 4) tb.bad[out][ct] = 0;
-          // 16 values a thread: a piece of a line, two pieces of a line of FP16.
-          // Eight threads read one line (heads of 64: two); those of the second half
-          // store their second piece first, so that the eight write to all banks.
-          constexpr int kLine = D == 64 ? 64 : 128, kPieces = D / 16;
-          const unsigned char* src = base + C::kStaged + in * C::kIn;
-          unsigned char* dst = base + out * C::kSlot;
-#pragma unroll 4
-          for (int i = ct; i < TT * kPieces; i += 128) {
-            const int row = i / kPieces, x = i % kPieces;  // dims [16 x, 16 x + 16)
-            const int sw = D == 64 ? (row >> 1) & 3 : row & 7;
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                src + (x * 16 / kLine) * (TT * kLine) + row * kLine + (((x % (kLine / 16)) ^ sw) << 4));
-            uint4 h[2];
-            h[0] = make_uint4(widen_lo(v.x), widen_hi(v.x), widen_lo(v.y), widen_hi(v.y));
-            h[1] = make_uint4(widen_lo(v.z), widen_hi(v.z), widen_lo(v.w), widen_hi(v.w));
-            unsigned char* line = dst + (x >> 2) * (TT * 128) + row * 128;
-            const int second = (x >> 2) & 1, y = 2 * (x & 3);
-            *reinterpret_cast<uint4*>(line + (((y + second) ^ (row & 7)) << 4)) = second ? h[1] : h[0];
-            *reinterpret_cast<uint4*>(line + (((y + 1 - second) ^ (row & 7)) << 4)) = second ? h[0] : h[1];
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(tb.full[out]));
-            mbar_arrive(bar(tb.in_empty[in]));
-          }
-        }
-      }
-    }
-  } else {
+  if (warp < C::kSoft / 32) {
+    C::more_registers();
     // ---------------- softmax ----------------
     const int g = warp >> 2, wl = warp & 3, r = wl * 32 + lane;   // warpgroup; row of 128
     const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
@@ -770,32 +620,41 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
           for (int w = 0; w < TT / 32; ++w) vis[w] = 0xffffffffu;
         }
-        // S comes from tensor memory twice, 32 columns at a time, for the maximum and
-        // for the weights: all of it at once does not fit in registers
         const uint32_t zs = lanes + u * C::kS;
-        const auto columns = [&](auto&& use) {
-          uint32_t z[2][32];
-          tc5_ld32(zs, z[0]);
+        if (edge) {                                        // hidden entries: -inf
 #pragma unroll
           for (int w = 0; w < TT / 32; ++w) {
-            uint32_t(&x)[32] = z[w & 1];
+            uint32_t x[32];
+            tc5_ld32(zs + w * 32, x);
             tc5_wait_ld();
             tc5_hold(x);
-            if (w + 1 < TT / 32) tc5_ld32(zs + (w + 1) * 32, z[(w + 1) & 1]);
-            if (edge) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((vis[w] >> i) & 1u)) x[i] = 0xff800000u;
-            }
-            use(w, x);
+            for (int i = 0; i < 32; ++i)
+              if (!((vis[w] >> i) & 1u)) x[i] = 0xff800000u;
+            tc5_st(zs + w * 32, x);
           }
-        };
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        columns([&](int, uint32_t(&x)[32]) {
+          tc5_wait_st();
+        }
+        // with the registers of an E4M3 walk half a row at a time, the first half read
+        // again for its weights (P, which shares S's columns with heads of 128, takes
+        // those of the second)
+        constexpr int kWords = TT / 32, kKeep = kFp8 && TT == 128 ? 2 : kWords, kFirst = kWords - kKeep;
+        uint32_t z[kKeep][32];
+        float mx[kWords];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
-        });
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), old = m;
+        for (int w0 = 0; w0 < kWords; w0 += kKeep) {
+#pragma unroll
+          for (int w = 0; w < kKeep; ++w) tc5_ld32_max(zs + (w0 + w) * 32, z[w], mx[w0 + w]);
+          tc5_wait_ld();
+#pragma unroll
+          for (int w = 0; w < kKeep; ++w) {
+            tc5_hold(z[w]);
+            tc5_hold(mx[w0 + w]);
+          }
+        }
+        float top = fmaxf(mx[0], mx[1]);
+        if constexpr (TT == 128) top = max3(top, mx[2], mx[3]);
+        const float old = m;
         const bool move = (top - m) * mult > chunk_slack(kBf16);
         if (move) m = top;
         if (__any_sync(0xffffffffu, move)) {
@@ -824,18 +683,34 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
         const float2 shift2 = make_float2(chunk_shift(kBf16), chunk_shift(kBf16));
         const uint32_t pa = lanes + C::kP + u * (D == 128 ? C::kS : TT / 2);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        columns([&](int w, uint32_t(&x)[32]) {
+        const auto weights = [&](int w, uint32_t(&x)[32]) {
           uint32_t h[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 z = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-            const float2 y = ffma2(fadd2(z, ref2), mult2, shift2);
+            const float2 y = ffma2(
+                fadd2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), ref2), mult2,
+                shift2);
             const float2 e = make_float2(cex2(y.x), cex2(y.y));
             sum[i & 1] = fadd2(sum[i & 1], e);
             h[i] = cpack2<kBf16>(e.x, e.y);
           }
           tc5_st(pa + w * 16, h);
-        });
+        };
+        if constexpr (kFirst == 0) {
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) weights(w, z[w]);
+        } else {
+          weights(2, z[0]);
+          tc5_ld32(zs, z[0]);
+          weights(3, z[1]);
+          tc5_wait_ld();
+          tc5_hold(z[0]);
+          tc5_ld32(zs + 32, z[1]);
+          weights(0, z[0]);
+          tc5_wait_ld();
+          tc5_hold(z[1]);
+          weights(1, z[1]);
+        }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (edge) {
           // 0 times what a hidden entry holds may be NaN: whatever is not finite in
@@ -971,6 +846,180 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
       if (split && steps > 1) named_sync<2, 256>();          // the stage is free for queries
       tc5_fence_before();
     }
+  } else {
+    C::fewer_registers();
+    if (warp == kIssuer - 2 || warp == kIssuer - 1) {
+    // ---------------- producers ----------------
+    const int kv = warp - (kIssuer - 2);
+    const int lg = p.c.page_log2;
+    const int box_rows = min(TT, 1 << lg), n_boxes = TT / box_rows;
+    const uint64_t policy = evict_normal_policy();
+    bool stop = false;
+    while (!stop && walk_next(p, walk, &seg)) {
+      const Sight s = sight_of(seg);
+      const int32_t* table = s.prefix ? p.prefix_table : p.c.bt + (int64_t)seg.tile.req * p.c.bt_s0;
+      // the entries that some row sees: [0, sink) and [lo, end)
+      const int32_t end = s.hi((seg.tile.row0 + seg.tile.rows - 1) / p.group);
+      const int32_t lo = s.lo(seg.tile.row0 / p.group), sink = s.window > 0 ? min(s.sink, end) : 0;
+      int col0 = -64;                                      // 32 page ids from this column on
+      int32_t ids = -1;
+      for (int t = seg.t0; t < seg.t1; ++t) {
+        const int32_t e0 = s.at(t) * TT;
+        const int col = e0 >> lg, cols = max(1, TT >> lg);
+        if (col < col0 || col + cols > col0 + 32) {
+          col0 = col;
+          // the columns of entries below `end` are inside the table
+          ids = ((int64_t)(col + lane) << lg) < end ? __ldg(table + col + lane) : -1;
+        }
+        const int32_t id =
+            __shfl_sync(0xffffffffu, ids, col - col0 + (lane < n_boxes ? (lane * box_rows) >> lg : 0));
+        const int32_t be = e0 + lane * box_rows;
+        const bool want = lane < n_boxes && be < end && (be + box_rows > lo || be < sink);
+        const bool good = want && id >= 0 && id < p.c.num_pages;
+        const uint32_t mask = __ballot_sync(0xffffffffu, good);
+        if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
+        // the slot that this fill takes: of the ring, or of the tiles as they come
+        const int n = kFp8 ? 2 * issued + kv : issued;
+        const int slot = kFp8 ? n % C::NI : C::slot(issued, kv), fills = kFp8 ? n / C::NI : issued / NS;
+        const uint32_t full = kFp8 ? bar(tb.in_full[slot]) : bar(tb.full[slot]);
+        const uint32_t empty = kFp8 ? bar(tb.in_empty[slot]) : bar(tb.empty[slot]);
+        if (fills > 0) {
+          bool ok = *s_abort == 0 && mbar_wait(empty, (uint32_t)((fills - 1) & 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            if (lane == 0 && *s_abort == 0) {
+              *s_abort = 1;
+              report(p.err, QSA_DERR_TIMEOUT);
+            }
+            stop = true;
+            break;
+          }
+        }
+        if (kv == 0) {
+          if (lane == 0) tb.boxes[issued % kTileFlags] = mask;
+        } else if (!kFp8 && lane < 4) {
+          tb.bad[slot - NS][lane] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * D * (kFp8 ? 1 : 2)));
+        __syncwarp();
+        if (good) {
+          constexpr int kLine = kFp8 && D == 64 ? 64 : 128, kLines = D * (kFp8 ? 1 : 2) / kLine;
+          const uint32_t dst = ring + (kFp8 ? C::kStaged + slot * C::kIn : slot * C::kSlot);
+#pragma unroll
+          for (int c = 0; c < kLines; ++c)
+            tma_load_4d(dst + c * (TT * kLine) + lane * box_rows * kLine, kv ? &vmap : &kmap,
+                        c * (kFp8 ? kLine : 64), seg.head, be & ((1 << lg) - 1), id, full, policy);
+        }
+        ++issued;
+      }
+    }
+    } else if (warp >= kIssuer) {
+    // ---------------- issuer ----------------
+    if (warp == kIssuer) {
+      constexpr uint32_t kQk = tc5_idesc(kBf16, 128, TT, false), kPv = tc5_idesc(kBf16, 128, D, true);
+      int fill = 0, units = 0;                             // tiles, row tiles before this segment
+      int ready[2] = {0, 0};
+      const auto stopped = [&]() { return __any_sync(0xffffffffu, *s_abort != 0); };
+      while (!stopped() && walk_next(p, walk, &seg)) {
+        // the same in every lane, and said so
+        const int tiles = __shfl_sync(0xffffffffu, seg.t1 - seg.t0, 0);
+        const bool dual = __shfl_sync(0xffffffffu, seg.tile.rows, 0) > 128;
+        if (tiles <= 0) continue;
+        const int steps = dual ? 2 * tiles : tiles;
+        wait_for(bar(tb.q_ready), (uint32_t)(units & 1));
+        ++units;
+        if (stopped()) break;
+        tc5_fence_after();
+        const auto qk = [&](int s) {
+          const int u = s & 1, f = fill + (dual ? s >> 1 : s), i = C::slot(f, 0);
+          if (!dual || u == 0) {
+            wait_for(bar(tb.full[i]), C::phase(f, 0));
+            tc5_fence_after();
+          }
+          // 16 dims a product: 32 bytes on in a line of 64, then the next block of lines
+          const uint64_t q = tc5_desc(ring + C::kQ + (dual ? u * C::kQTile : 0), 16);
+          const uint64_t k = tc5_desc(ring + i * C::kSlot, 16);
+          if (tc5_elect()) {
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+              tc5_mma_ss(tmem + u * C::kS, q + (x >> 2) * (128 * 128 / 16) + (x & 3) * 2,
+                         k + (x >> 2) * (TT * 128 / 16) + (x & 3) * 2, kQk, x > 0);
+            tc5_commit(bar(tb.s_full[u]));
+            if (!dual || u == 1) tc5_commit(bar(tb.empty[i]));
+          }
+          used = true;
+        };
+        const auto pv = [&](int s) {
+          const int u = s & 1, f = fill + (dual ? s >> 1 : s), slot = C::slot(f, 1);
+          wait_for(bar(tb.p_ready[u]), (uint32_t)(ready[u] & 1));
+          ++ready[u];
+          wait_for(bar(tb.full[slot]), C::phase(f, 1));
+          tc5_fence_after();
+          const uint64_t v = tc5_desc(ring + slot * C::kSlot, TT * 128);
+          const uint32_t o = tmem + C::kO + (C::kGroups == 2 ? u * D : 0);
+          const uint32_t pa = tmem + C::kP + u * (D == 128 ? C::kS : TT / 2);
+          const bool more = C::kGroups == 2 ? s > 1 : s > 0;
+          if (tc5_elect()) {
+#pragma unroll
+            for (int x = 0; x < TT / 16; ++x)
+              tc5_mma_ts(o, pa + x * 8, v + x * (16 * 128 / 16), kPv, more || x > 0);
+            if (!dual || u == 1) tc5_commit(bar(tb.empty[slot]));
+            if (C::kGroups == 1) tc5_commit(bar(tb.pv_done));
+            if (s + 1 == steps) tc5_commit(bar(tb.unit_done));
+          }
+        };
+        qk(0);
+        // (after a time-out without waits, on whatever the buffers hold)
+        for (int s = 0; s < steps; ++s) {
+          if (s + 1 < steps) qk(s + 1);
+          pv(s);
+        }
+        fill += tiles;
+      }
+    }
+    __syncwarp();
+    } else {
+    // ---------------- E4M3 tiles to FP16 ----------------
+    if constexpr (kFp8) {
+      const int ct = tid - C::kSoft;
+      int n = 0;                                           // K's and V's tiles in turn
+      while (*s_abort == 0 && walk_next(p, walk, &seg)) {
+        for (int end = n + 2 * (seg.t1 - seg.t0); n < end; ++n) {
+          const int in = n % C::NI, out = n % NS;
+          wait_for(bar(tb.in_full[in]), (uint32_t)((n / C::NI) & 1));
+          if (n >= NS) wait_for(bar(tb.empty[out]), (uint32_t)((n / NS - 1) & 1));
+          if ((n & 1) && ct < 4) tb.bad[out][ct] = 0;
+          // 16 values a thread: a piece of a line, two pieces of a line of FP16.
+          // Eight threads read one line (heads of 64: two); those of the second half
+          // store their second piece first, so that the eight write to all banks.
+          constexpr int kLine = D == 64 ? 64 : 128, kPieces = D / 16;
+          const unsigned char* src = base + C::kStaged + in * C::kIn;
+          unsigned char* dst = base + out * C::kSlot;
+#pragma unroll 4
+          for (int i = ct; i < TT * kPieces; i += 128) {
+            const int row = i / kPieces, x = i % kPieces;  // dims [16 x, 16 x + 16)
+            const int sw = D == 64 ? (row >> 1) & 3 : row & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                src + (x * 16 / kLine) * (TT * kLine) + row * kLine + (((x % (kLine / 16)) ^ sw) << 4));
+            uint4 h[2];
+            h[0] = make_uint4(widen_lo(v.x), widen_hi(v.x), widen_lo(v.y), widen_hi(v.y));
+            h[1] = make_uint4(widen_lo(v.z), widen_hi(v.z), widen_lo(v.w), widen_hi(v.w));
+            unsigned char* line = dst + (x >> 2) * (TT * 128) + row * 128;
+            const int second = (x >> 2) & 1, y = 2 * (x & 3);
+            *reinterpret_cast<uint4*>(line + (((y + second) ^ (row & 7)) << 4)) = second ? h[1] : h[0];
+            *reinterpret_cast<uint4*>(line + (((y + 1 - second) ^ (row & 7)) << 4)) = second ? h[0] : h[1];
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(tb.full[out]));
+            mbar_arrive(bar(tb.in_empty[in]));
+          }
+        }
+      }
+    }
+    }
   }
   __syncthreads();
   // after a time-out, what this CTA issued lands before it exits
@@ -985,8 +1034,8 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
                   (uint32_t)((n / slots) & 1), kDrainLimitNs);
       }
     }
-    if (warp == kIssuer && lane == 0 && used) {
-      tc5_commit(bar(tb.drain));
+    if (warp == kIssuer && __any_sync(0xffffffffu, used)) {
+      if (tc5_elect()) tc5_commit(bar(tb.drain));
       mbar_wait(bar(tb.drain), 0, kDrainLimitNs);
     }
     __syncthreads();

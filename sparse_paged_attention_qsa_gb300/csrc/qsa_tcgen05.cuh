@@ -13,6 +13,13 @@ __device__ __forceinline__ void tc5_fence_before() {
 __device__ __forceinline__ void tc5_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// One lane of a converged warp.  The warp runs the issuing loop together, so that
+// descriptors stay in uniform registers; the elected lane issues.
+__device__ __forceinline__ bool tc5_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 // one arrival on `bar` when all products that this thread has issued are done
 __device__ __forceinline__ void tc5_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -63,6 +70,14 @@ __device__ __forceinline__ void tc5_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
+// the same, and the largest of them (NaN apart)
+__device__ __forceinline__ void tc5_ld32_max(uint32_t taddr, uint32_t (&r)[32], float& top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(top)
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tc5_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -70,6 +85,8 @@ __device__ __forceinline__ void tc5_hold(uint32_t (&r)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
+
+__device__ __forceinline__ void tc5_hold(float& x) { asm volatile("" : "+f"(x)); }
 
 // 32 and 16 columns
 __device__ __forceinline__ void tc5_st(uint32_t taddr, const uint32_t (&r)[32]) {
