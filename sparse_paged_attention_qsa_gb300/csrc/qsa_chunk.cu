@@ -23,11 +23,11 @@ struct Layout {
   size_t tiles, pos, first, cuts, part_ml, part_o, res_ml[2], res_o[2], total;
 };
 Layout layout_of(const qsa_paged_cache& c, int64_t tokens, int64_t heads, bool prefix) {
-  const int64_t rows = tokens * (heads / c.num_heads), rt = chunk_rows((int)c.head_dim);
-  const int64_t tiles = (rows + rt - 1) / rt;
+  const int sub = chunk_heads((int)(heads / c.num_heads)), accs = chunk_accs((int)c.head_dim);
+  const int64_t acc_toks = 128 / sub, per = accs * acc_toks, tiles = (tokens + per - 1) / per;
   Layout l;
   l.max_tiles = tiles + std::min(c.num_reqs, tokens) + (prefix ? tiles : 0);
-  l.part_rows = std::min(rows, rt);
+  l.part_rows = tokens > acc_toks ? accs * 128 : tokens * sub;
   size_t at = round256(sizeof(ChunkPlan));
   const auto take = [&](size_t bytes) {
     const size_t x = at;
@@ -46,6 +46,22 @@ Layout layout_of(const qsa_paged_cache& c, int64_t tokens, int64_t heads, bool p
   }
   l.total = at;
   return l;
+}
+
+// q as (dim, head, token); a box is 64 dims (128 bytes) of a set's heads and of an
+// accumulator's tokens.
+bool encode_queries(CUtensorMap* map, const ChunkParams& p) {
+  const auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)p.c.dim, (cuuint64_t)p.heads, (cuuint64_t)p.tokens};
+  // a dimension of size 1 has any stride; the encoder wants a legal one
+  const cuuint64_t row = (cuuint64_t)p.c.dim * 2;
+  const cuuint64_t strides[2] = {p.q_head ? (cuuint64_t)p.q_head : row, p.q_row ? (cuuint64_t)p.q_row : row};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.sub, (cuuint32_t)p.acc_toks};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<unsigned char*>(p.q), dims, strides, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool sizes_ok(const qsa_paged_cache& c, int64_t tokens, int64_t heads) {
@@ -111,7 +127,11 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   p.ctx = ctx;
   p.tokens = (int32_t)tokens;
   p.heads = (int32_t)heads;
-  p.group = (int32_t)(heads / cache->num_heads);
+  const int group = (int)(heads / cache->num_heads);
+  p.sub = chunk_heads(group);
+  p.sets = (int32_t)(heads / p.sub);
+  p.per_kv = group / p.sub;
+  p.acc_toks = 128 / p.sub;
   p.scale_log2 = scale_log2;
   p.window = (int32_t)std::min<int64_t>(window, INT32_MAX - 16);
   p.sink = window > 0 ? (int32_t)std::min<int64_t>(sink, kMaxEntries) : 0;
@@ -135,13 +155,14 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
     p.res_o[i] = reinterpret_cast<float*>(w + l.res_o[i]);
   }
   const int box = (int)std::min<int64_t>(cache->page_size, chunk_tile(p.c.dim));
-  CUtensorMap kmap, vmap;
+  CUtensorMap kmap, vmap, qmap;
   if (!encode_view(&kmap, p.c.k, p.c, fp8 ? 1 : 2, p.c.k_page, p.c.k_token, p.c.k_head, box) ||
-      !encode_view(&vmap, p.c.v, p.c, fp8 ? 1 : 2, p.c.v_page, p.c.v_token, p.c.v_head, box))
+      !encode_view(&vmap, p.c.v, p.c, fp8 ? 1 : 2, p.c.v_page, p.c.v_token, p.c.v_head, box) ||
+      !encode_queries(&qmap, p))
     return QSA_ERR_CUDA;
-  const cudaError_t e = p.c.dim == 64    ? launch_chunk_64(p, bf16, fp8, kmap, vmap, s)
-                        : p.c.dim == 128 ? launch_chunk_128(p, bf16, fp8, kmap, vmap, s)
-                                         : launch_chunk_256(p, bf16, fp8, kmap, vmap, s);
+  const cudaError_t e = p.c.dim == 64    ? launch_chunk_64(p, bf16, fp8, kmap, vmap, qmap, s)
+                        : p.c.dim == 128 ? launch_chunk_128(p, bf16, fp8, kmap, vmap, qmap, s)
+                                         : launch_chunk_256(p, bf16, fp8, kmap, vmap, qmap, s);
   return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 

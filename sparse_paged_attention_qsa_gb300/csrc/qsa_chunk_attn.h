@@ -13,22 +13,28 @@ namespace qsa {
 
 constexpr int kChunkMaxCtas = 152;     // CTAs of the tile walk, one an SM (what the workspace is sized for)
 
-// Tokens of a K/V tile, and the query rows of a K/V head that share a walk over
-// the tiles: two tensor memory accumulators of 128 rows, one for heads of 256.
+// Tokens of a K/V tile, and the accumulators of 128 query rows that share a walk
+// over the tiles: two in tensor memory, one for heads of 256.
 constexpr int chunk_tile(int dim) { return dim == 256 ? 64 : 128; }
-constexpr int chunk_rows(int dim) { return dim == 256 ? 128 : 256; }
-// What a row tile costs beside its K/V tiles, in K/V tiles: its queries come in
-// and its output goes out while the products wait.
-constexpr int kChunkExtra = 2;
+constexpr int chunk_accs(int dim) { return dim == 256 ? 1 : 2; }
+// Query heads whose rows one accumulator holds side by side: the K/V head's group, or
+// the largest part of it that divides it and fits.
+inline int chunk_heads(int group) {
+  int n = group < 128 ? group : 128;
+  while (group % n != 0) --n;
+  return n;
+}
+// What a row tile costs beside its K/V tiles, in K/V tiles.
+constexpr int kChunkExtra = 1;
 
-// Query rows of one K/V head that walk K/V tiles together.  Row i of a request
-// is head i % group of its token i / group.
+// Query rows of one set of heads that walk K/V tiles together: the tokens [tok0, tok0
+// + toks) of a request, 128 / sub of them in each accumulator.
 struct ChunkTile {
   int32_t req;                  // its request; -1: the prefix, whose rows are all requests'
-  int32_t row0, rows, tiles;    // rows [row0, row0 + rows), K/V tiles they see
+  int32_t tok0, toks, tiles;    // its tokens, and the K/V tiles they see
 };
 struct ChunkPlan {
-  int64_t total;                // cost of all row tiles of one K/V head
+  int64_t total;                // cost of all row tiles of one set of heads
   int32_t n, n_prefix;          // row tiles, the first ones the prefix's
   int32_t token0, tokens;       // rows of q that belong to requests
 };
@@ -44,7 +50,10 @@ struct ChunkParams {
   int64_t out_row, out_head;    // bytes
   const int32_t* starts;        // [num_reqs + 1]
   const int32_t* ctx;
-  int32_t tokens, heads, group;
+  int32_t tokens, heads;
+  int32_t sub;                  // query heads of a set, whose rows walk together
+  int32_t sets, per_kv;         // sets in all, and of one K/V head
+  int32_t acc_toks;             // tokens of an accumulator: 128 / sub
   float scale_log2;             // scale * log2(e)
   int32_t window;               // 0: none; at most INT32_MAX - 16
   int32_t sink;                 // 0 without a window
@@ -56,19 +65,22 @@ struct ChunkParams {
   ChunkTile* tiles;             // [max_tiles]
   int64_t* pos;                 // [max_tiles + 1] cost of the row tiles before each
   int32_t* first;               // [num_reqs] each request's first row tile
-  int2* cuts;                   // [kChunkMaxCtas] row tile (-1: none) and head that a run cuts
-  int32_t part_rows;            // rows of a row tile, at most
+  int2* cuts;                   // [kChunkMaxCtas] row tile (-1: none) and set that a run cuts
+  int32_t part_rows;            // rows of a row tile, at most; accumulators 128 apart
   float* part_ml;               // [2 * kChunkMaxCtas][part_rows][2]
   float* part_o;                // [2 * kChunkMaxCtas][part_rows][dim]
   float* res_ml[2];             // with a prefix: whole results [tokens][heads][2], of the
   float* res_o[2];              //   prefix and of the requests' own entries [..][dim]
+#ifdef QSA_WAIT_TEST
+  int32_t test_withhold;        // test build: CTA 0 issues no copy for this slot fill (-1: none)
+#endif
 };
 
 cudaError_t launch_chunk_64(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
-                            const CUtensorMap& vmap, cudaStream_t st);
+                            const CUtensorMap& vmap, const CUtensorMap& qmap, cudaStream_t st);
 cudaError_t launch_chunk_128(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
-                             const CUtensorMap& vmap, cudaStream_t st);
+                            const CUtensorMap& vmap, const CUtensorMap& qmap, cudaStream_t st);
 cudaError_t launch_chunk_256(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
-                             const CUtensorMap& vmap, cudaStream_t st);
+                            const CUtensorMap& vmap, const CUtensorMap& qmap, cudaStream_t st);
 
 }  // namespace qsa

@@ -5,8 +5,8 @@
 namespace qsa {
 
 cudaError_t launch_chunk_64(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
-                            const CUtensorMap& vmap, cudaStream_t st) {
-  return launch_chunk<64>(p, bf16, fp8, kmap, vmap, st);
+                            const CUtensorMap& vmap, const CUtensorMap& qmap, cudaStream_t st) {
+  return launch_chunk<64>(p, bf16, fp8, kmap, vmap, qmap, st);
 }
 
 }  // namespace qsa

@@ -8,16 +8,16 @@
 // chunk_plan_kernel  cuts each request's rows into row tiles (and, where there is
 //   a prefix, all requests' rows once more) and lays their K/V tiles end to end.
 // chunk_walk_kernel  one CTA an SM walks an equal run of them.
-//   Two producer warps look pages up and load K and V tiles into a ring by TMA;
-//   one thread issues the products, S = Q K^T with Q and K in shared memory into
-//   tensor memory, then O += P V with P in tensor memory: 128 rows a product, two
-//   products' S and O beside each other, so that one is in the softmax while the
-//   other is in the tensor pipe.  Two warpgroups form the softmax, a thread a
-//   row: no reduction crosses threads.  The two are two halves of 256 rows over
-//   the same K/V tiles, or, for 128 rows and fewer, every other K/V tile of the
-//   same rows, merged at the row tile's end.  (Heads of 256 hold one O of 256
-//   columns: one warpgroup, two S.)  E4M3 tiles are widened to FP16 by a warpgroup
-//   of their own on the way to the ring.
+//   Three producer warps load the queries and, by way of the page tables, K and V
+//   tiles into a ring, all by TMA; one warp issues the products, S = Q K^T with Q
+//   and K in shared memory into tensor memory, then O += P V with P in tensor
+//   memory: 128 rows a product, two products' S and O beside each other, so that
+//   one is in the softmax while the other is in the tensor pipe.  Two warpgroups
+//   form the softmax, a thread a row: no reduction crosses threads.  The two hold
+//   two halves of 256 rows over the same K/V tiles, or, for 128 rows and fewer,
+//   every other K/V tile of the same rows, merged at the row tile's end.  (Heads of
+//   256 hold one O of 256 columns: one warpgroup, two S.)  Four more warps widen
+//   E4M3 tiles to FP16 on their way to the ring.
 // chunk_join_kernel, chunk_join_all_kernel  join the pieces of row tiles that runs
 //   cut; with a prefix, the prefix's and the requests' own.
 //
@@ -132,6 +132,7 @@ __device__ __forceinline__ Sight prefix_sight(const ChunkParams& p) {
   s.tiles = (s.cap + TT - 1) / TT;
   return s;
 }
+// of the tokens [j0, j1] of a request with ctx entries, n of them new
 template <int TT>
 __device__ __forceinline__ Sight request_sight(const ChunkParams& p, int32_t ctx, int32_t n, int j0,
                                                int j1) {
@@ -153,11 +154,11 @@ __device__ __forceinline__ int32_t tile_cost(int32_t tiles) {
   return tiles > 0 ? tiles + kChunkExtra : 1;
 }
 
-// Equal runs of all heads' row tiles.  Where the heads divide the CTAs evenly
-// enough every head has the same runs, so that the K/V heads of the same
+// Equal runs of all sets' row tiles.  Where the sets divide the CTAs evenly enough
+// every set has the same runs, so that the K/V heads of the same
 // entries, whose elements lie side by side, are read at the same time.
 struct ChunkRuns {
-  int64_t total, each, more;    // of one head, or of all
+  int64_t total, each, more;    // of one set of heads, or of all
   int n;                        // runs of it
   bool by_head;
 };
@@ -191,35 +192,37 @@ __device__ __forceinline__ int64_t chunk_owners(const ChunkParams& p, const Chun
   return base + a;
 }
 
-// The segments of a CTA: K/V tiles [t0, t1) of a row tile of one K/V head.
+// The segments of a CTA: K/V tiles [t0, t1) of a row tile of one set of heads.
 struct Segment {
-  int k, head, t0, t1, which;
-  bool whole;
-  ChunkTile tile;
+  Sight sight;
+  int32_t k, set, t0, t1;
+  int32_t req, token, tok0, toks;   // token: the row of q that tok0 counts from
+  int32_t which, whole;
 };
 struct Walk {
-  int64_t x, x1, total, base;    // position, end; cost of a head; where the head begins
-  int k, n, head;
+  int64_t x, x1, total, base;    // position, end; cost of a set; where the set begins
+  int k, n, set, token0;
   bool first;
 };
-__device__ __forceinline__ Walk walk_begin(const ChunkParams& p, int heads) {
+__device__ __forceinline__ void walk_begin(const ChunkParams& p, Walk* walk) {
   Walk w;
   const ChunkPlan plan = *p.plan;
   w.total = plan.total;
   w.n = plan.n;
+  w.token0 = plan.token0;
   w.first = true;
-  const ChunkRuns r = chunk_runs(plan.total, heads, gridDim.x);
+  const ChunkRuns r = chunk_runs(plan.total, p.sets, gridDim.x);
   if (r.by_head) {
-    const int run = blockIdx.x / heads;
-    w.head = blockIdx.x % heads;
+    const int run = blockIdx.x / p.sets;
+    w.set = blockIdx.x % p.sets;
     w.base = 0;
     w.x = run < r.n ? chunk_run_start(r, run) : 0;
     w.x1 = run < r.n ? chunk_run_start(r, run + 1) : 0;
   } else {
     w.x = chunk_run_start(r, blockIdx.x);
     w.x1 = chunk_run_start(r, blockIdx.x + 1);
-    w.head = plan.total > 0 ? (int)(w.x / plan.total) : 0;
-    w.base = w.total * w.head;
+    w.set = plan.total > 0 ? (int)(w.x / plan.total) : 0;
+    w.base = w.total * w.set;
   }
   int lo = 0, hi = w.n - 1;
   const int64_t at = w.x - w.base;
@@ -228,32 +231,56 @@ __device__ __forceinline__ Walk walk_begin(const ChunkParams& p, int heads) {
     if (p.pos[mid] <= at) lo = mid; else hi = mid - 1;
   }
   w.k = lo;
-  return w;
+  if ((threadIdx.x & 31) == 0) *walk = w;
+  __syncwarp();
 }
-// The next segment with something to do; false at the run's end.
-__device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk& w, Segment* s) {
-  while (w.x < w.x1) {
+// The next segment with something to do; false at the run's end.  A warp keeps its
+// place and its segments in shared memory: registers are short.
+template <int TT>
+__device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk* walk, Segment* segment) {
+  Walk w = *walk;
+  Segment s0, *s = &s0;
+  bool found = false;
+  while (!found && w.x < w.x1) {
     if (w.k == w.n) {
       w.k = 0;
-      ++w.head;
+      ++w.set;
       w.base += w.total;
     }
     const int64_t a = w.base + p.pos[w.k], b = w.base + p.pos[w.k + 1];
+    const ChunkTile t = p.tiles[w.k];
     const int64_t end = b < w.x1 ? b : w.x1;
+    const int extra = t.tiles > 0 ? kChunkExtra : 0;
     s->k = w.k;
-    s->head = w.head;
-    s->tile = p.tiles[w.k];
-    const int extra = s->tile.tiles > 0 ? kChunkExtra : 0;
+    s->set = w.set;
     s->t0 = (int)max((int64_t)0, w.x - a - extra);
-    s->t1 = s->tile.tiles > 0 ? (int)max((int64_t)0, end - a - extra) : 0;
-    s->whole = s->t0 == 0 && s->t1 == s->tile.tiles;
+    s->t1 = t.tiles > 0 ? (int)max((int64_t)0, end - a - extra) : 0;
+    s->whole = s->t0 == 0 && s->t1 == t.tiles;
     s->which = w.first ? 0 : 1;
     w.first = false;
     w.x = end;
     ++w.k;
-    if (s->t1 > s->t0 || s->tile.tiles == 0) return true;
+    if (s->t1 <= s->t0 && t.tiles > 0) continue;
+    s->req = t.req;
+    s->tok0 = t.tok0;
+    s->toks = t.toks;
+    if (t.req < 0) {
+      s->token = w.token0;
+      s->sight = prefix_sight<TT>(p);
+    } else {
+      int32_t n;
+      request_rows(p, t.req, &s->token, &n);
+      s->sight = request_sight<TT>(p, p.ctx[t.req], n, t.tok0, t.tok0 + t.toks - 1);
+    }
+    found = true;
   }
-  return false;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    *walk = w;
+    if (found) *segment = s0;
+  }
+  __syncwarp();
+  return found;
 }
 
 // --- plan -------------------------------------------------------------------------
@@ -286,17 +313,16 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
 // One CTA: row tiles of each request, then the cost of each row tile, both summed
 // up.  Row tiles past what the workspace holds (starts that are not in order) are
 // left out.
-template <int TT, int RT>
+template <int TT, int kAccs>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
   __shared__ int64_t s_sums[32];
-  const int tid = threadIdx.x, R = p.c.num_reqs;
+  const int tid = threadIdx.x, R = p.c.num_reqs, RT = kAccs * p.acc_toks;   // tokens of a row tile
   pdl_wait();
   const int32_t token0 = min(max(p.starts[0], 0), p.tokens);
   const int32_t tokens = min(max(p.starts[R], token0), p.tokens) - token0;
   const Sight pre = prefix_sight<TT>(p);
   if (tid == 0 && p.prefix_table && *p.prefix_len > p.prefix_cap) report(p.err, QSA_DERR_CONTEXT);
-  const int64_t all_rows = (int64_t)tokens * p.group;
-  const int n_prefix = pre.tiles > 0 ? (int)((all_rows + RT - 1) / RT) : 0;
+  const int n_prefix = pre.tiles > 0 ? (tokens + RT - 1) / RT : 0;
   int64_t before = n_prefix, all;
   for (int b0 = 0; b0 < R; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -304,7 +330,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     if (b < R) {
       int32_t t0, n;
       request_rows(p, b, &t0, &n);
-      k = ((int64_t)n * p.group + RT - 1) / RT;
+      k = (n + RT - 1) / RT;
       if (n > 0 && p.ctx[b] > p.c.cap) report(p.err, QSA_DERR_CONTEXT);
     }
     const int64_t at = before + block_scan(k, s_sums, &all);
@@ -321,8 +347,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       ChunkTile t;
       if (k < n_prefix) {
         t.req = -1;
-        t.row0 = k * RT;
-        t.rows = (int)min((int64_t)RT, all_rows - t.row0);
+        t.tok0 = k * RT;
+        t.toks = min(RT, tokens - t.tok0);
         t.tiles = pre.tiles;
       } else {
         int lo = 0, hi = R - 1;              // the last request that begins at or before k
@@ -333,10 +359,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         int32_t t0, m;
         request_rows(p, lo, &t0, &m);
         t.req = lo;
-        t.row0 = (k - p.first[lo]) * RT;
-        t.rows = (int)min((int64_t)RT, (int64_t)m * p.group - t.row0);
-        t.tiles = request_sight<TT>(p, p.ctx[lo], m, t.row0 / p.group,
-                                    (t.row0 + t.rows - 1) / p.group).tiles;
+        t.tok0 = (k - p.first[lo]) * RT;
+        t.toks = min(RT, m - t.tok0);
+        t.tiles = request_sight<TT>(p, p.ctx[lo], m, t.tok0, t.tok0 + t.toks - 1).tiles;
       }
       p.tiles[k] = t;
       c = tile_cost(t.tiles);
@@ -356,24 +381,27 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
 
 struct ChunkTables {
   uint64_t full[16], empty[16];            // ring: K's slots, then V's; E4M3: both in turn
-  uint64_t s_full[2], p_ready[2], q_ready, unit_done, pv_done, drain;
   uint64_t in_full[8], in_empty[8];        // E4M3: tiles as they came, K's and V's in turn
+  uint64_t s_full[2], p_half[2][2], o_done[2], scanned[2];
+  uint64_t q_full, q_ready, q_free, pv_done, drain;
   uint32_t boxes[kTileFlags];              // a bit per copy of a tile, 0: it had no page
   uint32_t bad[8][4];                      // entries of a V slot that hold what is not finite
   float ml[128][2];
-  float q_mul[256];                        // E4M3: what a row's queries were divided by
+  float q_mul[2][256];                     // E4M3: what a row's queries were divided by
+  Walk walk[16];                           // of each warp
+  Segment seg[16][2];                      // this one, the next one
   uint32_t tmem;
   int32_t abort;
-  int32_t pad[2];
+  int32_t pad[3];
 };
 
 template <int D, bool kFp8>
 struct ChunkShape {
-  static constexpr int TT = chunk_tile(D), RT = chunk_rows(D);
-  static constexpr int kGroups = RT / 128;
+  static constexpr int TT = chunk_tile(D);
+  static constexpr int kGroups = chunk_accs(D);            // softmax warpgroups
   static constexpr int kSoft = kGroups * 128;              // softmax threads
   static constexpr int kConvert = kFp8 ? 128 : 0;          // and those that widen E4M3 tiles
-  static constexpr int kThreads = kSoft + kConvert + 128;  // + K's, V's producer, the issuer
+  static constexpr int kThreads = kSoft + kConvert + 128;  // + K's, V's, Q's producer, the issuer
   static constexpr int kBlocks = D / 64;                   // of 64 dims: a line of 128 bytes
   static constexpr int kSlot = TT * D * 2;
   static constexpr int kQTile = 128 * D * 2;
@@ -382,9 +410,12 @@ struct ChunkShape {
   // filled while the products read two.
   static constexpr int NS = kFp8 ? (D == 64 ? 6 : 3) : (D == 64 ? 4 : 2);
   static constexpr int kIn = TT * D, NI = kFp8 ? (D == 64 ? 8 : 3) : 0;
-  static constexpr int kQ = (kFp8 ? NS : 2 * NS) * kSlot;  // offsets: ring, queries, E4M3, tables
+  // columns of O that a warp's rows leave through shared memory at a time
+  static constexpr int kOutCols = kFp8 && D == 128 ? 8 : 16;
+  static constexpr int kQ = (kFp8 ? NS : 2 * NS) * kSlot;  // offsets: ring, queries, E4M3, output, tables
   static constexpr int kStaged = kQ + kGroups * kQTile;
-  static constexpr int kTables = kStaged + NI * kIn;
+  static constexpr int kOut = kStaged + NI * kIn;
+  static constexpr int kTables = kOut + kGroups * 4 * 32 * kOutCols * 4;
   static constexpr size_t kSmem = 1024 + kTables + sizeof(ChunkTables);
   // tensor memory columns
   static constexpr int kS = TT, kP = D == 128 ? 64 : 2 * TT;
@@ -417,41 +448,53 @@ __device__ __forceinline__ uint32_t widen_hi(uint32_t x) {
   return r;
 }
 
-// 8 BF16 values of a row, whose others are in the kLanes aligned lanes, as FP16:
-// divided by the power of two *mul that brings the row's largest magnitude to
-// [2^14, 2^15) (1 where that has no exponent).
-template <int kLanes>
-__device__ __forceinline__ uint4 to_fp16(uint4 v, float* mul) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  float f[8], a = 0.f;
+// Row r of a query tile, BF16, as FP16 in its place: divided by the power of two,
+// returned, that brings its largest magnitude to [2^14, 2^15) (1 where that has no
+// exponent).
+template <int D>
+__device__ __forceinline__ float row_to_fp16(unsigned char* tile, int r) {
+  const auto at = [&](int x) {
+    return reinterpret_cast<uint4*>(tile + (x >> 3) * (128 * 128) + r * 128 + (((x & 7) ^ (r & 7)) << 4));
+  };
+  float a = 0.f;
+#pragma unroll 4
+  for (int x = 0; x < D / 8; ++x) {
+    const uint4 v = *at(x);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __uint_as_float(u[k] << 16);
-    f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-    a = fmaxf(a, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+    for (int k = 0; k < 4; ++k)
+      a = fmaxf(a, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u))));
   }
-#pragma unroll
-  for (int k = 1; k < kLanes; k <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, k));
   const int e = (int)(__float_as_uint(a) >> 23);
-  float by = 1.f;
-  *mul = 1.f;
+  float mul = 1.f, by = 1.f;
   if (e > 0 && e < 255) {
     const int up = min(14 + 127 - e, 120);
-    *mul = __uint_as_float((uint32_t)(127 - up) << 23);
+    mul = __uint_as_float((uint32_t)(127 - up) << 23);
     by = __uint_as_float((uint32_t)(127 + up) << 23);
   }
-  return make_uint4(cpack2<false>(f[0] * by, f[1] * by), cpack2<false>(f[2] * by, f[3] * by),
-                    cpack2<false>(f[4] * by, f[5] * by), cpack2<false>(f[6] * by, f[7] * by));
+#pragma unroll 4
+  for (int x = 0; x < D / 8; ++x) {
+    const uint4 v = *at(x);
+    const auto half = [&](uint32_t u) {
+      return cpack2<false>(__uint_as_float(u << 16) * by, __uint_as_float(u & 0xffff0000u) * by);
+    };
+    *at(x) = make_uint4(half(v.x), half(v.y), half(v.z), half(v.w));
+  }
+  return mul;
 }
 
 // T: the type of q and out; the products' is T, or FP16 over an E4M3 cache.
 template <typename T, int D, bool kFp8>
 __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
-chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
-                  const __grid_constant__ CUtensorMap vmap) {
+chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
   using C = ChunkShape<D, kFp8>;
   constexpr bool kOutBf16 = __is_same(T, __nv_bfloat16), kBf16 = kOutBf16 && !kFp8;
+  constexpr bool kQToFp16 = kOutBf16 && kFp8;
   constexpr int TT = C::TT, NS = C::NS;
+  // S of an E4M3 walk is read half a row at a time, the second half's weights first
+  constexpr int kWords = TT / 32, kKeep = kFp8 && TT == 128 ? 2 : kWords, kFirst = kWords - kKeep;
+  constexpr int kHalf0 = kFirst > 0 ? 1 : 0;               // the half of P that comes first
   extern __shared__ unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
@@ -473,16 +516,20 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(bar(tb.s_full[u]), 1);
-      mbar_init(bar(tb.p_ready[u]), 4);
+      mbar_init(bar(tb.p_half[u][0]), 4);
+      mbar_init(bar(tb.p_half[u][1]), 4);
+      mbar_init(bar(tb.o_done[u]), 1);
+      mbar_init(bar(tb.scanned[u]), 4);
     }
-    mbar_init(bar(tb.q_ready), C::kSoft / 32);
-    mbar_init(bar(tb.unit_done), 1);
+    mbar_init(bar(tb.q_full), 1);
+    mbar_init(bar(tb.q_ready), 4);
+    mbar_init(bar(tb.q_free), 1);
     mbar_init(bar(tb.pv_done), 1);
     mbar_init(bar(tb.drain), 1);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  constexpr int kIssuer = (C::kSoft + C::kConvert) / 32 + 2;
+  constexpr int kProducer = (C::kSoft + C::kConvert) / 32, kIssuer = kProducer + 2, kQueries = kProducer + 3;
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(&tb.tmem)),
@@ -505,107 +552,72 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
       report(p.err, QSA_DERR_TIMEOUT);
     }
   };
-  const auto sight_of = [&](const Segment& s) {
-    if (s.tile.req < 0) return prefix_sight<TT>(p);
-    int32_t t0, n;
-    request_rows(p, s.tile.req, &t0, &n);
-    return request_sight<TT>(p, p.ctx[s.tile.req], n, s.tile.row0 / p.group,
-                             (s.tile.row0 + s.tile.rows - 1) / p.group);
-  };
-
-  const int heads = p.c.heads;
-  Walk walk = walk_begin(p, heads);
-  Segment seg;
+  Walk* walk = &tb.walk[warp];
+  walk_begin(p, walk);
   int issued = 0;                                          // a producer's fills
   bool used = false;                                       // the issuer's products
+  int withheld = -1;                                       // test build: a slot fill left out
   if (warp < C::kSoft / 32) {
     C::more_registers();
     // ---------------- softmax ----------------
     const int g = warp >> 2, wl = warp & 3, r = wl * 32 + lane;   // warpgroup; row of 128
     const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
     const int box_log2 = min(p.c.page_log2, TT == 128 ? 7 : 6);
+    const int rj = r / p.sub, rh = r - rj * p.sub;         // the row's token and head in its accumulator
+    float* out_stage = reinterpret_cast<float*>(base + C::kOut + warp * (32 * C::kOutCols * 4));
     int fill = 0, units = 0, steps_done = 0;
-    int got[2] = {0, 0};
-    while (walk_next(p, walk, &seg)) {
+    int got[2] = {0, 0}, outs = 0, scans = 0;              // S of each buffer, O taken, V searched so far
+    int slot_of = 0;
+    bool more = walk_next<TT>(p, walk, &tb.seg[warp][0]);
+    while (more) {
+      const Segment& seg = tb.seg[warp][slot_of];
+      const Sight& s = seg.sight;
+      bool asked = false;                                  // for the next segment
       const int tiles = seg.t1 - seg.t0;
-      const bool dual = seg.tile.rows > 128;
-      const Sight s = sight_of(seg);
-      const int32_t first_token =
-          seg.tile.req < 0 ? p.plan->token0 : min(max(p.starts[seg.tile.req], 0), p.tokens);
-      // queries: 16-byte pieces of the rows' lines
-      if (tiles > 0) {
-        constexpr int kPieces = D / 8;
-        const int all = seg.tile.rows * kPieces;
-        constexpr int kAhead = 4;
-        for (int i0 = tid; i0 - lane < all; i0 += C::kSoft * kAhead) {
-          uint4 v[kAhead];
-#pragma unroll
-          for (int x = 0; x < kAhead; ++x) {
-            const int i = i0 + x * C::kSoft;
-            v[x] = make_uint4(0, 0, 0, 0);
-            if (i < all) {
-              const int row = seg.tile.row0 + i / kPieces, j = row / p.group;
-              v[x] = *reinterpret_cast<const uint4*>(
-                  p.q + (int64_t)(first_token + j) * p.q_row +
-                  (int64_t)(seg.head * p.group + row - j * p.group) * p.q_head + i % kPieces * 16);
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < kAhead; ++x) {
-            const int i = i0 + x * C::kSoft, row = i / kPieces, piece = i % kPieces;
-            if constexpr (kFp8) {
-              float mul = 1.f;
-              if constexpr (kOutBf16) v[x] = to_fp16<kPieces>(v[x], &mul);
-              if (i < all && piece == 0) tb.q_mul[row] = mul;
-            }
-            if (i < all)
-              *reinterpret_cast<uint4*>(base + C::kQ + (row >> 7) * C::kQTile + (piece >> 3) * (128 * 128) +
-                                        (row & 127) * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v[x];
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(tb.q_ready));
-      }
+      const bool dual = seg.toks > p.acc_toks;
       // this thread's row, and what all rows see
-      const int row = (dual ? g * 128 : 0) + r;
-      const bool mine = row < seg.tile.rows;
-      const int j = (seg.tile.row0 + min(row, seg.tile.rows - 1)) / p.group;
+      const int jt = (dual ? g * p.acc_toks : 0) + rj;     // of the row tile's tokens
+      const bool mine = rj < p.acc_toks && jt < seg.toks;
+      const int j = seg.tok0 + min(jt, seg.toks - 1), jl = seg.tok0 + seg.toks - 1;
       const int32_t hi = s.hi(j), lo = s.lo(j), sink = s.window > 0 ? min(s.sink, hi) : 0;
-      const int ja = seg.tile.row0 / p.group, jb = (seg.tile.row0 + seg.tile.rows - 1) / p.group;
-      const int32_t in_hi = s.hi(ja), in_lo = s.lo(jb);
+      const int32_t in_hi = s.hi(seg.tok0), in_lo = s.lo(jl);
       const int32_t in_sink = s.window > 0 ? min(s.sink, in_hi) : 0;
+      const int kv_head = seg.set / p.per_kv;
       float mult = p.scale_log2, q_mul = 1.f;
       if constexpr (kFp8) {
-        if (tiles > 0 && kOutBf16) {                       // the row's is another thread's
-          if (C::kGroups == 2) named_sync<2, 256>();
-          else named_sync<3, 128>();
-          q_mul = tb.q_mul[mine ? row : 0];
-        }
-        if (p.c.k_scale) mult *= p.c.k_scale[seg.head];
-        mult *= q_mul;
+        if (p.c.k_scale) mult *= p.c.k_scale[kv_head];
       }
       float m = -INFINITY, l = 0.f;
       const int steps = dual ? 2 * tiles : tiles;
-      for (int st = C::kGroups == 2 ? g : 0; st < steps; st += C::kGroups) {
+      // K/V tile t of the segment: from 0 on up to the sinks' end, then the window's
+      const int first_tile = seg.t0, first_gap = s.ns - seg.t0, rest_tile = seg.t0 - s.ns + s.w0;
+      int st = C::kGroups == 2 ? g : 0;
+      do {
+        if (st < steps) {
         const int u = st & 1, t = dual ? st >> 1 : st, f = fill + t;
-        const int32_t e0 = s.at(seg.t0 + t) * TT;
+        const int32_t e0 = (t < first_gap ? t + first_tile : t + rest_tile) * TT;
         wait_for(bar(tb.s_full[u]), (uint32_t)(got[u] & 1));
         ++got[u];
         tc5_fence_after();
+        if constexpr (kQToFp16) {
+          if (st < C::kGroups) {                           // the row's first
+            q_mul = tb.q_mul[units & 1][(dual ? g * 128 : 0) + r];
+            mult *= q_mul;
+          }
+        }
         const uint32_t boxes = tb.boxes[f % kTileFlags];
         const bool edge = e0 + TT > in_hi || (e0 < in_lo && e0 + TT > in_sink) ||
                           boxes != (1u << (TT >> box_log2)) - 1;
-        uint32_t vis[TT / 32];
-        if (edge) {
+        const uint32_t zs = lanes + u * C::kS;
+        uint32_t vis[kWords];
+        if (edge) {                                        // hidden entries: -inf
 #pragma unroll
-          for (int w = 0; w < TT / 32; ++w) {
+          for (int w = 0; w < kWords; ++w) {
             const int32_t b = e0 + w * 32;
             const auto upto = [&](int32_t x) -> uint32_t {   // entries below x
               const int32_t n = min(max(x - b, 0), 32);
               return n == 32 ? 0xffffffffu : (1u << n) - 1;
             };
-            uint32_t v = (upto(hi) & ~upto(lo)) | upto(sink);
             uint32_t there = 0;
             if (box_log2 >= 5) {
               there = (boxes >> ((w * 32) >> box_log2)) & 1u ? 0xffffffffu : 0u;
@@ -614,16 +626,7 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
               for (int x = 0; x < 32 >> box_log2; ++x)
                 if ((boxes >> (((w * 32) >> box_log2) + x)) & 1u) there |= one << (x << box_log2);
             }
-            vis[w] = v & there;
-          }
-        } else {
-#pragma unroll
-          for (int w = 0; w < TT / 32; ++w) vis[w] = 0xffffffffu;
-        }
-        const uint32_t zs = lanes + u * C::kS;
-        if (edge) {                                        // hidden entries: -inf
-#pragma unroll
-          for (int w = 0; w < TT / 32; ++w) {
+            vis[w] = ((upto(hi) & ~upto(lo)) | upto(sink)) & there;
             uint32_t x[32];
             tc5_ld32(zs + w * 32, x);
             tc5_wait_ld();
@@ -634,11 +637,13 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
             tc5_st(zs + w * 32, x);
           }
           tc5_wait_st();
+        } else {
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) vis[w] = 0xffffffffu;
         }
         // with the registers of an E4M3 walk half a row at a time, the first half read
         // again for its weights (P, which shares S's columns with heads of 128, takes
         // those of the second)
-        constexpr int kWords = TT / 32, kKeep = kFp8 && TT == 128 ? 2 : kWords, kFirst = kWords - kKeep;
         uint32_t z[kKeep][32];
         float mx[kWords];
 #pragma unroll
@@ -696,9 +701,18 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
           }
           tc5_st(pa + w * 16, h);
         };
+        const auto ready = [&](int half) {                 // the half's product may begin
+          tc5_wait_st();
+          tc5_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(tb.p_half[u][half]));
+        };
         if constexpr (kFirst == 0) {
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) weights(w, z[w]);
+          for (int w = 0; w < kWords / 2; ++w) weights(w, z[w]);
+          if (!edge) ready(0);
+#pragma unroll
+          for (int w = kWords / 2; w < kWords; ++w) weights(w, z[w]);
         } else {
           weights(2, z[0]);
           tc5_ld32(zs, z[0]);
@@ -706,6 +720,7 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
           tc5_wait_ld();
           tc5_hold(z[0]);
           tc5_ld32(zs + 32, z[1]);
+          if (!edge) ready(1);
           weights(0, z[0]);
           tc5_wait_ld();
           tc5_hold(z[1]);
@@ -731,212 +746,281 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (g == 0) named_sync<3, 128>();
-          else named_sync<4, 128>();
+          // (an mbarrier: which tiles are edges is not sure to be the same in all warps
+          // after a time-out, and waits on it end)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(tb.scanned[g]));
+          wait_for(bar(tb.scanned[g]), (uint32_t)(scans & 1));
+          ++scans;
 #pragma unroll
-          for (int w = 0; w < TT / 32; ++w)
+          for (int w = 0; w < kWords; ++w)
             if (vis[w] & *reinterpret_cast<volatile uint32_t*>(&tb.bad[i][w])) l = NAN;
+          ready(kHalf0);
         }
-        tc5_wait_st();
-        tc5_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(tb.p_ready[u]));
-      }
+        ready(1 - kHalf0);
+        }
+        if (!asked) more = walk_next<TT>(p, walk, &tb.seg[warp][slot_of ^ 1]);
+        asked = true;
+        st += C::kGroups;
+      } while (st < steps);
       steps_done += steps;
       fill += tiles;
+      if (tiles > 0) ++units;
       // ---- the row tile's end
-      if (tiles > 0) {
-        wait_for(bar(tb.unit_done), (uint32_t)(units & 1));
-        ++units;
+      const bool split = C::kGroups == 2 && !dual;         // both warpgroups hold the same rows
+      const bool both = split && steps > 1;
+      if (steps > 0 && (!split || g < steps)) {
+        wait_for(bar(tb.o_done[g]), (uint32_t)(outs & 1));
+        ++outs;
         tc5_fence_after();
       }
-      const bool split = C::kGroups == 2 && !dual;         // both warpgroups hold the same rows
-      float f0 = 1.f, f1 = 0.f;
-      if (split && steps > 1) {
-        float4* stage = reinterpret_cast<float4*>(base + C::kQ);
-        if (g == 1) {
-          tb.ml[r][0] = m;
-          tb.ml[r][1] = l;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t x[32];
-            tc5_ld32(lanes + C::kO + D + c, x);
-            tc5_wait_ld();
-            tc5_hold(x);
-            if (mine) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                stage[r * (D / 4) + ((c / 4 + i) ^ (r & 7))] =
-                    make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
-                                __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
-            }
+      const bool some = __any_sync(0xffffffffu, mine);     // the same in both warps of a pair
+      if (some && (!split || g == 0 || both)) {
+        // rows go out by way of shared memory, kOutCols columns at a time, so that
+        // stores are whole sectors; of a pair of warps that hold the same rows the
+        // second hands its columns to the first
+        const auto pair_sync = [&]() {
+          if (wl == 0) named_sync<5, 64>();
+          else if (wl == 1) named_sync<6, 64>();
+          else if (wl == 2) named_sync<7, 64>();
+          else named_sync<8, 64>();
+        };
+        float f0 = 1.f, f1 = 0.f;
+        if (both) {
+          if (g == 1) {
+            tb.ml[r][0] = m;
+            tb.ml[r][1] = l;
+          }
+          pair_sync();
+          if (g == 0) {
+            const float m1 = tb.ml[r][0], l1 = tb.ml[r][1], M = fmaxf(m, m1);
+            f0 = m == -INFINITY ? 0.f : cex2((m - M) * mult);
+            f1 = m1 == -INFINITY ? 0.f : cex2((m1 - M) * mult);
+            l = l * f0 + l1 * f1;
+            m = M;
           }
         }
-        named_sync<2, 256>();
-        if (g == 0) {
-          const float m1 = tb.ml[r][0], l1 = tb.ml[r][1], M = fmaxf(m, m1);
-          f0 = m == -INFINITY ? 0.f : cex2((m - M) * mult);
-          f1 = m1 == -INFINITY ? 0.f : cex2((m1 - M) * mult);
-          l = l * f0 + l1 * f1;
-          m = M;
-        }
-      }
-      if (!split || g == 0) {
-        const int qrow = seg.tile.row0 + row, qj = qrow / p.group;
-        const int64_t token = first_token + qj;
-        const int head = seg.head * p.group + qrow - qj * p.group;
+        const bool first = g == 0 || !split;               // writes
         const bool direct = seg.whole && !p.res_o[0];
-        const float inv = l == 0.f ? 0.f : (kFp8 && p.c.v_scale ? p.c.v_scale[seg.head] : 1.f) / l;
-        const int64_t rh = token * p.heads + head;
-        const int64_t piece = (2 * (int64_t)blockIdx.x + seg.which) * p.part_rows + row;
-        const int list = seg.tile.req < 0 ? 0 : 1;
-        float* dst = seg.whole ? p.res_o[list] + rh * D : p.part_o + piece * D;
-        if (mine) {
-          if (!direct)
-            *reinterpret_cast<float2*>(seg.whole ? p.res_ml[list] + rh * 2 : p.part_ml + piece * 2) =
-                make_float2(m * q_mul, l);               // as the products of q itself
-          else if (p.lse)
-            p.lse[rh] = row_lse<kBf16>(m, l, mult);
+        const int64_t token = seg.token + seg.tok0 + jt;
+        const int head = seg.set * p.sub + rh;
+        const int64_t at = token * p.heads + head;
+        const int list = seg.req < 0 ? 0 : 1;
+        const int64_t piece = (2 * (int64_t)blockIdx.x + seg.which) * p.part_rows + (dual ? g * 128 : 0) + r;
+        uint64_t dst = 0;                                  // the row's first element
+        float inv = 1.f;
+        if (mine && first) {
+          if (direct) {
+            dst = reinterpret_cast<uint64_t>(p.out + token * p.out_row + head * p.out_head);
+            inv = l == 0.f ? 0.f : (kFp8 && p.c.v_scale ? p.c.v_scale[kv_head] : 1.f) / l;
+            if (p.lse) p.lse[at] = row_lse<kBf16>(m, l, mult);
+          } else {
+            dst = reinterpret_cast<uint64_t>(seg.whole ? p.res_o[list] + at * D : p.part_o + piece * D);
+            *reinterpret_cast<float2*>(seg.whole ? p.res_ml[list] + at * 2 : p.part_ml + piece * 2) =
+                make_float2(m * q_mul, l);                 // as the products of q itself
+          }
         }
-        unsigned char* out = p.out + token * p.out_row + head * p.out_head;
-        const float4* stage = reinterpret_cast<const float4*>(base + C::kQ);
+        if (inv != 1.f) f0 *= inv, f1 *= inv;
+        constexpr int kQuads = C::kOutCols / 4;            // of a staged row
+        float4* stage = reinterpret_cast<float4*>(out_stage);
+        const auto place = [&](int row, int q) {           // eight rows' quads on all banks
+          return row * kQuads + (kQuads == 4 ? q ^ ((row >> 1) & 3) : q ^ ((row >> 2) & 1));
+        };
+        const float4* other = stage + 4 * 32 * kQuads;     // the second warpgroup's
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t x[32];
           if (tiles > 0) {
-            tc5_ld32(lanes + C::kO + (C::kGroups == 2 && dual ? g * D : 0) + c, x);
+            tc5_ld32(lanes + C::kO + (C::kGroups == 2 ? g * D : 0) + c, x);
             tc5_wait_ld();
             tc5_hold(x);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = 0;
           }
-          if (!mine) continue;
-          float o[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]);
-          if (split && steps > 1) {
+          for (int h = 0; h < 32; h += C::kOutCols) {
+            if (!first) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 y = stage[r * (D / 4) + ((c / 4 + i) ^ (r & 7))];
-              o[4 * i] = o[4 * i] * f0 + y.x * f1;
-              o[4 * i + 1] = o[4 * i + 1] * f0 + y.y * f1;
-              o[4 * i + 2] = o[4 * i + 2] * f0 + y.z * f1;
-              o[4 * i + 3] = o[4 * i + 3] * f0 + y.w * f1;
+              for (int q = 0; q < kQuads; ++q)
+                stage[place(lane, q)] =
+                    make_float4(__uint_as_float(x[h + 4 * q]), __uint_as_float(x[h + 4 * q + 1]),
+                                __uint_as_float(x[h + 4 * q + 2]), __uint_as_float(x[h + 4 * q + 3]));
+              pair_sync();                                 // there
+              pair_sync();                                 // taken
+              continue;
             }
-          }
-          if (direct) {
+            if (both) pair_sync();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(out + (c + 8 * i) * 2) = make_uint4(
-                  cpack2<kOutBf16>(o[8 * i] * inv, o[8 * i + 1] * inv),
-                  cpack2<kOutBf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                  cpack2<kOutBf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                  cpack2<kOutBf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-          } else {
+            for (int q = 0; q < kQuads; ++q) {
+              float4 o = make_float4(__uint_as_float(x[h + 4 * q]) * f0, __uint_as_float(x[h + 4 * q + 1]) * f0,
+                                     __uint_as_float(x[h + 4 * q + 2]) * f0, __uint_as_float(x[h + 4 * q + 3]) * f0);
+              if (both) {
+                const float4 y = other[place(lane, q)];
+                o.x = fmaf(y.x, f1, o.x);
+                o.y = fmaf(y.y, f1, o.y);
+                o.z = fmaf(y.z, f1, o.z);
+                o.w = fmaf(y.w, f1, o.w);
+              }
+              stage[place(lane, q)] = o;
+            }
+            if (both) pair_sync();
+            __syncwarp();
+            if (direct) {
+              constexpr int kLanes = C::kOutCols / 8;      // 16 bytes a lane
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(dst + c + 4 * i) =
-                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              for (int k = 0; k < kLanes; ++k) {
+                const int row = k * (32 / kLanes) + lane / kLanes, q = lane % kLanes * 2;
+                const uint64_t d = __shfl_sync(0xffffffffu, dst, row);
+                const float4 a = stage[place(row, q)], b = stage[place(row, q + 1)];
+                if (d)
+                  *reinterpret_cast<uint4*>(d + (uint64_t)(c + h + q * 4) * 2) =
+                      make_uint4(cpack2<kOutBf16>(a.x, a.y), cpack2<kOutBf16>(a.z, a.w),
+                                 cpack2<kOutBf16>(b.x, b.y), cpack2<kOutBf16>(b.z, b.w));
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < kQuads; ++k) {
+                const int row = k * (32 / kQuads) + lane / kQuads, q = lane % kQuads;
+                const uint64_t d = __shfl_sync(0xffffffffu, dst, row);
+                if (d) *reinterpret_cast<float4*>(d + (uint64_t)(c + h + q * 4) * 4) = stage[place(row, q)];
+              }
+            }
+            __syncwarp();
           }
         }
         // a run's first row tile, where it is not its beginning: for the join
-        if (seg.which == 0 && seg.t0 > 0 && row == 0) p.cuts[blockIdx.x] = make_int2(seg.k, seg.head);
+        if (seg.which == 0 && seg.t0 > 0 && r == 0 && g == 0) p.cuts[blockIdx.x] = make_int2(seg.k, seg.set);
       }
-      if (split && steps > 1) named_sync<2, 256>();          // the stage is free for queries
       tc5_fence_before();
+      slot_of ^= 1;
     }
   } else {
     C::fewer_registers();
-    if (warp == kIssuer - 2 || warp == kIssuer - 1) {
-    // ---------------- producers ----------------
-    const int kv = warp - (kIssuer - 2);
-    const int lg = p.c.page_log2;
-    const int box_rows = min(TT, 1 << lg), n_boxes = TT / box_rows;
-    const uint64_t policy = evict_normal_policy();
-    bool stop = false;
-    while (!stop && walk_next(p, walk, &seg)) {
-      const Sight s = sight_of(seg);
-      const int32_t* table = s.prefix ? p.prefix_table : p.c.bt + (int64_t)seg.tile.req * p.c.bt_s0;
-      // the entries that some row sees: [0, sink) and [lo, end)
-      const int32_t end = s.hi((seg.tile.row0 + seg.tile.rows - 1) / p.group);
-      const int32_t lo = s.lo(seg.tile.row0 / p.group), sink = s.window > 0 ? min(s.sink, end) : 0;
-      int col0 = -64;                                      // 32 page ids from this column on
-      int32_t ids = -1;
-      for (int t = seg.t0; t < seg.t1; ++t) {
-        const int32_t e0 = s.at(t) * TT;
-        const int col = e0 >> lg, cols = max(1, TT >> lg);
-        if (col < col0 || col + cols > col0 + 32) {
-          col0 = col;
-          // the columns of entries below `end` are inside the table
-          ids = ((int64_t)(col + lane) << lg) < end ? __ldg(table + col + lane) : -1;
-        }
-        const int32_t id =
-            __shfl_sync(0xffffffffu, ids, col - col0 + (lane < n_boxes ? (lane * box_rows) >> lg : 0));
-        const int32_t be = e0 + lane * box_rows;
-        const bool want = lane < n_boxes && be < end && (be + box_rows > lo || be < sink);
-        const bool good = want && id >= 0 && id < p.c.num_pages;
-        const uint32_t mask = __ballot_sync(0xffffffffu, good);
-        if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
-        // the slot that this fill takes: of the ring, or of the tiles as they come
-        const int n = kFp8 ? 2 * issued + kv : issued;
-        const int slot = kFp8 ? n % C::NI : C::slot(issued, kv), fills = kFp8 ? n / C::NI : issued / NS;
-        const uint32_t full = kFp8 ? bar(tb.in_full[slot]) : bar(tb.full[slot]);
-        const uint32_t empty = kFp8 ? bar(tb.in_empty[slot]) : bar(tb.empty[slot]);
-        if (fills > 0) {
-          bool ok = *s_abort == 0 && mbar_wait(empty, (uint32_t)((fills - 1) & 1));
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) {
-            if (lane == 0 && *s_abort == 0) {
-              *s_abort = 1;
-              report(p.err, QSA_DERR_TIMEOUT);
-            }
-            stop = true;
-            break;
+    if (warp == kProducer || warp == kProducer + 1) {
+      // ---------------- producers of K and V ----------------
+      const int kv = warp - kProducer;
+      const int lg = p.c.page_log2;
+      const int box_rows = min(TT, 1 << lg), n_boxes = TT / box_rows;
+      const uint64_t policy = evict_normal_policy();
+      bool stop = false;
+      const Segment& seg = tb.seg[warp][0];
+      while (!stop && walk_next<TT>(p, walk, &tb.seg[warp][0])) {
+        const Sight& s = seg.sight;
+        const int32_t* table = s.prefix ? p.prefix_table : p.c.bt + (int64_t)seg.req * p.c.bt_s0;
+        const int kv_head = seg.set / p.per_kv;
+        // the entries that some row sees: [0, sink) and [lo, end)
+        const int32_t end = s.hi(seg.tok0 + seg.toks - 1), lo = s.lo(seg.tok0);
+        const int32_t sink = s.window > 0 ? min(s.sink, end) : 0;
+        int col0 = -64;                                    // 32 page ids from this column on
+        int32_t ids = -1;
+        for (int t = seg.t0; t < seg.t1; ++t) {
+          const int32_t e0 = s.at(t) * TT;
+          const int col = e0 >> lg, cols = max(1, TT >> lg);
+          if (col < col0 || col + cols > col0 + 32) {
+            col0 = col;
+            // the columns of entries below `end` are inside the table
+            ids = ((int64_t)(col + lane) << lg) < end ? __ldg(table + col + lane) : -1;
           }
-        }
-        if (kv == 0) {
-          if (lane == 0) tb.boxes[issued % kTileFlags] = mask;
-        } else if (!kFp8 && lane < 4) {
-          tb.bad[slot - NS][lane] = 0;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * D * (kFp8 ? 1 : 2)));
-        __syncwarp();
-        if (good) {
-          constexpr int kLine = kFp8 && D == 64 ? 64 : 128, kLines = D * (kFp8 ? 1 : 2) / kLine;
-          const uint32_t dst = ring + (kFp8 ? C::kStaged + slot * C::kIn : slot * C::kSlot);
+          const int32_t id =
+              __shfl_sync(0xffffffffu, ids, col - col0 + (lane < n_boxes ? (lane * box_rows) >> lg : 0));
+          const int32_t be = e0 + lane * box_rows;
+          const bool want = lane < n_boxes && be < end && (be + box_rows > lo || be < sink);
+          const bool good = want && id >= 0 && id < p.c.num_pages;
+          const uint32_t mask = __ballot_sync(0xffffffffu, good);
+          if (__any_sync(0xffffffffu, want && !good) && lane == 0) report(p.err, QSA_DERR_KV_PAGE);
+          // the slot that this fill takes: of the ring, or of the tiles as they come
+          const int n = kFp8 ? 2 * issued + kv : issued;
+          const int slot = kFp8 ? n % C::NI : C::slot(issued, kv), fills = kFp8 ? n / C::NI : issued / NS;
+          const uint32_t full = kFp8 ? bar(tb.in_full[slot]) : bar(tb.full[slot]);
+          const uint32_t empty = kFp8 ? bar(tb.in_empty[slot]) : bar(tb.empty[slot]);
+          if (fills > 0) {
+            bool ok = *s_abort == 0 && mbar_wait(empty, (uint32_t)((fills - 1) & 1));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+              if (lane == 0 && *s_abort == 0) {
+                *s_abort = 1;
+                report(p.err, QSA_DERR_TIMEOUT);
+              }
+              stop = true;
+              break;
+            }
+          }
+          if (kv == 0) {
+            if (lane == 0) tb.boxes[issued % kTileFlags] = mask;
+          } else if (!kFp8 && lane < 4) {
+            tb.bad[slot - NS][lane] = 0;
+          }
+          __syncwarp();
+#ifdef QSA_WAIT_TEST
+          // test build: leave this fill without a copy, so that the waits on it run out
+          // (the failure-detection test)
+          const bool withhold = blockIdx.x == 0 && 2 * issued + kv == p.test_withhold;
+          if (withhold) withheld = issued;
+          if (!withhold)
+#endif
+          {
+            if (lane == 0) mbar_expect_tx(full, (uint32_t)(__popc(mask) * box_rows * D * (kFp8 ? 1 : 2)));
+            __syncwarp();
+            if (good) {
+              constexpr int kLine = kFp8 && D == 64 ? 64 : 128, kLines = D * (kFp8 ? 1 : 2) / kLine;
+              const uint32_t dst = ring + (kFp8 ? C::kStaged + slot * C::kIn : slot * C::kSlot);
 #pragma unroll
-          for (int c = 0; c < kLines; ++c)
-            tma_load_4d(dst + c * (TT * kLine) + lane * box_rows * kLine, kv ? &vmap : &kmap,
-                        c * (kFp8 ? kLine : 64), seg.head, be & ((1 << lg) - 1), id, full, policy);
+              for (int c = 0; c < kLines; ++c)
+                tma_load_4d(dst + c * (TT * kLine) + lane * box_rows * kLine, kv ? &vmap : &kmap,
+                            c * (kFp8 ? kLine : 64), kv_head, be & ((1 << lg) - 1), id, full, policy);
+            }
+          }
+          ++issued;
+        }
+      }
+    } else if (warp == kQueries) {
+      // ---------------- producer of the queries ----------------
+      const Segment& seg = tb.seg[warp][0];
+      while (walk_next<TT>(p, walk, &tb.seg[warp][0])) {
+        if (seg.t1 <= seg.t0) continue;
+        bool ok = *s_abort == 0 && (issued == 0 || mbar_wait(bar(tb.q_free), (uint32_t)((issued - 1) & 1)));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0 && *s_abort == 0) {
+            *s_abort = 1;
+            report(p.err, QSA_DERR_TIMEOUT);
+          }
+          break;
+        }
+        if (lane == 0) {
+          // a line of 64 dims for each head of the set and each token
+          const int accs = seg.toks > p.acc_toks ? 2 : 1;
+          mbar_expect_tx(bar(tb.q_full), (uint32_t)(accs * p.sub * p.acc_toks * D * 2));
+          for (int u = 0; u < accs; ++u)
+            for (int c = 0; c < C::kBlocks; ++c)
+              tma_load_3d(ring + C::kQ + u * C::kQTile + c * (128 * 128), &qmap, c * 64, seg.set * p.sub,
+                          seg.token + seg.tok0 + u * p.acc_toks, bar(tb.q_full));
         }
         ++issued;
       }
-    }
-    } else if (warp >= kIssuer) {
-    // ---------------- issuer ----------------
-    if (warp == kIssuer) {
+    } else if (warp == kIssuer) {
+      // ---------------- issuer ----------------
       constexpr uint32_t kQk = tc5_idesc(kBf16, 128, TT, false), kPv = tc5_idesc(kBf16, 128, D, true);
       int fill = 0, units = 0;                             // tiles, row tiles before this segment
       int ready[2] = {0, 0};
-      const auto stopped = [&]() { return __any_sync(0xffffffffu, *s_abort != 0); };
-      while (!stopped() && walk_next(p, walk, &seg)) {
+      const Segment& seg = tb.seg[warp][0];
+      bool more = walk_next<TT>(p, walk, &tb.seg[warp][0]);
+      while (more) {
         // the same in every lane, and said so
         const int tiles = __shfl_sync(0xffffffffu, seg.t1 - seg.t0, 0);
-        const bool dual = __shfl_sync(0xffffffffu, seg.tile.rows, 0) > 128;
-        if (tiles <= 0) continue;
+        const bool dual = __shfl_sync(0xffffffffu, seg.toks, 0) > p.acc_toks;
+        if (tiles <= 0) {
+          more = walk_next<TT>(p, walk, &tb.seg[warp][0]);
+          continue;
+        }
         const int steps = dual ? 2 * tiles : tiles;
-        wait_for(bar(tb.q_ready), (uint32_t)(units & 1));
+        wait_for(kQToFp16 ? bar(tb.q_ready) : bar(tb.q_full), (uint32_t)(units & 1));
         ++units;
-        if (stopped()) break;
-        tc5_fence_after();
-        const auto qk = [&](int s) {
+        const auto qk = [&](int s, bool there) {
           const int u = s & 1, f = fill + (dual ? s >> 1 : s), i = C::slot(f, 0);
-          if (!dual || u == 0) {
-            wait_for(bar(tb.full[i]), C::phase(f, 0));
-            tc5_fence_after();
-          }
+          if (!there) wait_for(bar(tb.full[i]), C::phase(f, 0));
+          tc5_fence_after();
           // 16 dims a product: 32 bytes on in a line of 64, then the next block of lines
           const uint64_t q = tc5_desc(ring + C::kQ + (dual ? u * C::kQTile : 0), 16);
           const uint64_t k = tc5_desc(ring + i * C::kSlot, 16);
@@ -947,44 +1031,65 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
                          k + (x >> 2) * (TT * 128 / 16) + (x & 3) * 2, kQk, x > 0);
             tc5_commit(bar(tb.s_full[u]));
             if (!dual || u == 1) tc5_commit(bar(tb.empty[i]));
+            if (s + 1 == steps) tc5_commit(bar(tb.q_free));
           }
           used = true;
         };
-        const auto pv = [&](int s) {
+        qk(0, false);
+        if (steps > 1) qk(1, dual);
+        more = walk_next<TT>(p, walk, &tb.seg[warp][0]);   // while the softmax has its first S
+        // (after a time-out without waits, on whatever the buffers hold)
+        for (int s = 0; s < steps; ++s) {
           const int u = s & 1, f = fill + (dual ? s >> 1 : s), slot = C::slot(f, 1);
-          wait_for(bar(tb.p_ready[u]), (uint32_t)(ready[u] & 1));
-          ++ready[u];
-          wait_for(bar(tb.full[slot]), C::phase(f, 1));
-          tc5_fence_after();
+          const int fk = fill + (dual ? (s + 2) >> 1 : s + 2);
+          // what is there already costs no wait behind the softmax's
+          const bool k_there = (dual && u == 1) ||
+                               (s + 2 < steps && mbar_test_wait(bar(tb.full[C::slot(fk, 0)]), C::phase(fk, 0)));
+          const bool v_there = mbar_test_wait(bar(tb.full[slot]), C::phase(f, 1));
           const uint64_t v = tc5_desc(ring + slot * C::kSlot, TT * 128);
           const uint32_t o = tmem + C::kO + (C::kGroups == 2 ? u * D : 0);
           const uint32_t pa = tmem + C::kP + u * (D == 128 ? C::kS : TT / 2);
-          const bool more = C::kGroups == 2 ? s > 1 : s > 0;
-          if (tc5_elect()) {
+          const bool add = C::kGroups == 2 ? s > 1 : s > 0;
+          const auto half = [&](int h) {
 #pragma unroll
-            for (int x = 0; x < TT / 16; ++x)
-              tc5_mma_ts(o, pa + x * 8, v + x * (16 * 128 / 16), kPv, more || x > 0);
+            for (int y = 0; y < TT / 32; ++y) {
+              const int x = h * (TT / 32) + y;
+              tc5_mma_ts(o, pa + x * 8, v + x * (16 * 128 / 16), kPv, add || h != kHalf0 || y > 0);
+            }
+          };
+          wait_for(bar(tb.p_half[u][kHalf0]), (uint32_t)(ready[u] & 1));
+          if (!__all_sync(0xffffffffu, v_there)) wait_for(bar(tb.full[slot]), C::phase(f, 1));
+          tc5_fence_after();
+          if (tc5_elect()) half(kHalf0);
+          wait_for(bar(tb.p_half[u][1 - kHalf0]), (uint32_t)(ready[u] & 1));
+          ++ready[u];
+          tc5_fence_after();
+          if (tc5_elect()) {
+            half(1 - kHalf0);
             if (!dual || u == 1) tc5_commit(bar(tb.empty[slot]));
             if (C::kGroups == 1) tc5_commit(bar(tb.pv_done));
-            if (s + 1 == steps) tc5_commit(bar(tb.unit_done));
+            if (s + C::kGroups >= steps) tc5_commit(bar(tb.o_done[C::kGroups == 2 ? u : 0]));
           }
-        };
-        qk(0);
-        // (after a time-out without waits, on whatever the buffers hold)
-        for (int s = 0; s < steps; ++s) {
-          if (s + 1 < steps) qk(s + 1);
-          pv(s);
+          if (s + 2 < steps) qk(s + 2, __all_sync(0xffffffffu, k_there));
         }
         fill += tiles;
       }
-    }
-    __syncwarp();
-    } else {
-    // ---------------- E4M3 tiles to FP16 ----------------
-    if constexpr (kFp8) {
+    } else if constexpr (kFp8) {
+      // ---------------- E4M3 tiles to FP16 ----------------
       const int ct = tid - C::kSoft;
-      int n = 0;                                           // K's and V's tiles in turn
-      while (*s_abort == 0 && walk_next(p, walk, &seg)) {
+      int n = 0, units = 0;                                // K's and V's tiles in turn
+      const Segment& seg = tb.seg[warp][0];
+      while (!__any_sync(0xffffffffu, *s_abort != 0) && walk_next<TT>(p, walk, &tb.seg[warp][0])) {
+        if (kQToFp16 && seg.t1 > seg.t0) {
+          wait_for(bar(tb.q_full), (uint32_t)(units & 1));
+          for (int u = 0; u < (seg.toks > p.acc_toks ? 2 : 1); ++u)
+            if (ct < p.sub * p.acc_toks)
+              tb.q_mul[units & 1][u * 128 + ct] = row_to_fp16<D>(base + C::kQ + u * C::kQTile, ct);
+          ++units;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(tb.q_ready));
+        }
         for (int end = n + 2 * (seg.t1 - seg.t0); n < end; ++n) {
           const int in = n % C::NI, out = n % NS;
           wait_for(bar(tb.in_full[in]), (uint32_t)((n / C::NI) & 1));
@@ -1019,21 +1124,22 @@ chunk_walk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap kmap,
         }
       }
     }
-    }
   }
   __syncthreads();
   // after a time-out, what this CTA issued lands before it exits
   if (*s_abort != 0) {
-    if (warp < kIssuer && warp >= kIssuer - 2 && lane == 0) {
-      const int kv = warp - (kIssuer - 2);
+    if ((warp == kProducer || warp == kProducer + 1) && lane == 0) {
+      const int kv = warp - kProducer;
       for (int i = max(0, issued - 8); i < issued; ++i) {
         const int n = kFp8 ? 2 * i + kv : i, slots = kFp8 ? C::NI : NS;
         const int last = kFp8 ? 2 * issued - 2 + kv : issued - 1;
-        if (n + slots <= last) continue;                   // refilled since
+        if (n + slots <= last || i == withheld) continue;  // refilled since, or never begun
         mbar_wait(kFp8 ? bar(tb.in_full[n % slots]) : bar(tb.full[C::slot(i, kv)]),
                   (uint32_t)((n / slots) & 1), kDrainLimitNs);
       }
     }
+    if (warp == kQueries && lane == 0 && issued > 0)
+      mbar_wait(bar(tb.q_full), (uint32_t)((issued - 1) & 1), kDrainLimitNs);
     if (warp == kIssuer && __any_sync(0xffffffffu, used)) {
       if (tc5_elect()) tc5_commit(bar(tb.drain));
       mbar_wait(bar(tb.drain), 0, kDrainLimitNs);
@@ -1066,21 +1172,25 @@ struct Acc {
   }
 };
 
-// What the logits of a K/V head are multiplied by, base 2.
-__device__ __forceinline__ float head_mult(const ChunkParams& p, int head) {
-  return p.scale_log2 * (p.c.k_scale ? p.c.k_scale[head] : 1.f);
+// What the logits of a set of heads are multiplied by, base 2.
+__device__ __forceinline__ float set_mult(const ChunkParams& p, int set) {
+  return p.scale_log2 * (p.c.k_scale ? p.c.k_scale[set / p.per_kv] : 1.f);
+}
+// Where row (token j of a row tile, head g of the set) lies among its rows.
+__device__ __forceinline__ int tile_row(const ChunkParams& p, int j, int g) {
+  return j < p.acc_toks ? j * p.sub + g : 128 + (j - p.acc_toks) * p.sub + g;
 }
 
-// Adds what the runs [c0, c1] left of local row i of a row tile that begins at x0;
+// Adds what the runs [c0, c1] left of row i of a row tile that begins at x0;
 // of them this thread's: k0, k0 + dk, ...
 template <int D>
-__device__ __forceinline__ void add_pieces(const ChunkParams& p, const ChunkRuns& r, int head, int64_t x0,
+__device__ __forceinline__ void add_pieces(const ChunkParams& p, const ChunkRuns& r, int set, int64_t x0,
                                            int c0, int c1, int i, int ln, int k0, int dk, float mult,
                                            Acc& acc) {
 #pragma unroll 4
   for (int c = c0 + k0; c <= c1; c += dk) {
     const int second = c == c0 && chunk_run_start(r, c) < x0;
-    const int64_t at = (int64_t)(2 * chunk_cta(r, p.c.heads, head, c) + second) * p.part_rows + i;
+    const int64_t at = (int64_t)(2 * chunk_cta(r, p.sets, set, c) + second) * p.part_rows + i;
     acc.add(*reinterpret_cast<const float2*>(p.part_ml + at * 2),
             *reinterpret_cast<const float4*>(p.part_o + at * D + ln * 4), mult);
   }
@@ -1088,10 +1198,10 @@ __device__ __forceinline__ void add_pieces(const ChunkParams& p, const ChunkRuns
 
 // kBf16: of out; kBf16W: of the weights, whose shift l holds.
 template <bool kBf16, bool kBf16W, int D>
-__device__ __forceinline__ void store_row(const ChunkParams& p, int64_t token, int kv_head, int g, int ln,
+__device__ __forceinline__ void store_row(const ChunkParams& p, int64_t token, int set, int g, int ln,
                                           float mult, const Acc& a) {
-  const float inv = a.l == 0.f ? 0.f : (p.c.v_scale ? p.c.v_scale[kv_head] : 1.f) / a.l;
-  const int head = kv_head * p.group + g;
+  const float inv = a.l == 0.f ? 0.f : (p.c.v_scale ? p.c.v_scale[set / p.per_kv] : 1.f) / a.l;
+  const int head = set * p.sub + g;
   *reinterpret_cast<uint2*>(p.out + token * p.out_row + head * p.out_head + ln * 8) =
       make_uint2(cpack2<kBf16>(a.o.x * inv, a.o.y * inv), cpack2<kBf16>(a.o.z * inv, a.o.w * inv));
   if (ln == 0 && p.lse)
@@ -1109,23 +1219,23 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const Chu
   pdl_wait();
   const int2 cut = p.cuts[blockIdx.x];
   if (cut.x < 0) return;
-  const int heads = p.c.heads;
   const ChunkPlan plan = *p.plan;
-  const ChunkRuns r = chunk_runs(plan.total, heads, ctas);
+  const ChunkRuns r = chunk_runs(plan.total, p.sets, ctas);
   int c0, c1;
   const int64_t x0 = chunk_owners(p, r, plan.total, cut.y, cut.x, &c0, &c1);
-  const int c = r.by_head ? blockIdx.x / heads : blockIdx.x;
+  const int c = r.by_head ? blockIdx.x / p.sets : blockIdx.x;
   if (c != c0 + 1) return;
   const ChunkTile t = p.tiles[cut.x];
   int32_t t0, n;
   request_rows(p, t.req, &t0, &n);
   const bool few = c1 - c0 < kFew;
-  const float mult = head_mult(p, cut.y);
-  for (int i0 = blockIdx.y * (few ? kG : 1); i0 < t.rows; i0 += gridDim.y * (few ? kG : 1)) {
-    const int i = few ? i0 + grp : i0;
+  const float mult = set_mult(p, cut.y);
+  const int rows = t.toks * p.sub;
+  for (int i0 = blockIdx.y * (few ? kG : 1); i0 < rows; i0 += gridDim.y * (few ? kG : 1)) {
+    const int i = few ? i0 + grp : i0, j = i / p.sub, g = i - j * p.sub;
     Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (i < t.rows)
-      add_pieces<D>(p, r, cut.y, x0, c0, c1, i, ln, few ? 0 : grp, few ? 1 : kG, mult, a);
+    if (i < rows)
+      add_pieces<D>(p, r, cut.y, x0, c0, c1, tile_row(p, j, g), ln, few ? 0 : grp, few ? 1 : kG, mult, a);
     if (!few) {
       __syncthreads();
       s_o[tid] = a.o;
@@ -1134,24 +1244,21 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const Chu
       if (grp > 0) continue;
       for (int k = 1; k < kG; ++k) a.add(s_ml[k], s_o[k * L + ln], mult);
     }
-    if (i < t.rows) {
-      const int row = t.row0 + i, j = row / p.group;
-      store_row<kBf16, kBf16W, D>(p, t0 + j, cut.y, row - j * p.group, ln, mult, a);
-    }
+    if (i < rows) store_row<kBf16, kBf16W, D>(p, t0 + t.tok0 + j, cut.y, g, ln, mult, a);
   }
 }
 
-// With a prefix: CTA (token, K/V head), D/4 threads a row; every row's two results.
+// With a prefix: CTA (token, set of heads), D/4 threads a row; every row's two results.
 template <bool kBf16, bool kBf16W, int D>
 __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const ChunkParams p, int ctas) {
-  constexpr int L = D / 4, kG = kChunkJoinThreads / L, RT = chunk_rows(D);
+  constexpr int L = D / 4, kG = kChunkJoinThreads / L;
   const int tid = threadIdx.x, lane = tid & 31, grp = tid / L, ln = tid % L;
-  const int heads = p.c.heads, R = p.c.num_reqs;
+  const int R = p.c.num_reqs, RT = chunk_accs(D) * p.acc_toks;
   pdl_wait();
   const ChunkPlan plan = *p.plan;
-  const ChunkRuns r = chunk_runs(plan.total, heads, ctas);
-  const int head = blockIdx.y;
-  const float mult = head_mult(p, head);
+  const ChunkRuns r = chunk_runs(plan.total, p.sets, ctas);
+  const int set = blockIdx.y;
+  const float mult = set_mult(p, set);
   for (int32_t token = plan.token0 + blockIdx.x; token < plan.token0 + plan.tokens; token += gridDim.x) {
     // the last request that starts at or before the token, 32 at a time
     int b = 0;
@@ -1163,22 +1270,22 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const
     int32_t t0, n;
     request_rows(p, b, &t0, &n);
     const bool own = token >= t0 && token < t0 + n;
-    for (int g = grp; g < p.group; g += kG) {
-      const int64_t rh = (int64_t)token * p.heads + head * p.group + g;
+    for (int g = grp; g < p.sub; g += kG) {
+      const int64_t rh = (int64_t)token * p.heads + set * p.sub + g;
       Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       for (int list = 0; list < 2; ++list) {
-        const int64_t row = (int64_t)(token - (list ? t0 : plan.token0)) * p.group + g;
-        const int64_t k = (list ? p.first[b] : 0) + row / RT;
+        const int32_t j = token - (list ? t0 : plan.token0);
+        const int k = (list ? p.first[b] : 0) + j / RT;
         if (list ? !own || k >= plan.n : k >= plan.n_prefix) continue;
         int c0, c1;
-        const int64_t x0 = chunk_owners(p, r, plan.total, head, (int)k, &c0, &c1);
+        const int64_t x0 = chunk_owners(p, r, plan.total, set, k, &c0, &c1);
         if (c0 == c1)
           a.add(*reinterpret_cast<const float2*>(p.res_ml[list] + rh * 2),
                 *reinterpret_cast<const float4*>(p.res_o[list] + rh * D + ln * 4), mult);
         else
-          add_pieces<D>(p, r, head, x0, c0, c1, (int)(row % RT), ln, 0, 1, mult, a);
+          add_pieces<D>(p, r, set, x0, c0, c1, tile_row(p, j % RT, g), ln, 0, 1, mult, a);
       }
-      store_row<kBf16, kBf16W, D>(p, token, head, g, ln, mult, a);
+      store_row<kBf16, kBf16W, D>(p, token, set, g, ln, mult, a);
     }
   }
 }
@@ -1210,22 +1317,22 @@ cudaError_t chunk_device(int* n_sms) {
 
 template <typename T, int D, bool kFp8>
 cudaError_t launch_chunk_typed(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                               cudaStream_t st) {
+                               const CUtensorMap& qmap, cudaStream_t st) {
   using C = ChunkShape<D, kFp8>;
   constexpr bool kBf16 = __is_same(T, __nv_bfloat16), kBf16W = kBf16 && !kFp8;
   int ctas = 0;
   cudaError_t e = chunk_device<T, D, kFp8>(&ctas);
   if (e != cudaSuccess) return e;
-  e = launch_after(chunk_plan_kernel<C::TT, C::RT>, dim3(1), dim3(kPlanThreads), 0, st, p);
+  e = launch_after(chunk_plan_kernel<C::TT, C::kGroups>, dim3(1), dim3(kPlanThreads), 0, st, p);
   if (e != cudaSuccess) return e;
   e = launch_after(chunk_walk_kernel<T, D, kFp8>, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, st, p,
-                   kmap, vmap);
+                   kmap, vmap, qmap);
   if (e != cudaSuccess) return e;
   if (p.res_o[0])
     return launch_after(chunk_join_all_kernel<kBf16, kBf16W, D>,
-                        dim3((unsigned)std::min(p.tokens, 16384), (unsigned)p.c.heads),
+                        dim3((unsigned)std::min(p.tokens, 16384), (unsigned)p.sets),
                         dim3(kChunkJoinThreads), 0, st, p, ctas);
-  const int64_t rows = std::min<int64_t>((int64_t)p.tokens * p.group, C::RT);
+  const int64_t rows = std::min<int64_t>((int64_t)p.tokens * p.sub, C::kGroups * 128);
   return launch_after(chunk_join_kernel<kBf16, kBf16W, D>,
                       dim3((unsigned)ctas, (unsigned)std::min<int64_t>(rows, 16)),
                       dim3(kChunkJoinThreads), 0, st, p, ctas);
@@ -1233,11 +1340,11 @@ cudaError_t launch_chunk_typed(const ChunkParams& p, const CUtensorMap& kmap, co
 
 template <int D>
 cudaError_t launch_chunk(const ChunkParams& p, bool bf16, bool fp8, const CUtensorMap& kmap,
-                         const CUtensorMap& vmap, cudaStream_t st) {
-  if (fp8) return bf16 ? launch_chunk_typed<__nv_bfloat16, D, true>(p, kmap, vmap, st)
-                       : launch_chunk_typed<__half, D, true>(p, kmap, vmap, st);
-  return bf16 ? launch_chunk_typed<__nv_bfloat16, D, false>(p, kmap, vmap, st)
-              : launch_chunk_typed<__half, D, false>(p, kmap, vmap, st);
+                         const CUtensorMap& vmap, const CUtensorMap& qmap, cudaStream_t st) {
+  if (fp8) return bf16 ? launch_chunk_typed<__nv_bfloat16, D, true>(p, kmap, vmap, qmap, st)
+                       : launch_chunk_typed<__half, D, true>(p, kmap, vmap, qmap, st);
+  return bf16 ? launch_chunk_typed<__nv_bfloat16, D, false>(p, kmap, vmap, qmap, st)
+              : launch_chunk_typed<__half, D, false>(p, kmap, vmap, qmap, st);
 }
 
 }  // namespace
