@@ -564,7 +564,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     const uint32_t lanes = tmem + ((uint32_t)(wl * 32) << 16);
     const int box_log2 = min(p.c.page_log2, TT == 128 ? 7 : 6);
     const int rj = r / p.sub, rh = r - rj * p.sub;         // the row's token and head in its accumulator
-    float* out_stage = reinterpret_cast<float*>(base + C::kOut + warp * (32 * C::kOutCols * 4));
+    unsigned char* out_stage = base + C::kOut + warp * (32 * C::kOutCols * 4);
     int fill = 0, units = 0, steps_done = 0;
     int got[2] = {0, 0}, outs = 0, scans = 0;              // S of each buffer, O taken, V searched so far
     int slot_of = 0;
@@ -821,12 +821,26 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           }
         }
         if (inv != 1.f) f0 *= inv, f1 *= inv;
-        constexpr int kQuads = C::kOutCols / 4;            // of a staged row
-        float4* stage = reinterpret_cast<float4*>(out_stage);
-        const auto place = [&](int row, int q) {           // eight rows' quads on all banks
+        constexpr int kQuads = C::kOutCols / 4;            // 16-byte pieces of a staged row
+        uint4* stage = reinterpret_cast<uint4*>(out_stage);
+        const auto place = [&](int row, int q) {           // eight rows' pieces on all banks
           return row * kQuads + (kQuads == 4 ? q ^ ((row >> 1) & 3) : q ^ ((row >> 2) & 1));
         };
-        const float4* other = stage + 4 * 32 * kQuads;     // the second warpgroup's
+        const uint4* other = stage + 4 * 32 * kQuads;      // the second warpgroup's
+        uint64_t to[kQuads];                               // the rows that this lane stores pieces of
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k)
+          to[k] = __shfl_sync(0xffffffffu, dst, k * (32 / kQuads) + lane / kQuads);
+        const auto store = [&](uint64_t offset) {          // the staged rows, `offset` bytes into them
+          __syncwarp();
+          uint4 v[kQuads];
+#pragma unroll
+          for (int k = 0; k < kQuads; ++k) v[k] = stage[place(k * (32 / kQuads) + lane / kQuads, lane % kQuads)];
+#pragma unroll
+          for (int k = 0; k < kQuads; ++k)
+            if (to[k]) *reinterpret_cast<uint4*>(to[k] + offset + lane % kQuads * 16) = v[k];
+          __syncwarp();
+        };
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t x[32];
@@ -838,55 +852,55 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = 0;
           }
+          const auto f = [&](int i) { return __uint_as_float(x[i]); };
+          if (!first) {
 #pragma unroll
-          for (int h = 0; h < 32; h += C::kOutCols) {
-            if (!first) {
+            for (int h = 0; h < 32; h += C::kOutCols) {
 #pragma unroll
               for (int q = 0; q < kQuads; ++q)
-                stage[place(lane, q)] =
-                    make_float4(__uint_as_float(x[h + 4 * q]), __uint_as_float(x[h + 4 * q + 1]),
-                                __uint_as_float(x[h + 4 * q + 2]), __uint_as_float(x[h + 4 * q + 3]));
+                stage[place(lane, q)] = make_uint4(x[h + 4 * q], x[h + 4 * q + 1], x[h + 4 * q + 2], x[h + 4 * q + 3]);
               pair_sync();                                 // there
               pair_sync();                                 // taken
-              continue;
             }
-            if (both) pair_sync();
+            continue;
+          }
 #pragma unroll
-            for (int q = 0; q < kQuads; ++q) {
-              float4 o = make_float4(__uint_as_float(x[h + 4 * q]) * f0, __uint_as_float(x[h + 4 * q + 1]) * f0,
-                                     __uint_as_float(x[h + 4 * q + 2]) * f0, __uint_as_float(x[h + 4 * q + 3]) * f0);
-              if (both) {
-                const float4 y = other[place(lane, q)];
-                o.x = fmaf(y.x, f1, o.x);
-                o.y = fmaf(y.y, f1, o.y);
-                o.z = fmaf(y.z, f1, o.z);
-                o.w = fmaf(y.w, f1, o.w);
+          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(f(i) * f0);
+          if (both) {
+#pragma unroll
+            for (int h = 0; h < 32; h += C::kOutCols) {
+              pair_sync();
+#pragma unroll
+              for (int q = 0; q < kQuads; ++q) {
+                const uint4 y = other[place(lane, q)];
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  x[h + 4 * q + i] = __float_as_uint(fmaf(__uint_as_float(w[i]), f1, f(h + 4 * q + i)));
               }
-              stage[place(lane, q)] = o;
+              pair_sync();
             }
-            if (both) pair_sync();
-            __syncwarp();
-            if (direct) {
-              constexpr int kLanes = C::kOutCols / 8;      // 16 bytes a lane
+          }
+          if (direct) {
 #pragma unroll
-              for (int k = 0; k < kLanes; ++k) {
-                const int row = k * (32 / kLanes) + lane / kLanes, q = lane % kLanes * 2;
-                const uint64_t d = __shfl_sync(0xffffffffu, dst, row);
-                const float4 a = stage[place(row, q)], b = stage[place(row, q + 1)];
-                if (d)
-                  *reinterpret_cast<uint4*>(d + (uint64_t)(c + h + q * 4) * 2) =
-                      make_uint4(cpack2<kOutBf16>(a.x, a.y), cpack2<kOutBf16>(a.z, a.w),
-                                 cpack2<kOutBf16>(b.x, b.y), cpack2<kOutBf16>(b.z, b.w));
-              }
-            } else {
+            for (int h = 0; h < 32; h += 2 * C::kOutCols) {
 #pragma unroll
-              for (int k = 0; k < kQuads; ++k) {
-                const int row = k * (32 / kQuads) + lane / kQuads, q = lane % kQuads;
-                const uint64_t d = __shfl_sync(0xffffffffu, dst, row);
-                if (d) *reinterpret_cast<float4*>(d + (uint64_t)(c + h + q * 4) * 4) = stage[place(row, q)];
+              for (int q = 0; q < kQuads; ++q) {
+                const int i = h + 8 * q;
+                stage[place(lane, q)] =
+                    make_uint4(cpack2<kOutBf16>(f(i), f(i + 1)), cpack2<kOutBf16>(f(i + 2), f(i + 3)),
+                               cpack2<kOutBf16>(f(i + 4), f(i + 5)), cpack2<kOutBf16>(f(i + 6), f(i + 7)));
               }
+              store((uint64_t)(c + h) * 2);
             }
-            __syncwarp();
+          } else {
+#pragma unroll
+            for (int h = 0; h < 32; h += C::kOutCols) {
+#pragma unroll
+              for (int q = 0; q < kQuads; ++q)
+                stage[place(lane, q)] = make_uint4(x[h + 4 * q], x[h + 4 * q + 1], x[h + 4 * q + 2], x[h + 4 * q + 3]);
+              store((uint64_t)(c + h) * 4);
+            }
           }
         }
         // a run's first row tile, where it is not its beginning: for the join
