@@ -19,14 +19,15 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 // The workspace: the plan of a call's row tiles, the pieces of those that runs
 // cut (at most two a run), and with a prefix the results of both lists.
 struct Layout {
-  int64_t max_tiles, part_rows;
-  size_t tiles, pos, first, cuts, part_ml, part_o, res_ml[2], res_o[2], total;
+  int64_t max_tiles, max_own, part_rows;
+  size_t tiles, pos, first, cuts, owners, part_ml, part_o, res_ml[2], res_o[2], total;
 };
 Layout layout_of(const qsa_paged_cache& c, int64_t tokens, int64_t heads, bool prefix) {
   const int sub = chunk_heads((int)(heads / c.num_heads)), accs = chunk_accs((int)c.head_dim);
   const int64_t acc_toks = 128 / sub, per = accs * acc_toks, tiles = (tokens + per - 1) / per;
   Layout l;
-  l.max_tiles = tiles + std::min(c.num_reqs, tokens) + (prefix ? tiles : 0);
+  l.max_own = tiles + std::min(c.num_reqs, tokens);
+  l.max_tiles = l.max_own + (prefix ? tiles : 0);
   l.part_rows = tokens > acc_toks ? accs * 128 : tokens * sub;
   size_t at = round256(sizeof(ChunkPlan));
   const auto take = [&](size_t bytes) {
@@ -37,7 +38,8 @@ Layout layout_of(const qsa_paged_cache& c, int64_t tokens, int64_t heads, bool p
   l.tiles = take((size_t)l.max_tiles * sizeof(ChunkTile));
   l.pos = take((size_t)(l.max_tiles + 1) * 8);
   l.first = take((size_t)c.num_reqs * 4);
-  l.cuts = take(kChunkMaxCtas * sizeof(int2));
+  l.cuts = take(kChunkMaxCtas * sizeof(ChunkCut));
+  l.owners = take(prefix ? (size_t)l.max_tiles * sizeof(int4) : 0);
   l.part_ml = take((size_t)(2 * kChunkMaxCtas * l.part_rows) * 8);
   l.part_o = take((size_t)(2 * kChunkMaxCtas * l.part_rows * c.head_dim) * 4);
   for (int i = 0; i < 2; ++i) {
@@ -146,7 +148,9 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   p.tiles = reinterpret_cast<ChunkTile*>(w + l.tiles);
   p.pos = reinterpret_cast<int64_t*>(w + l.pos);
   p.first = reinterpret_cast<int32_t*>(w + l.first);
-  p.cuts = reinterpret_cast<int2*>(w + l.cuts);
+  p.cuts = reinterpret_cast<ChunkCut*>(w + l.cuts);
+  p.owners = reinterpret_cast<int4*>(w + l.owners);
+  p.max_own = (int32_t)l.max_own;
   p.part_rows = (int32_t)l.part_rows;
   p.part_ml = reinterpret_cast<float*>(w + l.part_ml);
   p.part_o = reinterpret_cast<float*>(w + l.part_o);

@@ -26,6 +26,8 @@ inline int chunk_heads(int group) {
 }
 // What a row tile costs beside its K/V tiles, in K/V tiles.
 constexpr int kChunkExtra = 1;
+// Pieces of a row tile, from which on runs are longer, and how long at least.
+constexpr int kChunkPieces = 36, kChunkMinRun = 4;
 
 // Query rows of one set of heads that walk K/V tiles together: the tokens [tok0, tok0
 // + toks) of a request, 128 / sub of them in each accumulator.
@@ -37,6 +39,15 @@ struct ChunkPlan {
   int64_t total;                // cost of all row tiles of one set of heads
   int32_t n, n_prefix;          // row tiles, the first ones the prefix's
   int32_t token0, tokens;       // rows of q that belong to requests
+  int32_t longest, pad;         // cost of the longest row tile
+};
+
+// A row tile of a request that runs cut: its pieces lie with the runs [c0, c1], in c0
+// as its second segment or its first.
+struct ChunkCut {
+  int32_t set, c0, c1, second, by_head;
+  int32_t token, toks;          // its rows of q
+  int32_t pad;
 };
 
 struct ChunkParams {
@@ -65,7 +76,9 @@ struct ChunkParams {
   ChunkTile* tiles;             // [max_tiles]
   int64_t* pos;                 // [max_tiles + 1] cost of the row tiles before each
   int32_t* first;               // [num_reqs] each request's first row tile
-  int2* cuts;                   // [kChunkMaxCtas] row tile (-1: none) and set that a run cuts
+  ChunkCut* cuts;               // [kChunkMaxCtas] the one that a run's start cuts first (set -1: none)
+  int4* owners;                 // with a prefix: [max_tiles] the runs [x, y] of each, z as second
+  int32_t max_own;              // row tiles of requests, at most
   int32_t part_rows;            // rows of a row tile, at most; accumulators 128 apart
   float* part_ml;               // [2 * kChunkMaxCtas][part_rows][2]
   float* part_o;                // [2 * kChunkMaxCtas][part_rows][dim]

@@ -49,6 +49,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kChunkJoinThreads = 256;
+constexpr int64_t kJoinFew = 1 << 16;   // threads: rows up to here are joined by four times as many
 constexpr int kTileFlags = 16;      // tiles whose page masks are kept
 
 // A weight is at most 2^(shift + slack).  FP16 weights stay normal down to 2^-22 of
@@ -162,8 +163,13 @@ struct ChunkRuns {
   int n;                        // runs of it
   bool by_head;
 };
-__device__ __forceinline__ ChunkRuns chunk_runs(int64_t total, int heads, int ctas) {
+__device__ __forceinline__ ChunkRuns chunk_runs(const ChunkPlan& plan, int heads, int ctas) {
   ChunkRuns r;
+  const int64_t total = plan.total;
+  // a row tile in more than kChunkPieces pieces: longer runs, while they are short,
+  // cost the walk less than its pieces the join
+  const int least = min(kChunkMinRun, plan.longest / kChunkPieces + 1);
+  ctas = (int)max((int64_t)1, min((int64_t)ctas, total * heads / least));
   const int per = ctas / heads;
   r.by_head = per > 0 && per * heads * 16 >= ctas * 15;
   r.n = r.by_head ? per : ctas;
@@ -211,7 +217,7 @@ __device__ __forceinline__ void walk_begin(const ChunkParams& p, Walk* walk) {
   w.n = plan.n;
   w.token0 = plan.token0;
   w.first = true;
-  const ChunkRuns r = chunk_runs(plan.total, p.sets, gridDim.x);
+  const ChunkRuns r = chunk_runs(plan, p.sets, gridDim.x);
   if (r.by_head) {
     const int run = blockIdx.x / p.sets;
     w.set = blockIdx.x % p.sets;
@@ -219,8 +225,8 @@ __device__ __forceinline__ void walk_begin(const ChunkParams& p, Walk* walk) {
     w.x = run < r.n ? chunk_run_start(r, run) : 0;
     w.x1 = run < r.n ? chunk_run_start(r, run + 1) : 0;
   } else {
-    w.x = chunk_run_start(r, blockIdx.x);
-    w.x1 = chunk_run_start(r, blockIdx.x + 1);
+    w.x = (int)blockIdx.x < r.n ? chunk_run_start(r, blockIdx.x) : 0;
+    w.x1 = (int)blockIdx.x < r.n ? chunk_run_start(r, blockIdx.x + 1) : 0;
     w.set = plan.total > 0 ? (int)(w.x / plan.total) : 0;
     w.base = w.total * w.set;
   }
@@ -314,8 +320,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
 // up.  Row tiles past what the workspace holds (starts that are not in order) are
 // left out.
 template <int TT, int kAccs>
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p, int ctas) {
   __shared__ int64_t s_sums[32];
+  __shared__ int32_t s_longest;
   const int tid = threadIdx.x, R = p.c.num_reqs, RT = kAccs * p.acc_toks;   // tokens of a row tile
   pdl_wait();
   const int32_t token0 = min(max(p.starts[0], 0), p.tokens);
@@ -340,6 +347,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   const int n = (int)min(before, (int64_t)p.max_tiles);
   __syncthreads();
   int64_t cost = 0;
+  int32_t longest = 0;
   for (int k0 = 0; k0 < n; k0 += kPlanThreads) {
     const int k = k0 + tid;
     int64_t c = 0;
@@ -365,16 +373,33 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       }
       p.tiles[k] = t;
       c = tile_cost(t.tiles);
+      longest = max(longest, (int32_t)c);
     }
     const int64_t at = cost + block_scan(c, s_sums, &all);
     if (k < n) p.pos[k] = at;
     cost += all;
   }
+  if (tid == 0) s_longest = 0;
+  __syncthreads();
+  atomicMax(&s_longest, longest);
+  __syncthreads();
+  const ChunkPlan plan{cost, n, n_prefix, token0, tokens, s_longest, 0};
   if (tid == 0) {
     p.pos[n] = cost;
-    *p.plan = ChunkPlan{cost, n, n_prefix, token0, tokens};
+    *p.plan = plan;
   }
-  if (tid < kChunkMaxCtas) p.cuts[tid] = make_int2(-1, 0);
+  // with a prefix every row tile is joined: which runs hold it, where that is the
+  // same for all sets
+  const ChunkRuns r = chunk_runs(plan, p.sets, ctas);
+  if (p.res_o[0] && r.by_head) {
+    __syncthreads();
+    for (int k = tid; k < n; k += kPlanThreads) {
+      int c0, c1;
+      const int64_t x0 = chunk_owners(p, r, cost, 0, k, &c0, &c1);
+      p.owners[k] = make_int4(c0, c1, chunk_run_start(r, c0) < x0, 1);
+    }
+  }
+  if (tid < kChunkMaxCtas) p.cuts[tid].set = -1;
 }
 
 // --- walk -------------------------------------------------------------------------
@@ -904,7 +929,21 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           }
         }
         // a run's first row tile, where it is not its beginning: for the join
-        if (seg.which == 0 && seg.t0 > 0 && r == 0 && g == 0) p.cuts[blockIdx.x] = make_int2(seg.k, seg.set);
+        if (seg.which == 0 && seg.t0 > 0 && r == 0 && g == 0) {
+          const ChunkPlan plan = *p.plan;
+          const int64_t total = plan.total;
+          const ChunkRuns runs = chunk_runs(plan, p.sets, gridDim.x);
+          ChunkCut cut;
+          const int64_t x0 = chunk_owners(p, runs, total, seg.set, seg.k, &cut.c0, &cut.c1);
+          if ((int)(runs.by_head ? blockIdx.x / p.sets : blockIdx.x) == cut.c0 + 1) {
+            cut.set = seg.set;
+            cut.second = chunk_run_start(runs, cut.c0) < x0;
+            cut.by_head = runs.by_head;
+            cut.token = seg.token + seg.tok0;
+            cut.toks = seg.toks;
+            p.cuts[blockIdx.x] = cut;
+          }
+        }
       }
       tc5_fence_before();
       slot_of ^= 1;
@@ -1195,16 +1234,15 @@ __device__ __forceinline__ int tile_row(const ChunkParams& p, int j, int g) {
   return j < p.acc_toks ? j * p.sub + g : 128 + (j - p.acc_toks) * p.sub + g;
 }
 
-// Adds what the runs [c0, c1] left of row i of a row tile that begins at x0;
-// of them this thread's: k0, k0 + dk, ...
+// Adds what the runs [c0, c1] left of row i of a row tile, in c0 as its second
+// segment or its first; of them this thread's: k0, k0 + dk, ...
 template <int D>
-__device__ __forceinline__ void add_pieces(const ChunkParams& p, const ChunkRuns& r, int set, int64_t x0,
-                                           int c0, int c1, int i, int ln, int k0, int dk, float mult,
-                                           Acc& acc) {
+__device__ __forceinline__ void add_pieces(const ChunkParams& p, bool by_head, int set, int c0, int c1,
+                                           int second, int i, int ln, int k0, int dk, float mult, Acc& acc) {
 #pragma unroll 4
   for (int c = c0 + k0; c <= c1; c += dk) {
-    const int second = c == c0 && chunk_run_start(r, c) < x0;
-    const int64_t at = (int64_t)(2 * chunk_cta(r, p.sets, set, c) + second) * p.part_rows + i;
+    const int cta = by_head ? c * p.sets + set : c;
+    const int64_t at = (int64_t)(2 * cta + (c == c0 ? second : 0)) * p.part_rows + i;
     acc.add(*reinterpret_cast<const float2*>(p.part_ml + at * 2),
             *reinterpret_cast<const float4*>(p.part_o + at * D + ln * 4), mult);
   }
@@ -1225,31 +1263,23 @@ __device__ __forceinline__ void store_row(const ChunkParams& p, int64_t token, i
 // CTA (c, y): rows of the row tile that the start of CTA c's run cuts, if that is
 // its first cut.  D/4 threads a row; where it has many pieces, all threads one row.
 template <bool kBf16, bool kBf16W, int D>
-__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const ChunkParams p, int ctas) {
+__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const ChunkParams p) {
   constexpr int L = D / 4, kG = kChunkJoinThreads / L, kFew = 12;
   __shared__ __align__(16) float4 s_o[kChunkJoinThreads];
   __shared__ float2 s_ml[kG];
   const int tid = threadIdx.x, grp = tid / L, ln = tid % L;
   pdl_wait();
-  const int2 cut = p.cuts[blockIdx.x];
-  if (cut.x < 0) return;
-  const ChunkPlan plan = *p.plan;
-  const ChunkRuns r = chunk_runs(plan.total, p.sets, ctas);
-  int c0, c1;
-  const int64_t x0 = chunk_owners(p, r, plan.total, cut.y, cut.x, &c0, &c1);
-  const int c = r.by_head ? blockIdx.x / p.sets : blockIdx.x;
-  if (c != c0 + 1) return;
-  const ChunkTile t = p.tiles[cut.x];
-  int32_t t0, n;
-  request_rows(p, t.req, &t0, &n);
-  const bool few = c1 - c0 < kFew;
-  const float mult = set_mult(p, cut.y);
-  const int rows = t.toks * p.sub;
+  const ChunkCut cut = p.cuts[blockIdx.x];
+  if (cut.set < 0) return;
+  const bool few = cut.c1 - cut.c0 < kFew;
+  const float mult = set_mult(p, cut.set);
+  const int rows = cut.toks * p.sub;
   for (int i0 = blockIdx.y * (few ? kG : 1); i0 < rows; i0 += gridDim.y * (few ? kG : 1)) {
     const int i = few ? i0 + grp : i0, j = i / p.sub, g = i - j * p.sub;
     Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (i < rows)
-      add_pieces<D>(p, r, cut.y, x0, c0, c1, tile_row(p, j, g), ln, few ? 0 : grp, few ? 1 : kG, mult, a);
+      add_pieces<D>(p, cut.by_head, cut.set, cut.c0, cut.c1, cut.second, tile_row(p, j, g), ln,
+                    few ? 0 : grp, few ? 1 : kG, mult, a);
     if (!few) {
       __syncthreads();
       s_o[tid] = a.o;
@@ -1258,49 +1288,65 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const Chu
       if (grp > 0) continue;
       for (int k = 1; k < kG; ++k) a.add(s_ml[k], s_o[k * L + ln], mult);
     }
-    if (i < rows) store_row<kBf16, kBf16W, D>(p, t0 + t.tok0 + j, cut.y, g, ln, mult, a);
+    if (i < rows) store_row<kBf16, kBf16W, D>(p, cut.token + j, cut.set, g, ln, mult, a);
   }
 }
 
-// With a prefix: CTA (token, set of heads), D/4 threads a row; every row's two results.
+// With a prefix: CTA (row tile of a request, set of heads, some of its rows); D/4
+// threads a row, or `ways` times as many, which share its pieces.
 template <bool kBf16, bool kBf16W, int D>
-__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const ChunkParams p, int ctas) {
+__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const ChunkParams p, int ctas, int ways) {
   constexpr int L = D / 4, kG = kChunkJoinThreads / L;
-  const int tid = threadIdx.x, lane = tid & 31, grp = tid / L, ln = tid % L;
-  const int R = p.c.num_reqs, RT = chunk_accs(D) * p.acc_toks;
+  __shared__ __align__(16) float4 s_o[kChunkJoinThreads];
+  __shared__ float2 s_ml[kG];
+  const int tid = threadIdx.x, grp = tid / L, ln = tid % L, set = blockIdx.y;
+  const int RT = chunk_accs(D) * p.acc_toks;
   pdl_wait();
   const ChunkPlan plan = *p.plan;
-  const ChunkRuns r = chunk_runs(plan.total, p.sets, ctas);
-  const int set = blockIdx.y;
+  const int k1 = plan.n_prefix + blockIdx.x;
+  if (k1 >= plan.n) return;
+  const ChunkTile t = p.tiles[k1];
+  int32_t t0, n;
+  request_rows(p, t.req, &t0, &n);
+  const ChunkRuns r = chunk_runs(plan, p.sets, ctas);
   const float mult = set_mult(p, set);
-  for (int32_t token = plan.token0 + blockIdx.x; token < plan.token0 + plan.tokens; token += gridDim.x) {
-    // the last request that starts at or before the token, 32 at a time
-    int b = 0;
-    for (int step = 1 << 15; step >= 1; step >>= 5) {
-      const int64_t x = (int64_t)b + (int64_t)lane * step;
-      const uint32_t le = __ballot_sync(0xffffffffu, x < R && p.starts[min(x, (int64_t)R - 1)] <= token);
-      b += le ? (31 - __clz(le)) * step : 0;
-    }
-    int32_t t0, n;
-    request_rows(p, b, &t0, &n);
-    const bool own = token >= t0 && token < t0 + n;
-    for (int g = grp; g < p.sub; g += kG) {
+  const int all = t.toks * p.sub;
+  const int way = grp % ways, rows = kG / ways;
+  const auto owners = [&](int k) {
+    if (r.by_head) return p.owners[k];
+    int c0, c1;
+    const int64_t x0 = chunk_owners(p, r, plan.total, set, k, &c0, &c1);
+    return make_int4(c0, c1, chunk_run_start(r, c0) < x0, 0);
+  };
+  const int4 own = owners(k1);
+  for (int i0 = blockIdx.z * rows; i0 < all; i0 += gridDim.z * rows) {
+    const int i = i0 + grp / ways, j = i / p.sub, g = i - j * p.sub;
+    const int32_t token = t0 + t.tok0 + j;
+    Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (i < all) {
       const int64_t rh = (int64_t)token * p.heads + set * p.sub + g;
-      Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       for (int list = 0; list < 2; ++list) {
-        const int32_t j = token - (list ? t0 : plan.token0);
-        const int k = (list ? p.first[b] : 0) + j / RT;
-        if (list ? !own || k >= plan.n : k >= plan.n_prefix) continue;
-        int c0, c1;
-        const int64_t x0 = chunk_owners(p, r, plan.total, set, k, &c0, &c1);
-        if (c0 == c1)
+        const int32_t at = list ? t.tok0 + j : token - plan.token0;
+        const int k = list ? k1 : at / RT;
+        if (!list && (at < 0 || k >= plan.n_prefix)) continue;
+        const int4 o = list ? own : owners(k);
+        if (o.x < o.y)
+          add_pieces<D>(p, r.by_head, set, o.x, o.y, o.z, tile_row(p, list ? j : at % RT, g), ln, way,
+                        ways, mult, a);
+        else if (way == 0)
           a.add(*reinterpret_cast<const float2*>(p.res_ml[list] + rh * 2),
                 *reinterpret_cast<const float4*>(p.res_o[list] + rh * D + ln * 4), mult);
-        else
-          add_pieces<D>(p, r, set, x0, c0, c1, tile_row(p, j % RT, g), ln, 0, 1, mult, a);
       }
-      store_row<kBf16, kBf16W, D>(p, token, set, g, ln, mult, a);
     }
+    if (ways > 1) {
+      __syncthreads();
+      s_o[tid] = a.o;
+      if (ln == 0) s_ml[grp] = make_float2(a.m, a.l);
+      __syncthreads();
+      if (way == 0)
+        for (int k = 1; k < ways; ++k) a.add(s_ml[grp + k], s_o[(grp + k) * L + ln], mult);
+    }
+    if (i < all && way == 0) store_row<kBf16, kBf16W, D>(p, token, set, g, ln, mult, a);
   }
 }
 
@@ -1337,19 +1383,27 @@ cudaError_t launch_chunk_typed(const ChunkParams& p, const CUtensorMap& kmap, co
   int ctas = 0;
   cudaError_t e = chunk_device<T, D, kFp8>(&ctas);
   if (e != cudaSuccess) return e;
-  e = launch_after(chunk_plan_kernel<C::TT, C::kGroups>, dim3(1), dim3(kPlanThreads), 0, st, p);
+  e = launch_after(chunk_plan_kernel<C::TT, C::kGroups>, dim3(1), dim3(kPlanThreads), 0, st, p,
+                   ctas);
   if (e != cudaSuccess) return e;
   e = launch_after(chunk_walk_kernel<T, D, kFp8>, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, st, p,
                    kmap, vmap, qmap);
   if (e != cudaSuccess) return e;
-  if (p.res_o[0])
+  if (p.res_o[0]) {
+    // few rows: four times the threads a row, for the prefix's pieces
+    constexpr int kG = kChunkJoinThreads / (D / 4);
+    const int ways = (int64_t)p.tokens * p.heads * (D / 4) <= kJoinFew ? std::min(4, kG) : 1;
+    const int64_t rows = std::min<int64_t>((int64_t)p.tokens * p.sub / std::min(p.c.num_reqs, p.tokens) + 1,
+                                           C::kGroups * 128);
+    const int64_t z = std::min<int64_t>((rows * ways + kG - 1) / kG, 32);
     return launch_after(chunk_join_all_kernel<kBf16, kBf16W, D>,
-                        dim3((unsigned)std::min(p.tokens, 16384), (unsigned)p.sets),
-                        dim3(kChunkJoinThreads), 0, st, p, ctas);
+                        dim3((unsigned)p.max_own, (unsigned)p.sets, (unsigned)z),
+                        dim3(kChunkJoinThreads), 0, st, p, ctas, ways);
+  }
   const int64_t rows = std::min<int64_t>((int64_t)p.tokens * p.sub, C::kGroups * 128);
   return launch_after(chunk_join_kernel<kBf16, kBf16W, D>,
-                      dim3((unsigned)ctas, (unsigned)std::min<int64_t>(rows, 16)),
-                      dim3(kChunkJoinThreads), 0, st, p, ctas);
+                      dim3((unsigned)ctas, (unsigned)std::min<int64_t>(rows, 8)),
+                      dim3(kChunkJoinThreads), 0, st, p);
 }
 
 template <int D>
