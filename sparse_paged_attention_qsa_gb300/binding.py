@@ -946,15 +946,16 @@ def _chunk_call(fn, lib, prefix, q, k_cache, v_cache, block_tables, query_start_
 def qsa_chunk_attention(q, k_cache, v_cache, block_tables, query_start_loc, context_lens, *,
                         scale: float | None = None, window: int = 0, num_sink: int = 0,
                         k_scale=None, v_scale=None, out=None, lse=None, workspace=None,
-                        error_word=None, stream=None):
+                        error_word=None, stream=None, library=None):
     """Attention of ragged chunks of new tokens, q [tokens, heads, dim], over
     their requests' cached entries (include/qsa_chunk.h): request b's are the
     rows [query_start_loc[b], query_start_loc[b+1]) (int32 [requests + 1]), the
     last of its context_lens[b] (int32) entries.  A token sees the entries up to
     its own, with a window the last `window` of them and the first num_sink.
     scale: 1/sqrt(dim) unless given.  lse: fp32 [tokens, heads], filled when
-    given.  Rows of no request are left as they were.  Returns out."""
-    lib = _lib or load_library()
+    given.  Rows of no request are left as they were.  Returns out.  `library`
+    as in qsa_select_paged_tokens."""
+    lib = library or _lib or load_library()
     _on_current_device(q, k_cache, v_cache, block_tables, query_start_loc, context_lens, k_scale,
                        v_scale, out, lse, workspace, error_word)
     return _chunk_call(lib.qsa_chunk_attention, lib, (), q, k_cache, v_cache, block_tables,
@@ -965,12 +966,13 @@ def qsa_chunk_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
 def qsa_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_len, block_tables,
                          query_start_loc, context_lens, *, scale: float | None = None,
                          k_scale=None, v_scale=None, out=None, lse=None, workspace=None,
-                         error_word=None, stream=None):
+                         error_word=None, stream=None, library=None):
     """qsa_chunk_attention where every row sees besides the entries [0,
     prefix_len) (int32 [1]) of prefix_table (int32 [columns]), which the batch
     shares and which are read once for all of it (include/qsa_chunk.h);
-    block_tables and context_lens count what lies behind the prefix."""
-    lib = _lib or load_library()
+    block_tables and context_lens count what lies behind the prefix.  `library` as
+    in qsa_select_paged_tokens."""
+    lib = library or _lib or load_library()
     _on_current_device(q, k_cache, v_cache, prefix_table, prefix_len, block_tables,
                        query_start_loc, context_lens, k_scale, v_scale, out, lse, workspace,
                        error_word)

@@ -8,11 +8,11 @@ statically).  Objects go to ``_build/`` next to this file.
 
 ``build_wait_test()`` builds ``libqsa_waittest.so``, a test-only variant of
 the selection and attention entry points compiled with QSA_WAIT_TEST (the
-dense paged attention for heads of 64): its stage waits give up after 2 ms and
-it exports two extra symbols that make the first CTA of the score kernel (or
-of the fused small-batch kernel), or of the paged attention's walk, leave one
-stage fill without a copy, so the failure-detection tests can make a device
-wait run out.  The product library carries neither.
+dense paged attention and the chunk attention for heads of 64): its stage waits
+give up after 2 ms and it exports three extra symbols that make the first CTA of
+the score kernel (or of the fused small-batch kernel), or of the paged
+attention's or the chunk attention's walk, leave one stage fill without a copy,
+so the failure-detection tests can make a device wait run out.  The product library carries neither.
 """
 from __future__ import annotations
 
@@ -31,7 +31,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqsa.so")
 WAIT_TEST_LIB = os.path.join(PKG, "libqsa_waittest.so")
 WAIT_TEST_SOURCES = ("qsa_abi.cu", "qsa_select.cu", "qsa_attention.cu", "qsa_fused.cu",
-                     "qsa_paged_attention.cu", "qsa_paged_attn_64.cu")
+                     "qsa_paged_attention.cu", "qsa_paged_attn_64.cu", "qsa_chunk.cu",
+                     "qsa_chunk_attn_64.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]

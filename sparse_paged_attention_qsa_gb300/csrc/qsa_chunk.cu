@@ -14,6 +14,10 @@
 namespace qsa {
 namespace {
 
+#ifdef QSA_WAIT_TEST
+int32_t g_test_withhold = -1;
+#endif
+
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The workspace: the plan of a call's row tiles, the pieces of those that runs
@@ -164,9 +168,15 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
       !encode_view(&vmap, p.c.v, p.c, fp8 ? 1 : 2, p.c.v_page, p.c.v_token, p.c.v_head, box) ||
       !encode_queries(&qmap, p))
     return QSA_ERR_CUDA;
+#ifdef QSA_WAIT_TEST
+  p.test_withhold = g_test_withhold;                       // heads of 64 alone are built
+  const cudaError_t e = p.c.dim == 64 ? launch_chunk_64(p, bf16, fp8, kmap, vmap, qmap, s)
+                                      : cudaErrorNotSupported;
+#else
   const cudaError_t e = p.c.dim == 64    ? launch_chunk_64(p, bf16, fp8, kmap, vmap, qmap, s)
                         : p.c.dim == 128 ? launch_chunk_128(p, bf16, fp8, kmap, vmap, qmap, s)
                                          : launch_chunk_256(p, bf16, fp8, kmap, vmap, qmap, s);
+#endif
   return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 
@@ -206,3 +216,12 @@ extern "C" qsa_status qsa_prefix_attention(
                      num_heads, q_strides, query_start_loc, context_lens, scale, 0, 0, out,
                      out_strides, lse, workspace, workspace_bytes, error_word, stream);
 }
+
+#ifdef QSA_WAIT_TEST
+// Test build only, declared in no public header: the next chunk attention launches
+// leave slot fill `issue` (K's and V's tiles counted in turn) of the walk's CTA 0
+// without a copy (-1: none).
+extern "C" __attribute__((visibility("default"))) void qsa_test_withhold_chunk_fill(int32_t issue) {
+  qsa::g_test_withhold = issue;
+}
+#endif

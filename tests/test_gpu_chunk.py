@@ -376,6 +376,47 @@ def test_offsets_past_32_bits():
     assert torch.equal(out, want) and torch.equal(lse2, lse) and int(err) == 0
 
 
+@pytest.mark.parametrize("hq,hk", [(130, 1), (131, 1), (256, 2), (300, 1), (96, 1), (40, 8)])
+def test_groups_of_any_width(hq, hk):
+    for prefix, reqs in ((None, [(3, 40), (1, 200), (5, 0)]), (70, [(2, 9), (1, 0)])):
+        c = Case(reqs, hq, hk, 64, 16, BF16, prefix=prefix, seed=20)
+        out, lse, err = c.run()
+        assert c.check(out, lse)["err"] == int(err) == 0
+
+
+@pytest.mark.parametrize("cache", [F16, E4M3])
+def test_pages_that_no_row_sees_may_be_gone(cache):
+    reqs = [(1, 900), (40, 600), (1, 33)]
+    c = Case(reqs, 4, 2, 64, 16, F16, cache, window=100, sink=20, seed=21)
+    out, lse, err = c.run()
+    want = c.check(out, lse)
+    for b, (n, old) in enumerate(reqs):
+        for col in range(c.tables.shape[1]):
+            seen = any(e < old + n and (e >= old + 1 - 100 or e < 20) for e in range(col * 16, col * 16 + 16))
+            if not seen:
+                c.tables[b, col] = -1
+    out2, lse2, err = c.run()
+    assert torch.equal(out2, out) and torch.equal(lse2, lse) and int(err) == 0
+    c.check(out2, lse2, want)
+
+
+def test_two_streams_at_once():
+    cases = [Case([(300, 200), (1, 900), (2, 7)], 4, 1, 128, 16, F16, seed=22),
+             Case([(1, 3000)] * 20, 8, 2, 64, 32, BF16, prefix=400, seed=23)]
+    want = [c.run()[:2] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(c.run()[:2])
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
+
+
 def test_many_requests():
     g = torch.Generator().manual_seed(17)
     reqs = [(int(a), int(b)) for a, b in zip(torch.randint(0, 3, (3000,), generator=g),
