@@ -44,8 +44,9 @@ Layout layout_of(const qsa_paged_cache& c, int64_t tokens, int64_t heads, bool p
   l.first = take((size_t)c.num_reqs * 4);
   l.cuts = take(kChunkMaxCtas * sizeof(ChunkCut));
   l.owners = take(prefix ? (size_t)l.max_tiles * sizeof(int4) : 0);
-  l.part_ml = take((size_t)(2 * kChunkMaxCtas * l.part_rows) * 8);
-  l.part_o = take((size_t)(2 * kChunkMaxCtas * l.part_rows * c.head_dim) * 4);
+  const int64_t pieces = (prefix ? 4 : 2) * kChunkMaxCtas;
+  l.part_ml = take((size_t)(pieces * l.part_rows) * 8);
+  l.part_o = take((size_t)(pieces * l.part_rows * c.head_dim) * 4);
   for (int i = 0; i < 2; ++i) {
     l.res_ml[i] = prefix ? take((size_t)(tokens * heads) * 8) : 0;
     l.res_o[i] = prefix ? take((size_t)(tokens * heads * c.head_dim) * 4) : 0;
@@ -138,6 +139,7 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   p.sets = (int32_t)(heads / p.sub);
   p.per_kv = group / p.sub;
   p.acc_toks = 128 / p.sub;
+  p.heavy_rows = chunk_accs(p.c.dim) == 2 ? p.acc_toks * p.sub : 32;
   p.scale_log2 = scale_log2;
   p.window = (int32_t)std::min<int64_t>(window, INT32_MAX - 16);
   p.sink = window > 0 ? (int32_t)std::min<int64_t>(sink, kMaxEntries) : 0;

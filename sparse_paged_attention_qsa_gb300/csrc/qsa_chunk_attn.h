@@ -24,10 +24,16 @@ inline int chunk_heads(int group) {
   while (group % n != 0) --n;
   return n;
 }
-// What a row tile costs beside its K/V tiles, in K/V tiles.
-constexpr int kChunkExtra = 1;
+// What a K/V tile costs a row tile, and what the row tile costs beside, where two
+// accumulators share it (heads of 256: where one holds more than 32 rows) and where
+// not.  Measured, a row tile of 1, 2, 4, 8, 16 K/V tiles, in us an SM:
+//   heads of 128, 256 rows  7.4  9.3 13.3 21.6 34.3;  4 rows  4.0  5.5  8.2 14.1 25.6
+//   heads of 64,  256 rows  5.4  6.9  9.7 15.2 26.6;  4 rows  3.5  4.2  5.1  7.4 14.5
+//   heads of 256, 128 rows  5.9  7.3 10.3 16.3 28.1;  4 rows  3.3  4.4  6.7 12.1 23.3
+// and 1.4 a tile of heads of 128 over K/V that the L2 holds.
+constexpr int kTileCost = 4, kHeavyExtra = 14, kLightExtra = 8;
 // Pieces of a row tile, from which on runs are longer, and how long at least.
-constexpr int kChunkPieces = 36, kChunkMinRun = 4;
+constexpr int kChunkPieces = 36, kChunkMinRun = 14;
 
 // Query rows of one set of heads that walk K/V tiles together: the tokens [tok0, tok0
 // + toks) of a request, 128 / sub of them in each accumulator.
@@ -35,11 +41,14 @@ struct ChunkTile {
   int32_t req;                  // its request; -1: the prefix, whose rows are all requests'
   int32_t tok0, toks, tiles;    // its tokens, and the K/V tiles they see
 };
+struct ChunkList {
+  int64_t total;                // cost of its row tiles, for one set of heads
+  int32_t k0, k1;               // they are [k0, k1)
+  int32_t longest, pad;         // the largest cost
+};
 struct ChunkPlan {
-  int64_t total;                // cost of all row tiles of one set of heads
-  int32_t n, n_prefix;          // row tiles, the first ones the prefix's
+  ChunkList list[2];            // the prefix's row tiles, the requests' own
   int32_t token0, tokens;       // rows of q that belong to requests
-  int32_t longest, pad;         // cost of the longest row tile
 };
 
 // A row tile of a request that runs cut: its pieces lie with the runs [c0, c1], in c0
@@ -65,6 +74,7 @@ struct ChunkParams {
   int32_t sub;                  // query heads of a set, whose rows walk together
   int32_t sets, per_kv;         // sets in all, and of one K/V head
   int32_t acc_toks;             // tokens of an accumulator: 128 / sub
+  int32_t heavy_rows;           // more rows than that cost the more
   float scale_log2;             // scale * log2(e)
   int32_t window;               // 0: none; at most INT32_MAX - 16
   int32_t sink;                 // 0 without a window
@@ -80,8 +90,8 @@ struct ChunkParams {
   int4* owners;                 // with a prefix: [max_tiles] the runs [x, y] of each, z as second
   int32_t max_own;              // row tiles of requests, at most
   int32_t part_rows;            // rows of a row tile, at most; accumulators 128 apart
-  float* part_ml;               // [2 * kChunkMaxCtas][part_rows][2]
-  float* part_o;                // [2 * kChunkMaxCtas][part_rows][dim]
+  float* part_ml;               // [2 * kChunkMaxCtas, twice that with a prefix][part_rows][2]
+  float* part_o;                // [the same][part_rows][dim]
   float* res_ml[2];             // with a prefix: whole results [tokens][heads][2], of the
   float* res_o[2];              //   prefix and of the requests' own entries [..][dim]
 #ifdef QSA_WAIT_TEST

@@ -51,6 +51,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kChunkJoinThreads = 256;
 constexpr int64_t kJoinFew = 1 << 16;   // threads: rows up to here are joined by four times as many
 constexpr int kTileFlags = 16;      // tiles whose page masks are kept
+constexpr int kSegments = 4;        // segments known ahead
 
 // A weight is at most 2^(shift + slack).  FP16 weights stay normal down to 2^-22 of
 // the largest; BF16 has binary32's exponents.
@@ -92,11 +93,6 @@ template <bool kBf16>
 __device__ __forceinline__ float row_lse(float m, float l, float mult) {
   return l == 0.f ? -INFINITY : fmaf(m, mult, log2f(l) - chunk_shift(kBf16)) * 0.693147180559945309f;
 }
-template <int kId, int kThreads>
-__device__ __forceinline__ void named_sync() {
-  asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kThreads) : "memory");
-}
-
 // --- geometry ---------------------------------------------------------------------
 
 // The rows of request b, cut to what q holds.
@@ -151,24 +147,34 @@ __device__ __forceinline__ Sight request_sight(const ChunkParams& p, int32_t ctx
   s.tiles = hi > 0 ? s.ns + (hi + TT - 1) / TT - s.w0 : 0;
   return s;
 }
-__device__ __forceinline__ int32_t tile_cost(int32_t tiles) {
-  return tiles > 0 ? tiles + kChunkExtra : 1;
+// The first row of a CTA's piece: its first segment of a list, or a later one.
+__device__ __forceinline__ int64_t piece_at(const ChunkParams& p, int list, int cta, int second) {
+  return (int64_t)((list ? 0 : 2 * kChunkMaxCtas) + 2 * cta + second) * p.part_rows;
+}
+// What a row tile costs beside its K/V tiles (kTileCost each): its queries' way in
+// and its output's way out.  (One that sees nothing costs 1 in all.)
+__device__ __forceinline__ int32_t extra_cost(const ChunkParams& p, int32_t toks) {
+  return toks * p.sub > p.heavy_rows ? kHeavyExtra : kLightExtra;
 }
 
-// Equal runs of all sets' row tiles.  Where the sets divide the CTAs evenly enough
-// every set has the same runs, so that the K/V heads of the same
-// entries, whose elements lie side by side, are read at the same time.
+// Equal runs of all sets' row tiles, of the prefix's and of the requests' own: a CTA
+// walks one of each, so that it does not matter what the one costs beside the other,
+// and half of the CTAs begin with either, products and memory side by side.  Where
+// the sets divide the CTAs evenly enough every set has the same runs, so that the K/V
+// heads of the same entries, whose elements lie side by side, are read at the same
+// time.
 struct ChunkRuns {
   int64_t total, each, more;    // of one set of heads, or of all
   int n;                        // runs of it
   bool by_head;
 };
-__device__ __forceinline__ ChunkRuns chunk_runs(const ChunkPlan& plan, int heads, int ctas) {
+__device__ __forceinline__ ChunkRuns chunk_runs(const ChunkList& list, int heads, int ctas) {
   ChunkRuns r;
-  const int64_t total = plan.total;
+  const int64_t total = list.total;
   // a row tile in more than kChunkPieces pieces: longer runs, while they are short,
   // cost the walk less than its pieces the join
-  const int least = min(kChunkMinRun, plan.longest / kChunkPieces + 1);
+  // (and no run without a tile's end: kTileCost at least)
+  const int least = max(kTileCost, min(kChunkMinRun, list.longest / kChunkPieces + 1));
   ctas = (int)max((int64_t)1, min((int64_t)ctas, total * heads / least));
   const int per = ctas / heads;
   r.by_head = per > 0 && per * heads * 16 >= ctas * 15;
@@ -190,10 +196,12 @@ __device__ __forceinline__ int chunk_cta(const ChunkRuns& r, int heads, int head
   return r.by_head ? c * heads + head : c;
 }
 // the runs [*c0, *c1] that hold K/V tiles of row tile k of a head, and where it begins
-__device__ __forceinline__ int64_t chunk_owners(const ChunkParams& p, const ChunkRuns& r, int64_t total,
-                                                int head, int k, int* c0, int* c1) {
-  const int64_t a = p.pos[k], b = p.pos[k + 1], base = r.by_head ? 0 : total * head;
-  *c0 = chunk_run_of(r, base + a + (b - a > kChunkExtra ? kChunkExtra : 0));
+__device__ __forceinline__ int64_t chunk_owners(const ChunkParams& p, const ChunkRuns& r,
+                                                const ChunkList& list, int head, int k, int* c0, int* c1) {
+  const int64_t at = p.pos[list.k0], a = p.pos[k] - at, b = p.pos[k + 1] - at;
+  const int64_t base = r.by_head ? 0 : list.total * head;
+  // the first tile is the run's that holds its end
+  *c0 = chunk_run_of(r, base + (b - a > 1 ? a + extra_cost(p, p.tiles[k].toks) + kTileCost - 1 : a));
   *c1 = chunk_run_of(r, base + b - 1);
   return base + a;
 }
@@ -203,66 +211,80 @@ struct Segment {
   Sight sight;
   int32_t k, set, t0, t1;
   int32_t req, token, tok0, toks;   // token: the row of q that tok0 counts from
-  int32_t which, whole;
+  int32_t which, whole, list;
 };
 struct Walk {
-  int64_t x, x1, total, base;    // position, end; cost of a set; where the set begins
-  int k, n, set, token0;
+  int64_t x, x1, total, base;    // position, end; cost of a set; what p.pos[k] is past it
+  int32_t k, k0, k1, set, token0, list;
   bool first;
 };
-__device__ __forceinline__ void walk_begin(const ChunkParams& p, Walk* walk) {
+// Where this CTA's run of a list begins.
+__device__ __forceinline__ Walk walk_start(const ChunkParams& p, const ChunkPlan& plan, int list) {
   Walk w;
-  const ChunkPlan plan = *p.plan;
-  w.total = plan.total;
-  w.n = plan.n;
+  const ChunkList l = plan.list[list];
+  w.total = l.total;
+  w.k0 = l.k0;
+  w.k1 = l.k1;
   w.token0 = plan.token0;
+  w.list = list;
   w.first = true;
-  const ChunkRuns r = chunk_runs(plan, p.sets, gridDim.x);
-  if (r.by_head) {
-    const int run = blockIdx.x / p.sets;
-    w.set = blockIdx.x % p.sets;
-    w.base = 0;
-    w.x = run < r.n ? chunk_run_start(r, run) : 0;
-    w.x1 = run < r.n ? chunk_run_start(r, run + 1) : 0;
-  } else {
-    w.x = (int)blockIdx.x < r.n ? chunk_run_start(r, blockIdx.x) : 0;
-    w.x1 = (int)blockIdx.x < r.n ? chunk_run_start(r, blockIdx.x + 1) : 0;
-    w.set = plan.total > 0 ? (int)(w.x / plan.total) : 0;
-    w.base = w.total * w.set;
-  }
-  int lo = 0, hi = w.n - 1;
-  const int64_t at = w.x - w.base;
+  w.x = w.x1 = w.base = 0;
+  w.k = l.k0;
+  w.set = 0;
+  if (l.total == 0) return w;
+  const ChunkRuns r = chunk_runs(l, p.sets, gridDim.x);
+  const int run = r.by_head ? blockIdx.x / p.sets : blockIdx.x;
+  if (run >= r.n) return w;
+  w.x = chunk_run_start(r, run);
+  w.x1 = chunk_run_start(r, run + 1);
+  w.set = r.by_head ? blockIdx.x % p.sets : (int)(w.x / l.total);
+  const int64_t base = r.by_head ? 0 : l.total * w.set, at0 = p.pos[l.k0];
+  const int64_t at = w.x - base + at0;
+  int lo = l.k0, hi = l.k1 - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.pos[mid] <= at) lo = mid; else hi = mid - 1;
   }
   w.k = lo;
-  if ((threadIdx.x & 31) == 0) *walk = w;
-  __syncwarp();
+  w.base = base - at0;
+  return w;
 }
-// The next segment with something to do; false at the run's end.  A warp keeps its
-// place and its segments in shared memory: registers are short.
+// The CTA's two runs, one after the other; the next segment with something to do.
+struct Runs2 {
+  Walk w, later;
+  bool last;
+};
+__device__ __forceinline__ Runs2 walk_begin(const ChunkParams& p) {
+  const ChunkPlan plan = *p.plan;
+  const int order = (blockIdx.x / p.sets) & 1;             // the same for all sets
+  return Runs2{walk_start(p, plan, order), walk_start(p, plan, order ^ 1), false};
+}
 template <int TT>
-__device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk* walk, Segment* segment) {
-  Walk w = *walk;
-  Segment s0, *s = &s0;
-  bool found = false;
-  while (!found && w.x < w.x1) {
-    if (w.k == w.n) {
-      w.k = 0;
+__device__ __forceinline__ bool walk_next(const ChunkParams& p, Runs2& runs, Segment* s) {
+  for (;;) {
+    Walk& w = runs.w;
+    if (w.x >= w.x1) {
+      if (runs.last) return false;
+      w = runs.later;
+      runs.last = true;
+      continue;
+    }
+    if (w.k == w.k1) {
+      w.k = w.k0;
       ++w.set;
       w.base += w.total;
     }
     const int64_t a = w.base + p.pos[w.k], b = w.base + p.pos[w.k + 1];
     const ChunkTile t = p.tiles[w.k];
     const int64_t end = b < w.x1 ? b : w.x1;
-    const int extra = t.tiles > 0 ? kChunkExtra : 0;
+    const int extra = extra_cost(p, t.toks);
     s->k = w.k;
     s->set = w.set;
-    s->t0 = (int)max((int64_t)0, w.x - a - extra);
-    s->t1 = t.tiles > 0 ? (int)max((int64_t)0, end - a - extra) : 0;
+    s->t0 = t.tiles > 0 ? (int)(max((int64_t)0, w.x - a - extra) / kTileCost) : 0;
+    s->t1 = t.tiles > 0 ? (int)(max((int64_t)0, end - a - extra) / kTileCost) : 0;
     s->whole = s->t0 == 0 && s->t1 == t.tiles;
     s->which = w.first ? 0 : 1;
+    s->list = w.list;
     w.first = false;
     w.x = end;
     ++w.k;
@@ -278,15 +300,8 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk* walk, Segm
       request_rows(p, t.req, &s->token, &n);
       s->sight = request_sight<TT>(p, p.ctx[t.req], n, t.tok0, t.tok0 + t.toks - 1);
     }
-    found = true;
+    return true;
   }
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    *walk = w;
-    if (found) *segment = s0;
-  }
-  __syncwarp();
-  return found;
 }
 
 // --- plan -------------------------------------------------------------------------
@@ -322,7 +337,8 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
 template <int TT, int kAccs>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p, int ctas) {
   __shared__ int64_t s_sums[32];
-  __shared__ int32_t s_longest;
+  __shared__ int32_t s_longest[2];
+  __shared__ int64_t s_own;
   const int tid = threadIdx.x, R = p.c.num_reqs, RT = kAccs * p.acc_toks;   // tokens of a row tile
   pdl_wait();
   const int32_t token0 = min(max(p.starts[0], 0), p.tokens);
@@ -347,7 +363,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   const int n = (int)min(before, (int64_t)p.max_tiles);
   __syncthreads();
   int64_t cost = 0;
-  int32_t longest = 0;
+  if (tid < 2) s_longest[tid] = 0;
   for (int k0 = 0; k0 < n; k0 += kPlanThreads) {
     const int k = k0 + tid;
     int64_t c = 0;
@@ -372,31 +388,36 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         t.tiles = request_sight<TT>(p, p.ctx[lo], m, t.tok0, t.tok0 + t.toks - 1).tiles;
       }
       p.tiles[k] = t;
-      c = tile_cost(t.tiles);
-      longest = max(longest, (int32_t)c);
+      c = t.tiles > 0 ? (int64_t)t.tiles * kTileCost + extra_cost(p, t.toks) : 1;
     }
     const int64_t at = cost + block_scan(c, s_sums, &all);
-    if (k < n) p.pos[k] = at;
+    if (k < n) {
+      p.pos[k] = at;
+      atomicMax(&s_longest[k >= n_prefix], (int32_t)min(c, (int64_t)INT32_MAX));
+      if (k == n_prefix) s_own = at;
+    }
     cost += all;
   }
-  if (tid == 0) s_longest = 0;
+  if (tid == 0 && n_prefix >= n) s_own = cost;
   __syncthreads();
-  atomicMax(&s_longest, longest);
-  __syncthreads();
-  const ChunkPlan plan{cost, n, n_prefix, token0, tokens, s_longest, 0};
+  const ChunkPlan plan{{{s_own, 0, min(n_prefix, n), s_longest[0], 0},
+                        {cost - s_own, min(n_prefix, n), n, s_longest[1], 0}},
+                       token0, tokens};
   if (tid == 0) {
     p.pos[n] = cost;
     *p.plan = plan;
   }
   // with a prefix every row tile is joined: which runs hold it, where that is the
   // same for all sets
-  const ChunkRuns r = chunk_runs(plan, p.sets, ctas);
-  if (p.res_o[0] && r.by_head) {
+  if (p.res_o[0]) {
     __syncthreads();
-    for (int k = tid; k < n; k += kPlanThreads) {
-      int c0, c1;
-      const int64_t x0 = chunk_owners(p, r, cost, 0, k, &c0, &c1);
-      p.owners[k] = make_int4(c0, c1, chunk_run_start(r, c0) < x0, 1);
+    for (int x = 0; x < 2; ++x) {
+      const ChunkRuns r = chunk_runs(plan.list[x], p.sets, ctas);
+      for (int k = plan.list[x].k0 + tid; r.by_head && k < plan.list[x].k1; k += kPlanThreads) {
+        int c0, c1;
+        const int64_t x0 = chunk_owners(p, r, plan.list[x], 0, k, &c0, &c1);
+        p.owners[k] = make_int4(c0, c1, chunk_run_start(r, c0) < x0, 1);
+      }
     }
   }
   if (tid < kChunkMaxCtas) p.cuts[tid].set = -1;
@@ -409,12 +430,12 @@ struct ChunkTables {
   uint64_t in_full[8], in_empty[8];        // E4M3: tiles as they came, K's and V's in turn
   uint64_t s_full[2], p_half[2][2], o_done[2], scanned[2];
   uint64_t q_full, q_ready, q_free, pv_done, drain;
+  uint64_t seg_full[kSegments], seg_empty[kSegments], pair[4];
   uint32_t boxes[kTileFlags];              // a bit per copy of a tile, 0: it had no page
   uint32_t bad[8][4];                      // entries of a V slot that hold what is not finite
   float ml[128][2];
   float q_mul[2][256];                     // E4M3: what a row's queries were divided by
-  Walk walk[16];                           // of each warp
-  Segment seg[16][2];                      // this one, the next one
+  Segment seg[kSegments];                  // the next ones; k < 0: no more
   uint32_t tmem;
   int32_t abort;
   int32_t pad[3];
@@ -551,6 +572,11 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     mbar_init(bar(tb.q_free), 1);
     mbar_init(bar(tb.pv_done), 1);
     mbar_init(bar(tb.drain), 1);
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(bar(tb.seg_full[i]), 1);
+      mbar_init(bar(tb.seg_empty[i]), (C::kSoft + C::kConvert) / 32 + 3);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(bar(tb.pair[i]), 2);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -569,16 +595,24 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
   pdl_wait();
   pdl_trigger();
 
-  // After a time-out nothing waits any more: roles run their loops to the end, so
-  // that the barriers between the softmax's warps stay matched.
-  const auto wait_for = [&](uint32_t b, uint32_t phase) {
-    if (!mbar_try_wait(b, phase) && *s_abort == 0 && !mbar_wait(b, phase)) {
+  // No wait is without an end, and after a time-out nothing waits any more: roles
+  // leave at their next segment.
+  const auto wait_for = [&](uint32_t b, uint32_t phase, uint64_t limit = kWaitLimitNs) {
+    if (!mbar_try_wait(b, phase) && *s_abort == 0 && !mbar_wait(b, phase, limit)) {
       *s_abort = 1;
       report(p.err, QSA_DERR_TIMEOUT);
     }
   };
-  Walk* walk = &tb.walk[warp];
-  walk_begin(p, walk);
+  // The n-th segment, as the queries' producer has made it known; null: no more.
+  const auto segment = [&](int n) -> const Segment* {
+    wait_for(bar(tb.seg_full[n % kSegments]), (uint32_t)((n / kSegments) & 1));
+    const Segment* s = &tb.seg[n % kSegments];
+    return __any_sync(0xffffffffu, *s_abort != 0) || s->k < 0 ? nullptr : s;
+  };
+  const auto segment_done = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(tb.seg_empty[n % kSegments]));
+  };
   int issued = 0;                                          // a producer's fills
   bool used = false;                                       // the issuer's products
   int withheld = -1;                                       // test build: a slot fill left out
@@ -592,12 +626,12 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     unsigned char* out_stage = base + C::kOut + warp * (32 * C::kOutCols * 4);
     int fill = 0, units = 0, steps_done = 0;
     int got[2] = {0, 0}, outs = 0, scans = 0;              // S of each buffer, O taken, V searched so far
-    int slot_of = 0;
-    bool more = walk_next<TT>(p, walk, &tb.seg[warp][0]);
-    while (more) {
-      const Segment& seg = tb.seg[warp][slot_of];
+    int pairs = 0;                                         // meetings of two warps that hold the same rows
+    for (int sn = 0;; ++sn) {
+      const Segment* next = segment(sn);
+      if (!next) break;
+      const Segment& seg = *next;
       const Sight& s = seg.sight;
-      bool asked = false;                                  // for the next segment
       const int tiles = seg.t1 - seg.t0;
       const bool dual = seg.toks > p.acc_toks;
       // this thread's row, and what all rows see
@@ -616,9 +650,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       const int steps = dual ? 2 * tiles : tiles;
       // K/V tile t of the segment: from 0 on up to the sinks' end, then the window's
       const int first_tile = seg.t0, first_gap = s.ns - seg.t0, rest_tile = seg.t0 - s.ns + s.w0;
-      int st = C::kGroups == 2 ? g : 0;
-      do {
-        if (st < steps) {
+      for (int st = C::kGroups == 2 ? g : 0; st < steps; st += C::kGroups) {
         const int u = st & 1, t = dual ? st >> 1 : st, f = fill + t;
         const int32_t e0 = (t < first_gap ? t + first_tile : t + rest_tile) * TT;
         wait_for(bar(tb.s_full[u]), (uint32_t)(got[u] & 1));
@@ -783,11 +815,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           ready(kHalf0);
         }
         ready(1 - kHalf0);
-        }
-        if (!asked) more = walk_next<TT>(p, walk, &tb.seg[warp][slot_of ^ 1]);
-        asked = true;
-        st += C::kGroups;
-      } while (st < steps);
+      }
       steps_done += steps;
       fill += tiles;
       if (tiles > 0) ++units;
@@ -805,10 +833,10 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         // stores are whole sectors; of a pair of warps that hold the same rows the
         // second hands its columns to the first
         const auto pair_sync = [&]() {
-          if (wl == 0) named_sync<5, 64>();
-          else if (wl == 1) named_sync<6, 64>();
-          else if (wl == 2) named_sync<7, 64>();
-          else named_sync<8, 64>();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(tb.pair[wl]));
+          wait_for(bar(tb.pair[wl]), (uint32_t)(pairs & 1));
+          ++pairs;
         };
         float f0 = 1.f, f1 = 0.f;
         if (both) {
@@ -826,12 +854,13 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           }
         }
         const bool first = g == 0 || !split;               // writes
+        constexpr int kFew = C::kGroups == 1 ? 16 : 4 * 32 * C::kOutCols / D;
+        const bool few = !dual && seg.toks * p.sub <= kFew;
         const bool direct = seg.whole && !p.res_o[0];
         const int64_t token = seg.token + seg.tok0 + jt;
         const int head = seg.set * p.sub + rh;
         const int64_t at = token * p.heads + head;
-        const int list = seg.req < 0 ? 0 : 1;
-        const int64_t piece = (2 * (int64_t)blockIdx.x + seg.which) * p.part_rows + (dual ? g * 128 : 0) + r;
+        const int64_t piece = piece_at(p, seg.list, blockIdx.x, seg.which) + (dual ? g * 128 : 0) + r;
         uint64_t dst = 0;                                  // the row's first element
         float inv = 1.f;
         if (mine && first) {
@@ -840,8 +869,8 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             inv = l == 0.f ? 0.f : (kFp8 && p.c.v_scale ? p.c.v_scale[kv_head] : 1.f) / l;
             if (p.lse) p.lse[at] = row_lse<kBf16>(m, l, mult);
           } else {
-            dst = reinterpret_cast<uint64_t>(seg.whole ? p.res_o[list] + at * D : p.part_o + piece * D);
-            *reinterpret_cast<float2*>(seg.whole ? p.res_ml[list] + at * 2 : p.part_ml + piece * 2) =
+            dst = reinterpret_cast<uint64_t>(seg.whole ? p.res_o[seg.list] + at * D : p.part_o + piece * D);
+            *reinterpret_cast<float2*>(seg.whole ? p.res_ml[seg.list] + at * 2 : p.part_ml + piece * 2) =
                 make_float2(m * q_mul, l);                 // as the products of q itself
           }
         }
@@ -852,6 +881,12 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           return row * kQuads + (kQuads == 4 ? q ^ ((row >> 1) & 3) : q ^ ((row >> 2) & 1));
         };
         const uint4* other = stage + 4 * 32 * kQuads;      // the second warpgroup's
+        // Few rows (one warp's): the second warpgroup's go over at once, through the
+        // stage of all its warps, which has been read since: its product waited for
+        // the first one's next weights.
+        uint4* whole = reinterpret_cast<uint4*>(base + C::kOut) + 4 * 32 * kQuads;
+        const auto spot = [&](int q) { return lane * (D / 4) + (q ^ (lane & 7)); };
+        if (few && both && g == 0) pair_sync();
         uint64_t to[kQuads];                               // the rows that this lane stores pieces of
 #pragma unroll
         for (int k = 0; k < kQuads; ++k)
@@ -878,6 +913,15 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             for (int i = 0; i < 32; ++i) x[i] = 0;
           }
           const auto f = [&](int i) { return __uint_as_float(x[i]); };
+          if (!first && few) {
+            if (mine) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                whole[spot(c / 4 + q)] = make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            }
+            if (c + 32 == D) pair_sync();
+            continue;
+          }
           if (!first) {
 #pragma unroll
             for (int h = 0; h < 32; h += C::kOutCols) {
@@ -891,7 +935,18 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(f(i) * f0);
-          if (both) {
+          if (both && few) {
+            if (mine) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const uint4 y = whole[spot(c / 4 + q)];
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  x[4 * q + i] = __float_as_uint(fmaf(__uint_as_float(w[i]), f1, f(4 * q + i)));
+              }
+            }
+          } else if (both) {
 #pragma unroll
             for (int h = 0; h < 32; h += C::kOutCols) {
               pair_sync();
@@ -906,7 +961,19 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
               pair_sync();
             }
           }
-          if (direct) {
+          if (few) {
+            if (dst && direct) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(dst + (uint64_t)(c + i) * 2) =
+                    make_uint4(cpack2<kOutBf16>(f(i), f(i + 1)), cpack2<kOutBf16>(f(i + 2), f(i + 3)),
+                               cpack2<kOutBf16>(f(i + 4), f(i + 5)), cpack2<kOutBf16>(f(i + 6), f(i + 7)));
+            } else if (dst) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4*>(dst + (uint64_t)(c + i) * 4) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            }
+          } else if (direct) {
 #pragma unroll
             for (int h = 0; h < 32; h += 2 * C::kOutCols) {
 #pragma unroll
@@ -929,12 +996,11 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           }
         }
         // a run's first row tile, where it is not its beginning: for the join
-        if (seg.which == 0 && seg.t0 > 0 && r == 0 && g == 0) {
+        if (!p.res_o[0] && seg.which == 0 && seg.t0 > 0 && r == 0 && g == 0) {
           const ChunkPlan plan = *p.plan;
-          const int64_t total = plan.total;
-          const ChunkRuns runs = chunk_runs(plan, p.sets, gridDim.x);
+          const ChunkRuns runs = chunk_runs(plan.list[1], p.sets, gridDim.x);
           ChunkCut cut;
-          const int64_t x0 = chunk_owners(p, runs, total, seg.set, seg.k, &cut.c0, &cut.c1);
+          const int64_t x0 = chunk_owners(p, runs, plan.list[1], seg.set, seg.k, &cut.c0, &cut.c1);
           if ((int)(runs.by_head ? blockIdx.x / p.sets : blockIdx.x) == cut.c0 + 1) {
             cut.set = seg.set;
             cut.second = chunk_run_start(runs, cut.c0) < x0;
@@ -946,7 +1012,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         }
       }
       tc5_fence_before();
-      slot_of ^= 1;
+      segment_done(sn);
     }
   } else {
     C::fewer_registers();
@@ -957,8 +1023,10 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       const int box_rows = min(TT, 1 << lg), n_boxes = TT / box_rows;
       const uint64_t policy = evict_normal_policy();
       bool stop = false;
-      const Segment& seg = tb.seg[warp][0];
-      while (!stop && walk_next<TT>(p, walk, &tb.seg[warp][0])) {
+      for (int sn = 0; !stop; ++sn) {
+        const Segment* next = segment(sn);
+        if (!next) break;
+        const Segment& seg = *next;
         const Sight& s = seg.sight;
         const int32_t* table = s.prefix ? p.prefix_table : p.c.bt + (int64_t)seg.req * p.c.bt_s0;
         const int kv_head = seg.set / p.per_kv;
@@ -1026,21 +1094,33 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           }
           ++issued;
         }
+        segment_done(sn);
       }
     } else if (warp == kQueries) {
-      // ---------------- producer of the queries ----------------
-      const Segment& seg = tb.seg[warp][0];
-      while (walk_next<TT>(p, walk, &tb.seg[warp][0])) {
-        if (seg.t1 <= seg.t0) continue;
-        bool ok = *s_abort == 0 && (issued == 0 || mbar_wait(bar(tb.q_free), (uint32_t)((issued - 1) & 1)));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (lane == 0 && *s_abort == 0) {
-            *s_abort = 1;
-            report(p.err, QSA_DERR_TIMEOUT);
-          }
-          break;
+      // ---------------- producer of the segments and the queries ----------------
+      // waits here are for row tiles of any length: 20 us a K/V tile more
+      Runs2 runs = walk_begin(p);
+      int64_t recent = 0;                                  // K/V tiles of the last segments
+      for (int sn = 0;; ++sn) {
+        Segment seg;
+        seg.t0 = seg.t1 = 0;
+        const bool more = walk_next<TT>(p, runs, &seg);
+        if (!more) seg.k = -1;
+        if (sn >= kSegments)
+          wait_for(bar(tb.seg_empty[sn % kSegments]), (uint32_t)((sn / kSegments - 1) & 1),
+                   kWaitLimitNs + (uint64_t)recent * 20000);
+        if (__any_sync(0xffffffffu, *s_abort != 0)) break;
+        if (lane == 0) {
+          tb.seg[sn % kSegments] = seg;
+          mbar_arrive(bar(tb.seg_full[sn % kSegments]));
         }
+        __syncwarp();
+        if (!more) break;
+        if (seg.t1 <= seg.t0) continue;
+        if (issued > 0)
+          wait_for(bar(tb.q_free), (uint32_t)((issued - 1) & 1), kWaitLimitNs + (uint64_t)recent * 20000);
+        recent = (recent * 7 >> 3) + (seg.t1 - seg.t0);
+        if (__any_sync(0xffffffffu, *s_abort != 0)) break;
         if (lane == 0) {
           // a line of 64 dims for each head of the set and each token
           const int accs = seg.toks > p.acc_toks ? 2 : 1;
@@ -1050,6 +1130,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
               tma_load_3d(ring + C::kQ + u * C::kQTile + c * (128 * 128), &qmap, c * 64, seg.set * p.sub,
                           seg.token + seg.tok0 + u * p.acc_toks, bar(tb.q_full));
         }
+        __syncwarp();
         ++issued;
       }
     } else if (warp == kIssuer) {
@@ -1057,16 +1138,14 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       constexpr uint32_t kQk = tc5_idesc(kBf16, 128, TT, false), kPv = tc5_idesc(kBf16, 128, D, true);
       int fill = 0, units = 0;                             // tiles, row tiles before this segment
       int ready[2] = {0, 0};
-      const Segment& seg = tb.seg[warp][0];
-      bool more = walk_next<TT>(p, walk, &tb.seg[warp][0]);
-      while (more) {
+      for (int sn = 0;; ++sn) {
+        const Segment* next = segment(sn);
+        if (!next) break;
         // the same in every lane, and said so
-        const int tiles = __shfl_sync(0xffffffffu, seg.t1 - seg.t0, 0);
-        const bool dual = __shfl_sync(0xffffffffu, seg.toks, 0) > p.acc_toks;
-        if (tiles <= 0) {
-          more = walk_next<TT>(p, walk, &tb.seg[warp][0]);
-          continue;
-        }
+        const int tiles = __shfl_sync(0xffffffffu, next->t1 - next->t0, 0);
+        const bool dual = __shfl_sync(0xffffffffu, next->toks, 0) > p.acc_toks;
+        segment_done(sn);
+        if (tiles <= 0) continue;
         const int steps = dual ? 2 * tiles : tiles;
         wait_for(kQToFp16 ? bar(tb.q_ready) : bar(tb.q_full), (uint32_t)(units & 1));
         ++units;
@@ -1090,7 +1169,6 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         };
         qk(0, false);
         if (steps > 1) qk(1, dual);
-        more = walk_next<TT>(p, walk, &tb.seg[warp][0]);   // while the softmax has its first S
         // (after a time-out without waits, on whatever the buffers hold)
         for (int s = 0; s < steps; ++s) {
           const int u = s & 1, f = fill + (dual ? s >> 1 : s), slot = C::slot(f, 1);
@@ -1131,8 +1209,10 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       // ---------------- E4M3 tiles to FP16 ----------------
       const int ct = tid - C::kSoft;
       int n = 0, units = 0;                                // K's and V's tiles in turn
-      const Segment& seg = tb.seg[warp][0];
-      while (!__any_sync(0xffffffffu, *s_abort != 0) && walk_next<TT>(p, walk, &tb.seg[warp][0])) {
+      for (int sn = 0;; ++sn) {
+        const Segment* next = segment(sn);
+        if (!next) break;
+        const Segment& seg = *next;
         if (kQToFp16 && seg.t1 > seg.t0) {
           wait_for(bar(tb.q_full), (uint32_t)(units & 1));
           for (int u = 0; u < (seg.toks > p.acc_toks ? 2 : 1); ++u)
@@ -1175,6 +1255,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             mbar_arrive(bar(tb.in_empty[in]));
           }
         }
+        segment_done(sn);
       }
     }
   }
@@ -1237,12 +1318,12 @@ __device__ __forceinline__ int tile_row(const ChunkParams& p, int j, int g) {
 // Adds what the runs [c0, c1] left of row i of a row tile, in c0 as its second
 // segment or its first; of them this thread's: k0, k0 + dk, ...
 template <int D>
-__device__ __forceinline__ void add_pieces(const ChunkParams& p, bool by_head, int set, int c0, int c1,
+__device__ __forceinline__ void add_pieces(const ChunkParams& p, int list, bool by_head, int set, int c0, int c1,
                                            int second, int i, int ln, int k0, int dk, float mult, Acc& acc) {
 #pragma unroll 4
   for (int c = c0 + k0; c <= c1; c += dk) {
     const int cta = by_head ? c * p.sets + set : c;
-    const int64_t at = (int64_t)(2 * cta + (c == c0 ? second : 0)) * p.part_rows + i;
+    const int64_t at = piece_at(p, list, cta, c == c0 ? second : 0) + i;
     acc.add(*reinterpret_cast<const float2*>(p.part_ml + at * 2),
             *reinterpret_cast<const float4*>(p.part_o + at * D + ln * 4), mult);
   }
@@ -1278,7 +1359,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const Chu
     const int i = few ? i0 + grp : i0, j = i / p.sub, g = i - j * p.sub;
     Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (i < rows)
-      add_pieces<D>(p, cut.by_head, cut.set, cut.c0, cut.c1, cut.second, tile_row(p, j, g), ln,
+      add_pieces<D>(p, 1, cut.by_head, cut.set, cut.c0, cut.c1, cut.second, tile_row(p, j, g), ln,
                     few ? 0 : grp, few ? 1 : kG, mult, a);
     if (!few) {
       __syncthreads();
@@ -1303,22 +1384,23 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const
   const int RT = chunk_accs(D) * p.acc_toks;
   pdl_wait();
   const ChunkPlan plan = *p.plan;
-  const int k1 = plan.n_prefix + blockIdx.x;
-  if (k1 >= plan.n) return;
+  const int k1 = plan.list[1].k0 + blockIdx.x;
+  if (k1 >= plan.list[1].k1) return;
   const ChunkTile t = p.tiles[k1];
   int32_t t0, n;
   request_rows(p, t.req, &t0, &n);
-  const ChunkRuns r = chunk_runs(plan, p.sets, ctas);
+  const ChunkRuns runs[2] = {chunk_runs(plan.list[0], p.sets, ctas), chunk_runs(plan.list[1], p.sets, ctas)};
   const float mult = set_mult(p, set);
   const int all = t.toks * p.sub;
   const int way = grp % ways, rows = kG / ways;
-  const auto owners = [&](int k) {
+  const auto owners = [&](int list, int k) {
+    const ChunkRuns& r = runs[list];
     if (r.by_head) return p.owners[k];
     int c0, c1;
-    const int64_t x0 = chunk_owners(p, r, plan.total, set, k, &c0, &c1);
+    const int64_t x0 = chunk_owners(p, r, plan.list[list], set, k, &c0, &c1);
     return make_int4(c0, c1, chunk_run_start(r, c0) < x0, 0);
   };
-  const int4 own = owners(k1);
+  const int4 own = owners(1, k1);
   for (int i0 = blockIdx.z * rows; i0 < all; i0 += gridDim.z * rows) {
     const int i = i0 + grp / ways, j = i / p.sub, g = i - j * p.sub;
     const int32_t token = t0 + t.tok0 + j;
@@ -1328,10 +1410,10 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const
       for (int list = 0; list < 2; ++list) {
         const int32_t at = list ? t.tok0 + j : token - plan.token0;
         const int k = list ? k1 : at / RT;
-        if (!list && (at < 0 || k >= plan.n_prefix)) continue;
-        const int4 o = list ? own : owners(k);
+        if (!list && (at < 0 || k >= plan.list[0].k1)) continue;
+        const int4 o = list ? own : owners(0, k);
         if (o.x < o.y)
-          add_pieces<D>(p, r.by_head, set, o.x, o.y, o.z, tile_row(p, list ? j : at % RT, g), ln, way,
+          add_pieces<D>(p, list, runs[list].by_head, set, o.x, o.y, o.z, tile_row(p, list ? j : at % RT, g), ln, way,
                         ways, mult, a);
         else if (way == 0)
           a.add(*reinterpret_cast<const float2*>(p.res_ml[list] + rh * 2),

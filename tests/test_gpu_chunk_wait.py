@@ -20,7 +20,7 @@ DEV = "cuda"
 
 
 @pytest.mark.parametrize("reqs,prefix,fill", [
-    ([(1, 30000), (2, 0), (1, 5000)], None, 0), ([(1, 30000), (2, 0), (1, 5000)], None, 3),
+    ([(1, 200000), (2, 0), (1, 5000)], None, 0), ([(1, 200000), (2, 0), (1, 5000)], None, 3),
     ([(4000, 900), (2000, 0)], None, 2), ([(4000, 900), (2000, 0)], None, 9), ([(1, 20)] * 400, 8000, 1),
     ([(90, 60)] * 150, None, 5)],
     ids=["first K", "long V", "prompt K", "prompt V", "prefix", "edges"])
