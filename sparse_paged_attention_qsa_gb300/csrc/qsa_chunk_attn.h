@@ -32,6 +32,8 @@ inline int chunk_heads(int group) {
 //   heads of 256, 128 rows  5.9  7.3 10.3 16.3 28.1;  4 rows  3.3  4.4  6.7 12.1 23.3
 // and 1.4 a tile of heads of 128 over K/V that the L2 holds.
 constexpr int kTileCost = 4, kHeavyExtra = 14, kLightExtra = 8;
+// K/V tiles from which on two warpgroups share a row tile of one accumulator.
+constexpr int kChunkSplit = 12;
 // Pieces of a row tile, from which on runs are longer, and how long at least.
 constexpr int kChunkPieces = 36, kChunkMinRun = 14;
 

@@ -14,10 +14,11 @@
 //   memory: 128 rows a product, two products' S and O beside each other, so that
 //   one is in the softmax while the other is in the tensor pipe.  Two warpgroups
 //   form the softmax, a thread a row: no reduction crosses threads.  The two hold
-//   two halves of 256 rows over the same K/V tiles, or, for 128 rows and fewer,
-//   every other K/V tile of the same rows, merged at the row tile's end.  (Heads of
-//   256 hold one O of 256 columns: one warpgroup, two S.)  Four more warps widen
-//   E4M3 tiles to FP16 on their way to the ring.
+//   two halves of 256 rows over the same K/V tiles.  Of 128 rows and fewer they take
+//   every other K/V tile each and merge at the end, or, where those are few, one row
+//   tile each in turn, so that one's output leaves while the other is at work.
+//   (Heads of 256 hold one O of 256 columns: one warpgroup, two S.)  Four more warps
+//   widen E4M3 tiles to FP16 on their way to the ring.
 // chunk_join_kernel, chunk_join_all_kernel  join the pieces of row tiles that runs
 //   cut; with a prefix, the prefix's and the requests' own.
 //
@@ -119,6 +120,11 @@ struct Sight {
 };
 __device__ __forceinline__ int32_t prefix_entries(const ChunkParams& p) {
   return p.prefix_table ? min(max(*p.prefix_len, 0), p.prefix_cap) : 0;
+}
+// Both warpgroups share a row tile of one accumulator.
+template <int kGroups>
+__device__ __forceinline__ bool splits(bool dual, int tiles) {
+  return kGroups == 2 && !dual && tiles >= kChunkSplit;
 }
 template <int TT>
 __device__ __forceinline__ Sight prefix_sight(const ChunkParams& p) {
@@ -428,7 +434,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
 struct ChunkTables {
   uint64_t full[16], empty[16];            // ring: K's slots, then V's; E4M3: both in turn
   uint64_t in_full[8], in_empty[8];        // E4M3: tiles as they came, K's and V's in turn
-  uint64_t s_full[2], p_half[2][2], o_done[2], scanned[2];
+  uint64_t s_full[2][2];                   // of a warpgroup's S in each buffer
+  uint64_t p_half[2][2], o_done[2], scanned[2];
   uint64_t q_full, q_ready, q_free, pv_done, drain;
   uint64_t seg_full[kSegments], seg_empty[kSegments], pair[4];
   uint32_t boxes[kTileFlags];              // a bit per copy of a tile, 0: it had no page
@@ -561,7 +568,8 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       mbar_init(bar(tb.in_empty[i]), 4);
     }
     for (int u = 0; u < 2; ++u) {
-      mbar_init(bar(tb.s_full[u]), 1);
+      mbar_init(bar(tb.s_full[u][0]), 1);
+      mbar_init(bar(tb.s_full[u][1]), 1);
       mbar_init(bar(tb.p_half[u][0]), 4);
       mbar_init(bar(tb.p_half[u][1]), 4);
       mbar_init(bar(tb.o_done[u]), 1);
@@ -626,6 +634,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     unsigned char* out_stage = base + C::kOut + warp * (32 * C::kOutCols * 4);
     int fill = 0, units = 0, steps_done = 0;
     int got[2] = {0, 0}, outs = 0, scans = 0;              // S of each buffer, O taken, V searched so far
+    int turn = 0;                                          // whose the next row tile of one O is
     int pairs = 0;                                         // meetings of two warps that hold the same rows
     for (int sn = 0;; ++sn) {
       const Segment* next = segment(sn);
@@ -633,10 +642,11 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       const Segment& seg = *next;
       const Sight& s = seg.sight;
       const int tiles = seg.t1 - seg.t0;
-      const bool dual = seg.toks > p.acc_toks;
+      const bool dual = seg.toks > p.acc_toks, split = splits<C::kGroups>(dual, tiles), two = dual || split;
+      const bool own = C::kGroups == 1 || two || g == turn;
       // this thread's row, and what all rows see
       const int jt = (dual ? g * p.acc_toks : 0) + rj;     // of the row tile's tokens
-      const bool mine = rj < p.acc_toks && jt < seg.toks;
+      const bool mine = own && rj < p.acc_toks && jt < seg.toks;
       const int j = seg.tok0 + min(jt, seg.toks - 1), jl = seg.tok0 + seg.toks - 1;
       const int32_t hi = s.hi(j), lo = s.lo(j), sink = s.window > 0 ? min(s.sink, hi) : 0;
       const int32_t in_hi = s.hi(seg.tok0), in_lo = s.lo(jl);
@@ -650,14 +660,15 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       const int steps = dual ? 2 * tiles : tiles;
       // K/V tile t of the segment: from 0 on up to the sinks' end, then the window's
       const int first_tile = seg.t0, first_gap = s.ns - seg.t0, rest_tile = seg.t0 - s.ns + s.w0;
-      for (int st = C::kGroups == 2 ? g : 0; st < steps; st += C::kGroups) {
+      const int stride = two ? 2 : 1;
+      for (int st = two ? g : own ? 0 : steps; st < steps; st += stride) {
         const int u = st & 1, t = dual ? st >> 1 : st, f = fill + t;
         const int32_t e0 = (t < first_gap ? t + first_tile : t + rest_tile) * TT;
-        wait_for(bar(tb.s_full[u]), (uint32_t)(got[u] & 1));
+        wait_for(bar(tb.s_full[g][u]), (uint32_t)(got[u] & 1));
         ++got[u];
         tc5_fence_after();
         if constexpr (kQToFp16) {
-          if (st < C::kGroups) {                           // the row's first
+          if (st < stride) {                               // the row's first
             q_mul = tb.q_mul[units & 1][(dual ? g * 128 : 0) + r];
             mult *= q_mul;
           }
@@ -722,12 +733,12 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         if (__any_sync(0xffffffffu, move)) {
           const float a = !move ? 1.f : old == -INFINITY ? 0.f : cex2((old - m) * mult);
           l *= a;
-          if (C::kGroups == 2 ? st > 1 : st > 0) {
-            // the product before this one into the same O: done with two buffers of
-            // S and O (S of this step came behind it), else to be waited for
-            if (C::kGroups == 1) wait_for(bar(tb.pv_done), (uint32_t)((steps_done + st - 1) & 1));
+          if (st >= stride) {
+            // the product before this one into the same O: done with two O (S of this
+            // step came behind it), else to be waited for
+            if (!two) wait_for(bar(tb.pv_done), (uint32_t)((steps_done + st - 1) & 1));
             tc5_fence_after();
-            const uint32_t o = lanes + C::kO + (C::kGroups == 2 ? u * D : 0);
+            const uint32_t o = lanes + C::kO + g * D;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t x[32];
@@ -816,19 +827,17 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         }
         ready(1 - kHalf0);
       }
-      steps_done += steps;
+      if (!two) steps_done += steps;
       fill += tiles;
       if (tiles > 0) ++units;
+      if (!two) turn ^= 1;
       // ---- the row tile's end
-      const bool split = C::kGroups == 2 && !dual;         // both warpgroups hold the same rows
-      const bool both = split && steps > 1;
-      if (steps > 0 && (!split || g < steps)) {
+      if (own && steps > 0) {
         wait_for(bar(tb.o_done[g]), (uint32_t)(outs & 1));
         ++outs;
         tc5_fence_after();
       }
-      const bool some = __any_sync(0xffffffffu, mine);     // the same in both warps of a pair
-      if (some && (!split || g == 0 || both)) {
+      if (__any_sync(0xffffffffu, mine)) {                 // the same in both warps of a pair
         // rows go out by way of shared memory, kOutCols columns at a time, so that
         // stores are whole sectors; of a pair of warps that hold the same rows the
         // second hands its columns to the first
@@ -839,7 +848,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           ++pairs;
         };
         float f0 = 1.f, f1 = 0.f;
-        if (both) {
+        if (split) {
           if (g == 1) {
             tb.ml[r][0] = m;
             tb.ml[r][1] = l;
@@ -886,7 +895,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         // the first one's next weights.
         uint4* whole = reinterpret_cast<uint4*>(base + C::kOut) + 4 * 32 * kQuads;
         const auto spot = [&](int q) { return lane * (D / 4) + (q ^ (lane & 7)); };
-        if (few && both && g == 0) pair_sync();
+        if (few && split && g == 0) pair_sync();
         uint64_t to[kQuads];                               // the rows that this lane stores pieces of
 #pragma unroll
         for (int k = 0; k < kQuads; ++k)
@@ -905,7 +914,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         for (int c = 0; c < D; c += 32) {
           uint32_t x[32];
           if (tiles > 0) {
-            tc5_ld32(lanes + C::kO + (C::kGroups == 2 ? g * D : 0) + c, x);
+            tc5_ld32(lanes + C::kO + g * D + c, x);
             tc5_wait_ld();
             tc5_hold(x);
           } else {
@@ -935,7 +944,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(f(i) * f0);
-          if (both && few) {
+          if (split && few) {
             if (mine) {
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
@@ -946,7 +955,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
                   x[4 * q + i] = __float_as_uint(fmaf(__uint_as_float(w[i]), f1, f(4 * q + i)));
               }
             }
-          } else if (both) {
+          } else if (split) {
 #pragma unroll
             for (int h = 0; h < 32; h += C::kOutCols) {
               pair_sync();
@@ -996,7 +1005,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           }
         }
         // a run's first row tile, where it is not its beginning: for the join
-        if (!p.res_o[0] && seg.which == 0 && seg.t0 > 0 && r == 0 && g == 0) {
+        if (!p.res_o[0] && seg.which == 0 && seg.t0 > 0 && r == 0 && (g == 0 || !two)) {
           const ChunkPlan plan = *p.plan;
           const ChunkRuns runs = chunk_runs(plan.list[1], p.sets, gridDim.x);
           ChunkCut cut;
@@ -1137,15 +1146,19 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       // ---------------- issuer ----------------
       constexpr uint32_t kQk = tc5_idesc(kBf16, 128, TT, false), kPv = tc5_idesc(kBf16, 128, D, true);
       int fill = 0, units = 0;                             // tiles, row tiles before this segment
-      int ready[2] = {0, 0};
+      int ready[2] = {0, 0}, turn = 0;
       for (int sn = 0;; ++sn) {
         const Segment* next = segment(sn);
         if (!next) break;
         // the same in every lane, and said so
         const int tiles = __shfl_sync(0xffffffffu, next->t1 - next->t0, 0);
         const bool dual = __shfl_sync(0xffffffffu, next->toks, 0) > p.acc_toks;
+        const bool two = dual || splits<C::kGroups>(dual, tiles);
         segment_done(sn);
-        if (tiles <= 0) continue;
+        if (tiles <= 0) {
+          if (!two) turn ^= 1;
+          continue;
+        }
         const int steps = dual ? 2 * tiles : tiles;
         wait_for(kQToFp16 ? bar(tb.q_ready) : bar(tb.q_full), (uint32_t)(units & 1));
         ++units;
@@ -1161,7 +1174,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             for (int x = 0; x < D / 16; ++x)
               tc5_mma_ss(tmem + u * C::kS, q + (x >> 2) * (128 * 128 / 16) + (x & 3) * 2,
                          k + (x >> 2) * (TT * 128 / 16) + (x & 3) * 2, kQk, x > 0);
-            tc5_commit(bar(tb.s_full[u]));
+            tc5_commit(bar(tb.s_full[C::kGroups == 1 ? 0 : two ? u : turn][u]));
             if (!dual || u == 1) tc5_commit(bar(tb.empty[i]));
             if (s + 1 == steps) tc5_commit(bar(tb.q_free));
           }
@@ -1178,9 +1191,9 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
                                (s + 2 < steps && mbar_test_wait(bar(tb.full[C::slot(fk, 0)]), C::phase(fk, 0)));
           const bool v_there = mbar_test_wait(bar(tb.full[slot]), C::phase(f, 1));
           const uint64_t v = tc5_desc(ring + slot * C::kSlot, TT * 128);
-          const uint32_t o = tmem + C::kO + (C::kGroups == 2 ? u * D : 0);
+          const uint32_t o = tmem + C::kO + (C::kGroups == 1 ? 0 : two ? u * D : turn * D);
           const uint32_t pa = tmem + C::kP + u * (D == 128 ? C::kS : TT / 2);
-          const bool add = C::kGroups == 2 ? s > 1 : s > 0;
+          const bool add = s > (two ? 1 : 0);
           const auto half = [&](int h) {
 #pragma unroll
             for (int y = 0; y < TT / 32; ++y) {
@@ -1198,12 +1211,14 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           if (tc5_elect()) {
             half(1 - kHalf0);
             if (!dual || u == 1) tc5_commit(bar(tb.empty[slot]));
-            if (C::kGroups == 1) tc5_commit(bar(tb.pv_done));
-            if (s + C::kGroups >= steps) tc5_commit(bar(tb.o_done[C::kGroups == 2 ? u : 0]));
+            if (!two) tc5_commit(bar(tb.pv_done));
+            if (s + (two ? 2 : 1) >= steps)
+              tc5_commit(bar(tb.o_done[C::kGroups == 1 ? 0 : two ? u : turn]));
           }
           if (s + 2 < steps) qk(s + 2, __all_sync(0xffffffffu, k_there));
         }
         fill += tiles;
+        if (!two) turn ^= 1;
       }
     } else if constexpr (kFp8) {
       // ---------------- E4M3 tiles to FP16 ----------------
