@@ -43,7 +43,7 @@ Layout layout_of(const qsa_paged_cache& c, int64_t tokens, int64_t heads, bool p
   l.pos = take((size_t)(l.max_tiles + 1) * 8);
   l.first = take((size_t)c.num_reqs * 4);
   l.cuts = take(kChunkMaxCtas * sizeof(ChunkCut));
-  l.owners = take(prefix ? (size_t)l.max_tiles * sizeof(int4) : 0);
+  l.owners = take(prefix ? (size_t)l.max_tiles * sizeof(ChunkOwner) : 0);
   const int64_t pieces = (prefix ? 4 : 2) * kChunkMaxCtas;
   l.part_ml = take((size_t)(pieces * l.part_rows) * 8);
   l.part_o = take((size_t)(pieces * l.part_rows * c.head_dim) * 4);
@@ -155,7 +155,7 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   p.pos = reinterpret_cast<int64_t*>(w + l.pos);
   p.first = reinterpret_cast<int32_t*>(w + l.first);
   p.cuts = reinterpret_cast<ChunkCut*>(w + l.cuts);
-  p.owners = reinterpret_cast<int4*>(w + l.owners);
+  p.owners = reinterpret_cast<ChunkOwner*>(w + l.owners);
   p.max_own = (int32_t)l.max_own;
   p.part_rows = (int32_t)l.part_rows;
   p.part_ml = reinterpret_cast<float*>(w + l.part_ml);

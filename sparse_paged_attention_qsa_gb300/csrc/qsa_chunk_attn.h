@@ -31,7 +31,10 @@ inline int chunk_heads(int group) {
 //   heads of 64,  256 rows  5.4  6.9  9.7 15.2 26.6;  4 rows  3.5  4.2  5.1  7.4 14.5
 //   heads of 256, 128 rows  5.9  7.3 10.3 16.3 28.1;  4 rows  3.3  4.4  6.7 12.1 23.3
 // and 1.4 a tile of heads of 128 over K/V that the L2 holds.
-constexpr int kTileCost = 4, kHeavyExtra = 14, kLightExtra = 8;
+constexpr int kTileCostLog2 = 2, kTileCost = 4, kHeavyExtra = 14, kLightExtra = 8;
+// A CTA's share of a batch behind a prefix, below which it gets a run of the prefix's
+// or of the requests' own alone.
+constexpr int kChunkShare = 60;
 // K/V tiles from which on two warpgroups share a row tile of one accumulator.
 constexpr int kChunkSplit = 12;
 // Pieces of a row tile, from which on runs are longer, and how long at least.
@@ -46,7 +49,8 @@ struct ChunkTile {
 struct ChunkList {
   int64_t total;                // cost of its row tiles, for one set of heads
   int32_t k0, k1;               // they are [k0, k1)
-  int32_t longest, pad;         // the largest cost
+  int32_t longest;              // the largest cost
+  int32_t cta0, ctas;           // the CTAs that walk them
 };
 struct ChunkPlan {
   ChunkList list[2];            // the prefix's row tiles, the requests' own
@@ -60,6 +64,13 @@ struct ChunkCut {
   int32_t token, toks;          // its rows of q
   int32_t pad;
 };
+
+// With a prefix, for the join: the runs [c0, c1] of a row tile (c0 -1: other ones for
+// each set of heads), in c0 as its second segment or its first; its rows of q.
+struct ChunkOwner {
+  int32_t c0, c1, second, token, toks;
+};
+constexpr int32_t kBySet = 1 << 30;
 
 struct ChunkParams {
   CacheView c;
@@ -89,7 +100,7 @@ struct ChunkParams {
   int64_t* pos;                 // [max_tiles + 1] cost of the row tiles before each
   int32_t* first;               // [num_reqs] each request's first row tile
   ChunkCut* cuts;               // [kChunkMaxCtas] the one that a run's start cuts first (set -1: none)
-  int4* owners;                 // with a prefix: [max_tiles] the runs [x, y] of each, z as second
+  ChunkOwner* owners;           // with a prefix: [max_tiles]
   int32_t max_own;              // row tiles of requests, at most
   int32_t part_rows;            // rows of a row tile, at most; accumulators 128 apart
   float* part_ml;               // [2 * kChunkMaxCtas, twice that with a prefix][part_rows][2]

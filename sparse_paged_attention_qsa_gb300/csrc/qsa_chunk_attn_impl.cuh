@@ -163,30 +163,34 @@ __device__ __forceinline__ int32_t extra_cost(const ChunkParams& p, int32_t toks
   return toks * p.sub > p.heavy_rows ? kHeavyExtra : kLightExtra;
 }
 
+// Not negative; 64-bit divisions take several times as long.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // Equal runs of all sets' row tiles, of the prefix's and of the requests' own: a CTA
 // walks one of each, so that it does not matter what the one costs beside the other,
 // and half of the CTAs begin with either, products and memory side by side.  Where
 // the sets divide the CTAs evenly enough every set has the same runs, so that the K/V
 // heads of the same entries, whose elements lie side by side, are read at the same
-// time.
+// time.  Where a CTA's two runs would be short, the lists get CTAs of their own.
 struct ChunkRuns {
   int64_t total, each, more;    // of one set of heads, or of all
   int n;                        // runs of it
   bool by_head;
 };
-__device__ __forceinline__ ChunkRuns chunk_runs(const ChunkList& list, int heads, int ctas) {
+__device__ __forceinline__ ChunkRuns chunk_runs(const ChunkList& list, int heads) {
   ChunkRuns r;
   const int64_t total = list.total;
   // a row tile in more than kChunkPieces pieces: longer runs, while they are short,
   // cost the walk less than its pieces the join
   // (and no run without a tile's end: kTileCost at least)
   const int least = max(kTileCost, min(kChunkMinRun, list.longest / kChunkPieces + 1));
-  ctas = (int)max((int64_t)1, min((int64_t)ctas, total * heads / least));
+  const int ctas = (int)max((int64_t)1, min((int64_t)list.ctas, total * heads / least));
   const int per = ctas / heads;
   r.by_head = per > 0 && per * heads * 16 >= ctas * 15;
   r.n = r.by_head ? per : ctas;
   r.total = r.by_head ? total : total * heads;
-  r.each = r.total / r.n;
+  r.each = divide(r.total, r.n);
   r.more = r.total - r.each * r.n;
   return r;
 }
@@ -195,11 +199,7 @@ __device__ __forceinline__ int64_t chunk_run_start(const ChunkRuns& r, int c) {
 }
 __device__ __forceinline__ int chunk_run_of(const ChunkRuns& r, int64_t x) {
   const int64_t big = (r.each + 1) * r.more;
-  return (int)(x < big ? x / (r.each + 1) : r.more + (x - big) / r.each);
-}
-// the CTA that walks run c of a head
-__device__ __forceinline__ int chunk_cta(const ChunkRuns& r, int heads, int head, int c) {
-  return r.by_head ? c * heads + head : c;
+  return (int)(x < big ? divide(x, r.each + 1) : r.more + divide(x - big, r.each));
 }
 // the runs [*c0, *c1] that hold K/V tiles of row tile k of a head, and where it begins
 __device__ __forceinline__ int64_t chunk_owners(const ChunkParams& p, const ChunkRuns& r,
@@ -238,12 +238,12 @@ __device__ __forceinline__ Walk walk_start(const ChunkParams& p, const ChunkPlan
   w.k = l.k0;
   w.set = 0;
   if (l.total == 0) return w;
-  const ChunkRuns r = chunk_runs(l, p.sets, gridDim.x);
-  const int run = r.by_head ? blockIdx.x / p.sets : blockIdx.x;
-  if (run >= r.n) return w;
+  const ChunkRuns r = chunk_runs(l, p.sets);
+  const int cta = (int)blockIdx.x - l.cta0, run = r.by_head ? cta / p.sets : cta;
+  if (cta < 0 || run >= r.n) return w;
   w.x = chunk_run_start(r, run);
   w.x1 = chunk_run_start(r, run + 1);
-  w.set = r.by_head ? blockIdx.x % p.sets : (int)(w.x / l.total);
+  w.set = r.by_head ? cta % p.sets : (int)divide(w.x, l.total);
   const int64_t base = r.by_head ? 0 : l.total * w.set, at0 = p.pos[l.k0];
   const int64_t at = w.x - base + at0;
   int lo = l.k0, hi = l.k1 - 1;
@@ -255,24 +255,29 @@ __device__ __forceinline__ Walk walk_start(const ChunkParams& p, const ChunkPlan
   w.base = base - at0;
   return w;
 }
-// The CTA's two runs, one after the other; the next segment with something to do.
+// The CTA's two runs, one after the other.
 struct Runs2 {
-  Walk w, later;
-  bool last;
+  Walk w;
+  int32_t left;                  // lists not begun
 };
-__device__ __forceinline__ Runs2 walk_begin(const ChunkParams& p) {
-  const ChunkPlan plan = *p.plan;
-  const int order = (blockIdx.x / p.sets) & 1;             // the same for all sets
-  return Runs2{walk_start(p, plan, order), walk_start(p, plan, order ^ 1), false};
+__device__ __forceinline__ Runs2 walk_begin() {
+  Runs2 r;
+  r.w.x = r.w.x1 = 0;
+  r.left = 2;
+  return r;
 }
+// The next segment with something to do; false where there is none.
 template <int TT>
 __device__ __forceinline__ bool walk_next(const ChunkParams& p, Runs2& runs, Segment* s) {
   for (;;) {
     Walk& w = runs.w;
     if (w.x >= w.x1) {
-      if (runs.last) return false;
-      w = runs.later;
-      runs.last = true;
+      if (runs.left == 0) return false;
+      const ChunkPlan plan = *p.plan;
+      // every other run, the same for all sets, begins with the requests' own
+      const int order = plan.list[1].cta0 > 0 ? 0 : (blockIdx.x / p.sets) & 1;
+      w = walk_start(p, plan, runs.left == 2 ? order : order ^ 1);
+      --runs.left;
       continue;
     }
     if (w.k == w.k1) {
@@ -286,8 +291,8 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, Runs2& runs, Seg
     const int extra = extra_cost(p, t.toks);
     s->k = w.k;
     s->set = w.set;
-    s->t0 = t.tiles > 0 ? (int)(max((int64_t)0, w.x - a - extra) / kTileCost) : 0;
-    s->t1 = t.tiles > 0 ? (int)(max((int64_t)0, end - a - extra) / kTileCost) : 0;
+    s->t0 = t.tiles > 0 ? (int)(max((int64_t)0, w.x - a - extra) >> kTileCostLog2) : 0;
+    s->t1 = t.tiles > 0 ? (int)(max((int64_t)0, end - a - extra) >> kTileCostLog2) : 0;
     s->whole = s->t0 == 0 && s->t1 == t.tiles;
     s->which = w.first ? 0 : 1;
     s->list = w.list;
@@ -345,6 +350,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   __shared__ int64_t s_sums[32];
   __shared__ int32_t s_longest[2];
   __shared__ int64_t s_own;
+  __shared__ int32_t s_first[kPlanThreads];  // of up to as many requests
   const int tid = threadIdx.x, R = p.c.num_reqs, RT = kAccs * p.acc_toks;   // tokens of a row tile
   pdl_wait();
   const int32_t token0 = min(max(p.starts[0], 0), p.tokens);
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       if (n > 0 && p.ctx[b] > p.c.cap) report(p.err, QSA_DERR_CONTEXT);
     }
     const int64_t at = before + block_scan(k, s_sums, &all);
-    if (b < R) p.first[b] = (int)min(at, (int64_t)p.max_tiles);
+    if (b < R) p.first[b] = s_first[tid] = (int)min(at, (int64_t)p.max_tiles);
     before += all;
   }
   const int n = (int)min(before, (int64_t)p.max_tiles);
@@ -381,15 +387,16 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         t.toks = min(RT, tokens - t.tok0);
         t.tiles = pre.tiles;
       } else {
+        const int32_t* first = R <= kPlanThreads ? s_first : p.first;
         int lo = 0, hi = R - 1;              // the last request that begins at or before k
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (p.first[mid] <= k) lo = mid; else hi = mid - 1;
+          if (first[mid] <= k) lo = mid; else hi = mid - 1;
         }
         int32_t t0, m;
         request_rows(p, lo, &t0, &m);
         t.req = lo;
-        t.tok0 = (k - p.first[lo]) * RT;
+        t.tok0 = (k - first[lo]) * RT;
         t.toks = min(RT, m - t.tok0);
         t.tiles = request_sight<TT>(p, p.ctx[lo], m, t.tok0, t.tok0 + t.toks - 1).tiles;
       }
@@ -406,8 +413,16 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   }
   if (tid == 0 && n_prefix >= n) s_own = cost;
   __syncthreads();
-  const ChunkPlan plan{{{s_own, 0, min(n_prefix, n), s_longest[0], 0},
-                        {cost - s_own, min(n_prefix, n), n, s_longest[1], 0}},
+  // CTAs of their own where a CTA's two runs would be short
+  const int64_t t0 = s_own, t1 = cost - s_own;
+  int shares = ctas, cut = 0;                // CTAs of the first list; of both to the second
+  if (t0 > 0 && t1 > 0 && (t0 + t1) * p.sets < (int64_t)ctas * kChunkShare) {
+    const int unit = ctas >= 2 * p.sets ? p.sets : 1, all_units = ctas / unit;
+    cut = unit * (int)min(max((all_units * t0 + (t0 + t1) / 2) / (t0 + t1), (int64_t)1), (int64_t)all_units - 1);
+    shares = cut;
+  }
+  const ChunkPlan plan{{{t0, 0, min(n_prefix, n), s_longest[0], 0, shares},
+                        {t1, min(n_prefix, n), n, s_longest[1], cut, ctas - cut}},
                        token0, tokens};
   if (tid == 0) {
     p.pos[n] = cost;
@@ -418,11 +433,20 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   if (p.res_o[0]) {
     __syncthreads();
     for (int x = 0; x < 2; ++x) {
-      const ChunkRuns r = chunk_runs(plan.list[x], p.sets, ctas);
-      for (int k = plan.list[x].k0 + tid; r.by_head && k < plan.list[x].k1; k += kPlanThreads) {
-        int c0, c1;
-        const int64_t x0 = chunk_owners(p, r, plan.list[x], 0, k, &c0, &c1);
-        p.owners[k] = make_int4(c0, c1, chunk_run_start(r, c0) < x0, 1);
+      const ChunkRuns r = chunk_runs(plan.list[x], p.sets);
+      for (int k = plan.list[x].k0 + tid; k < plan.list[x].k1; k += kPlanThreads) {
+        ChunkOwner o;
+        o.c0 = -1;                           // to be found for each set
+        if (r.by_head) {
+          const int64_t x0 = chunk_owners(p, r, plan.list[x], 0, k, &o.c0, &o.c1);
+          o.second = chunk_run_start(r, o.c0) < x0;
+        }
+        const ChunkTile t = p.tiles[k];
+        int32_t begin = token0, m;
+        if (t.req >= 0) request_rows(p, t.req, &begin, &m);
+        o.token = begin + t.tok0;
+        o.toks = t.toks;
+        p.owners[k] = o;
       }
     }
   }
@@ -475,13 +499,13 @@ struct ChunkShape {
   static constexpr int kO = D == 128 ? 256 : D == 64 ? 384 : 256;
   static_assert(kSmem <= 232448, "shared memory");
   // Registers: 384 threads of 168 at launch, dealt out as 208, 208 and 88 a thread
-  // of a warpgroup; over an E4M3 cache 512 of 128 as 160, 160, 96, 96.
+  // of a warpgroup; over an E4M3 cache 512 of 128 as 192, 192, 64, 64.
   static __device__ __forceinline__ void more_registers() {
-    if constexpr (kGroups == 2 && kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    if constexpr (kGroups == 2 && kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else if constexpr (kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   }
   static __device__ __forceinline__ void fewer_registers() {
-    if constexpr (kGroups == 2 && kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if constexpr (kGroups == 2 && kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     else if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   }
   // the ring's slot of tile f's K (V), and the phase in which it is full
@@ -545,9 +569,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
   constexpr bool kOutBf16 = __is_same(T, __nv_bfloat16), kBf16 = kOutBf16 && !kFp8;
   constexpr bool kQToFp16 = kOutBf16 && kFp8;
   constexpr int TT = C::TT, NS = C::NS;
-  // S of an E4M3 walk is read half a row at a time, the second half's weights first
-  constexpr int kWords = TT / 32, kKeep = kFp8 && TT == 128 ? 2 : kWords, kFirst = kWords - kKeep;
-  constexpr int kHalf0 = kFirst > 0 ? 1 : 0;               // the half of P that comes first
+  constexpr int kWords = TT / 32;                          // of 32 columns of S
   extern __shared__ unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
@@ -709,21 +731,15 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
 #pragma unroll
           for (int w = 0; w < kWords; ++w) vis[w] = 0xffffffffu;
         }
-        // with the registers of an E4M3 walk half a row at a time, the first half read
-        // again for its weights (P, which shares S's columns with heads of 128, takes
-        // those of the second)
-        uint32_t z[kKeep][32];
+        uint32_t z[kWords][32];
         float mx[kWords];
 #pragma unroll
-        for (int w0 = 0; w0 < kWords; w0 += kKeep) {
+        for (int w = 0; w < kWords; ++w) tc5_ld32_max(zs + w * 32, z[w], mx[w]);
+        tc5_wait_ld();
 #pragma unroll
-          for (int w = 0; w < kKeep; ++w) tc5_ld32_max(zs + (w0 + w) * 32, z[w], mx[w0 + w]);
-          tc5_wait_ld();
-#pragma unroll
-          for (int w = 0; w < kKeep; ++w) {
-            tc5_hold(z[w]);
-            tc5_hold(mx[w0 + w]);
-          }
+        for (int w = 0; w < kWords; ++w) {
+          tc5_hold(z[w]);
+          tc5_hold(mx[w]);
         }
         float top = fmaxf(mx[0], mx[1]);
         if constexpr (TT == 128) top = max3(top, mx[2], mx[3]);
@@ -775,25 +791,11 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(tb.p_half[u][half]));
         };
-        if constexpr (kFirst == 0) {
 #pragma unroll
-          for (int w = 0; w < kWords / 2; ++w) weights(w, z[w]);
-          if (!edge) ready(0);
+        for (int w = 0; w < kWords / 2; ++w) weights(w, z[w]);
+        if (!edge) ready(0);
 #pragma unroll
-          for (int w = kWords / 2; w < kWords; ++w) weights(w, z[w]);
-        } else {
-          weights(2, z[0]);
-          tc5_ld32(zs, z[0]);
-          weights(3, z[1]);
-          tc5_wait_ld();
-          tc5_hold(z[0]);
-          tc5_ld32(zs + 32, z[1]);
-          if (!edge) ready(1);
-          weights(0, z[0]);
-          tc5_wait_ld();
-          tc5_hold(z[1]);
-          weights(1, z[1]);
-        }
+        for (int w = kWords / 2; w < kWords; ++w) weights(w, z[w]);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (edge) {
           // 0 times what a hidden entry holds may be NaN: whatever is not finite in
@@ -823,9 +825,9 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
 #pragma unroll
           for (int w = 0; w < kWords; ++w)
             if (vis[w] & *reinterpret_cast<volatile uint32_t*>(&tb.bad[i][w])) l = NAN;
-          ready(kHalf0);
+          ready(0);
         }
-        ready(1 - kHalf0);
+        ready(1);
       }
       if (!two) steps_done += steps;
       fill += tiles;
@@ -1007,7 +1009,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         // a run's first row tile, where it is not its beginning: for the join
         if (!p.res_o[0] && seg.which == 0 && seg.t0 > 0 && r == 0 && (g == 0 || !two)) {
           const ChunkPlan plan = *p.plan;
-          const ChunkRuns runs = chunk_runs(plan.list[1], p.sets, gridDim.x);
+          const ChunkRuns runs = chunk_runs(plan.list[1], p.sets);
           ChunkCut cut;
           const int64_t x0 = chunk_owners(p, runs, plan.list[1], seg.set, seg.k, &cut.c0, &cut.c1);
           if ((int)(runs.by_head ? blockIdx.x / p.sets : blockIdx.x) == cut.c0 + 1) {
@@ -1108,7 +1110,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     } else if (warp == kQueries) {
       // ---------------- producer of the segments and the queries ----------------
       // waits here are for row tiles of any length: 20 us a K/V tile more
-      Runs2 runs = walk_begin(p);
+      Runs2 runs = walk_begin();
       int64_t recent = 0;                                  // K/V tiles of the last segments
       for (int sn = 0;; ++sn) {
         Segment seg;
@@ -1198,18 +1200,18 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
 #pragma unroll
             for (int y = 0; y < TT / 32; ++y) {
               const int x = h * (TT / 32) + y;
-              tc5_mma_ts(o, pa + x * 8, v + x * (16 * 128 / 16), kPv, add || h != kHalf0 || y > 0);
+              tc5_mma_ts(o, pa + x * 8, v + x * (16 * 128 / 16), kPv, add || x > 0);
             }
           };
-          wait_for(bar(tb.p_half[u][kHalf0]), (uint32_t)(ready[u] & 1));
+          wait_for(bar(tb.p_half[u][0]), (uint32_t)(ready[u] & 1));
           if (!__all_sync(0xffffffffu, v_there)) wait_for(bar(tb.full[slot]), C::phase(f, 1));
           tc5_fence_after();
-          if (tc5_elect()) half(kHalf0);
-          wait_for(bar(tb.p_half[u][1 - kHalf0]), (uint32_t)(ready[u] & 1));
+          if (tc5_elect()) half(0);
+          wait_for(bar(tb.p_half[u][1]), (uint32_t)(ready[u] & 1));
           ++ready[u];
           tc5_fence_after();
           if (tc5_elect()) {
-            half(1 - kHalf0);
+            half(1);
             if (!dual || u == 1) tc5_commit(bar(tb.empty[slot]));
             if (!two) tc5_commit(bar(tb.pv_done));
             if (s + (two ? 2 : 1) >= steps)
@@ -1333,11 +1335,11 @@ __device__ __forceinline__ int tile_row(const ChunkParams& p, int j, int g) {
 // Adds what the runs [c0, c1] left of row i of a row tile, in c0 as its second
 // segment or its first; of them this thread's: k0, k0 + dk, ...
 template <int D>
-__device__ __forceinline__ void add_pieces(const ChunkParams& p, int list, bool by_head, int set, int c0, int c1,
+__device__ __forceinline__ void add_pieces(const ChunkParams& p, int list, int cta0, bool by_head, int set, int c0, int c1,
                                            int second, int i, int ln, int k0, int dk, float mult, Acc& acc) {
 #pragma unroll 4
   for (int c = c0 + k0; c <= c1; c += dk) {
-    const int cta = by_head ? c * p.sets + set : c;
+    const int cta = cta0 + (by_head ? c * p.sets + set : c);
     const int64_t at = piece_at(p, list, cta, c == c0 ? second : 0) + i;
     acc.add(*reinterpret_cast<const float2*>(p.part_ml + at * 2),
             *reinterpret_cast<const float4*>(p.part_o + at * D + ln * 4), mult);
@@ -1374,7 +1376,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const Chu
     const int i = few ? i0 + grp : i0, j = i / p.sub, g = i - j * p.sub;
     Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (i < rows)
-      add_pieces<D>(p, 1, cut.by_head, cut.set, cut.c0, cut.c1, cut.second, tile_row(p, j, g), ln,
+      add_pieces<D>(p, 1, 0, cut.by_head, cut.set, cut.c0, cut.c1, cut.second, tile_row(p, j, g), ln,
                     few ? 0 : grp, few ? 1 : kG, mult, a);
     if (!few) {
       __syncthreads();
@@ -1391,7 +1393,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_kernel(const Chu
 // With a prefix: CTA (row tile of a request, set of heads, some of its rows); D/4
 // threads a row, or `ways` times as many, which share its pieces.
 template <bool kBf16, bool kBf16W, int D>
-__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const ChunkParams p, int ctas, int ways) {
+__global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const ChunkParams p, int ways) {
   constexpr int L = D / 4, kG = kChunkJoinThreads / L;
   __shared__ __align__(16) float4 s_o[kChunkJoinThreads];
   __shared__ float2 s_ml[kG];
@@ -1401,35 +1403,35 @@ __global__ void __launch_bounds__(kChunkJoinThreads) chunk_join_all_kernel(const
   const ChunkPlan plan = *p.plan;
   const int k1 = plan.list[1].k0 + blockIdx.x;
   if (k1 >= plan.list[1].k1) return;
-  const ChunkTile t = p.tiles[k1];
-  int32_t t0, n;
-  request_rows(p, t.req, &t0, &n);
-  const ChunkRuns runs[2] = {chunk_runs(plan.list[0], p.sets, ctas), chunk_runs(plan.list[1], p.sets, ctas)};
-  const float mult = set_mult(p, set);
-  const int all = t.toks * p.sub;
-  const int way = grp % ways, rows = kG / ways;
-  const auto owners = [&](int list, int k) {
-    const ChunkRuns& r = runs[list];
-    if (r.by_head) return p.owners[k];
-    int c0, c1;
-    const int64_t x0 = chunk_owners(p, r, plan.list[list], set, k, &c0, &c1);
-    return make_int4(c0, c1, chunk_run_start(r, c0) < x0, 0);
+  const auto owner = [&](int list, int k) {
+    ChunkOwner o = p.owners[k];
+    if (o.c0 < 0) {                                        // not the same for all sets
+      const ChunkRuns r = chunk_runs(plan.list[list], p.sets);
+      const int64_t x0 = chunk_owners(p, r, plan.list[list], set, k, &o.c0, &o.c1);
+      o.second = chunk_run_start(r, o.c0) < x0;
+      o.c0 |= kBySet;
+    }
+    return o;
   };
-  const int4 own = owners(1, k1);
+  const ChunkOwner own = owner(1, k1);
+  const float mult = set_mult(p, set);
+  const int all = own.toks * p.sub;
+  const int way = grp % ways, rows = kG / ways;
   for (int i0 = blockIdx.z * rows; i0 < all; i0 += gridDim.z * rows) {
     const int i = i0 + grp / ways, j = i / p.sub, g = i - j * p.sub;
-    const int32_t token = t0 + t.tok0 + j;
+    const int32_t token = own.token + j;
     Acc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (i < all) {
       const int64_t rh = (int64_t)token * p.heads + set * p.sub + g;
       for (int list = 0; list < 2; ++list) {
-        const int32_t at = list ? t.tok0 + j : token - plan.token0;
+        const int32_t at = token - plan.token0;
         const int k = list ? k1 : at / RT;
         if (!list && (at < 0 || k >= plan.list[0].k1)) continue;
-        const int4 o = list ? own : owners(0, k);
-        if (o.x < o.y)
-          add_pieces<D>(p, list, runs[list].by_head, set, o.x, o.y, o.z, tile_row(p, list ? j : at % RT, g), ln, way,
-                        ways, mult, a);
+        const ChunkOwner o = list ? own : owner(0, k);
+        const int c0 = o.c0 & ~kBySet;
+        if (c0 < o.c1)
+          add_pieces<D>(p, list, plan.list[list].cta0, !(o.c0 & kBySet), set, c0, o.c1, o.second,
+                        tile_row(p, list ? j : at % RT, g), ln, way, ways, mult, a);
         else if (way == 0)
           a.add(*reinterpret_cast<const float2*>(p.res_ml[list] + rh * 2),
                 *reinterpret_cast<const float4*>(p.res_o[list] + rh * D + ln * 4), mult);
@@ -1495,7 +1497,7 @@ cudaError_t launch_chunk_typed(const ChunkParams& p, const CUtensorMap& kmap, co
     const int64_t z = std::min<int64_t>((rows * ways + kG - 1) / kG, 32);
     return launch_after(chunk_join_all_kernel<kBf16, kBf16W, D>,
                         dim3((unsigned)p.max_own, (unsigned)p.sets, (unsigned)z),
-                        dim3(kChunkJoinThreads), 0, st, p, ctas, ways);
+                        dim3(kChunkJoinThreads), 0, st, p, ways);
   }
   const int64_t rows = std::min<int64_t>((int64_t)p.tokens * p.sub, C::kGroups * 128);
   return launch_after(chunk_join_kernel<kBf16, kBf16W, D>,
