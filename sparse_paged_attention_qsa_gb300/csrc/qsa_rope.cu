@@ -4,8 +4,8 @@
 // A head of D elements lies in the lanes of half a warp (D = 128) or of what
 // D/8 rounds up to, 16 bytes a lane: the sum of squares is a few shuffles, and a
 // pair whose elements lie rot_dim/2 apart is one more.  A warp takes heads of one
-// token, since their angles are the same: each lane forms the sines and cosines
-// of its own elements once and turns every head with them.
+// token, since their angles are the same: its lanes form the sines and cosines once,
+// each its share, and turn every head with them.
 //
 // Angles.  A turn is 2^64: a frequency f becomes F = f / (2 pi) * 2^64 (its 24
 // bits times 1/(2 pi) to 64 bits, an integer product), and position * F modulo
@@ -13,7 +13,10 @@
 // position (binary32 products are off by a radian at position 2^24).  Binary64
 // would do as well; its rate here is a sixtieth of the integer one.
 //
-// Bytes bound it: each element is read and written once.
+// Bytes bound it: each element is read and written once.  16344 tokens of 40 heads
+// of 128: pairs side by side 56.5 us (5.9 TB/s), half a head apart 70 (two shuffles
+// more a pair); each lane forming all angles of its own elements, with heads of q and
+// k in one loop, 78 and 106; two and four CTAs an SM 65 and 70, 71 and 98.
 #include "qsa_cache_host.h"
 #include "qsa_device.cuh"
 #include "qsa_host.h"
@@ -30,6 +33,7 @@ namespace qsa {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeCtas = 3;       // of an SM
 constexpr int kRopeUnroll = 4;     // heads of a lane in flight
 
 struct RopeParams {
@@ -60,6 +64,8 @@ __device__ __forceinline__ uint64_t turns(float f) {
   return u >> 31 ? 0 - t : t;
 }
 
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) { return ffma2(a, b, make_float2(-0.f, -0.f)); }
+
 template <typename T>
 __device__ __forceinline__ float2 widen(uint32_t x) {
   if constexpr (__is_same(T, __nv_bfloat16))
@@ -79,8 +85,11 @@ __device__ __forceinline__ uint32_t narrow(float lo, float hi) {
 
 // L lanes a head, 8 elements a lane.
 template <typename T, typename WT, int L, bool kPairs>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeParams p) {
   constexpr int kHeads = 32 / L;                            // heads of a warp at a time
+  __shared__ uint64_t s_freq[QSA_ROPE_MAX_DIM / 2];
+  __shared__ __align__(16) float2 s_angles[kRopeThreads / 32][QSA_ROPE_MAX_DIM / 2];
+  float2* angles = s_angles[threadIdx.x >> 5];              // cosine and sine
   const int lane = threadIdx.x & 31, piece = lane % L;
   const int64_t warps = (int64_t)gridDim.x * (kRopeThreads / 32);
   const int64_t warp = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
@@ -89,87 +98,96 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const bool upper = piece >= half;
   // the lane that holds the other elements of this lane's pairs
   const int other = kPairs || !turned ? lane : upper ? lane - half : lane + half;
-  constexpr int kAngles = kPairs ? 4 : 8;
-  uint64_t freq[kAngles];
-  float w[2][8];
+  float2 w[2][4];
   pdl_wait();          // whatever is read may be the kernel's before it
-#pragma unroll
-  for (int i = 0; i < kAngles; ++i)
-    freq[i] = turned ? turns(p.inv_freq[kPairs ? piece * 4 + i : (upper ? piece - half : piece) * 8 + i])
-                     : 0;
+  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) s_freq[i] = turns(p.inv_freq[i]);
+  __syncthreads();
 #pragma unroll
   for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[x][i] = there && p.weight[x] ? (float)static_cast<const WT*>(p.weight[x])[piece * 8 + i] : 1.f;
-  const int all = p.heads[0] + p.heads[1];
+    for (int i = 0; i < 4; ++i) {
+      const WT* v = static_cast<const WT*>(p.weight[x]) + piece * 8 + i * 2;
+      w[x][i] = there && p.weight[x] ? make_float2((float)v[0], (float)v[1]) : make_float2(1.f, 1.f);
+    }
   const int64_t items = p.tokens * p.split;
   for (int64_t item = warp; item < items; item += warps) {
     const int64_t t = item / p.split;
     const int part = (int)(item - t * p.split);
     const int64_t pos = p.positions[t];
     if (pos < 0) continue;
-    float c[kAngles], s[kAngles];
-#pragma unroll
-    for (int i = 0; i < kAngles; ++i) {
+    __syncwarp();                                           // the last token's have been read
+#pragma unroll 2
+    for (int i = lane; i < p.rot / 2; i += 32) {
       // half turns in [-1, 1)
-      const float x = (float)(int32_t)(uint32_t)((uint64_t)pos * freq[i] >> 32) * 0x1p-31f;
-      sincospif(x, &s[i], &c[i]);
-      if (!kPairs && !upper) s[i] = -s[i];
+      const float x = (float)(int32_t)(uint32_t)((uint64_t)pos * s_freq[i] >> 32) * 0x1p-31f;
+      float2 a;
+      sincospif(x, &a.y, &a.x);
+      angles[i] = a;
     }
-    for (int h0 = part * kHeads + lane / L; h0 - lane / L < all; h0 += p.split * kHeads * kRopeUnroll) {
-      uint4 v[kRopeUnroll];
+    __syncwarp();
+    // a rotated element: its own times the cosine, the pair's other one times the sine
+    // (neighbours, or the same element of another lane); cosines and sines as pairs of
+    // neighbouring elements
+    float2 c[4], s[4];
+    const float4* mine = reinterpret_cast<const float4*>(
+        angles + (!turned ? 0 : kPairs ? piece * 4 : (upper ? piece - half : piece) * 8));
 #pragma unroll
-      for (int k = 0; k < kRopeUnroll; ++k) {
-        const int h = h0 + k * p.split * kHeads, x = h >= p.heads[0];
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (there && h < all)
-          v[k] = *reinterpret_cast<const uint4*>(p.in[x] + t * p.in_tok[x] +
-                                                 (h - (x ? p.heads[0] : 0)) * p.in_head[x] + piece * 16);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kPairs) {
+        const float4 a = mine[i / 2];
+        const float2 b = i & 1 ? make_float2(a.z, a.w) : make_float2(a.x, a.y);
+        c[i] = make_float2(b.x, b.x);
+        s[i] = make_float2(-b.y, b.y);
+      } else {
+        const float4 a = mine[i];
+        c[i] = make_float2(a.x, a.z);
+        s[i] = upper ? make_float2(a.y, a.w) : make_float2(-a.y, -a.w);
       }
+    }
 #pragma unroll
-      for (int k = 0; k < kRopeUnroll; ++k) {
-        const int h = h0 + k * p.split * kHeads, x = h >= p.heads[0];
-        if (h - lane / L >= all) break;                     // the whole warp's
-        const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        float y[8];
+    for (int x = 0; x < 2; ++x) {
+      const int heads = p.heads[x], step = p.split * kHeads;
+      const int64_t in_step = step * p.in_head[x], out_step = step * p.out_head[x];
+      int h = part * kHeads + lane / L;
+      const unsigned char* in = p.in[x] + t * p.in_tok[x] + h * p.in_head[x] + piece * 16;
+      unsigned char* out = p.out[x] + t * p.out_tok[x] + h * p.out_head[x] + piece * 16;
+      for (int h0 = part * kHeads; h0 < heads; h0 += step * kRopeUnroll) {
+        uint4 v[kRopeUnroll];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = widen<T>(u[i]);
-          y[2 * i] = f.x;
-          y[2 * i + 1] = f.y;
+        for (int k = 0; k < kRopeUnroll; ++k) {
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (there && h + k * step < heads) v[k] = *reinterpret_cast<const uint4*>(in + k * in_step);
         }
-        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
-#pragma unroll
-        for (int i = 1; i < L; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-        const float r = 1.f / sqrtf(fmaf(sum, p.inv_dim, p.eps));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= r * (x ? w[1][i] : w[0][i]);
-        float z[8];
-        if constexpr (kPairs) {
+        for (int k = 0; k < kRopeUnroll; ++k) {
+          if (h0 + k * step >= heads) break;                // the whole warp's
+          const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          float2 y[4], sum2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            z[2 * i] = y[2 * i] * c[i] - y[2 * i + 1] * s[i];
-            z[2 * i + 1] = y[2 * i + 1] * c[i] + y[2 * i] * s[i];
+            y[i] = widen<T>(u[i]);
+            sum2 = ffma2(y[i], y[i], sum2);
           }
-        } else {
+          float sum = sum2.x + sum2.y;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(0xffffffffu, y[i], other);
-            z[i] = y[i] * c[i] + o * s[i];
+          for (int i = 1; i < L; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+          const float r = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
+          uint32_t z[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i] = fmul2(y[i], fmul2(w[x][i], make_float2(r, r)));
+            float2 o;
+            if constexpr (kPairs) o = make_float2(y[i].y, y[i].x);
+            else o = make_float2(__shfl_sync(0xffffffffu, y[i].x, other), __shfl_sync(0xffffffffu, y[i].y, other));
+            const float2 q = ffma2(o, s[i], fmul2(y[i], c[i]));
+            z[i] = turned ? narrow<T>(q.x, q.y) : narrow<T>(y[i].x, y[i].y);
           }
+          if (there && h + k * step < heads)
+            *reinterpret_cast<uint4*>(out + k * out_step) = make_uint4(z[0], z[1], z[2], z[3]);
         }
-        if (!turned) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = y[i];
-        }
-        if (there && h < all)
-          *reinterpret_cast<uint4*>(p.out[x] + t * p.out_tok[x] +
-                                    (h - (x ? p.heads[0] : 0)) * p.out_head[x] + piece * 16) =
-              make_uint4(narrow<T>(z[0], z[1]), narrow<T>(z[2], z[3]), narrow<T>(z[4], z[5]),
-                         narrow<T>(z[6], z[7]));
+        h += step * kRopeUnroll;
+        in += in_step * kRopeUnroll;
+        out += out_step * kRopeUnroll;
       }
     }
   }
@@ -293,12 +311,14 @@ extern "C" qsa_status qsa_qk_norm_rope(
   int lanes = 1;
   while (lanes * 8 < head_dim) lanes *= 2;
   bind_calling_thread();
-  // a token's heads over as many warps as fill the GPU, no more than it has
+  // a token's heads over several warps where there are few tokens, each of which forms
+  // the angles again (256 tokens of 40 heads of 128: 5.0 us with up to 8 warps an SM,
+  // 6.5 with 4, 5.3 with 16, 7.4 with 32)
   const int64_t rounds = (q_heads + k_heads + 32 / lanes - 1) / (32 / lanes);
-  constexpr int64_t kWarps = 152 * 32;
+  constexpr int64_t kWarps = 152 * 8;
   p.split = (int32_t)std::max<int64_t>(1, std::min<int64_t>(rounds, kWarps / num_tokens));
   const int64_t ctas = (num_tokens * p.split + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  const int grid = (int)std::min<int64_t>(ctas, 152 * 8);
+  const int grid = (int)std::min<int64_t>(ctas, 152 * kRopeCtas);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool pairs = interleaved != 0, wide = weight_dtype == QSA_DT_F32;
   cudaError_t e;
