@@ -123,7 +123,7 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   const int64_t pcap = prefix ? prefix_cols << p.c.page_log2 : 0;
   p.prefix_table = prefix && prefix_cols > 0 ? prefix_table : nullptr;
   p.prefix_cap = (int32_t)std::min<int64_t>(pcap, kMaxEntries);
-  p.prefix_len = prefix_len;
+  p.prefix_len = prefix ? prefix_len : nullptr;
   p.q = static_cast<const unsigned char*>(q);
   p.q_row = tokens > 1 ? q_strides[0] * 2 : 0;
   p.q_head = heads > 1 ? q_strides[1] * 2 : 0;
@@ -141,7 +141,8 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   p.acc_toks = 128 / p.sub;
   p.heavy_rows = chunk_accs(p.c.dim) == 2 ? p.acc_toks * p.sub : 32;
   p.scale_log2 = scale_log2;
-  p.window = (int32_t)std::min<int64_t>(window, INT32_MAX - 16);
+  // (a context is 2^31 - 1 at most: a window as wide hides nothing)
+  p.window = (int32_t)std::min<int64_t>(window, INT32_MAX);
   p.sink = window > 0 ? (int32_t)std::min<int64_t>(sink, kMaxEntries) : 0;
   p.lse = lse;
   p.err = error_word;

@@ -62,7 +62,6 @@ struct ChunkPlan {
 struct ChunkCut {
   int32_t set, c0, c1, second, by_head;
   int32_t token, toks;          // its rows of q
-  int32_t pad;
 };
 
 // With a prefix, for the join: the runs [c0, c1] of a row tile (c0 -1: other ones for
@@ -74,9 +73,9 @@ constexpr int32_t kBySet = 1 << 30;
 
 struct ChunkParams {
   CacheView c;
-  const int32_t* prefix_table;  // nullable: no prefix
+  const int32_t* prefix_table;  // nullable: no prefix, or no entries of it
   int32_t prefix_cap;           // entries that its columns can hold
-  const int32_t* prefix_len;
+  const int32_t* prefix_len;    // nullable: no prefix
   const unsigned char* q;
   int64_t q_row, q_head;        // bytes
   unsigned char* out;
@@ -89,7 +88,7 @@ struct ChunkParams {
   int32_t acc_toks;             // tokens of an accumulator: 128 / sub
   int32_t heavy_rows;           // more rows than that cost the more
   float scale_log2;             // scale * log2(e)
-  int32_t window;               // 0: none; at most INT32_MAX - 16
+  int32_t window;               // 0: none
   int32_t sink;                 // 0 without a window
   float* lse;                   // nullable
   uint32_t* err;

@@ -114,7 +114,7 @@ struct Sight {
     return prefix ? cap : min(max(base + j, 0), cap);
   }
   __device__ __forceinline__ int32_t lo(int j) const {
-    return window > 0 ? min(max(base + j - window, 0), cap) : 0;
+    return window > 0 ? (int32_t)min(max((int64_t)base + j - window, (int64_t)0), (int64_t)cap) : 0;
   }
   __device__ __forceinline__ int32_t at(int t) const { return t < ns ? t : t - ns + w0; }
 };
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   const int32_t token0 = min(max(p.starts[0], 0), p.tokens);
   const int32_t tokens = min(max(p.starts[R], token0), p.tokens) - token0;
   const Sight pre = prefix_sight<TT>(p);
-  if (tid == 0 && p.prefix_table && *p.prefix_len > p.prefix_cap) report(p.err, QSA_DERR_CONTEXT);
+  if (tid == 0 && p.prefix_len && *p.prefix_len > p.prefix_cap) report(p.err, QSA_DERR_CONTEXT);
   const int n_prefix = pre.tiles > 0 ? (tokens + RT - 1) / RT : 0;
   int64_t before = n_prefix, all;
   for (int b0 = 0; b0 < R; b0 += kPlanThreads) {

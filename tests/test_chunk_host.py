@@ -108,7 +108,8 @@ BAD = [
     (dict(out=_addr(9) + 4), ALIGN), (dict(starts=_addr(7) + 2), ALIGN), (dict(lse=_addr(10) + 1), ALIGN),
     (dict(err=_addr(12) + 1), ALIGN), (dict(out=_addr(6)), ALIAS), (dict(out=_addr(1)), ALIAS),
     (dict(lse=_addr(8)), ALIAS), (dict(lse=_addr(9)), ALIAS), (dict(err=_addr(7) + 16), ALIAS),
-    (dict(out=_addr(3) - 64), ALIAS),
+    (dict(out=_addr(3) - 64), ALIAS), (dict(ws=0), WORKSPACE), (dict(wsb=1000), WORKSPACE),
+    (dict(ws=_addr(11) + 128), ALIGN), (dict(ws=_addr(9) - 256), ALIAS), (dict(ws=_addr(6) - 256), ALIAS),
 ]
 
 
@@ -123,6 +124,21 @@ def test_chunk_refuses(lib, over, want):
     (dict(lse=_addr(5)), ALIAS)])
 def test_prefix_refuses(lib, over, want):
     assert _attend(lib, prefix=True, **over) == want
+
+
+def test_workspace_grows_with_what_needs_it(lib):
+    need = [_attend(lib, prefix, True) for prefix in (False, True)]
+    assert 0 < need[0] < need[1] and all(n % 256 == 0 for n in need)
+    for prefix, n in zip((False, True), need):
+        # one byte less is refused; nothing in the size depends on addresses
+        assert _attend(lib, prefix, wsb=n - 1) == WORKSPACE
+        assert _attend(lib, prefix, True, k=_addr(30), v=_addr(31), bt=_addr(32)) == n
+        assert _attend(lib, prefix, True, tokens=13) >= n
+        for over in (dict(tokens=0), dict(tokens=-1), dict(hq=3), dict(reqs=0), dict(dim=96), dict(size=12)):
+            assert _attend(lib, prefix, True, **over) == 0
+        # any number of tokens and heads that a call may have
+        assert _attend(lib, prefix, True, tokens=16777216, hq=126) > 0
+        assert _attend(lib, prefix, True, tokens=30000, hq=65534) > 0
 
 
 def test_attention_no_ops(lib):

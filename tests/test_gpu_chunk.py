@@ -251,6 +251,16 @@ def test_bad_pages_long_contexts_and_empty_rows():
     c.plen.fill_(-3)
     out, lse, err = c.run()
     assert c.check(out, lse)["err"] == int(err) == 0
+    c.plen.fill_(9)                                          # and none to look up
+    c.ptable = c.ptable[:0]
+    out, lse, err = c.run()
+    assert c.check(out, lse)["err"] == int(err) == K.DERR_CONTEXT
+    # fewer entries than new tokens, a window wider than any context
+    for window in (2 ** 31 - 1, 2 ** 40):
+        c = Case([(300, 0), (1, 50)], 4, 2, 64, 16, window=window, sink=2, seed=9)
+        c.ctx[0] = 40
+        out, lse, err = c.run()
+        assert c.check(out, lse)["err"] == int(err) == 0
     # no pages at all
     c = Case([(2, 3)], 2, 1, 64, 16, seed=9)
     c.k, c.v = c.k[:0], c.v[:0]
