@@ -34,7 +34,7 @@ extern "C" {
  * token with a negative position (the metadata builder's padding) is left as
  * it was in both.  The product of position and frequency is reduced to one
  * turn in 64 bits before it is rounded, so an angle is off by at most 2^-24 of
- * a half turn at every position below 2^36.
+ * a half turn wherever positions[t] * (1 + |inv_freq[i]|) is below 2^37.
  *
  * Arguments
  *   q, k           [num_tokens, q_heads, head_dim], [num_tokens, k_heads,

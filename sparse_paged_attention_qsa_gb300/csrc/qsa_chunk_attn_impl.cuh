@@ -27,6 +27,13 @@
 // that binary32 products have.  It moves only when weights would pass 2^15 (FP16)
 // or 2^8 (BF16), and O in tensor memory is rescaled at such moves alone.
 //
+// What bounds it.  Long prompts: shared memory, which Q K^T reads at its whole rate
+// (8 KB a product of 128 x 128 x 16, 64 cycles), beside the softmax's own chain of
+// 1400 cycles a tile: 2630 cycles for 256 rows by 128 entries of heads of 128, where
+// the tensor pipe alone takes 2048.  4096 tokens behind 4096 others, 16 heads of 128:
+// 170 us, 1.2 PFLOP/s, 0.61 of the measured cuBLAS rate.  Single tokens: HBM (64
+// requests of 8192 entries, 8 K/V heads of 128: 313 us, 6.9 TB/s).
+//
 // Rounding: q, K and V enter the products as they are (E4M3 as FP16, exactly; BF16
 // queries of an E4M3 cache as FP16 after a power-of-two scaling of the row, where
 // only bits 2^-25 below the row's largest element can be lost), weights rounded to
@@ -417,8 +424,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   const int64_t t0 = s_own, t1 = cost - s_own;
   int shares = ctas, cut = 0;                // CTAs of the first list; of both to the second
   if (t0 > 0 && t1 > 0 && (t0 + t1) * p.sets < (int64_t)ctas * kChunkShare) {
-    const int unit = ctas >= 2 * p.sets ? p.sets : 1, all_units = ctas / unit;
-    cut = unit * (int)min(max((all_units * t0 + (t0 + t1) / 2) / (t0 + t1), (int64_t)1), (int64_t)all_units - 1);
+    const int unit = ctas >= 2 * p.sets ? p.sets : 1, units = ctas / unit;
+    cut = (int)min(max((units * t0 + (t0 + t1) / 2) / (t0 + t1), (int64_t)1), (int64_t)units - 1);
+    cut *= unit;
     shares = cut;
   }
   const ChunkPlan plan{{{t0, 0, min(n_prefix, n), s_longest[0], 0, shares},
@@ -499,18 +507,25 @@ struct ChunkShape {
   static constexpr int kO = D == 128 ? 256 : D == 64 ? 384 : 256;
   static_assert(kSmem <= 232448, "shared memory");
   // Registers: 384 threads of 168 at launch, dealt out as 208, 208 and 88 a thread
-  // of a warpgroup; over an E4M3 cache 512 of 128 as 192, 192, 64, 64.
+  // of a warpgroup; over an E4M3 cache 512 of 128 as 192, 192, 64, 64.  A row of S
+  // stays in registers whole.
+  static constexpr int kRegs = kGroups == 1 ? 0 : kFp8 ? 128 : 168;
+  static constexpr int kMore = kFp8 ? 192 : 208, kFewer = kFp8 ? 64 : 88;
+  static_assert(2 * kMore + (kThreads / 128 - 2) * kFewer <= kThreads / 128 * kRegs || kGroups == 1,
+                "no more registers than the launch has");
   static __device__ __forceinline__ void more_registers() {
-    if constexpr (kGroups == 2 && kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    else if constexpr (kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMore));
   }
   static __device__ __forceinline__ void fewer_registers() {
-    if constexpr (kGroups == 2 && kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    else if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewer));
   }
   // the ring's slot of tile f's K (V), and the phase in which it is full
-  static __device__ __forceinline__ int slot(int f, int kv) { return kFp8 ? (2 * f + kv) % NS : kv * NS + f % NS; }
-  static __device__ __forceinline__ uint32_t phase(int f, int kv) { return (uint32_t)((kFp8 ? (2 * f + kv) / NS : f / NS) & 1); }
+  static __device__ __forceinline__ int slot(int f, int kv) {
+    return kFp8 ? (2 * f + kv) % NS : kv * NS + f % NS;
+  }
+  static __device__ __forceinline__ uint32_t phase(int f, int kv) {
+    return (uint32_t)((kFp8 ? (2 * f + kv) / NS : f / NS) & 1);
+  }
 };
 
 // Two E4M3 values (the low, the high half of x) as FP16, exactly.
@@ -802,7 +817,8 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           // V leaves the tile, and rows that see it get NaN
           const int slot = C::slot(f, 1), i = kFp8 ? slot : slot - NS;
           wait_for(bar(tb.full[slot]), C::phase(f, 1));
-          constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kUp = kBf16 ? 0x00800080u : 0x04000400u;
+          constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+          constexpr uint32_t kUp = kBf16 ? 0x00800080u : 0x04000400u;
           uint4* v = reinterpret_cast<uint4*>(base + slot * C::kSlot);
           for (int x = r; x < C::kSlot / 16; x += 128) {
             const uint4 y = v[x];
@@ -906,7 +922,8 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           __syncwarp();
           uint4 v[kQuads];
 #pragma unroll
-          for (int k = 0; k < kQuads; ++k) v[k] = stage[place(k * (32 / kQuads) + lane / kQuads, lane % kQuads)];
+          for (int k = 0; k < kQuads; ++k)
+            v[k] = stage[place(k * (32 / kQuads) + lane / kQuads, lane % kQuads)];
 #pragma unroll
           for (int k = 0; k < kQuads; ++k)
             if (to[k]) *reinterpret_cast<uint4*>(to[k] + offset + lane % kQuads * 16) = v[k];
@@ -938,7 +955,8 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             for (int h = 0; h < 32; h += C::kOutCols) {
 #pragma unroll
               for (int q = 0; q < kQuads; ++q)
-                stage[place(lane, q)] = make_uint4(x[h + 4 * q], x[h + 4 * q + 1], x[h + 4 * q + 2], x[h + 4 * q + 3]);
+                stage[place(lane, q)] =
+                    make_uint4(x[h + 4 * q], x[h + 4 * q + 1], x[h + 4 * q + 2], x[h + 4 * q + 3]);
               pair_sync();                                 // there
               pair_sync();                                 // taken
             }
@@ -982,7 +1000,8 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             } else if (dst) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<uint4*>(dst + (uint64_t)(c + i) * 4) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                *reinterpret_cast<uint4*>(dst + (uint64_t)(c + i) * 4) =
+                    make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
             }
           } else if (direct) {
 #pragma unroll
@@ -1001,7 +1020,8 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             for (int h = 0; h < 32; h += C::kOutCols) {
 #pragma unroll
               for (int q = 0; q < kQuads; ++q)
-                stage[place(lane, q)] = make_uint4(x[h + 4 * q], x[h + 4 * q + 1], x[h + 4 * q + 2], x[h + 4 * q + 3]);
+                stage[place(lane, q)] =
+                    make_uint4(x[h + 4 * q], x[h + 4 * q + 1], x[h + 4 * q + 2], x[h + 4 * q + 3]);
               store((uint64_t)(c + h) * 4);
             }
           }
@@ -1335,7 +1355,8 @@ __device__ __forceinline__ int tile_row(const ChunkParams& p, int j, int g) {
 // Adds what the runs [c0, c1] left of row i of a row tile, in c0 as its second
 // segment or its first; of them this thread's: k0, k0 + dk, ...
 template <int D>
-__device__ __forceinline__ void add_pieces(const ChunkParams& p, int list, int cta0, bool by_head, int set, int c0, int c1,
+__device__ __forceinline__ void add_pieces(const ChunkParams& p, int list, int cta0, bool by_head,
+                                           int set, int c0, int c1,
                                            int second, int i, int ln, int k0, int dk, float mult, Acc& acc) {
 #pragma unroll 4
   for (int c = c0 + k0; c <= c1; c += dk) {
@@ -1465,6 +1486,12 @@ cudaError_t chunk_device(int* n_sms) {
     int n = 0;
     e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
+    // the registers that warpgroups deal out among themselves are those of the launch:
+    // with fewer, one would wait for its share without end
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, chunk_walk_kernel<T, D, kFp8>);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs < ChunkShape<D, kFp8>::kRegs) return cudaErrorInvalidKernelImage;
     e = cudaFuncSetAttribute(chunk_walk_kernel<T, D, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)ChunkShape<D, kFp8>::kSmem);
     if (e != cudaSuccess) return e;

@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
             y[i] = fmul2(y[i], fmul2(w[x][i], make_float2(r, r)));
             float2 o;
             if constexpr (kPairs) o = make_float2(y[i].y, y[i].x);
-            else o = make_float2(__shfl_sync(0xffffffffu, y[i].x, other), __shfl_sync(0xffffffffu, y[i].y, other));
+            else o = make_float2(__shfl_sync(0xffffffffu, y[i].x, other),
+                                 __shfl_sync(0xffffffffu, y[i].y, other));
             const float2 q = ffma2(o, s[i], fmul2(y[i], c[i]));
             z[i] = turned ? narrow<T>(q.x, q.y) : narrow<T>(y[i].x, y[i].y);
           }
