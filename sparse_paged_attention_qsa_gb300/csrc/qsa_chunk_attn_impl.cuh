@@ -1265,26 +1265,32 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           wait_for(bar(tb.in_full[in]), (uint32_t)((n / C::NI) & 1));
           if (n >= NS) wait_for(bar(tb.empty[out]), (uint32_t)((n / NS - 1) & 1));
           if ((n & 1) && ct < 4) tb.bad[out][ct] = 0;
-          // 16 values a thread: a piece of a line, two pieces of a line of FP16.
-          // Eight threads read one line (heads of 64: two); those of the second half
-          // store their second piece first, so that the eight write to all banks.
+          // 16 values a thread and step, 8 and 8: of a line, pieces of a line of FP16.
+          // Lanes that would meet in a bank take their halves in the other order.
           constexpr int kLine = D == 64 ? 64 : 128, kPieces = D / 16;
-          const unsigned char* src = base + C::kStaged + in * C::kIn;
-          unsigned char* dst = base + out * C::kSlot;
-#pragma unroll 4
-          for (int i = ct; i < TT * kPieces; i += 128) {
-            const int row = i / kPieces, x = i % kPieces;  // dims [16 x, 16 x + 16)
-            const int sw = D == 64 ? (row >> 1) & 3 : row & 7;
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                src + (x * 16 / kLine) * (TT * kLine) + row * kLine + (((x % (kLine / 16)) ^ sw) << 4));
-            uint4 h[2];
-            h[0] = make_uint4(widen_lo(v.x), widen_hi(v.x), widen_lo(v.y), widen_hi(v.y));
-            h[1] = make_uint4(widen_lo(v.z), widen_hi(v.z), widen_lo(v.w), widen_hi(v.w));
-            unsigned char* line = dst + (x >> 2) * (TT * 128) + row * 128;
-            const int second = (x >> 2) & 1, y = 2 * (x & 3);
-            *reinterpret_cast<uint4*>(line + (((y + second) ^ (row & 7)) << 4)) = second ? h[1] : h[0];
-            *reinterpret_cast<uint4*>(line + (((y + 1 - second) ^ (row & 7)) << 4)) = second ? h[0] : h[1];
-          }
+          constexpr int kSteps = TT * kPieces / 128, kRows = 128 / kPieces;
+          static_assert(kRows % 8 == 0, "the same place in each line");
+          const int row = ct / kPieces, x = ct % kPieces;  // dims [16 x, 16 x + 16)
+          const int sw = D == 64 ? (row >> 1) & 3 : row & 7, y = 2 * (x & 3);
+          const int turned = (D == 64 ? row >> 1 : D == 128 ? x >> 2 ^ row : x >> 2 ^ x >> 3) & 1;
+          const unsigned char* src = base + C::kStaged + in * C::kIn + (x * 16 / kLine) * (TT * kLine) +
+                                     row * kLine + (((x % (kLine / 16)) ^ sw) << 4);
+          unsigned char* line = base + out * C::kSlot + (x >> 2) * (TT * 128) + row * 128;
+          unsigned char* dst[2] = {line + (((y + turned) ^ (row & 7)) << 4),
+                                   line + (((y + 1 - turned) ^ (row & 7)) << 4)};
+          uint2 v[kSteps][2];
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              v[i][h] = *reinterpret_cast<const uint2*>(src + i * (kRows * kLine) + (h ^ turned) * 8);
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<uint4*>(dst[h] + i * (kRows * 128)) =
+                  make_uint4(widen_lo(v[i][h].x), widen_hi(v[i][h].x), widen_lo(v[i][h].y),
+                             widen_hi(v[i][h].y));
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
