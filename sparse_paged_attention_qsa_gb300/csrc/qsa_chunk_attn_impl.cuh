@@ -40,6 +40,7 @@
 // the products' type.
 #pragma once
 
+
 #include "qsa_chunk_attn.h"
 #include "qsa_device.cuh"
 #include "qsa_internal.h"
@@ -48,6 +49,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <mutex>
@@ -128,10 +130,14 @@ struct Sight {
 __device__ __forceinline__ int32_t prefix_entries(const ChunkParams& p) {
   return p.prefix_table ? min(max(*p.prefix_len, 0), p.prefix_cap) : 0;
 }
-// Both warpgroups share a row tile of one accumulator.
-template <int kGroups>
+// Both warpgroups share a row tile of one accumulator.  Heads of 64, whose K/V tiles
+// come faster than one warpgroup takes them: 64 requests of 16384 entries, 4 rows a
+// K/V head, 328 us (by one 358), E4M3 356 (416).  Wider heads wait for K and V, and
+// their joint row tile is only begun and ended later: E4M3 heads of 128 with 128 rows a
+// K/V head, 8 x 32768 entries, 107 (98).
+template <int D>
 __device__ __forceinline__ bool splits(bool dual, int tiles) {
-  return kGroups == 2 && !dual && tiles >= kChunkSplit;
+  return D == 64 && !dual && tiles >= kChunkSplit;
 }
 template <int TT>
 __device__ __forceinline__ Sight prefix_sight(const ChunkParams& p) {
@@ -528,6 +534,22 @@ struct ChunkShape {
   }
 };
 
+// A slot of the ring and the phase in which it is full, for K or V in turn.
+template <int NS, bool kFp8>
+struct Ring {
+  int slot;                                                // V's of its own: NS on
+  uint32_t phase;
+  __device__ __forceinline__ void next() {
+    if constexpr (kFp8) {
+      slot += 2;
+      if (slot >= NS) slot -= NS, phase ^= 1;
+    } else {
+      ++slot;
+      if (slot % NS == 0) slot -= NS, phase ^= 1;
+    }
+  }
+};
+
 // Two E4M3 values (the low, the high half of x) as FP16, exactly.
 __device__ __forceinline__ uint32_t widen_lo(uint32_t x) {
   uint32_t r;
@@ -679,7 +701,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       const Segment& seg = *next;
       const Sight& s = seg.sight;
       const int tiles = seg.t1 - seg.t0;
-      const bool dual = seg.toks > p.acc_toks, split = splits<C::kGroups>(dual, tiles), two = dual || split;
+      const bool dual = seg.toks > p.acc_toks, split = splits<D>(dual, tiles), two = dual || split;
       const bool own = C::kGroups == 1 || two || g == turn;
       // this thread's row, and what all rows see
       const int jt = (dual ? g * p.acc_toks : 0) + rj;     // of the row tile's tokens
@@ -808,6 +830,8 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         };
 #pragma unroll
         for (int w = 0; w < kWords / 2; ++w) weights(w, z[w]);
+        // V is there too before its first product is asked for
+        if (wl == 0) wait_for(bar(tb.full[C::slot(f, 1)]), C::phase(f, 1));
         if (!edge) ready(0);
 #pragma unroll
         for (int w = kWords / 2; w < kWords; ++w) weights(w, z[w]);
@@ -1167,15 +1191,18 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     } else if (warp == kIssuer) {
       // ---------------- issuer ----------------
       constexpr uint32_t kQk = tc5_idesc(kBf16, 128, TT, false), kPv = tc5_idesc(kBf16, 128, D, true);
-      int fill = 0, units = 0;                             // tiles, row tiles before this segment
-      int ready[2] = {0, 0}, turn = 0;
+      const uint64_t q0 = tc5_desc(ring + C::kQ, 16), k0 = tc5_desc(ring, 16), v0 = tc5_desc(ring, TT * 128);
+      const bool leader = tc5_elect();
+      Ring<NS, kFp8> ks{0, 0}, vs{kFp8 ? 1 : NS, 0};       // the next K's and V's slot
+      uint32_t ready[2] = {0, 0};                          // phases of P
+      int units = 0, turn = 0;                             // row tiles; whose the next of one O is
       for (int sn = 0;; ++sn) {
         const Segment* next = segment(sn);
         if (!next) break;
         // the same in every lane, and said so
         const int tiles = __shfl_sync(0xffffffffu, next->t1 - next->t0, 0);
         const bool dual = __shfl_sync(0xffffffffu, next->toks, 0) > p.acc_toks;
-        const bool two = dual || splits<C::kGroups>(dual, tiles);
+        const bool two = dual || splits<D>(dual, tiles);
         segment_done(sn);
         if (tiles <= 0) {
           if (!two) turn ^= 1;
@@ -1184,62 +1211,77 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         const int steps = dual ? 2 * tiles : tiles;
         wait_for(kQToFp16 ? bar(tb.q_ready) : bar(tb.q_full), (uint32_t)(units & 1));
         ++units;
-        const auto qk = [&](int s, bool there) {
-          const int u = s & 1, f = fill + (dual ? s >> 1 : s), i = C::slot(f, 0);
-          if (!there) wait_for(bar(tb.full[i]), C::phase(f, 0));
-          tc5_fence_after();
-          // 16 dims a product: 32 bytes on in a line of 64, then the next block of lines
-          const uint64_t q = tc5_desc(ring + C::kQ + (dual ? u * C::kQTile : 0), 16);
-          const uint64_t k = tc5_desc(ring + i * C::kSlot, 16);
-          if (tc5_elect()) {
+        // Few instructions: this warp's own time is on the way of every product.  Which
+        // buffer and which mode are constants in each use, slots go round by adding
+        // (4096 tokens behind 4096 others, 16 heads of 128: 169 -> 150 us).
+        const auto run = [&](auto dual_) {
+          constexpr bool kDual = decltype(dual_)::value;
+          const int which = C::kGroups == 1 ? 0 : turn;    // of !two: whose row tile it is
+          const auto qk = [&](int s, auto u_, bool there) {
+            constexpr int u = decltype(u_)::value;
+            if (!there) wait_for(bar(tb.full[0]) + ks.slot * 8, ks.phase);
+            tc5_fence_after();
+            // 16 dims a product: 32 bytes on in a line of 64, then the next block of lines
+            const uint64_t q = q0 + (kDual ? u * (C::kQTile >> 4) : 0), k = k0 + ks.slot * (C::kSlot >> 4);
+            if (leader) {
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x)
-              tc5_mma_ss(tmem + u * C::kS, q + (x >> 2) * (128 * 128 / 16) + (x & 3) * 2,
-                         k + (x >> 2) * (TT * 128 / 16) + (x & 3) * 2, kQk, x > 0);
-            tc5_commit(bar(tb.s_full[C::kGroups == 1 ? 0 : two ? u : turn][u]));
-            if (!dual || u == 1) tc5_commit(bar(tb.empty[i]));
-            if (s + 1 == steps) tc5_commit(bar(tb.q_free));
-          }
-          used = true;
-        };
-        qk(0, false);
-        if (steps > 1) qk(1, dual);
-        // (after a time-out without waits, on whatever the buffers hold)
-        for (int s = 0; s < steps; ++s) {
-          const int u = s & 1, f = fill + (dual ? s >> 1 : s), slot = C::slot(f, 1);
-          const int fk = fill + (dual ? (s + 2) >> 1 : s + 2);
-          // what is there already costs no wait behind the softmax's
-          const bool k_there = (dual && u == 1) ||
-                               (s + 2 < steps && mbar_test_wait(bar(tb.full[C::slot(fk, 0)]), C::phase(fk, 0)));
-          const bool v_there = mbar_test_wait(bar(tb.full[slot]), C::phase(f, 1));
-          const uint64_t v = tc5_desc(ring + slot * C::kSlot, TT * 128);
-          const uint32_t o = tmem + C::kO + (C::kGroups == 1 ? 0 : two ? u * D : turn * D);
-          const uint32_t pa = tmem + C::kP + u * (D == 128 ? C::kS : TT / 2);
-          const bool add = s > (two ? 1 : 0);
-          const auto half = [&](int h) {
-#pragma unroll
-            for (int y = 0; y < TT / 32; ++y) {
-              const int x = h * (TT / 32) + y;
-              tc5_mma_ts(o, pa + x * 8, v + x * (16 * 128 / 16), kPv, add || x > 0);
+              for (int x = 0; x < D / 16; ++x)
+                tc5_mma_ss(tmem + u * C::kS, q + (x >> 2) * (128 * 128 / 16) + (x & 3) * 2,
+                           k + (x >> 2) * (TT * 128 / 16) + (x & 3) * 2, kQk, x > 0);
+              tc5_commit(bar(tb.s_full[0][u]) + (kDual ? u * 16 : two ? u * 16 : which * 16));
+              if (!kDual || u == 1) tc5_commit(bar(tb.empty[0]) + ks.slot * 8);
+              if (s + 1 == steps) tc5_commit(bar(tb.q_free));
             }
+            __syncwarp();
+            if (!kDual || u == 1) ks.next();
+            used = true;
           };
-          wait_for(bar(tb.p_half[u][0]), (uint32_t)(ready[u] & 1));
-          if (!__all_sync(0xffffffffu, v_there)) wait_for(bar(tb.full[slot]), C::phase(f, 1));
-          tc5_fence_after();
-          if (tc5_elect()) half(0);
-          wait_for(bar(tb.p_half[u][1]), (uint32_t)(ready[u] & 1));
-          ++ready[u];
-          tc5_fence_after();
-          if (tc5_elect()) {
-            half(1);
-            if (!dual || u == 1) tc5_commit(bar(tb.empty[slot]));
-            if (!two) tc5_commit(bar(tb.pv_done));
-            if (s + (two ? 2 : 1) >= steps)
-              tc5_commit(bar(tb.o_done[C::kGroups == 1 ? 0 : two ? u : turn]));
+          // (after a time-out without waits, on whatever the buffers hold)
+          const auto step = [&](int s, auto u_) {
+            constexpr int u = decltype(u_)::value;
+            // what is there already costs no wait behind the softmax's
+            const bool k_there =
+                (kDual && u == 1) || mbar_test_wait(bar(tb.full[0]) + ks.slot * 8, ks.phase);
+            const uint64_t v = v0 + vs.slot * (C::kSlot >> 4);
+            const uint32_t o = tmem + C::kO + (kDual ? u * D : two ? u * D : which * D);
+            constexpr int kPa = C::kP + u * (D == 128 ? C::kS : TT / 2);
+            const bool add = s > (kDual || two ? 1 : 0);
+            const auto half = [&](int h) {
+#pragma unroll
+              for (int y = 0; y < TT / 32; ++y) {
+                const int x = h * (TT / 32) + y;
+                tc5_mma_ts(o, tmem + kPa + x * 8, v + x * (16 * 128 / 16), kPv, add || x > 0);
+              }
+            };
+            wait_for(bar(tb.p_half[u][0]), ready[u]);
+            tc5_fence_after();
+            if (leader) half(0);
+            __syncwarp();
+            wait_for(bar(tb.p_half[u][1]), ready[u]);
+            ready[u] ^= 1;
+            tc5_fence_after();
+            if (leader) {
+              half(1);
+              if (!kDual || u == 1) tc5_commit(bar(tb.empty[0]) + vs.slot * 8);
+              if (!kDual && !two) tc5_commit(bar(tb.pv_done));
+              if (s + (kDual || two ? 2 : 1) >= steps)
+                tc5_commit(bar(tb.o_done[0]) + (kDual ? u * 8 : two ? u * 8 : which * 8));
+            }
+            __syncwarp();
+            if (!kDual || u == 1) vs.next();
+            if (s + 2 < steps) qk(s + 2, u_, __all_sync(0xffffffffu, k_there));
+          };
+          using Zero = std::integral_constant<int, 0>;
+          using One = std::integral_constant<int, 1>;
+          qk(0, Zero(), false);
+          if (kDual || steps > 1) qk(1, One(), kDual);
+          for (int s = 0; s < steps; s += 2) {
+            step(s, Zero());
+            if (kDual || s + 1 < steps) step(s + 1, One());
           }
-          if (s + 2 < steps) qk(s + 2, __all_sync(0xffffffffu, k_there));
-        }
-        fill += tiles;
+        };
+        if (C::kGroups == 2 && dual) run(std::bool_constant<C::kGroups == 2>());
+        else run(std::false_type());
         if (!two) turn ^= 1;
       }
     } else if constexpr (kFp8) {
