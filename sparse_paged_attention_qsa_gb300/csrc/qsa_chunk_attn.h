@@ -27,17 +27,24 @@ inline int chunk_heads(int group) {
 // What a K/V tile costs a row tile, and what the row tile costs beside, where two
 // accumulators share it (heads of 256: where one holds more than 32 rows) and where
 // not.  Measured, a row tile of 1, 2, 4, 8, 16 K/V tiles, in us an SM:
-//   heads of 128, 256 rows  7.4  9.3 13.3 21.6 34.3;  4 rows  4.0  5.5  8.2 14.1 25.6
-//   heads of 64,  256 rows  5.4  6.9  9.7 15.2 26.6;  4 rows  3.5  4.2  5.1  7.4 14.5
-//   heads of 256, 128 rows  5.9  7.3 10.3 16.3 28.1;  4 rows  3.3  4.4  6.7 12.1 23.3
-// and 1.4 a tile of heads of 128 over K/V that the L2 holds.
+//   heads of 128, 256 rows  6.3  8.3 11.9 18.8 31.7;  4 rows  3.0  4.0  6.6 12.5 23.7
+//   (over E4M3              8.4 10.2 13.7 20.8 32.8;          4.0  5.0  6.4 10.2 20.4)
+//   heads of 64,  256 rows  5.5  6.8  9.5 14.1 24.6;  4 rows  3.3  4.0  5.1  8.1 14.8
+//   heads of 256, 128 rows  5.7  7.3 10.1 16.0 27.2;  4 rows  2.8  3.5  6.4 11.7 22.9
+// A heavy extra of 11 takes 12 prompts 561 us, of 14 552; a light one of 6 and 8 differ
+// in nothing that was timed; few rows' tiles at 3 for 4 took 256 requests behind
+// 32768 entries 290 us in place of 253.
 constexpr int kTileCostLog2 = 2, kTileCost = 4, kHeavyExtra = 14, kLightExtra = 8;
 // A CTA's share of a batch behind a prefix, below which it gets a run of the prefix's
-// or of the requests' own alone.
+// or of the requests' own alone: both cost it the start of a second row tile (8 requests
+// behind 2000 entries 24.5 us, with both 25.9; 64 drafts behind 100000, far above it,
+// 109 either way).
 constexpr int kChunkShare = 60;
-// K/V tiles from which on two warpgroups share a row tile of one accumulator.
+// K/V tiles from which on two warpgroups share a row tile of one accumulator (from 6
+// on: 256 requests behind 32768 entries 241 us in place of 234, when all widths did).
 constexpr int kChunkSplit = 12;
-// Pieces of a row tile, from which on runs are longer, and how long at least.
+// Pieces of a row tile, from which on runs are longer, and how long at least (one
+// request of 9215 entries 21.9 us, with runs of one K/V tile 28).
 constexpr int kChunkPieces = 36, kChunkMinRun = 14;
 
 // Query rows of one set of heads that walk K/V tiles together: the tokens [tok0, tok0

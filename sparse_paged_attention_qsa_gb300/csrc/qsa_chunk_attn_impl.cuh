@@ -15,8 +15,8 @@
 //   one is in the softmax while the other is in the tensor pipe.  Two warpgroups
 //   form the softmax, a thread a row: no reduction crosses threads.  The two hold
 //   two halves of 256 rows over the same K/V tiles.  Of 128 rows and fewer they take
-//   every other K/V tile each and merge at the end, or, where those are few, one row
-//   tile each in turn, so that one's output leaves while the other is at work.
+//   one row tile each in turn, so that one's output leaves while the other is at work,
+//   or (heads of 64, many K/V tiles) every other K/V tile each and merge at the end.
 //   (Heads of 256 hold one O of 256 columns: one warpgroup, two S.)  Four more warps
 //   widen E4M3 tiles to FP16 on their way to the ring.
 // chunk_join_kernel, chunk_join_all_kernel  join the pieces of row tiles that runs
@@ -28,18 +28,20 @@
 // or 2^8 (BF16), and O in tensor memory is rescaled at such moves alone.
 //
 // What bounds it.  Long prompts: shared memory, which Q K^T reads at its whole rate
-// (8 KB a product of 128 x 128 x 16, 64 cycles), beside the softmax's own chain of
-// 1400 cycles a tile: 2630 cycles for 256 rows by 128 entries of heads of 128, where
-// the tensor pipe alone takes 2048.  4096 tokens behind 4096 others, 16 heads of 128:
-// 170 us, 1.2 PFLOP/s, 0.61 of the measured cuBLAS rate.  Single tokens: HBM (64
-// requests of 8192 entries, 8 K/V heads of 128: 313 us, 6.9 TB/s).
+// (8 KB a product of 128 x 128 x 16, 64 cycles), and the chain softmax (1400 cycles a
+// tile), issuing warp, products, of which two row halves hide each other's but in
+// part.  4096 tokens behind 4096 others, 16 heads: of 128 150 us, 1.35 PFLOP/s, 0.69 of
+// the measured cuBLAS rate; of 256 (2048 behind 8192, 8 heads) 129 us, 1.18 PFLOP/s; of
+// 64 129 us, 0.78 PFLOP/s.  A row tile's end (output, next queries, first S) is 5600
+// cycles, a sixth of prompts of 2000 tokens.  Single tokens: HBM (64 requests of 8192
+// entries, 8 K/V heads of 128: 310 us, 6.9 TB/s); over E4M3 caches the widening and the
+// slots that it waits for (257 us, 0.6 of HBM).
 //
 // Rounding: q, K and V enter the products as they are (E4M3 as FP16, exactly; BF16
 // queries of an E4M3 cache as FP16 after a power-of-two scaling of the row, where
 // only bits 2^-25 below the row's largest element can be lost), weights rounded to
 // the products' type.
 #pragma once
-
 
 #include "qsa_chunk_attn.h"
 #include "qsa_device.cuh"
