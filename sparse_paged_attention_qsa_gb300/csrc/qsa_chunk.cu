@@ -140,6 +140,7 @@ qsa_status attend(const qsa_paged_cache* cache, bool prefix, const int32_t* pref
   p.per_kv = group / p.sub;
   p.acc_toks = 128 / p.sub;
   p.heavy_rows = chunk_accs(p.c.dim) == 2 ? p.acc_toks * p.sub : 32;
+  p.heavy_extra = fp8 ? kHeavyExtraE4M3 : kHeavyExtra;
   p.scale_log2 = scale_log2;
   // (a context is 2^31 - 1 at most: a window as wide hides nothing)
   p.window = (int32_t)std::min<int64_t>(window, INT32_MAX);

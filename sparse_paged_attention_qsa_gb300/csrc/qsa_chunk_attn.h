@@ -31,10 +31,12 @@ inline int chunk_heads(int group) {
 //   (over E4M3              8.4 10.2 13.7 20.8 32.8;          4.0  5.0  6.4 10.2 20.4)
 //   heads of 64,  256 rows  5.5  6.8  9.5 14.1 24.6;  4 rows  3.3  4.0  5.1  8.1 14.8
 //   heads of 256, 128 rows  5.7  7.3 10.1 16.0 27.2;  4 rows  2.8  3.5  6.4 11.7 22.9
-// A heavy extra of 11 takes 12 prompts 561 us, of 14 552; a light one of 6 and 8 differ
+// A heavy extra of 11 takes 12 prompts 561 us, of 14 552, of 17 571 (24 E4M3 chunks with
+// 14 557, 17 553, 20 548); a light one of 6 and 8 differ
 // in nothing that was timed; few rows' tiles at 3 for 4 took 256 requests behind
 // 32768 entries 290 us in place of 253.
-constexpr int kTileCostLog2 = 2, kTileCost = 4, kHeavyExtra = 14, kLightExtra = 8;
+constexpr int kTileCostLog2 = 2, kTileCost = 4, kHeavyExtra = 14, kHeavyExtraE4M3 = 20,
+              kLightExtra = 8;
 // A CTA's share of a batch behind a prefix, below which it gets a run of the prefix's
 // or of the requests' own alone: both cost it the start of a second row tile (8 requests
 // behind 2000 entries 24.5 us, with both 25.9; 64 drafts behind 100000, far above it,
@@ -93,7 +95,8 @@ struct ChunkParams {
   int32_t sub;                  // query heads of a set, whose rows walk together
   int32_t sets, per_kv;         // sets in all, and of one K/V head
   int32_t acc_toks;             // tokens of an accumulator: 128 / sub
-  int32_t heavy_rows;           // more rows than that cost the more
+  int32_t heavy_rows;           // more rows than that cost heavy_extra
+  int32_t heavy_extra;
   float scale_log2;             // scale * log2(e)
   int32_t window;               // 0: none
   int32_t sink;                 // 0 without a window

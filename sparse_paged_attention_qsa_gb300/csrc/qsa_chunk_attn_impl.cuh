@@ -175,7 +175,7 @@ __device__ __forceinline__ int64_t piece_at(const ChunkParams& p, int list, int 
 // What a row tile costs beside its K/V tiles (kTileCost each): its queries' way in
 // and its output's way out.  (One that sees nothing costs 1 in all.)
 __device__ __forceinline__ int32_t extra_cost(const ChunkParams& p, int32_t toks) {
-  return toks * p.sub > p.heavy_rows ? kHeavyExtra : kLightExtra;
+  return toks * p.sub > p.heavy_rows ? p.heavy_extra : kLightExtra;
 }
 
 // Not negative; 64-bit divisions take several times as long.
