@@ -474,9 +474,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
 struct ChunkTables {
   uint64_t full[16], empty[16];            // ring: K's slots, then V's; E4M3: both in turn
   uint64_t in_full[8], in_empty[8];        // E4M3: tiles as they came, K's and V's in turn
-  uint64_t s_full[2][2];                   // of a warpgroup's S in each buffer
-  uint64_t p_half[2][2], o_done[2], scanned[2];
-  uint64_t q_full, q_ready, q_free, pv_done, drain;
+  uint64_t s_full[2][3];                   // of a warpgroup's S in each buffer
+  uint64_t p_half[3][2], o_done[2], scanned[2];
+  uint64_t q_full, q_ready, q_free, pv_done[2], drain;   // products of even and odd steps
   uint64_t seg_full[kSegments], seg_empty[kSegments], pair[4];
   uint32_t boxes[kTileFlags];              // a bit per copy of a tile, 0: it had no page
   uint32_t bad[8][4];                      // entries of a V slot that hold what is not finite
@@ -510,9 +510,14 @@ struct ChunkShape {
   static constexpr int kOut = kStaged + NI * kIn;
   static constexpr int kTables = kOut + kGroups * 4 * 32 * kOutCols * 4;
   static constexpr size_t kSmem = 1024 + kTables + sizeof(ChunkTables);
-  // tensor memory columns
-  static constexpr int kS = TT, kP = D == 128 ? 64 : 2 * TT;
-  static constexpr int kO = D == 128 ? 256 : D == 64 ? 384 : 256;
+  // Tensor memory columns.  S in turn in kBufs buffers: two, a warpgroup's own where it
+  // has half of the rows.  Heads of 64 leave room for a third: a warpgroup finds its
+  // next S formed while it was in the softmax, where two buffers make it wait for the
+  // product with its weights first.  Weights take the place of half of their S (heads of
+  // 256: beside it).
+  static constexpr int kBufs = D == 64 ? 3 : 2;
+  static constexpr int kS = TT, kP = D == 256 ? 2 * TT : 64, kPs = D == 256 ? TT / 2 : kS;
+  static constexpr int kO = D == 64 ? 384 : 256;
   static_assert(kSmem <= 232448, "shared memory");
   // Registers: 384 threads of 168 at launch, dealt out as 208, 208 and 88 a thread
   // of a warpgroup; over an E4M3 cache 512 of 128 as 192, 192, 64, 64.  A row of S
@@ -629,17 +634,17 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       mbar_init(bar(tb.in_empty[i]), 4);
     }
     for (int u = 0; u < 2; ++u) {
-      mbar_init(bar(tb.s_full[u][0]), 1);
-      mbar_init(bar(tb.s_full[u][1]), 1);
-      mbar_init(bar(tb.p_half[u][0]), 4);
-      mbar_init(bar(tb.p_half[u][1]), 4);
+      mbar_init(bar(tb.pv_done[u]), 1);
+      for (int b = 0; b < C::kBufs; ++b) {
+        mbar_init(bar(tb.s_full[u][b]), 1);
+        mbar_init(bar(tb.p_half[b][u]), 4);
+      }
       mbar_init(bar(tb.o_done[u]), 1);
       mbar_init(bar(tb.scanned[u]), 4);
     }
     mbar_init(bar(tb.q_full), 1);
     mbar_init(bar(tb.q_ready), 4);
     mbar_init(bar(tb.q_free), 1);
-    mbar_init(bar(tb.pv_done), 1);
     mbar_init(bar(tb.drain), 1);
     for (int i = 0; i < kSegments; ++i) {
       mbar_init(bar(tb.seg_full[i]), 1);
@@ -693,8 +698,10 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
     const int box_log2 = min(p.c.page_log2, TT == 128 ? 7 : 6);
     const int rj = r / p.sub, rh = r - rj * p.sub;         // the row's token and head in its accumulator
     unsigned char* out_stage = base + C::kOut + warp * (32 * C::kOutCols * 4);
-    int fill = 0, units = 0, steps_done = 0;
-    int got[2] = {0, 0}, outs = 0, scans = 0;              // S of each buffer, O taken, V searched so far
+    int fill = 0, units = 0;
+    uint32_t pvs[2] = {0, 0};                              // products with weights, of even and odd steps
+    uint32_t got = 0;                                      // phases of S, a bit a buffer
+    int outs = 0, scans = 0;                               // O taken, V searched so far
     int turn = 0;                                          // whose the next row tile of one O is
     int pairs = 0;                                         // meetings of two warps that hold the same rows
     for (int sn = 0;; ++sn) {
@@ -722,11 +729,16 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       // K/V tile t of the segment: from 0 on up to the sinks' end, then the window's
       const int first_tile = seg.t0, first_gap = s.ns - seg.t0, rest_tile = seg.t0 - s.ns + s.w0;
       const int stride = two ? 2 : 1;
-      for (int st = two ? g : own ? 0 : steps; st < steps; st += stride) {
-        const int u = st & 1, t = dual ? st >> 1 : st, f = fill + t;
+      int u = two ? g : 0;                                 // the buffer of S: st modulo kBufs
+      const auto next_buffer = [&]() {
+        u += stride;
+        if (u >= C::kBufs) u -= C::kBufs;
+      };
+      for (int st = two ? g : own ? 0 : steps; st < steps; st += stride, next_buffer()) {
+        const int t = dual ? st >> 1 : st, f = fill + t;
         const int32_t e0 = (t < first_gap ? t + first_tile : t + rest_tile) * TT;
-        wait_for(bar(tb.s_full[g][u]), (uint32_t)(got[u] & 1));
-        ++got[u];
+        wait_for(bar(tb.s_full[g][0]) + u * 8, got >> u & 1);
+        got ^= 1u << u;
         tc5_fence_after();
         if constexpr (kQToFp16) {
           if (st < stride) {                               // the row's first
@@ -789,9 +801,12 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           const float a = !move ? 1.f : old == -INFINITY ? 0.f : cex2((old - m) * mult);
           l *= a;
           if (st >= stride) {
-            // the product before this one into the same O: done with two O (S of this
-            // step came behind it), else to be waited for
-            if (!two) wait_for(bar(tb.pv_done), (uint32_t)((steps_done + st - 1) & 1));
+            // the product before this one into the same O: done where S of this step
+            // came behind it, else to be waited for (the one before that is done, so
+            // that its phase is not taken for this one's)
+            const int last = st - stride;
+            if (C::kBufs > stride)
+              wait_for(bar(tb.pv_done[last & 1]), ((last & 1 ? pvs[1] : pvs[0]) + (last >> 1)) & 1);
             tc5_fence_after();
             const uint32_t o = lanes + C::kO + g * D;
 #pragma unroll 1
@@ -809,7 +824,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         const float ref = m == -INFINITY ? 0.f : m;
         const float2 mult2 = make_float2(mult, mult), ref2 = make_float2(-ref, -ref);
         const float2 shift2 = make_float2(chunk_shift(kBf16), chunk_shift(kBf16));
-        const uint32_t pa = lanes + C::kP + u * (D == 128 ? C::kS : TT / 2);
+        const uint32_t pa = lanes + C::kP + u * C::kPs;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const auto weights = [&](int w, uint32_t(&x)[32]) {
           uint32_t h[16];
@@ -828,7 +843,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           tc5_wait_st();
           tc5_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(tb.p_half[u][half]));
+          if (lane == 0) mbar_arrive(bar(tb.p_half[0][half]) + u * 16);
         };
 #pragma unroll
         for (int w = 0; w < kWords / 2; ++w) weights(w, z[w]);
@@ -871,7 +886,10 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         }
         ready(1);
       }
-      if (!two) steps_done += steps;
+      if (C::kBufs == 3 || !two) {
+        pvs[0] += (steps + 1) >> 1;
+        pvs[1] += steps >> 1;
+      }
       fill += tiles;
       if (tiles > 0) ++units;
       if (!two) turn ^= 1;
@@ -1196,7 +1214,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       const uint64_t q0 = tc5_desc(ring + C::kQ, 16), k0 = tc5_desc(ring, 16), v0 = tc5_desc(ring, TT * 128);
       const bool leader = tc5_elect();
       Ring<NS, kFp8> ks{0, 0}, vs{kFp8 ? 1 : NS, 0};       // the next K's and V's slot
-      uint32_t ready[2] = {0, 0};                          // phases of P
+      uint32_t ready[2] = {0, 0};                          // phases of P (of three buffers a bit each)
       int units = 0, turn = 0;                             // row tiles; whose the next of one O is
       for (int sn = 0;; ++sn) {
         const Segment* next = segment(sn);
@@ -1219,8 +1237,10 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         const auto run = [&](auto dual_) {
           constexpr bool kDual = decltype(dual_)::value;
           const int which = C::kGroups == 1 ? 0 : turn;    // of !two: whose row tile it is
-          const auto qk = [&](int s, auto u_, bool there) {
+          // S of step s; its buffer (with two a constant), and whose it is
+          const auto qk = [&](int s, int turn_b, auto u_, bool there) {
             constexpr int u = decltype(u_)::value;
+            const int b = C::kBufs == 2 ? u : turn_b;
             if (!there) wait_for(bar(tb.full[0]) + ks.slot * 8, ks.phase);
             tc5_fence_after();
             // 16 dims a product: 32 bytes on in a line of 64, then the next block of lines
@@ -1228,9 +1248,9 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             if (leader) {
 #pragma unroll
               for (int x = 0; x < D / 16; ++x)
-                tc5_mma_ss(tmem + u * C::kS, q + (x >> 2) * (128 * 128 / 16) + (x & 3) * 2,
+                tc5_mma_ss(tmem + b * C::kS, q + (x >> 2) * (128 * 128 / 16) + (x & 3) * 2,
                            k + (x >> 2) * (TT * 128 / 16) + (x & 3) * 2, kQk, x > 0);
-              tc5_commit(bar(tb.s_full[0][u]) + (kDual ? u * 16 : two ? u * 16 : which * 16));
+              tc5_commit(bar(tb.s_full[0][0]) + b * 8 + (kDual || two ? u : which) * 24);
               if (!kDual || u == 1) tc5_commit(bar(tb.empty[0]) + ks.slot * 8);
               if (s + 1 == steps) tc5_commit(bar(tb.q_free));
             }
@@ -1239,47 +1259,62 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
             used = true;
           };
           // (after a time-out without waits, on whatever the buffers hold)
-          const auto step = [&](int s, auto u_) {
-            constexpr int u = decltype(u_)::value;
+          const auto step = [&](int s, int turn_b, auto u_) {
+            constexpr int u = decltype(u_)::value, un = (u + C::kBufs) & 1;
+            const int b = C::kBufs == 2 ? u : turn_b;
             // what is there already costs no wait behind the softmax's
             const bool k_there =
-                (kDual && u == 1) || mbar_test_wait(bar(tb.full[0]) + ks.slot * 8, ks.phase);
+                (kDual && un == 1) || mbar_test_wait(bar(tb.full[0]) + ks.slot * 8, ks.phase);
             const uint64_t v = v0 + vs.slot * (C::kSlot >> 4);
-            const uint32_t o = tmem + C::kO + (kDual ? u * D : two ? u * D : which * D);
-            constexpr int kPa = C::kP + u * (D == 128 ? C::kS : TT / 2);
+            const uint32_t o = tmem + C::kO + (kDual || two ? u * D : which * D);
+            const uint32_t pa = tmem + C::kP + b * C::kPs;
+            const auto phase = [&]() { return C::kBufs == 2 ? ready[u] : ready[0] >> b & 1; };
             const bool add = s > (kDual || two ? 1 : 0);
             const auto half = [&](int h) {
 #pragma unroll
               for (int y = 0; y < TT / 32; ++y) {
                 const int x = h * (TT / 32) + y;
-                tc5_mma_ts(o, tmem + kPa + x * 8, v + x * (16 * 128 / 16), kPv, add || x > 0);
+                tc5_mma_ts(o, pa + x * 8, v + x * (16 * 128 / 16), kPv, add || x > 0);
               }
             };
-            wait_for(bar(tb.p_half[u][0]), ready[u]);
+            wait_for(bar(tb.p_half[b][0]), phase());
             tc5_fence_after();
             if (leader) half(0);
             __syncwarp();
-            wait_for(bar(tb.p_half[u][1]), ready[u]);
-            ready[u] ^= 1;
+            wait_for(bar(tb.p_half[b][1]), phase());
+            if constexpr (C::kBufs == 2) ready[u] ^= 1;
+            else ready[0] ^= 1u << b;
             tc5_fence_after();
             if (leader) {
               half(1);
               if (!kDual || u == 1) tc5_commit(bar(tb.empty[0]) + vs.slot * 8);
-              if (!kDual && !two) tc5_commit(bar(tb.pv_done));
+              if (C::kBufs == 3 || (!kDual && !two)) tc5_commit(bar(tb.pv_done[u]));
               if (s + (kDual || two ? 2 : 1) >= steps)
-                tc5_commit(bar(tb.o_done[0]) + (kDual ? u * 8 : two ? u * 8 : which * 8));
+                tc5_commit(bar(tb.o_done[0]) + (kDual || two ? u : which) * 8);
             }
             __syncwarp();
             if (!kDual || u == 1) vs.next();
-            if (s + 2 < steps) qk(s + 2, u_, __all_sync(0xffffffffu, k_there));
+            if (s + C::kBufs < steps)
+              qk(s + C::kBufs, b, std::integral_constant<int, un>(), __all_sync(0xffffffffu, k_there));
           };
           using Zero = std::integral_constant<int, 0>;
           using One = std::integral_constant<int, 1>;
-          qk(0, Zero(), false);
-          if (kDual || steps > 1) qk(1, One(), kDual);
-          for (int s = 0; s < steps; s += 2) {
-            step(s, Zero());
-            if (kDual || s + 1 < steps) step(s + 1, One());
+          qk(0, 0, Zero(), false);
+          if (kDual || steps > 1) qk(1, 1, One(), kDual);
+          if (C::kBufs == 3 && steps > 2) qk(2, 2, Zero(), false);
+          if constexpr (C::kBufs == 2) {
+            for (int s = 0; s < steps; s += 2) {
+              step(s, 0, Zero());
+              if (kDual || s + 1 < steps) step(s + 1, 1, One());
+            }
+          } else {
+            int b = 0;
+            for (int s = 0; s < steps; s += 2) {
+              step(s, b, Zero());
+              b = b == 2 ? 0 : b + 1;
+              if (kDual || s + 1 < steps) step(s + 1, b, One());
+              b = b == 2 ? 0 : b + 1;
+            }
           }
         };
         if (C::kGroups == 2 && dual) run(std::bool_constant<C::kGroups == 2>());
