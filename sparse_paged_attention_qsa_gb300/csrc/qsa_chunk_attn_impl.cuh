@@ -32,7 +32,7 @@
 // tile), issuing warp, products, of which two row halves hide each other's but in
 // part.  4096 tokens behind 4096 others, 16 heads: of 128 150 us, 1.35 PFLOP/s, 0.69 of
 // the measured cuBLAS rate; of 256 (2048 behind 8192, 8 heads) 129 us, 1.18 PFLOP/s; of
-// 64 129 us, 0.78 PFLOP/s.  A row tile's end (output, next queries, first S) is 5600
+// 64 118 us, 0.85 PFLOP/s.  A row tile's end (output, next queries, first S) is 5600
 // cycles, a sixth of prompts of 2000 tokens.  Single tokens: HBM (64 requests of 8192
 // entries, 8 K/V heads of 128: 310 us, 6.9 TB/s); over E4M3 caches the widening and the
 // slots that it waits for (257 us, 0.6 of HBM).
@@ -134,7 +134,7 @@ __device__ __forceinline__ int32_t prefix_entries(const ChunkParams& p) {
 }
 // Both warpgroups share a row tile of one accumulator.  Heads of 64, whose K/V tiles
 // come faster than one warpgroup takes them: 64 requests of 16384 entries, 4 rows a
-// K/V head, 328 us (by one 358), E4M3 356 (416).  Wider heads wait for K and V, and
+// K/V head, 328 us (by one 358), E4M3 356 (416), with two buffers of S.  Wider heads wait for K and V, and
 // their joint row tile is only begun and ended later: E4M3 heads of 128 with 128 rows a
 // K/V head, 8 x 32768 entries, 107 (98).
 template <int D>
@@ -513,7 +513,8 @@ struct ChunkShape {
   // Tensor memory columns.  S in turn in kBufs buffers: two, a warpgroup's own where it
   // has half of the rows.  Heads of 64 leave room for a third: a warpgroup finds its
   // next S formed while it was in the softmax, where two buffers make it wait for the
-  // product with its weights first.  Weights take the place of half of their S (heads of
+  // product with its weights first (one prompt of 32768 tokens, window 4096, 16 heads:
+  // 582 us for 647).  Weights take the place of half of their S (heads of
   // 256: beside it).
   static constexpr int kBufs = D == 64 ? 3 : 2;
   static constexpr int kS = TT, kP = D == 256 ? 2 * TT : 64, kPs = D == 256 ? TT / 2 : kS;

@@ -304,6 +304,26 @@ def test_scales_of_any_size(mul, dtype):
         c.check(out, None, c2)
 
 
+@pytest.mark.parametrize("reqs", [[(200, 1300)], [(1, 1500)], [(20, 700), (3, 1200), (1, 250)]])
+@pytest.mark.parametrize("dtype,cache", [(F16, F16), (BF16, BF16), (F16, E4M3)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_maxima_that_move_at_every_tile(d, dtype, cache, reqs):
+    # logits that rise by 12 every 128 entries: the sums so far are rescaled each time
+    c = Case(reqs, 4, 2, d, 64, dtype, cache, scale=12.0, seed=19)
+    c.q.mul_(2.0 ** -6)
+    c.q[..., 0] = 1
+    k = c.k.float()
+    for b, (n, old) in enumerate(reqs):
+        e = torch.arange(n + old, device=DEV)
+        k[c.tables[b].long()[e // 64], e % 64, :, 0] = (e // 128).float()[:, None]
+    c.k.copy_(k.to(cache))
+    if cache == E4M3:
+        c.k_scale.fill_(1.0)
+    out, lse, err = c.run()
+    c.check(out, lse)
+    assert int(err) == 0
+
+
 def test_equal_logits_far_up_share_evenly():
     # logits of 2^30 and more: their reference is a binary32 value of its own
     c = Case([(1, 99)], 1, 1, 64, 16, F16, scale=1e9, seed=12)
