@@ -514,7 +514,8 @@ struct ChunkShape {
   // has half of the rows.  Heads of 64 leave room for a third: a warpgroup finds its
   // next S formed while it was in the softmax, where two buffers make it wait for the
   // product with its weights first (one prompt of 32768 tokens, window 4096, 16 heads:
-  // 582 us for 647).  Weights take the place of half of their S (heads of
+  // 582 us for 647; heads of 256, one warpgroup on all rows, gain nothing, 130 for 129 in
+  // 2048 behind 8192).  Weights take the place of half of their S (heads of
   // 256: beside it).
   static constexpr int kBufs = D == 64 ? 3 : 2;
   static constexpr int kS = TT, kP = D == 256 ? 2 * TT : 64, kPs = D == 256 ? TT / 2 : kS;
