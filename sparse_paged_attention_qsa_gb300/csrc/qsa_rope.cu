@@ -224,7 +224,8 @@ bool apart(const View& a, const View& b) {
   if (!cache_host::overlaps(a.all, b.all)) return true;
   if (a.tokens <= 1 || b.tokens <= 1 || a.step != b.step) return false;
   const int64_t d = (int64_t)((b.all.lo - a.all.lo) % (uintptr_t)a.step);
-  const int64_t off = b.all.lo >= a.all.lo ? d : a.step - (int64_t)((a.all.lo - b.all.lo) % (uintptr_t)a.step);
+  const int64_t off =
+      b.all.lo >= a.all.lo ? d : a.step - (int64_t)((a.all.lo - b.all.lo) % (uintptr_t)a.step);
   const int64_t o = off == a.step ? 0 : off;
   return o >= a.inner && o + b.inner <= a.step;
 }

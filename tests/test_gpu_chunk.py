@@ -304,12 +304,14 @@ def test_scales_of_any_size(mul, dtype):
         c.check(out, None, c2)
 
 
-@pytest.mark.parametrize("reqs", [[(200, 1300)], [(1, 1500)], [(20, 700), (3, 1200), (1, 250)]])
+@pytest.mark.parametrize("hq,hk,reqs", [
+    (4, 2, [(200, 1300)]), (4, 2, [(1, 1500)]), (4, 2, [(20, 700), (3, 1200), (1, 250)]),
+    (16, 8, [(128, 1400)] * 4), (8, 8, [(1, 1700)] * 64)])     # long runs of each mode
 @pytest.mark.parametrize("dtype,cache", [(F16, F16), (BF16, BF16), (F16, E4M3)])
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_maxima_that_move_at_every_tile(d, dtype, cache, reqs):
+def test_maxima_that_move_at_every_tile(d, dtype, cache, hq, hk, reqs):
     # logits that rise by 12 every 128 entries: the sums so far are rescaled each time
-    c = Case(reqs, 4, 2, d, 64, dtype, cache, scale=12.0, seed=19)
+    c = Case(reqs, hq, hk, d, 64, dtype, cache, scale=12.0, seed=19)
     c.q.mul_(2.0 ** -6)
     c.q[..., 0] = 1
     k = c.k.float()
