@@ -508,7 +508,13 @@ struct ChunkShape {
   static constexpr int kQ = (kFp8 ? NS : 2 * NS) * kSlot;  // offsets: ring, queries, E4M3, output, tables
   static constexpr int kStaged = kQ + kGroups * kQTile;
   static constexpr int kOut = kStaged + NI * kIn;
-  static constexpr int kTables = kOut + kGroups * 4 * 32 * kOutCols * 4;
+  // Rows of a row tile whose ends leave without the stages: those that one warp holds.
+  static constexpr int kFew = kGroups == 1 ? 16 : 4 * 32 * kOutCols / D;
+  // Where both warpgroups share a row tile of so few, the second's columns of them, in
+  // bytes of their own: the stages of its other warps, which hold none of the rows, may
+  // be in use for its next row tile by the time that the first warpgroup reads.
+  static constexpr int kHand = kOut + kGroups * 4 * 32 * kOutCols * 4;
+  static constexpr int kTables = kHand + (D == 64 ? kFew * D * 4 : 0);
   static constexpr size_t kSmem = 1024 + kTables + sizeof(ChunkTables);
   // Tensor memory columns.  S in turn in kBufs buffers: two, a warpgroup's own where it
   // has half of the rows.  Heads of 64 leave room for a third: a warpgroup finds its
@@ -521,6 +527,7 @@ struct ChunkShape {
   static constexpr int kS = TT, kP = D == 256 ? 2 * TT : 64, kPs = D == 256 ? TT / 2 : kS;
   static constexpr int kO = D == 64 ? 384 : 256;
   static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kHand >= kOut + kSoft / 32 * (32 * kOutCols * 4), "apart from every warp's stage");
   // Registers: 384 threads of 168 at launch, dealt out as 208, 208 and 88 a thread
   // of a warpgroup; over an E4M3 cache 512 of 128 as 192, 192, 64, 64.  A row of S
   // stays in registers whole.
@@ -927,8 +934,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           }
         }
         const bool first = g == 0 || !split;               // writes
-        constexpr int kFew = C::kGroups == 1 ? 16 : 4 * 32 * C::kOutCols / D;
-        const bool few = !dual && seg.toks * p.sub <= kFew;
+        const bool few = !dual && seg.toks * p.sub <= C::kFew;
         const bool direct = seg.whole && !p.res_o[0];
         const int64_t token = seg.token + seg.tok0 + jt;
         const int head = seg.set * p.sub + rh;
@@ -954,10 +960,9 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           return row * kQuads + (kQuads == 4 ? q ^ ((row >> 1) & 3) : q ^ ((row >> 2) & 1));
         };
         const uint4* other = stage + 4 * 32 * kQuads;      // the second warpgroup's
-        // Few rows (one warp's): the second warpgroup's go over at once, through the
-        // stage of all its warps, which has been read since: its product waited for
-        // the first one's next weights.
-        uint4* whole = reinterpret_cast<uint4*>(base + C::kOut) + 4 * 32 * kQuads;
+        // Few rows (one warp's): the second warpgroup's go over at once.  The first one
+        // has read the last ones when it comes to this row tile's first meeting.
+        uint4* whole = reinterpret_cast<uint4*>(base + C::kHand);
         const auto spot = [&](int q) { return lane * (D / 4) + (q ^ (lane & 7)); };
         if (few && split && g == 0) pair_sync();
         uint64_t to[kQuads];                               // the rows that this lane stores pieces of
