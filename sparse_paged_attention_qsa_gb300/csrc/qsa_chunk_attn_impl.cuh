@@ -25,7 +25,8 @@
 // The reference m_i is a product that occurred, the row's maximum when it was
 // taken, subtracted before the scaling: logits of any size keep the differences
 // that binary32 products have.  It moves only when weights would pass 2^15 (FP16)
-// or 2^8 (BF16), and O in tensor memory is rescaled at such moves alone.
+// or 1 (BF16, the reference's own 2^-8), and O in tensor memory is rescaled at such
+// moves alone.
 //
 // What bounds it.  Long prompts: shared memory, which Q K^T reads at its whole rate
 // (8 KB a product of 128 x 128 x 16, 64 cycles), and the chain softmax (1400 cycles a
@@ -65,9 +66,10 @@ constexpr int64_t kJoinFew = 1 << 16;   // threads: rows up to here are joined b
 constexpr int kTileFlags = 16;      // tiles whose page masks are kept
 constexpr int kSegments = 4;        // segments known ahead
 
-// A weight is at most 2^(shift + slack).  FP16 weights stay normal down to 2^-22 of
-// the largest; BF16 has binary32's exponents.
-constexpr float chunk_shift(bool bf16) { return bf16 ? 0.f : 8.f; }
+// A weight is at most 2^(shift + slack), the reference's own 2^shift.  FP16 weights
+// stay normal down to 2^-22 of the reference's.  BF16 has binary32's exponents, for V
+// as well: weights of 1 at most keep the sums of w V within those of |V|.
+constexpr float chunk_shift(bool bf16) { return bf16 ? -8.f : 8.f; }
 constexpr float chunk_slack(bool bf16) { return bf16 ? 8.f : 7.f; }
 
 __device__ __forceinline__ float cex2(float x) {
