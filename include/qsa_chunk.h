@@ -57,8 +57,9 @@ QSA_API size_t qsa_chunk_attention_workspace_bytes(const qsa_paged_cache* cache,
  * they were.  What an entry holds (infinities and NaN too) does not matter to a
  * row that does not see it.  The softmax's statistics and sums are binary32, so
  * q . K_e, z_e and the sum of |V_e| over the entries that a row sees have to be
- * finite there.  The results are the same bit for bit each time a call is
- * repeated on one kind of GPU.
+ * finite there; over an E4M3 cache also q . K_e without K's scale, and scale *
+ * log2(e) * k_scale[h] from 2^-126 to 2^127.  The results are the same bit for bit
+ * each time a call is repeated on one kind of GPU.
  *
  * The weights multiply V rounded, relative to themselves, by at most 2^-12
  * (FP16, and any E4M3 cache) or 2^-9 (BF16); lse does not carry that rounding.

@@ -50,6 +50,7 @@
 #include "qsa_tcgen05.cuh"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -106,6 +107,10 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
 template <bool kBf16>
 __device__ __forceinline__ float row_lse(float m, float l, float mult) {
   return l == 0.f ? -INFINITY : fmaf(m, mult, log2f(l) - chunk_shift(kBf16)) * 0.693147180559945309f;
+}
+// What the logits of a set of heads are multiplied by, base 2.
+__device__ __forceinline__ float set_mult(const ChunkParams& p, int set) {
+  return p.scale_log2 * (p.c.k_scale ? p.c.k_scale[set / p.per_kv] : 1.f);
 }
 // --- geometry ---------------------------------------------------------------------
 
@@ -581,8 +586,8 @@ __device__ __forceinline__ uint32_t widen_hi(uint32_t x) {
 }
 
 // Row r of a query tile, BF16, as FP16 in its place: divided by the power of two,
-// returned, that brings its largest magnitude to [2^14, 2^15) (1 where that has no
-// exponent).
+// returned, that brings its largest magnitude to [2^14, 2^15), or by 2^-120 where that
+// takes less (1 where the magnitude is not finite).
 template <int D>
 __device__ __forceinline__ float row_to_fp16(unsigned char* tile, int r) {
   const auto at = [&](int x) {
@@ -599,7 +604,7 @@ __device__ __forceinline__ float row_to_fp16(unsigned char* tile, int r) {
   }
   const int e = (int)(__float_as_uint(a) >> 23);
   float mul = 1.f, by = 1.f;
-  if (e > 0 && e < 255) {
+  if (e < 255) {
     const int up = min(14 + 127 - e, 120);
     mul = __uint_as_float((uint32_t)(127 - up) << 23);
     by = __uint_as_float((uint32_t)(127 + up) << 23);
@@ -731,10 +736,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
       const int32_t in_hi = s.hi(seg.tok0), in_lo = s.lo(jl);
       const int32_t in_sink = s.window > 0 ? min(s.sink, in_hi) : 0;
       const int kv_head = seg.set / p.per_kv;
-      float mult = p.scale_log2, q_mul = 1.f;
-      if constexpr (kFp8) {
-        if (p.c.k_scale) mult *= p.c.k_scale[kv_head];
-      }
+      float mult = kFp8 ? set_mult(p, seg.set) : p.scale_log2, q_mul = 1.f;
       float m = -INFINITY, l = 0.f;
       const int steps = dual ? 2 * tiles : tiles;
       // K/V tile t of the segment: from 0 on up to the sinks' end, then the window's
@@ -754,7 +756,9 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
         if constexpr (kQToFp16) {
           if (st < stride) {                               // the row's first
             q_mul = tb.q_mul[units & 1][(dual ? g * 128 : 0) + r];
-            mult *= q_mul;
+            // where it leaves binary32's normal numbers, logits are either the same to
+            // 2^-90 or apart by 2^90: its ends do as well, and keep infinities from zeros
+            mult = fminf(fmaxf(mult * q_mul, FLT_MIN), FLT_MAX);
           }
         }
         const uint32_t boxes = tb.boxes[f % kTileFlags];
@@ -948,7 +952,7 @@ chunk_walk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__
           if (direct) {
             dst = reinterpret_cast<uint64_t>(p.out + token * p.out_row + head * p.out_head);
             inv = l == 0.f ? 0.f : (kFp8 && p.c.v_scale ? p.c.v_scale[kv_head] : 1.f) / l;
-            if (p.lse) p.lse[at] = row_lse<kBf16>(m, l, mult);
+            if (p.lse) p.lse[at] = row_lse<kBf16>(m * q_mul, l, kFp8 ? set_mult(p, seg.set) : mult);
           } else {
             dst = reinterpret_cast<uint64_t>(seg.whole ? p.res_o[seg.list] + at * D : p.part_o + piece * D);
             *reinterpret_cast<float2*>(seg.whole ? p.res_ml[seg.list] + at * 2 : p.part_ml + piece * 2) =
@@ -1437,10 +1441,6 @@ struct Acc {
   }
 };
 
-// What the logits of a set of heads are multiplied by, base 2.
-__device__ __forceinline__ float set_mult(const ChunkParams& p, int set) {
-  return p.scale_log2 * (p.c.k_scale ? p.c.k_scale[set / p.per_kv] : 1.f);
-}
 // Where row (token j of a row tile, head g of the set) lies among its rows.
 __device__ __forceinline__ int tile_row(const ChunkParams& p, int j, int g) {
   return j < p.acc_toks ? j * p.sub + g : 128 + (j - p.acc_toks) * p.sub + g;
