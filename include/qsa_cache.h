@@ -148,8 +148,10 @@ QSA_API size_t qsa_paged_attention_workspace_bytes(const qsa_paged_cache* cache,
  *
  * The weights enter the product with V rounded, relative to themselves, by 2^-22
  * (FP16) or 2^-16 (BF16) where next_n * num_heads / cache->num_heads is 32 or less
- * and the cache is not E4M3; by 2^-12 (FP16, and any E4M3 cache) or 2^-9 (BF16)
- * elsewhere.  lse and weight sums do not carry that rounding.
+ * and the cache is not E4M3; by 2^-11 (FP16, and any E4M3 cache) or 2^-8 (BF16)
+ * elsewhere; or by 2^-39 of the row's sum of weights (FP16; logits past 2^19:
+ * 2^-25), 2^-126 (BF16), where that is more.  lse and weight sums do not carry that
+ * rounding.
  *
  * Weight sums need every logit until its row is complete: num_reqs * next_n *
  * num_heads * table_cols * page_size * 4 bytes of workspace, whatever the

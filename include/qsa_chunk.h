@@ -61,8 +61,10 @@ QSA_API size_t qsa_chunk_attention_workspace_bytes(const qsa_paged_cache* cache,
  * log2(e) * k_scale[h] from 2^-126 to 2^127.  The results are the same bit for bit
  * each time a call is repeated on one kind of GPU.
  *
- * The weights multiply V rounded, relative to themselves, by at most 2^-12
- * (FP16, and any E4M3 cache) or 2^-9 (BF16); lse does not carry that rounding.
+ * The weights multiply V rounded to one value of 16 bits: each is off by at most
+ * 2^-11 of itself, or 2^-33 of its row's sum of weights where that is more (FP16,
+ * and any E4M3 cache), 2^-8 or 2^-118 (BF16).  lse does not carry that rounding.
+ * (qsa_paged_attention rounds few rows' weights less.)
  *
  * Arguments
  *   q             [num_tokens, num_heads, head_dim], dtype QSA_DT_F16 or
