@@ -30,11 +30,15 @@ extern "C" {
  *         a = i, b = i + rot_dim / 2, or with interleaved != 0
  *         a = 2 i, b = 2 i + 1
  *
- * z goes to q_out or k_out, rounded once; everything before is binary32.  A
- * token with a negative position (the metadata builder's padding) is left as
- * it was in both.  The product of position and frequency is reduced to one
- * turn in 64 bits before it is rounded, so an angle is off by at most 2^-24 of
- * a half turn wherever positions[t] * (1 + |inv_freq[i]|) is below 2^37.
+ * z goes to q_out or k_out, rounded once; everything before is binary32:
+ * sum_j x_j^2 has to be finite there (as it is for elements up to 2^59), eps +
+ * (sum_j x_j^2) / head_dim 2^-120 at least, and w_i over its root a normal number
+ * or 0.  (FP16 rows are within the first two whatever numbers they hold, but for
+ * zeros with eps 0, which give NaN.)  A token with a negative position (the
+ * metadata builder's padding) is left as it was in both.  The product of position
+ * and frequency is reduced to one turn in 64 bits before it is rounded, so an
+ * angle is off by at most 2^-24 of a half turn wherever positions[t] * (1 +
+ * |inv_freq[i]|) is below 2^37.
  *
  * Arguments
  *   q, k           [num_tokens, q_heads, head_dim], [num_tokens, k_heads,

@@ -90,3 +90,24 @@ def test_dense_attentions_weights(dtype):
         _hold(w, _off(w, dtype, False), one[i], far, 1.0)
     else:
         assert least_b >= 2.0 ** -126
+
+
+def test_norms_sum_of_squares():
+    # the least mean square that the header names, from squares that binary32 rounds to
+    # multiples of 2^-149: off by less than its own rounding; and the elements that it says
+    # are never too large
+    words = _words("qsa_rope.h", "qsa_qk_norm_rope")
+    assert "sum_j x_j^2 has to be finite there" in words
+    least, = _powers(words, r"eps \+ \(sum_j x_j\^2\) / head_dim 2\^-(\d+) at least")
+    large = float(2 ** int(re.search(r"elements up to 2\^(\d+)\)", words).group(1)))
+    for dim in (8, 128, 256):
+        for spread in (0.0, 8.0, 16.0):                      # elements of 2^-spread besides
+            x = torch.full((dim,), 2.0 ** -spread, dtype=torch.float64)
+            x[0] = 1.0
+            x = (x * (least / (x * x).mean()).sqrt() * 1.01).to(BF16).float()
+            exact = (x.double() ** 2).mean()
+            got = (x * x).double().mean()
+            assert exact >= least and (got / exact - 1).abs() <= 2.0 ** -24
+        x = torch.full((dim,), large, dtype=torch.float32)
+        assert (x * x).sum().isfinite()
+    assert dim * (2.0 * large) ** 2 >= 2.0 ** 128            # twice as much would be
