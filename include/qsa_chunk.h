@@ -32,6 +32,12 @@ extern "C" {
  * num_tokens new tokens with num_heads query heads over this cache.  What the
  * cache's pointers hold does not matter.  0 for a call that needs none and for
  * one that is refused.  Alignment 256 bytes.
+ *
+ * qsa_chunk_attention needs head_dim * 0.33 MB at most for the pieces of row tiles
+ * that runs cut, and 48 bytes for each token and request besides.
+ * qsa_prefix_attention needs twice that and 8 bytes for each element of q, 16 for
+ * each of its rows and heads: what a row sees of the prefix and what of its
+ * request's entries, both in binary32 (30000 tokens of 32 heads of 128: 1 GB).
  */
 QSA_API size_t qsa_chunk_attention_workspace_bytes(const qsa_paged_cache* cache,
                                                    int64_t num_tokens, int64_t num_heads,

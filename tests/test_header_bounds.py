@@ -17,7 +17,7 @@ def _words(name, function):
     """The comment before a function's declaration, one space between words."""
     with open(os.path.join(ROOT, "include", name)) as f:
         text = f.read()
-    text = text[:text.index(f" {function}(\n")]
+    text = text[:re.search(rf"QSA_API \w+ {function}\(", text).start()]
     return " ".join(text[text.rindex("/*"):].replace("\n *", " ").split())
 
 
