@@ -537,7 +537,8 @@ struct ChunkShape {
   static_assert(kHand >= kOut + kSoft / 32 * (32 * kOutCols * 4), "apart from every warp's stage");
   // Registers: 384 threads of 168 at launch, dealt out as 208, 208 and 88 a thread
   // of a warpgroup; over an E4M3 cache 512 of 128 as 192, 192, 64, 64.  A row of S
-  // stays in registers whole.
+  // stays in registers whole.  (The compiler allots by the launch's share: over an
+  // E4M3 cache 40 to 64 bytes a thread lie on the stack, elsewhere none.)
   static constexpr int kRegs = kGroups == 1 ? 0 : kFp8 ? 128 : 168;
   static constexpr int kMore = kFp8 ? 192 : 208, kFewer = kFp8 ? 64 : 88;
   static_assert(2 * kMore + (kThreads / 128 - 2) * kFewer <= kThreads / 128 * kRegs || kGroups == 1,

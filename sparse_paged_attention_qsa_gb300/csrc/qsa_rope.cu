@@ -14,9 +14,11 @@
 // would do as well; its rate here is a sixtieth of the integer one.
 //
 // Bytes bound it: each element is read and written once.  16344 tokens of 40 heads
-// of 128: pairs side by side 56.5 us (5.9 TB/s), half a head apart 70 (two shuffles
-// more a pair); each lane forming all angles of its own elements, with heads of q and
-// k in one loop, 78 and 106; two and four CTAs an SM 65 and 70, 71 and 98.
+// of 128: pairs side by side 56.5 us (5.9 TB/s), half a head apart 70 (4.8 TB/s: two
+// shuffles more a pair, and the 80 registers of three CTAs an SM leave 96 to 112 bytes
+// a thread on the stack, where the other order has 8 at most); each lane forming all
+// angles of its own elements, with heads of q and k in one loop, 78 and 106; two and
+// four CTAs an SM 65 and 70, 71 and 98.
 #include "qsa_cache_host.h"
 #include "qsa_device.cuh"
 #include "qsa_host.h"
